@@ -39,6 +39,10 @@ DFLASH_WT_Q5_0 = 2
 DFLASH_WT_Q4_0 = 3
 WEIGHT_TYPE_IDS = {"bf16": DFLASH_WT_BF16, "q8_0": DFLASH_WT_Q8_0, "q5_0": DFLASH_WT_Q5_0, "q4_0": DFLASH_WT_Q4_0}
 
+DFLASH_T_FP32 = 0
+DFLASH_T_BF16 = 1
+DFLASH_T_FP16 = 2
+
 DFLASH_MAX_LAYERS = 8
 DFLASH_MAX_BLOCK = 8
 DFLASH_MIN_BLOCK = 2
@@ -80,11 +84,19 @@ class DflashWeights(ctypes.Structure):
     ]
 
 
+class DflashKv4Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 # ------------------------------------------------------------------ loading
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_Z = ctypes.c_size_t
+_KV4 = ctypes.POINTER(DflashKv4Cache)
 _SIGS = {
     "dflash_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "dflash_last_cuda_error": (ctypes.c_char_p, []),
@@ -114,6 +126,16 @@ _SIGS = {
     "dflash_state_flush": (ctypes.c_int, [_P, _P]),
     "dflash_state_read_draft_probs": (ctypes.c_int, [_P, _P, _P]),
     "dflash_head_argmax_static": (ctypes.c_int, [_P, _P, _I, _P, _P, _P]),
+    "dflash_page_tables": (ctypes.c_int, [_P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "dflash_kv4_check": (ctypes.c_int, [_KV4]),
+    "dflash_kv4_bytes": (_Z, [_I, _I, _I, _I]),
+    "dflash_kv4_write": (ctypes.c_int, [_KV4, _P, _P, _I, _L, _L, _P, _I, _P, _P]),
+    "dflash_kv4_read": (ctypes.c_int, [_KV4, _P, _I, _P, _P, _P, _P]),
+    "dflash_kv4_attention": (ctypes.c_int, [_KV4, _P, _P, _I, _L, _L, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I,
+                                            ctypes.c_float, _P, _Z, _P, _P]),
+    "dflash_kv4_attention_workspace": (_Z, [_KV4, _I, _I, _I, _I]),
+    "dflash_token_logprobs": (ctypes.c_int, [_P, _I, _L, _I, _I, _P, _P, _P, _I, _P, _P, _P, _Z, _P, _P]),
+    "dflash_token_logprobs_workspace": (_Z, [_I, _I, _I, _I]),
 }
 
 
@@ -319,3 +341,62 @@ def dflash_state_set_attn_chunks(state: int, chunks: int = 0) -> int:
     _check(load_library().dflash_state_set_attn_chunks(state, chunks, ctypes.byref(mx)),
            "dflash_state_set_attn_chunks")
     return mx.value
+
+
+# -------------------------------------------------------------- verify step
+def dflash_kv4_check(cache: DflashKv4Cache) -> int:
+    return load_library().dflash_kv4_check(ctypes.byref(cache))
+
+
+def dflash_kv4_bytes(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    return load_library().dflash_kv4_bytes(n_pages, page_size, n_kv_heads, head_dim)
+
+
+def dflash_page_tables(lengths: int, new_rows: int, n_seq: int, page_size: int, n_pages: int, held_in: int,
+                       held_out: int, table: int, table_stride: int, ring: int, ring_in: int, ring_out: int,
+                       row_offsets: int, slots: int, positions: int, row_cap: int, dev_status: int = 0,
+                       stream: int = 0) -> None:
+    _check(load_library().dflash_page_tables(lengths, new_rows, n_seq, page_size, n_pages, held_in, held_out, table,
+                                             table_stride, ring, ring_in, ring_out, row_offsets, slots or None,
+                                             positions or None, row_cap, dev_status or None, stream or None),
+           "dflash_page_tables")
+
+
+def dflash_kv4_write(cache: DflashKv4Cache, k: int, v: int, value_type: int, k_stride: int, v_stride: int, slots: int,
+                     n_rows: int, dev_status: int = 0, stream: int = 0) -> None:
+    _check(load_library().dflash_kv4_write(ctypes.byref(cache), k, v, value_type, k_stride, v_stride, slots, n_rows,
+                                           dev_status or None, stream or None), "dflash_kv4_write")
+
+
+def dflash_kv4_read(cache: DflashKv4Cache, slots: int, n_rows: int, k_out: int, v_out: int, dev_status: int = 0,
+                    stream: int = 0) -> None:
+    _check(load_library().dflash_kv4_read(ctypes.byref(cache), slots, n_rows, k_out or None, v_out or None,
+                                          dev_status or None, stream or None), "dflash_kv4_read")
+
+
+def dflash_kv4_attention(cache: DflashKv4Cache, q: int, out: int, value_type: int, q_stride: int, out_stride: int,
+                         n_tokens: int, n_q_heads: int, n_seq: int, max_rows: int, row_offsets: int, kv_len: int,
+                         table: int, table_stride: int, causal: bool, window: int, scale: float, workspace: int,
+                         workspace_bytes: int, dev_status: int = 0, stream: int = 0) -> None:
+    _check(load_library().dflash_kv4_attention(ctypes.byref(cache), q, out, value_type, q_stride, out_stride, n_tokens,
+                                               n_q_heads, n_seq, max_rows, row_offsets, kv_len, table, table_stride,
+                                               1 if causal else 0, window, scale, workspace, workspace_bytes,
+                                               dev_status or None, stream or None), "dflash_kv4_attention")
+
+
+def dflash_kv4_attention_workspace(cache: DflashKv4Cache, n_q_heads: int, n_seq: int, max_rows: int,
+                                   table_stride: int) -> int:
+    return load_library().dflash_kv4_attention_workspace(ctypes.byref(cache), n_q_heads, n_seq, max_rows, table_stride)
+
+
+def dflash_token_logprobs(logits: int, value_type: int, row_stride: int, n_rows: int, vocab: int, tokens: int,
+                          logprob: int, entropy: int, top_k: int, top_ids: int, top_logprobs: int, workspace: int,
+                          workspace_bytes: int, dev_status: int = 0, stream: int = 0) -> None:
+    _check(load_library().dflash_token_logprobs(logits, value_type, row_stride, n_rows, vocab, tokens or None,
+                                                logprob or None, entropy or None, top_k, top_ids or None,
+                                                top_logprobs or None, workspace or None, workspace_bytes,
+                                                dev_status or None, stream or None), "dflash_token_logprobs")
+
+
+def dflash_token_logprobs_workspace(n_rows: int, vocab: int, value_type: int, top_k: int) -> int:
+    return load_library().dflash_token_logprobs_workspace(n_rows, vocab, value_type, top_k)

@@ -328,6 +328,10 @@ bool is_dev_ptr(const void* p) {
 
 }  // namespace
 
+namespace dflash {
+int cuda_status(cudaError_t e, const char* what) { return check_gemv(e, what); }
+}  // namespace dflash
+
 extern "C" {
 
 const char* dflash_status_string(int status) {

@@ -92,4 +92,10 @@ int attn_smem_bytes(int D, int M);
 // Diagnostic builds: the next per-CTA timestamp slot of a launch (else null).
 unsigned long long* trace_slot(State& st);
 
+// Records a CUDA error for dflash_last_cuda_error and returns its dflash_status
+// (DFLASH_OK for cudaSuccess).
+int cuda_status(cudaError_t e, const char* what);
+// log2 of a (checked) 4-bit cache's page size.
+int log2_page(const dflash_kv4_cache* c);
+
 }  // namespace dflash

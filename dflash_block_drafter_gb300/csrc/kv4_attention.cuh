@@ -1,0 +1,214 @@
+// What the kernels of the 4-bit paged attention share: arguments, the plan
+// that shares a call's work out over CTAs, and the merge of split segments.
+//
+// A sequence s with r rows over kv cells has, per kv head, G * r query rows
+// (row m = token m / G, head of the group m % G) which read the same cells.
+// They are cut into row groups of R rows; (sequence, kv head, row group) is
+// a segment.  A segment walks its visible cells in steps; all segments'
+// steps laid end to end are shared out evenly over C CTAs, so that every CTA
+// has the same work whatever the lengths.  A segment that lies inside one CTA
+// is written out by it; one that crosses into others leaves a piece (running
+// maximum, sum, unnormalised O in FP32) per CTA, and the merge kernel joins
+// them.  A CTA's range can hold at most two pieces: of the segment that began
+// before it (slot 2c) and of one that begins in it and goes on (slot 2c + 1).
+//
+// The lengths are on the device, so every CTA forms the plan itself (prefix
+// sums over at most kKv4MaxSeq sequences).
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "kernels.h"
+#include "kv4.cuh"
+
+namespace dflash {
+
+constexpr int kKv4MaxSeq = 1024;
+
+struct Kv4AttnArgs {
+  const uint8_t* cache;
+  int n_pages, page_shift, n_kv, G;
+  const uint16_t* q;
+  uint16_t* out;
+  int bf16;
+  long long q_stride, out_stride;  // elements between tokens
+  int n_seq, max_rows, n_tokens;
+  const int32_t* row_offsets;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int table_stride;
+  int causal, window;
+  float scale_log2;  // softmax scale * log2(e)
+  float* part;       // pieces' O [2 C][R][D]
+  float2* part_ml;   // [2 C][R]: maximum (log2 units) and sum
+  int32_t* status;
+};
+
+// What sequence s asks for.
+struct Kv4Seq {
+  int r0, rows, kv;  // first token, tokens, cells
+  int base, hi;      // visible cells [lo, hi) of any row, base = lo down to a step
+  int lo;
+  int steps, groups;
+};
+
+template <int STEP, int R>
+__device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool report) {
+  Kv4Seq q;
+  q.r0 = a.row_offsets[s];
+  const int r1 = a.row_offsets[s + 1];
+  q.rows = r1 - q.r0;
+  if (q.r0 < 0 || r1 > a.n_tokens || r1 < q.r0 || q.rows > a.max_rows) {
+    if (report) set_status(a.status, DFLASH_DEV_BAD_BLOCK);
+    q.rows = 0;
+  }
+  const long long cap = static_cast<long long>(a.table_stride) << a.page_shift;
+  int kv = a.kv_len[s];
+  if (kv > cap) {
+    if (report) set_status(a.status, DFLASH_DEV_CAPACITY);
+    kv = static_cast<int>(cap);
+  }
+  q.kv = max(kv, 0);
+  q.hi = q.kv;
+  q.lo = 0;
+  if (a.window > 0) {  // the first row that any window reaches
+    const int first = a.causal ? q.kv - q.rows : q.kv - 1;
+    q.lo = min(max(first - a.window + 1, 0), q.hi);
+  }
+  q.base = q.lo - q.lo % STEP;
+  // rows that see no cell take one masked step, which writes their zeros
+  q.steps = q.rows == 0 ? 0 : max((q.hi - q.base + STEP - 1) / STEP, 1);
+  q.groups = (q.rows * a.G + R - 1) / R;
+  return q;
+}
+
+// Visible cells [lo, hi) of token i of the sequence.
+__device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, int i) {
+  const int last = a.causal ? q.kv - q.rows + i : q.kv - 1;  // the row's own position
+  const int lo = a.window > 0 ? max(last - a.window + 1, 0) : 0;
+  return make_int2(lo, max(last + 1, 0));
+}
+
+// Prefix sums of the sequences' steps (over kv heads and row groups) in
+// `pre` [n_seq + 1] by the whole CTA; returns the total.
+template <int STEP, int R>
+__device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* pre, long long* scratch, bool report) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
+  long long carry = 0;
+  for (int s0 = 0; s0 < a.n_seq; s0 += n) {
+    const int s = s0 + tid;
+    long long v = 0;
+    if (s < a.n_seq) {
+      const Kv4Seq q = kv4_seq<STEP, R>(a, s, report);
+      v = static_cast<long long>(q.steps) * q.groups * a.n_kv;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    long long below = carry;
+    for (int w = 0; w < n / 32; ++w) {
+      if (w < warp) below += scratch[w];
+      carry += scratch[w];
+    }
+    if (s < a.n_seq) pre[s + 1] = below + v;
+    __syncthreads();
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+  return carry;
+}
+
+// CTAs that a call of T steps uses: at most `most`, each with `least` steps or more.
+__device__ __forceinline__ int kv4_ctas(long long T, int most, int least) {
+  const long long c = (T + least - 1) / least;
+  return c < 1 ? 1 : (c > most ? most : static_cast<int>(c));
+}
+__device__ __forceinline__ long long kv4_start(long long T, int C, int c) { return T * c / C; }
+// The CTA whose range holds step x.
+__device__ __forceinline__ int kv4_owner(long long T, int C, long long x) {
+  int c = static_cast<int>(x * C / T);
+  while (kv4_start(T, C, c + 1) <= x) ++c;
+  while (kv4_start(T, C, c) > x) --c;
+  return c;
+}
+// Sequence that holds step x.
+__device__ __forceinline__ int kv4_find(const long long* pre, int n_seq, long long x) {
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid + 1] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Joins the pieces of one row of a segment: block (c, row); the block of the
+// segment's second CTA does it, the others leave.  o = sum_i 2^(m_i - m) O_i /
+// sum_i 2^(m_i - m) l_i.
+template <int D, int STEP, int R>
+__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int most, int least) {
+  __shared__ long long pre[kKv4MaxSeq + 1];
+  __shared__ long long scratch[8];
+  constexpr int LANES = D / 4, PAR = 256 / LANES;
+  __shared__ float4 acc[256];
+  __shared__ float accl[PAR];
+  const int c = blockIdx.x, m = blockIdx.y;
+  const long long T = kv4_plan<STEP, R>(a, pre, scratch, false);
+  pdl_wait();
+  const int C = kv4_ctas(T, most, least);
+  if (c == 0 || c >= C || T == 0) return;
+  const long long x = kv4_start(T, C, c);
+  const int s = kv4_find(pre, a.n_seq, x);
+  const Kv4Seq q = kv4_seq<STEP, R>(a, s, false);
+  const long long rel = x - pre[s];
+  const int unit = static_cast<int>(rel / q.steps);  // head * groups + row group
+  const long long b0 = pre[s] + static_cast<long long>(unit) * q.steps, b1 = b0 + q.steps;
+  if (x == b0 || kv4_owner(T, C, b0) != c - 1) return;
+  const int head = unit / q.groups, rg = unit % q.groups;
+  const int row = rg * R + m;
+  if (row >= q.rows * a.G) return;
+  const int last = kv4_owner(T, C, b1 - 1);
+  const int n = last - c + 2;  // pieces: CTA c - 1 and c .. last
+  auto slot = [&](int i) { return 2 * (c - 1 + i) + (i == 0); };
+  const int lane = threadIdx.x % LANES, p = threadIdx.x / LANES;
+  float top = -INFINITY;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.part_ml + static_cast<size_t>(slot(i)) * R + m).x);
+  const float base = top == -INFINITY ? 0.f : top;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int i = p; i < n; i += PAR) {
+    const size_t at = static_cast<size_t>(slot(i)) * R + m;
+    const float2 ml = __ldcg(a.part_ml + at);
+    const float w = ex2_approx(ml.x - base);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + lane);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+    l = fmaf(w, ml.y, l);
+  }
+  acc[threadIdx.x] = o;
+  if (lane == 0) accl[p] = l;
+  __syncthreads();
+  if (p != 0) return;
+  for (int i = 1; i < PAR; ++i) {
+    const float4 v = acc[i * LANES + lane];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+    l += accl[i];
+  }
+  if (!(l < INFINITY) && lane == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* dst = a.out + (q.r0 + row / a.G) * a.out_stride + (head * a.G + row % a.G) * D + lane * 4;
+  const uint2 w = a.bf16 ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv))
+                         : make_uint2(pack_f16x2(o.x * inv, o.y * inv), pack_f16x2(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2*>(dst) = w;
+}
+
+}  // namespace dflash

@@ -1,0 +1,251 @@
+// Page tables and slot maps of requests whose lengths only the device knows
+// (dflash_page_tables in include/dflash.h).
+//
+// Per request: need = ceil((length + new_rows) / page); it takes need - held
+// pages from the ring of free pages or gives held - need back.  Which page is
+// whose, and where a request's rows lie, are prefix sums over the requests.
+// The work is a few bytes per request and per row, so launches are what it
+// costs: one launch does it all.  Every CTA forms the prefix sums of all
+// requests in its own shared memory (at most kMaxRequests of them), then the
+// rows, taken pages and given pages are shared out over all CTAs, each item
+// finding its request by binary search.  The CTAs form one cluster, whose
+// barrier orders their last read of held / ring_state before the first CTA
+// updates them, so that both may be updated in place.
+#include "common.cuh"
+#include "internal.h"
+#include "kernels.h"
+
+namespace dflash {
+namespace {
+
+constexpr int kMaxRequests = 4096;
+constexpr int kThreads = 1024;
+constexpr int kCluster = 8;
+
+struct PageArgs {
+  const int32_t* lengths;
+  const int32_t* new_rows;
+  int n_seq, page_shift, n_pages;
+  const int32_t* held_in;
+  int32_t* held_out;
+  int32_t* table;
+  int table_stride;
+  int32_t* ring;
+  const int32_t* ring_in;
+  int32_t* ring_out;
+  int32_t* row_offsets;
+  int32_t* slots;
+  int32_t* positions;
+  int row_cap;
+  int32_t* status;
+};
+
+__device__ __forceinline__ int saturate(long long v) { return v > 0x7fffffffll ? 0x7fffffff : static_cast<int>(v); }
+
+// What a request asks for.
+struct Request {
+  bool valid, fits;  // in play; its pages fit the table's width
+  int held, need, rows;
+};
+__device__ __forceinline__ Request request(const PageArgs& a, int s) {
+  Request q;
+  const int len = a.lengths[s], rows = a.new_rows[s];
+  q.valid = len >= 0 && rows >= 0;
+  q.held = min(max(a.held_in[s], 0), a.table_stride);
+  const long long total = static_cast<long long>(len) + rows;
+  const long long need = q.valid ? (total + (1 << a.page_shift) - 1) >> a.page_shift : 0;
+  q.fits = q.valid && need <= a.table_stride;
+  q.need = q.fits ? static_cast<int>(need) : q.held;
+  q.rows = q.valid ? rows : 0;
+  return q;
+}
+
+// First s with end[s] > x (end ascending, x < end[n - 1]).
+__device__ __forceinline__ int upper(const int* end, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a) {
+  extern __shared__ int ends[];  // [3][n_seq]: rows, pages taken, pages given, up to and with a request
+  __shared__ long long part[3][33];
+  __shared__ int s_taken;
+  int* row_end = ends;
+  int* take_end = ends + a.n_seq;
+  int* give_end = ends + 2 * a.n_seq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x;  // one cluster: the grid is the cluster
+  const int head = a.ring_in[0], free_pages = min(max(a.ring_in[1], 0), a.n_pages);
+  const int ring0 = head >= 0 && head < a.n_pages ? head : 0;
+  if (tid == 0) {
+    s_taken = 0;
+    if (rank == 0 && (ring0 != head || free_pages != a.ring_in[1])) set_status(a.status, DFLASH_DEV_CAPACITY);
+  }
+  long long carry[3] = {0, 0, 0};
+  for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
+    const int s = s0 + tid;
+    long long v[3] = {0, 0, 0};
+    if (s < a.n_seq) {
+      const Request q = request(a, s);
+      v[0] = q.rows;
+      v[1] = max(q.need - q.held, 0);
+      v[2] = max(q.held - q.need, 0);
+      if (rank == 0 && q.valid && !q.fits) set_status(a.status, DFLASH_DEV_CAPACITY);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const long long u = __shfl_up_sync(0xffffffffu, v[j], o);
+        if (lane >= o) v[j] += u;
+      }
+    if (lane == 31)
+      for (int j = 0; j < 3; ++j) part[j][warp] = v[j];
+    __syncthreads();
+    if (warp < 3) {  // warp j: prefix sums of the warps' totals of quantity j
+      long long x = part[warp][lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+      }
+      __syncwarp();
+      part[warp][lane + 1] = x;
+      if (lane == 0) part[warp][0] = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      if (s < a.n_seq) ends[j * a.n_seq + s] = saturate(carry[j] + part[j][warp] + v[j]);
+      carry[j] += part[j][32];
+    }
+    __syncthreads();
+  }
+  // requests whose pages are all there get them: those up to the first that
+  // asks for more than is left, and those that ask for none
+  for (int s = tid; s < a.n_seq; s += kThreads)
+    if (take_end[s] <= free_pages) atomicMax(&s_taken, take_end[s]);
+  __syncthreads();
+  const int taken = s_taken;
+  const int rows = saturate(carry[0]);
+  const int given_all = saturate(carry[2]);
+  const int given = min(given_all, a.n_pages - free_pages);  // more: a page was both free and held
+  if (rank == 0 && tid == 0 && (rows > a.row_cap || given < given_all || carry[1] > free_pages))
+    set_status(a.status, DFLASH_DEV_CAPACITY);
+  const int t0 = rank * kThreads + tid, step = gridDim.x * kThreads;
+  bool bad = false;
+  // pages taken: ring -> table
+  for (int i = t0; i < taken; i += step) {
+    const int s = upper(take_end, a.n_seq, i);
+    const int first = s ? take_end[s - 1] : 0;
+    const int held = min(max(a.held_in[s], 0), a.table_stride);
+    int at = ring0 + i;
+    if (at >= a.n_pages) at -= a.n_pages;
+    a.table[static_cast<size_t>(s) * a.table_stride + held + (i - first)] = a.ring[at];
+  }
+  // pages given back: table -> ring's tail
+  for (int i = t0; i < given; i += step) {
+    const int s = upper(give_end, a.n_seq, i);
+    const int first = s ? give_end[s - 1] : 0;
+    const int page = a.table[static_cast<size_t>(s) * a.table_stride + request(a, s).need + (i - first)];
+    long long at = static_cast<long long>(ring0) + free_pages + i;
+    at -= at >= a.n_pages ? a.n_pages : 0;
+    at -= at >= a.n_pages ? a.n_pages : 0;
+    a.ring[at] = page;
+    bad |= page < 0 || page >= a.n_pages;
+  }
+  // slots and positions of the rows
+  for (int r = t0; r < a.row_cap; r += step) {
+    int slot = -1, pos = -1;
+    if (r < rows) {
+      const int s = upper(row_end, a.n_seq, r);
+      const Request q = request(a, s);
+      const int len = a.lengths[s];
+      const int before = s ? row_end[s - 1] : 0;
+      const int take0 = s ? take_end[s - 1] : 0, take1 = take_end[s];
+      pos = saturate(static_cast<long long>(len) + (r - before));
+      if (q.fits && (take1 == take0 || take1 <= free_pages)) {
+        const int p = pos >> a.page_shift;
+        int page;
+        if (p < q.held) {
+          page = a.table[static_cast<size_t>(s) * a.table_stride + p];
+        } else {
+          int at = ring0 + take0 + (p - q.held);
+          if (at >= a.n_pages) at -= a.n_pages;
+          page = a.ring[at];
+        }
+        if (page >= 0 && page < a.n_pages) slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        else bad = true;
+      }
+    }
+    a.slots[r] = slot;
+    if (a.positions) a.positions[r] = pos;
+  }
+  if (bad) set_status(a.status, DFLASH_DEV_CAPACITY);
+  // every CTA has read what the first now updates
+  if (gridDim.x > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (rank != 0) return;
+  for (int s = tid; s < a.n_seq; s += kThreads) {
+    const Request q = request(a, s);
+    const int take0 = s ? take_end[s - 1] : 0, take1 = take_end[s];
+    a.held_out[s] = q.fits && (take1 == take0 || take1 <= free_pages) ? q.need : q.held;
+    a.row_offsets[s + 1] = row_end[s];
+  }
+  if (tid == 0) {
+    a.row_offsets[0] = 0;
+    int h = ring0 + taken;
+    if (h >= a.n_pages) h -= a.n_pages;
+    a.ring_out[0] = h;
+    a.ring_out[1] = free_pages - taken + given;
+  }
+}
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" int dflash_page_tables(const int32_t* lengths, const int32_t* new_rows, int32_t n_seq, int32_t page_size,
+                                  int32_t n_pages, const int32_t* held_in, int32_t* held_out, int32_t* table,
+                                  int32_t table_stride, int32_t* ring, const int32_t* ring_in, int32_t* ring_out,
+                                  int32_t* row_offsets, int32_t* slots, int32_t* positions, int32_t row_cap,
+                                  int32_t* dev_status, dflash_stream_t stream) {
+  if (!lengths || !new_rows || !held_in || !held_out || !table || !ring || !ring_in || !ring_out || !row_offsets)
+    return DFLASH_ERR_INVALID_ARG;
+  if (n_seq < 1 || table_stride < 1 || n_pages < 1 || row_cap < 0 || (row_cap > 0 && !slots))
+    return DFLASH_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return DFLASH_ERR_UNSUPPORTED;
+  if (n_seq > kMaxRequests || static_cast<long long>(n_pages) * page_size > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
+  PageArgs a{lengths, new_rows, n_seq, 0, n_pages, held_in, held_out, table, table_stride, ring, ring_in, ring_out,
+             row_offsets, slots, positions, row_cap, dev_status};
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  cudaLaunchConfig_t cfg = {};
+  // one CTA for a step's rows; the whole cluster for prompts
+  cfg.gridDim = dim3(row_cap <= 4 * kThreads ? 1 : kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 3 * sizeof(int) * n_seq;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cfg.gridDim.x;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               3 * static_cast<int>(sizeof(int)) * kMaxRequests);
+    if (e != cudaSuccess) return cuda_status(e, "page tables");
+  }
+  return cuda_status(cudaLaunchKernelEx(&cfg, page_tables_kernel, a), "page tables");
+}

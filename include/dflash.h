@@ -400,6 +400,157 @@ int dflash_state_read_draft_probs(const dflash_state* state, float* out, dflash_
 int dflash_head_argmax_static(const dflash_model* model, const float* hidden, int32_t n_rows, int32_t* ids,
                               int32_t* dev_status, dflash_stream_t stream);
 
+/* ------------------------------------------------------ the verify step
+ * Operators of the step that checks a block beside the draft pass: the paged
+ * K/V cache of a served model in 4 bits, its page tables, the attention that
+ * reads it for single tokens and for blocks, and the scores of the verifier's
+ * logits.  They need no dflash_model: they run on the current CUDA device,
+ * which the stream and every pointer must belong to.  The pages have no
+ * counterpart of them.
+ *
+ * A cache's cells are numbered: cell = page * page_size + offset.  Requests
+ * address them through a table of page ids, [n_seq, table_stride] int32, the
+ * cell of position p of request s lying in page table[s][p / page_size].
+ * A slot is a cell number, or -1 for a row without a cell. */
+
+/* Element types of the operators' tensors. */
+enum dflash_value_type { DFLASH_T_FP32 = 0, DFLASH_T_BF16 = 1, DFLASH_T_FP16 = 2 };
+
+/* The 4-bit cache: a host description of caller-owned device memory,
+ *   uint8 [n_pages][n_kv_heads][page_size / 16][18 * head_dim].
+ * Per 32 consecutive channels of a cell's K (or V) row the cache holds an
+ * FP16 scale d and 4-bit codes c; a value is d * (c - 8).  The 18 * head_dim
+ * bytes of 16 cells are: K codes (16 rows of head_dim / 2 bytes), K scales (16
+ * rows of head_dim / 32), V codes, V scales.  Word w of a row of codes holds
+ * channels 8w .. 8w + 7, channel 8w + i in bits 4i .. 4i + 3, with c = cell % 16
+ * and D = head_dim, at word
+ *   K: ((w % 4) * (D / 32) + w / 4) ^ (D == 256 ? 4 * ((c / 4) % 2) : 0)
+ *   V: ((w % 8) ^ (D == 256 ? 2 * (c % 4) : D == 128 ? 4 * ((c / 2) % 2) : 0)) * (D / 64) + w / 8
+ * of the row; V's scale of block b is at place (b % 2) * (D / 64) + b / 2 of its
+ * row, K's at place b.
+ * data: 16-byte aligned.  page_size: 16, 32, 64, 128 or 256.  head_dim: 64,
+ * 128 or 256.  1 <= n_kv_heads <= 256.  n_pages * page_size < 2^31. */
+typedef struct dflash_kv4_cache {
+  void* data;
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+} dflash_kv4_cache;
+
+/* Host-only check of a description; DFLASH_OK if the operators take it. */
+int dflash_kv4_check(const dflash_kv4_cache* cache);
+/* Bytes of a cache's memory (0 for a geometry the check refuses). */
+size_t dflash_kv4_bytes(int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim);
+
+/* Bring the requests' pages up to date and find the cells of the rows they
+ * append, from lengths that may live on the device only.
+ *   lengths:  [n_seq] int32, tokens each request holds before the step (the
+ *             position of its first new row).
+ *   new_rows: [n_seq] int32, rows it appends.  Where either is negative the
+ *             request is left alone: it keeps its pages and has no rows.  A
+ *             finished request (0, 0) gives all of its pages back.
+ *   held_in / held_out: [n_seq] int32, pages held before and after.
+ *   table:    [n_seq, table_stride] int32, in and out: page ids.  Entries up
+ *             to held are read, entries of pages taken are written, all
+ *             others stay as they were.
+ *   ring:     [n_pages] int32, in and out: the free pages, a ring.
+ *   ring_in / ring_out: [2] int32, the ring's head and the count of free pages
+ *             before and after.
+ *   row_offsets: [n_seq + 1] int32 out: request s's rows are
+ *             [row_offsets[s], row_offsets[s + 1]).
+ *   slots:    [row_cap] int32 out: each row's cell; -1 behind the last row.
+ *   positions: optional [row_cap] int32 out: each row's position, else -1.
+ * A request then holds ceil((length + new_rows) / page_size) pages: it takes
+ * what it lacks from the ring's head, requests in order, or puts what it has
+ * too much at the ring's tail, where this call takes none of them.  If
+ * the free pages do not suffice, the first request that lacks some and every
+ * later one that lacks any get none, keep what they held, and their rows have
+ * slot -1; the same holds for a request whose pages do not fit table_stride:
+ * DFLASH_DEV_CAPACITY.  The same bit reports more rows than row_cap (those
+ * beyond are dropped), a page id outside [0, n_pages) (slot -1), a ring head or
+ * count out of range, and more pages given back than the ring has room for.
+ * held_out may be held_in and ring_out may be ring_in; no other arrays may
+ * overlap.  n_seq <= 4096 (else DFLASH_ERR_CAPACITY).  One launch. */
+int dflash_page_tables(const int32_t* lengths, const int32_t* new_rows, int32_t n_seq, int32_t page_size,
+                       int32_t n_pages, const int32_t* held_in, int32_t* held_out, int32_t* table,
+                       int32_t table_stride, int32_t* ring, const int32_t* ring_in, int32_t* ring_out,
+                       int32_t* row_offsets, int32_t* slots, int32_t* positions, int32_t row_cap,
+                       int32_t* dev_status, dflash_stream_t stream);
+
+/* Quantise n_rows rows of K and V into the cells `slots` names.
+ *   k, v:  rows of n_kv_heads * head_dim values (BF16 or FP16: `type`),
+ *          k_stride / v_stride elements apart (multiples of 8; a fused
+ *          projection's output can be passed as it is), 16-byte aligned.
+ *   slots: [n_rows] int32, distinct; a negative slot skips its row, one beyond
+ *          the cache too, with DFLASH_DEV_CAPACITY.
+ * Per block of 32 channels: m is the value of largest magnitude (the first of
+ * equals), d = fp16(m / -8), code = min(max(rint(x / d), -8), 7) + 8 with
+ * halves to even, 8 where d is 0.  A block with a value beyond FP16's range, an
+ * infinity or a NaN is stored as zeros and reported as DFLASH_DEV_NONFINITE. */
+int dflash_kv4_write(const dflash_kv4_cache* cache, const void* k, const void* v, int32_t type, int64_t k_stride,
+                     int64_t v_stride, const int32_t* slots, int32_t n_rows, int32_t* dev_status,
+                     dflash_stream_t stream);
+
+/* Read cells back as float (exact), [n_rows, n_kv_heads, head_dim] each; k_out
+ * or v_out may be NULL.  Rows with a slot outside the cache are zeros (beyond
+ * it: DFLASH_DEV_CAPACITY too).  Outputs 16-byte aligned. */
+int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t n_rows, float* k_out, float* v_out,
+                    int32_t* dev_status, dflash_stream_t stream);
+
+/* Attention of n_seq sequences' rows over their cells.
+ *   q, out: [n_tokens] rows of n_q_heads * head_dim values (BF16 or FP16:
+ *           `type`), q_stride / out_stride elements apart (multiples of 8),
+ *           16-byte aligned; q head h reads kv head h / (n_q / n_kv).
+ *   row_offsets: [n_seq + 1] int32: sequence s's rows are
+ *           [row_offsets[s], row_offsets[s + 1]), at most max_rows (1 .. 8) of
+ *           them; (n_q / n_kv) * max_rows <= 128.
+ *   kv_len: [n_seq] int32, the cells of each sequence, those of its rows
+ *           among them: row i of r is at position kv_len - r + i.
+ *   table:  [n_seq, table_stride] int32, page ids.
+ *   causal: non-zero: a row sees the positions up to its own; zero: all
+ *           kv_len.  window W > 0: of those only the W last.
+ *   scale:  the softmax scale, finite and positive.
+ * A row that sees no cell is written as zeros.  Rows of no sequence are left
+ * as they were.  Scores, sums and O are FP32; K enters exactly, V and the
+ * probabilities rounded to FP16.  Cells that no row sees may hold anything,
+ * pages behind the last cell of a sequence are not looked up.
+ * DFLASH_DEV_BAD_BLOCK: offsets that descend, pass n_tokens or hold more than
+ * max_rows rows (that sequence is skipped).  DFLASH_DEV_CAPACITY: a kv_len
+ * beyond the table's width (clamped), a page id outside the cache.
+ * DFLASH_DEV_NONFINITE: a row whose scores are not finite.
+ *   workspace: dflash_kv4_attention_workspace bytes, 16-byte aligned; calls
+ *           that overlap in time need one each.  Nothing in it has to be set
+ *           or outlives the call.
+ * n_seq <= 1024 (else DFLASH_ERR_CAPACITY). */
+int dflash_kv4_attention(const dflash_kv4_cache* cache, const void* q, void* out, int32_t type, int64_t q_stride,
+                         int64_t out_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_seq, int32_t max_rows,
+                         const int32_t* row_offsets, const int32_t* kv_len, const int32_t* table, int32_t table_stride,
+                         int32_t causal, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+                         int32_t* dev_status, dflash_stream_t stream);
+/* Workspace of such a call on the current device (0: arguments it refuses). */
+size_t dflash_kv4_attention_workspace(const dflash_kv4_cache* cache, int32_t n_q_heads, int32_t n_seq, int32_t max_rows,
+                                      int32_t table_stride);
+
+/* Scores of n_rows rows of logits (FP32, BF16 or FP16: `type`), row_stride
+ * elements apart (any stride >= vocab; any alignment of the type).
+ *   tokens, logprob: [n_rows] int32 in, [n_rows] float out, or both NULL: the log
+ *           probability of row i's token; 0 for token -1 (none), any other id
+ *           outside [0, vocab) is DFLASH_DEV_BAD_TOKEN and 0.
+ *   entropy: optional [n_rows] float out, of the whole distribution, in nats.
+ *   top_k:  0 .. 32 (more: DFLASH_ERR_CAPACITY); top_ids [n_rows, top_k] int32 and
+ *           top_logprobs [n_rows, top_k] float out, the likeliest tokens in
+ *           descending order, ties to the lowest id: top_ids[i][0] is the
+ *           greedy id that dflash_accept takes.
+ * A logit of -infinity is a masked token: it has probability 0 and is no
+ * alternative (id -1, log probability -infinity where fewer than top_k are left).
+ * A row with every token masked has entropy 0 and log probabilities
+ * -infinity.  A NaN or +infinity sets DFLASH_DEV_NONFINITE; that row's outputs are
+ * unspecified.  workspace: dflash_token_logprobs_workspace bytes (may be 0),
+ * 16-byte aligned, not shared by calls that overlap in time. */
+int dflash_token_logprobs(const void* logits, int32_t type, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                          const int32_t* tokens, float* logprob, float* entropy, int32_t top_k, int32_t* top_ids,
+                          float* top_logprobs, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          dflash_stream_t stream);
+size_t dflash_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t type, int32_t top_k);
+
 #ifdef __cplusplus
 }
 #endif
