@@ -25,10 +25,15 @@
 // rounded to FP16 (2^-12 relative at most, 2^-25 absolute; the sums are FP32 of
 // the unrounded p).
 //
-// Work: 4 warps per CTA, each walks every fourth step of 32 cells of the
-// CTA's range with its own maximum, sum and O in registers; bulk copies of
-// whole groups (K, V and scales together) run a ring of stages ahead per warp.
-// At a segment's end the warps' results are joined through the ring's memory.
+// Work: the 4 warps of a CTA take a tile of 64 (D 256) or 128 cells together.
+// For S^T each warp has its own 16 or 32 cells and all channels; P goes through
+// shared memory; for O^T each warp has its own quarter of the channels and all
+// cells.  So O is 16 registers per 8 rows, three CTAs fit an SM, and a segment
+// ends without joining warps.  One barrier per tile orders P, the ring's
+// stages and the vote on the maximum: scores are taken relative to a reference
+// that stays until some score passes it by 2^8 (P stays far inside FP16's
+// range), so that the first tile and few others pay for a rescaling.  Bulk copies of
+// whole groups (K, V and scales together) run two tiles ahead.
 #include <cstddef>
 
 #include "kv4_attention.cuh"
@@ -36,21 +41,26 @@
 namespace dflash {
 namespace {
 
-constexpr int kStep = 32;     // cells of a step: two groups
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeast = 4;     // steps that a CTA takes at least: one per warp
+constexpr int kLeast = 1;     // tiles that a CTA takes at least
+constexpr int kPerSm = 3;     // CTAs per SM
+constexpr float kSlack = 8.f; // log2 units by which a score may pass the reference
 
 template <int D, int NT>
 struct Geo {
   static constexpr int R = 8 * NT;                 // rows of a row group
-  static constexpr int STAGE = 2 * Kv4<D>::GROUP_BYTES;
-  static constexpr int STAGES = D == 256 ? 2 : D == 128 ? 4 : 8;
-  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int MT = D == 256 ? 1 : 2;      // 16-cell groups of a warp in a tile
+  static constexpr int GROUPS = kWarps * MT;
+  static constexpr int TILE = 16 * GROUPS;         // cells of a tile
+  static constexpr int STAGE = GROUPS * Kv4<D>::GROUP_BYTES;
+  static constexpr int STAGES = 3;
+  static constexpr int RING = STAGES * STAGE;
   static constexpr int QF = NT * (D / 32) * 512;   // Q fragments
   static constexpr int QS = NT * (D / 32) * 8 * 4; // accumulator start values
-  static constexpr int SMEM = RING + QF + QS;
-  static_assert(kWarps * R * D * 4 <= RING, "the warps' O fit the ring");
+  static constexpr int P = GROUPS * NT * 256;      // P fragments of a tile, double-buffered
+  static constexpr int SMEM = RING + QF + QS + 2 * P;
+  static constexpr int JT = D / 64;                // 16-channel tiles of O^T that a warp owns
 };
 
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
@@ -90,46 +100,47 @@ __device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[N]) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4AttnArgs a) {
   using F = Kv4<D>;
   using G = Geo<D, NT>;
-  constexpr int R = G::R, B = F::BLOCKS, U = D / 64, ST = G::STAGES;
+  constexpr int R = G::R, B = F::BLOCKS, U = D / 64, ST = G::STAGES, MT = G::MT, TILE = G::TILE, JT = G::JT;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* qf = smem + G::RING;                                // [NT][B][32 lanes][16 B]
   float* qstart = reinterpret_cast<float*>(qf + G::QF);        // [NT][B][8 rows]
+  uint8_t* pf = qf + G::QF + G::QS;                            // [2][GROUPS][NT][32 lanes][8 B]
   __shared__ long long pre[kKv4MaxSeq + 1];
   __shared__ long long scratch[kWarps];
-  __shared__ uint64_t bars[kWarps][ST];
+  __shared__ uint64_t full[ST];
   __shared__ float s_factor[R];
-  __shared__ float2 s_ml[kWarps][R];
+  __shared__ float s_max[kWarps][R], s_sum[kWarps][R];
   __shared__ int2 s_sees[R];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int i = 0; i < ST; ++i) mbar_init(&bars[w][i], 1);
+    for (int i = 0; i < ST; ++i) mbar_init(&full[i], kWarps);
     fence_barrier_init();
   }
-  const long long T = kv4_plan<kStep, R>(a, pre, scratch, blockIdx.x == 0);
+  const long long T = kv4_plan<TILE, R>(a, pre, scratch, blockIdx.x == 0);
   const int C = kv4_ctas(T, gridDim.x, kLeast);
   const int c = blockIdx.x;
   pdl_launch_dependents();
-  if (c >= C || T == 0) return;
+  if (c >= C || T == 0) {
+    if (tid == 0) a.jobs[c].n_rows = 0;
+    return;
+  }
   long long x = kv4_start(T, C, c);
   const long long x_end = kv4_start(T, C, c + 1);
 
   const int groups_of_page = 1 << (a.page_shift - 4);
   const int cell_g = (g & 1) ? 7 - (g >> 1) : g >> 1;  // cell of S^T's row g (and 8 + cell_g of row g + 8)
-  uint8_t* my_ring = ring + warp * (ST * G::STAGE);
-  uint64_t* my_bar = bars[warp];
-  uint32_t phases = 0;  // bit i: parity of the next fill of the warp's stage i
-  bool ok = true;
+  uint32_t fills = 0;  // tiles that the ring has taken, over all segments
+  bool ok = true, job = false;
 
   while (x < x_end) {
     const int s = kv4_find(pre, a.n_seq, x);
-    const Kv4Seq q = kv4_seq<kStep, R>(a, s, false);
+    const Kv4Seq q = kv4_seq<TILE, R>(a, s, false);
     const long long rel = x - pre[s];
     const int unit = static_cast<int>(rel / q.steps);
     const int k0 = static_cast<int>(rel - static_cast<long long>(unit) * q.steps);
@@ -137,49 +148,48 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     const int head = unit / q.groups, row0 = unit % q.groups * R;
     const int n_rows = min(R, q.rows * a.G - row0);
     x += k1 - k0;
+    const int n = ok ? k1 - k0 : 0;  // tiles
 
-    // ---- copies: step k's groups go to stage i of the warp's ring
+    // ---- copies: this warp's groups of tile i
     const int32_t* pages = a.table + static_cast<long long>(s) * a.table_stride;
-    // lanes look up the groups of 16 of the warp's steps at a time
-    int my_page = 0, look0 = -1;
-    auto issue = [&](int i) {  // the warp's i-th step
-      const int k = k0 + warp + i * kWarps;
-      if ((i >> 4) != look0) {
-        look0 = i >> 4;
-        const int kk = k0 + warp + ((look0 << 4) + (lane >> 1)) * kWarps;
-        const int pos = q.base + kk * kStep + (lane & 1) * 16;
+    int my_page = 0, looked = -1;
+    auto issue = [&](int i) {
+      if (i / (32 / MT) != looked) {  // the lanes look up the groups of 32 / MT tiles at a time
+        looked = i / (32 / MT);
+        const int ii = looked * (32 / MT) + lane / MT;
+        const int pos = q.base + (k0 + ii) * TILE + (warp * MT + lane % MT) * 16;
         my_page = -1;
-        if (kk < k1 && pos < q.hi) {
-          int page = pages[pos >> a.page_shift];
-          if (page < 0 || page >= a.n_pages) {
+        if (ii < n && pos < q.hi) {
+          my_page = pages[pos >> a.page_shift];
+          if (my_page < 0 || my_page >= a.n_pages) {
             set_status(a.status, DFLASH_DEV_CAPACITY);
-            page = 0;
+            my_page = 0;
           }
-          my_page = page;
         }
       }
-      const int p0 = __shfl_sync(0xffffffffu, my_page, (i & 15) * 2);
-      const int p1 = __shfl_sync(0xffffffffu, my_page, (i & 15) * 2 + 1);
+      const int st = (fills + i) % ST;
+      const int at = i % (32 / MT) * MT;
+      int page[MT], bytes = 0;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        page[j] = __shfl_sync(0xffffffffu, my_page, at + j);
+        bytes += page[j] >= 0 ? F::GROUP_BYTES : 0;
+      }
       if (lane == 0) {
-        const int st = i % ST;
-        uint8_t* dst = my_ring + st * G::STAGE;
-        const int grp = ((q.base + k * kStep) >> 4) & (groups_of_page - 1);
-        const int grp1 = ((q.base + k * kStep + 16) >> 4) & (groups_of_page - 1);
-        mbar_arrive_expect_tx(&my_bar[st], ((p0 >= 0) + (p1 >= 0)) * F::GROUP_BYTES);
-        if (p0 >= 0)
-          bulk_g2s(dst, a.cache + ((static_cast<size_t>(p0) * a.n_kv + head) * groups_of_page + grp) * F::GROUP_BYTES,
-                   F::GROUP_BYTES, &my_bar[st]);
-        if (p1 >= 0)
-          bulk_g2s(dst + F::GROUP_BYTES,
-                   a.cache + ((static_cast<size_t>(p1) * a.n_kv + head) * groups_of_page + grp1) * F::GROUP_BYTES,
-                   F::GROUP_BYTES, &my_bar[st]);
+        mbar_arrive_expect_tx(&full[st], bytes);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const int gi = warp * MT + j;
+          const int grp = ((q.base + (k0 + i) * TILE + gi * 16) >> 4) & (groups_of_page - 1);
+          if (page[j] >= 0)
+            bulk_g2s(ring + st * G::STAGE + gi * F::GROUP_BYTES,
+                     a.cache + ((static_cast<size_t>(page[j]) * a.n_kv + head) * groups_of_page + grp) * F::GROUP_BYTES,
+                     F::GROUP_BYTES, &full[st]);
+        }
       }
     };
-    const int mine = ok && k1 - k0 > warp ? (k1 - k0 - warp + kWarps - 1) / kWarps : 0;  // the warp's steps
-    // the ring was last read (and written, by the join) through the generic proxy
-    fence_proxy_async_smem();
-    __syncthreads();
-    for (int i = 0; i < min(mine, ST); ++i) issue(i);
+    __syncthreads();  // the last segment is done with the ring, Q and P
+    for (int i = 0; i < min(n, ST); ++i) issue(i);
 
     // ---- Q: 8 threads a row find its maximum, scale it and lay out the fragments
     for (int m = tid >> 3; m < R; m += kThreads / 8) {
@@ -251,29 +261,27 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     }
     __syncthreads();
 
-    float o[U][4][NT][4];
+    float o[JT][NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < JT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[u][i][n][e] = 0.f;
-    float m_run[NT][2], l_run[NT][2], fac[NT][2];
-    int2 sees[NT][2];
+        for (int e = 0; e < 4; ++e) o[j][n2][e] = 0.f;
+    // of rows 8 n2 + 2t + e: reference, sum over this lane's cells, factor
+    float m_ref[NT][2], l_run[NT][2], fac[NT][2];
     int all_lo = 0, all_hi = 0x7fffffff;  // cells that every row sees
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m_run[n][e] = -INFINITY;
-        l_run[n][e] = 0.f;
-        fac[n][e] = s_factor[n * 8 + 2 * t + e];
-        sees[n][e] = s_sees[n * 8 + 2 * t + e];
-        if (n * 8 + 2 * t + e < n_rows) {
-          all_lo = max(all_lo, sees[n][e].x);
-          all_hi = min(all_hi, sees[n][e].y);
+        const int m = n2 * 8 + 2 * t + e;
+        m_ref[n2][e] = -INFINITY;
+        l_run[n2][e] = 0.f;
+        fac[n2][e] = s_factor[m];
+        if (m < n_rows) {
+          all_lo = max(all_lo, s_sees[m].x);
+          all_hi = min(all_hi, s_sees[m].y);
         }
       }
 #pragma unroll
@@ -282,26 +290,26 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, w));
     }
 
-    for (int i = 0; i < mine; ++i) {
-      const int st = i % ST;
-      ok = __all_sync(0xffffffffu, mbar_wait(&my_bar[st], (phases >> st) & 1));
-      if (!ok) {
-        // give up: nothing more is issued; what is in flight lands before the CTA ends
-        for (int j = i; j < min(mine, i + ST); ++j) mbar_wait(&my_bar[j % ST], (phases >> (j % ST)) & 1);
-        if (lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
-        break;
-      }
-      phases ^= 1u << st;
-      const uint32_t base = smem_u32(my_ring + st * G::STAGE);
-      const int pos0 = q.base + (k0 + warp + i * kWarps) * kStep;
-      const bool edge = pos0 < all_lo || pos0 + kStep > all_hi;
-      float sc[2][NT][4];
-      // ---- S^T
+    for (int i = 0; i < n; ++i) {
+      const uint32_t fill = fills + i;
+      const int st = fill % ST;
+      const bool late = !mbar_wait(&full[st], (fill / ST) & 1);
+      const uint32_t base = smem_u32(ring + st * G::STAGE);
+      const int pos0 = q.base + (k0 + i) * TILE;
+      const bool edge = pos0 < all_lo || pos0 + TILE > all_hi;
+      // ---- S^T of this warp's cells
+      float sc[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t gb = base + mt * F::GROUP_BYTES;
-        // the lane's words and scales of cells cell_g and 8 + cell_g
-        uint32_t wa[B], wb[B];
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[mt][n2][e] = 0.f;
+      // the lane's words and scales of cells cell_g and 8 + cell_g
+      uint32_t wa[MT][B], wb[MT][B], da[MT][B / 2], db[MT][B / 2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t gb = base + (warp * MT + mt) * F::GROUP_BYTES;
 #pragma unroll
         for (int h = 0; h < (B + 3) / 4; ++h) {
           constexpr int N = B < 4 ? B : 4;
@@ -309,209 +317,229 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           const uint32_t at = gb + cell_g * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cell_g));
           load_words<N>(at, tmp);
 #pragma unroll
-          for (int e = 0; e < N; ++e) wa[4 * h + e] = tmp[e];
+          for (int e = 0; e < N; ++e) wa[mt][4 * h + e] = tmp[e];
           // cell 8 + cell_g: k_swap goes by bit 2 of the cell, the same
           load_words<N>(at + 8 * F::ROW, tmp);
 #pragma unroll
-          for (int e = 0; e < N; ++e) wb[4 * h + e] = tmp[e];
+          for (int e = 0; e < N; ++e) wb[mt][4 * h + e] = tmp[e];
         }
-        uint32_t da[B / 2], db[B / 2];
-        load_words<B / 2>(gb + F::K_SCALES + cell_g * F::SROW, da);
-        load_words<B / 2>(gb + F::K_SCALES + (cell_g + 8) * F::SROW, db);
+        load_words<B / 2>(gb + F::K_SCALES + cell_g * F::SROW, da[mt]);
+        load_words<B / 2>(gb + F::K_SCALES + (cell_g + 8) * F::SROW, db[mt]);
+      }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int b = 0; b < B; ++b) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+        for (int n2 = 0; n2 < NT; ++n2) {
+          const uint4 bq = *reinterpret_cast<const uint4*>(qf + ((n2 * B + b) * 32 + lane) * 16);
+          const float2 start = *reinterpret_cast<const float2*>(qstart + (n2 * B + b) * 8 + 2 * t);
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          const __half2 ha = *reinterpret_cast<const __half2*>(&da[b >> 1]);
-          const __half2 hb = *reinterpret_cast<const __half2*>(&db[b >> 1]);
-          const float fa = (b & 1) ? __high2float(ha) : __low2float(ha);
-          const float fb = (b & 1) ? __high2float(hb) : __low2float(hb);
-          const uint32_t va = wa[b] >> 8, vb = wb[b] >> 8;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 bq = *reinterpret_cast<const uint4*>(qf + ((n * B + b) * 32 + lane) * 16);
-            const float2 start = *reinterpret_cast<const float2*>(qstart + (n * B + b) * 8 + 2 * t);
+          for (int mt = 0; mt < MT; ++mt) {
+            const __half2 ha = *reinterpret_cast<const __half2*>(&da[mt][b >> 1]);
+            const __half2 hb = *reinterpret_cast<const __half2*>(&db[mt][b >> 1]);
+            const float fa = (b & 1) ? __high2float(ha) : __low2float(ha);
+            const float fb = (b & 1) ? __high2float(hb) : __low2float(hb);
+            const uint32_t ua = wa[mt][b], ub = wb[mt][b], va = ua >> 8, vb = ub >> 8;
             float acc[4];
-            mma_from(acc, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, bq.x,
-                     bq.y, start.x, start.y);
+            mma_from(acc, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, bq.x, bq.y, start.x,
+                     start.y);
             mma_f16_16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, bq.z, bq.w);
-            sc[mt][n][0] = fmaf(fa, acc[0], sc[mt][n][0]);
-            sc[mt][n][1] = fmaf(fa, acc[1], sc[mt][n][1]);
-            sc[mt][n][2] = fmaf(fb, acc[2], sc[mt][n][2]);
-            sc[mt][n][3] = fmaf(fb, acc[3], sc[mt][n][3]);
+            sc[mt][n2][0] = fmaf(fa, acc[0], sc[mt][n2][0]);
+            sc[mt][n2][1] = fmaf(fa, acc[1], sc[mt][n2][1]);
+            sc[mt][n2][2] = fmaf(fb, acc[2], sc[mt][n2][2]);
+            sc[mt][n2][3] = fmaf(fb, acc[3], sc[mt][n2][3]);
           }
         }
       }
-      // ---- softmax: maximum over the step's cells, P in the B operand's layout
-      uint32_t pb[2][NT][2];
+      // ---- scores in log2 units; does any pass its row's reference by too much?
+      bool over = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float top[2] = {-INFINITY, -INFINITY};
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float v = sc[mt][n][e] * fac[n][e & 1];
+            float v = sc[mt][n2][e] * fac[n2][e & 1];
             if (edge) {
-              const int pos = pos0 + mt * 16 + cell_g + (e >> 1) * 8;
-              if (pos < sees[n][e & 1].x || pos >= sees[n][e & 1].y) v = -INFINITY;
+              const int pos = pos0 + (warp * MT + mt) * 16 + cell_g + (e >> 1) * 8;
+              const int2 sees = s_sees[n2 * 8 + 2 * t + (e & 1)];
+              if (pos < sees.x || pos >= sees.y) v = -INFINITY;
             }
-            sc[mt][n][e] = v;
-            top[e & 1] = fmaxf(top[e & 1], v);
+            sc[mt][n2][e] = v;
+            over |= v > m_ref[n2][e & 1] + kSlack;
           }
-        float from[2], alpha[2];
+      uint8_t* pt = pf + (i & 1) * G::P;
+      auto write_p = [&](float (&sum)[NT][2]) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int n2 = 0; n2 < NT; ++n2) {
+          const float f0 = m_ref[n2][0] == -INFINITY ? 0.f : m_ref[n2][0];
+          const float f1 = m_ref[n2][1] == -INFINITY ? 0.f : m_ref[n2][1];
+          sum[n2][0] = sum[n2][1] = 0.f;
 #pragma unroll
-          for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], w));
-          const float m_new = fmaxf(m_run[n][e], top[e]);
-          from[e] = m_new == -INFINITY ? 0.f : m_new;
-          alpha[e] = ex2_approx(m_run[n][e] - from[e]);
-          m_run[n][e] = m_new;
-          l_run[n][e] *= alpha[e];
-        }
-        if (__any_sync(0xffffffffu, alpha[0] < 1.f || alpha[1] < 1.f)) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[u][j][n][e] *= alpha[e & 1];
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(sc[mt][n][e] - from[e & 1]);
-            l_run[n][e & 1] += p[e];
+          for (int mt = 0; mt < MT; ++mt) {
+            const float p0 = ex2_approx(sc[mt][n2][0] - f0), p1 = ex2_approx(sc[mt][n2][1] - f1);
+            const float p2 = ex2_approx(sc[mt][n2][2] - f0), p3 = ex2_approx(sc[mt][n2][3] - f1);
+            sum[n2][0] += p0 + p2;
+            sum[n2][1] += p1 + p3;
+            *reinterpret_cast<uint2*>(pt + (((warp * MT + mt) * NT + n2) * 32 + lane) * 8) =
+                make_uint2(movmatrix_t(pack_f16x2(p0, p1)), movmatrix_t(pack_f16x2(p2, p3)));
           }
-          pb[mt][n][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
-          pb[mt][n][1] = movmatrix_t(pack_f16x2(p[2], p[3]));
         }
+      };
+      float sum[NT][2];
+      write_p(sum);
+      if (__syncthreads_or(over || late)) {
+        if (__syncthreads_or(late)) {
+          // a copy did not come in time: nothing more is issued or computed; what
+          // is in flight lands before the CTA ends
+          for (int j = i; j < min(n, i + ST); ++j) mbar_wait(&full[(fills + j) % ST], ((fills + j) / ST) & 1);
+          if (tid == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
+          ok = false;
+          break;
+        }
+        // new references: the rows' maxima so far over all warps
+        float top[NT][2];
+#pragma unroll
+        for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n2][e], sc[mt][n2][2 + e]));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
+            top[n2][e] = v;
+            if (g == 0) s_max[warp][n2 * 8 + 2 * t + e] = v;
+          }
+        __syncthreads();
+#pragma unroll
+        for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = m_ref[n2][e];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v = fmaxf(v, s_max[w][n2 * 8 + 2 * t + e]);
+            const float alpha = v == -INFINITY ? 0.f : ex2_approx(m_ref[n2][e] - v);
+            m_ref[n2][e] = v;
+            l_run[n2][e] *= alpha;
+#pragma unroll
+            for (int j = 0; j < JT; ++j) {
+              o[j][n2][e] *= alpha;
+              o[j][n2][2 + e] *= alpha;
+            }
+          }
+        write_p(sum);
+        __syncthreads();
       }
-      // ---- O^T: cells t, 7 - t and 8 + t, 15 - t of each group
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t gb = base + mt * F::GROUP_BYTES;
-        uint32_t vw[4][U];
-        uint32_t vs[4][(U + 1) / 2];
+      for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l_run[n2][e] += sum[n2][e];
+      // every warp has finished the tile before: its stage takes a new one
+      if (i > 0 && i - 1 + ST < n) issue(i - 1 + ST);
+      // ---- O^T: cells t, 7 - t and 8 + t, 15 - t of each group, this warp's channels
+      const int u = warp * JT / 4, j0 = warp * JT % 4;  // its word of each V chunk, its first 16-channel tile in the word
+#pragma unroll
+      for (int gi = 0; gi < G::GROUPS; ++gi) {
+        const uint32_t gb = base + gi * F::GROUP_BYTES;
+        uint32_t vw[4], vs[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int cell = (k & 1 ? 7 - t : t) + (k >> 1) * 8;
-          load_words<U>(gb + F::V_CODES + cell * F::ROW + 4 * U * (g ^ F::v_swap(cell)), vw[k]);
-          const uint32_t at = gb + F::V_SCALES + cell * F::SROW + (g >> 2) * (U * 2);
-          if constexpr (U == 1) {
-            uint16_t h;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-            vs[k][0] = h;
-          } else {
-            load_words<U / 2>(at, vs[k]);
-          }
+          vw[k] = lds32(gb + F::V_CODES + cell * F::ROW + 4 * (U * (g ^ F::v_swap(cell)) + u));
+          uint16_t h;
+          asm volatile("ld.shared.u16 %0, [%1];"
+                       : "=h"(h)
+                       : "r"(gb + F::V_SCALES + cell * F::SROW + ((g >> 2) * U + u) * 2));
+          vs[k] = h;
           if (edge) {  // cells that no row sees may hold anything: no weight times NaN
-            const int pos = pos0 + mt * 16 + cell;
-            if (pos < q.lo || pos >= q.hi) {
-#pragma unroll
-              for (int e = 0; e < (U + 1) / 2; ++e) vs[k][e] = 0;
-            }
+            const int pos = pos0 + gi * 16 + cell;
+            if (pos < q.lo || pos >= q.hi) vs[k] = 0;
           }
         }
+        const uint32_t d0 = prmt(vs[0], vs[1], 0x5410), d1 = prmt(vs[2], vs[3], 0x5410);
+        uint2 pb[NT];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t sel = (u & 1) ? 0x7632u : 0x5410u;
-          const uint32_t d0 = prmt(vs[0][u >> 1], vs[1][u >> 1], sel);
-          const uint32_t d1 = prmt(vs[2][u >> 1], vs[3][u >> 1], sel);
+        for (int n2 = 0; n2 < NT; ++n2)
+          pb[n2] = *reinterpret_cast<const uint2*>(pt + ((gi * NT + n2) * 32 + lane) * 8);
+        uint32_t lo[2], hi[2];
+        if constexpr (JT == 4) {
+          lo[0] = prmt(vw[0], vw[1], 0x5410), hi[0] = prmt(vw[2], vw[3], 0x5410);
+          lo[1] = prmt(vw[0], vw[1], 0x7632), hi[1] = prmt(vw[2], vw[3], 0x7632);
+        } else {
+          const uint32_t sel = j0 >= 2 ? 0x7632u : 0x5410u;
+          lo[0] = prmt(vw[0], vw[1], sel), hi[0] = prmt(vw[2], vw[3], sel);
+          if (JT == 1 && (j0 & 1)) lo[0] >>= 8, hi[0] >>= 8;
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // channels 64u + 8g + 2j, + 1
-            const uint32_t half = (j >> 1) ? 0x7632u : 0x5410u;
-            uint32_t lo = prmt(vw[0][u], vw[1][u], half), hi = prmt(vw[2][u], vw[3][u], half);
-            if (j & 1) {
-              lo >>= 8;
-              hi >>= 8;
-            }
-            constexpr uint32_t MINUS_1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, MINUS_72 = 0xd480d480u;
-            const uint32_t a0 = hmul2_u32(hfma2_u32(and_or(lo, 0x000f000fu, 0x64006400u), 0x3c003c00u, MINUS_1032), d0);
-            const uint32_t a1 = hmul2_u32(hfma2_u32(and_or(lo, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d0);
-            const uint32_t a2 = hmul2_u32(hfma2_u32(and_or(hi, 0x000f000fu, 0x64006400u), 0x3c003c00u, MINUS_1032), d1);
-            const uint32_t a3 = hmul2_u32(hfma2_u32(and_or(hi, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d1);
+        for (int j = 0; j < JT; ++j) {  // channels 64u + 8g + 2 (j0 + j), + 1
+          const uint32_t l = (j & 1) ? lo[j >> 1] >> 8 : lo[j >> 1], h = (j & 1) ? hi[j >> 1] >> 8 : hi[j >> 1];
+          constexpr uint32_t ONE = 0x3c003c00u, MINUS_1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, MINUS_72 = 0xd480d480u;
+          const uint32_t a0 = hmul2_u32(hfma2_u32(and_or(l, 0x000f000fu, 0x64006400u), ONE, MINUS_1032), d0);
+          const uint32_t a1 = hmul2_u32(hfma2_u32(and_or(l, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d0);
+          const uint32_t a2 = hmul2_u32(hfma2_u32(and_or(h, 0x000f000fu, 0x64006400u), ONE, MINUS_1032), d1);
+          const uint32_t a3 = hmul2_u32(hfma2_u32(and_or(h, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16_16816(o[u][j][n], a0, a1, a2, a3, pb[mt][n][0], pb[mt][n][1]);
-          }
+          for (int n2 = 0; n2 < NT; ++n2) mma_f16_16816(o[j][n2], a0, a1, a2, a3, pb[n2].x, pb[n2].y);
         }
       }
-      __syncwarp();
-      if (i + ST < mine) issue(i + ST);
     }
-    // ---- join the warps: factors to the common maximum, then sums through the ring's memory
+    fills += n;
+    // ---- the rows' sums over all warps
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], w);
-        if (g == 0) s_ml[warp][n * 8 + 2 * t + e] = make_float2(m_run[n][e], l_run[n][e]);
-      }
-    __syncthreads();
-    float* buf = reinterpret_cast<float*>(ring);  // [warp][row][D]
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int m = n * 8 + 2 * t + e;
-        float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][m].x);
-        const float f = top == -INFINITY ? 0.f : ex2_approx(m_run[n][e] - top);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float* dst = buf + (warp * R + m) * D + 64 * u + 8 * g;
-          *reinterpret_cast<float4*>(dst) =
-              make_float4(o[u][0][n][e] * f, o[u][0][n][2 + e] * f, o[u][1][n][e] * f, o[u][1][n][2 + e] * f);
-          *reinterpret_cast<float4*>(dst + 4) =
-              make_float4(o[u][2][n][e] * f, o[u][2][n][2 + e] * f, o[u][3][n][e] * f, o[u][3][n][2 + e] * f);
-        }
+        for (int w = 4; w < 32; w <<= 1) l_run[n2][e] += __shfl_xor_sync(0xffffffffu, l_run[n2][e], w);
+        if (g == 0) s_sum[warp][n2 * 8 + 2 * t + e] = l_run[n2][e];
       }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == q.steps;
     const int slot = 2 * c + (k0 == 0 ? 1 : 0);
-    for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
-      const int m = i / (D / 4), col = i % (D / 4) * 4;
-      float top = -INFINITY;
+    const int col = 64 * (warp * JT / 4) + 8 * g + 2 * (warp * JT % 4);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][m].x);
-      const float from = top == -INFINITY ? 0.f : top;
-      float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
+    for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(buf + (w * R + m) * D + col);
-        r.x += v.x;
-        r.y += v.y;
-        r.z += v.z;
-        r.w += v.w;
-        l = fmaf(s_ml[w][m].y, ex2_approx(s_ml[w][m].x - from), l);
+      for (int e = 0; e < 2; ++e) {
+        const int m = n2 * 8 + 2 * t + e;
+        if (m >= n_rows) continue;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += s_sum[w][m];
+        float f = 1.f;
+        if (whole) {
+          f = l > 0.f ? 1.f / l : 0.f;
+          if (!(l < INFINITY)) set_status(a.status, DFLASH_DEV_NONFINITE);
+          const int row = row0 + m;
+          uint16_t* dst = a.out + (q.r0 + row / a.G) * a.out_stride + (head * a.G + row % a.G) * D + col;
+          uint32_t w[JT];
+#pragma unroll
+          for (int j = 0; j < JT; ++j)
+            w[j] = a.bf16 ? pack_bf16x2(o[j][n2][e] * f, o[j][n2][2 + e] * f) : pack_f16x2(o[j][n2][e] * f, o[j][n2][2 + e] * f);
+          if constexpr (JT == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          else if constexpr (JT == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+          else *reinterpret_cast<uint32_t*>(dst) = w[0];
+        } else {
+          float* dst = a.part + (static_cast<size_t>(slot) * R + m) * D + col;
+#pragma unroll
+          for (int j = 0; j < JT; ++j) __stcg(reinterpret_cast<float2*>(dst) + j, make_float2(o[j][n2][e], o[j][n2][2 + e]));
+          if (warp == 0 && g == 0) __stcg(a.part_ml + static_cast<size_t>(slot) * R + m, make_float2(m_ref[n2][e], l));
+        }
       }
-      if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        if (!(l < INFINITY)) set_status(a.status, DFLASH_DEV_NONFINITE);
-        const int row = row0 + m;
-        uint16_t* dst = a.out + (q.r0 + row / a.G) * a.out_stride + (head * a.G + row % a.G) * D + col;
-        *reinterpret_cast<uint2*>(dst) =
-            a.bf16 ? make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv))
-                   : make_uint2(pack_f16x2(r.x * inv, r.y * inv), pack_f16x2(r.z * inv, r.w * inv));
-      } else {
-        __stcg(reinterpret_cast<float4*>(a.part + (static_cast<size_t>(slot) * R + m) * D + col), r);
-        if (col == 0) __stcg(a.part_ml + static_cast<size_t>(slot) * R + m, make_float2(top, l));
+    if (!whole && k0 == 0) {  // the segment goes on in the next CTAs
+      job = true;
+      if (tid == 0) {
+        const long long end = x - k1 + q.steps;  // first step behind the segment
+        Kv4Job r{q.r0, row0, head, n_rows, kv4_owner(T, C, end - 1), {0, 0, 0}};
+        a.jobs[c] = r;
       }
     }
   }
+  if (!job && tid == 0) a.jobs[c].n_rows = 0;
 }
 
-
 template <int D, int NT>
-cudaError_t launch_attn(const Kv4AttnArgs& a, int most, cudaStream_t st) {
+cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
   using G = Geo<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
@@ -519,20 +547,23 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, int most, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || most == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(most, G::R);
-  cfg.blockDim = dim3(256);
+  // one block per segment that may be split and per row and 64 channels of it, fewer where there are many
+  const int z = G::R * (D / 64), y = 2048 / jobs;
+  cfg.gridDim = dim3(jobs, y < 1 ? 1 : y < z ? y : z);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, kStep, G::R>, a, most, kLeast);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, G::R>, a, most);
 }
 
-// Rows per kv head that a call can have choose the width of the row groups.
+// What the host knows of a call: 8-row tiles of a row group, CTAs and
+// segments at most.
 struct Shape {
-  int nt, most;
+  int nt, most, jobs;
 };
 cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Shape* out) {
   int dev = 0, sms = 0;
@@ -540,11 +571,16 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int rows = n_q_heads / c->n_kv_heads * max_rows;
-  out->nt = rows <= 8 ? 1 : 2;
-  const long long groups = (rows + 8 * out->nt - 1) / (8 * out->nt);
-  const long long steps = (static_cast<long long>(table_stride) * c->page_size + kStep - 1) / kStep + 1;
-  const long long ctas = (static_cast<long long>(n_seq) * c->n_kv_heads * groups * steps + kLeast - 1) / kLeast;
-  out->most = static_cast<int>(ctas < 2 * sms ? ctas : 2 * sms);
+  // as few row groups as 32 rows allow, each no wider than it needs
+  const int groups = (rows + 31) / 32;
+  out->nt = ((rows + groups - 1) / groups + 7) / 8;
+  const int tile = c->head_dim == 256 ? 64 : 128;
+  const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads * groups;
+  // (a window may begin anywhere in a tile)
+  const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
+  const long long ctas = (segments * tiles + kLeast - 1) / kLeast;
+  out->most = static_cast<int>(ctas < kPerSm * sms ? ctas : kPerSm * sms);
+  out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
   return cudaSuccess;
 }
 
@@ -558,7 +594,17 @@ int check_call(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows
 }
 
 size_t bytes_of(const dflash_kv4_cache* c, const Shape& s) {
-  return static_cast<size_t>(2 * s.most) * 8 * s.nt * (c->head_dim * 4 + 8);
+  return s.most * (sizeof(Kv4Job) + 2 * size_t(8) * s.nt * (c->head_dim * 4 + 8));
+}
+
+template <int D>
+cudaError_t launch_nt(const Kv4AttnArgs& a, const Shape& s, cudaStream_t st) {
+  switch (s.nt) {
+    case 1: return launch_attn<D, 1>(a, s.most, s.jobs, st);
+    case 2: return launch_attn<D, 2>(a, s.most, s.jobs, st);
+    case 3: return launch_attn<D, 3>(a, s.most, s.jobs, st);
+    default: return launch_attn<D, 4>(a, s.most, s.jobs, st);
+  }
 }
 
 }  // namespace
@@ -617,14 +663,15 @@ int dflash_kv4_attention(const dflash_kv4_cache* c, const void* q, void* out, in
   a.causal = causal != 0;
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.part = static_cast<float*>(workspace);
+  a.jobs = static_cast<Kv4Job*>(workspace);
+  a.part = reinterpret_cast<float*>(a.jobs + s.most);
   a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * 8 * s.nt * c->head_dim);
   a.status = dev_status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (c->head_dim) {
-    case 64: e = s.nt == 1 ? launch_attn<64, 1>(a, s.most, st) : launch_attn<64, 2>(a, s.most, st); break;
-    case 128: e = s.nt == 1 ? launch_attn<128, 1>(a, s.most, st) : launch_attn<128, 2>(a, s.most, st); break;
-    default: e = s.nt == 1 ? launch_attn<256, 1>(a, s.most, st) : launch_attn<256, 2>(a, s.most, st); break;
+    case 64: e = launch_nt<64>(a, s, st); break;
+    case 128: e = launch_nt<128>(a, s, st); break;
+    default: e = launch_nt<256>(a, s, st); break;
   }
   return cuda_status(e, "kv4 attention");
 }

@@ -25,6 +25,8 @@ namespace dflash {
 
 constexpr int kKv4MaxSeq = 1024;
 
+struct Kv4Job;
+
 struct Kv4AttnArgs {
   const uint8_t* cache;
   int n_pages, page_shift, n_kv, G;
@@ -41,6 +43,7 @@ struct Kv4AttnArgs {
   float scale_log2;  // softmax scale * log2(e)
   float* part;       // pieces' O [2 C][R][D]
   float2* part_ml;   // [2 C][R]: maximum (log2 units) and sum
+  Kv4Job* jobs;  // [C]
   int32_t* status;
 };
 
@@ -146,69 +149,116 @@ __device__ __forceinline__ int kv4_find(const long long* pre, int n_seq, long lo
   return lo;
 }
 
-// Joins the pieces of one row of a segment: block (c, row); the block of the
-// segment's second CTA does it, the others leave.  o = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i.
-template <int D, int STEP, int R>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int most, int least) {
-  __shared__ long long pre[kKv4MaxSeq + 1];
-  __shared__ long long scratch[8];
-  constexpr int LANES = D / 4, PAR = 256 / LANES;
-  __shared__ float4 acc[256];
-  __shared__ float accl[PAR];
-  const int c = blockIdx.x, m = blockIdx.y;
-  const long long T = kv4_plan<STEP, R>(a, pre, scratch, false);
+// What a split segment's first CTA leaves for the merge kernel.
+struct Kv4Job {
+  int r0, row0, head, n_rows;  // n_rows 0: no segment that goes on begins in this CTA
+  int last, pad[3];            // CTA of the last piece; the others lie between
+};
+
+// Joins the pieces of split segments: o = sum_i 2^(m_i - m) O_i /
+// sum_i 2^(m_i - m) l_i.  Block (j, z): the j-th split segment, found by
+// counting the records; its rows and 64-channel slices z, z + gridDim.y, ...
+// 16 lanes hold a slice, 16 groups of them take every 16th piece, so that a
+// segment of 150 pieces costs a thread ten loads in flight, not 150 in turn.
+constexpr int kMergeThreads = 256;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnArgs a, int most) {
+  __shared__ int s_count[kMergeThreads / 32];
+  __shared__ int s_cta;
+  __shared__ float4 acc[kMergeThreads];
+  __shared__ float2 accl[16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_cta = -1;
   pdl_wait();
-  const int C = kv4_ctas(T, most, least);
-  if (c == 0 || c >= C || T == 0) return;
-  const long long x = kv4_start(T, C, c);
-  const int s = kv4_find(pre, a.n_seq, x);
-  const Kv4Seq q = kv4_seq<STEP, R>(a, s, false);
-  const long long rel = x - pre[s];
-  const int unit = static_cast<int>(rel / q.steps);  // head * groups + row group
-  const long long b0 = pre[s] + static_cast<long long>(unit) * q.steps, b1 = b0 + q.steps;
-  if (x == b0 || kv4_owner(T, C, b0) != c - 1) return;
-  const int head = unit / q.groups, rg = unit % q.groups;
-  const int row = rg * R + m;
-  if (row >= q.rows * a.G) return;
-  const int last = kv4_owner(T, C, b1 - 1);
-  const int n = last - c + 2;  // pieces: CTA c - 1 and c .. last
-  auto slot = [&](int i) { return 2 * (c - 1 + i) + (i == 0); };
-  const int lane = threadIdx.x % LANES, p = threadIdx.x / LANES;
-  float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.part_ml + static_cast<size_t>(slot(i)) * R + m).x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int i = p; i < n; i += PAR) {
-    const size_t at = static_cast<size_t>(slot(i)) * R + m;
-    const float2 ml = __ldcg(a.part_ml + at);
-    const float w = ex2_approx(ml.x - base);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + lane);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-    l = fmaf(w, ml.y, l);
+  int before = 0;  // split segments of earlier CTAs
+  for (int c0 = 0; c0 < most; c0 += kMergeThreads) {
+    const int c = c0 + tid;
+    const bool is = c < most && __ldcg(&a.jobs[c].n_rows) > 0;
+    const unsigned m = __ballot_sync(0xffffffffu, is);
+    if (lane == 0) s_count[warp] = __popc(m);
+    __syncthreads();
+    int n = before + __popc(m & ((1u << lane) - 1));
+    for (int w = 0; w < kMergeThreads / 32; ++w) {
+      if (w < warp) n += s_count[w];
+      before += s_count[w];
+    }
+    if (is && n == static_cast<int>(blockIdx.x)) s_cta = c;
+    __syncthreads();
   }
-  acc[threadIdx.x] = o;
-  if (lane == 0) accl[p] = l;
-  __syncthreads();
-  if (p != 0) return;
-  for (int i = 1; i < PAR; ++i) {
-    const float4 v = acc[i * LANES + lane];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
-    l += accl[i];
+  const int c = s_cta;
+  if (c < 0) return;
+  const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));
+  const int last = __ldcg(&a.jobs[c].last);
+  const int n = last - c + 1;
+  auto slot = [&](int i) { return 2 * (c + i) + (i == 0); };
+  const int l16 = tid & 15, p = tid >> 4;
+  for (int z = blockIdx.y; z < j0.w * (D / 64); z += gridDim.y) {
+    const int m = z / (D / 64), col = (z % (D / 64)) * 64 + l16 * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, top = -INFINITY;
+    constexpr int U = 4;
+    for (int i0 = p; i0 < n; i0 += 16 * U) {
+      float2 ml[U];
+      float4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 16 * u;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const size_t at = static_cast<size_t>(slot(i)) * R + m;
+          ml[u] = __ldcg(a.part_ml + at);
+          v[u] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + col));
+        }
+      }
+      float t = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) t = fmaxf(t, ml[u].x);
+      const float from = t == -INFINITY ? 0.f : t, f = ex2_approx(top - from);
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      l *= f;
+      top = t;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2_approx(ml[u].x - from);
+        o.x = fmaf(w, v[u].x, o.x);
+        o.y = fmaf(w, v[u].y, o.y);
+        o.z = fmaf(w, v[u].z, o.z);
+        o.w = fmaf(w, v[u].w, o.w);
+        l = fmaf(w, ml[u].y, l);
+      }
+    }
+    __syncthreads();  // the last round's sums have been read
+    acc[tid] = o;
+    if (l16 == 0) accl[p] = make_float2(top, l);
+    __syncthreads();
+    if (p == 0) {
+      float t = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t = fmaxf(t, accl[i].x);
+      const float from = t == -INFINITY ? 0.f : t;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float w = ex2_approx(accl[i].x - from);
+        const float4 v = acc[i * 16 + l16];
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+        l = fmaf(w, accl[i].y, l);
+      }
+      if (!(l < INFINITY) && l16 == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int row = j0.y + m;
+      uint16_t* dst = a.out + (j0.x + row / a.G) * a.out_stride + (j0.z * a.G + row % a.G) * D + col;
+      *reinterpret_cast<uint2*>(dst) =
+          a.bf16 ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv))
+                 : make_uint2(pack_f16x2(o.x * inv, o.y * inv), pack_f16x2(o.z * inv, o.w * inv));
+    }
   }
-  if (!(l < INFINITY) && lane == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* dst = a.out + (q.r0 + row / a.G) * a.out_stride + (head * a.G + row % a.G) * D + lane * 4;
-  const uint2 w = a.bf16 ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv))
-                         : make_uint2(pack_f16x2(o.x * inv, o.y * inv), pack_f16x2(o.z * inv, o.w * inv));
-  *reinterpret_cast<uint2*>(dst) = w;
 }
 
 }  // namespace dflash
