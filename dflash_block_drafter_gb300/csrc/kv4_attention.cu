@@ -47,6 +47,8 @@ constexpr int kLeast = 1;     // tiles that a CTA takes at least
 constexpr int kPerSm = 3;     // CTAs per SM
 constexpr float kSlack = 8.f; // log2 units by which a score may pass the reference
 
+constexpr int kPlanBytes(int n_seq) { return (n_seq + 1) * 8; }
+
 template <int D, int NT>
 struct Geo {
   static constexpr int R = 8 * NT;                 // rows of a row group
@@ -57,7 +59,7 @@ struct Geo {
   static constexpr int STAGES = 3;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int QF = NT * (D / 32) * 512;   // Q fragments
-  static constexpr int QS = NT * (D / 32) * 8 * 4; // accumulator start values
+  static constexpr int QS = NT * 256;              // fragments of the blocks' sums
   static constexpr int P = GROUPS * NT * 256;      // P fragments of a tile, double-buffered
   static constexpr int SMEM = RING + QF + QS + 2 * P;
   static constexpr int JT = D / 64;                // 16-channel tiles of O^T that a warp owns
@@ -65,13 +67,13 @@ struct Geo {
 
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
 
-// D = A B + C for one 16 x 8 tile with a start value.
-__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, float c0, float c1) {
+// D = A B for one 16 x 8 tile.
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
@@ -107,9 +109,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* qf = smem + G::RING;                                // [NT][B][32 lanes][16 B]
-  float* qstart = reinterpret_cast<float*>(qf + G::QF);        // [NT][B][8 rows]
+  __half* qsum = reinterpret_cast<__half*>(qf + G::QF);         // [NT][32 lanes][2 terms][2]
   uint8_t* pf = qf + G::QF + G::QS;                            // [2][GROUPS][NT][32 lanes][8 B]
-  __shared__ long long pre[kKv4MaxSeq + 1];
+  long long* pre = reinterpret_cast<long long*>(pf + 2 * G::P);  // [n_seq + 1]
   __shared__ long long scratch[kWarps];
   __shared__ uint64_t full[ST];
   __shared__ float s_factor[R];
@@ -135,61 +137,77 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
 
   const int groups_of_page = 1 << (a.page_shift - 4);
   const int cell_g = (g & 1) ? 7 - (g >> 1) : g >> 1;  // cell of S^T's row g (and 8 + cell_g of row g + 8)
-  uint32_t fills = 0;  // tiles that the ring has taken, over all segments
+  uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
   bool ok = true, job = false;
 
-  while (x < x_end) {
-    const int s = kv4_find(pre, a.n_seq, x);
-    const Kv4Seq q = kv4_seq<TILE, R>(a, s, false);
-    const long long rel = x - pre[s];
-    const int unit = static_cast<int>(rel / q.steps);
-    const int k0 = static_cast<int>(rel - static_cast<long long>(unit) * q.steps);
-    const int k1 = static_cast<int>(min(static_cast<long long>(q.steps), k0 + (x_end - x)));
-    const int head = unit / q.groups, row0 = unit % q.groups * R;
-    const int n_rows = min(R, q.rows * a.G - row0);
-    x += k1 - k0;
-    const int n = ok ? k1 - k0 : 0;  // tiles
-
-    // ---- copies: this warp's groups of tile i
-    const int32_t* pages = a.table + static_cast<long long>(s) * a.table_stride;
-    int my_page = 0, looked = -1;
-    auto issue = [&](int i) {
-      if (i / (32 / MT) != looked) {  // the lanes look up the groups of 32 / MT tiles at a time
-        looked = i / (32 / MT);
-        const int ii = looked * (32 / MT) + lane / MT;
-        const int pos = q.base + (k0 + ii) * TILE + (warp * MT + lane % MT) * 16;
-        my_page = -1;
-        if (ii < n && pos < q.hi) {
-          my_page = pages[pos >> a.page_shift];
-          if (my_page < 0 || my_page >= a.n_pages) {
-            set_status(a.status, DFLASH_DEV_CAPACITY);
-            my_page = 0;
-          }
-        }
-      }
-      const int st = (fills + i) % ST;
-      const int at = i % (32 / MT) * MT;
-      int page[MT], bytes = 0;
+  // a segment's part in this CTA: tiles [k0, k0 + n) of a sequence, kv head and row group
+  struct Part {
+    Kv4Seq q;
+    int s, head, row0, k0, n;
+  };
+  auto part_at = [&](long long at) {
+    Part p{};
+    if (at >= x_end) return p;
+    p.s = kv4_find(pre, a.n_seq, at);
+    p.q = kv4_seq<TILE, R>(a, p.s, false);
+    const long long rel = at - pre[p.s];
+    const int unit = static_cast<int>(rel / p.q.steps);
+    p.k0 = static_cast<int>(rel - static_cast<long long>(unit) * p.q.steps);
+    p.n = static_cast<int>(min(static_cast<long long>(p.q.steps - p.k0), x_end - at));
+    p.head = unit / p.q.groups;
+    p.row0 = unit % p.q.groups * R;
+    return p;
+  };
+  // the lanes look up the pages of this warp's groups, 32 / MT tiles at a time
+  auto look_up = [&](const Part& p, int from) {
+    const int i = from + lane / MT;
+    const int pos = p.q.base + (p.k0 + i) * TILE + (warp * MT + lane % MT) * 16;
+    if (i >= p.n || pos >= p.q.hi) return -1;
+    int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
+    if (page < 0 || page >= a.n_pages) {
+      set_status(a.status, DFLASH_DEV_CAPACITY);
+      page = 0;
+    }
+    return page;
+  };
+  // copies this warp's groups of tile i of a part as the ring's fill `fill`
+  auto issue = [&](const Part& p, int i, uint32_t fill, int pages) {
+    const int st = fill % ST;
+    int page[MT], bytes = 0;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      page[j] = __shfl_sync(0xffffffffu, pages, i % (32 / MT) * MT + j);
+      bytes += page[j] >= 0 ? F::GROUP_BYTES : 0;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[st], bytes);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        page[j] = __shfl_sync(0xffffffffu, my_page, at + j);
-        bytes += page[j] >= 0 ? F::GROUP_BYTES : 0;
+        const int gi = warp * MT + j;
+        const int grp = ((p.q.base + (p.k0 + i) * TILE + gi * 16) >> 4) & (groups_of_page - 1);
+        if (page[j] >= 0)
+          bulk_g2s(ring + st * G::STAGE + gi * F::GROUP_BYTES,
+                   a.cache + ((static_cast<size_t>(page[j]) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES,
+                   F::GROUP_BYTES, &full[st]);
       }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], bytes);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const int gi = warp * MT + j;
-          const int grp = ((q.base + (k0 + i) * TILE + gi * 16) >> 4) & (groups_of_page - 1);
-          if (page[j] >= 0)
-            bulk_g2s(ring + st * G::STAGE + gi * F::GROUP_BYTES,
-                     a.cache + ((static_cast<size_t>(page[j]) * a.n_kv + head) * groups_of_page + grp) * F::GROUP_BYTES,
-                     F::GROUP_BYTES, &full[st]);
-        }
-      }
-    };
-    __syncthreads();  // the last segment is done with the ring, Q and P
-    for (int i = 0; i < min(n, ST); ++i) issue(i);
+    }
+  };
+
+  Part cur = part_at(x);
+  int pages = look_up(cur, 0);
+  int issued = 0;  // tiles of the current part that are on their way
+  for (; issued < min(cur.n, ST); ++issued) issue(cur, issued, issued, pages);
+  while (cur.n > 0) {
+    const Kv4Seq q = cur.q;
+    const int k0 = cur.k0, k1 = cur.k0 + cur.n, head = cur.head, row0 = cur.row0;
+    const int n_rows = min(R, q.rows * a.G - row0);
+    x += cur.n;
+    const int n = ok ? cur.n : 0;  // tiles
+    // the next part's first tiles follow this one's last without a gap
+    const Part next = part_at(x);
+    int next_pages = look_up(next, 0);
+    int next_issued = 0;
+    __syncthreads();  // the last segment is done with Q and P
 
     // ---- Q: 8 threads a row find its maximum, scale it and lay out the fragments
     for (int m = tid >> 3; m < R; m += kThreads / 8) {
@@ -243,20 +261,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         };
         *reinterpret_cast<uint4*>(qf + (((m >> 3) * B + b) * 32 + (m & 7) * 4 + tt) * 16) =
             make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
-        if constexpr (E == 32) {
-          if (e == 24) {
-            qstart[((m >> 3) * B + b) * 8 + (m & 7)] = sum * (-8.f / 16777216.f);
-            sum = 0.f;
-          }
-        }
       }
+      // -8 2^-24 times the block's sum, in two terms: term h of block b is row
+      // 8 h + b of the product's B operand, held by lane (m % 8, b / 2)
       if constexpr (E < 32) {  // 32 / E threads share a block
 #pragma unroll
         for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (part % (32 / E) == 0) {
-          const int b = part * E / 32;
-          qstart[((m >> 3) * B + b) * 8 + (m & 7)] = sum * (-8.f / 16777216.f);
-        }
+      }
+      __half* at = qsum + ((m >> 3) * 32 + (m & 7) * 4) * 4;
+      if (part % (32 / E) == 0) {
+        const int b = part * E / 32;
+        const float v8 = sum * (-8.f / 16777216.f);
+        const __half hi = __float2half_rn(v8);
+        at[(b >> 1) * 4 + (b & 1)] = hi;
+        at[(b >> 1) * 4 + 2 + (b & 1)] = __float2half_rn(v8 - __half2float(hi));
+      } else {  // rows of no block
+        const int b = B + part - part * E / 32 - 1;
+        at[(b >> 1) * 4 + (b & 1)] = at[(b >> 1) * 4 + 2 + (b & 1)] = __ushort_as_half(0);
       }
     }
     __syncthreads();
@@ -297,14 +318,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
       const uint32_t base = smem_u32(ring + st * G::STAGE);
       const int pos0 = q.base + (k0 + i) * TILE;
       const bool edge = pos0 < all_lo || pos0 + TILE > all_hi;
-      // ---- S^T of this warp's cells
-      float sc[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n2 = 0; n2 < NT; ++n2)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][n2][e] = 0.f;
       // the lane's words and scales of cells cell_g and 8 + cell_g
       uint32_t wa[MT][B], wb[MT][B], da[MT][B / 2], db[MT][B / 2];
 #pragma unroll
@@ -326,12 +339,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         load_words<B / 2>(gb + F::K_SCALES + cell_g * F::SROW, da[mt]);
         load_words<B / 2>(gb + F::K_SCALES + (cell_g + 8) * F::SROW, db[mt]);
       }
+      // ---- S^T of this warp's cells, from the codes' -8 (scales of blocks 2t, 2t + 1)
+      float sc[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t at = base + (warp * MT + mt) * F::GROUP_BYTES + F::K_SCALES + cell_g * F::SROW + 4 * t;
+        uint32_t s0 = 0, s1 = 0;
+        if (2 * t < B) s0 = lds32(at), s1 = lds32(at + 8 * F::SROW);
+#pragma unroll
+        for (int n2 = 0; n2 < NT; ++n2) {
+          const uint2 qs = *reinterpret_cast<const uint2*>(qsum + (n2 * 32 + lane) * 4);
+          mma_zero(sc[mt][n2], s0, s1, s0, s1, qs.x, qs.y);
+        }
+      }
 #pragma unroll
       for (int b = 0; b < B; ++b) {
 #pragma unroll
         for (int n2 = 0; n2 < NT; ++n2) {
           const uint4 bq = *reinterpret_cast<const uint4*>(qf + ((n2 * B + b) * 32 + lane) * 16);
-          const float2 start = *reinterpret_cast<const float2*>(qstart + (n2 * B + b) * 8 + 2 * t);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const __half2 ha = *reinterpret_cast<const __half2*>(&da[mt][b >> 1]);
@@ -340,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
             const float fb = (b & 1) ? __high2float(hb) : __low2float(hb);
             const uint32_t ua = wa[mt][b], ub = wb[mt][b], va = ua >> 8, vb = ub >> 8;
             float acc[4];
-            mma_from(acc, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, bq.x, bq.y, start.x,
-                     start.y);
+            mma_zero(acc, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, bq.x, bq.y);
             mma_f16_16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, bq.z, bq.w);
             sc[mt][n2][0] = fmaf(fa, acc[0], sc[mt][n2][0]);
             sc[mt][n2][1] = fmaf(fa, acc[1], sc[mt][n2][1]);
@@ -351,22 +375,45 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         }
       }
       // ---- scores in log2 units; does any pass its row's reference by too much?
-      bool over = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
+          for (int e = 0; e < 4; ++e) sc[mt][n2][e] *= fac[n2][e & 1];
+      if (edge) {
+        // cells that a row does not see
+#pragma unroll
+        for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float v = sc[mt][n2][e] * fac[n2][e & 1];
-            if (edge) {
+            const int2 sees = s_sees[n2 * 8 + 2 * t + (e & 1)];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
               const int pos = pos0 + (warp * MT + mt) * 16 + cell_g + (e >> 1) * 8;
-              const int2 sees = s_sees[n2 * 8 + 2 * t + (e & 1)];
-              if (pos < sees.x || pos >= sees.y) v = -INFINITY;
+              if (pos < sees.x || pos >= sees.y) sc[mt][n2][e] = -INFINITY;
             }
-            sc[mt][n2][e] = v;
-            over |= v > m_ref[n2][e & 1] + kSlack;
           }
+        // and cells that none sees may hold anything: no weight times NaN, so
+        // their V scales become 0 (the barrier below orders it before the reads)
+        for (int j = lane; j < MT * 16 * (F::SROW / 4); j += 32) {
+          const int cell = j / (F::SROW / 4), pos = pos0 + warp * MT * 16 + cell;
+          if (pos < q.lo || pos >= q.hi)
+            *reinterpret_cast<uint32_t*>(ring + st * G::STAGE + (warp * MT + cell / 16) * F::GROUP_BYTES + F::V_SCALES +
+                                         (cell % 16) * F::SROW + j % (F::SROW / 4) * 4) = 0;
+        }
+        fence_proxy_async_smem();  // the stage's next copy comes after these writes
+      }
+      bool over = false;
+#pragma unroll
+      for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(sc[0][n2][e], sc[0][n2][2 + e]);
+#pragma unroll
+          for (int mt = 1; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n2][e], sc[mt][n2][2 + e]));
+          over |= v > m_ref[n2][e] + kSlack;
+        }
       uint8_t* pt = pf + (i & 1) * G::P;
       auto write_p = [&](float (&sum)[NT][2]) {
 #pragma unroll
@@ -391,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         if (__syncthreads_or(late)) {
           // a copy did not come in time: nothing more is issued or computed; what
           // is in flight lands before the CTA ends
-          for (int j = i; j < min(n, i + ST); ++j) mbar_wait(&full[(fills + j) % ST], ((fills + j) / ST) & 1);
+          for (int j = i; j < issued + next_issued; ++j) mbar_wait(&full[(fills + j) % ST], ((fills + j) / ST) & 1);
           if (tid == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
           ok = false;
           break;
@@ -435,7 +482,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
 #pragma unroll
         for (int e = 0; e < 2; ++e) l_run[n2][e] += sum[n2][e];
       // every warp has finished the tile before: its stage takes a new one
-      if (i > 0 && i - 1 + ST < n) issue(i - 1 + ST);
+      if (i > 0) {
+        if (issued < n) {
+          if (issued % (32 / MT) == 0) pages = look_up(cur, issued);
+          issue(cur, issued, fills + issued, pages);
+          ++issued;
+        } else if (next_issued < min(next.n, 32 / MT)) {
+          issue(next, next_issued, fills + n + next_issued, next_pages);
+          ++next_issued;
+        }
+      }
       // ---- O^T: cells t, 7 - t and 8 + t, 15 - t of each group, this warp's channels
       const int u = warp * JT / 4, j0 = warp * JT % 4;  // its word of each V chunk, its first 16-channel tile in the word
 #pragma unroll
@@ -451,10 +507,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
                        : "=h"(h)
                        : "r"(gb + F::V_SCALES + cell * F::SROW + ((g >> 2) * U + u) * 2));
           vs[k] = h;
-          if (edge) {  // cells that no row sees may hold anything: no weight times NaN
-            const int pos = pos0 + gi * 16 + cell;
-            if (pos < q.lo || pos >= q.hi) vs[k] = 0;
-          }
         }
         const uint32_t d0 = prmt(vs[0], vs[1], 0x5410), d1 = prmt(vs[2], vs[3], 0x5410);
         uint2 pb[NT];
@@ -484,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
       }
     }
     fills += n;
+    // (the last tile's stage is free once every warp is behind the barrier below)
     // ---- the rows' sums over all warps
 #pragma unroll
     for (int n2 = 0; n2 < NT; ++n2)
@@ -494,6 +547,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         if (g == 0) s_sum[warp][n2 * 8 + 2 * t + e] = l_run[n2][e];
       }
     __syncthreads();
+    if (ok) {
+      for (; next_issued < min(next.n, ST); ++next_issued) issue(next, next_issued, fills + next_issued, next_pages);
+    }
     const bool whole = k0 == 0 && k1 == q.steps;
     const int slot = 2 * c + (k0 == 0 ? 1 : 0);
     const int col = 64 * (warp * JT / 4) + 8 * g + 2 * (warp * JT % 4);
@@ -534,6 +590,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         a.jobs[c] = r;
       }
     }
+    cur = next;
+    pages = next_pages;
+    issued = next_issued;
   }
   if (!job && tid == 0) a.jobs[c].n_rows = 0;
 }
@@ -541,9 +600,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
 template <int D, int NT>
 cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
   using G = Geo<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       G::SMEM + kPlanBytes(kKv4MaxSeq));
   if (e != cudaSuccess) return e;
-  kv4_attn_kernel<D, NT><<<most, kThreads, G::SMEM, st>>>(a);
+  kv4_attn_kernel<D, NT><<<most, kThreads, G::SMEM + kPlanBytes(a.n_seq), st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || most == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -558,6 +618,24 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, G::R>, a, most);
+}
+
+// Shared memory of an SM, and what a CTA takes of it besides its dynamic part
+// (its static arrays and the system's 1 KB).
+constexpr int kSmemOfSm = 228 * 1024, kStaticSmem = 2560;
+int smem_of(int d, int nt) {
+  switch (d * 8 + nt) {
+#define DFLASH_KV4_SMEM(D) \
+  case D * 8 + 1: return Geo<D, 1>::SMEM; \
+  case D * 8 + 2: return Geo<D, 2>::SMEM; \
+  case D * 8 + 3: return Geo<D, 3>::SMEM; \
+  case D * 8 + 4: return Geo<D, 4>::SMEM;
+    DFLASH_KV4_SMEM(64)
+    DFLASH_KV4_SMEM(128)
+    DFLASH_KV4_SMEM(256)
+#undef DFLASH_KV4_SMEM
+  }
+  return 0;
 }
 
 // What the host knows of a call: 8-row tiles of a row group, CTAs and
@@ -579,7 +657,10 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   // (a window may begin anywhere in a tile)
   const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
   const long long ctas = (segments * tiles + kLeast - 1) / kLeast;
-  out->most = static_cast<int>(ctas < kPerSm * sms ? ctas : kPerSm * sms);
+  // one wave of CTAs: every one of them has the same share
+  const int smem = smem_of(c->head_dim, out->nt) + kPlanBytes(n_seq) + kStaticSmem;
+  const int per_sm = kSmemOfSm / smem < kPerSm ? kSmemOfSm / smem : kPerSm;
+  out->most = static_cast<int>(ctas < per_sm * sms ? ctas : per_sm * sms);
   out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
   return cudaSuccess;
 }
