@@ -26,7 +26,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompil
          "-Xcompiler", "-Wall", "-Xptxas", "-warn-spills", "-I", INCLUDE]
 SOURCES = ["api.cu", "attention.cu", "misc.cu", "gemv_head.cu", "gemv_bf16.cu", "gemv_q8_0.cu",
            "gemv_q5_0.cu", "gemv_q4_0.cu", "head_static.cu", "head_tc.cu", "gemv_tc.cu",
-           "kv4_attention.cu", "kv4_cells.cu", "page_tables.cu", "token_logprobs.cu"]
+           "kv4_attention.cu", "kv4_attention_tc.cu", "kv4_cells.cu", "page_tables.cu", "token_logprobs.cu"]
 
 
 def nvcc() -> str:

@@ -67,33 +67,40 @@ struct Geo {
 
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
 
-// D = A B for one 16 x 8 tile.
+// D = A B and D += A B for one 16 x 8 tile.  Not volatile, like the plain loads
+// below: the compiler may run a group's loads and unpacking under another's products.
 __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
-// N consecutive bytes (4, 8 or 16 a load) from shared memory.
+// N consecutive words (1, 2 or 4).
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
-    w[0] = lds32(addr);
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (N == 2) {
-    const uint2 v = lds64(addr);
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
   } else {
     static_assert(N == 4, "words");
-    const uint4 v = lds128(addr);
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x;
     w[1] = v.y;
     w[2] = v.z;
@@ -315,19 +322,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
       const uint32_t fill = fills + i;
       const int st = fill % ST;
       const bool late = !mbar_wait(&full[st], (fill / ST) & 1);
-      const uint32_t base = smem_u32(ring + st * G::STAGE);
+      const uint8_t* base = ring + st * G::STAGE;
       const int pos0 = q.base + (k0 + i) * TILE;
       const bool edge = pos0 < all_lo || pos0 + TILE > all_hi;
       // the lane's words and scales of cells cell_g and 8 + cell_g
       uint32_t wa[MT][B], wb[MT][B], da[MT][B / 2], db[MT][B / 2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t gb = base + (warp * MT + mt) * F::GROUP_BYTES;
+        const uint8_t* gb = base + (warp * MT + mt) * F::GROUP_BYTES;
 #pragma unroll
         for (int h = 0; h < (B + 3) / 4; ++h) {
           constexpr int N = B < 4 ? B : 4;
           uint32_t tmp[N];
-          const uint32_t at = gb + cell_g * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cell_g));
+          const uint8_t* at = gb + cell_g * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cell_g));
           load_words<N>(at, tmp);
 #pragma unroll
           for (int e = 0; e < N; ++e) wa[mt][4 * h + e] = tmp[e];
@@ -343,9 +350,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
       float sc[MT][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t at = base + (warp * MT + mt) * F::GROUP_BYTES + F::K_SCALES + cell_g * F::SROW + 4 * t;
+        const uint8_t* at = base + (warp * MT + mt) * F::GROUP_BYTES + F::K_SCALES + cell_g * F::SROW + 4 * t;
         uint32_t s0 = 0, s1 = 0;
-        if (2 * t < B) s0 = lds32(at), s1 = lds32(at + 8 * F::SROW);
+        if (2 * t < B) {
+          s0 = *reinterpret_cast<const uint32_t*>(at);
+          s1 = *reinterpret_cast<const uint32_t*>(at + 8 * F::SROW);
+        }
 #pragma unroll
         for (int n2 = 0; n2 < NT; ++n2) {
           const uint2 qs = *reinterpret_cast<const uint2*>(qsum + (n2 * 32 + lane) * 4);
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
             const uint32_t ua = wa[mt][b], ub = wb[mt][b], va = ua >> 8, vb = ub >> 8;
             float acc[4];
             mma_zero(acc, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, bq.x, bq.y);
-            mma_f16_16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, bq.z, bq.w);
+            mma_add(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, bq.z, bq.w);
             sc[mt][n2][0] = fmaf(fa, acc[0], sc[mt][n2][0]);
             sc[mt][n2][1] = fmaf(fa, acc[1], sc[mt][n2][1]);
             sc[mt][n2][2] = fmaf(fb, acc[2], sc[mt][n2][2]);
@@ -496,17 +506,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
       const int u = warp * JT / 4, j0 = warp * JT % 4;  // its word of each V chunk, its first 16-channel tile in the word
 #pragma unroll
       for (int gi = 0; gi < G::GROUPS; ++gi) {
-        const uint32_t gb = base + gi * F::GROUP_BYTES;
+        const uint8_t* gb = base + gi * F::GROUP_BYTES;
         uint32_t vw[4], vs[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int cell = (k & 1 ? 7 - t : t) + (k >> 1) * 8;
-          vw[k] = lds32(gb + F::V_CODES + cell * F::ROW + 4 * (U * (g ^ F::v_swap(cell)) + u));
-          uint16_t h;
-          asm volatile("ld.shared.u16 %0, [%1];"
-                       : "=h"(h)
-                       : "r"(gb + F::V_SCALES + cell * F::SROW + ((g >> 2) * U + u) * 2));
-          vs[k] = h;
+          vw[k] = *reinterpret_cast<const uint32_t*>(gb + F::V_CODES + cell * F::ROW + 4 * (U * (g ^ F::v_swap(cell)) + u));
+          vs[k] = *reinterpret_cast<const uint16_t*>(gb + F::V_SCALES + cell * F::SROW + ((g >> 2) * U + u) * 2);
         }
         const uint32_t d0 = prmt(vs[0], vs[1], 0x5410), d1 = prmt(vs[2], vs[3], 0x5410);
         uint2 pb[NT];
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
           const uint32_t a2 = hmul2_u32(hfma2_u32(and_or(h, 0x000f000fu, 0x64006400u), ONE, MINUS_1032), d1);
           const uint32_t a3 = hmul2_u32(hfma2_u32(and_or(h, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d1);
 #pragma unroll
-          for (int n2 = 0; n2 < NT; ++n2) mma_f16_16816(o[j][n2], a0, a1, a2, a3, pb[n2].x, pb[n2].y);
+          for (int n2 = 0; n2 < NT; ++n2) mma_add(o[j][n2], a0, a1, a2, a3, pb[n2].x, pb[n2].y);
         }
       }
     }
@@ -606,18 +612,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t s
   kv4_attn_kernel<D, NT><<<most, kThreads, G::SMEM + kPlanBytes(a.n_seq), st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || most == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  // one block per segment that may be split and per row and 64 channels of it, fewer where there are many
-  const int z = G::R * (D / 64), y = 2048 / jobs;
-  cfg.gridDim = dim3(jobs, y < 1 ? 1 : y < z ? y : z);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, G::R>, a, most);
+  return launch_kv4_merge<D, G::R>(a, most, jobs, st);
 }
 
 // Shared memory of an SM, and what a CTA takes of it besides its dynamic part
@@ -641,14 +636,27 @@ int smem_of(int d, int nt) {
 // What the host knows of a call: 8-row tiles of a row group, CTAs and
 // segments at most.
 struct Shape {
-  int nt, most, jobs;
+  bool tc;    // the tcgen05 kernel: row groups of 128
+  int nt;     // else: 8-row tiles of a row group
+  int most, jobs;
+  int rows_of_group() const { return tc ? 128 : 8 * nt; }
 };
+constexpr int kTcRows = 16;  // more rows per kv head than this go to the tcgen05 kernel
 cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Shape* out) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int rows = n_q_heads / c->n_kv_heads * max_rows;
+  out->tc = rows > kTcRows;
+  if (out->tc) {
+    out->nt = 0;
+    const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads;
+    const long long tiles = (static_cast<long long>(table_stride) * c->page_size + 63) / 64 + 1;
+    out->most = static_cast<int>(segments * tiles < sms ? segments * tiles : sms);
+    out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
+    return cudaSuccess;
+  }
   // as few row groups as 32 rows allow, each no wider than it needs
   const int groups = (rows + 31) / 32;
   out->nt = ((rows + groups - 1) / groups + 7) / 8;
@@ -675,7 +683,7 @@ int check_call(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows
 }
 
 size_t bytes_of(const dflash_kv4_cache* c, const Shape& s) {
-  return s.most * (sizeof(Kv4Job) + 2 * size_t(8) * s.nt * (c->head_dim * 4 + 8));
+  return s.most * (sizeof(Kv4Job) + 2 * size_t(s.rows_of_group()) * (c->head_dim * 4 + 8));
 }
 
 template <int D>
@@ -746,13 +754,17 @@ int dflash_kv4_attention(const dflash_kv4_cache* c, const void* q, void* out, in
   a.scale_log2 = scale * 1.4426950408889634f;
   a.jobs = static_cast<Kv4Job*>(workspace);
   a.part = reinterpret_cast<float*>(a.jobs + s.most);
-  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * 8 * s.nt * c->head_dim);
+  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * s.rows_of_group() * c->head_dim);
   a.status = dev_status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  switch (c->head_dim) {
-    case 64: e = launch_nt<64>(a, s, st); break;
-    case 128: e = launch_nt<128>(a, s, st); break;
-    default: e = launch_nt<256>(a, s, st); break;
+  if (s.tc) {
+    e = launch_kv4_attn_tc(c->head_dim, a, s.most, s.jobs, st);
+  } else {
+    switch (c->head_dim) {
+      case 64: e = launch_nt<64>(a, s, st); break;
+      case 128: e = launch_nt<128>(a, s, st); break;
+      default: e = launch_nt<256>(a, s, st); break;
+    }
   }
   return cuda_status(e, "kv4 attention");
 }

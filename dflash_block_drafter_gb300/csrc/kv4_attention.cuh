@@ -261,4 +261,25 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
   }
 }
 
+// Launches the merge behind an attention kernel of `most` CTAs, of which at
+// most `jobs` segments can be split.
+template <int D, int R>
+cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  // one block per segment that may be split and per row and 64 channels of it, fewer where there are many
+  const int z = R * (D / 64), y = 2048 / jobs;
+  cfg.gridDim = dim3(jobs, y < 1 ? 1 : y < z ? y : z);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, R>, a, most);
+}
+
+// kv4_attention_tc.cu: row groups of 128, tiles of 64 cells, one CTA per SM.
+cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st);
+
 }  // namespace dflash
