@@ -65,8 +65,6 @@ struct Geo {
   static constexpr int JT = D / 64;                // 16-channel tiles of O^T that a warp owns
 };
 
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
-
 // D = A B and D += A B for one 16 x 8 tile.  Not volatile, like the plain loads
 // below: the compiler may run a group's loads and unpacking under another's products.
 __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -144,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
 
   const int groups_of_page = 1 << (a.page_shift - 4);
   const int cell_g = (g & 1) ? 7 - (g >> 1) : g >> 1;  // cell of S^T's row g (and 8 + cell_g of row g + 8)
+  const Kv4Consts kc;
   uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
   bool ok = true, job = false;
 
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
     for (int i = 0; i < n; ++i) {
       const uint32_t fill = fills + i;
       const int st = fill % ST;
-      const bool late = !mbar_wait(&full[st], (fill / ST) & 1);
+      const bool late = !kv4_wait(&full[st], (fill / ST) & 1);
       const uint8_t* base = ring + st * G::STAGE;
       const int pos0 = q.base + (k0 + i) * TILE;
       const bool edge = pos0 < all_lo || pos0 + TILE > all_hi;
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
         if (__syncthreads_or(late)) {
           // a copy did not come in time: nothing more is issued or computed; what
           // is in flight lands before the CTA ends
-          for (int j = i; j < issued + next_issued; ++j) mbar_wait(&full[(fills + j) % ST], ((fills + j) / ST) & 1);
+          for (int j = i; j < issued + next_issued; ++j) kv4_wait(&full[(fills + j) % ST], ((fills + j) / ST) & 1);
           if (tid == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
           ok = false;
           break;
@@ -531,11 +530,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
 #pragma unroll
         for (int j = 0; j < JT; ++j) {  // channels 64u + 8g + 2 (j0 + j), + 1
           const uint32_t l = (j & 1) ? lo[j >> 1] >> 8 : lo[j >> 1], h = (j & 1) ? hi[j >> 1] >> 8 : hi[j >> 1];
-          constexpr uint32_t ONE = 0x3c003c00u, MINUS_1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, MINUS_72 = 0xd480d480u;
-          const uint32_t a0 = hmul2_u32(hfma2_u32(and_or(l, 0x000f000fu, 0x64006400u), ONE, MINUS_1032), d0);
-          const uint32_t a1 = hmul2_u32(hfma2_u32(and_or(l, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d0);
-          const uint32_t a2 = hmul2_u32(hfma2_u32(and_or(h, 0x000f000fu, 0x64006400u), ONE, MINUS_1032), d1);
-          const uint32_t a3 = hmul2_u32(hfma2_u32(and_or(h, 0x00f000f0u, 0x64006400u), SIXTEENTH, MINUS_72), d1);
+          const uint32_t a0 = hmul2_u32(kc.even(l), d0), a1 = hmul2_u32(kc.odd(l), d0);
+          const uint32_t a2 = hmul2_u32(kc.even(h), d1), a3 = hmul2_u32(kc.odd(h), d1);
 #pragma unroll
           for (int n2 = 0; n2 < NT; ++n2) mma_add(o[j][n2], a0, a1, a2, a3, pb[n2].x, pb[n2].y);
         }

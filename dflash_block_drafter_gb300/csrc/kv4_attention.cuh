@@ -25,6 +25,52 @@ namespace dflash {
 
 constexpr int kKv4MaxSeq = 1024;
 
+// Bounded wait for a phase of an mbarrier, as mbar_wait; the hint lets the
+// hardware hold the warp up to 20 us per try instead of having it spin, which
+// would take issue slots from the warps that unpack.
+__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitTimeoutNs) return false;
+  }
+}
+
+// The constants that turn the codes of a word into FP16 code - 8.  Held in
+// registers that the compiler takes for unknown: as immediates, the AND and
+// the OR of a code would be two instructions (and the FMA's second constant a
+// move), a third of the unpacking's arithmetic.
+struct Kv4Consts {
+  uint32_t base, minus_72;
+  __device__ __forceinline__ Kv4Consts() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(base));      // 1024: a code in its low mantissa bits is added
+    asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(minus_72));
+  }
+  // codes 0 and 4 of a word (of a word shifted by 8: 2 and 6)
+  __device__ __forceinline__ uint32_t even(uint32_t w) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(r) : "r"(w), "r"(base));
+    return hsub2_u32(r, 0x64086408u);  // - 1032
+  }
+  // codes 1 and 5 (3 and 7), which count 16
+  __device__ __forceinline__ uint32_t odd(uint32_t w) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(r) : "r"(w), "r"(base));
+    return hfma2_u32(r, 0x2c002c00u, minus_72);  // / 16 - 72
+  }
+};
+
 struct Kv4Job;
 
 struct Kv4AttnArgs {

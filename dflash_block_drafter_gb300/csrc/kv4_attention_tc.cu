@@ -2,17 +2,21 @@
 // (blocks of several tokens over wide groups), on the tcgen05 tensor cores.
 //
 // One CTA per SM takes tiles of 64 cells for up to 128 query rows:
-//   warp 0        copies the tiles' packed groups into a ring (bulk copies);
-//   warps 10..17  unpack a tile once for all rows: K and V as FP16
-//                 d (code - 8), in the 128-byte-swizzled layouts the MMAs read,
-//                 double-buffered;
-//   warp 1        issues S = Q K^T (M 128, N 64) and O += P V (M 128, N = D);
-//   warps 2..9    softmax: a thread has one row (TMEM lane) and 32 of the
-//                 tile's 64 cells.
-// Q and P are the MMAs' A operands in tensor memory (FP16 pairs), so shared
-// memory carries only K and V: per tile and D = 256 64 KB written and read
-// (about 1000 cycles of its bandwidth, as many as the MMAs take), against 790
-// cycles for the tile's bytes from HBM.  P lies over the S it came from; the columns are
+//   warp 0        issues S = Q K^T (M 128, N 64), warp 2 O += P V (M 128, N = D):
+//                 two warps, because a wait and the issue of a tile's MMAs
+//                 take one warp as long as the MMAs themselves;
+//   warp 1        copies the tiles' packed groups into a ring (bulk copies);
+//   warps 4..11   softmax: a thread has one row (TMEM lane) of every other
+//                 tile: warps 4..7 the even ones, 8..11 the odd ones, so that the
+//                 waits and fences of one tile lie under the arithmetic of the next;
+//   warps 12..19  unpack K, warps 20..27 unpack V, once for all rows: FP16
+//                 d (code - 8) in the 128-byte-swizzled layouts the MMAs read,
+//                 double-buffered; four warps each for the even and the odd tiles.
+// Q is an A operand in tensor memory (FP16 pairs), P one in shared memory (over
+// S in tensor memory it would keep the next but one Q K^T waiting for P V).
+// Per tile and D = 256, shared memory takes 64 KB of K and V written and read
+// and 16 KB of P (about 1300 cycles of its bandwidth), the MMAs 1024
+// cycles and the tile's bytes from HBM 790; the columns of tensor memory are
 // S0 | S1 | O | Q = 64 + 64 + D + D / 2.
 //
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
@@ -20,7 +24,8 @@
 // and O's are read back in it.
 // Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-25 absolute), Q exact (rows
 // scaled by a power of two); scores, sums and O in FP32.  Scores are taken
-// relative to a reference that moves only when a row passes it by 2^8.
+// relative to a reference that moves only when a row passes it by 2^8; the two
+// softmax warps of a quarter of the rows hand it to each other tile by tile.
 #include "kv4_attention.cuh"
 
 namespace dflash {
@@ -29,10 +34,18 @@ namespace {
 constexpr int kTile = 64;       // cells of a tile
 constexpr int kGroups = 4;
 constexpr int kRows = 128;
-constexpr int kSoftWarps = 8, kUnpackWarps = 8;
-constexpr int kThreads = 32 * (2 + kSoftWarps + kUnpackWarps);
+constexpr int kSoftWarps = 8, kUnpackWarps = 8;  // (unpacking: K and V each)
+constexpr int kQkWarp = 0, kCopyWarp = 1, kPvWarp = 2;  // (3 fills their warpgroup)
+constexpr int kSoftWarp0 = 4, kUnpackWarp0 = kSoftWarp0 + kSoftWarps;
+constexpr int kThreads = 32 * (kSoftWarps + 2 * kUnpackWarps + 4);  // whole warpgroups
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kPacked = 4;      // stages of the packed ring
+// Registers a thread: 72 at launch (64512 in all), then 104, 64 and 40 by role:
+// 256 * 104 + 512 * 64 + 128 * 40 = 64512.
+constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
+static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
+              "the roles' registers come out of the launch's");
+constexpr int kPacked = 3;      // stages of the packed ring
+constexpr int kAhead = 7;       // tiles that L2 is asked for in advance (fewer than 8)
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
 
@@ -40,20 +53,81 @@ template <int D>
 struct Geo {
   static constexpr int STAGE = kGroups * Kv4<D>::GROUP_BYTES;
   static constexpr int BUF = kTile * D * 2;  // one unpacked K or V tile
-  static constexpr int RED = (2 * 2 * kRows + 2 * kRows) * 4;
-  static constexpr int SMEM = 1024 + 4 * BUF + kPacked * STAGE + RED;
+  static constexpr int RED = 3 * kRows * 4;
+  static constexpr int PBUF = kRows * kTile * 2;
+  static constexpr int SMEM = 1024 + 4 * BUF + 2 * PBUF + kPacked * STAGE + RED;
   static constexpr int S_COL = 0, O_COL = 2 * kTile, Q_COL = O_COL + D;
 };
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A * B[smem desc], kind::f16, one CTA; A in tensor memory or by a
+// descriptor too.  A descriptor comes in two words: only its low one, the address, changes between the
+// MMAs of a tile, so that a warp that computes it as a whole keeps it in
+// uniform registers and issues an MMA in a few instructions (with one lane's
+// 64-bit descriptors the issue, not the tensor cores, took the time).
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void umma_f16_sa(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two FP32 values in one register pair, and the instructions that take both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]) {
@@ -65,15 +139,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]
 }
 
 // One code word times its block's scale (twice in d): 8 FP16 in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 unpack(uint32_t w, uint32_t d) {
-  constexpr uint32_t ONE = 0x3c003c00u, MINUS_1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, MINUS_72 = 0xd480d480u;
-  constexpr uint32_t BASE = 0x64006400u;  // 1024: the code lies in the low mantissa bits
+__device__ __forceinline__ uint4 unpack(uint32_t w, uint32_t d, const Kv4Consts& k) {
   const uint32_t v = w >> 8;
   uint4 r;
-  r.x = hmul2_u32(hfma2_u32((w & 0x000f000fu) | BASE, ONE, MINUS_1032), d);
-  r.y = hmul2_u32(hfma2_u32((w & 0x00f000f0u) | BASE, SIXTEENTH, MINUS_72), d);
-  r.z = hmul2_u32(hfma2_u32((v & 0x000f000fu) | BASE, ONE, MINUS_1032), d);
-  r.w = hmul2_u32(hfma2_u32((v & 0x00f000f0u) | BASE, SIXTEENTH, MINUS_72), d);
+  r.x = hmul2_u32(k.even(w), d);
+  r.y = hmul2_u32(k.odd(w), d);
+  r.z = hmul2_u32(k.even(v), d);
+  r.w = hmul2_u32(k.odd(v), d);
   return r;
 }
 
@@ -116,12 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                       // [2][D / 64 boxes][64 cells][128 B]
   uint8_t* vbuf = kbuf + 2 * G::BUF;          // [2]
-  uint8_t* ring = vbuf + 2 * G::BUF;          // [NP] packed tiles
-  float* red_max = reinterpret_cast<float*>(ring + NP * G::STAGE);  // [2][2 halves][128 rows]
-  float* red_sum = red_max + 2 * 2 * R;                             // [2 halves][128 rows]
+  uint8_t* pbuf = vbuf + 2 * G::BUF;          // [2][128 rows][128 B]
+  uint8_t* ring = pbuf + 2 * G::PBUF;         // [NP] packed tiles
+  float* s_ref = reinterpret_cast<float*>(ring + NP * G::STAGE);    // [128 rows] references of the scores
+  float* red_sum = s_ref + R;                                       // [2][128 rows]
   long long* pre = reinterpret_cast<long long*>(red_sum + 2 * R);   // [n_seq + 1]
   __shared__ long long scratch[kThreads / 32];
-  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[2], pready[2], qready, ofree, mdone;
+  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[2], sfree[2], pready[2], qready, ofree, done[2];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,16 +204,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       mbar_init(&pfree[i], kUnpackWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kready[i], kUnpackWarps);
+      mbar_init(&kready[i], kUnpackWarps / 2);
       mbar_init(&kfree[i], 1);
-      mbar_init(&vready[i], kUnpackWarps);
+      mbar_init(&vready[i], kUnpackWarps / 2);
       mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], kSoftWarps);
+      mbar_init(&sfree[i], kSoftWarps / 2);
+      mbar_init(&pready[i], kSoftWarps / 2);
+      mbar_init(&done[i], 1);
     }
     mbar_init(&qready, kSoftWarps);
     mbar_init(&ofree, kSoftWarps);
-    mbar_init(&mdone, 1);
     fence_barrier_init();
   }
   const long long T = kv4_plan<kTile, R>(a, pre, scratch, blockIdx.x == 0);
@@ -151,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     if (tid == 0) a.jobs[c].n_rows = 0;
     return;
   }
-  if (warp == 1) {
+  if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -182,96 +256,131 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     return p;
   };
 
-  if (warp == 0) {
+  if (warp < kSoftWarp0) fewer_registers<kOtherRegs>();
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------ producer
     const int groups_of_page = 1 << (a.page_shift - 4);
     uint32_t g = 0;  // tiles over all parts
     for (long long x = x_begin; x < x_end && ok;) {
       const Part p = part_at(x);
       x += p.n;
-      int page = -1;
+      // the lanes hold the pages of the groups of 8 tiles, and those of the next 8
+      auto look_up = [&](int from) {
+        const int i = from + (lane >> 2);
+        const int pos = p.q.base + (p.k0 + i) * kTile + (lane & 3) * 16;
+        if (i >= p.n || pos >= p.q.hi) return -1;
+        int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
+        if (page < 0 || page >= a.n_pages) {
+          set_status(a.status, DFLASH_DEV_CAPACITY);
+          page = 0;
+        }
+        return page;
+      };
+      auto address = [&](int page, int i) {  // lane: group lane % 4 of tile i
+        const int grp = ((p.q.base + (p.k0 + i) * kTile + (lane & 3) * 16) >> 4) & (groups_of_page - 1);
+        return a.cache + ((static_cast<size_t>(page) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES;
+      };
+      int page = -1, later = look_up(0);
       for (int i = 0; i < p.n && ok; ++i, ++g) {
-        if (i % 8 == 0) {  // the lanes look up the groups of 8 tiles
-          const int ii = i + (lane >> 2);
-          const int pos = p.q.base + (p.k0 + ii) * kTile + (lane & 3) * 16;
-          page = -1;
-          if (ii < p.n && pos < p.q.hi) {
-            page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
-            if (page < 0 || page >= a.n_pages) {
-              set_status(a.status, DFLASH_DEV_CAPACITY);
-              page = 0;
-            }
-          }
+        if (i % 8 == 0) {
+          page = later;
+          later = look_up(i + 8);
+        }
+        // the ring is too short for HBM's latency: tile i + kAhead is asked of
+        // L2 now (at the part's start, all tiles up to it; those in `page` only)
+        for (int j = i == 0 ? NP : i + kAhead; j <= i + kAhead; ++j) {
+          const int there = __shfl_sync(0xffffffffu, j % 8 > i % 8 ? page : later, (j % 8) * 4 + (lane & 3));
+          if (lane < kGroups && there >= 0) bulk_prefetch_l2_plain(address(there, j), F::GROUP_BYTES);
         }
         const int st = g % NP;
-        if (g >= NP) ok = __all_sync(0xffffffffu, mbar_wait(&pfree[st], (g / NP - 1) & 1));
+        if (g >= NP) ok = __all_sync(0xffffffffu, kv4_wait(&pfree[st], (g / NP - 1) & 1));
         if (!ok) break;
         const int mine = __shfl_sync(0xffffffffu, page, (i % 8) * 4 + (lane & 3));
         const unsigned have = __ballot_sync(0xffffffffu, lane < kGroups && mine >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have) * F::GROUP_BYTES);
         __syncwarp();
         if (lane < kGroups && mine >= 0) {
-          const int grp = ((p.q.base + (p.k0 + i) * kTile + lane * 16) >> 4) & (groups_of_page - 1);
-          bulk_g2s(ring + st * G::STAGE + lane * F::GROUP_BYTES,
-                   a.cache + ((static_cast<size_t>(mine) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES,
-                   F::GROUP_BYTES, &pfull[st]);
+          bulk_g2s(ring + st * G::STAGE + lane * F::GROUP_BYTES, address(mine, i), F::GROUP_BYTES, &pfull[st]);
         }
       }
     }
     // every copy lands before the CTA ends
     for (uint32_t i = g < NP ? 0 : g - NP; i < g; ++i)
-      if (!mbar_wait(&pfull[i % NP], (i / NP) & 1)) ok = false;
+      if (!kv4_wait(&pfull[i % NP], (i / NP) & 1)) ok = false;
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = umma_idesc_f16(128, kTile, false, false);
-      constexpr uint32_t idesc_pv = umma_idesc_f16(128, D, false, true);
-      const uint32_t k_s = smem_u32(kbuf), v_s = smem_u32(vbuf);
-      // S[g % 2] = Q K_g^T, once K_g is there and P of tile g - 2, which lies in the same columns, has been used
-      auto issue_qk = [&](uint32_t g) -> bool {
-        if (!mbar_wait(&kready[g & 1], (g >> 1) & 1)) return false;
-        if (g >= 2 && !mbar_wait(&vfree[g & 1], ((g >> 1) - 1) & 1)) return false;
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------ S = Q K^T
+    // (the whole warp waits and computes, one lane issues)
+    constexpr uint32_t idesc = umma_idesc_f16(128, kTile, false, false);
+    const uint64_t kd = umma_desc_sw128(smem_u32(kbuf), 16, 1024);
+    const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+    const bool one = elect_one();
+    uint32_t g = 0, part = 0;
+    for (long long x = x_begin; x < x_end && ok; ++part) {
+      const int n = part_at(x).n;
+      x += n;
+      ok = __all_sync(0xffffffffu, kv4_wait(&qready, part & 1));
+      for (int i = 0; i < n && ok; ++i, ++g) {
+        const uint32_t b = g & 1, was = (g >> 1) & 1;
+        bool here = kv4_wait(&kready[b], was);
+        if (g >= 2) here = here && kv4_wait(&sfree[b], was ^ 1);
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
         tc_fence_after();
+        const uint32_t lo = k_lo + b * (G::BUF >> 4), to = tmem + G::S_COL + b * kTile;
+        if (one) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t db = umma_desc_sw128(k_s + (g & 1) * G::BUF + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024);
-          umma_f16_ta(tmem + G::S_COL + (g & 1) * kTile, tmem + G::Q_COL + kk * 8, db, idesc_qk, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_f16_ta(to, tmem + G::Q_COL + kk * 8, lo + (((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4), k_hi, idesc, kk > 0);
+          umma_commit(&sfull[b]);
+          umma_commit(&kfree[b]);
         }
-        umma_commit(&sfull[g & 1]);
-        umma_commit(&kfree[g & 1]);
-        return true;
-      };
-      uint32_t g = 0, part = 0;
-      for (long long x = x_begin; x < x_end && ok; ++part) {
-        const int n = part_at(x).n;
-        x += n;
-        if (!mbar_wait(&qready, part & 1)) ok = false;
-        if (ok && !issue_qk(g)) ok = false;
-        for (int i = 0; i < n && ok; ++i, ++g) {
-          if (i + 1 < n && !issue_qk(g + 1)) ok = false;
-          if (ok && i == 0 && part > 0 && !mbar_wait(&ofree, (part - 1) & 1)) ok = false;
-          if (!ok || !mbar_wait(&vready[g & 1], (g >> 1) & 1) || !mbar_wait(&pready[g & 1], (g >> 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
-            const uint64_t db = umma_desc_sw128(v_s + (g & 1) * G::BUF + kk * 2048, kTile * 128, 1024);
-            umma_f16_ta(tmem + G::O_COL, tmem + G::S_COL + (g & 1) * kTile + kk * 8, db, idesc_pv, (i > 0 || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(&vfree[g & 1]);
-        }
+        __syncwarp();
       }
-      // tensor memory may only be freed once every issued MMA has finished
-      umma_commit(&mdone);
-      if (!mbar_wait(&mdone, 0)) ok = false;
-      if (!ok) set_status(a.status, DFLASH_DEV_TIMEOUT);
     }
-  } else if (warp < 2 + kSoftWarps) {
+    // tensor memory may only be freed once every issued MMA has finished
+    if (one) umma_commit(&done[0]);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, kv4_wait(&done[0], 0))) ok = false;
+    if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t idesc = umma_idesc_f16(128, D, false, true);
+    const uint64_t vd = umma_desc_sw128(smem_u32(vbuf), kTile * 128, 1024), pd = umma_desc_sw128(smem_u32(pbuf), 16, 1024);
+    const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
+    const uint32_t p_lo = static_cast<uint32_t>(pd), p_hi = static_cast<uint32_t>(pd >> 32);
+    const bool one = elect_one();
+    uint32_t g = 0, part = 0;
+    for (long long x = x_begin; x < x_end && ok; ++part) {
+      const int n = part_at(x).n;
+      x += n;
+      // O of the part before has been read
+      if (part > 0) ok = __all_sync(0xffffffffu, kv4_wait(&ofree, (part - 1) & 1));
+      for (int i = 0; i < n && ok; ++i, ++g) {
+        const uint32_t b = g & 1, was = (g >> 1) & 1;
+        const bool here = kv4_wait(&vready[b], was) && kv4_wait(&pready[b], was);
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t lo = v_lo + b * (G::BUF >> 4), from = p_lo + b * (G::PBUF >> 4), more = i > 0;
+        if (one) {
+          umma_f16_sa(tmem + G::O_COL, from, p_hi, lo, v_hi, idesc, more);
+#pragma unroll
+          for (int kk = 1; kk < kTile / 16; ++kk)
+            umma_f16_sa(tmem + G::O_COL, from + kk * (32 >> 4), p_hi, lo + kk * (2048 >> 4), v_hi, idesc, 1);
+          umma_commit(&vfree[b]);
+        }
+        __syncwarp();
+      }
+    }
+    if (one) umma_commit(&done[1]);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, kv4_wait(&done[1], 0))) ok = false;
+    if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
+  } else if (warp >= kSoftWarp0 && warp < kUnpackWarp0) {
     // ------------------------------------------------------------ softmax
-    const int q4 = warp & 3, cs = (warp - 2) >> 2;  // TMEM lane quarter, half of the tile's cells (and of O's columns)
+    more_registers<kSoftRegs>();
+    const int q4 = warp & 3, cs = (warp - kSoftWarp0) >> 2;  // TMEM lane quarter; tiles by parity, and half of Q's and O's columns
     const int m = q4 * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     uint32_t g = 0;
@@ -329,76 +438,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&qready);
-      // ---- tiles
-      float m_ref = -INFINITY, l = 0.f;
-      for (int i = 0; i < p.n; ++i, ++g) {
-        const int b = g & 1;
+      // ---- tiles of this warp's parity
+      float m_ref = -INFINITY, l = 0.f;  // l in units of 2^m_ref
+      const uint32_t g_end = g + p.n, g_first = g;
+      for (g += (g ^ cs) & 1; g < g_end; g += 2) {
+        const int b = cs, i = g - g_first;
         const uint32_t s_addr = lane_addr + G::S_COL + b * kTile;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sfull[b], (g >> 1) & 1));
+        if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&sfull[b], (g >> 1) & 1));
         tc_fence_after();
-        const int pos0 = p.q.base + (p.k0 + i) * kTile + cs * 32;
-        uint32_t r[32];
+        const int pos0 = p.q.base + (p.k0 + i) * kTile;
+        uint32_t r[2][32];
         float mx = -INFINITY;
-        const bool edge = pos0 < all_lo || pos0 + 32 > all_hi;
         if (live) {
-          tmem_ld32(s_addr + cs * 32, r);
+          tmem_ld32(s_addr, r[0]);
+          tmem_ld32(s_addr + 32, r[1]);
           tmem_wait_ld();
-          tmem_reg_fence(r);
-          if (edge) {
+          tmem_reg_fence(r[0]);
+          tmem_reg_fence(r[1]);
+        }
+        // S[b] has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[b]);
+        if (live) {
+          if (pos0 < all_lo || pos0 + kTile > all_hi) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (pos0 + e < sees.x || pos0 + e >= sees.y) r[e] = 0xff800000u;  // -infinity
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (pos0 + 32 * h + e < sees.x || pos0 + 32 * h + e >= sees.y) r[h][e] = 0xff800000u;  // -infinity
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(r[e]));
+          for (int e = 0; e < 32; ++e) mx = max3(mx, __uint_as_float(r[0][e]), __uint_as_float(r[1][e]));
           mx *= factor;  // positive: the order stays
         }
-        red_max[b * 2 * R + cs * R + m] = mx;
-        named_bar_sync(1, kSoftThreads);  // also: every half's S has been read
+        // the reference that the tile before left (barrier 2 + 2 q4 + parity)
+        if (g > 0) named_bar_sync(2 + 2 * q4 + b, 64);
         if (live) {
-          mx = fmaxf(red_max[b * 2 * R + m], red_max[b * 2 * R + R + m]);
-          float alpha = 1.f;
-          if (mx > m_ref + kSlack) {
-            alpha = ex2_approx(m_ref - mx);
-            m_ref = mx;
-            l *= alpha;
-          }
-          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // the products so far, once they are all in O: half cs of the columns
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&vfree[b ^ 1], ((g - 1) >> 1) & 1));
-            tc_fence_after();
+          const float was = i > 0 ? s_ref[m] : -INFINITY;
+          const bool over = mx > was + kSlack;
+          const float ref = over ? mx : was;
+          if (i == 0 || __any_sync(0xffffffffu, over)) {
+            s_ref[m] = ref;
+            if (i > 0) {
+              // the products so far, once they are all in O
+              if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[b ^ 1], ((g - 1) >> 1) & 1));
+              tc_fence_after();
+              const float alpha = over ? ex2_approx(was - ref) : 1.f;
 #pragma unroll 1
-            for (int h = 0; h < D / 2; h += 32) {
-              uint32_t o[32];
-              const uint32_t at = lane_addr + G::O_COL + cs * (D / 2) + h;
-              tmem_ld32(at, o);
-              tmem_wait_ld();
-              tmem_reg_fence(o);
+              for (int h = 0; h < D; h += 16) {
+                uint32_t o[16];
+                const uint32_t at = lane_addr + G::O_COL + h;
+                tmem_ld16(at, o);
+                tmem_wait_ld();
+                tmem_reg_fence(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(at, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(at, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
-          const float from = m_ref == -INFINITY ? 0.f : m_ref;
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(r[e]), factor, -from));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(r[e + 1]), factor, -from));
-            l += p0 + p1;
-            w[e >> 1] = pack_f16x2(p0, p1);
+          if (ref > m_ref) {
+            l *= ex2_approx(m_ref - ref);
+            m_ref = ref;
           }
-          tmem_st16(s_addr + cs * 16, w);
-          tmem_wait_st();
         }
+        __syncwarp();
+        named_bar_arrive(2 + 2 * q4 + (b ^ 1), 64);
+        if (live) {
+          const float from = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t factor2 = pack2(factor, factor), from2 = pack2(-from, -from);
+          uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              unpack2(fma2(pack2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), factor2, from2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              sum2 = add2(sum2, pack2(p0, p1));
+              r[h][e >> 1] = pack_f16x2(p0, p1);
+            }
+          float s0, s1;
+          unpack2(sum2, s0, s1);
+          l += s0 + s1;
+        }
+        // P[b] is free once P V of tile g - 2 is done.  Warps without rows wait
+        // too: S of tile g only waits for S of g - 2 to be read, so they could
+        // otherwise announce P of tile g before the others that of g - 2.
+        if (ok && g >= 2) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[b], ((g >> 1) - 1) & 1));
+        if (live) {
+          uint8_t* prow = pbuf + b * G::PBUF + m * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(prow + ((k ^ (m & 7)) << 4)) =
+                make_uint4(r[k >> 2][4 * (k & 3)], r[k >> 2][4 * (k & 3) + 1], r[k >> 2][4 * (k & 3) + 2], r[k >> 2][4 * (k & 3) + 3]);
+        }
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[b]);
       }
+      g = g_end;
       // ---- O of the part
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&vfree[(g - 1) & 1], ((g - 1) >> 1) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[(g - 1) & 1], ((g - 1) >> 1) & 1));
       tc_fence_after();
+      named_bar_sync(1, kSoftThreads);  // the last reference
+      if (live) {
+        const float ref = s_ref[m];
+        l = l > 0.f ? l * ex2_approx(m_ref - ref) : l;  // (not of a NaN; a parity without weight has 0)
+        m_ref = ref;
+      }
       red_sum[cs * R + m] = l;
       named_bar_sync(1, kSoftThreads);
       l = red_sum[m] + red_sum[R + m];
@@ -439,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       tc_fence_before();
       named_bar_sync(1, kSoftThreads);  // red_sum has been read
       if (lane == 0) mbar_arrive(&ofree);
-      if (warp == 2 && lane == 0 && x >= x_end) {
+      if (warp == kSoftWarp0 && lane == 0 && x >= x_end) {
         // the last part: does its segment begin here and go on in the next CTAs?
         Kv4Job r{p.q.r0, p.row0, p.head, 0, 0, {0, 0, 0}};
         if (!whole && p.k0 == 0) {
@@ -450,87 +601,107 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       }
     }
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
-  } else {
+  } else if (warp >= kUnpackWarp0) {
     // ------------------------------------------------------------ unpacking
-    const int w8 = warp - 2 - kSoftWarps;
-    const int t = lane & 3;
+    fewer_registers<kUnpackRegs>();
+    const bool v_side = warp >= kUnpackWarp0 + kUnpackWarps;
+    const int w4 = warp & 3, b = ((warp - kUnpackWarp0) >> 2) & 1;  // of four warps; parity of its tiles
+    uint64_t* ready = (v_side ? vready : kready) + b;
+    uint64_t* free_ = (v_side ? vfree : kfree) + b;
+    const Kv4Consts kc;
+    // A lane's first cell of a tile, its codes and scales there (in the packed
+    // tile) and its first 16 bytes in the unpacked tile; the others lie whole
+    // groups further.  K: 8 lanes take the four quads t of two cells whose
+    // rows lie in different banks, both as codes and, swizzled, as FP16; a lane has
+    // words of blocks 4h .. (word 4 blk + t goes to box blk / 2, chunk 4 (blk % 2) + t).
+    // V: 8 lanes take the 8 channel groups of one cell (word 8u + ch: box u, chunk ch).
+    constexpr int KW = B < 4 ? B : 4;           // words of a lane in a K row
+    constexpr int KSTEP = D == 256 ? 16 : 32;   // cells between a lane's K rows
+    int cell, codes, scales, first;
+    if (v_side) {
+      const int ch = lane & 7;
+      cell = w4 * 4 + (lane >> 3);
+      codes = F::V_CODES + cell * F::ROW + 4 * U * (ch ^ F::v_swap(cell));
+      scales = F::V_SCALES + cell * F::SROW + 2 * U * (ch >> 2);
+      first = cell * 128 + ((ch ^ (cell & 7)) << 4);
+    } else {
+      const int t = lane & 3;
+      int h = 0;
+      if constexpr (D == 256) {
+        const int q = w4 * 4 + (lane >> 3);
+        h = q & 1;
+        cell = ((q >> 3) << 3) + ((q >> 1) & 3) + ((lane >> 2) & 1) * 4;
+      } else if constexpr (D == 128) {
+        const int q = w4 * 4 + (lane >> 3);
+        cell = ((q >> 2) << 3) + ((q & 3) ^ (((lane >> 2) & 1) * 5));
+      } else {
+        const int q = w4 * 2 + (lane >> 4), k = (lane >> 2) & 3;
+        cell = ((q >> 1) << 3) + ((q & 1) ^ ((k & 1) * 5) ^ ((k >> 1) * 2));
+      }
+      const int cg = cell & 15;
+      codes = (cell >> 4) * F::GROUP_BYTES + F::K_CODES + cg * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cg));
+      scales = (cell >> 4) * F::GROUP_BYTES + F::K_SCALES + cg * F::SROW + 8 * h;
+      first = 2 * h * (kTile * 128) + cell * 128 + ((t ^ (cell & 7)) << 4);
+    }
+    uint8_t* to = (v_side ? vbuf : kbuf) + b * G::BUF + first;
+    uint8_t* to4 = (v_side ? vbuf : kbuf) + b * G::BUF + (first ^ 64);  // chunk + 4
     uint32_t g = 0;
     for (long long x = x_begin; x < x_end && ok;) {
       const Part p = part_at(x);
       x += p.n;
-      for (int i = 0; i < p.n && ok; ++i, ++g) {
-        const int st = g % NP, b = g & 1;
+      const uint32_t g_end = g + p.n, g_first = g;
+      for (g += (g ^ b) & 1; g < g_end; g += 2) {
+        const int st = g % NP;
         const uint8_t* packed = ring + st * G::STAGE;
-        const int pos0 = p.q.base + (p.k0 + i) * kTile;
-        const bool edge = pos0 < p.q.lo || pos0 + kTile > p.q.hi;
+        const int pos0 = p.q.base + (p.k0 + static_cast<int>(g - g_first)) * kTile;
         // cells that no row sees may hold anything: they become zeros
-        auto hidden = [&](int cell) { return edge && (pos0 + cell < p.q.lo || pos0 + cell >= p.q.hi); };
-        bool here = mbar_wait(&pfull[st], (g / NP) & 1);
-        if (g >= 2) here = here && mbar_wait(&kfree[b], ((g >> 1) - 1) & 1);
+        const bool edge = pos0 < p.q.lo || pos0 + kTile > p.q.hi;
+        auto hidden = [&](int off) { return pos0 + cell + off < p.q.lo || pos0 + cell + off >= p.q.hi; };
+        bool here = kv4_wait(&pfull[st], (g / NP) & 1);
+        if (g >= 2) here = here && kv4_wait(free_, ((g >> 1) - 1) & 1);
         if (!__all_sync(0xffffffffu, here)) {
           ok = false;
           break;
         }
-        // K: 8 lanes take the four quads t of two cells whose rows lie in
-        // different banks, both as codes and, swizzled, as FP16
-        uint8_t* kb = kbuf + b * G::BUF;
-        constexpr int KW = B < 4 ? B : 4;  // words of a lane: blocks KW h ..
+        if (!v_side) {
+          constexpr int N = kTile / KSTEP;
+          uint32_t w[N][KW], d[N][KW];
 #pragma unroll
-        for (int it = 0; it < (D == 256 ? 2 : 1); ++it) {
-          int cell, h = 0;
-          if constexpr (D == 256) {
-            const int q = it * 32 + w8 * 4 + (lane >> 3);
-            h = q & 1;
-            cell = ((q >> 3) << 3) + ((q >> 1) & 3) + ((lane >> 2) & 1) * 4;
-          } else if constexpr (D == 128) {
-            const int q = w8 * 4 + (lane >> 3);
-            cell = ((q >> 2) << 3) + ((q & 3) ^ (((lane >> 2) & 1) * 5));
-          } else {
-            const int q = w8 * 2 + (lane >> 4), k = (lane >> 2) & 3;
-            cell = ((q >> 1) << 3) + ((q & 1) ^ ((k & 1) * 5) ^ ((k >> 1) * 2));
+          for (int it = 0; it < N; ++it) {
+            load_words<KW>(packed + codes + it * (KSTEP / 16) * F::GROUP_BYTES, w[it]);
+            load_scales<KW>(packed + scales + it * (KSTEP / 16) * F::GROUP_BYTES, d[it]);
+            if (edge && hidden(it * KSTEP))
+              for (int j = 0; j < KW; ++j) d[it][j] = 0;
           }
-          const uint8_t* grp = packed + (cell >> 4) * F::GROUP_BYTES;
-          const int cg = cell & 15;
-          uint32_t w[KW], d[KW];
-          load_words<KW>(grp + F::K_CODES + cg * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cg)), w);
-          load_scales<KW>(grp + F::K_SCALES + cg * F::SROW + 8 * h, d);
-          const bool zero = hidden(cell);
 #pragma unroll
-          for (int j = 0; j < KW; ++j) {
-            const int blk = 4 * h + j;  // word 4 blk + t: box blk / 2, chunk 4 (blk % 2) + t
-            const uint4 v = unpack(w[j], zero ? 0u : d[j]);
-            *reinterpret_cast<uint4*>(kb + (blk >> 1) * (kTile * 128) + cell * 128 + (((4 * (blk & 1) + t) ^ (cell & 7)) << 4)) = v;
+          for (int it = 0; it < N; ++it)
+#pragma unroll
+            for (int j = 0; j < KW; ++j)
+              *reinterpret_cast<uint4*>(((j & 1) ? to4 : to) + (j >> 1) * (kTile * 128) + it * KSTEP * 128) =
+                  unpack(w[it][j], d[it][j], kc);
+        } else {
+          uint32_t w[4][U], d[4][U];
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            load_words<U>(packed + codes + it * F::GROUP_BYTES, w[it]);
+            load_scales<U>(packed + scales + it * F::GROUP_BYTES, d[it]);
+            if (edge && hidden(it * 16))
+              for (int u = 0; u < U; ++u) d[it][u] = 0;
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kready[b]);
-        // V: 8 lanes take the 8 channel groups of one cell
-        if (g >= 2 && !__all_sync(0xffffffffu, mbar_wait(&vfree[b], ((g >> 1) - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        uint8_t* vb = vbuf + b * G::BUF;
-        const int ch = lane & 7;
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-          const int cell = it * 32 + w8 * 4 + (lane >> 3), cg = cell & 15;
-          const uint8_t* grp = packed + (cell >> 4) * F::GROUP_BYTES;
-          uint32_t w[U], d[U];
-          load_words<U>(grp + F::V_CODES + cg * F::ROW + 4 * U * (ch ^ F::v_swap(cg)), w);
-          load_scales<U>(grp + F::V_SCALES + cg * F::SROW + 2 * U * (ch >> 2), d);
-          const bool zero = hidden(cell);
+          for (int it = 0; it < 4; ++it)
 #pragma unroll
-          for (int u = 0; u < U; ++u)  // word 8u + ch: box u, chunk ch
-            *reinterpret_cast<uint4*>(vb + u * (kTile * 128) + cell * 128 + ((ch ^ (cell & 7)) << 4)) = unpack(w[u], zero ? 0u : d[u]);
+            for (int u = 0; u < U; ++u)
+              *reinterpret_cast<uint4*>(to + u * (kTile * 128) + it * 16 * 128) = unpack(w[it][u], d[it][u], kc);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&vready[b]);
+          mbar_arrive(ready);
           mbar_arrive(&pfree[st]);
         }
       }
+      g = g_end;
     }
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
   }
@@ -538,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kQkWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

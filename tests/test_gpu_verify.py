@@ -274,6 +274,14 @@ def test_attention_split_over_ctas(R, d, G, rows, kind):
     check_attn(R, attn_case(G, d, 1, G, [5000, 130, 9, 2500], [rows, 1, rows, 1], 64, kind), True)
 
 
+@pytest.mark.parametrize("d,heads,G,rows", [(64, 2, 3, 8), (64, 1, 16, 8), (128, 2, 8, 4), (256, 2, 12, 8), (256, 2, 12, 1), (128, 4, 4, 1)])
+def test_attention_many_tiles_per_cta(R, d, heads, G, rows):
+    """More tiles than a CTA's buffers hold, with and without quarters of rows that are empty, and parts of several
+    sequences in one CTA."""
+    lens = [20000, 40, 700, 12000, 9000] if d == 256 else [30000, 100, 2000, 17000]
+    check_attn(R, attn_case(d + rows, d, heads, G, lens, [rows] * len(lens), 128, "bf16"), True)
+
+
 def test_attention_many_short(R):
     rng = np.random.default_rng(5)
     lens = rng.integers(1, 60, 700)
