@@ -134,8 +134,7 @@ _SIGS = {
     "dflash_kv4_attention": (ctypes.c_int, [_KV4, _P, _P, _I, _L, _L, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I,
                                             ctypes.c_float, _P, _Z, _P, _P]),
     "dflash_kv4_attention_workspace": (_Z, [_KV4, _I, _I, _I, _I]),
-    "dflash_token_logprobs": (ctypes.c_int, [_P, _I, _L, _I, _I, _P, _P, _P, _I, _P, _P, _P, _Z, _P, _P]),
-    "dflash_token_logprobs_workspace": (_Z, [_I, _I, _I, _I]),
+    "dflash_token_logprobs": (ctypes.c_int, [_P, _I, _L, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
 }
 
 
@@ -390,13 +389,9 @@ def dflash_kv4_attention_workspace(cache: DflashKv4Cache, n_q_heads: int, n_seq:
 
 
 def dflash_token_logprobs(logits: int, value_type: int, row_stride: int, n_rows: int, vocab: int, tokens: int,
-                          logprob: int, entropy: int, top_k: int, top_ids: int, top_logprobs: int, workspace: int,
-                          workspace_bytes: int, dev_status: int = 0, stream: int = 0) -> None:
+                          logprob: int, entropy: int, top_k: int, top_ids: int, top_logprobs: int, dev_status: int = 0,
+                          stream: int = 0) -> None:
     _check(load_library().dflash_token_logprobs(logits, value_type, row_stride, n_rows, vocab, tokens or None,
                                                 logprob or None, entropy or None, top_k, top_ids or None,
-                                                top_logprobs or None, workspace or None, workspace_bytes,
-                                                dev_status or None, stream or None), "dflash_token_logprobs")
-
-
-def dflash_token_logprobs_workspace(n_rows: int, vocab: int, value_type: int, top_k: int) -> int:
-    return load_library().dflash_token_logprobs_workspace(n_rows, vocab, value_type, top_k)
+                                                top_logprobs or None, dev_status or None, stream or None),
+           "dflash_token_logprobs")

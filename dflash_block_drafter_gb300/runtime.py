@@ -17,7 +17,7 @@ from . import (DFLASH_ERR_INVALID_ARG, DFLASH_MAX_BLOCK, DFLASH_T_BF16, DFLASH_T
                dflash_state_read_draft_probs, dflash_state_set_spec_min_p, dflash_state_write_kv, load_library,
                dflash_state_set_defer_kv, dflash_state_flush,
                dflash_kv4_attention, dflash_kv4_attention_workspace, dflash_kv4_bytes, dflash_kv4_read,
-               dflash_kv4_write, dflash_page_tables, dflash_token_logprobs, dflash_token_logprobs_workspace,
+               dflash_kv4_write, dflash_page_tables, dflash_token_logprobs,
                make_config, make_weights)
 
 
@@ -338,12 +338,10 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     _int32(dev, "token_logprobs", tokens, status)
     stride, kind = logits.stride(0) if n > 1 else vocab, _VALUE_TYPES[logits.dtype]
     with _On(dev, stream) as st:
-        need = dflash_token_logprobs_workspace(n, vocab, kind, top_k)
         f = torch.empty(n * (2 + top_k), dtype=torch.float32, device=dev)
         ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         at = f.data_ptr()
         dflash_token_logprobs(logits.data_ptr(), kind, stride, n, vocab, _ptr(tokens), at if tokens is not None else 0,
-                              at + 4 * n, top_k, ids.data_ptr() if top_k else 0, at + 8 * n if top_k else 0, _ptr(ws),
-                              need, _ptr(status), st)
+                              at + 4 * n, top_k, ids.data_ptr() if top_k else 0, at + 8 * n if top_k else 0,
+                              _ptr(status), st)
     return f[:n] if tokens is not None else None, f[n: 2 * n], ids, f[2 * n:].view(n, top_k)

@@ -543,13 +543,10 @@ size_t dflash_kv4_attention_workspace(const dflash_kv4_cache* cache, int32_t n_q
  * alternative (id -1, log probability -infinity where fewer than top_k are left).
  * A row with every token masked has entropy 0 and log probabilities
  * -infinity.  A NaN or +infinity sets DFLASH_DEV_NONFINITE; that row's outputs are
- * unspecified.  workspace: dflash_token_logprobs_workspace bytes (may be 0),
- * 16-byte aligned, not shared by calls that overlap in time. */
+ * unspecified.  One launch. */
 int dflash_token_logprobs(const void* logits, int32_t type, int64_t row_stride, int32_t n_rows, int32_t vocab,
                           const int32_t* tokens, float* logprob, float* entropy, int32_t top_k, int32_t* top_ids,
-                          float* top_logprobs, void* workspace, size_t workspace_bytes, int32_t* dev_status,
-                          dflash_stream_t stream);
-size_t dflash_token_logprobs_workspace(int32_t n_rows, int32_t vocab, int32_t type, int32_t top_k);
+                          float* top_logprobs, int32_t* dev_status, dflash_stream_t stream);
 
 #ifdef __cplusplus
 }

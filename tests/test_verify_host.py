@@ -114,7 +114,7 @@ def test_page_tables_refusals(lib):
 
 def test_logprobs_refusals(lib):
     good = dict(x=FAKE, type=D.DFLASH_T_FP32, stride=100, rows=1, vocab=100, tok=FAKE, lp=FAKE, ent=FAKE, k=4, ids=FAKE, top=FAKE,
-                ws=FAKE, wsb=1 << 30, st=None, stream=None)
+                st=None, stream=None)
 
     def call(**kw):
         return lib.dflash_token_logprobs(*{**good, **kw}.values())
