@@ -4,12 +4,14 @@
 // (the first of equals), d = fp16(m / -8), code = clamp(rint(x / d), -8, 7) + 8
 // (rint: halves to even; every code 8 where d is 0); a cell's value is
 // d * (code - 8), so m itself is met to d's rounding.  x / d is a quotient of
-// two 11-bit significands at most: the 32-bit quotient lies on a half only
-// where the exact one does, so rounding it is rounding the exact quotient.
+// two 11-bit significands at most, which lies on a half or at least 2^-15 of
+// itself away from one: x times the rounded 1 / d (2^-23) rounds as x / d does,
+// unless x - (that half) d is exactly 0, where the even neighbour is taken.
 //
 // Both kernels are bound by memory: a thread holds the 8 channels of one code
-// word (a 16-byte load of K or V, one 4-byte store), the quad of a block
-// finds m by shuffles, and a warp covers 256 consecutive channels of a row.
+// word of K and of V (two 16-byte loads, two 4-byte stores; reading: two codes in,
+// 64 bytes out), the quad of a block finds m by shuffles, and a warp covers
+// 256 consecutive channels of a row.
 #include <cstddef>
 
 #include "internal.h"
@@ -31,6 +33,8 @@ struct CellArgs {
   float* k_out;
   float* v_out;
   int32_t* status;
+  int rows_of_block;
+  uint32_t magic;  // ceil(2^32 / words of a row)
 };
 
 // Address of the group of (slot, head); the cell in the group is slot % 16.
@@ -49,33 +53,34 @@ __device__ __forceinline__ float widen(uint32_t pair, int half) {
   return half ? __high2float(h) : __low2float(h);
 }
 
-// Thread = (row, side, head, word): words of a head fastest, then heads, then
-// K / V, then rows.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) kv4_write_kernel(const CellArgs a) {
-  using F = Kv4<D>;
-  const int per_row = 2 * a.n_kv * F::WORDS;
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long row = i / per_row;
-  if (row >= a.n_rows) return;  // whole quads leave: per_row is a multiple of 16
-  const int in_row = static_cast<int>(i - row * per_row);
-  const int w = in_row % F::WORDS, hs = in_row / F::WORDS;
-  const int side = hs >= a.n_kv, head = hs - side * a.n_kv;
-  const int slot = a.slots[row];
-  const long long cells = static_cast<long long>(a.n_pages) << a.page_shift;
-  if (slot < 0 || slot >= cells) {  // the same for the whole quad
-    if (slot >= cells && in_row == 0) set_status(a.status, DFLASH_DEV_CAPACITY);
-    return;
-  }
-  const unsigned quad = 0xfu << (threadIdx.x & 28);
-  const uint16_t* src = side ? a.v + row * a.v_stride : a.k + row * a.k_stride;
-  const uint4 raw = *reinterpret_cast<const uint4*>(src + head * D + w * 8);
+// A block takes the words of `rows` rows (a multiple of 4 words each, so
+// that quads stay whole): item = row * words + word of the row's heads.
+// Dividing by `words` is a multiplication: both are far below 2^16.
+struct Item {
+  int row, head, w;  // row in the block; head; word of the head
+  bool in;
+};
+template <int D>
+__device__ __forceinline__ Item item_of(const CellArgs& a, int i) {
+  Item t;
+  const int words = a.n_kv * Kv4<D>::WORDS;
+  t.row = static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.magic));
+  const int word = i - t.row * words;
+  t.head = word / Kv4<D>::WORDS;
+  t.w = word % Kv4<D>::WORDS;
+  t.in = t.row < a.rows_of_block;
+  return t;
+}
+
+// The code word and scale of 8 of a block's 32 values, whose other lanes are the quad's.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantise(uint4 raw, int w, unsigned quad, __half& scale, bool& bad) {
   const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = widen<BF16>(pr[e >> 1], e & 1);
   float top = 0.f;
-  bool bad = false;
+  bad = false;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     top = fmaxf(top, fabsf(x[e]));
@@ -91,64 +96,99 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const CellArgs a) {
     if (fabsf(x[e]) == top) first = ((w & 3) * 8 + e) * 2 + (x[e] < 0.f ? 1 : 0);
   first = min(first, __shfl_xor_sync(quad, first, 1));
   first = min(first, __shfl_xor_sync(quad, first, 2));
-  const __half dh = __float2half_rn((first & 1) ? top * 0.125f : top * -0.125f);
-  const float d = __half2float(dh);
-  uint32_t code = 0x88888888u;
-  __half store = dh;
-  if (bad) {
-    store = __ushort_as_half(0);
-    if ((w & 3) == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-  } else if (d != 0.f) {
-    code = 0;
+  scale = __float2half_rn((first & 1) ? top * 0.125f : top * -0.125f);
+  const float d = __half2float(scale);
+  if (bad) scale = __ushort_as_half(0);
+  if (bad || d == 0.f) return 0x88888888u;
+  const float inv = 1.f / d, half = fabsf(d) * 0.5f;
+  uint32_t code = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int q = static_cast<int>(fminf(fmaxf(rintf(x[e] / d), -8.f), 7.f)) + 8;
-      code |= static_cast<uint32_t>(q) << (4 * e);
+  for (int e = 0; e < 8; ++e) {
+    float r = rintf(x[e] * inv);
+    const float rest = fmaf(-r, d, x[e]);  // exact: a few bits
+    // on a half, and the odd neighbour was met
+    if (fabsf(rest) == half && (static_cast<int>(r) & 1)) r += (rest < 0.f) != (d < 0.f) ? -1.f : 1.f;
+    const int q = static_cast<int>(fminf(fmaxf(r, -8.f), 7.f)) + 8;
+    code |= static_cast<uint32_t>(q) << (4 * e);
+  }
+  return code;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) kv4_write_kernel(const CellArgs a) {
+  using F = Kv4<D>;
+  const int total = a.rows_of_block * a.n_kv * F::WORDS;
+  const unsigned quad = 0xfu << (threadIdx.x & 28);
+  for (int i = threadIdx.x; i < total; i += 256) {
+    const Item t = item_of<D>(a, i);
+    const long long row = static_cast<long long>(blockIdx.x) * a.rows_of_block + t.row;
+    if (!t.in || row >= a.n_rows) continue;  // the same for the whole quad, as the slot's
+    const int slot = a.slots[row];
+    const long long cells = static_cast<long long>(a.n_pages) << a.page_shift;
+    if (slot < 0 || slot >= cells) {
+      if (slot >= cells && t.head == 0 && t.w == 0) set_status(a.status, DFLASH_DEV_CAPACITY);
+      continue;
+    }
+    const int col = t.head * D + t.w * 8;
+    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(a.k + row * a.k_stride + col));
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(a.v + row * a.v_stride + col));
+    __half ks, vs;
+    bool kbad, vbad;
+    const uint32_t kc = quantise<BF16>(k, t.w, quad, ks, kbad), vc = quantise<BF16>(v, t.w, quad, vs, vbad);
+    uint8_t* g = group_of<D>(a, slot, t.head);
+    const int cell = slot & 15;
+    *reinterpret_cast<uint32_t*>(g + F::k_word(cell, t.w)) = kc;
+    *reinterpret_cast<uint32_t*>(g + F::v_word(cell, t.w)) = vc;
+    if ((t.w & 3) == 0) {
+      *reinterpret_cast<__half*>(g + F::k_scale(cell, t.w >> 2)) = ks;
+      *reinterpret_cast<__half*>(g + F::v_scale(cell, t.w >> 2)) = vs;
+      if (kbad || vbad) set_status(a.status, DFLASH_DEV_NONFINITE);
     }
   }
-  uint8_t* g = group_of<D>(a, slot, head);
-  const int cell = slot & 15;
-  *reinterpret_cast<uint32_t*>(g + (side ? F::v_word(cell, w) : F::k_word(cell, w))) = code;
-  if ((w & 3) == 0) *reinterpret_cast<__half*>(g + (side ? F::v_scale(cell, w >> 2) : F::k_scale(cell, w >> 2))) = store;
+}
+
+__device__ __forceinline__ void put_values(float* out, uint32_t code, float d) {
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = d * static_cast<float>(static_cast<int>((code >> (4 * e)) & 15u) - 8);
+  __stcs(reinterpret_cast<float4*>(out), make_float4(y[0], y[1], y[2], y[3]));
+  __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(y[4], y[5], y[6], y[7]));
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const CellArgs a) {
   using F = Kv4<D>;
-  const int per_row = 2 * a.n_kv * F::WORDS;
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long row = i / per_row;
-  if (row >= a.n_rows) return;
-  const int in_row = static_cast<int>(i - row * per_row);
-  const int w = in_row % F::WORDS, hs = in_row / F::WORDS;
-  const int side = hs >= a.n_kv, head = hs - side * a.n_kv;
-  float* base = side ? a.v_out : a.k_out;
-  if (!base) return;
-  const int slot = a.slots[row];
-  const long long cells = static_cast<long long>(a.n_pages) << a.page_shift;
-  float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (slot >= 0 && slot < cells) {
-    const uint8_t* g = group_of<D>(a, slot, head);
-    const int cell = slot & 15;
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(g + (side ? F::v_word(cell, w) : F::k_word(cell, w)));
-    const float d = __half2float(
-        *reinterpret_cast<const __half*>(g + (side ? F::v_scale(cell, w >> 2) : F::k_scale(cell, w >> 2))));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = d * static_cast<float>(static_cast<int>((code >> (4 * e)) & 15u) - 8);
-  } else if (slot >= cells && in_row == 0) {
-    set_status(a.status, DFLASH_DEV_CAPACITY);
+  const int total = a.rows_of_block * a.n_kv * F::WORDS;
+  for (int i = threadIdx.x; i < total; i += 256) {
+    const Item t = item_of<D>(a, i);
+    const long long row = static_cast<long long>(blockIdx.x) * a.rows_of_block + t.row;
+    if (!t.in || row >= a.n_rows) continue;
+    const int slot = a.slots[row];
+    const long long cells = static_cast<long long>(a.n_pages) << a.page_shift;
+    uint32_t kc = 0, vc = 0;
+    float kd = 0.f, vd = 0.f;
+    if (slot >= 0 && slot < cells) {
+      const uint8_t* g = group_of<D>(a, slot, t.head);
+      const int cell = slot & 15;
+      kc = *reinterpret_cast<const uint32_t*>(g + F::k_word(cell, t.w));
+      vc = *reinterpret_cast<const uint32_t*>(g + F::v_word(cell, t.w));
+      kd = __half2float(*reinterpret_cast<const __half*>(g + F::k_scale(cell, t.w >> 2)));
+      vd = __half2float(*reinterpret_cast<const __half*>(g + F::v_scale(cell, t.w >> 2)));
+    } else if (slot >= cells && t.head == 0 && t.w == 0) {
+      set_status(a.status, DFLASH_DEV_CAPACITY);
+    }
+    const long long at = (row * a.n_kv + t.head) * D + t.w * 8;
+    if (a.k_out) put_values(a.k_out + at, kc, kd);
+    if (a.v_out) put_values(a.v_out + at, vc, vd);
   }
-  float4* out = reinterpret_cast<float4*>(base + (row * a.n_kv + head) * D + w * 8);
-  out[0] = make_float4(y[0], y[1], y[2], y[3]);
-  out[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
 template <int D>
-cudaError_t launch(const CellArgs& a, int type, bool write, cudaStream_t st) {
-  const long long total = static_cast<long long>(a.n_rows) * 2 * a.n_kv * Kv4<D>::WORDS;
-  const long long blocks = (total + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const unsigned grid = static_cast<unsigned>(blocks);
+cudaError_t launch(CellArgs a, int type, bool write, cudaStream_t st) {
+  const int words = a.n_kv * Kv4<D>::WORDS;  // 8 .. 8192
+  a.rows_of_block = words >= 512 ? 1 : 512 / words;
+  a.magic = static_cast<uint32_t>(((1ull << 32) + words - 1) / words);
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.n_rows) + a.rows_of_block - 1) / a.rows_of_block);
   if (!write) kv4_read_kernel<D><<<grid, 256, 0, st>>>(a);
   else if (type == DFLASH_T_BF16) kv4_write_kernel<D, true><<<grid, 256, 0, st>>>(a);
   else kv4_write_kernel<D, false><<<grid, 256, 0, st>>>(a);

@@ -7,10 +7,11 @@
 // The work is a few bytes per request and per row, so launches are what it
 // costs: one launch does it all.  Every CTA forms the prefix sums of all
 // requests in its own shared memory (at most kMaxRequests of them), then the
-// rows, taken pages and given pages are shared out over all CTAs, each item
-// finding its request by binary search.  The CTAs form one cluster, whose
-// barrier orders their last read of held / ring_state before the first CTA
-// updates them, so that both may be updated in place.
+// rows (four neighbours a thread, for one search and one store), taken pages
+// and given pages are shared out over all CTAs, each item finding its request
+// by binary search.  The CTAs form one cluster, whose barrier orders their
+// last read of held / ring_state before the first CTA updates them, so that
+// both may be updated in place.
 #include "common.cuh"
 #include "internal.h"
 #include "kernels.h"
@@ -20,7 +21,7 @@ namespace {
 
 constexpr int kMaxRequests = 4096;
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;
+constexpr int kCluster = 16;  // CTAs at most
 
 struct PageArgs {
   const int32_t* lengths;
@@ -72,12 +73,17 @@ __device__ __forceinline__ int upper(const int* end, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a) {
-  extern __shared__ int ends[];  // [3][n_seq]: rows, pages taken, pages given, up to and with a request
+  // [5][n_seq]: rows, pages taken, pages given, up to and with a request; its
+  // length; its pages held before (their complement where it has no place in
+  // the table)
+  extern __shared__ int ends[];
   __shared__ long long part[3][33];
   __shared__ int s_taken;
   int* row_end = ends;
   int* take_end = ends + a.n_seq;
   int* give_end = ends + 2 * a.n_seq;
+  int* s_len = ends + 3 * a.n_seq;
+  int* s_held = ends + 4 * a.n_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x;  // one cluster: the grid is the cluster
   const int head = a.ring_in[0], free_pages = min(max(a.ring_in[1], 0), a.n_pages);
@@ -95,6 +101,8 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a)
       v[0] = q.rows;
       v[1] = max(q.need - q.held, 0);
       v[2] = max(q.held - q.need, 0);
+      s_len[s] = a.lengths[s];
+      s_held[s] = q.fits ? q.held : ~q.held;
       if (rank == 0 && q.valid && !q.fits) set_status(a.status, DFLASH_DEV_CAPACITY);
     }
 #pragma unroll
@@ -143,16 +151,16 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a)
   for (int i = t0; i < taken; i += step) {
     const int s = upper(take_end, a.n_seq, i);
     const int first = s ? take_end[s - 1] : 0;
-    const int held = min(max(a.held_in[s], 0), a.table_stride);
     int at = ring0 + i;
     if (at >= a.n_pages) at -= a.n_pages;
-    a.table[static_cast<size_t>(s) * a.table_stride + held + (i - first)] = a.ring[at];
+    a.table[static_cast<size_t>(s) * a.table_stride + s_held[s] + (i - first)] = a.ring[at];
   }
   // pages given back: table -> ring's tail
   for (int i = t0; i < given; i += step) {
     const int s = upper(give_end, a.n_seq, i);
     const int first = s ? give_end[s - 1] : 0;
-    const int page = a.table[static_cast<size_t>(s) * a.table_stride + request(a, s).need + (i - first)];
+    const int need = s_held[s] - (give_end[s] - first);
+    const int page = a.table[static_cast<size_t>(s) * a.table_stride + need + (i - first)];
     long long at = static_cast<long long>(ring0) + free_pages + i;
     at -= at >= a.n_pages ? a.n_pages : 0;
     at -= at >= a.n_pages ? a.n_pages : 0;
@@ -160,31 +168,45 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a)
     bad |= page < 0 || page >= a.n_pages;
   }
   // slots and positions of the rows
-  for (int r = t0; r < a.row_cap; r += step) {
-    int slot = -1, pos = -1;
-    if (r < rows) {
-      const int s = upper(row_end, a.n_seq, r);
-      const Request q = request(a, s);
-      const int len = a.lengths[s];
-      const int before = s ? row_end[s - 1] : 0;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) % 16 == 0;
+  for (long long r0 = 4ll * t0; r0 < a.row_cap; r0 += 4ll * step) {
+    int slot[4], pos[4];
+    int s = r0 < rows ? upper(row_end, a.n_seq, static_cast<int>(r0)) : 0;
+    int seen_s = -1, seen_p = -1, page = -1;  // the page looked up last
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long r = r0 + j;
+      slot[j] = pos[j] = -1;
+      if (r >= rows || r >= a.row_cap) continue;
+      while (row_end[s] <= r) ++s;
+      const int before = s ? row_end[s - 1] : 0, held = s_held[s];
       const int take0 = s ? take_end[s - 1] : 0, take1 = take_end[s];
-      pos = saturate(static_cast<long long>(len) + (r - before));
-      if (q.fits && (take1 == take0 || take1 <= free_pages)) {
-        const int p = pos >> a.page_shift;
-        int page;
-        if (p < q.held) {
+      pos[j] = saturate(s_len[s] + (r - before));
+      if (held < 0 || (take1 > take0 && take1 > free_pages)) continue;
+      const int p = pos[j] >> a.page_shift;
+      if (s != seen_s || p != seen_p) {
+        if (p < held) {
           page = a.table[static_cast<size_t>(s) * a.table_stride + p];
         } else {
-          int at = ring0 + take0 + (p - q.held);
+          int at = ring0 + take0 + (p - held);
           if (at >= a.n_pages) at -= a.n_pages;
           page = a.ring[at];
         }
-        if (page >= 0 && page < a.n_pages) slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-        else bad = true;
+        seen_s = s;
+        seen_p = p;
+      }
+      if (page >= 0 && page < a.n_pages) slot[j] = (page << a.page_shift) + (pos[j] & ((1 << a.page_shift) - 1));
+      else bad = true;
+    }
+    if (wide && r0 + 4 <= a.row_cap) {
+      *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (a.positions) *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int j = 0; j < 4 && r0 + j < a.row_cap; ++j) {
+        a.slots[r0 + j] = slot[j];
+        if (a.positions) a.positions[r0 + j] = pos[j];
       }
     }
-    a.slots[r] = slot;
-    if (a.positions) a.positions[r] = pos;
   }
   if (bad) set_status(a.status, DFLASH_DEV_CAPACITY);
   // every CTA has read what the first now updates
@@ -197,9 +219,9 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a)
   }
   if (rank != 0) return;
   for (int s = tid; s < a.n_seq; s += kThreads) {
-    const Request q = request(a, s);
-    const int take0 = s ? take_end[s - 1] : 0, take1 = take_end[s];
-    a.held_out[s] = q.fits && (take1 == take0 || take1 <= free_pages) ? q.need : q.held;
+    const int take0 = s ? take_end[s - 1] : 0, take1 = take_end[s], give0 = s ? give_end[s - 1] : 0;
+    const int held = s_held[s];
+    a.held_out[s] = held < 0 ? ~held : take1 == take0 ? held - (give_end[s] - give0) : take1 <= free_pages ? held + take1 - take0 : held;
     a.row_offsets[s + 1] = row_end[s];
   }
   if (tid == 0) {
@@ -231,21 +253,25 @@ extern "C" int dflash_page_tables(const int32_t* lengths, const int32_t* new_row
              row_offsets, slots, positions, row_cap, dev_status};
   while ((1 << a.page_shift) < page_size) ++a.page_shift;
   cudaLaunchConfig_t cfg = {};
-  // one CTA for a step's rows; the whole cluster for prompts
-  cfg.gridDim = dim3(row_cap <= 4 * kThreads ? 1 : kCluster);
+  // a CTA for every 4096 rows: one for a decoding step, the largest cluster for prompts
+  int ctas = 1;
+  while (ctas < kCluster && row_cap > 4 * kThreads * ctas) ctas *= 2;
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 3 * sizeof(int) * n_seq;
+  cfg.dynamicSmemBytes = 5 * sizeof(int) * n_seq;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cfg.gridDim.x;
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cfg.dynamicSmemBytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               3 * static_cast<int>(sizeof(int)) * kMaxRequests);
-    if (e != cudaSuccess) return cuda_status(e, "page tables");
-  }
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  cudaError_t e = cudaSuccess;
+  if (cfg.dynamicSmemBytes > 40 * 1024)
+    e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             5 * static_cast<int>(sizeof(int)) * kMaxRequests);
+  if (e == cudaSuccess && ctas > 8)  // beyond the portable size
+    e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_status(e, "page tables");
   return cuda_status(cudaLaunchKernelEx(&cfg, page_tables_kernel, a), "page tables");
 }

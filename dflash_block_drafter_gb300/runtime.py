@@ -186,67 +186,59 @@ def commit_positions(anchor_pos: torch.Tensor, accept_len: torch.Tensor, positio
 
 # -------------------------------------------------------------- verify step
 # The operators of include/dflash.h's verify step on torch tensors.  Each runs
-# on the device of its first tensor, on that device's current stream unless
-# one is given; outputs and workspaces come from torch's allocator on that
+# on the device of its tensors, on that device's current stream unless one is
+# given; outputs and workspaces come from torch's allocator on the current
 # stream.  `status` is an optional int32 tensor for the DFLASH_DEV_* bits.
+# (Small calls take as long as their Python: the checks are plain ones.)
 _VALUE_TYPES = {torch.float32: DFLASH_T_FP32, torch.bfloat16: DFLASH_T_BF16, torch.float16: DFLASH_T_FP16}
+_INT32 = torch.int32
 
 
-def _refuse(ok: bool, what: str) -> None:
-    if not ok:
-        raise DflashError(DFLASH_ERR_INVALID_ARG, what)
+def _refuse(what: str):
+    raise DflashError(DFLASH_ERR_INVALID_ARG, what)
 
 
-class _On:
-    """The device of a call made current, and its stream."""
-
-    def __init__(self, device: torch.device, stream):
-        self.before = torch.cuda.current_device()
-        self.device = self.before if device.index is None else device.index
-        self.given = stream
-
-    def __enter__(self) -> int:
-        if self.device != self.before:
-            torch.cuda.set_device(self.device)
-        if self.given is not None and self.given.device_index != self.device:
-            self.__exit__()
-            _refuse(False, "the stream is of another device")
-        return (self.given or torch.cuda.current_stream()).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.device != self.before:
-            torch.cuda.set_device(self.before)
+def _raw_stream(index: int, stream) -> int:
+    """The stream to launch on, on the (current) device `index`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        _refuse("the stream is of another device")
+    return stream.cuda_stream
 
 
 def _int32(device, what: str, *tensors) -> None:
     for x in tensors:
-        if x is not None and not (x.dtype == torch.int32 and x.device == device and x.is_contiguous()):
-            _refuse(False, f"{what}: contiguous int32 tensors on {device}")
-
-
-def _ptr(x: Optional[torch.Tensor]) -> int:
-    return 0 if x is None else x.data_ptr()
+        if x is not None and (x.dtype != _INT32 or x.device != device or not x.is_contiguous()):
+            _refuse(what + ": contiguous int32 tensors on the device of the call")
 
 
 def kv4_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda:0") -> torch.Tensor:
     """A zeroed 4-bit paged K/V cache: uint8 [n_pages, n_kv_heads, page_size / 16, 18 * head_dim]."""
     load_library()
-    _refuse(dflash_kv4_bytes(n_pages, page_size, n_kv_heads, head_dim) > 0, "kv4_cache: geometry")
+    if dflash_kv4_bytes(n_pages, page_size, n_kv_heads, head_dim) == 0:
+        _refuse("kv4_cache: geometry")
     return torch.zeros((n_pages, n_kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
 
 
 def _kv4(cache: torch.Tensor) -> DflashKv4Cache:
-    _refuse(cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 4 and cache.is_contiguous()
-            and cache.shape[3] % 18 == 0, "a 4-bit cache is a contiguous uint8 tensor of kv4_cache's shape")
+    if not (cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 4 and cache.is_contiguous()):
+        _refuse("a 4-bit cache is a contiguous uint8 tensor of kv4_cache's shape")
     n_pages, heads, groups, size = cache.shape
+    if size % 18:
+        _refuse("a 4-bit cache is a contiguous uint8 tensor of kv4_cache's shape")
     return DflashKv4Cache(cache.data_ptr(), n_pages, 16 * groups, heads, size // 18)
 
 
-def _rows(x: torch.Tensor, device, what: str) -> int:
+def _row_stride(x: torch.Tensor, device, what: str) -> int:
     """Elements between the rows of [rows, heads, head_dim] values whose heads are dense."""
-    _refuse(x.device == device and x.dim() == 3 and x.stride(2) == 1 and x.stride(1) == x.shape[2]
-            and x.dtype in (torch.bfloat16, torch.float16), f"{what}: [rows, heads, head_dim] BF16 or FP16, heads dense")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    if x.dim() != 3 or x.device != device or x.dtype not in _VALUE_TYPES:
+        _refuse(what + ": [rows, heads, head_dim] values on the device of the call")
+    rows, heads, d = x.shape
+    stride, by_head, by_value = x.stride()
+    if by_value != 1 or (by_head != d and heads > 1):
+        _refuse(what + ": the heads of a row must be dense")
+    return stride if rows > 1 else heads * d
 
 
 def page_tables(lengths: torch.Tensor, new_rows: torch.Tensor, held: torch.Tensor, table: torch.Tensor,
@@ -256,43 +248,60 @@ def page_tables(lengths: torch.Tensor, new_rows: torch.Tensor, held: torch.Tenso
     (row_offsets [n_seq + 1], slots [row_cap], positions [row_cap]).  `table`
     and `ring` are updated in place, `held` and `ring_state` too unless
     held_out / ring_state_out are given."""
-    dev, n = table.device, lengths.numel()
-    held_out = held if held_out is None else held_out
-    ring_state_out = ring_state if ring_state_out is None else ring_state_out
+    dev = table.device
+    if not table.is_cuda:
+        _refuse("page_tables: CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return page_tables(lengths, new_rows, held, table, ring, ring_state, page_size, row_cap, held_out,
+                               ring_state_out, status, stream)
+    if held_out is None:
+        held_out = held
+    if ring_state_out is None:
+        ring_state_out = ring_state
     _int32(dev, "page_tables", lengths, new_rows, held, table, ring, ring_state, held_out, ring_state_out, status)
-    _refuse(table.is_cuda and table.dim() == 2 and table.shape[0] == n and new_rows.numel() == n and held.numel() == n
-            and held_out.numel() == n and ring_state.numel() == 2 and ring_state_out.numel() == 2, "page_tables: sizes")
-    with _On(dev, stream) as st:
-        out = torch.empty(n + 1 + 2 * row_cap, dtype=torch.int32, device=dev)
-        at = out.data_ptr()
-        dflash_page_tables(lengths.data_ptr(), new_rows.data_ptr(), n, page_size, ring.numel(), held.data_ptr(),
-                           held_out.data_ptr(), table.data_ptr(), table.shape[1], ring.data_ptr(),
-                           ring_state.data_ptr(), ring_state_out.data_ptr(), at, at + 4 * (n + 1),
-                           at + 4 * (n + 1 + row_cap), row_cap, _ptr(status), st)
-    return out[: n + 1], out[n + 1: n + 1 + row_cap], out[n + 1 + row_cap:]
+    n = lengths.numel()
+    if (table.dim() != 2 or table.shape[0] != n or new_rows.numel() != n or held.numel() != n or held_out.numel() != n
+            or ring_state.numel() != 2 or ring_state_out.numel() != 2 or row_cap < 0):
+        _refuse("page_tables: sizes")
+    wide = (row_cap + 3) & ~3  # slots and positions start on 16 bytes
+    out = torch.empty(2 * wide + n + 1, dtype=_INT32, device=dev)
+    at = out.data_ptr()
+    dflash_page_tables(lengths.data_ptr(), new_rows.data_ptr(), n, page_size, ring.numel(), held.data_ptr(),
+                       held_out.data_ptr(), table.data_ptr(), table.shape[1], ring.data_ptr(), ring_state.data_ptr(),
+                       ring_state_out.data_ptr(), at + 8 * wide, at, at + 4 * wide, row_cap,
+                       0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+    return out[2 * wide:], out[:row_cap], out[wide: wide + row_cap]
 
 
 def kv4_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, status=None,
               stream=None) -> None:
     """Quantise rows k, v [n, n_kv_heads, head_dim] into the cells `slots` [n] (-1: none)."""
     c, dev = _kv4(cache), cache.device
-    ks, vs = _rows(k, dev, "kv4_write k"), _rows(v, dev, "kv4_write v")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_write(cache, k, v, slots, status, stream)
+    ks, vs = _row_stride(k, dev, "kv4_write k"), _row_stride(v, dev, "kv4_write v")
     _int32(dev, "kv4_write slots", slots, status)
-    _refuse(k.shape == v.shape and k.dtype == v.dtype and k.shape[0] == slots.numel() and k.shape[1] == c.n_kv_heads
-            and k.shape[2] == c.head_dim, "kv4_write: shapes")
-    with _On(dev, stream) as st:
-        dflash_kv4_write(c, k.data_ptr(), v.data_ptr(), _VALUE_TYPES[k.dtype], ks, vs, slots.data_ptr(),
-                         slots.numel(), _ptr(status), st)
+    n, heads, d = k.shape
+    if k.shape != v.shape or k.dtype != v.dtype or n != slots.numel() or heads != c.n_kv_heads or d != c.head_dim:
+        _refuse("kv4_write: shapes")
+    dflash_kv4_write(c, k.data_ptr(), v.data_ptr(), _VALUE_TYPES[k.dtype], ks, vs, slots.data_ptr(), n,
+                     0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
 
 
 def kv4_read(cache: torch.Tensor, slots: torch.Tensor, status=None, stream=None):
     """(k, v), float [n, n_kv_heads, head_dim], of the cells `slots` (zeros for -1)."""
     c, dev = _kv4(cache), cache.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_read(cache, slots, status, stream)
     _int32(dev, "kv4_read slots", slots, status)
-    with _On(dev, stream) as st:
-        out = torch.empty((2, slots.numel(), c.n_kv_heads, c.head_dim), dtype=torch.float32, device=dev)
-        k, v = out.unbind(0)
-        dflash_kv4_read(c, slots.data_ptr(), slots.numel(), k.data_ptr(), v.data_ptr(), _ptr(status), st)
+    n = slots.numel()
+    k = torch.empty((n, c.n_kv_heads, c.head_dim), dtype=torch.float32, device=dev)
+    v = torch.empty((n, c.n_kv_heads, c.head_dim), dtype=torch.float32, device=dev)
+    dflash_kv4_read(c, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), 0 if status is None else status.data_ptr(),
+                    _raw_stream(dev.index, stream))
     return k, v
 
 
@@ -303,26 +312,33 @@ def kv4_attention(cache: torch.Tensor, q: torch.Tensor, table: torch.Tensor, kv_
     their sequences; scale None is head_dim ** -0.5.  Rows of no sequence keep
     what `out` held (unset if out is None)."""
     c, dev = _kv4(cache), cache.device
-    qs = _rows(q, dev, "kv4_attention q")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_attention(cache, q, table, kv_len, row_offsets, max_rows, causal, window, scale, out, workspace,
+                                 status, stream)
+    qs = _row_stride(q, dev, "kv4_attention q")
     _int32(dev, "kv4_attention", table, kv_len, row_offsets, status)
+    tokens, heads, d = q.shape
     n = kv_len.numel()
-    _refuse(q.shape[2] == c.head_dim and table.dim() == 2 and table.shape[0] == n and row_offsets.numel() == n + 1,
-            "kv4_attention: shapes")
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            os_ = c.head_dim * q.shape[1]
-        else:
-            _refuse(out.shape == q.shape and out.dtype == q.dtype, "kv4_attention: out")
-            os_ = _rows(out, dev, "kv4_attention out")
-        need = dflash_kv4_attention_workspace(c, q.shape[1], n, max_rows, table.shape[1])
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _refuse(workspace.device == dev and workspace.is_contiguous(), "kv4_attention: workspace")
-        dflash_kv4_attention(c, q.data_ptr(), out.data_ptr(), _VALUE_TYPES[q.dtype], qs, os_, q.shape[0], q.shape[1],
-                             n, max_rows, row_offsets.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1],
-                             causal, window, c.head_dim ** -0.5 if scale is None else scale, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _ptr(status), st)
+    if d != c.head_dim or table.dim() != 2 or table.shape[0] != n or row_offsets.numel() != n + 1:
+        _refuse("kv4_attention: shapes")
+    if out is None:
+        out, os_ = torch.empty((tokens, heads, d), dtype=q.dtype, device=dev), heads * d
+    else:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            _refuse("kv4_attention: out")
+        os_ = _row_stride(out, dev, "kv4_attention out")
+    if workspace is None:
+        size = dflash_kv4_attention_workspace(c, heads, n, max_rows, table.shape[1])
+        workspace = torch.empty(size + 16, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != dev or not workspace.is_contiguous():
+            _refuse("kv4_attention: workspace")
+    dflash_kv4_attention(c, q.data_ptr(), out.data_ptr(), _VALUE_TYPES[q.dtype], qs, os_, tokens, heads, n, max_rows,
+                         row_offsets.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1], causal, window,
+                         d ** -0.5 if scale is None else scale, workspace.data_ptr(), size,
+                         0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
     return out
 
 
@@ -331,17 +347,23 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     """Scores of logits [rows, vocab]: (logprob [rows] of `tokens` or None,
     entropy [rows], top_ids [rows, top_k], top_logprobs [rows, top_k])."""
     dev = logits.device
-    _refuse(logits.is_cuda and logits.dim() == 2 and logits.dtype in _VALUE_TYPES
-            and (logits.stride(1) == 1 or logits.shape[1] == 1), "token_logprobs: [rows, vocab] logits, rows dense")
+    kind = _VALUE_TYPES.get(logits.dtype)
+    if not logits.is_cuda or logits.dim() != 2 or kind is None:
+        _refuse("token_logprobs: [rows, vocab] logits on a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, tokens, top_k, status, stream)
     n, vocab = logits.shape
-    _refuse(tokens is None or tokens.numel() == n, "token_logprobs: one token a row")
+    stride, by_value = logits.stride()
+    if (by_value != 1 and vocab != 1) or (tokens is not None and tokens.numel() != n) or top_k < 0:
+        _refuse("token_logprobs: dense rows, one token each")
     _int32(dev, "token_logprobs", tokens, status)
-    stride, kind = logits.stride(0) if n > 1 else vocab, _VALUE_TYPES[logits.dtype]
-    with _On(dev, stream) as st:
-        f = torch.empty(n * (2 + top_k), dtype=torch.float32, device=dev)
-        ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
-        at = f.data_ptr()
-        dflash_token_logprobs(logits.data_ptr(), kind, stride, n, vocab, _ptr(tokens), at if tokens is not None else 0,
-                              at + 4 * n, top_k, ids.data_ptr() if top_k else 0, at + 8 * n if top_k else 0,
-                              _ptr(status), st)
-    return f[:n] if tokens is not None else None, f[n: 2 * n], ids, f[2 * n:].view(n, top_k)
+    logp = None if tokens is None else torch.empty(n, dtype=torch.float32, device=dev)
+    entropy = torch.empty(n, dtype=torch.float32, device=dev)
+    ids = torch.empty((n, top_k), dtype=_INT32, device=dev)
+    top = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+    dflash_token_logprobs(logits.data_ptr(), kind, stride if n > 1 else vocab, n, vocab,
+                          0 if tokens is None else tokens.data_ptr(), 0 if logp is None else logp.data_ptr(),
+                          entropy.data_ptr(), top_k, ids.data_ptr(), top.data_ptr(),
+                          0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+    return logp, entropy, ids, top
