@@ -5,8 +5,11 @@
 // (rint: halves to even; every code 8 where d is 0); a cell's value is
 // d * (code - 8), so m itself is met to d's rounding.  x / d is a quotient of
 // two 11-bit significands at most, which lies on a half or at least 2^-15 of
-// itself away from one: x times the rounded 1 / d (2^-23) rounds as x / d does,
-// unless x - (that half) d is exactly 0, where the even neighbour is taken.
+// itself away from one: x times the rounded 1 / d (2^-24) rounds as x / d does,
+// but for the halves themselves.  They show in |x - round * d| = |d| / 2, exactly,
+// and are put right in a branch of their own (with BF16 values about every tenth
+// block has one); a block that has m with both signs, or a d so small that |x / d|
+// passes 8.4, takes the plain way, a division per value.
 //
 // Both kernels are bound by memory: a thread holds the 8 channels of one code
 // word of K and of V (two 16-byte loads, two 4-byte stores; reading: two codes in,
@@ -72,44 +75,101 @@ __device__ __forceinline__ Item item_of(const CellArgs& a, int i) {
   return t;
 }
 
+// max and min that return NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The plain way, by the definition; `first` is the sign of m's first occurrence.
+template <bool BF16>
+__device__ __noinline__ uint32_t quantise_plain(uint4 raw, int w, unsigned quad, float top, __half* scale) {
+  const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
+  int first = 1 << 10;  // smallest (index, sign)
+  for (int e = 7; e >= 0; --e) {
+    const float x = widen<BF16>(e < 2 ? pr[0] : e < 4 ? pr[1] : e < 6 ? pr[2] : pr[3], e & 1);
+    if (fabsf(x) == top) first = ((w & 3) * 8 + e) * 2 + (x < 0.f ? 1 : 0);
+  }
+  first = min(first, __shfl_xor_sync(quad, first, 1));
+  first = min(first, __shfl_xor_sync(quad, first, 2));
+  *scale = __float2half_rn((first & 1) ? top * 0.125f : top * -0.125f);
+  const float d = __half2float(*scale);
+  if (d == 0.f) return 0x88888888u;
+  uint32_t code = 0;
+  for (int e = 0; e < 8; ++e) {
+    const float x = widen<BF16>(e < 2 ? pr[0] : e < 4 ? pr[1] : e < 6 ? pr[2] : pr[3], e & 1);
+    const int q = static_cast<int>(fminf(fmaxf(rintf(x / d), -8.f), 7.f)) + 8;
+    code |= static_cast<uint32_t>(q) << (4 * e);
+  }
+  return code;
+}
+
 // The code word and scale of 8 of a block's 32 values, whose other lanes are the quad's.
 template <bool BF16>
 __device__ __forceinline__ uint32_t quantise(uint4 raw, int w, unsigned quad, __half& scale, bool& bad) {
-  const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = widen<BF16>(pr[e >> 1], e & 1);
-  float top = 0.f;
-  bad = false;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    top = fmaxf(top, fabsf(x[e]));
-    bad |= !(fabsf(x[e]) <= 65504.f);  // beyond FP16's range, infinite or NaN
-  }
-  top = fmaxf(top, __shfl_xor_sync(quad, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(quad, top, 2));
-  bad = __any_sync(quad, bad);
-  // sign of the first element of that magnitude: smallest (index, sign)
-  int first = 1 << 10;
-#pragma unroll
-  for (int e = 7; e >= 0; --e)
-    if (fabsf(x[e]) == top) first = ((w & 3) * 8 + e) * 2 + (x[e] < 0.f ? 1 : 0);
-  first = min(first, __shfl_xor_sync(quad, first, 1));
-  first = min(first, __shfl_xor_sync(quad, first, 2));
-  scale = __float2half_rn((first & 1) ? top * 0.125f : top * -0.125f);
+  const uint32_t up = max_pair<BF16>(max_pair<BF16>(raw.x, raw.y), max_pair<BF16>(raw.z, raw.w));
+  const uint32_t down = min_pair<BF16>(min_pair<BF16>(raw.x, raw.y), min_pair<BF16>(raw.z, raw.w));
+  float hi = max_nan(widen<BF16>(up, 0), widen<BF16>(up, 1)), lo = -min_nan(widen<BF16>(down, 0), widen<BF16>(down, 1));
+  hi = max_nan(hi, __shfl_xor_sync(quad, hi, 1));
+  lo = max_nan(lo, __shfl_xor_sync(quad, lo, 1));
+  hi = max_nan(hi, __shfl_xor_sync(quad, hi, 2));
+  lo = max_nan(lo, __shfl_xor_sync(quad, lo, 2));
+  const float top = max_nan(hi, lo);
+  bad = !(top <= 65504.f);  // a value beyond FP16's range, an infinity or a NaN
+  scale = __float2half_rn(hi > lo ? top * -0.125f : top * 0.125f);
   const float d = __half2float(scale);
-  if (bad) scale = __ushort_as_half(0);
-  if (bad || d == 0.f) return 0x88888888u;
   const float inv = 1.f / d, half = fabsf(d) * 0.5f;
-  uint32_t code = 0;
+  constexpr float MAGIC = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, which its low bits then hold
+  const bool plain = hi == lo || !(top * fabsf(inv) < 8.4f);
+  bool tie = false;
+  const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
+  float r[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float r = rintf(x[e] * inv);
-    const float rest = fmaf(-r, d, x[e]);  // exact: a few bits
-    // on a half, and the odd neighbour was met
-    if (fabsf(rest) == half && (static_cast<int>(r) & 1)) r += (rest < 0.f) != (d < 0.f) ? -1.f : 1.f;
-    const int q = static_cast<int>(fminf(fmaxf(r, -8.f), 7.f)) + 8;
-    code |= static_cast<uint32_t>(q) << (4 * e);
+    const float x = widen<BF16>(pr[e >> 1], e & 1);
+    r[e] = fmaf(x, inv, MAGIC);
+    tie |= fabsf(fmaf(MAGIC - r[e], d, x)) == half;  // (exact: a few bits)
+  }
+  if (tie) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = widen<BF16>(pr[e >> 1], e & 1), rest = fmaf(MAGIC - r[e], d, x);
+      // the odd neighbour was met: to the even one, on the side of the rest
+      if (fabsf(rest) == half && (__float_as_uint(r[e]) & 1u)) r[e] += (rest < 0.f) != (d < 0.f) ? -1.f : 1.f;
+    }
+  }
+  uint32_t y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(fminf(r[e], MAGIC + 7.f));
+  // low nibbles, plus 8: bytes of the even and the odd values, then side by side
+  const uint32_t even = prmt(prmt(y[0], y[2], 0x0040u), prmt(y[4], y[6], 0x0040u), 0x5410u) & 0x0f0f0f0fu;
+  const uint32_t odd = prmt(prmt(y[1], y[3], 0x0040u), prmt(y[5], y[7], 0x0040u), 0x5410u) & 0x0f0f0f0fu;
+  uint32_t code = (even | odd << 4) ^ 0x88888888u;
+  if (bad) {
+    scale = __ushort_as_half(0);
+    code = 0x88888888u;
+  } else if (__any_sync(quad, plain)) {
+    code = quantise_plain<BF16>(raw, w, quad, top, &scale);
   }
   return code;
 }
@@ -151,8 +211,10 @@ __device__ __forceinline__ void put_values(float* out, uint32_t code, float d) {
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = d * static_cast<float>(static_cast<int>((code >> (4 * e)) & 15u) - 8);
-  __stcs(reinterpret_cast<float4*>(out), make_float4(y[0], y[1], y[2], y[3]));
-  __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(y[4], y[5], y[6], y[7]));
+  // one store of a whole 32-byte sector: two of 16 bytes would each write half of all the warp's sectors
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(y[0]), "f"(y[1]), "f"(y[2]),
+               "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+               : "memory");
 }
 
 template <int D>
@@ -264,7 +326,7 @@ int dflash_kv4_read(const dflash_kv4_cache* c, const int32_t* slots, int32_t n_r
   if (const int e = dflash_kv4_check(c)) return e;
   if (n_rows < 0) return DFLASH_ERR_INVALID_ARG;
   if (n_rows == 0 || (!k_out && !v_out)) return DFLASH_OK;
-  if (!slots || reinterpret_cast<uintptr_t>(k_out) % 16 || reinterpret_cast<uintptr_t>(v_out) % 16)
+  if (!slots || reinterpret_cast<uintptr_t>(k_out) % 32 || reinterpret_cast<uintptr_t>(v_out) % 32)
     return DFLASH_ERR_INVALID_ARG;
   CellArgs a{};
   a.data = static_cast<uint8_t*>(c->data);

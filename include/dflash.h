@@ -491,7 +491,7 @@ int dflash_kv4_write(const dflash_kv4_cache* cache, const void* k, const void* v
 
 /* Read cells back as float (exact), [n_rows, n_kv_heads, head_dim] each; k_out
  * or v_out may be NULL.  Rows with a slot outside the cache are zeros (beyond
- * it: DFLASH_DEV_CAPACITY too).  Outputs 16-byte aligned. */
+ * it: DFLASH_DEV_CAPACITY too).  Outputs 32-byte aligned. */
 int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t n_rows, float* k_out, float* v_out,
                     int32_t* dev_status, dflash_stream_t stream);
 

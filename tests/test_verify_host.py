@@ -70,7 +70,7 @@ def test_write_and_read_refusals(lib):
     assert w(c, None, None, D.DFLASH_T_FP16, 0, 0, None, 0, None, None) == D.DFLASH_OK  # no rows: nothing to do
     r = lib.dflash_kv4_read
     assert r(c, None, 1, FAKE, FAKE, None, None) == inv
-    assert r(c, FAKE, 1, P(4100), FAKE, None, None) == inv
+    assert r(c, FAKE, 1, P(4112), FAKE, None, None) == inv
     assert r(c, FAKE, -1, FAKE, FAKE, None, None) == inv
     assert r(c, FAKE, 0, FAKE, FAKE, None, None) == D.DFLASH_OK
     assert r(c, FAKE, 3, None, None, None, None) == D.DFLASH_OK
