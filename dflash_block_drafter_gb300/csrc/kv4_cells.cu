@@ -4,12 +4,12 @@
 // (the first of equals), d = fp16(m / -8), code = clamp(rint(x / d), -8, 7) + 8
 // (rint: halves to even; every code 8 where d is 0); a cell's value is
 // d * (code - 8), so m itself is met to d's rounding.  x / d is a quotient of
-// two 11-bit significands at most, which lies on a half or at least 2^-15 of
-// itself away from one: x times the rounded 1 / d (2^-24) rounds as x / d does,
-// but for the halves themselves.  They show in |x - round * d| = |d| / 2, exactly,
-// and are put right in a branch of their own (with BF16 values about every tenth
-// block has one); a block that has m with both signs, or a d so small that |x / d|
-// passes 8.4, takes the plain way, a division per value.
+// two 11-bit significands at most: near 0.5 .. 8.5 it lies on a half or more
+// than 2^-13 away from one.  x times the approximate 1 / d is off by less than
+// 2^-19; rounded to a multiple of 2^-17 (one FMA onto 96) it is on a half exactly
+// where x / d is, and on the same side elsewhere, so that one more addition rounds
+// it as the definition says.  Where d is so small (FP16's subnormals) that |x / d|
+// passes 8.4, each value is divided.
 //
 // Both kernels are bound by memory: a thread holds the 8 channels of one code
 // word of K and of V (two 16-byte loads, two 4-byte stores; reading: two codes in,
@@ -101,24 +101,30 @@ __device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The plain way, by the definition; `first` is the sign of m's first occurrence.
+// Whether the block's first value of magnitude `top` is negative.
 template <bool BF16>
-__device__ __noinline__ uint32_t quantise_plain(uint4 raw, int w, unsigned quad, float top, __half* scale) {
+__device__ __noinline__ bool first_is_negative(uint4 raw, int w, unsigned quad, float top) {
   const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
   int first = 1 << 10;  // smallest (index, sign)
+#pragma unroll
   for (int e = 7; e >= 0; --e) {
-    const float x = widen<BF16>(e < 2 ? pr[0] : e < 4 ? pr[1] : e < 6 ? pr[2] : pr[3], e & 1);
+    const float x = widen<BF16>(pr[e >> 1], e & 1);
     if (fabsf(x) == top) first = ((w & 3) * 8 + e) * 2 + (x < 0.f ? 1 : 0);
   }
   first = min(first, __shfl_xor_sync(quad, first, 1));
   first = min(first, __shfl_xor_sync(quad, first, 2));
-  *scale = __float2half_rn((first & 1) ? top * 0.125f : top * -0.125f);
-  const float d = __half2float(*scale);
+  return first & 1;
+}
+
+// The codes by a division per value (d may be 0).
+template <bool BF16>
+__device__ __noinline__ uint32_t divide_all(uint4 raw, float d) {
   if (d == 0.f) return 0x88888888u;
+  const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t code = 0;
+#pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float x = widen<BF16>(e < 2 ? pr[0] : e < 4 ? pr[1] : e < 6 ? pr[2] : pr[3], e & 1);
-    const int q = static_cast<int>(fminf(fmaxf(rintf(x / d), -8.f), 7.f)) + 8;
+    const int q = static_cast<int>(fminf(fmaxf(rintf(widen<BF16>(pr[e >> 1], e & 1) / d), -8.f), 7.f)) + 8;
     code |= static_cast<uint32_t>(q) << (4 * e);
   }
   return code;
@@ -136,31 +142,20 @@ __device__ __forceinline__ uint32_t quantise(uint4 raw, int w, unsigned quad, __
   lo = max_nan(lo, __shfl_xor_sync(quad, lo, 2));
   const float top = max_nan(hi, lo);
   bad = !(top <= 65504.f);  // a value beyond FP16's range, an infinity or a NaN
-  scale = __float2half_rn(hi > lo ? top * -0.125f : top * 0.125f);
+  bool negative = lo > hi;
+  if (hi == lo) negative = first_is_negative<BF16>(raw, w, quad, top);  // m with both signs, or all zeros
+  scale = __float2half_rn(negative ? top * 0.125f : top * -0.125f);
   const float d = __half2float(scale);
-  const float inv = 1.f / d, half = fabsf(d) * 0.5f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
   constexpr float MAGIC = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, which its low bits then hold
-  const bool plain = hi == lo || !(top * fabsf(inv) < 8.4f);
-  bool tie = false;
   const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
-  float r[8];
+  uint32_t y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float x = widen<BF16>(pr[e >> 1], e & 1);
-    r[e] = fmaf(x, inv, MAGIC);
-    tie |= fabsf(fmaf(MAGIC - r[e], d, x)) == half;  // (exact: a few bits)
+    y[e] = __float_as_uint(fminf(fmaf(x, inv, 96.f) + (MAGIC - 96.f), MAGIC + 7.f));
   }
-  if (tie) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = widen<BF16>(pr[e >> 1], e & 1), rest = fmaf(MAGIC - r[e], d, x);
-      // the odd neighbour was met: to the even one, on the side of the rest
-      if (fabsf(rest) == half && (__float_as_uint(r[e]) & 1u)) r[e] += (rest < 0.f) != (d < 0.f) ? -1.f : 1.f;
-    }
-  }
-  uint32_t y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(fminf(r[e], MAGIC + 7.f));
   // low nibbles, plus 8: bytes of the even and the odd values, then side by side
   const uint32_t even = prmt(prmt(y[0], y[2], 0x0040u), prmt(y[4], y[6], 0x0040u), 0x5410u) & 0x0f0f0f0fu;
   const uint32_t odd = prmt(prmt(y[1], y[3], 0x0040u), prmt(y[5], y[7], 0x0040u), 0x5410u) & 0x0f0f0f0fu;
@@ -168,8 +163,8 @@ __device__ __forceinline__ uint32_t quantise(uint4 raw, int w, unsigned quad, __
   if (bad) {
     scale = __ushort_as_half(0);
     code = 0x88888888u;
-  } else if (__any_sync(quad, plain)) {
-    code = quantise_plain<BF16>(raw, w, quad, top, &scale);
+  } else if (!(top * fabsf(inv) < 8.4f)) {  // (the same for the quad)
+    code = divide_all<BF16>(raw, d);
   }
   return code;
 }
