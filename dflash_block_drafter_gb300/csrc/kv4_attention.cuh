@@ -202,18 +202,22 @@ struct Kv4Job {
 };
 
 // Joins the pieces of split segments: o = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i.  Block (j, z): the j-th split segment, found by
-// counting the records; its rows and 64-channel slices z, z + gridDim.y, ...
-// 16 lanes hold a slice, 16 groups of them take every 16th piece, so that a
-// segment of 150 pieces costs a thread ten loads in flight, not 150 in turn.
+// sum_i 2^(m_i - m) l_i.  Blocks (j, y): the j-th split segment, found by
+// counting the records.  A warp has a row, a lane D / 32 channels of it.  With up to
+// kFewPieces pieces the 8 warps of the blocks y take a row each; with more, the 8
+// warps of a block share a row's pieces and join through shared memory, so that a
+// segment of 150 pieces costs a warp 19 of them, four or eight in flight, not 150
+// in turn.
 constexpr int kMergeThreads = 256;
+constexpr int kFewPieces = 8;
 
 template <int D, int R>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnArgs a, int most) {
-  __shared__ int s_count[kMergeThreads / 32];
+  constexpr int E = D / 32, WARPS = kMergeThreads / 32, U = D == 256 ? 4 : 8;
+  __shared__ int s_count[WARPS];
   __shared__ int s_cta;
-  __shared__ float4 acc[kMergeThreads];
-  __shared__ float2 accl[16];
+  __shared__ float acc[WARPS][D];
+  __shared__ float2 accl[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_cta = -1;
   pdl_wait();
@@ -225,84 +229,98 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
     if (lane == 0) s_count[warp] = __popc(m);
     __syncthreads();
     int n = before + __popc(m & ((1u << lane) - 1));
-    for (int w = 0; w < kMergeThreads / 32; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) n += s_count[w];
       before += s_count[w];
     }
     if (is && n == static_cast<int>(blockIdx.x)) s_cta = c;
     __syncthreads();
+    if (s_cta >= 0) break;
   }
   const int c = s_cta;
   if (c < 0) return;
-  const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));
-  const int last = __ldcg(&a.jobs[c].last);
-  const int n = last - c + 1;
-  auto slot = [&](int i) { return 2 * (c + i) + (i == 0); };
-  const int l16 = tid & 15, p = tid >> 4;
-  for (int z = blockIdx.y; z < j0.w * (D / 64); z += gridDim.y) {
-    const int m = z / (D / 64), col = (z % (D / 64)) * 64 + l16 * 4;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f, top = -INFINITY;
-    constexpr int U = 4;
-    for (int i0 = p; i0 < n; i0 += 16 * U) {
+  const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));  // r0, row0, head, rows
+  const int n = __ldcg(&a.jobs[c].last) - c + 1;
+  const bool few = n <= kFewPieces;
+  const int i0 = few ? 0 : warp, step = few ? 1 : WARPS;
+  const int m0 = few ? blockIdx.y * WARPS + warp : blockIdx.y, m_step = gridDim.y * (few ? WARPS : 1);
+  for (int m = m0; m < j0.w; m += m_step) {
+    float o[E], l = 0.f, top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int i = i0; i < n; i += step * U) {
       float2 ml[U];
-      float4 v[U];
+      float v[U][E];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + 16 * u;
+        const int k = i + u * step;
         ml[u] = make_float2(-INFINITY, 0.f);
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n) {
-          const size_t at = static_cast<size_t>(slot(i)) * R + m;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+        if (k < n) {
+          const size_t at = static_cast<size_t>(2 * (c + k) + (k == 0)) * R + m;
           ml[u] = __ldcg(a.part_ml + at);
-          v[u] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + col));
+#pragma unroll
+          for (int e = 0; e < E; e += (E < 4 ? 2 : 4)) {  // 64 or 128 channels of the row a load
+            if constexpr (E < 4) {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part + at * D) + lane);
+              v[u][0] = x.x, v[u][1] = x.y;
+            } else {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + (e >> 2) * 32 + lane);
+              v[u][e] = x.x, v[u][e + 1] = x.y, v[u][e + 2] = x.z, v[u][e + 3] = x.w;
+            }
+          }
         }
       }
       float t = top;
 #pragma unroll
       for (int u = 0; u < U; ++u) t = fmaxf(t, ml[u].x);
       const float from = t == -INFINITY ? 0.f : t, f = ex2_approx(top - from);
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
       l *= f;
       top = t;
 #pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
       for (int u = 0; u < U; ++u) {
         const float w = ex2_approx(ml[u].x - from);
-        o.x = fmaf(w, v[u].x, o.x);
-        o.y = fmaf(w, v[u].y, o.y);
-        o.z = fmaf(w, v[u].z, o.z);
-        o.w = fmaf(w, v[u].w, o.w);
         l = fmaf(w, ml[u].y, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[u][e], o[e]);
       }
     }
-    __syncthreads();  // the last round's sums have been read
-    acc[tid] = o;
-    if (l16 == 0) accl[p] = make_float2(top, l);
-    __syncthreads();
-    if (p == 0) {
+    if (!few) {  // the warps' results: every warp adds up D / 8 channels
+      __syncthreads();  // the last row's have been read
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[warp][e * 32 + lane] = o[e];
+      if (lane == 0) accl[warp] = make_float2(top, l);
+      __syncthreads();
+      if (warp > 0) continue;
       float t = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t = fmaxf(t, accl[i].x);
+      for (int w = 0; w < WARPS; ++w) t = fmaxf(t, accl[w].x);
       const float from = t == -INFINITY ? 0.f : t;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
       l = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = ex2_approx(accl[i].x - from);
-        const float4 v = acc[i * 16 + l16];
-        o.x = fmaf(w, v.x, o.x);
-        o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z);
-        o.w = fmaf(w, v.w, o.w);
-        l = fmaf(w, accl[i].y, l);
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ex2_approx(accl[w].x - from);
+        l = fmaf(f, accl[w].y, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, acc[w][e * 32 + lane], o[e]);
       }
-      if (!(l < INFINITY) && l16 == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int row = j0.y + m;
-      uint16_t* dst = a.out + (j0.x + row / a.G) * a.out_stride + (j0.z * a.G + row % a.G) * D + col;
-      *reinterpret_cast<uint2*>(dst) =
-          a.bf16 ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv))
-                 : make_uint2(pack_f16x2(o.x * inv, o.y * inv), pack_f16x2(o.z * inv, o.w * inv));
+    }
+    if (!(l < INFINITY) && lane == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int row = j0.y + m;
+    uint16_t* dst = a.out + (j0.x + row / a.G) * a.out_stride + (j0.z * a.G + row % a.G) * D;
+    auto pack = [&](float x, float y) { return a.bf16 ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv); };
+    if constexpr (E < 4) {
+      reinterpret_cast<uint32_t*>(dst)[lane] = pack(o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        reinterpret_cast<uint2*>(dst)[(e >> 2) * 32 + lane] = make_uint2(pack(o[e], o[e + 1]), pack(o[e + 2], o[e + 3]));
     }
   }
 }
@@ -312,9 +330,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
 template <int D, int R>
 cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  // one block per segment that may be split and per row and 64 channels of it, fewer where there are many
-  const int z = R * (D / 64), y = 2048 / jobs;
-  cfg.gridDim = dim3(jobs, y < 1 ? 1 : y < z ? y : z);
+  // few segments: one block per row, which many pieces want; many: at least one warp per row
+  const int y = 1536 / jobs, few = (R + 7) / 8;
+  cfg.gridDim = dim3(jobs, y < few ? few : y < R ? y : R);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

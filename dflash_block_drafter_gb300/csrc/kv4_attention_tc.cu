@@ -12,12 +12,11 @@
 //   warps 12..19  unpack K, warps 20..27 unpack V, once for all rows: FP16
 //                 d (code - 8) in the 128-byte-swizzled layouts the MMAs read,
 //                 double-buffered; four warps each for the even and the odd tiles.
-// Q is an A operand in tensor memory (FP16 pairs), P one in shared memory (over
-// S in tensor memory it would keep the next but one Q K^T waiting for P V).
-// Per tile and D = 256, shared memory takes 64 KB of K and V written and read
-// and 16 KB of P (about 1300 cycles of its bandwidth), the MMAs 1024
-// cycles and the tile's bytes from HBM 790; the columns of tensor memory are
-// S0 | S1 | O | Q = 64 + 64 + D + D / 2.
+// Q and P are the MMAs' A operands in tensor memory (FP16 pairs), P over the S it
+// came from, so that shared memory, which bounds the kernel, carries only K and V:
+// per tile and D = 256 64 KB written and read (1000 cycles), as much as the
+// MMAs take, against 790 cycles for the tile's bytes from HBM; the columns of
+// tensor memory are S0 | S1 | O | Q = 64 + 64 + D + D / 2.
 //
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
 // masking the word yields pairs: Q's columns are stored in the same order,
@@ -44,7 +43,7 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
               "the roles' registers come out of the launch's");
-constexpr int kPacked = 3;      // stages of the packed ring
+constexpr int kPacked = 4;      // stages of the packed ring
 constexpr int kAhead = 7;       // tiles that L2 is asked for in advance (fewer than 8)
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
@@ -54,13 +53,12 @@ struct Geo {
   static constexpr int STAGE = kGroups * Kv4<D>::GROUP_BYTES;
   static constexpr int BUF = kTile * D * 2;  // one unpacked K or V tile
   static constexpr int RED = 3 * kRows * 4;
-  static constexpr int PBUF = kRows * kTile * 2;
-  static constexpr int SMEM = 1024 + 4 * BUF + 2 * PBUF + kPacked * STAGE + RED;
+  static constexpr int SMEM = 1024 + 4 * BUF + kPacked * STAGE + RED;
   static constexpr int S_COL = 0, O_COL = 2 * kTile, Q_COL = O_COL + D;
 };
 
-// D[tmem] (+)= A * B[smem desc], kind::f16, one CTA; A in tensor memory or by a
-// descriptor too.  A descriptor comes in two words: only its low one, the address, changes between the
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA.  The descriptor
+// comes in two words: only its low one, the address, changes between the
 // MMAs of a tile, so that a warp that computes it as a whole keeps it in
 // uniform registers and issues an MMA in a few instructions (with one lane's
 // 64-bit descriptors the issue, not the tensor cores, took the time).
@@ -82,18 +80,6 @@ __device__ __forceinline__ void more_registers() {
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void umma_f16_sa(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "mov.b64 a, {%1, %2};\n\t"
-      "mov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 // Two FP32 values in one register pair, and the instructions that take both.
@@ -188,13 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                       // [2][D / 64 boxes][64 cells][128 B]
   uint8_t* vbuf = kbuf + 2 * G::BUF;          // [2]
-  uint8_t* pbuf = vbuf + 2 * G::BUF;          // [2][128 rows][128 B]
-  uint8_t* ring = pbuf + 2 * G::PBUF;         // [NP] packed tiles
+  uint8_t* ring = vbuf + 2 * G::BUF;          // [NP] packed tiles
   float* s_ref = reinterpret_cast<float*>(ring + NP * G::STAGE);    // [128 rows] references of the scores
   float* red_sum = s_ref + R;                                       // [2][128 rows]
   long long* pre = reinterpret_cast<long long*>(red_sum + 2 * R);   // [n_seq + 1]
   __shared__ long long scratch[kThreads / 32];
-  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[2], sfree[2], pready[2], qready, ofree, done[2];
+  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[2], pready[2], qready, ofree, done[2];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -209,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       mbar_init(&vready[i], kUnpackWarps / 2);
       mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&sfree[i], kSoftWarps / 2);
       mbar_init(&pready[i], kSoftWarps / 2);
       mbar_init(&done[i], 1);
     }
@@ -323,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       for (int i = 0; i < n && ok; ++i, ++g) {
         const uint32_t b = g & 1, was = (g >> 1) & 1;
         bool here = kv4_wait(&kready[b], was);
-        if (g >= 2) here = here && kv4_wait(&sfree[b], was ^ 1);
+        if (g >= 2) here = here && kv4_wait(&vfree[b], was ^ 1);  // P of tile g - 2 lies in the same columns
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
@@ -346,9 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------ O += P V
     constexpr uint32_t idesc = umma_idesc_f16(128, D, false, true);
-    const uint64_t vd = umma_desc_sw128(smem_u32(vbuf), kTile * 128, 1024), pd = umma_desc_sw128(smem_u32(pbuf), 16, 1024);
+    const uint64_t vd = umma_desc_sw128(smem_u32(vbuf), kTile * 128, 1024);
     const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
-    const uint32_t p_lo = static_cast<uint32_t>(pd), p_hi = static_cast<uint32_t>(pd >> 32);
     const bool one = elect_one();
     uint32_t g = 0, part = 0;
     for (long long x = x_begin; x < x_end && ok; ++part) {
@@ -362,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t lo = v_lo + b * (G::BUF >> 4), from = p_lo + b * (G::PBUF >> 4), more = i > 0;
+        const uint32_t lo = v_lo + b * (G::BUF >> 4), from = tmem + G::S_COL + b * kTile, more = i > 0;
         if (one) {
-          umma_f16_sa(tmem + G::O_COL, from, p_hi, lo, v_hi, idesc, more);
+          umma_f16_ta(tmem + G::O_COL, from, lo, v_hi, idesc, more);
 #pragma unroll
           for (int kk = 1; kk < kTile / 16; ++kk)
-            umma_f16_sa(tmem + G::O_COL, from + kk * (32 >> 4), p_hi, lo + kk * (2048 >> 4), v_hi, idesc, 1);
+            umma_f16_ta(tmem + G::O_COL, from + kk * 8, lo + kk * (2048 >> 4), v_hi, idesc, 1);
           umma_commit(&vfree[b]);
         }
         __syncwarp();
@@ -456,10 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           tmem_reg_fence(r[0]);
           tmem_reg_fence(r[1]);
         }
-        // S[b] has been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[b]);
         if (live) {
           if (pos0 < all_lo || pos0 + kTile > all_hi) {
 #pragma unroll
@@ -518,24 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               unpack2(fma2(pack2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), factor2, from2), x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               sum2 = add2(sum2, pack2(p0, p1));
-              r[h][e >> 1] = pack_f16x2(p0, p1);
+              r[0][16 * h + (e >> 1)] = pack_f16x2(p0, p1);
             }
           float s0, s1;
           unpack2(sum2, s0, s1);
           l += s0 + s1;
+          tmem_st32(s_addr, r[0]);
+          tmem_wait_st();
         }
-        // P[b] is free once P V of tile g - 2 is done.  Warps without rows wait
-        // too: S of tile g only waits for S of g - 2 to be read, so they could
-        // otherwise announce P of tile g before the others that of g - 2.
-        if (ok && g >= 2) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[b], ((g >> 1) - 1) & 1));
-        if (live) {
-          uint8_t* prow = pbuf + b * G::PBUF + m * 128;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(prow + ((k ^ (m & 7)) << 4)) =
-                make_uint4(r[k >> 2][4 * (k & 3)], r[k >> 2][4 * (k & 3) + 1], r[k >> 2][4 * (k & 3) + 2], r[k >> 2][4 * (k & 3) + 3]);
-        }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[b]);
