@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeast = 1;     // tiles that a CTA takes at least
+constexpr int kOverhead = 2;  // a segment's beginning and end, in tiles
 constexpr int kPerSm = 3;     // CTAs per SM
 constexpr float kSlack = 8.f; // log2 units by which a score may pass the reference
 
@@ -129,15 +129,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
     for (int i = 0; i < ST; ++i) mbar_init(&full[i], kWarps);
     fence_barrier_init();
   }
-  const long long T = kv4_plan<TILE, R>(a, pre, scratch, blockIdx.x == 0);
-  const int C = kv4_ctas(T, gridDim.x, kLeast);
+  const long long T = kv4_plan<TILE, R, kOverhead>(a, pre, scratch, blockIdx.x == 0);
+  const int C = kv4_ctas(T, gridDim.x);
   const int c = blockIdx.x;
   pdl_launch_dependents();
   if (c >= C || T == 0) {
     if (tid == 0) a.jobs[c].n_rows = 0;
     return;
   }
-  long long x = kv4_start(T, C, c);
   const long long x_end = kv4_start(T, C, c + 1);
 
   const int groups_of_page = 1 << (a.page_shift - 4);
@@ -146,26 +145,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
   uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
   bool ok = true, job = false;
 
-  // a segment's part in this CTA: tiles [k0, k0 + n) of a sequence, kv head and row group
-  struct Part {
-    Kv4Seq q;
-    int s, head, row0, k0, n;
-  };
-  auto part_at = [&](long long at) {
-    Part p{};
-    if (at >= x_end) return p;
-    p.s = kv4_find(pre, a.n_seq, at);
-    p.q = kv4_seq<TILE, R>(a, p.s, false);
-    const long long rel = at - pre[p.s];
-    const int unit = static_cast<int>(rel / p.q.steps);
-    p.k0 = static_cast<int>(rel - static_cast<long long>(unit) * p.q.steps);
-    p.n = static_cast<int>(min(static_cast<long long>(p.q.steps - p.k0), x_end - at));
-    p.head = unit / p.q.groups;
-    p.row0 = unit % p.q.groups * R;
-    return p;
-  };
   // the lanes look up the pages of this warp's groups, 32 / MT tiles at a time
-  auto look_up = [&](const Part& p, int from) {
+  auto look_up = [&](const Kv4Part& p, int from) {
     const int i = from + lane / MT;
     const int pos = p.q.base + (p.k0 + i) * TILE + (warp * MT + lane % MT) * 16;
     if (i >= p.n || pos >= p.q.hi) return -1;
@@ -177,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
     return page;
   };
   // copies this warp's groups of tile i of a part as the ring's fill `fill`
-  auto issue = [&](const Part& p, int i, uint32_t fill, int pages) {
+  auto issue = [&](const Kv4Part& p, int i, uint32_t fill, int pages) {
     const int st = fill % ST;
     int page[MT], bytes = 0;
 #pragma unroll
@@ -199,18 +180,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
     }
   };
 
-  Part cur = part_at(x);
+  Kv4Part cur = kv4_part<TILE, R, kOverhead>(a, pre, kv4_start(T, C, c), x_end, Kv4Part{});
   int pages = look_up(cur, 0);
   int issued = 0;  // tiles of the current part that are on their way
   for (; issued < min(cur.n, ST); ++issued) issue(cur, issued, issued, pages);
   while (cur.n > 0) {
     const Kv4Seq q = cur.q;
     const int k0 = cur.k0, k1 = cur.k0 + cur.n, head = cur.head, row0 = cur.row0;
-    const int n_rows = min(R, q.rows * a.G - row0);
-    x += cur.n;
+    const int n_rows = cur.rows;
     const int n = ok ? cur.n : 0;  // tiles
     // the next part's first tiles follow this one's last without a gap
-    const Part next = part_at(x);
+    const Kv4Part next = kv4_part<TILE, R, kOverhead>(a, pre, cur.next, x_end, cur);
     int next_pages = look_up(next, 0);
     int next_issued = 0;
     __syncthreads();  // the last segment is done with Q and P
@@ -587,8 +567,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4Att
     if (!whole && k0 == 0) {  // the segment goes on in the next CTAs
       job = true;
       if (tid == 0) {
-        const long long end = x - k1 + q.steps;  // first step behind the segment
-        Kv4Job r{q.r0, row0, head, n_rows, kv4_owner(T, C, end - 1), {0, 0, 0}};
+        Kv4Job r{q.r0, row0, head, n_rows, kv4_owner(T, C, cur.end - 1), {0, 0, 0}};
         a.jobs[c] = r;
       }
     }
@@ -660,7 +639,7 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads * groups;
   // (a window may begin anywhere in a tile)
   const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
-  const long long ctas = (segments * tiles + kLeast - 1) / kLeast;
+  const long long ctas = segments * (tiles + kOverhead);
   // one wave of CTAs: every one of them has the same share
   const int smem = smem_of(c->head_dim, out->nt) + kPlanBytes(n_seq) + kStaticSmem;
   const int per_sm = kSmemOfSm / smem < kPerSm ? kSmemOfSm / smem : kPerSm;

@@ -4,9 +4,12 @@
 // A sequence s with r rows over kv cells has, per kv head, G * r query rows
 // (row m = token m / G, head of the group m % G) which read the same cells.
 // They are cut into row groups of R rows; (sequence, kv head, row group) is
-// a segment.  A segment walks its visible cells in steps; all segments'
-// steps laid end to end are shared out evenly over C CTAs, so that every CTA
-// has the same work whatever the lengths.  A segment that lies inside one CTA
+// a segment.  A segment walks its visible cells in steps.  It counts as its
+// steps plus OV units, which stand for what it costs to begin and to end one;
+// all segments' units laid end to end are shared out evenly over C CTAs, so that
+// every CTA has about the same work whatever the lengths (counted by steps
+// alone, a CTA of 200 short requests got 17 segments where the mean was 4, and took
+// twice the mean's time).  A segment that lies inside one CTA
 // is written out by it; one that crosses into others leaves a piece (running
 // maximum, sum, unnormalised O in FP32) per CTA, and the merge kernel joins
 // them.  A CTA's range can hold at most two pieces: of the segment that began
@@ -138,9 +141,9 @@ __device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, 
   return make_int2(lo, max(last + 1, 0));
 }
 
-// Prefix sums of the sequences' steps (over kv heads and row groups) in
+// Prefix sums of the sequences' units (over kv heads and row groups) in
 // `pre` [n_seq + 1] by the whole CTA; returns the total.
-template <int STEP, int R>
+template <int STEP, int R, int OV>
 __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* pre, long long* scratch, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
   long long carry = 0;
@@ -149,7 +152,7 @@ __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* p
     long long v = 0;
     if (s < a.n_seq) {
       const Kv4Seq q = kv4_seq<STEP, R>(a, s, report);
-      v = static_cast<long long>(q.steps) * q.groups * a.n_kv;
+      if (q.rows > 0) v = static_cast<long long>(q.steps + OV) * q.groups * a.n_kv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,28 +174,65 @@ __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* p
   return carry;
 }
 
-// CTAs that a call of T steps uses: at most `most`, each with `least` steps or more.
-__device__ __forceinline__ int kv4_ctas(long long T, int most, int least) {
-  const long long c = (T + least - 1) / least;
-  return c < 1 ? 1 : (c > most ? most : static_cast<int>(c));
-}
+// CTAs that a call of T units uses, at most `most`, and the unit that CTA c begins with.
+__device__ __forceinline__ int kv4_ctas(long long T, int most) { return T < most ? max(static_cast<int>(T), 1) : most; }
 __device__ __forceinline__ long long kv4_start(long long T, int C, int c) { return T * c / C; }
-// The CTA whose range holds step x.
+// The CTA whose range holds unit x.
 __device__ __forceinline__ int kv4_owner(long long T, int C, long long x) {
   int c = static_cast<int>(x * C / T);
   while (kv4_start(T, C, c + 1) <= x) ++c;
   while (kv4_start(T, C, c) > x) --c;
   return c;
 }
-// Sequence that holds step x.
-__device__ __forceinline__ int kv4_find(const long long* pre, int n_seq, long long x) {
-  int lo = 0, hi = n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] > x) hi = mid;
-    else lo = mid + 1;
+
+// A segment's part in a CTA: tiles [k0, k0 + n) of a sequence, kv head and
+// row group (n 0: no more parts).
+struct Kv4Part {
+  Kv4Seq q;
+  int s, head, row0, rows, k0, n;
+  long long end, next;  // units: the segment's end; where this part ends
+};
+// The first part with a tile in [at, x_end); `hint` is the part before it (or a zeroed one).
+template <int STEP, int R, int OV>
+__device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long long* pre, long long at, long long x_end,
+                                            const Kv4Part& hint) {
+  Kv4Part p = hint;
+  p.n = 0;
+  p.next = x_end;
+  while (at < x_end) {
+    int s = p.s;
+    if (!(p.q.rows > 0 && pre[s] <= at && at < pre[s + 1])) {
+      if (s + 1 < a.n_seq && pre[s + 1] <= at && at < pre[s + 2]) {
+        ++s;
+      } else {
+        int lo = 0, hi = a.n_seq - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[mid + 1] > at) hi = mid;
+          else lo = mid + 1;
+        }
+        s = lo;
+      }
+      p.s = s;
+      p.q = kv4_seq<STEP, R>(a, s, false);
+    }
+    const int units = p.q.steps + OV;
+    const long long rel = at - pre[s];
+    const int seg = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
+    const long long begin = pre[s] + static_cast<long long>(seg) * units;
+    p.end = begin + units;
+    p.next = p.end < x_end ? p.end : x_end;
+    p.k0 = max(static_cast<int>(at - begin) - OV, 0);
+    p.n = max(static_cast<int>(p.next - begin) - OV, 0) - p.k0;
+    if (p.n > 0) {
+      p.head = seg / p.q.groups;
+      p.row0 = (seg - p.head * p.q.groups) * R;
+      p.rows = min(R, p.q.rows * a.G - p.row0);
+      break;
+    }
+    at = p.next;
   }
-  return lo;
+  return p;
 }
 
 // What a split segment's first CTA leaves for the merge kernel.

@@ -33,6 +33,7 @@ namespace {
 constexpr int kTile = 64;       // cells of a tile
 constexpr int kGroups = 4;
 constexpr int kRows = 128;
+constexpr int kOverhead = 5;   // a segment's beginning and end, in tiles
 constexpr int kSoftWarps = 8, kUnpackWarps = 8;  // (unpacking: K and V each)
 constexpr int kQkWarp = 0, kCopyWarp = 1, kPvWarp = 2;  // (3 fills their warpgroup)
 constexpr int kSoftWarp0 = 4, kUnpackWarp0 = kSoftWarp0 + kSoftWarps;
@@ -201,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     mbar_init(&ofree, kSoftWarps);
     fence_barrier_init();
   }
-  const long long T = kv4_plan<kTile, R>(a, pre, scratch, blockIdx.x == 0);
-  const int C = kv4_ctas(T, gridDim.x, 1);
+  const long long T = kv4_plan<kTile, R, kOverhead>(a, pre, scratch, blockIdx.x == 0);
+  const int C = kv4_ctas(T, gridDim.x);
   const int c = blockIdx.x;
   pdl_launch_dependents();
   if (c >= C || T == 0) {
@@ -220,34 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   const long long x_begin = kv4_start(T, C, c), x_end = kv4_start(T, C, c + 1);
   bool ok = true;
 
-  // a segment's part in this CTA: tiles [k0, k0 + n) of a sequence, kv head and row group
-  struct Part {
-    Kv4Seq q;
-    int s, head, row0, k0, n, rows;
-  };
-  auto part_at = [&](long long at) {
-    Part p{};
-    if (at >= x_end) return p;
-    p.s = kv4_find(pre, a.n_seq, at);
-    p.q = kv4_seq<kTile, R>(a, p.s, false);
-    const long long rel = at - pre[p.s];
-    const int unit = static_cast<int>(rel / p.q.steps);
-    p.k0 = static_cast<int>(rel - static_cast<long long>(unit) * p.q.steps);
-    p.n = static_cast<int>(min(static_cast<long long>(p.q.steps - p.k0), x_end - at));
-    p.head = unit / p.q.groups;
-    p.row0 = unit % p.q.groups * R;
-    p.rows = min(R, p.q.rows * a.G - p.row0);
-    return p;
-  };
+  const Kv4Part none{};
+  auto part_at = [&](long long at, const Kv4Part& before) { return kv4_part<kTile, R, kOverhead>(a, pre, at, x_end, before); };
 
   if (warp < kSoftWarp0) fewer_registers<kOtherRegs>();
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ producer
     const int groups_of_page = 1 << (a.page_shift - 4);
     uint32_t g = 0;  // tiles over all parts
-    for (long long x = x_begin; x < x_end && ok;) {
-      const Part p = part_at(x);
-      x += p.n;
+    for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p)) {
       // the lanes hold the pages of the groups of 8 tiles, and those of the next 8
       auto look_up = [&](int from) {
         const int i = from + (lane >> 2);
@@ -300,9 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
     const bool one = elect_one();
     uint32_t g = 0, part = 0;
-    for (long long x = x_begin; x < x_end && ok; ++part) {
-      const int n = part_at(x).n;
-      x += n;
+    for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p), ++part) {
+      const int n = p.n;
       ok = __all_sync(0xffffffffu, kv4_wait(&qready, part & 1));
       for (int i = 0; i < n && ok; ++i, ++g) {
         const uint32_t b = g & 1, was = (g >> 1) & 1;
@@ -334,9 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
     const bool one = elect_one();
     uint32_t g = 0, part = 0;
-    for (long long x = x_begin; x < x_end && ok; ++part) {
-      const int n = part_at(x).n;
-      x += n;
+    for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p), ++part) {
+      const int n = p.n;
       // O of the part before has been read
       if (part > 0) ok = __all_sync(0xffffffffu, kv4_wait(&ofree, (part - 1) & 1));
       for (int i = 0; i < n && ok; ++i, ++g) {
@@ -367,9 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int m = q4 * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     uint32_t g = 0;
-    for (long long x = x_begin; x < x_end;) {
-      const Part p = part_at(x);
-      x += p.n;
+    Kv4Job job{};  // the segment that begins here and goes on in the next CTAs, if one does
+    for (Kv4Part p = part_at(x_begin, none); p.n > 0; p = part_at(p.next, p)) {
       const bool mine = m < p.rows, live = q4 * 32 < p.rows;  // the row; any row of the quarter
       const int row = p.row0 + m;
       const int2 sees = mine ? kv4_sees(a, p.q, row / a.G) : make_int2(0, 0);
@@ -559,16 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       tc_fence_before();
       named_bar_sync(1, kSoftThreads);  // red_sum has been read
       if (lane == 0) mbar_arrive(&ofree);
-      if (warp == kSoftWarp0 && lane == 0 && x >= x_end) {
-        // the last part: does its segment begin here and go on in the next CTAs?
-        Kv4Job r{p.q.r0, p.row0, p.head, 0, 0, {0, 0, 0}};
-        if (!whole && p.k0 == 0) {
-          r.n_rows = p.rows;
-          r.last = kv4_owner(T, C, x - p.n + p.q.steps - 1);
-        }
-        a.jobs[c] = r;
-      }
+      if (!whole && p.k0 == 0) job = Kv4Job{p.q.r0, p.row0, p.head, p.rows, kv4_owner(T, C, p.end - 1), {0, 0, 0}};
     }
+    if (warp == kSoftWarp0 && lane == 0) a.jobs[c] = job;
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
   } else if (warp >= kUnpackWarp0) {
     // ------------------------------------------------------------ unpacking
@@ -615,9 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     uint8_t* to = (v_side ? vbuf : kbuf) + b * G::BUF + first;
     uint8_t* to4 = (v_side ? vbuf : kbuf) + b * G::BUF + (first ^ 64);  // chunk + 4
     uint32_t g = 0;
-    for (long long x = x_begin; x < x_end && ok;) {
-      const Part p = part_at(x);
-      x += p.n;
+    for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p)) {
       const uint32_t g_end = g + p.n, g_first = g;
       for (g += (g ^ b) & 1; g < g_end; g += 2) {
         const int st = g % NP;
