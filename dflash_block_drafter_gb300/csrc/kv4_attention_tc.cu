@@ -13,10 +13,12 @@
 //                 d (code - 8) in the 128-byte-swizzled layouts the MMAs read,
 //                 double-buffered; four warps each for the even and the odd tiles.
 // Q and P are the MMAs' A operands in tensor memory (FP16 pairs), P over the S it
-// came from, so that shared memory, which bounds the kernel, carries only K and V:
-// per tile and D = 256 64 KB written and read (1000 cycles), as much as the
-// MMAs take, against 790 cycles for the tile's bytes from HBM; the columns of
-// tensor memory are S0 | S1 | O | Q = 64 + 64 + D + D / 2.
+// came from, so that shared memory carries little more than K and V: per tile and D =
+// 256 64 KB written and read (1000 cycles), as much as the MMAs take, against 790
+// cycles for the tile's bytes from HBM.  There are three S, because the chain from
+// one S over the softmax and P V to the next in its place takes the longest; the
+// columns are S0 | S1 | S2 | O | Q = 3 * 64 + D + D / 2, of which D = 256 has room for
+// half of Q: its channels from 128 on are an operand in shared memory.
 //
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
 // masking the word yields pairs: Q's columns are stored in the same order,
@@ -33,7 +35,7 @@ namespace {
 constexpr int kTile = 64;       // cells of a tile
 constexpr int kGroups = 4;
 constexpr int kRows = 128;
-constexpr int kOverhead = 5;   // a segment's beginning and end, in tiles
+constexpr int kOverhead = 8;   // a segment's beginning and end, in tiles
 constexpr int kSoftWarps = 8, kUnpackWarps = 8;  // (unpacking: K and V each)
 constexpr int kQkWarp = 0, kCopyWarp = 1, kPvWarp = 2;  // (3 fills their warpgroup)
 constexpr int kSoftWarp0 = 4, kUnpackWarp0 = kSoftWarp0 + kSoftWarps;
@@ -44,7 +46,8 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
               "the roles' registers come out of the launch's");
-constexpr int kPacked = 4;      // stages of the packed ring
+constexpr int kPacked = 3;      // stages of the packed ring
+constexpr int kScores = 3;      // S buffers
 constexpr int kAhead = 7;       // tiles that L2 is asked for in advance (fewer than 8)
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
@@ -54,12 +57,15 @@ struct Geo {
   static constexpr int STAGE = kGroups * Kv4<D>::GROUP_BYTES;
   static constexpr int BUF = kTile * D * 2;  // one unpacked K or V tile
   static constexpr int RED = 3 * kRows * 4;
-  static constexpr int SMEM = 1024 + 4 * BUF + kPacked * STAGE + RED;
-  static constexpr int S_COL = 0, O_COL = 2 * kTile, Q_COL = O_COL + D;
+  static constexpr int QT = D == 256 ? 128 : D;              // channels of Q in tensor memory
+  static constexpr int QBUF = kRows * (D - QT) * 2;          // the others, [64-channel boxes][128 rows][128 B]
+  static constexpr int SMEM = 1024 + 4 * BUF + QBUF + kPacked * STAGE + RED;
+  static constexpr int S_COL = 0, O_COL = kScores * kTile, Q_COL = O_COL + D;
+  static_assert(Q_COL + QT / 2 <= kTmemCols, "columns");
 };
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA.  The descriptor
-// comes in two words: only its low one, the address, changes between the
+// D[tmem] (+)= A * B[smem desc], kind::f16, one CTA; A in tensor memory (ta) or
+// by a descriptor too (sa).  A descriptor comes in two words: only its low one, the address, changes between the
 // MMAs of a tile, so that a warp that computes it as a whole keeps it in
 // uniform registers and issues an MMA in a few instructions (with one lane's
 // 64-bit descriptors the issue, not the tensor cores, took the time).
@@ -81,6 +87,18 @@ __device__ __forceinline__ void more_registers() {
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void umma_f16_sa(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // Two FP32 values in one register pair, and the instructions that take both.
@@ -175,12 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                       // [2][D / 64 boxes][64 cells][128 B]
   uint8_t* vbuf = kbuf + 2 * G::BUF;          // [2]
-  uint8_t* ring = vbuf + 2 * G::BUF;          // [NP] packed tiles
+  uint8_t* qbuf = vbuf + 2 * G::BUF;          // Q's channels from QT on
+  uint8_t* ring = qbuf + G::QBUF;             // [NP] packed tiles
   float* s_ref = reinterpret_cast<float*>(ring + NP * G::STAGE);    // [128 rows] references of the scores
   float* red_sum = s_ref + R;                                       // [2][128 rows]
   long long* pre = reinterpret_cast<long long*>(red_sum + 2 * R);   // [n_seq + 1]
   __shared__ long long scratch[kThreads / 32];
-  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[2], pready[2], qready, ofree, done[2];
+  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[kScores], sfree[kScores], pready[kScores], qready, ofree, done[2];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -194,9 +213,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       mbar_init(&kfree[i], 1);
       mbar_init(&vready[i], kUnpackWarps / 2);
       mbar_init(&vfree[i], 1);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], kSoftWarps / 2);
       mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < kScores; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 1);
+      mbar_init(&pready[i], kSoftWarps / 2);
     }
     mbar_init(&qready, kSoftWarps);
     mbar_init(&ofree, kSoftWarps);
@@ -280,24 +302,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     constexpr uint32_t idesc = umma_idesc_f16(128, kTile, false, false);
     const uint64_t kd = umma_desc_sw128(smem_u32(kbuf), 16, 1024);
     const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+    const uint64_t qd = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
+    const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
     const bool one = elect_one();
     uint32_t g = 0, part = 0;
     for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p), ++part) {
       const int n = p.n;
       ok = __all_sync(0xffffffffu, kv4_wait(&qready, part & 1));
       for (int i = 0; i < n && ok; ++i, ++g) {
-        const uint32_t b = g & 1, was = (g >> 1) & 1;
-        bool here = kv4_wait(&kready[b], was);
-        if (g >= 2) here = here && kv4_wait(&vfree[b], was ^ 1);  // P of tile g - 2 lies in the same columns
+        const uint32_t b = g & 1, sb = g % kScores, turn = g / kScores;
+        bool here = kv4_wait(&kready[b], (g >> 1) & 1);
+        if (turn > 0) here = here && kv4_wait(&sfree[sb], (turn - 1) & 1);  // P of the tile that had this S
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t lo = k_lo + b * (G::BUF >> 4), to = tmem + G::S_COL + b * kTile;
+        const uint32_t lo = k_lo + b * (G::BUF >> 4), to = tmem + G::S_COL + sb * kTile;
         if (one) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_f16_ta(to, tmem + G::Q_COL + kk * 8, lo + (((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4), k_hi, idesc, kk > 0);
-          umma_commit(&sfull[b]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t k_at = lo + (((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4);
+            if (kk * 16 < G::QT) {
+              umma_f16_ta(to, tmem + G::Q_COL + kk * 8, k_at, k_hi, idesc, kk > 0);
+            } else {
+              constexpr int K0 = G::QT / 16;
+              umma_f16_sa(to, q_lo + ((((kk - K0) >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4), q_hi, k_at, k_hi, idesc, 1);
+            }
+          }
+          umma_commit(&sfull[sb]);
           umma_commit(&kfree[b]);
         }
         __syncwarp();
@@ -320,18 +351,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       // O of the part before has been read
       if (part > 0) ok = __all_sync(0xffffffffu, kv4_wait(&ofree, (part - 1) & 1));
       for (int i = 0; i < n && ok; ++i, ++g) {
-        const uint32_t b = g & 1, was = (g >> 1) & 1;
-        const bool here = kv4_wait(&vready[b], was) && kv4_wait(&pready[b], was);
+        const uint32_t b = g & 1, sb = g % kScores;
+        const bool here = kv4_wait(&vready[b], (g >> 1) & 1) && kv4_wait(&pready[sb], (g / kScores) & 1);
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t lo = v_lo + b * (G::BUF >> 4), from = tmem + G::S_COL + b * kTile, more = i > 0;
+        const uint32_t lo = v_lo + b * (G::BUF >> 4), from = tmem + G::S_COL + sb * kTile, more = i > 0;
         if (one) {
           umma_f16_ta(tmem + G::O_COL, from, lo, v_hi, idesc, more);
 #pragma unroll
           for (int kk = 1; kk < kTile / 16; ++kk)
             umma_f16_ta(tmem + G::O_COL, from + kk * 8, lo + kk * (2048 >> 4), v_hi, idesc, 1);
           umma_commit(&vfree[b]);
+          umma_commit(&sfree[sb]);
         }
         __syncwarp();
       }
@@ -393,10 +425,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               w[4 * k + i] = pack_f16x2(value(lo) * f, value(hi) * f);
             }
           }
-          tmem_st16(lane_addr + G::Q_COL + (cs * (D / 2) + e) / 2, w);
+          if (cs * (D / 2) < G::QT) {
+            tmem_st16(lane_addr + G::Q_COL + (cs * (D / 2) + e) / 2, w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(qbuf + (e >> 6) * (kRows * 128) + m * 128 + (((((e & 63) >> 3) + k) ^ (m & 7)) << 4)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
         }
         tmem_wait_st();
       }
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&qready);
@@ -404,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       float m_ref = -INFINITY, l = 0.f;  // l in units of 2^m_ref
       const uint32_t g_end = g + p.n, g_first = g;
       for (g += (g ^ cs) & 1; g < g_end; g += 2) {
-        const int b = cs, i = g - g_first;
-        const uint32_t s_addr = lane_addr + G::S_COL + b * kTile;
-        if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&sfull[b], (g >> 1) & 1));
+        const int b = cs, sb = g % kScores, i = g - g_first;
+        const uint32_t s_addr = lane_addr + G::S_COL + sb * kTile;
+        if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&sfull[sb], (g / kScores) & 1));
         tc_fence_after();
         const int pos0 = p.q.base + (p.k0 + i) * kTile;
         uint32_t r[2][32];
@@ -486,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[b]);
+        if (lane == 0) mbar_arrive(&pready[sb]);
       }
       g = g_end;
       // ---- O of the part
