@@ -44,7 +44,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kOverhead = 2;  // a segment's beginning and end, in tiles
-constexpr int kPerSm = 3;     // CTAs per SM
 constexpr float kSlack = 8.f; // log2 units by which a score may pass the reference
 
 constexpr int kPlanBytes(int n_seq) { return (n_seq + 1) * 8; }
@@ -52,11 +51,12 @@ constexpr int kPlanBytes(int n_seq) { return (n_seq + 1) * 8; }
 template <int D, int NT>
 struct Geo {
   static constexpr int R = 8 * NT;                 // rows of a row group
-  static constexpr int MT = D == 256 ? 1 : 2;      // 16-cell groups of a warp in a tile
+  static constexpr int MT = 2;                     // 16-cell groups of a warp in a tile
   static constexpr int GROUPS = kWarps * MT;
   static constexpr int TILE = 16 * GROUPS;         // cells of a tile
   static constexpr int STAGE = GROUPS * Kv4<D>::GROUP_BYTES;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D == 256 ? 2 : 3;
+  static constexpr int PER_SM = D == 256 ? 2 : 3;  // CTAs per SM
   static constexpr int RING = STAGES * STAGE;
   static constexpr int QF = NT * (D / 32) * 512;   // Q fragments
   static constexpr int QS = NT * 256;              // fragments of the blocks' sums
@@ -107,7 +107,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kPerSm) kv4_attn_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kernel(const Kv4AttnArgs a) {
   using F = Kv4<D>;
   using G = Geo<D, NT>;
   constexpr int R = G::R, B = F::BLOCKS, U = D / 64, ST = G::STAGES, MT = G::MT, TILE = G::TILE, JT = G::JT;
@@ -616,7 +616,11 @@ struct Shape {
   int most, jobs;
   int rows_of_group() const { return tc ? 128 : 8 * nt; }
 };
-constexpr int kTcRows = 16;  // more rows per kv head than this go to the tcgen05 kernel
+// More rows per kv head than this go to the tcgen05 kernel.  Measured on 16
+// sequences of 2048 .. 32768 cells, 2 kv heads of 256 (64 of 512 .. 8192, 8 of 128):
+// 12 rows 56 us here, 100 there; 24 rows 81 and 103 (165 and 256); 32 rows 88 and
+// 105 (226 and 255); beyond, this kernel unpacks every cell once per 32 rows.
+constexpr int kTcRows = 32;
 cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Shape* out) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -635,14 +639,15 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   // as few row groups as 32 rows allow, each no wider than it needs
   const int groups = (rows + 31) / 32;
   out->nt = ((rows + groups - 1) / groups + 7) / 8;
-  const int tile = c->head_dim == 256 ? 64 : 128;
+  const int tile = 128;
   const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads * groups;
   // (a window may begin anywhere in a tile)
   const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
   const long long ctas = segments * (tiles + kOverhead);
   // one wave of CTAs: every one of them has the same share
   const int smem = smem_of(c->head_dim, out->nt) + kPlanBytes(n_seq) + kStaticSmem;
-  const int per_sm = kSmemOfSm / smem < kPerSm ? kSmemOfSm / smem : kPerSm;
+  const int most_per_sm = c->head_dim == 256 ? 2 : 3;
+  const int per_sm = kSmemOfSm / smem < most_per_sm ? kSmemOfSm / smem : most_per_sm;
   out->most = static_cast<int>(ctas < per_sm * sms ? ctas : per_sm * sms);
   out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
   return cudaSuccess;

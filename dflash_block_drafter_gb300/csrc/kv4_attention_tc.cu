@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   float* red_sum = s_ref + R;                                       // [2][128 rows]
   long long* pre = reinterpret_cast<long long*>(red_sum + 2 * R);   // [n_seq + 1]
   __shared__ long long scratch[kThreads / 32];
-  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[kScores], sfree[kScores], pready[kScores], qready, ofree, done[2];
+  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[kScores], sfree[kScores], pready[kScores], qready, odone, ofree, done[2];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       mbar_init(&pready[i], kSoftWarps / 2);
     }
     mbar_init(&qready, kSoftWarps);
+    mbar_init(&odone, 1);
     mbar_init(&ofree, kSoftWarps);
     fence_barrier_init();
   }
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
             umma_f16_ta(tmem + G::O_COL, from + kk * 8, lo + kk * (2048 >> 4), v_hi, idesc, 1);
           umma_commit(&vfree[b]);
           umma_commit(&sfree[sb]);
+          if (i == n - 1) umma_commit(&odone);  // (a barrier of its own: vfree may be two phases behind then)
         }
         __syncwarp();
       }
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int q4 = warp & 3, cs = (warp - kSoftWarp0) >> 2;  // TMEM lane quarter; tiles by parity, and half of Q's and O's columns
     const int m = q4 * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    uint32_t g = 0;
+    uint32_t g = 0, part = 0;
     Kv4Job job{};  // the segment that begins here and goes on in the next CTAs, if one does
     for (Kv4Part p = part_at(x_begin, none); p.n > 0; p = part_at(p.next, p)) {
       const bool mine = m < p.rows, live = q4 * 32 < p.rows;  // the row; any row of the quarter
@@ -479,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           if (i == 0 || __any_sync(0xffffffffu, over)) {
             s_ref[m] = ref;
             if (i > 0) {
-              // the products so far, once they are all in O
+              // the products so far, once they are all in O (S of this tile says
+              // that P V of tile g - 3 is done: the parity means tile g - 1)
               if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[b ^ 1], ((g - 1) >> 1) & 1));
               tc_fence_after();
               const float alpha = over ? ex2_approx(was - ref) : 1.f;
@@ -530,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       }
       g = g_end;
       // ---- O of the part
-      if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[(g - 1) & 1], ((g - 1) >> 1) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&odone, part & 1));
+      ++part;
       tc_fence_after();
       named_bar_sync(1, kSoftThreads);  // the last reference
       if (live) {
@@ -636,8 +640,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         // cells that no row sees may hold anything: they become zeros
         const bool edge = pos0 < p.q.lo || pos0 + kTile > p.q.hi;
         auto hidden = [&](int off) { return pos0 + cell + off < p.q.lo || pos0 + cell + off >= p.q.hi; };
-        bool here = kv4_wait(&pfull[st], (g / NP) & 1);
-        if (g >= 2) here = here && kv4_wait(free_, ((g >> 1) - 1) & 1);
+        // First the buffer: that tile g - 2 has been used says that the stage's
+        // last tile, g - NP, has been unpacked (by the other parity's warps), so that
+        // the parity below cannot be taken for that of an earlier phase.
+        static_assert(NP >= 2, "see above");
+        bool here = true;
+        if (g >= 2) here = kv4_wait(free_, ((g >> 1) - 1) & 1);
+        here = here && kv4_wait(&pfull[st], (g / NP) & 1);
         if (!__all_sync(0xffffffffu, here)) {
           ok = false;
           break;

@@ -274,12 +274,27 @@ def test_attention_split_over_ctas(R, d, G, rows, kind):
     check_attn(R, attn_case(G, d, 1, G, [5000, 130, 9, 2500], [rows, 1, rows, 1], 64, kind), True)
 
 
-@pytest.mark.parametrize("d,heads,G,rows", [(64, 2, 3, 8), (64, 1, 16, 8), (128, 2, 8, 4), (256, 2, 12, 8), (256, 2, 12, 1), (128, 4, 4, 1)])
+@pytest.mark.parametrize("d,heads,G,rows", [(64, 2, 5, 8), (64, 1, 16, 8), (128, 2, 9, 4), (64, 2, 3, 8), (256, 2, 12, 8), (256, 2, 12, 1), (128, 4, 4, 1)])
 def test_attention_many_tiles_per_cta(R, d, heads, G, rows):
     """More tiles than a CTA's buffers hold, with and without quarters of rows that are empty, and parts of several
     sequences in one CTA."""
     lens = [20000, 40, 700, 12000, 9000] if d == 256 else [30000, 100, 2000, 17000]
     check_attn(R, attn_case(d + rows, d, heads, G, lens, [rows] * len(lens), 128, "bf16"), True)
+
+
+@pytest.mark.parametrize("d,G", [(64, 5), (128, 6), (256, 5), (128, 3)])
+def test_attention_same_result_again(R, d, G):
+    """Many parts of many sequences per CTA, over and over: the same bits each time, and the right ones."""
+    rng = np.random.default_rng(d)
+    lens = rng.integers(64, 2500 if d < 256 else 1200, 40).tolist()
+    case = attn_case(d, d, 2, G, lens, rng.integers(2, 9, 40).tolist(), 64, "bf16")
+    first = check_attn(R, case, True, max_rows=8)
+    cache, q, table, ln, off = case
+    c, t, ln, off = torch.as_tensor(cache, device="cuda"), ints(table), ints(ln), ints(off)
+    n = first.shape[0]
+    outs = [R.kv4_attention(c, q, t, ln, off, 8) for _ in range(100)]
+    for o in outs:
+        assert np.array_equal(o[:n].double().cpu().numpy(), first)
 
 
 def test_attention_many_short(R):
