@@ -631,7 +631,8 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   if (out->tc) {
     out->nt = 0;
     const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads;
-    const long long tiles = (static_cast<long long>(table_stride) * c->page_size + 63) / 64 + 1;
+    const int tile = c->head_dim == 256 ? 64 : 128;
+    const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
     out->most = static_cast<int>(segments * tiles < sms ? segments * tiles : sms);
     out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
     return cudaSuccess;

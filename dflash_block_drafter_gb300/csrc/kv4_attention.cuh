@@ -124,8 +124,8 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool repo
   q.hi = q.kv;
   q.lo = 0;
   if (a.window > 0) {  // the first row that any window reaches
-    const int first = a.causal ? q.kv - q.rows : q.kv - 1;
-    q.lo = min(max(first - a.window + 1, 0), q.hi);
+    const int upto = a.causal ? q.kv - q.rows + 1 : q.kv;  // behind the first row's own position
+    q.lo = min(upto > a.window ? upto - a.window : 0, q.hi);
   }
   q.base = q.lo - q.lo % STEP;
   // rows that see no cell take one masked step, which writes their zeros
@@ -136,9 +136,8 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool repo
 
 // Visible cells [lo, hi) of token i of the sequence.
 __device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, int i) {
-  const int last = a.causal ? q.kv - q.rows + i : q.kv - 1;  // the row's own position
-  const int lo = a.window > 0 ? max(last - a.window + 1, 0) : 0;
-  return make_int2(lo, max(last + 1, 0));
+  const int upto = a.causal ? q.kv - q.rows + i + 1 : q.kv;  // behind the row's own position
+  return make_int2(a.window > 0 && upto > a.window ? upto - a.window : 0, max(upto, 0));
 }
 
 // Prefix sums of the sequences' units (over kv heads and row groups) in

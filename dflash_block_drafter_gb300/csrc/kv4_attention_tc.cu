@@ -1,8 +1,9 @@
 // Attention over the 4-bit paged K/V cache for many query rows per kv head
 // (blocks of several tokens over wide groups), on the tcgen05 tensor cores.
 //
-// One CTA per SM takes tiles of 64 cells for up to 128 query rows:
-//   warp 0        issues S = Q K^T (M 128, N 64), warp 2 O += P V (M 128, N = D):
+// One CTA per SM takes tiles of T cells (64 at D = 256, else 128: a tile costs
+// about as much in hand-overs as in work) for up to 128 query rows:
+//   warp 0        issues S = Q K^T (M 128, N = T), warp 2 O += P V (M 128, N = D):
 //                 two warps, because a wait and the issue of a tile's MMAs
 //                 take one warp as long as the MMAs themselves;
 //   warp 1        copies the tiles' packed groups into a ring (bulk copies);
@@ -15,10 +16,10 @@
 // Q and P are the MMAs' A operands in tensor memory (FP16 pairs), P over the S it
 // came from, so that shared memory carries little more than K and V: per tile and D =
 // 256 64 KB written and read (1000 cycles), as much as the MMAs take, against 790
-// cycles for the tile's bytes from HBM.  There are three S, because the chain from
-// one S over the softmax and P V to the next in its place takes the longest; the
-// columns are S0 | S1 | S2 | O | Q = 3 * 64 + D + D / 2, of which D = 256 has room for
-// half of Q: its channels from 128 on are an operand in shared memory.
+// cycles for the tile's bytes from HBM.  There are three S where they fit, because the
+// chain from one S over the softmax and P V to the next in its place takes the longest.
+// Columns: S | O | Q = 3 * 64 + 256 + 64 at D = 256 (half of Q: its channels from 128
+// on are an operand in shared memory), 2 * 128 + 128 + 64 at D = 128, 3 * 128 + 64 + 32.
 //
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
 // masking the word yields pairs: Q's columns are stored in the same order,
@@ -32,8 +33,6 @@
 namespace dflash {
 namespace {
 
-constexpr int kTile = 64;       // cells of a tile
-constexpr int kGroups = 4;
 constexpr int kRows = 128;
 constexpr int kOverhead = 8;   // a segment's beginning and end, in tiles
 constexpr int kSoftWarps = 8, kUnpackWarps = 8;  // (unpacking: K and V each)
@@ -47,20 +46,21 @@ constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
               "the roles' registers come out of the launch's");
 constexpr int kPacked = 3;      // stages of the packed ring
-constexpr int kScores = 3;      // S buffers
-constexpr int kAhead = 7;       // tiles that L2 is asked for in advance (fewer than 8)
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
 
 template <int D>
 struct Geo {
-  static constexpr int STAGE = kGroups * Kv4<D>::GROUP_BYTES;
-  static constexpr int BUF = kTile * D * 2;  // one unpacked K or V tile
+  static constexpr int TILE = D == 256 ? 64 : 128;           // cells of a tile
+  static constexpr int GROUPS = TILE / 16;
+  static constexpr int SCORES = D == 128 ? 2 : 3;            // S buffers
+  static constexpr int STAGE = GROUPS * Kv4<D>::GROUP_BYTES;
+  static constexpr int BUF = TILE * D * 2;                   // one unpacked K or V tile
   static constexpr int RED = 3 * kRows * 4;
   static constexpr int QT = D == 256 ? 128 : D;              // channels of Q in tensor memory
   static constexpr int QBUF = kRows * (D - QT) * 2;          // the others, [64-channel boxes][128 rows][128 B]
   static constexpr int SMEM = 1024 + 4 * BUF + QBUF + kPacked * STAGE + RED;
-  static constexpr int S_COL = 0, O_COL = kScores * kTile, Q_COL = O_COL + D;
+  static constexpr int S_COL = 0, O_COL = SCORES * TILE, Q_COL = O_COL + D;
   static_assert(Q_COL + QT / 2 <= kTmemCols, "columns");
 };
 
@@ -188,10 +188,10 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a) {
   using F = Kv4<D>;
   using G = Geo<D>;
-  constexpr int R = kRows, NP = kPacked, U = D / 64, B = D / 32;
+  constexpr int R = kRows, NP = kPacked, U = D / 64, B = D / 32, kTile = G::TILE, kScores = G::SCORES, kGroups = G::GROUPS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* kbuf = smem;                       // [2][D / 64 boxes][64 cells][128 B]
+  uint8_t* kbuf = smem;                       // [2][D / 64 boxes][T cells][128 B]
   uint8_t* vbuf = kbuf + 2 * G::BUF;          // [2]
   uint8_t* qbuf = vbuf + 2 * G::BUF;          // Q's channels from QT on
   uint8_t* ring = qbuf + G::QBUF;             // [NP] packed tiles
@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int groups_of_page = 1 << (a.page_shift - 4);
     uint32_t g = 0;  // tiles over all parts
     for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p)) {
-      // the lanes hold the pages of the groups of 8 tiles, and those of the next 8
+      // the lanes hold the pages of the groups of WIN tiles, and those of the next WIN
+      constexpr int WIN = 32 / kGroups, AHEAD = WIN - 1;
+      const int lane_tile = lane / kGroups, lane_group = lane % kGroups;
       auto look_up = [&](int from) {
-        const int i = from + (lane >> 2);
-        const int pos = p.q.base + (p.k0 + i) * kTile + (lane & 3) * 16;
+        const int i = from + lane_tile;
+        const int pos = p.q.base + (p.k0 + i) * kTile + lane_group * 16;
         if (i >= p.n || pos >= p.q.hi) return -1;
         int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
         if (page < 0 || page >= a.n_pages) {
@@ -265,26 +267,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         return page;
       };
-      auto address = [&](int page, int i) {  // lane: group lane % 4 of tile i
-        const int grp = ((p.q.base + (p.k0 + i) * kTile + (lane & 3) * 16) >> 4) & (groups_of_page - 1);
+      auto address = [&](int page, int i) {  // of this lane's group of tile i
+        const int grp = ((p.q.base + (p.k0 + i) * kTile + lane_group * 16) >> 4) & (groups_of_page - 1);
         return a.cache + ((static_cast<size_t>(page) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES;
       };
       int page = -1, later = look_up(0);
       for (int i = 0; i < p.n && ok; ++i, ++g) {
-        if (i % 8 == 0) {
+        if (i % WIN == 0) {
           page = later;
-          later = look_up(i + 8);
+          later = look_up(i + WIN);
         }
-        // the ring is too short for HBM's latency: tile i + kAhead is asked of
-        // L2 now (at the part's start, all tiles up to it; those in `page` only)
-        for (int j = i == 0 ? NP : i + kAhead; j <= i + kAhead; ++j) {
-          const int there = __shfl_sync(0xffffffffu, j % 8 > i % 8 ? page : later, (j % 8) * 4 + (lane & 3));
+        // the ring is too short for HBM's latency: tile i + AHEAD is asked of L2
+        // now (at the part's start, all tiles behind the ring up to it)
+        for (int j = i == 0 ? NP : i + AHEAD; j <= i + AHEAD; ++j) {
+          const int there = __shfl_sync(0xffffffffu, j / WIN == i / WIN ? page : later, (j % WIN) * kGroups + lane_group);
           if (lane < kGroups && there >= 0) bulk_prefetch_l2_plain(address(there, j), F::GROUP_BYTES);
         }
         const int st = g % NP;
         if (g >= NP) ok = __all_sync(0xffffffffu, kv4_wait(&pfree[st], (g / NP - 1) & 1));
         if (!ok) break;
-        const int mine = __shfl_sync(0xffffffffu, page, (i % 8) * 4 + (lane & 3));
+        const int mine = __shfl_sync(0xffffffffu, page, (i % WIN) * kGroups + lane_group);
         const unsigned have = __ballot_sync(0xffffffffu, lane < kGroups && mine >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have) * F::GROUP_BYTES);
         __syncwarp();
@@ -451,25 +453,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&sfull[sb], (g / kScores) & 1));
         tc_fence_after();
         const int pos0 = p.q.base + (p.k0 + i) * kTile;
+        // 64 cells at a time (S of a tile of 128 is read twice: for the maximum, and
+        // again for P, which by then may lie over the half before)
+        constexpr int HALVES = kTile / 64;
         uint32_t r[2][32];
-        float mx = -INFINITY;
-        if (live) {
-          tmem_ld32(s_addr, r[0]);
-          tmem_ld32(s_addr + 32, r[1]);
+        auto read_s = [&](int half) {
+          tmem_ld32(s_addr + half * 64, r[0]);
+          tmem_ld32(s_addr + half * 64 + 32, r[1]);
           tmem_wait_ld();
           tmem_reg_fence(r[0]);
           tmem_reg_fence(r[1]);
-        }
-        if (live) {
-          if (pos0 < all_lo || pos0 + kTile > all_hi) {
+          const int pos = pos0 + half * 64;
+          if (pos < all_lo || pos + 64 > all_hi) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (pos0 + 32 * h + e < sees.x || pos0 + 32 * h + e >= sees.y) r[h][e] = 0xff800000u;  // -infinity
+                if (pos + 32 * h + e < sees.x || pos + 32 * h + e >= sees.y) r[h][e] = 0xff800000u;  // -infinity
           }
+        };
+        float mx = -INFINITY;
+        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = max3(mx, __uint_as_float(r[0][e]), __uint_as_float(r[1][e]));
+          for (int half = 0; half < HALVES; ++half) {
+            read_s(half);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = max3(mx, __uint_as_float(r[0][e]), __uint_as_float(r[1][e]));
+          }
           mx *= factor;  // positive: the order stays
         }
         // the reference that the tile before left (barrier 2 + 2 q4 + parity)
@@ -481,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           if (i == 0 || __any_sync(0xffffffffu, over)) {
             s_ref[m] = ref;
             if (i > 0) {
-              // the products so far, once they are all in O (S of this tile says
-              // that P V of tile g - 3 is done: the parity means tile g - 1)
+              // the products so far, once they are all in O (that this tile has its S
+              // says that P V of tile g - 3 is done: the parity means tile g - 1)
               if (ok) ok = __all_sync(0xffffffffu, kv4_wait(&vfree[b ^ 1], ((g - 1) >> 1) & 1));
               tc_fence_after();
               const float alpha = over ? ex2_approx(was - ref) : 1.f;
@@ -512,19 +522,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           const uint64_t factor2 = pack2(factor, factor), from2 = pack2(-from, -from);
           uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int half = 0; half < HALVES; ++half) {
+            if (HALVES > 1) read_s(half);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), factor2, from2), x0, x1);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              sum2 = add2(sum2, pack2(p0, p1));
-              r[0][16 * h + (e >> 1)] = pack_f16x2(p0, p1);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x0, x1;
+                unpack2(fma2(pack2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), factor2, from2), x0, x1);
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                sum2 = add2(sum2, pack2(p0, p1));
+                r[0][16 * h + (e >> 1)] = pack_f16x2(p0, p1);
+              }
+            tmem_st32(s_addr + half * 32, r[0]);
+          }
           float s0, s1;
           unpack2(sum2, s0, s1);
           l += s0 + s1;
-          tmem_st32(s_addr, r[0]);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -668,16 +682,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               *reinterpret_cast<uint4*>(((j & 1) ? to4 : to) + (j >> 1) * (kTile * 128) + it * KSTEP * 128) =
                   unpack(w[it][j], d[it][j], kc);
         } else {
-          uint32_t w[4][U], d[4][U];
+          constexpr int N = kGroups;
+          uint32_t w[N][U], d[N][U];
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
+          for (int it = 0; it < N; ++it) {
             load_words<U>(packed + codes + it * F::GROUP_BYTES, w[it]);
             load_scales<U>(packed + scales + it * F::GROUP_BYTES, d[it]);
             if (edge && hidden(it * 16))
               for (int u = 0; u < U; ++u) d[it][u] = 0;
           }
 #pragma unroll
-          for (int it = 0; it < 4; ++it)
+          for (int it = 0; it < N; ++it)
 #pragma unroll
             for (int u = 0; u < U; ++u)
               *reinterpret_cast<uint4*>(to + u * (kTile * 128) + it * 16 * 128) = unpack(w[it][u], d[it][u], kc);

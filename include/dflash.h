@@ -498,7 +498,8 @@ int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t
 /* Attention of n_seq sequences' rows over their cells.
  *   q, out: [n_tokens] rows of n_q_heads * head_dim values (BF16 or FP16:
  *           `type`), q_stride / out_stride elements apart (multiples of 8),
- *           16-byte aligned; q head h reads kv head h / (n_q / n_kv).
+ *           16-byte aligned, not overlapping; q head h reads kv head
+ *           h / (n_q / n_kv).
  *   row_offsets: [n_seq + 1] int32: sequence s's rows are
  *           [row_offsets[s], row_offsets[s + 1]), at most max_rows (1 .. 8) of
  *           them; (n_q / n_kv) * max_rows <= 128.

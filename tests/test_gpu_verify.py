@@ -261,7 +261,7 @@ def test_attention(R, d, kind, heads, G, lens, rows, page, causal):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 10 ** 6])
+@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 2 ** 31 - 1])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_window(R, d, window, causal):
     check_attn(R, attn_case(d + window, d, 2, 4, [200, 31, 4, 64], [3, 1, 4, 8], 16, "bf16"), causal, window)
@@ -364,9 +364,10 @@ def test_attention_reports(R):
     assert st == D.DFLASH_DEV_NONFINITE and torch.equal(out[1:3], good[1][1:3])
 
 
-def test_attention_streams_and_graph(R):
-    """Two calls at once on two streams, and a captured call replayed with other lengths."""
-    a = attn_case(8, 128, 2, 4, [900, 30], [2, 1], 32, "bf16")
+@pytest.mark.parametrize("G", [4, 17])
+def test_attention_streams_and_graph(R, G):
+    """Two calls at once on two streams, and a captured call replayed with other lengths; both kernels."""
+    a = attn_case(8, 128, 2, G, [900, 30], [2, 1], 32, "bf16")
     cache, q, table, lens, offsets = a
     c, t = torch.as_tensor(cache, device="cuda"), ints(table)
     ln, off = ints(lens), ints(offsets)
@@ -390,6 +391,37 @@ def test_attention_streams_and_graph(R):
         ln.copy_(ints(lengths))
         g.replay()
         assert torch.equal(out[:3], w)
+
+
+def test_cells_beyond_4_gb(R):
+    """Pages whose bytes lie beyond 32 bits: written, read back and attended to."""
+    heads, d, page, n_pages = 8, 256, 256, 9000  # 5.3 GB
+    cache = torch.empty((n_pages, heads, page // 16, 18 * d), dtype=torch.uint8, device="cuda")
+    cache[-4:] = 0xFF
+    cache[:4] = 0xFF
+    rng = np.random.default_rng(1)
+    n, rows = 300, 2
+    pages = np.array([n_pages - 1, n_pages - 3], np.int32)
+    slots = ints([int(pages[p // page]) * page + p % page for p in range(n)])
+    k, v = (torch.as_tensor(rng.standard_normal((n, heads, d)), device="cuda").bfloat16() for _ in range(2))
+    st = status()
+    R.kv4_write(cache, k, v, slots, status=st)
+    kk, vv = (x.double().cpu().numpy() for x in R.kv4_read(cache, slots, status=st))
+    for x, y in ((k, kk), (v, vv)):
+        assert np.array_equal(V.dequantise(*V.quantise(x.double().cpu().numpy())), y)
+    for G in (1, 17):
+        q = torch.as_tensor(rng.standard_normal((rows, heads * G, d)), device="cuda").bfloat16()
+        o = R.kv4_attention(cache, q, ints([pages]), ints([n]), ints([0, rows]), rows, status=st).double().cpu().numpy()
+        qq = q.double().cpu().numpy()
+        for i in range(rows):
+            for h in range(heads * G):
+                m = n - rows + i + 1
+                x = kk[:m, h // G] @ qq[i, h] / 16.0
+                p = np.exp(x - x.max())
+                want, spread = p @ vv[:m, h // G] / p.sum(), p @ np.abs(vv[:m, h // G]) / p.sum()
+                tol = spread * (2.0 ** -10 + 2.0 ** -16 * (1 + np.abs(x).max())) + m * 2.0 ** -25 * 8 + 2.0 ** -8 * np.abs(want)
+                assert np.all(np.abs(o[i, h] - want) <= tol)
+    assert int(st) == 0
 
 
 # ------------------------------------------------------------------ logprobs
