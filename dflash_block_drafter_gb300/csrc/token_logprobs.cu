@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   if (split == 0 && warp == 0) finish_row<TYPE>(a, row, st, list, lane);
 }
 
-// CTAs per row: up to the four per SM that are resident, each warp with a batch
-// at least (128 rows of 100003 FP32 values: 34 us with two CTAs a row, see DESIGN).
+// CTAs per row: until every SM has one, each warp with a batch at least (128
+// rows of 100003 FP32 values: 34 us with two CTAs a row, 36 with four).
 cudaError_t splits_of(int n_rows, int vocab, int type, int* out) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -426,7 +426,7 @@ cudaError_t splits_of(int n_rows, int vocab, int type, int* out) {
   const int batch = 32 * kLoads * (type == DFLASH_T_FP32 ? 4 : 8);
   const int most = (vocab + batch * kWarps - 1) / (batch * kWarps);
   int s = 1;  // powers of two
-  while (2 * s <= kMaxSplits && 2 * s <= most && static_cast<long long>(n_rows) * 2 * s <= 4 * sms) s *= 2;
+  while (2 * s <= kMaxSplits && 2 * s <= most && static_cast<long long>(n_rows) * s < sms) s *= 2;
   *out = s;
   return cudaSuccess;
 }
