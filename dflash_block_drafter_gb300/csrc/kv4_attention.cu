@@ -15,25 +15,32 @@
 // is the subnormal c 2^-24, which the tensor cores take exactly (c 2^-20 for
 // the mask 0x00f000f0), so unpacking K is 4 ANDs and a shift per word.  Q
 // carries the other factor (FP16 rows scaled by a power of two, so nothing of
-// BF16 is lost), the -8 of the codes is the accumulator's start value
-// -8 2^-24 sum(q) of the 32-channel block, and the block's scale multiplies the
-// finished FP32 sum: K enters the scores without any rounding.
+// BF16 is lost), and a block's scale multiplies the finished FP32 sum of its 32
+// channels.  The -8 of the codes is one more product, of a cell's scales with -8
+// times the blocks' sums of q, each held as two FP16 terms (22 bits).  K itself
+// enters the scores without any rounding.
 // O^T = V^T P^T.  Two cells' words are interleaved (prmt) into pairs along the
 // cells, turned into code - 8 (1024 + c, minus 1032) and multiplied by the
-// cells' scales in FP16: one rounding of 2^-12 at most relative to the value.
+// cells' scales in FP16: one rounding of 2^-11 at most relative to the value.
 // P goes through movmatrix from the accumulator layout to the B operand's and is
-// rounded to FP16 (2^-12 relative at most, 2^-25 absolute; the sums are FP32 of
+// rounded to FP16 (2^-11 relative at most, 2^-25 absolute; the sums are FP32 of
 // the unrounded p).
 //
-// Work: the 4 warps of a CTA take a tile of 64 (D 256) or 128 cells together.
-// For S^T each warp has its own 16 or 32 cells and all channels; P goes through
-// shared memory; for O^T each warp has its own quarter of the channels and all
-// cells.  So O is 16 registers per 8 rows, three CTAs fit an SM, and a segment
-// ends without joining warps.  One barrier per tile orders P, the ring's
-// stages and the vote on the maximum: scores are taken relative to a reference
+// Work: the 4 warps of a CTA take a tile of 128 cells together.  For S^T
+// each warp has its own 32 cells and all channels; P goes through shared memory; for
+// O^T each warp has its own quarter of the channels and all cells.  So O is 16
+// registers per 8 rows at most, two or three CTAs fit an SM, and a segment ends
+// without joining warps.  One barrier per tile orders P, the ring's stages and the vote on the maximum: scores are taken relative to a reference
 // that stays until some score passes it by 2^8 (P stays far inside FP16's
 // range), so that the first tile and few others pay for a rescaling.  Bulk copies of
-// whole groups (K, V and scales together) run two tiles ahead.
+// whole groups (K, V and scales together) run one or two tiles ahead, into the
+// CTA's next segment too.
+//
+// Measured: 16 single tokens of 24 / 2 heads of 256 over 2048 .. 32768 cells 56 us for
+// 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 81 us for 224 MB.
+// The issue of instructions bounds it (about half of the slots are used; 57 % of
+// the instructions unpack), not the copies: one per tile instead of four, or deeper
+// rings, change nothing.
 #include <cstddef>
 
 #include "kv4_attention.cuh"

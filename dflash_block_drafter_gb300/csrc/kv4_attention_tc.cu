@@ -28,6 +28,11 @@
 // scaled by a power of two); scores, sums and O in FP32.  Scores are taken
 // relative to a reference that moves only when a row passes it by 2^8; the two
 // softmax warps of a quarter of the rows hand it to each other tile by tile.
+//
+// Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 93 us (557
+// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 95 us.  No unit is full
+// (issue 41 %, ALU 45 %, tensor pipe 27 %): a tile takes about 2500 cycles for its way
+// through eight barriers, and about 1800 with all the arithmetic taken out.
 #include "kv4_attention.cuh"
 
 namespace dflash {

@@ -11,10 +11,12 @@
 // it as the definition says.  Where d is so small (FP16's subnormals) that |x / d|
 // passes 8.4, each value is divided.
 //
-// Both kernels are bound by memory: a thread holds the 8 channels of one code
-// word of K and of V (two 16-byte loads, two 4-byte stores; reading: two codes in,
-// 64 bytes out), the quad of a block finds m by shuffles, and a warp covers
-// 256 consecutive channels of a row.
+// A thread holds the 8 channels of one code word of K and of V (two 16-byte
+// loads, two 4-byte stores; reading: two codes in, 64 bytes out), the quad of a
+// block finds m by shuffles, and a warp covers 256 consecutive channels of a row.
+// Measured on 30001 rows of 8 heads of 128 in random slots: written in 41 us (bound
+// by the extremes, roundings and packing; the bytes alone take 23; a division per
+// value took 88), read in 44 us (the bytes: 41).
 #include <cstddef>
 
 #include "internal.h"
