@@ -186,9 +186,10 @@ def commit_positions(anchor_pos: torch.Tensor, accept_len: torch.Tensor, positio
 
 # -------------------------------------------------------------- verify step
 # The operators of include/dflash.h's verify step on torch tensors.  Each runs
-# on the device of its tensors, on that device's current stream unless one is
-# given; outputs and workspaces come from torch's allocator on the current
-# stream.  `status` is an optional int32 tensor for the DFLASH_DEV_* bits.
+# on the device of its tensors, on that device's current stream; with `stream`
+# as if called inside torch.cuda.stream(stream), so that outputs and workspaces
+# come from that stream's memory.  `status` is an optional int32 tensor for the
+# DFLASH_DEV_* bits.
 # (Small calls take as long as their Python: the checks are plain ones.)
 _VALUE_TYPES = {torch.float32: DFLASH_T_FP32, torch.bfloat16: DFLASH_T_BF16, torch.float16: DFLASH_T_FP16}
 _INT32 = torch.int32
@@ -198,13 +199,17 @@ def _refuse(what: str):
     raise DflashError(DFLASH_ERR_INVALID_ARG, what)
 
 
-def _raw_stream(index: int, stream) -> int:
-    """The stream to launch on, on the (current) device `index`."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    if stream.device_index != index:
-        _refuse("the stream is of another device")
-    return stream.cuda_stream
+def _elsewhere(dev: torch.device, stream):
+    """The context that makes the call's device and stream the current ones; None if they are."""
+    if stream is not None:
+        if stream.device_index != dev.index:
+            _refuse("the stream is of another device")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+
+def _current(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _int32(device, what: str, *tensors) -> None:
@@ -251,10 +256,11 @@ def page_tables(lengths: torch.Tensor, new_rows: torch.Tensor, held: torch.Tenso
     dev = table.device
     if not table.is_cuda:
         _refuse("page_tables: CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
             return page_tables(lengths, new_rows, held, table, ring, ring_state, page_size, row_cap, held_out,
-                               ring_state_out, status, stream)
+                               ring_state_out, status)
     if held_out is None:
         held_out = held
     if ring_state_out is None:
@@ -270,7 +276,7 @@ def page_tables(lengths: torch.Tensor, new_rows: torch.Tensor, held: torch.Tenso
     dflash_page_tables(lengths.data_ptr(), new_rows.data_ptr(), n, page_size, ring.numel(), held.data_ptr(),
                        held_out.data_ptr(), table.data_ptr(), table.shape[1], ring.data_ptr(), ring_state.data_ptr(),
                        ring_state_out.data_ptr(), at + 8 * wide, at, at + 4 * wide, row_cap,
-                       0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+                       0 if status is None else status.data_ptr(), _current(dev))
     return out[2 * wide:], out[:row_cap], out[wide: wide + row_cap]
 
 
@@ -278,30 +284,32 @@ def kv4_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torc
               stream=None) -> None:
     """Quantise rows k, v [n, n_kv_heads, head_dim] into the cells `slots` [n] (-1: none)."""
     c, dev = _kv4(cache), cache.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return kv4_write(cache, k, v, slots, status, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv4_write(cache, k, v, slots, status)
     ks, vs = _row_stride(k, dev, "kv4_write k"), _row_stride(v, dev, "kv4_write v")
     _int32(dev, "kv4_write slots", slots, status)
     n, heads, d = k.shape
     if k.shape != v.shape or k.dtype != v.dtype or n != slots.numel() or heads != c.n_kv_heads or d != c.head_dim:
         _refuse("kv4_write: shapes")
     dflash_kv4_write(c, k.data_ptr(), v.data_ptr(), _VALUE_TYPES[k.dtype], ks, vs, slots.data_ptr(), n,
-                     0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+                     0 if status is None else status.data_ptr(), _current(dev))
 
 
 def kv4_read(cache: torch.Tensor, slots: torch.Tensor, status=None, stream=None):
     """(k, v), float [n, n_kv_heads, head_dim], of the cells `slots` (zeros for -1)."""
     c, dev = _kv4(cache), cache.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return kv4_read(cache, slots, status, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv4_read(cache, slots, status)
     _int32(dev, "kv4_read slots", slots, status)
     n = slots.numel()
     k = torch.empty((n, c.n_kv_heads, c.head_dim), dtype=torch.float32, device=dev)
     v = torch.empty((n, c.n_kv_heads, c.head_dim), dtype=torch.float32, device=dev)
     dflash_kv4_read(c, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), 0 if status is None else status.data_ptr(),
-                    _raw_stream(dev.index, stream))
+                    _current(dev))
     return k, v
 
 
@@ -312,10 +320,11 @@ def kv4_attention(cache: torch.Tensor, q: torch.Tensor, table: torch.Tensor, kv_
     their sequences; scale None is head_dim ** -0.5.  Rows of no sequence keep
     what `out` held (unset if out is None)."""
     c, dev = _kv4(cache), cache.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
             return kv4_attention(cache, q, table, kv_len, row_offsets, max_rows, causal, window, scale, out, workspace,
-                                 status, stream)
+                                 status)
     qs = _row_stride(q, dev, "kv4_attention q")
     _int32(dev, "kv4_attention", table, kv_len, row_offsets, status)
     tokens, heads, d = q.shape
@@ -338,7 +347,7 @@ def kv4_attention(cache: torch.Tensor, q: torch.Tensor, table: torch.Tensor, kv_
     dflash_kv4_attention(c, q.data_ptr(), out.data_ptr(), _VALUE_TYPES[q.dtype], qs, os_, tokens, heads, n, max_rows,
                          row_offsets.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.shape[1], causal, window,
                          d ** -0.5 if scale is None else scale, workspace.data_ptr(), size,
-                         0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+                         0 if status is None else status.data_ptr(), _current(dev))
     return out
 
 
@@ -350,9 +359,10 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     kind = _VALUE_TYPES.get(logits.dtype)
     if not logits.is_cuda or logits.dim() != 2 or kind is None:
         _refuse("token_logprobs: [rows, vocab] logits on a CUDA device")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return token_logprobs(logits, tokens, top_k, status, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return token_logprobs(logits, tokens, top_k, status)
     n, vocab = logits.shape
     stride, by_value = logits.stride()
     if (by_value != 1 and vocab != 1) or (tokens is not None and tokens.numel() != n) or top_k < 0:
@@ -365,5 +375,5 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     dflash_token_logprobs(logits.data_ptr(), kind, stride if n > 1 else vocab, n, vocab,
                           0 if tokens is None else tokens.data_ptr(), 0 if logp is None else logp.data_ptr(),
                           entropy.data_ptr(), top_k, ids.data_ptr(), top.data_ptr(),
-                          0 if status is None else status.data_ptr(), _raw_stream(dev.index, stream))
+                          0 if status is None else status.data_ptr(), _current(dev))
     return logp, entropy, ids, top

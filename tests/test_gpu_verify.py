@@ -393,6 +393,30 @@ def test_attention_streams_and_graph(R, G):
         assert torch.equal(out[:3], w)
 
 
+def test_stream_argument(R):
+    """A call on a stream that has not come to it yet: its workspace and outputs are not handed to the current stream."""
+    cache, q, table, lens, offsets = attn_case(6, 128, 2, 4, [3000, 70], [1, 2], 64, "bf16")
+    c, table, lens, offsets = torch.as_tensor(cache, device="cuda"), ints(table), ints(lens), ints(offsets)
+    n = int(offsets[-1])
+    plain = R.kv4_attention(c, q, table, lens, offsets, 2)[:n].clone()
+    logits = q.flatten(1)
+    scores = R.token_logprobs(logits, top_k=3)
+    args = D.DflashKv4Cache(c.data_ptr(), c.shape[0], 64, 2, 128)
+    size = D.dflash_kv4_attention_workspace(args, 8, 2, 2, table.shape[1]) + 16
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    out = R.kv4_attention(c, q, table, lens, offsets, 2, stream=side)
+    mine = torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda")
+    again = R.token_logprobs(logits, top_k=3, stream=side)
+    torch.cuda.synchronize()
+    assert bool((mine == 0x7F).all())
+    assert torch.equal(out[:n], plain)
+    for x, y in zip(scores[1:], again[1:]):
+        assert torch.equal(x, y)
+
+
 def test_cells_beyond_4_gb(R):
     """Pages whose bytes lie beyond 32 bits: written, read back and attended to."""
     heads, d, page, n_pages = 8, 256, 256, 9000  # 5.3 GB
