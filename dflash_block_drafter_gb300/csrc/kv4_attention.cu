@@ -665,7 +665,8 @@ int check_call(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows
   if (const int e = dflash_kv4_check(c)) return e;
   if (n_seq < 1 || table_stride < 1 || n_q_heads < 1 || n_q_heads % c->n_kv_heads) return DFLASH_ERR_INVALID_ARG;
   if (max_rows < 1 || max_rows > DFLASH_MAX_BLOCK) return DFLASH_ERR_INVALID_ARG;
-  if (n_seq > kKv4MaxSeq) return DFLASH_ERR_CAPACITY;
+  // (positions up to a tile behind the table's last stay within 31 bits)
+  if (n_seq > kKv4MaxSeq || static_cast<long long>(table_stride) * c->page_size > 0x7fffff00ll) return DFLASH_ERR_CAPACITY;
   if (n_q_heads / c->n_kv_heads * max_rows > 128) return DFLASH_ERR_UNSUPPORTED;
   return DFLASH_OK;
 }

@@ -250,7 +250,10 @@ extern "C" int dflash_page_tables(const int32_t* lengths, const int32_t* new_row
   if (n_seq < 1 || table_stride < 1 || n_pages < 1 || row_cap < 0 || (row_cap > 0 && !slots))
     return DFLASH_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return DFLASH_ERR_UNSUPPORTED;
-  if (n_seq > kMaxRequests || static_cast<long long>(n_pages) * page_size > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
+  // (n_seq * table_stride: the sums of pages taken and given back stay within 31 bits)
+  if (n_seq > kMaxRequests || static_cast<long long>(n_pages) * page_size > 0x7fffffffll ||
+      static_cast<long long>(n_seq) * table_stride >= 0x7fffffffll)
+    return DFLASH_ERR_CAPACITY;
   PageArgs a{lengths, new_rows, n_seq, 0, n_pages, held_in, held_out, table, table_stride, ring, ring_in, ring_out,
              row_offsets, slots, positions, row_cap, dev_status};
   while ((1 << a.page_shift) < page_size) ++a.page_shift;

@@ -468,7 +468,8 @@ size_t dflash_kv4_bytes(int32_t n_pages, int32_t page_size, int32_t n_kv_heads, 
  * beyond are dropped), a page id outside [0, n_pages) (slot -1), a ring head or
  * count out of range, and more pages given back than the ring has room for.
  * held_out may be held_in and ring_out may be ring_in; no other arrays may
- * overlap.  n_seq <= 4096 (else DFLASH_ERR_CAPACITY).  One launch. */
+ * overlap.  n_seq <= 4096 and n_seq * table_stride < 2^31 - 1 (else
+ * DFLASH_ERR_CAPACITY).  One launch. */
 int dflash_page_tables(const int32_t* lengths, const int32_t* new_rows, int32_t n_seq, int32_t page_size,
                        int32_t n_pages, const int32_t* held_in, int32_t* held_out, int32_t* table,
                        int32_t table_stride, int32_t* ring, const int32_t* ring_in, int32_t* ring_out,
@@ -521,7 +522,8 @@ int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t
  *   workspace: dflash_kv4_attention_workspace bytes, 16-byte aligned; calls
  *           that overlap in time need one each.  Nothing in it has to be set
  *           or outlives the call.
- * n_seq <= 1024 (else DFLASH_ERR_CAPACITY). */
+ * n_seq <= 1024 and table_stride * page_size <= 2^31 - 256 (else
+ * DFLASH_ERR_CAPACITY). */
 int dflash_kv4_attention(const dflash_kv4_cache* cache, const void* q, void* out, int32_t type, int64_t q_stride,
                          int64_t out_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_seq, int32_t max_rows,
                          const int32_t* row_offsets, const int32_t* kv_len, const int32_t* table, int32_t table_stride,

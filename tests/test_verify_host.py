@@ -92,6 +92,8 @@ def test_attention_refusals(lib):
     assert call(type=D.DFLASH_T_FP32) == D.DFLASH_ERR_UNSUPPORTED
     assert call(nq=34, rows=8, qs=34 * 128, os=34 * 128) == D.DFLASH_ERR_UNSUPPORTED  # 17 heads of a group x 8 rows > 128
     assert call(n_seq=1025) == D.DFLASH_ERR_CAPACITY
+    assert call(width=1 << 25) == D.DFLASH_ERR_CAPACITY  # positions beyond 31 bits
+    assert D.dflash_kv4_attention_workspace(_cache(), 8, 1, 1, 1 << 25) == 0
     assert call(tokens=0) == D.DFLASH_OK
 
 
@@ -110,6 +112,7 @@ def test_page_tables_refusals(lib):
         assert call(**kw) == D.DFLASH_ERR_UNSUPPORTED, kw
     assert call(n_seq=4097) == D.DFLASH_ERR_CAPACITY
     assert call(pages=1 << 27) == D.DFLASH_ERR_CAPACITY
+    assert call(n_seq=4096, width=1 << 19) == D.DFLASH_ERR_CAPACITY
 
 
 def test_logprobs_refusals(lib):
