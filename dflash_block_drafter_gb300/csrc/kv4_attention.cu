@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       const int up = top > 0.f ? min(12 + 127 - ex, 120) : 0;
       const float f = ldexpf(1.f, up);
       if (part == 0) {
-        s_factor[m] = ldexpf(a.scale_log2, 24 - up);
+        // (beyond 2^100 any two scores that differ are too far apart to share weight)
+        s_factor[m] = fminf(ldexpf(a.scale_log2, 24 - up), 0x1p100f);
         s_sees[m] = m < n_rows ? kv4_sees(a, q, row / a.G) : make_int2(0, 0);
       }
       // element e of block b, quad tt: word 4b + tt, nibble e; even nibbles as

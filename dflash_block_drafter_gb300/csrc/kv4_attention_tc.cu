@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       top = fmaxf(red_sum[m], red_sum[R + m]);
       // power of two that brings the row's maximum into [2^12, 2^13)
       const int up = top > 0.f ? min(12 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 120) : 0;
-      const float f = ldexpf(1.f, up), factor = fmaxf(ldexpf(a.scale_log2, -up), 1.17549435e-38f);
+      const float f = ldexpf(1.f, up), factor = fminf(fmaxf(ldexpf(a.scale_log2, -up), 1.17549435e-38f), 0x1p80f);  // (beyond, any two scores that differ are too far apart to share weight)
       if (live) {
 #pragma unroll 1
         for (int e = 0; e < D / 2; e += 32) {

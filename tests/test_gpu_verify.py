@@ -318,6 +318,23 @@ def test_attention_ranges(R, kind, gain, scale):
     check_attn(R, attn_case(1, 128, 1, 4, [300], [2], 32, kind, gain=gain), True, scale=scale)
 
 
+@pytest.mark.parametrize("d,G,rows,seed", [(64, 4, 1, 70), (128, 3, 4, 70), (256, 5, 8, 99)])
+def test_attention_huge_queries(R, d, G, rows, seed):
+    """Scores near FP32's largest value: all weight on one cell, which both kernels must find."""
+    cache, q, table, lens, offsets = attn_case(seed, d, 1, G, [8], [rows], 16, "bf16", gain=1e36)
+    st = status()
+    out = R.kv4_attention(torch.as_tensor(cache, device="cuda"), q, ints(table), ints(lens), ints(offsets), rows, causal=False, status=st)
+    n = offsets[-1]
+    got, x = out[:n].double().cpu().numpy(), q[:n].double().cpu().numpy()
+    k, v = V.load(cache, table[0, 0].astype(np.int64) * 16 + np.arange(8))
+    s, size = np.einsum("rgd,cd->rgc", x, k[:, 0]), np.einsum("rgd,cd->rgc", np.abs(x), np.abs(k[:, 0]))
+    two = np.sort(s, -1)[..., -2:]
+    assert np.all(two[..., 1] - two[..., 0] > 2.0 ** -9 * size.max(-1))  # more than K's rounding moves two scores
+    want = v[:, 0][s.argmax(-1)]
+    assert int(st) == 0
+    assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -8))  # V to FP16, the output to BF16
+
+
 @pytest.mark.parametrize("vgain", [1e-4, 3e3])
 def test_attention_value_range(R, vgain):
     check_attn(R, attn_case(2, 64, 1, 4, [100], [1], 16, "bf16", vgain=vgain), True)
