@@ -147,6 +147,11 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
   const long long x_end = kv4_start(T, C, c + 1);
 
   const int groups_of_page = 1 << (a.page_shift - 4);
+  // Word of the V chunk of channel group g that this lane takes, and its first pair of
+  // channels there.  The word differs by g, so that the 8 groups of 4 cells, exchanged as
+  // Kv4::v_swap says, lie in 32 different banks (the same word for all g: 4 ways of
+  // conflicts at D 256, 2 at 128).
+  const int u = (warp * JT / 4) ^ (D == 256 ? g >> 1 : D == 128 ? g >> 2 : 0), j0 = warp * JT % 4;
   const int cell_g = (g & 1) ? 7 - (g >> 1) : g >> 1;  // cell of S^T's row g (and 8 + cell_g of row g + 8)
   const Kv4Consts kc;
   uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
@@ -490,7 +495,6 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
         }
       }
       // ---- O^T: cells t, 7 - t and 8 + t, 15 - t of each group, this warp's channels
-      const int u = warp * JT / 4, j0 = warp * JT % 4;  // its word of each V chunk, its first 16-channel tile in the word
 #pragma unroll
       for (int gi = 0; gi < G::GROUPS; ++gi) {
         const uint8_t* gb = base + gi * F::GROUP_BYTES;
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
     }
     const bool whole = k0 == 0 && k1 == q.steps;
     const int slot = 2 * c + (k0 == 0 ? 1 : 0);
-    const int col = 64 * (warp * JT / 4) + 8 * g + 2 * (warp * JT % 4);
+    const int col = 64 * u + 8 * g + 2 * j0;
 #pragma unroll
     for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
