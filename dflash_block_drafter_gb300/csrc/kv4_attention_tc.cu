@@ -41,7 +41,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kOverhead = 8;   // a segment's beginning and end, in tiles
 constexpr int kSoftWarps = 8, kUnpackWarps = 8;  // (unpacking: K and V each)
-constexpr int kQkWarp = 0, kCopyWarp = 1, kPvWarp = 2;  // (3 fills their warpgroup)
+constexpr int kQkWarp = 0, kCopyKWarp = 1, kPvWarp = 2, kCopyVWarp = 3;
 constexpr int kSoftWarp0 = 4, kUnpackWarp0 = kSoftWarp0 + kSoftWarps;
 constexpr int kThreads = 32 * (kSoftWarps + 2 * kUnpackWarps + 4);  // whole warpgroups
 constexpr int kSoftThreads = 32 * kSoftWarps;
@@ -50,7 +50,6 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
               "the roles' registers come out of the launch's");
-constexpr int kPacked = 3;      // stages of the packed ring
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
 
@@ -59,12 +58,15 @@ struct Geo {
   static constexpr int TILE = D == 256 ? 64 : 128;           // cells of a tile
   static constexpr int GROUPS = TILE / 16;
   static constexpr int SCORES = D == 128 ? 2 : 3;            // S buffers
-  static constexpr int STAGE = GROUPS * Kv4<D>::GROUP_BYTES;
+  static constexpr int PACKED = D == 256 ? 3 : D == 128 ? 4 : 6;  // stages of the packed rings
+  static constexpr int HALF = Kv4<D>::GROUP_BYTES / 2;       // K or V of a group: codes, then scales
+  static constexpr int STAGE = GROUPS * HALF;
+  static_assert(Kv4<D>::V_CODES == HALF && Kv4<D>::V_SCALES == HALF + Kv4<D>::K_SCALES, "halves");
   static constexpr int BUF = TILE * D * 2;                   // one unpacked K or V tile
   static constexpr int RED = 3 * kRows * 4;
   static constexpr int QT = D == 256 ? 128 : D;              // channels of Q in tensor memory
   static constexpr int QBUF = kRows * (D - QT) * 2;          // the others, [64-channel boxes][128 rows][128 B]
-  static constexpr int SMEM = 1024 + 4 * BUF + QBUF + kPacked * STAGE + RED;
+  static constexpr int SMEM = 1024 + 4 * BUF + QBUF + 2 * PACKED * STAGE + RED;
   static constexpr int S_COL = 0, O_COL = SCORES * TILE, Q_COL = O_COL + D;
   static_assert(Q_COL + QT / 2 <= kTmemCols, "columns");
 };
@@ -193,25 +195,28 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a) {
   using F = Kv4<D>;
   using G = Geo<D>;
-  constexpr int R = kRows, NP = kPacked, U = D / 64, B = D / 32, kTile = G::TILE, kScores = G::SCORES, kGroups = G::GROUPS;
+  constexpr int R = kRows, NP = G::PACKED, U = D / 64, B = D / 32, kTile = G::TILE, kScores = G::SCORES, kGroups = G::GROUPS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                       // [2][D / 64 boxes][T cells][128 B]
   uint8_t* vbuf = kbuf + 2 * G::BUF;          // [2]
   uint8_t* qbuf = vbuf + 2 * G::BUF;          // Q's channels from QT on
-  uint8_t* ring = qbuf + G::QBUF;             // [NP] packed tiles
-  float* s_ref = reinterpret_cast<float*>(ring + NP * G::STAGE);    // [128 rows] references of the scores
+  uint8_t* kring = qbuf + G::QBUF;            // [NP] packed tiles of K
+  uint8_t* vring = kring + NP * G::STAGE;     // and of V
+  float* s_ref = reinterpret_cast<float*>(vring + NP * G::STAGE);   // [128 rows] references of the scores
   float* red_sum = s_ref + R;                                       // [2][128 rows]
   long long* pre = reinterpret_cast<long long*>(red_sum + 2 * R);   // [n_seq + 1]
   __shared__ long long scratch[kThreads / 32];
-  __shared__ uint64_t pfull[NP], pfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[kScores], sfree[kScores], pready[kScores], qready, odone, ofree, done[2];
+  __shared__ uint64_t kpfull[NP], kpfree[NP], vpfull[NP], vpfree[NP], kready[2], kfree[2], vready[2], vfree[2], sfull[kScores], sfree[kScores], pready[kScores], qready, odone, ofree, done[2];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < NP; ++i) {
-      mbar_init(&pfull[i], 1);
-      mbar_init(&pfree[i], kUnpackWarps);
+      mbar_init(&kpfull[i], 1);
+      mbar_init(&kpfree[i], kUnpackWarps / 2);
+      mbar_init(&vpfull[i], 1);
+      mbar_init(&vpfree[i], kUnpackWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kready[i], kUnpackWarps / 2);
@@ -253,51 +258,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   auto part_at = [&](long long at, const Kv4Part& before) { return kv4_part<kTile, R, kOverhead>(a, pre, at, x_end, before); };
 
   if (warp < kSoftWarp0) fewer_registers<kOtherRegs>();
-  if (warp == kCopyWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp == kCopyKWarp || warp == kCopyVWarp) {
+    // ------------------------------------------------------------ producers
+    const bool v_side = warp == kCopyVWarp;
+    uint64_t* pfull = v_side ? vpfull : kpfull;
+    uint64_t* pfree = v_side ? vpfree : kpfree;
+    uint8_t* ring = v_side ? vring : kring;
     const int groups_of_page = 1 << (a.page_shift - 4);
     uint32_t g = 0;  // tiles over all parts
     for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p)) {
-      // the lanes hold the pages of the groups of WIN tiles, and those of the next WIN
-      constexpr int WIN = 32 / kGroups, AHEAD = WIN - 1;
+      // a lane holds the address of its group of its tile of WIN (0: nothing to copy),
+      // and that of the WIN tiles after them
+      constexpr int WIN = 32 / kGroups;
       const int lane_tile = lane / kGroups, lane_group = lane % kGroups;
-      auto look_up = [&](int from) {
+      auto look_up = [&](int from) -> const uint8_t* {
         const int i = from + lane_tile;
         const int pos = p.q.base + (p.k0 + i) * kTile + lane_group * 16;
-        if (i >= p.n || pos >= p.q.hi) return -1;
+        if (i >= p.n || pos >= p.q.hi) return nullptr;
         int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
         if (page < 0 || page >= a.n_pages) {
           set_status(a.status, DFLASH_DEV_CAPACITY);
           page = 0;
         }
-        return page;
+        const int grp = (pos >> 4) & (groups_of_page - 1);
+        return a.cache + ((static_cast<size_t>(page) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES +
+               (v_side ? F::V_CODES : F::K_CODES);
       };
-      auto address = [&](int page, int i) {  // of this lane's group of tile i
-        const int grp = ((p.q.base + (p.k0 + i) * kTile + lane_group * 16) >> 4) & (groups_of_page - 1);
-        return a.cache + ((static_cast<size_t>(page) * a.n_kv + p.head) * groups_of_page + grp) * F::GROUP_BYTES;
-      };
-      int page = -1, later = look_up(0);
+      const uint8_t *from = nullptr, *later = look_up(0);
+      // the ring is too short for HBM's latency: L2 is asked for the tiles behind it
+      // now, then for each tile WIN - 1 tiles before it is copied
+      if (lane_tile >= NP && later) bulk_prefetch_l2_plain(later, G::HALF);
+      unsigned have = 0;
       for (int i = 0; i < p.n && ok; ++i, ++g) {
-        if (i % WIN == 0) {
-          page = later;
+        const int t = i % WIN, st = g % NP;
+        if (t == 0) {
+          from = later;
+          have = __ballot_sync(0xffffffffu, from != nullptr);
           later = look_up(i + WIN);
         }
-        // the ring is too short for HBM's latency: tile i + AHEAD is asked of L2
-        // now (at the part's start, all tiles behind the ring up to it)
-        for (int j = i == 0 ? NP : i + AHEAD; j <= i + AHEAD; ++j) {
-          const int there = __shfl_sync(0xffffffffu, j / WIN == i / WIN ? page : later, (j % WIN) * kGroups + lane_group);
-          if (lane < kGroups && there >= 0) bulk_prefetch_l2_plain(address(there, j), F::GROUP_BYTES);
-        }
-        const int st = g % NP;
         if (g >= NP) ok = __all_sync(0xffffffffu, kv4_wait(&pfree[st], (g / NP - 1) & 1));
         if (!ok) break;
-        const int mine = __shfl_sync(0xffffffffu, page, (i % WIN) * kGroups + lane_group);
-        const unsigned have = __ballot_sync(0xffffffffu, lane < kGroups && mine >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have) * F::GROUP_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have >> (t * kGroups) & ((1u << kGroups) - 1)) * G::HALF);
         __syncwarp();
-        if (lane < kGroups && mine >= 0) {
-          bulk_g2s(ring + st * G::STAGE + lane * F::GROUP_BYTES, address(mine, i), F::GROUP_BYTES, &pfull[st]);
-        }
+        if (lane_tile == t && from) bulk_g2s(ring + st * G::STAGE + lane_group * G::HALF, from, G::HALF, &pfull[st]);
+        if (t > 0 && lane_tile == t - 1 && later) bulk_prefetch_l2_plain(later, G::HALF);
+        if (t == 0 && i > 0 && lane_tile == WIN - 1 && from) bulk_prefetch_l2_plain(from, G::HALF);
       }
     }
     // every copy lands before the CTA ends
@@ -612,6 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int w4 = warp & 3, b = ((warp - kUnpackWarp0) >> 2) & 1;  // of four warps; parity of its tiles
     uint64_t* ready = (v_side ? vready : kready) + b;
     uint64_t* free_ = (v_side ? vfree : kfree) + b;
+    uint64_t* pfull = v_side ? vpfull : kpfull;
+    uint64_t* pfree = v_side ? vpfree : kpfree;
+    const uint8_t* ring = v_side ? vring : kring;
     const Kv4Consts kc;
     // A lane's first cell of a tile, its codes and scales there (in the packed
     // tile) and its first 16 bytes in the unpacked tile; the others lie whole
@@ -625,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     if (v_side) {
       const int ch = lane & 7;
       cell = w4 * 4 + (lane >> 3);
-      codes = F::V_CODES + cell * F::ROW + 4 * U * (ch ^ F::v_swap(cell));
-      scales = F::V_SCALES + cell * F::SROW + 2 * U * (ch >> 2);
+      codes = cell * F::ROW + 4 * U * (ch ^ F::v_swap(cell));
+      scales = F::K_SCALES + cell * F::SROW + 2 * U * (ch >> 2);
       first = cell * 128 + ((ch ^ (cell & 7)) << 4);
     } else {
       const int t = lane & 3;
@@ -643,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         cell = ((q >> 1) << 3) + ((q & 1) ^ ((k & 1) * 5) ^ ((k >> 1) * 2));
       }
       const int cg = cell & 15;
-      codes = (cell >> 4) * F::GROUP_BYTES + F::K_CODES + cg * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cg));
-      scales = (cell >> 4) * F::GROUP_BYTES + F::K_SCALES + cg * F::SROW + 8 * h;
+      codes = (cell >> 4) * G::HALF + cg * F::ROW + 4 * ((t * B + 4 * h) ^ F::k_swap(cg));
+      scales = (cell >> 4) * G::HALF + F::K_SCALES + cg * F::SROW + 8 * h;
       first = 2 * h * (kTile * 128) + cell * 128 + ((t ^ (cell & 7)) << 4);
     }
     uint8_t* to = (v_side ? vbuf : kbuf) + b * G::BUF + first;
@@ -675,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           uint32_t w[N][KW], d[N][KW];
 #pragma unroll
           for (int it = 0; it < N; ++it) {
-            load_words<KW>(packed + codes + it * (KSTEP / 16) * F::GROUP_BYTES, w[it]);
-            load_scales<KW>(packed + scales + it * (KSTEP / 16) * F::GROUP_BYTES, d[it]);
+            load_words<KW>(packed + codes + it * (KSTEP / 16) * G::HALF, w[it]);
+            load_scales<KW>(packed + scales + it * (KSTEP / 16) * G::HALF, d[it]);
             if (edge && hidden(it * KSTEP))
               for (int j = 0; j < KW; ++j) d[it][j] = 0;
           }
@@ -691,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           uint32_t w[N][U], d[N][U];
 #pragma unroll
           for (int it = 0; it < N; ++it) {
-            load_words<U>(packed + codes + it * F::GROUP_BYTES, w[it]);
-            load_scales<U>(packed + scales + it * F::GROUP_BYTES, d[it]);
+            load_words<U>(packed + codes + it * G::HALF, w[it]);
+            load_scales<U>(packed + scales + it * G::HALF, d[it]);
             if (edge && hidden(it * 16))
               for (int u = 0; u < U; ++u) d[it][u] = 0;
           }
