@@ -134,6 +134,11 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool repo
   return q;
 }
 
+// The token x / G of a query row x < 1024: x * ceil(2^17 / G) >> 17 (off by less than
+// x G / 2^17 / G, below the 1 / G that a quotient lies from the next integer).
+__device__ __forceinline__ uint32_t kv4_per_token(int G) { return ((1u << 17) + G - 1) / G; }
+__device__ __forceinline__ int kv4_token(int x, uint32_t per_g) { return static_cast<int>(static_cast<uint32_t>(x) * per_g >> 17); }
+
 // Visible cells [lo, hi) of token i of the sequence.
 __device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, int i) {
   const int upto = a.causal ? q.kv - q.rows + i + 1 : q.kv;  // behind the row's own position

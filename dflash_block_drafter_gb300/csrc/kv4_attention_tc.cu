@@ -6,7 +6,8 @@
 //   warp 0        issues S = Q K^T (M 128, N = T), warp 2 O += P V (M 128, N = D):
 //                 two warps, because a wait and the issue of a tile's MMAs
 //                 take one warp as long as the MMAs themselves;
-//   warp 1        copies the tiles' packed groups into a ring (bulk copies);
+//   warps 1, 3    copy the tiles' packed K and V into rings (bulk copies): V's stages
+//                 are held longer, and one warp's copies took as long as a tile;
 //   warps 4..11   softmax: a thread has one row (TMEM lane) of every other
 //                 tile: warps 4..7 the even ones, 8..11 the odd ones, so that the
 //                 waits and fences of one tile lie under the arithmetic of the next;
@@ -29,10 +30,10 @@
 // relative to a reference that moves only when a row passes it by 2^8; the two
 // softmax warps of a quarter of the rows hand it to each other tile by tile.
 //
-// Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 93 us (557
-// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 95 us.  No unit is full
-// (issue 41 %, ALU 45 %, tensor pipe 27 %): a tile takes about 2500 cycles for its way
-// through eight barriers, and about 1800 with all the arithmetic taken out.
+// Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 91 us (568
+// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 92 us.  No unit is full
+// (issue 41 %, ALU 45 %, tensor pipe 27 %): a tile takes about 1900 cycles for its way
+// through eight barriers, and the first ones wait 13 us for the plan and Q.
 #include "kv4_attention.cuh"
 
 namespace dflash {
@@ -286,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       };
       const uint8_t *from = nullptr, *later = look_up(0);
       // the ring is too short for HBM's latency: L2 is asked for the tiles behind it
-      // now, then for each tile WIN - 1 tiles before it is copied
-      if (lane_tile >= NP && later) bulk_prefetch_l2_plain(later, G::HALF);
+      // now (in the CTA's first part only once Q is there, whose loads would have to wait
+      // behind them), then for each tile WIN - 1 tiles before it is copied
+      if (g > 0 && lane_tile >= NP && later) bulk_prefetch_l2_plain(later, G::HALF);
       unsigned have = 0;
       for (int i = 0; i < p.n && ok; ++i, ++g) {
         const int t = i % WIN, st = g % NP;
@@ -301,6 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have >> (t * kGroups) & ((1u << kGroups) - 1)) * G::HALF);
         __syncwarp();
         if (lane_tile == t && from) bulk_g2s(ring + st * G::STAGE + lane_group * G::HALF, from, G::HALF, &pfull[st]);
+        if (g == NP - 1 && i == NP - 1) {
+          ok = __all_sync(0xffffffffu, kv4_wait(&qready, 0));
+          if (lane_tile >= NP && from) bulk_prefetch_l2_plain(from, G::HALF);
+        }
         if (t > 0 && lane_tile == t - 1 && later) bulk_prefetch_l2_plain(later, G::HALF);
         if (t == 0 && i > 0 && lane_tile == WIN - 1 && from) bulk_prefetch_l2_plain(from, G::HALF);
       }
@@ -393,11 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int m = q4 * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     uint32_t g = 0, part = 0;
+    const uint32_t per_g = kv4_per_token(a.G);
     Kv4Job job{};  // the segment that begins here and goes on in the next CTAs, if one does
     for (Kv4Part p = part_at(x_begin, none); p.n > 0; p = part_at(p.next, p)) {
       const bool mine = m < p.rows, live = q4 * 32 < p.rows;  // the row; any row of the quarter
       const int row = p.row0 + m;
-      const int2 sees = mine ? kv4_sees(a, p.q, row / a.G) : make_int2(0, 0);
+      const int2 sees = mine ? kv4_sees(a, p.q, kv4_token(row, per_g)) : make_int2(0, 0);
       int all_lo = mine ? sees.x : 0, all_hi = mine ? sees.y : 0x7fffffff;  // cells that every row of the quarter sees
 #pragma unroll
       for (int w = 1; w < 32; w <<= 1) {
@@ -405,24 +412,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, w));
       }
       // ---- Q into tensor memory: half cs of the row's channels
-      const uint16_t* src = a.q + (p.q.r0 + row / a.G) * a.q_stride + (p.head * a.G + row % a.G) * D + cs * (D / 2);
-      auto value = [&](uint32_t h) { return a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(h))); };
-      float top = 0.f;
-      if (mine) {
-#pragma unroll 4
-        for (int e = 0; e < D / 2; e += 8) {
-          const uint4 r = *reinterpret_cast<const uint4*>(src + e);
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(value(w[j] & 0xffffu)), fabsf(value(w[j] >> 16))));
+      // (Nothing else runs until Q is there, and an instruction of a chain costs several
+      // cycles: FP16 rows are taken as they are, magnitudes compared as pairs of bits,
+      // powers of two made of bits, the token of a row found by a multiplication.)
+      const uint16_t* src = a.q + p.q.r0 * a.q_stride + kv4_token(row, per_g) * (a.q_stride - a.G * D) +
+                            (p.head * a.G + row) * D + cs * (D / 2);
+      int up = 0;
+      if (a.bf16) {
+        uint32_t top = 0;
+        if (mine) {
+#pragma unroll 8
+          for (int e = 0; e < D / 2; e += 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + e);
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+          }
         }
+        red_sum[cs * R + m] = __uint_as_float(top);
+        named_bar_sync(1, kSoftThreads);
+        top = __vmaxu2(__float_as_uint(red_sum[m]), __float_as_uint(red_sum[R + m]));
+        // power of two that brings the row's maximum into [2^12, 2^13)
+        const int ex = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);
+        if (top) up = min(12 + 127 - ex, 120);
       }
-      red_sum[cs * R + m] = top;
-      named_bar_sync(1, kSoftThreads);
-      top = fmaxf(red_sum[m], red_sum[R + m]);
-      // power of two that brings the row's maximum into [2^12, 2^13)
-      const int up = top > 0.f ? min(12 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 120) : 0;
-      const float f = ldexpf(1.f, up), factor = fminf(fmaxf(ldexpf(a.scale_log2, -up), 1.17549435e-38f), 0x1p80f);  // (beyond, any two scores that differ are too far apart to share weight)
+      auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
+      // (beyond 2^80 any two scores that differ are too far apart to share weight)
+      const float f = power(up), factor = fminf(fmaxf(a.scale_log2 * power(-up), 1.17549435e-38f), 0x1p80f);
       if (live) {
 #pragma unroll 1
         for (int e = 0; e < D / 2; e += 32) {
@@ -431,12 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           for (int k = 0; k < 4; ++k) {
             uint4 r = make_uint4(0, 0, 0, 0);
             if (mine) r = *reinterpret_cast<const uint4*>(src + e + 8 * k);
-            const uint32_t v[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // channels i and i + 4
-              const uint32_t lo = (i & 1) ? v[i >> 1] >> 16 : v[i >> 1] & 0xffffu;
-              const uint32_t hi = (i & 1) ? v[2 + (i >> 1)] >> 16 : v[2 + (i >> 1)] & 0xffffu;
-              w[4 * k + i] = pack_f16x2(value(lo) * f, value(hi) * f);
+            if (a.bf16) {  // channels i and i + 4
+              auto pair = [&](uint32_t lo, uint32_t hi) { return pack_f16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f); };
+              w[4 * k] = pair(r.x << 16, r.z << 16), w[4 * k + 1] = pair(r.x & 0xffff0000u, r.z & 0xffff0000u);
+              w[4 * k + 2] = pair(r.y << 16, r.w << 16), w[4 * k + 3] = pair(r.y & 0xffff0000u, r.w & 0xffff0000u);
+            } else {
+              w[4 * k] = prmt(r.x, r.z, 0x5410u), w[4 * k + 1] = prmt(r.x, r.z, 0x7632u);
+              w[4 * k + 2] = prmt(r.y, r.w, 0x5410u), w[4 * k + 3] = prmt(r.y, r.w, 0x7632u);
             }
           }
           if (cs * (D / 2) < G::QT) {
@@ -588,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[(e >> 1) + 4 * (e & 1)] = __uint_as_float(o[8 * k + e]) * inv;
               if (whole) {
-                uint16_t* dst = a.out + (p.q.r0 + row / a.G) * a.out_stride + (p.head * a.G + row % a.G) * D + col + 8 * k;
+                uint16_t* dst = a.out + p.q.r0 * a.out_stride + kv4_token(row, per_g) * (a.out_stride - a.G * D) + (p.head * a.G + row) * D + col + 8 * k;
                 *reinterpret_cast<uint4*>(dst) =
                     a.bf16 ? make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]))
                            : make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
