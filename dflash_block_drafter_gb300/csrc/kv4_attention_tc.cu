@@ -25,15 +25,15 @@
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
 // masking the word yields pairs: Q's columns are stored in the same order,
 // and O's are read back in it.
-// Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-25 absolute), Q exact (rows
-// scaled by a power of two); scores, sums and O in FP32.  Scores are taken
+// Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-25 absolute), Q by 2^-27 of a
+// row's largest value at most (BF16 rows are scaled by a power of two, FP16 exact); scores, sums and O in FP32.  Scores are taken
 // relative to a reference that moves only when a row passes it by 2^8; the two
 // softmax warps of a quarter of the rows hand it to each other tile by tile.
 //
 // Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 91 us (568
-// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 92 us.  No unit is full
+// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 90 us.  No unit is full
 // (issue 41 %, ALU 45 %, tensor pipe 27 %): a tile takes about 1900 cycles for its way
-// through eight barriers, and the first ones wait 13 us for the plan and Q.
+// through eight barriers, and the first ones wait 12 us for the plan and Q.
 #include "kv4_attention.cuh"
 
 namespace dflash {
@@ -417,54 +417,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       // powers of two made of bits, the token of a row found by a multiplication.)
       const uint16_t* src = a.q + p.q.r0 * a.q_stride + kv4_token(row, per_g) * (a.q_stride - a.G * D) +
                             (p.head * a.G + row) * D + cs * (D / 2);
-      int up = 0;
-      if (a.bf16) {
+      // BF16 rows are scaled into FP16's range: by 2^8 where their largest magnitude is
+      // in [2^-6, 2^7) (what falls below FP16's smallest value is 2^-27 of that, at most), so
+      // that one pass over Q does; else by the power that brings it into [2^12, 2^13).
+      auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
+      int up = a.bf16 ? 8 : 0;
+      for (bool again = false;; again = true) {
         uint32_t top = 0;
-        if (mine) {
-#pragma unroll 8
-          for (int e = 0; e < D / 2; e += 8) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + e);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        if (live) {
+          const float f = power(up);
+#pragma unroll 1
+          for (int e = 0; e < D / 2; e += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 r = make_uint4(0, 0, 0, 0);
+              if (mine) r = *reinterpret_cast<const uint4*>(src + e + 8 * k);
+              if (a.bf16) {  // channels i and i + 4
+                auto pair = [&](uint32_t lo, uint32_t hi) { return pack_f16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f); };
+                w[4 * k] = pair(r.x << 16, r.z << 16), w[4 * k + 1] = pair(r.x & 0xffff0000u, r.z & 0xffff0000u);
+                w[4 * k + 2] = pair(r.y << 16, r.w << 16), w[4 * k + 3] = pair(r.y & 0xffff0000u, r.w & 0xffff0000u);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu), __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu)));
+              } else {
+                w[4 * k] = prmt(r.x, r.z, 0x5410u), w[4 * k + 1] = prmt(r.x, r.z, 0x7632u);
+                w[4 * k + 2] = prmt(r.y, r.w, 0x5410u), w[4 * k + 3] = prmt(r.y, r.w, 0x7632u);
+              }
+            }
+            if (cs * (D / 2) < G::QT) {
+              tmem_st16(lane_addr + G::Q_COL + (cs * (D / 2) + e) / 2, w);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(qbuf + (e >> 6) * (kRows * 128) + m * 128 + (((((e & 63) >> 3) + k) ^ (m & 7)) << 4)) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
           }
+          tmem_wait_st();
         }
+        if (again || !a.bf16) break;
         red_sum[cs * R + m] = __uint_as_float(top);
         named_bar_sync(1, kSoftThreads);
         top = __vmaxu2(__float_as_uint(red_sum[m]), __float_as_uint(red_sum[R + m]));
-        // power of two that brings the row's maximum into [2^12, 2^13)
         const int ex = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);
-        if (top) up = min(12 + 127 - ex, 120);
+        const bool other = top && (ex < 127 - 6 || ex > 127 + 6);
+        if (!__any_sync(0xffffffffu, other)) break;
+        if (other) up = min(12 + 127 - ex, 120);
       }
-      auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
       // (beyond 2^80 any two scores that differ are too far apart to share weight)
-      const float f = power(up), factor = fminf(fmaxf(a.scale_log2 * power(-up), 1.17549435e-38f), 0x1p80f);
-      if (live) {
-#pragma unroll 1
-        for (int e = 0; e < D / 2; e += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (mine) r = *reinterpret_cast<const uint4*>(src + e + 8 * k);
-            if (a.bf16) {  // channels i and i + 4
-              auto pair = [&](uint32_t lo, uint32_t hi) { return pack_f16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f); };
-              w[4 * k] = pair(r.x << 16, r.z << 16), w[4 * k + 1] = pair(r.x & 0xffff0000u, r.z & 0xffff0000u);
-              w[4 * k + 2] = pair(r.y << 16, r.w << 16), w[4 * k + 3] = pair(r.y & 0xffff0000u, r.w & 0xffff0000u);
-            } else {
-              w[4 * k] = prmt(r.x, r.z, 0x5410u), w[4 * k + 1] = prmt(r.x, r.z, 0x7632u);
-              w[4 * k + 2] = prmt(r.y, r.w, 0x5410u), w[4 * k + 3] = prmt(r.y, r.w, 0x7632u);
-            }
-          }
-          if (cs * (D / 2) < G::QT) {
-            tmem_st16(lane_addr + G::Q_COL + (cs * (D / 2) + e) / 2, w);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(qbuf + (e >> 6) * (kRows * 128) + m * 128 + (((((e & 63) >> 3) + k) ^ (m & 7)) << 4)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          }
-        }
-        tmem_wait_st();
-      }
+      const float factor = fminf(fmaxf(a.scale_log2 * power(-up), 1.17549435e-38f), 0x1p80f);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();

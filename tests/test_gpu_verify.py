@@ -318,6 +318,18 @@ def test_attention_ranges(R, kind, gain, scale):
     check_attn(R, attn_case(1, 128, 1, 4, [300], [2], 32, kind, gain=gain), True, scale=scale)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("G,rows", [(3, 8), (13, 8)])
+def test_attention_rows_of_unequal_size(R, d, kind, G, rows):
+    """Rows of very different magnitudes side by side, in both kernels."""
+    cache, q, table, lens, offsets = attn_case(d + G, d, 1, G, [300, 90], [rows, 3], 16, kind)
+    size = torch.tensor([2.0 ** 9, 1.0, 2.0 ** -5, 2.0 ** -12, 2.0 ** 7, 2.0 ** -8, 0.0], device="cuda")
+    n = q.shape[0] * q.shape[1]
+    q = (q.float() * size[torch.arange(n, device="cuda") % 7].view(q.shape[0], q.shape[1], 1)).to(q.dtype)
+    check_attn(R, (cache, q, table, lens, offsets), True, scale=d ** -0.5 * 2.0 ** -9)
+
+
 @pytest.mark.parametrize("d,G,rows,seed", [(64, 4, 1, 70), (128, 3, 4, 70), (256, 5, 8, 99)])
 def test_attention_huge_queries(R, d, G, rows, seed):
     """Scores near FP32's largest value: all weight on one cell, which both kernels must find."""
