@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
   const int u = (warp * JT / 4) ^ (D == 256 ? g >> 1 : D == 128 ? g >> 2 : 0), j0 = warp * JT % 4;
   const int cell_g = (g & 1) ? 7 - (g >> 1) : g >> 1;  // cell of S^T's row g (and 8 + cell_g of row g + 8)
   const Kv4Consts kc;
+  const uint32_t per_g = kv4_per_token(a.G);
   uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
   bool ok = true, job = false;
 
@@ -215,16 +216,22 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       float top = 0.f;
       const int row = row0 + m;
       if (m < n_rows) {
-        const uint16_t* src = a.q + (q.r0 + row / a.G) * a.q_stride + (head * a.G + row % a.G) * D + part * E;
+        const uint16_t* src = a.q + q.r0 * a.q_stride + kv4_token(row, per_g) * (a.q_stride - a.G * D) + (head * a.G + row) * D + part * E;
 #pragma unroll
         for (int e = 0; e < E; e += 8) {
           const uint4 raw = *reinterpret_cast<const uint4*>(src + e);
           const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t h = (j & 1) ? pr[j >> 1] >> 16 : pr[j >> 1] & 0xffffu;
-            v[e + j] = a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
-            top = fmaxf(top, fabsf(v[e + j]));
+          for (int j = 0; j < 4; ++j) {
+            if (a.bf16) {
+              v[e + 2 * j] = __uint_as_float(pr[j] << 16);
+              v[e + 2 * j + 1] = __uint_as_float(pr[j] & 0xffff0000u);
+            } else {
+              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pr[j]));
+              v[e + 2 * j] = x.x;
+              v[e + 2 * j + 1] = x.y;
+            }
+            top = fmaxf(top, fmaxf(fabsf(v[e + 2 * j]), fabsf(v[e + 2 * j + 1])));
           }
         }
       } else {
@@ -236,11 +243,12 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       // power of two that brings the row's maximum into [2^12, 2^13)
       const int ex = static_cast<int>(__float_as_uint(top) >> 23);
       const int up = top > 0.f ? min(12 + 127 - ex, 120) : 0;
-      const float f = ldexpf(1.f, up);
+      auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
+      const float f = power(up);
       if (part == 0) {
         // (beyond 2^100 any two scores that differ are too far apart to share weight)
-        s_factor[m] = fminf(ldexpf(a.scale_log2, 24 - up), 0x1p100f);
-        s_sees[m] = m < n_rows ? kv4_sees(a, q, row / a.G) : make_int2(0, 0);
+        s_factor[m] = fminf(a.scale_log2 * power(-up) * 0x1p24f, 0x1p100f);
+        s_sees[m] = m < n_rows ? kv4_sees(a, q, kv4_token(row, per_g)) : make_int2(0, 0);
       }
       // element e of block b, quad tt: word 4b + tt, nibble e; even nibbles as
       // they are, odd ones / 16 (their codes are 16 times as large)
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
           f = l > 0.f ? 1.f / l : 0.f;
           if (!(l < INFINITY)) set_status(a.status, DFLASH_DEV_NONFINITE);
           const int row = row0 + m;
-          uint16_t* dst = a.out + (q.r0 + row / a.G) * a.out_stride + (head * a.G + row % a.G) * D + col;
+          uint16_t* dst = a.out + q.r0 * a.out_stride + kv4_token(row, per_g) * (a.out_stride - a.G * D) + (head * a.G + row) * D + col;
           uint32_t w[JT];
 #pragma unroll
           for (int j = 0; j < JT; ++j)
