@@ -37,10 +37,11 @@
 // CTA's next segment too.
 //
 // Measured: 16 single tokens of 24 / 2 heads of 256 over 2048 .. 32768 cells 56 us for
-// 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 81 us for 224 MB.
-// The issue of instructions bounds it (about half of the slots are used; 57 % of
-// the instructions unpack), not the copies: one per tile instead of four, or deeper
-// rings, change nothing.
+// 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 80 us for 224 MB.
+// The chains of unpacking and products of the two or three warps per scheduler bound
+// it (about half of the issue slots are used), not the copies: one per tile instead of
+// four, or deeper rings, change nothing; eight warps on a tile, four per scheduler,
+// with 128 registers each take 64 and 104 us.
 #include <cstddef>
 
 #include "kv4_attention.cuh"

@@ -32,7 +32,7 @@
 //
 // Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 91 us (568
 // TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 90 us.  No unit is full
-// (issue 41 %, ALU 45 %, tensor pipe 27 %): a tile takes about 1900 cycles for its way
+// (issue 47 %, ALU 37 %, tensor pipe 36 %): a tile takes about 1900 cycles for its way
 // through eight barriers, and the first ones wait 12 us for the plan and Q.
 #include "kv4_attention.cuh"
 
