@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (lane == 0) mbar_arrive_expect_tx(&pfull[st], __popc(have >> (t * kGroups) & ((1u << kGroups) - 1)) * G::HALF);
         __syncwarp();
         if (lane_tile == t && from) bulk_g2s(ring + st * G::STAGE + lane_group * G::HALF, from, G::HALF, &pfull[st]);
-        if (g == NP - 1 && i == NP - 1) {
+        // (tiles of this part are still to come, so that it cannot end, and `qready` not
+        // go on to the next part's phase, before this warp has seen it)
+        if (g == NP - 1 && i == NP - 1 && i + 1 < p.n) {
           ok = __all_sync(0xffffffffu, kv4_wait(&qready, 0));
           if (lane_tile >= NP && from) bulk_prefetch_l2_plain(from, G::HALF);
         }
