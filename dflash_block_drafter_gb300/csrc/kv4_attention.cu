@@ -159,11 +159,12 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
   uint32_t fills = 0;  // tiles that the ring has taken in earlier segments
   bool ok = true, job = false;
 
-  // the lanes look up the pages of this warp's groups, 32 / MT tiles at a time
+  // the lanes look up the pages of this warp's groups, 32 / MT tiles at a time (groups
+  // that no row sees have no page: those before a window may have been given back)
   auto look_up = [&](const Kv4Part& p, int from) {
     const int i = from + lane / MT;
     const int pos = p.q.base + (p.k0 + i) * TILE + (warp * MT + lane % MT) * 16;
-    if (i >= p.n || pos >= p.q.hi) return -1;
+    if (i >= p.n || pos + 16 <= p.q.lo || pos >= p.q.hi) return -1;
     int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
     if (page < 0 || page >= a.n_pages) {
       set_status(a.status, DFLASH_DEV_CAPACITY);

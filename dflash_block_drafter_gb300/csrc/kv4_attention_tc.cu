@@ -268,14 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int groups_of_page = 1 << (a.page_shift - 4);
     uint32_t g = 0;  // tiles over all parts
     for (Kv4Part p = part_at(x_begin, none); p.n > 0 && ok; p = part_at(p.next, p)) {
-      // a lane holds the address of its group of its tile of WIN (0: nothing to copy),
-      // and that of the WIN tiles after them
+      // a lane holds the address of its group of its tile of WIN (0: nothing to copy, for
+      // groups that no row sees: those before a window may have been given back), and
+      // that of the WIN tiles after them
       constexpr int WIN = 32 / kGroups;
       const int lane_tile = lane / kGroups, lane_group = lane % kGroups;
       auto look_up = [&](int from) -> const uint8_t* {
         const int i = from + lane_tile;
         const int pos = p.q.base + (p.k0 + i) * kTile + lane_group * 16;
-        if (i >= p.n || pos >= p.q.hi) return nullptr;
+        if (i >= p.n || pos + 16 <= p.q.lo || pos >= p.q.hi) return nullptr;
         int page = a.table[static_cast<long long>(p.s) * a.table_stride + (pos >> a.page_shift)];
         if (page < 0 || page >= a.n_pages) {
           set_status(a.status, DFLASH_DEV_CAPACITY);

@@ -513,8 +513,9 @@ int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t
  * A row that sees no cell is written as zeros.  Rows of no sequence are left
  * as they were.  Scores, sums and O are FP32; the probabilities and V's values
  * are rounded to FP16, K's too where (n_q / n_kv) * max_rows > 32.  Cells that
- * no row sees may hold anything, pages behind the last cell of a sequence are
- * not looked up.
+ * no row sees may hold anything, and pages that hold none of the cells that a
+ * row sees are not looked up: behind the last cell of a sequence, and before its
+ * window, where a caller may have given them back.
  * DFLASH_DEV_BAD_BLOCK: offsets that descend, pass n_tokens or hold more than
  * max_rows rows (that sequence is skipped).  DFLASH_DEV_CAPACITY: a kv_len
  * beyond the table's width (clamped), a page id outside the cache.
