@@ -23,18 +23,18 @@
 // cells, turned into code - 8 (1024 + c, minus 1032) and multiplied by the
 // cells' scales in FP16: one rounding of 2^-11 at most relative to the value.
 // P goes through movmatrix from the accumulator layout to the B operand's and is
-// rounded to FP16 (2^-11 relative at most, 2^-25 absolute; the sums are FP32 of
-// the unrounded p).
+// rounded to FP16 (2^-11 relative at most, 2^-32 of the largest weight absolute; the
+// sums are FP32 of the unrounded p).
 //
 // Work: the 4 warps of a CTA take a tile of 128 cells together.  For S^T
 // each warp has its own 32 cells and all channels; P goes through shared memory; for
 // O^T each warp has its own quarter of the channels and all cells.  So O is 16
 // registers per 8 rows at most, two or three CTAs fit an SM, and a segment ends
-// without joining warps.  One barrier per tile orders P, the ring's stages and the vote on the maximum: scores are taken relative to a reference
-// that stays until some score passes it by 2^8 (P stays far inside FP16's
-// range), so that the first tile and few others pay for a rescaling.  Bulk copies of
-// whole groups (K, V and scales together) run one or two tiles ahead, into the
-// CTA's next segment too.
+// without joining warps.  One barrier per tile orders P, the ring's stages and the
+// vote on the maximum: the reference of a row's weights moves seldom (kKv4Slack), so
+// that the first tile and few others pay for a rescaling.
+// Bulk copies of whole groups (K, V and scales together) run one or two tiles ahead,
+// into the CTA's next segment too.
 //
 // Measured: 16 single tokens of 24 / 2 heads of 256 over 2048 .. 32768 cells 56 us for
 // 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 80 us for 224 MB.
@@ -52,7 +52,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kOverhead = 2;  // a segment's beginning and end, in tiles
-constexpr float kSlack = 8.f; // log2 units by which a score may pass the reference
 
 constexpr int kPlanBytes(int n_seq) { return (n_seq + 1) * 8; }
 
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
           float v = fmaxf(sc[0][n2][e], sc[0][n2][2 + e]);
 #pragma unroll
           for (int mt = 1; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n2][e], sc[mt][n2][2 + e]));
-          over |= v > m_ref[n2][e] + kSlack;
+          over |= v > m_ref[n2][e] + kKv4Slack;
         }
       uint8_t* pt = pf + (i & 1) * G::P;
       auto write_p = [&](float (&sum)[NT][2]) {
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
           for (int e = 0; e < 2; ++e) {
             float v = m_ref[n2][e];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v = fmaxf(v, s_max[w][n2 * 8 + 2 * t + e]);
+            for (int w = 0; w < kWarps; ++w) v = fmaxf(v, s_max[w][n2 * 8 + 2 * t + e] - kKv4Lift);
             const float alpha = v == -INFINITY ? 0.f : ex2_approx(m_ref[n2][e] - v);
             m_ref[n2][e] = v;
             l_run[n2][e] *= alpha;

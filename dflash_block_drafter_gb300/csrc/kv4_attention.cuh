@@ -74,6 +74,14 @@ struct Kv4Consts {
   }
 };
 
+// P is 2^(score - reference).  A row's reference is put kKv4Lift below its largest score so
+// far and stays until a score passes it by 2^kKv4Slack, so that few tiles pay for a
+// rescaling.  P up to 2^15 stays inside FP16's range, and at the lift a cell's weight is
+// off by FP16's smallest step (2^-25) only 2^-32 below the largest, so that a
+// long tail below one dominating cell keeps its sum (with the reference at the largest
+// score, 32767 cells 2^-25.5 below another were lost).
+constexpr float kKv4Slack = 15.f, kKv4Lift = 7.f;
+
 struct Kv4Job;
 
 struct Kv4AttnArgs {

@@ -25,10 +25,10 @@
 // The 8 channels of a code word lie in the order 0 4 1 5 2 6 3 7, in which
 // masking the word yields pairs: Q's columns are stored in the same order,
 // and O's are read back in it.
-// Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-25 absolute), Q by 2^-27 of a
-// row's largest value at most (BF16 rows are scaled by a power of two, FP16 exact); scores, sums and O in FP32.  Scores are taken
-// relative to a reference that moves only when a row passes it by 2^8; the two
-// softmax warps of a quarter of the rows hand it to each other tile by tile.
+// Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-32 of the row's largest weight
+// absolute), Q by 2^-27 of a row's largest value at most (BF16 rows are scaled by a
+// power of two, FP16 exact); scores, sums and O in FP32.  The two softmax warps of a
+// quarter of the rows hand a row's reference to each other tile by tile.
 //
 // Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 91 us (568
 // TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 90 us.  No unit is full
@@ -52,7 +52,6 @@ constexpr int kSoftRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(kThreads * 72 <= 65536 && kSoftThreads * kSoftRegs + 64 * kUnpackWarps * kUnpackRegs + 128 * kOtherRegs <= kThreads * 72,
               "the roles' registers come out of the launch's");
 constexpr int kTmemCols = 512;
-constexpr float kSlack = 8.f;   // log2 units by which a score may pass the reference
 
 template <int D>
 struct Geo {
@@ -514,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (g > 0) named_bar_sync(2 + 2 * q4 + b, 64);
         if (live) {
           const float was = i > 0 ? s_ref[m] : -INFINITY;
-          const bool over = mx > was + kSlack;
-          const float ref = over ? mx : was;
+          const bool over = mx > was + kKv4Slack;
+          const float ref = over ? mx - kKv4Lift : was;
           if (i == 0 || __any_sync(0xffffffffu, over)) {
             s_ref[m] = ref;
             if (i > 0) {

@@ -26,3 +26,44 @@ def test_window_with_pages_given_back(R, d, heads, G, page, window, causal):
         table[s, : first // page] = -1
     assert (table[0, 0] == -1) and (table[3, 0] == -1)
     check_attn(R, case, causal, window)
+
+
+# -------------------------------------------------------------- values, weights
+def integer_cells(R, k, v, page):
+    """A cache whose cells 0 .. n - 1 (in order, one kv head) hold the integers k, v [n, d] exactly, one for all of its heads: values of
+    -8 .. 7 with a -8 in each block of 32 channels, whose scale then is 1."""
+    n, d = k.shape
+    cache = R.kv4_cache(-(-n // page), page, 1, d)
+    R.kv4_write(cache, *(torch.as_tensor(x, device="cuda").half()[:, None] for x in (k, v)), ints(np.arange(n)))
+    back = R.kv4_read(cache, ints(np.arange(n)))
+    assert all(np.array_equal(b[:, 0].cpu().numpy(), x) for b, x in zip(back, (k, v)))
+    return cache
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G,rows", [(4, 2), (5, 8)])  # the warp-level and the tcgen05 kernel
+@pytest.mark.parametrize("below", [24.5, 25.5, 20.25])
+def test_long_tail_below_one_cell(R, d, G, rows, below):
+    """One cell outweighs each of 32767 others by 2^below, and the others alone make the output: their sum must not be lost in
+    P's smallest step.  So many sequences (over the same pages) that segments are hardly split."""
+    n, page, n_seq = 32768, 64, 512
+    k, v = np.zeros((n, d)), np.full((n, d), 4.0)
+    k[:, 31::32] = v[:, 31::32] = -8
+    k[0, 0], v[0, :] = 7, 0
+    v[0, 31::32] = -8
+    cache = integer_cells(R, k, v, page)
+    q = torch.zeros((n_seq * rows, G, d), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1
+    st = status()
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").repeat(n_seq, 1)
+    out = R.kv4_attention(cache, q, table, ints(np.full(n_seq, n)), ints(np.arange(n_seq + 1) * rows), rows, causal=False,
+                          scale=below * np.log(2) / 7, status=st).double().cpu().numpy()
+    tail = 4 * (n - 1) * 2.0 ** -below
+    want = np.where(np.arange(d) % 32 == 31, -8.0, tail / (1 + tail / 4))
+    # a weight to FP16: half of its smallest step, 2^-25 of 2^7 at the reference, a cell (or 2^-11 of it); the power of two and the
+    # score in FP32: 2^-21 of the weight; the sum of n terms in FP32, 16 a step; the output to FP16
+    tol = 4 * n * 2.0 ** -32 + tail * (2.0 ** -11 + 2.0 ** -21 + n / 16 * 2.0 ** -23) + np.abs(want) * 2.0 ** -11
+    tol = np.where(np.arange(d) % 32 == 31, 8 * (2.0 ** -11 + n / 16 * 2.0 ** -23) + 8 * 2.0 ** -11, tol)
+    assert int(st) == 0
+    worst = np.max(np.abs(out - want) / tol)
+    assert worst <= 1, worst
