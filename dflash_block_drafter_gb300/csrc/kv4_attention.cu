@@ -14,11 +14,13 @@
 // already a pair of FP16 numbers: a code c in the low bits of an FP16 pattern
 // is the subnormal c 2^-24, which the tensor cores take exactly (c 2^-20 for
 // the mask 0x00f000f0), so unpacking K is 4 ANDs and a shift per word.  Q
-// carries the other factor (FP16 rows scaled by a power of two, so nothing of
-// BF16 is lost), and a block's scale multiplies the finished FP32 sum of its 32
+// carries the other factor: FP16 rows scaled by the power of two that brings their
+// largest value into [2^15, 2^16), so that a value is off by 2^-36 of the row's
+// largest at most.  A block's scale multiplies the finished FP32 sum of its 32
 // channels.  The -8 of the codes is one more product, of a cell's scales with -8
-// times the blocks' sums of q, each held as two FP16 terms (22 bits).  K itself
-// enters the scores without any rounding.
+// times the blocks' sums of q, each held as two FP16 terms: 22 bits, or as many as
+// FP16's smallest step leaves, 2^-19 of the row's largest value.  K itself enters the
+// scores without any rounding.
 // O^T = V^T P^T.  Two cells' words are interleaved (prmt) into pairs along the
 // cells, turned into code - 8 (1024 + c, minus 1032) and multiplied by the
 // cells' scales in FP16: one rounding of 2^-11 at most relative to the value.
@@ -241,9 +243,10 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       }
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // power of two that brings the row's maximum into [2^12, 2^13)
+      // power of two that brings the row's maximum into [2^15, 2^16) (a BF16 or FP16 value's
+      // bits reach FP16's largest there, 65504, and do not pass it)
       const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-      const int up = top > 0.f ? min(12 + 127 - ex, 120) : 0;
+      const int up = top > 0.f ? min(15 + 127 - ex, 120) : 0;
       auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
       const float f = power(up);
       if (part == 0) {

@@ -67,3 +67,25 @@ def test_long_tail_below_one_cell(R, d, G, rows, below):
     assert int(st) == 0
     worst = np.max(np.abs(out - want) / tol)
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("G,rows", [(3, 1), (4, 8), (5, 8)])
+def test_small_part_of_a_query(R, d, kind, G, rows):
+    """A query with one large and one small value, over cells whose values there are zeros with a large scale: all scores are 0."""
+    k, v = np.zeros((2, d)), np.ones((2, d))
+    v[1], v[:, 31::32] = -1, -8
+    cache = integer_cells(R, np.where(np.arange(d) % 32 == 31, -8.0, k), v, 16)
+    wide = np.zeros((2, 1, d))
+    wide[0, 0, 31::32] = -512  # cell 0: scale 64; cell 1: no scale
+    R.kv4_write(cache, torch.as_tensor(wide, device="cuda").half(), torch.as_tensor(v, device="cuda").half()[:, None], ints([0, 1]))
+    q = torch.zeros((rows, G, d), dtype=TYPES[kind], device="cuda")
+    q[:, :, 0::32], q[:, :, 2::32] = 1, 2.0 ** -16
+    st = status()
+    out = R.kv4_attention(cache, q, ints([[0]]), ints([2]), ints([0, rows]), rows, causal=False, scale=16.0, status=st).double().cpu().numpy()
+    # the sum of a block of q is off by 2^-19 of the row's largest, 1; with the scale 64 and the codes' 8 a score is off by 2^-10 a
+    # block, times 16; two weights that should be equal give half of that; each to FP16: 2^-11
+    tol = d / 32 * 2.0 ** -7 + 2.0 ** -10
+    assert int(st) == 0
+    assert np.abs(out[..., :31]).max() <= tol, np.abs(out[..., :31]).max()
