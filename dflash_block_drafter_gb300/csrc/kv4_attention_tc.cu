@@ -439,11 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
                 auto pair = [&](uint32_t lo, uint32_t hi) { return pack_f16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f); };
                 w[4 * k] = pair(r.x << 16, r.z << 16), w[4 * k + 1] = pair(r.x & 0xffff0000u, r.z & 0xffff0000u);
                 w[4 * k + 2] = pair(r.y << 16, r.w << 16), w[4 * k + 3] = pair(r.y & 0xffff0000u, r.w & 0xffff0000u);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu), __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu)));
               } else {
                 w[4 * k] = prmt(r.x, r.z, 0x5410u), w[4 * k + 1] = prmt(r.x, r.z, 0x7632u);
                 w[4 * k + 2] = prmt(r.y, r.w, 0x5410u), w[4 * k + 3] = prmt(r.y, r.w, 0x7632u);
               }
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu), __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu)));
             }
             if (cs * (D / 2) < G::QT) {
               tmem_st16(lane_addr + G::Q_COL + (cs * (D / 2) + e) / 2, w);
@@ -456,6 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           }
           tmem_wait_st();
         }
+        // A row with an infinity or a NaN is reported here already: below, where the sum of its
+        // weights shows them, a score of -infinity passes for a cell that the row does not see.
+        if (!again && max(top & 0xffffu, top >> 16) >= (a.bf16 ? 0x7f80u : 0x7c00u)) set_status(a.status, DFLASH_DEV_NONFINITE);
         if (again || !a.bf16) break;
         red_sum[cs * R + m] = __uint_as_float(top);
         named_bar_sync(1, kSoftThreads);

@@ -89,3 +89,29 @@ def test_small_part_of_a_query(R, d, kind, G, rows):
     tol = d / 32 * 2.0 ** -7 + 2.0 ** -10
     assert int(st) == 0
     assert np.abs(out[..., :31]).max() <= tol, np.abs(out[..., :31]).max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("G,rows", [(4, 8), (5, 8)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("channel", [0, -2])
+def test_queries_that_are_not_finite(R, d, kind, G, rows, bad, channel):
+    """An infinity or a NaN in a row's query is reported, also where it makes all of the scores -infinity; other rows keep theirs."""
+    k, v = np.full((90, d), 3.0), np.ones((90, d))
+    k[:, 31::32] = v[:, 31::32] = -8
+    cache = integer_cells(R, k, v, 16)
+    q = torch.ones((rows, G, d), dtype=TYPES[kind], device="cuda")
+
+    def call(q):
+        st = status()
+        return R.kv4_attention(cache, q, ints([np.arange(6)]), ints([90]), ints([0, rows]), rows, causal=False, status=st), int(st)
+
+    want, st = call(q)
+    assert st == 0
+    q[1, 2, channel] = bad
+    got, st = call(q)
+    assert st == D.DFLASH_DEV_NONFINITE
+    others = torch.ones((rows, G), dtype=torch.bool, device="cuda")
+    others[1, 2] = False
+    assert torch.equal(got[others], want[others])
