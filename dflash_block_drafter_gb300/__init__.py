@@ -343,11 +343,19 @@ def dflash_state_set_attn_chunks(state: int, chunks: int = 0) -> int:
 
 
 # -------------------------------------------------------------- verify step
+# (ctypes cuts an int to the 32 bits of a C argument: sizes beyond them are refused here.)
+def _refuse_wide(what: str, *sizes: int) -> None:
+    if not all(-2 ** 31 <= n < 2 ** 31 for n in sizes):
+        raise DflashError(DFLASH_ERR_INVALID_ARG, what + ": sizes are 32-bit")
+
+
 def dflash_kv4_check(cache: DflashKv4Cache) -> int:
     return load_library().dflash_kv4_check(ctypes.byref(cache))
 
 
 def dflash_kv4_bytes(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    if (n_pages | page_size | n_kv_heads | head_dim) >> 31:
+        return 0
     return load_library().dflash_kv4_bytes(n_pages, page_size, n_kv_heads, head_dim)
 
 
@@ -355,6 +363,8 @@ def dflash_page_tables(lengths: int, new_rows: int, n_seq: int, page_size: int, 
                        held_out: int, table: int, table_stride: int, ring: int, ring_in: int, ring_out: int,
                        row_offsets: int, slots: int, positions: int, row_cap: int, dev_status: int = 0,
                        stream: int = 0) -> None:
+    if (n_seq | page_size | n_pages | table_stride | row_cap) >> 31:  # negative or wide
+        _refuse_wide("dflash_page_tables", n_seq, page_size, n_pages, table_stride, row_cap)
     _check(load_library().dflash_page_tables(lengths, new_rows, n_seq, page_size, n_pages, held_in, held_out, table,
                                              table_stride, ring, ring_in, ring_out, row_offsets, slots or None,
                                              positions or None, row_cap, dev_status or None, stream or None),
@@ -363,12 +373,16 @@ def dflash_page_tables(lengths: int, new_rows: int, n_seq: int, page_size: int, 
 
 def dflash_kv4_write(cache: DflashKv4Cache, k: int, v: int, value_type: int, k_stride: int, v_stride: int, slots: int,
                      n_rows: int, dev_status: int = 0, stream: int = 0) -> None:
+    if (n_rows) >> 31:  # negative or wide
+        _refuse_wide("dflash_kv4_write", n_rows)
     _check(load_library().dflash_kv4_write(ctypes.byref(cache), k, v, value_type, k_stride, v_stride, slots, n_rows,
                                            dev_status or None, stream or None), "dflash_kv4_write")
 
 
 def dflash_kv4_read(cache: DflashKv4Cache, slots: int, n_rows: int, k_out: int, v_out: int, dev_status: int = 0,
                     stream: int = 0) -> None:
+    if (n_rows) >> 31:  # negative or wide
+        _refuse_wide("dflash_kv4_read", n_rows)
     _check(load_library().dflash_kv4_read(ctypes.byref(cache), slots, n_rows, k_out or None, v_out or None,
                                           dev_status or None, stream or None), "dflash_kv4_read")
 
@@ -377,6 +391,8 @@ def dflash_kv4_attention(cache: DflashKv4Cache, q: int, out: int, value_type: in
                          n_tokens: int, n_q_heads: int, n_seq: int, max_rows: int, row_offsets: int, kv_len: int,
                          table: int, table_stride: int, causal: bool, window: int, scale: float, workspace: int,
                          workspace_bytes: int, dev_status: int = 0, stream: int = 0) -> None:
+    if (n_tokens | n_q_heads | n_seq | max_rows | table_stride | window) >> 31:  # negative or wide
+        _refuse_wide("dflash_kv4_attention", n_tokens, n_q_heads, n_seq, max_rows, table_stride, window)
     _check(load_library().dflash_kv4_attention(ctypes.byref(cache), q, out, value_type, q_stride, out_stride, n_tokens,
                                                n_q_heads, n_seq, max_rows, row_offsets, kv_len, table, table_stride,
                                                1 if causal else 0, window, scale, workspace, workspace_bytes,
@@ -385,12 +401,16 @@ def dflash_kv4_attention(cache: DflashKv4Cache, q: int, out: int, value_type: in
 
 def dflash_kv4_attention_workspace(cache: DflashKv4Cache, n_q_heads: int, n_seq: int, max_rows: int,
                                    table_stride: int) -> int:
+    if (n_q_heads | n_seq | max_rows | table_stride) >> 31:
+        return 0
     return load_library().dflash_kv4_attention_workspace(ctypes.byref(cache), n_q_heads, n_seq, max_rows, table_stride)
 
 
 def dflash_token_logprobs(logits: int, value_type: int, row_stride: int, n_rows: int, vocab: int, tokens: int,
                           logprob: int, entropy: int, top_k: int, top_ids: int, top_logprobs: int, dev_status: int = 0,
                           stream: int = 0) -> None:
+    if (n_rows | vocab | top_k) >> 31:  # negative or wide
+        _refuse_wide("dflash_token_logprobs", n_rows, vocab, top_k)
     _check(load_library().dflash_token_logprobs(logits, value_type, row_stride, n_rows, vocab, tokens or None,
                                                 logprob or None, entropy or None, top_k, top_ids or None,
                                                 top_logprobs or None, dev_status or None, stream or None),

@@ -1,0 +1,37 @@
+"""Host-side checks of the verify-step operators beyond their plain refusals: sizes of more than 32 bits.  No GPU is used."""
+import pytest
+
+import dflash_block_drafter_gb300 as D
+from test_verify_host import _cache, lib  # noqa: F401
+
+WIDE = 2 ** 32  # a size that 32 bits would cut to 0
+FAR = 4096      # an address that is never read: the calls are refused before anything is enqueued
+
+
+@pytest.mark.parametrize("size", [WIDE, WIDE + 8, 2 ** 31, -WIDE + 8])
+def test_sizes_beyond_32_bits(lib, size):  # noqa: F811
+    c = _cache()
+
+    def pages(n_seq=1, page=16, n_pages=8, width=4, cap=8):
+        D.dflash_page_tables(FAR, FAR, n_seq, page, n_pages, FAR, FAR, FAR, width, FAR, FAR, FAR, FAR, FAR, 0, cap)
+
+    def attention(tokens=1, nq=8, n_seq=1, rows=1, width=4, window=0):
+        D.dflash_kv4_attention(c, FAR, FAR, D.DFLASH_T_BF16, 1024, 1024, tokens, nq, n_seq, rows, FAR, FAR, FAR, width, True, window, 1.0, FAR,
+                               1 << 30)
+
+    calls = [lambda: pages(n_seq=size), lambda: pages(page=size), lambda: pages(n_pages=size), lambda: pages(width=size),
+             lambda: pages(cap=size), lambda: attention(tokens=size), lambda: attention(nq=size), lambda: attention(n_seq=size),
+             lambda: attention(rows=size), lambda: attention(width=size), lambda: attention(window=size),
+             lambda: D.dflash_kv4_write(c, FAR, FAR, D.DFLASH_T_BF16, 256, 256, FAR, size),
+             lambda: D.dflash_kv4_read(c, FAR, size, FAR, FAR),
+             lambda: D.dflash_token_logprobs(FAR, D.DFLASH_T_BF16, WIDE * 2, size, 8, 0, 0, FAR, 0, 0, 0),
+             lambda: D.dflash_token_logprobs(FAR, D.DFLASH_T_BF16, WIDE * 2, 1, size, 0, 0, FAR, 0, 0, 0),
+             lambda: D.dflash_token_logprobs(FAR, D.DFLASH_T_BF16, WIDE * 2, 1, 8, 0, 0, FAR, size, FAR, FAR)]
+    for i, call in enumerate(calls):
+        with pytest.raises(D.DflashError) as e:
+            call()
+        assert e.value.status == D.DFLASH_ERR_INVALID_ARG, i
+    for kw in ("n_pages", "page_size", "n_kv_heads", "head_dim"):
+        assert D.dflash_kv4_bytes(**{**dict(n_pages=8, page_size=64, n_kv_heads=2, head_dim=128), kw: size}) == 0
+    for kw in ("n_q_heads", "n_seq", "max_rows", "table_stride"):
+        assert D.dflash_kv4_attention_workspace(c, **{**dict(n_q_heads=8, n_seq=1, max_rows=1, table_stride=4), kw: size}) == 0
