@@ -726,7 +726,8 @@ int dflash_kv4_attention(const dflash_kv4_cache* c, const void* q, void* out, in
   if (const int e = check_call(c, n_q_heads, n_seq, max_rows, table_stride)) return e;
   if (type != DFLASH_T_BF16 && type != DFLASH_T_FP16) return DFLASH_ERR_UNSUPPORTED;
   const int64_t width = static_cast<int64_t>(n_q_heads) * c->head_dim;
-  if (n_tokens < 0 || window < 0 || !(scale > 0.f) || !(scale < INFINITY)) return DFLASH_ERR_INVALID_ARG;
+  // (2^127: its product with log2(e) is still finite)
+  if (n_tokens < 0 || window < 0 || !(scale > 0.f) || !(scale <= 0x1p127f)) return DFLASH_ERR_INVALID_ARG;
   if (!row_offsets || !kv_len || !table) return DFLASH_ERR_INVALID_ARG;
   if (n_tokens == 0) return DFLASH_OK;
   if (!q || !out || reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16 || q_stride < width ||

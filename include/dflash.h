@@ -509,7 +509,7 @@ int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t
  *   table:  [n_seq, table_stride] int32, page ids.
  *   causal: non-zero: a row sees the positions up to its own; zero: all
  *           kv_len.  window W > 0: of those only the W last.
- *   scale:  the softmax scale, finite and positive.
+ *   scale:  the softmax scale, positive and at most 2^127.
  * A row that sees no cell is written as zeros.  Rows of no sequence are left
  * as they were.  Scores, sums and O are FP32; the probabilities and V's values
  * are rounded to FP16, K's too where (n_q / n_kv) * max_rows > 32.  Cells that

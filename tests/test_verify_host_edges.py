@@ -1,4 +1,7 @@
-"""Host-side checks of the verify-step operators beyond their plain refusals: sizes of more than 32 bits.  No GPU is used."""
+"""Host-side checks of the verify-step operators beyond their plain refusals: sizes of more than 32 bits, the largest softmax
+scale.  No GPU is used."""
+import ctypes
+
 import pytest
 
 import dflash_block_drafter_gb300 as D
@@ -35,3 +38,16 @@ def test_sizes_beyond_32_bits(lib, size):  # noqa: F811
         assert D.dflash_kv4_bytes(**{**dict(n_pages=8, page_size=64, n_kv_heads=2, head_dim=128), kw: size}) == 0
     for kw in ("n_q_heads", "n_seq", "max_rows", "table_stride"):
         assert D.dflash_kv4_attention_workspace(c, **{**dict(n_q_heads=8, n_seq=1, max_rows=1, table_stride=4), kw: size}) == 0
+
+
+def test_largest_scale(lib):  # noqa: F811
+    """A scale whose product with log2(e) is infinite in FP32 would give every row the largest factor there is."""
+    c, far = _cache(), ctypes.c_void_p(FAR)
+
+    def call(scale):
+        return lib.dflash_kv4_attention(ctypes.byref(c), far, far, D.DFLASH_T_BF16, 1024, 1024, 0, 8, 1, 1, far, far, far, 4, 1, 0, scale,
+                                        None, 0, None, None)
+
+    assert call(2.0 ** 127) == D.DFLASH_OK  # no tokens: nothing to do
+    for scale in (2.0 ** 127 * (1 + 2.0 ** -20), 3e38):
+        assert call(scale) == D.DFLASH_ERR_INVALID_ARG
