@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageArgs a)
       v[2] = max(q.held - q.need, 0);
       s_len[s] = a.lengths[s];
       s_held[s] = q.fits ? q.held : ~q.held;
-      if (rank == 0 && q.valid && !q.fits) set_status(a.status, DFLASH_DEV_CAPACITY);
+      if (rank == 0 && ((q.valid && !q.fits) || q.held != a.held_in[s])) set_status(a.status, DFLASH_DEV_CAPACITY);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)

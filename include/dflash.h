@@ -465,8 +465,9 @@ size_t dflash_kv4_bytes(int32_t n_pages, int32_t page_size, int32_t n_kv_heads, 
  * later one that lacks any get none, keep what they held, and their rows have
  * slot -1; the same holds for a request whose pages do not fit table_stride:
  * DFLASH_DEV_CAPACITY.  The same bit reports more rows than row_cap (those
- * beyond are dropped), a page id outside [0, n_pages) (slot -1), a ring head or
- * count out of range, and more pages given back than the ring has room for.
+ * beyond are dropped), a page id outside [0, n_pages) (slot -1), a held_in
+ * outside [0, table_stride] (taken as the nearer end), a ring head or count out
+ * of range, and more pages given back than the ring has room for.
  * held_out may be held_in and ring_out may be ring_in; no other arrays may
  * overlap.  n_seq <= 4096 and n_seq * table_stride < 2^31 - 1 (else
  * DFLASH_ERR_CAPACITY).  One launch. */

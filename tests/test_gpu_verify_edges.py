@@ -115,3 +115,20 @@ def test_queries_that_are_not_finite(R, d, kind, G, rows, bad, channel):
     others = torch.ones((rows, G), dtype=torch.bool, device="cuda")
     others[1, 2] = False
     assert torch.equal(got[others], want[others])
+
+
+# --------------------------------------------------------------- page tables
+@pytest.mark.parametrize("held,nearest", [([-1, 1, 1], [0, 1, 1]), ([1, 5, 1], [1, 4, 1]), ([1, 1, 2 ** 31 - 1], [1, 1, 4]),
+                                          ([1, 1, -(2 ** 31)], [1, 1, 0])])
+@pytest.mark.parametrize("lengths", [[3, 60, 0], [3, 60, -1]])
+def test_held_out_of_range(R, held, nearest, lengths):
+    """A count of pages that no table row can hold is reported; the call goes on as with the nearer end."""
+    def call(h):
+        table, ring, st = ints(np.arange(12).reshape(3, 4)), ints(np.arange(12, 24).tolist() + [-1] * 12), status()
+        h, rs = ints(h), ints([0, 12])
+        out = R.page_tables(ints(lengths), ints([2, 2, 0]), h, table, ring, rs, 16, 8, status=st)
+        return int(st), [x.tolist() for x in (h, table, ring, rs, *out)]
+
+    st, got = call(held)
+    assert st == D.DFLASH_DEV_CAPACITY
+    assert call(nearest) == (0, got)
