@@ -59,7 +59,7 @@ constexpr int kPlanBytes(int n_seq) { return (n_seq + 1) * 8; }
 
 template <int D, int NT>
 struct Geo {
-  static constexpr int R = 8 * NT;                 // rows of a row group
+  static constexpr int R = 8 * NT;                 // query rows of a segment, at most
   static constexpr int MT = 2;                     // 16-cell groups of a warp in a tile
   static constexpr int GROUPS = kWarps * MT;
   static constexpr int TILE = 16 * GROUPS;         // cells of a tile
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
     for (int i = 0; i < ST; ++i) mbar_init(&full[i], kWarps);
     fence_barrier_init();
   }
-  const long long T = kv4_plan<TILE, R, kOverhead>(a, pre, scratch, blockIdx.x == 0);
+  const long long T = kv4_plan<TILE, kOverhead>(a, pre, scratch, blockIdx.x == 0);
   const int C = kv4_ctas(T, gridDim.x);
   const int c = blockIdx.x;
   pdl_launch_dependents();
@@ -196,17 +196,17 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
     }
   };
 
-  Kv4Part cur = kv4_part<TILE, R, kOverhead>(a, pre, kv4_start(T, C, c), x_end, Kv4Part{});
+  Kv4Part cur = kv4_part<TILE, kOverhead>(a, pre, kv4_start(T, C, c), x_end, Kv4Part{});
   int pages = look_up(cur, 0);
   int issued = 0;  // tiles of the current part that are on their way
   for (; issued < min(cur.n, ST); ++issued) issue(cur, issued, issued, pages);
   while (cur.n > 0) {
     const Kv4Seq q = cur.q;
-    const int k0 = cur.k0, k1 = cur.k0 + cur.n, head = cur.head, row0 = cur.row0;
+    const int k0 = cur.k0, k1 = cur.k0 + cur.n, head = cur.head;
     const int n_rows = cur.rows;
     const int n = ok ? cur.n : 0;  // tiles
     // the next part's first tiles follow this one's last without a gap
-    const Kv4Part next = kv4_part<TILE, R, kOverhead>(a, pre, cur.next, x_end, cur);
+    const Kv4Part next = kv4_part<TILE, kOverhead>(a, pre, cur.next, x_end, cur);
     int next_pages = look_up(next, 0);
     int next_issued = 0;
     __syncthreads();  // the last segment is done with Q and P
@@ -217,9 +217,8 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       const int part = tid & 7;
       float v[E];
       float top = 0.f;
-      const int row = row0 + m;
       if (m < n_rows) {
-        const uint16_t* src = a.q + q.r0 * a.q_stride + kv4_token(row, per_g) * (a.q_stride - a.G * D) + (head * a.G + row) * D + part * E;
+        const uint16_t* src = a.q + q.r0 * a.q_stride + kv4_token(m, per_g) * (a.q_stride - a.G * D) + (head * a.G + m) * D + part * E;
 #pragma unroll
         for (int e = 0; e < E; e += 8) {
           const uint4 raw = *reinterpret_cast<const uint4*>(src + e);
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
       if (part == 0) {
         // (beyond 2^100 any two scores that differ are too far apart to share weight)
         s_factor[m] = fminf(a.scale_log2 * power(-up) * 0x1p24f, 0x1p100f);
-        s_sees[m] = m < n_rows ? kv4_sees(a, q, kv4_token(row, per_g)) : make_int2(0, 0);
+        s_sees[m] = m < n_rows ? kv4_sees(a, q, kv4_token(m, per_g)) : make_int2(0, 0);
       }
       // element e of block b, quad tt: word 4b + tt, nibble e; even nibbles as
       // they are, odd ones / 16 (their codes are 16 times as large)
@@ -572,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
         if (whole) {
           f = l > 0.f ? 1.f / l : 0.f;
           if (!(l < INFINITY)) set_status(a.status, DFLASH_DEV_NONFINITE);
-          const int row = row0 + m;
-          uint16_t* dst = a.out + q.r0 * a.out_stride + kv4_token(row, per_g) * (a.out_stride - a.G * D) + (head * a.G + row) * D + col;
+          uint16_t* dst = a.out + q.r0 * a.out_stride + kv4_token(m, per_g) * (a.out_stride - a.G * D) + (head * a.G + m) * D + col;
           uint32_t w[JT];
 #pragma unroll
           for (int j = 0; j < JT; ++j)
@@ -591,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
     if (!whole && k0 == 0) {  // the segment goes on in the next CTAs
       job = true;
       if (tid == 0) {
-        Kv4Job r{q.r0, row0, head, n_rows, kv4_owner(T, C, cur.end - 1), {0, 0, 0}};
-        a.jobs[c] = r;
+        a.jobs[c] = Kv4Job{q.r0, head, n_rows, kv4_owner(T, C, cur.end - 1)};
       }
     }
     cur = next;
@@ -632,18 +629,17 @@ int smem_of(int d, int nt) {
   return 0;
 }
 
-// What the host knows of a call: 8-row tiles of a row group, CTAs and
-// segments at most.
+// What the host knows of a call: its kernel, CTAs and split segments at most.
 struct Shape {
-  bool tc;    // the tcgen05 kernel: row groups of 128
-  int nt;     // else: 8-row tiles of a row group
+  bool tc;    // the tcgen05 kernel: up to 128 query rows a segment
+  int nt;     // else: 8-row tiles of them
   int most, jobs;
-  int rows_of_group() const { return tc ? 128 : 8 * nt; }
+  int rows() const { return tc ? 128 : 8 * nt; }
 };
 // More rows per kv head than this go to the tcgen05 kernel.  Measured on 16
 // sequences of 2048 .. 32768 cells, 2 kv heads of 256 (64 of 512 .. 8192, 8 of 128):
 // 12 rows 56 us here, 100 there; 24 rows 81 and 103 (165 and 256); 32 rows 88 and
-// 105 (226 and 255); beyond, this kernel unpacks every cell once per 32 rows.
+// 105 (226 and 255); beyond, a kernel of this kind would unpack every cell once per 32 rows.
 constexpr int kTcRows = 32;
 cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Shape* out) {
   int dev = 0, sms = 0;
@@ -661,11 +657,9 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
     out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
     return cudaSuccess;
   }
-  // as few row groups as 32 rows allow, each no wider than it needs
-  const int groups = (rows + 31) / 32;
-  out->nt = ((rows + groups - 1) / groups + 7) / 8;
+  out->nt = (rows + 7) / 8;
   const int tile = 128;
-  const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads * groups;
+  const long long segments = static_cast<long long>(n_seq) * c->n_kv_heads;
   // (a window may begin anywhere in a tile)
   const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
   const long long ctas = segments * (tiles + kOverhead);
@@ -689,7 +683,7 @@ int check_call(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows
 }
 
 size_t bytes_of(const dflash_kv4_cache* c, const Shape& s) {
-  return s.most * (sizeof(Kv4Job) + 2 * size_t(s.rows_of_group()) * (c->head_dim * 4 + 8));
+  return s.most * (sizeof(Kv4Job) + 2 * size_t(s.rows()) * (c->head_dim * 4 + 8));
 }
 
 template <int D>
@@ -761,7 +755,7 @@ int dflash_kv4_attention(const dflash_kv4_cache* c, const void* q, void* out, in
   a.scale_log2 = scale * 1.4426950408889634f;
   a.jobs = static_cast<Kv4Job*>(workspace);
   a.part = reinterpret_cast<float*>(a.jobs + s.most);
-  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * s.rows_of_group() * c->head_dim);
+  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * s.rows() * c->head_dim);
   a.status = dev_status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (s.tc) {

@@ -2,9 +2,9 @@
 // that shares a call's work out over CTAs, and the merge of split segments.
 //
 // A sequence s with r rows over kv cells has, per kv head, G * r query rows
-// (row m = token m / G, head of the group m % G) which read the same cells.
-// They are cut into row groups of R rows; (sequence, kv head, row group) is
-// a segment.  A segment walks its visible cells in steps.  It counts as its
+// (row m = token m / G, head of the group m % G) which read the same cells: a
+// segment.  They are at most as many as a CTA takes, R (the host picks the kernel and
+// its R by G * max_rows).  A segment walks its visible cells in steps.  It counts as its
 // steps plus OV units, which stand for what it costs to begin and to end one;
 // all segments' units laid end to end are shared out evenly over C CTAs, so that
 // every CTA has about the same work whatever the lengths (counted by steps
@@ -109,10 +109,10 @@ struct Kv4Seq {
   int r0, rows, kv;  // first token, tokens, cells
   int base, hi;      // visible cells [lo, hi) of any row, base = lo down to a step
   int lo;
-  int steps, groups;
+  int steps;
 };
 
-template <int STEP, int R>
+template <int STEP>
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool report) {
   Kv4Seq q;
   q.r0 = a.row_offsets[s];
@@ -138,11 +138,10 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool repo
   q.base = q.lo - q.lo % STEP;
   // rows that see no cell take one masked step, which writes their zeros
   q.steps = q.rows == 0 ? 0 : max((q.hi - q.base + STEP - 1) / STEP, 1);
-  q.groups = (q.rows * a.G + R - 1) / R;
   return q;
 }
 
-// The token x / G of a query row x < 1024: x * ceil(2^17 / G) >> 17 (off by less than
+// The token x / G of a query row x < 128: x * ceil(2^17 / G) >> 17 (off by less than
 // x G / 2^17 / G, below the 1 / G that a quotient lies from the next integer).
 __device__ __forceinline__ uint32_t kv4_per_token(int G) { return ((1u << 17) + G - 1) / G; }
 __device__ __forceinline__ int kv4_token(int x, uint32_t per_g) { return static_cast<int>(static_cast<uint32_t>(x) * per_g >> 17); }
@@ -153,9 +152,9 @@ __device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, 
   return make_int2(a.window > 0 && upto > a.window ? upto - a.window : 0, max(upto, 0));
 }
 
-// Prefix sums of the sequences' units (over kv heads and row groups) in
+// Prefix sums of the sequences' units (over kv heads) in
 // `pre` [n_seq + 1] by the whole CTA; returns the total.
-template <int STEP, int R, int OV>
+template <int STEP, int OV>
 __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* pre, long long* scratch, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
   long long carry = 0;
@@ -163,8 +162,8 @@ __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* p
     const int s = s0 + tid;
     long long v = 0;
     if (s < a.n_seq) {
-      const Kv4Seq q = kv4_seq<STEP, R>(a, s, report);
-      if (q.rows > 0) v = static_cast<long long>(q.steps + OV) * q.groups * a.n_kv;
+      const Kv4Seq q = kv4_seq<STEP>(a, s, report);
+      if (q.rows > 0) v = static_cast<long long>(q.steps + OV) * a.n_kv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,15 +196,15 @@ __device__ __forceinline__ int kv4_owner(long long T, int C, long long x) {
   return c;
 }
 
-// A segment's part in a CTA: tiles [k0, k0 + n) of a sequence, kv head and
-// row group (n 0: no more parts).
+// A segment's part in a CTA: tiles [k0, k0 + n) of a sequence and kv head (n 0: no
+// more parts).
 struct Kv4Part {
   Kv4Seq q;
-  int s, head, row0, rows, k0, n;
+  int s, head, rows, k0, n;  // rows: query rows
   long long end, next;  // units: the segment's end; where this part ends
 };
 // The first part with a tile in [at, x_end); `hint` is the part before it (or a zeroed one).
-template <int STEP, int R, int OV>
+template <int STEP, int OV>
 __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long long* pre, long long at, long long x_end,
                                             const Kv4Part& hint) {
   Kv4Part p = hint;
@@ -226,20 +225,19 @@ __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long lon
         s = lo;
       }
       p.s = s;
-      p.q = kv4_seq<STEP, R>(a, s, false);
+      p.q = kv4_seq<STEP>(a, s, false);
     }
     const int units = p.q.steps + OV;
     const long long rel = at - pre[s];
-    const int seg = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
-    const long long begin = pre[s] + static_cast<long long>(seg) * units;
+    const int head = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
+    const long long begin = pre[s] + static_cast<long long>(head) * units;
     p.end = begin + units;
     p.next = p.end < x_end ? p.end : x_end;
     p.k0 = max(static_cast<int>(at - begin) - OV, 0);
     p.n = max(static_cast<int>(p.next - begin) - OV, 0) - p.k0;
     if (p.n > 0) {
-      p.head = seg / p.q.groups;
-      p.row0 = (seg - p.head * p.q.groups) * R;
-      p.rows = min(R, p.q.rows * a.G - p.row0);
+      p.head = head;
+      p.rows = p.q.rows * a.G;
       break;
     }
     at = p.next;
@@ -249,8 +247,8 @@ __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long lon
 
 // What a split segment's first CTA leaves for the merge kernel.
 struct Kv4Job {
-  int r0, row0, head, n_rows;  // n_rows 0: no segment that goes on begins in this CTA
-  int last, pad[3];            // CTA of the last piece; the others lie between
+  int r0, head, n_rows;  // n_rows 0: no segment that goes on begins in this CTA
+  int last;              // CTA of the last piece; the others lie between
 };
 
 // Joins the pieces of split segments: o = sum_i 2^(m_i - m) O_i /
@@ -291,12 +289,12 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
   }
   const int c = s_cta;
   if (c < 0) return;
-  const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));  // r0, row0, head, rows
-  const int n = __ldcg(&a.jobs[c].last) - c + 1;
+  const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));  // r0, head, rows, last
+  const int n = j0.w - c + 1;
   const bool few = n <= kFewPieces;
   const int i0 = few ? 0 : warp, step = few ? 1 : WARPS;
   const int m0 = few ? blockIdx.y * WARPS + warp : blockIdx.y, m_step = gridDim.y * (few ? WARPS : 1);
-  for (int m = m0; m < j0.w; m += m_step) {
+  for (int m = m0; m < j0.z; m += m_step) {
     float o[E], l = 0.f, top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -364,8 +362,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
     }
     if (!(l < INFINITY) && lane == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int row = j0.y + m;
-    uint16_t* dst = a.out + (j0.x + row / a.G) * a.out_stride + (j0.z * a.G + row % a.G) * D;
+    uint16_t* dst = a.out + (j0.x + m / a.G) * a.out_stride + (j0.y * a.G + m % a.G) * D;
     auto pack = [&](float x, float y) { return a.bf16 ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv); };
     if constexpr (E < 4) {
       reinterpret_cast<uint32_t*>(dst)[lane] = pack(o[0], o[1]);
@@ -395,7 +392,7 @@ cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStrea
   return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, R>, a, most);
 }
 
-// kv4_attention_tc.cu: row groups of 128, tiles of 64 cells, one CTA per SM.
+// kv4_attention_tc.cu: up to 128 rows, tiles of 64 cells at 256 channels, else of 128, one CTA per SM.
 cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st);
 
 }  // namespace dflash

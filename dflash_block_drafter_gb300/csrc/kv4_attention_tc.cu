@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     mbar_init(&ofree, kSoftWarps);
     fence_barrier_init();
   }
-  const long long T = kv4_plan<kTile, R, kOverhead>(a, pre, scratch, blockIdx.x == 0);
+  const long long T = kv4_plan<kTile, kOverhead>(a, pre, scratch, blockIdx.x == 0);
   const int C = kv4_ctas(T, gridDim.x);
   const int c = blockIdx.x;
   pdl_launch_dependents();
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   bool ok = true;
 
   const Kv4Part none{};
-  auto part_at = [&](long long at, const Kv4Part& before) { return kv4_part<kTile, R, kOverhead>(a, pre, at, x_end, before); };
+  auto part_at = [&](long long at, const Kv4Part& before) { return kv4_part<kTile, kOverhead>(a, pre, at, x_end, before); };
 
   if (warp < kSoftWarp0) fewer_registers<kOtherRegs>();
   if (warp == kCopyKWarp || warp == kCopyVWarp) {
@@ -405,8 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     Kv4Job job{};  // the segment that begins here and goes on in the next CTAs, if one does
     for (Kv4Part p = part_at(x_begin, none); p.n > 0; p = part_at(p.next, p)) {
       const bool mine = m < p.rows, live = q4 * 32 < p.rows;  // the row; any row of the quarter
-      const int row = p.row0 + m;
-      const int2 sees = mine ? kv4_sees(a, p.q, kv4_token(row, per_g)) : make_int2(0, 0);
+      const int2 sees = mine ? kv4_sees(a, p.q, kv4_token(m, per_g)) : make_int2(0, 0);
       int all_lo = mine ? sees.x : 0, all_hi = mine ? sees.y : 0x7fffffff;  // cells that every row of the quarter sees
 #pragma unroll
       for (int w = 1; w < 32; w <<= 1) {
@@ -417,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       // (Nothing else runs until Q is there, and an instruction of a chain costs several
       // cycles: FP16 rows are taken as they are, magnitudes compared as pairs of bits,
       // powers of two made of bits, the token of a row found by a multiplication.)
-      const uint16_t* src = a.q + p.q.r0 * a.q_stride + kv4_token(row, per_g) * (a.q_stride - a.G * D) +
-                            (p.head * a.G + row) * D + cs * (D / 2);
+      const uint16_t* src = a.q + p.q.r0 * a.q_stride + kv4_token(m, per_g) * (a.q_stride - a.G * D) +
+                            (p.head * a.G + m) * D + cs * (D / 2);
       // BF16 rows are scaled into FP16's range: by 2^8 where their largest magnitude is
       // in [2^-6, 2^7) (what falls below FP16's smallest value is 2^-27 of that, at most), so
       // that one pass over Q does; else by the power that brings it into [2^12, 2^13).
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[(e >> 1) + 4 * (e & 1)] = __uint_as_float(o[8 * k + e]) * inv;
               if (whole) {
-                uint16_t* dst = a.out + p.q.r0 * a.out_stride + kv4_token(row, per_g) * (a.out_stride - a.G * D) + (p.head * a.G + row) * D + col + 8 * k;
+                uint16_t* dst = a.out + p.q.r0 * a.out_stride + kv4_token(m, per_g) * (a.out_stride - a.G * D) + (p.head * a.G + m) * D + col + 8 * k;
                 *reinterpret_cast<uint4*>(dst) =
                     a.bf16 ? make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]))
                            : make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       tc_fence_before();
       named_bar_sync(1, kSoftThreads);  // red_sum has been read
       if (lane == 0) mbar_arrive(&ofree);
-      if (!whole && p.k0 == 0) job = Kv4Job{p.q.r0, p.row0, p.head, p.rows, kv4_owner(T, C, p.end - 1), {0, 0, 0}};
+      if (!whole && p.k0 == 0) job = Kv4Job{p.q.r0, p.head, p.rows, kv4_owner(T, C, p.end - 1)};
     }
     if (warp == kSoftWarp0 && lane == 0) a.jobs[c] = job;
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
