@@ -286,10 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
                (v_side ? F::V_CODES : F::K_CODES);
       };
       const uint8_t *from = nullptr, *later = look_up(0);
-      // the ring is too short for HBM's latency: L2 is asked for the tiles behind it
-      // now (in the CTA's first part only once Q is there, whose loads would have to wait
-      // behind them), then for each tile WIN - 1 tiles before it is copied
-      if (g > 0 && lane_tile >= NP && later) bulk_prefetch_l2_plain(later, G::HALF);
+      // the ring is too short for HBM's latency: L2 is asked for each tile WIN - 1 tiles
+      // before it is copied, and at a part's beginning for those looked up that the ring
+      // does not take (at 256 channels; in the CTA's first part only once Q is there,
+      // whose loads would have to wait behind them)
+      constexpr bool BEHIND = WIN > NP;
+      if (BEHIND && g > 0 && lane_tile >= NP && later) bulk_prefetch_l2_plain(later, G::HALF);
       unsigned have = 0;
       for (int i = 0; i < p.n && ok; ++i, ++g) {
         const int t = i % WIN, st = g % NP;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (lane_tile == t && from) bulk_g2s(ring + st * G::STAGE + lane_group * G::HALF, from, G::HALF, &pfull[st]);
         // (tiles of this part are still to come, so that it cannot end, and `qready` not
         // go on to the next part's phase, before this warp has seen it)
-        if (g == NP - 1 && i == NP - 1 && i + 1 < p.n) {
+        if (BEHIND && g == NP - 1 && i == NP - 1 && i + 1 < p.n) {
           ok = __all_sync(0xffffffffu, kv4_wait(&qready, 0));
           if (lane_tile >= NP && from) bulk_prefetch_l2_plain(from, G::HALF);
         }
