@@ -203,45 +203,40 @@ struct Kv4Part {
   int s, head, rows, k0, n;  // rows: query rows
   long long end, next;  // units: the segment's end; where this part ends
 };
-// The first part with a tile in [at, x_end); `hint` is the part before it (or a zeroed one).
+// The first part with a tile in [at, x_end).  `hint`: the part before it, which ended at
+// `at` (or a zeroed one for a CTA's first part, which may begin anywhere in a segment).
 template <int STEP, int OV>
 __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long long* pre, long long at, long long x_end,
                                             const Kv4Part& hint) {
   Kv4Part p = hint;
   p.n = 0;
   p.next = x_end;
-  while (at < x_end) {
-    int s = p.s;
-    if (!(p.q.rows > 0 && pre[s] <= at && at < pre[s + 1])) {
-      if (s + 1 < a.n_seq && pre[s + 1] <= at && at < pre[s + 2]) {
-        ++s;
-      } else {
-        int lo = 0, hi = a.n_seq - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (pre[mid + 1] > at) hi = mid;
-          else lo = mid + 1;
-        }
-        s = lo;
-      }
-      p.s = s;
-      p.q = kv4_seq<STEP>(a, s, false);
+  if (at >= x_end) return p;
+  const bool first = hint.n == 0;
+  if (first || ++p.head == a.n_kv) {  // another sequence
+    int lo = 0, hi = a.n_seq - 1;
+    if (!first && pre[p.s + 1] <= at && at < pre[p.s + 2]) lo = hi = p.s + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid + 1] > at) hi = mid;
+      else lo = mid + 1;
     }
-    const int units = p.q.steps + OV;
-    const long long rel = at - pre[s];
-    const int head = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
-    const long long begin = pre[s] + static_cast<long long>(head) * units;
-    p.end = begin + units;
-    p.next = p.end < x_end ? p.end : x_end;
-    p.k0 = max(static_cast<int>(at - begin) - OV, 0);
-    p.n = max(static_cast<int>(p.next - begin) - OV, 0) - p.k0;
-    if (p.n > 0) {
-      p.head = head;
-      p.rows = p.q.rows * a.G;
-      break;
-    }
-    at = p.next;
+    p.s = lo;
+    p.q = kv4_seq<STEP>(a, lo, false);
+    p.head = 0;
   }
+  const int units = p.q.steps + OV;
+  long long begin = at;
+  if (first) {
+    const long long rel = at - pre[p.s];
+    p.head = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
+    begin = pre[p.s] + static_cast<long long>(p.head) * units;
+  }
+  p.end = begin + units;
+  p.next = p.end < x_end ? p.end : x_end;
+  p.k0 = max(static_cast<int>(at - begin) - OV, 0);
+  p.n = max(static_cast<int>(p.next - begin) - OV, 0) - p.k0;  // 0: the range ends before the segment's first tile
+  p.rows = p.q.rows * a.G;
   return p;
 }
 

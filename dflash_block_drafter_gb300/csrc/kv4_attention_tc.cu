@@ -403,9 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int m = q4 * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     uint32_t g = 0, part = 0;
-    const uint32_t per_g = kv4_per_token(a.G);
     Kv4Job job{};  // the segment that begins here and goes on in the next CTAs, if one does
     for (Kv4Part p = part_at(x_begin, none); p.n > 0; p = part_at(p.next, p)) {
+      const uint32_t per_g = kv4_per_token(a.G);
       const bool mine = m < p.rows, live = q4 * 32 < p.rows;  // the row; any row of the quarter
       const int2 sees = mine ? kv4_sees(a, p.q, kv4_token(m, per_g)) : make_int2(0, 0);
       int all_lo = mine ? sees.x : 0, all_hi = mine ? sees.y : 0x7fffffff;  // cells that every row of the quarter sees
