@@ -6,6 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import dflash_block_drafter_gb300 as D  # noqa: E402
+import verify_exact as E  # noqa: E402
 import verify_ref as V  # noqa: E402
 from test_gpu_verify import R, TYPES, attn_case, check_attn, ints, status  # noqa: E402,F401
 
@@ -132,3 +133,176 @@ def test_held_out_of_range(R, held, nearest, lengths):
     st, got = call(held)
     assert st == D.DFLASH_DEV_CAPACITY
     assert call(nearest) == (0, got)
+
+
+# ---------------------------------------------------------- every cell, once
+def exact_cache(R, rng, lens, heads, d, page):
+    """(cache, table, [(k, v)]) of sequences of exact cells."""
+    counts = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(counts))
+    cache = R.kv4_cache(len(order), page, heads, d)
+    cache.fill_(0xFF)
+    table = np.full((len(lens), max(counts)), -1, np.int32)
+    parts, at = [], 0
+    for s, n in enumerate(lens):
+        table[s, : counts[s]] = order[at: at + counts[s]]
+        at += counts[s]
+        parts.append(E.cells(rng, n, heads, d))
+        pos = np.arange(n)
+        R.kv4_write(cache, *(torch.as_tensor(x, device="cuda").half() for x in parts[s]), ints(table[s, pos // page] * page + pos % page))
+    return cache, table, parts
+
+
+@pytest.mark.parametrize("d,heads,G,rows", [(64, 2, 5, 8), (128, 1, 9, 8), (256, 2, 12, 8), (256, 1, 5, 8), (64, 2, 3, 8), (128, 2, 4, 8),
+                                            (128, 4, 4, 1), (256, 2, 12, 1), (64, 1, 16, 1)])
+@pytest.mark.parametrize("lens", ["long", "many"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1500)])
+def test_every_cell_once(R, d, heads, G, rows, lens, causal, window):
+    """Long and many sequences whose result shows a single tile that is lost, taken twice or stale."""
+    rng = np.random.default_rng(d + G)
+    lens = ([30000, 100, 2000, 17000] if d < 256 else [20000, 40, 700, 12000]) if lens == "long" else rng.integers(64, 2500, 40).tolist()
+    cache, table, parts = exact_cache(R, rng, lens, heads, d, 64)
+    q = E.queries(rng, rows * len(lens), heads * G, d)
+    st = status()
+    out = R.kv4_attention(cache, torch.as_tensor(q, device="cuda").half(), ints(table), ints(lens), ints(np.arange(len(lens) + 1) * rows), rows,
+                          causal=causal, window=window, scale=float(np.log(2)), status=st).double().cpu().numpy()
+    assert int(st) == 0
+    for s, (k, v) in enumerate(parts):
+        mine = slice(s * rows, s * rows + rows)
+        o, spread = E.attend(k, v, q[mine], causal, window)
+        worst = np.max(np.abs(out[mine] - o) / E.tolerance(o, spread, 2.0 ** -11))
+        assert worst <= 1, (s, worst)
+
+
+@pytest.mark.parametrize("d,G,rows", [(64, 5, 8), (128, 5, 8), (256, 5, 8), (64, 4, 1), (128, 4, 8), (256, 4, 1)])
+def test_every_cell_once_unsplit(R, d, G, rows):
+    """More segments than CTAs, all of them long, over the same pages."""
+    rng = np.random.default_rng(d)
+    n, n_seq = 12000, 400
+    cache, table, parts = exact_cache(R, rng, [n], 2, d, 64)
+    q = E.queries(rng, rows, 2 * G, d)
+    out = R.kv4_attention(cache, torch.as_tensor(q, device="cuda").half().repeat(n_seq, 1, 1), ints(np.repeat(table, n_seq, 0)),
+                          ints(np.full(n_seq, n)), ints(np.arange(n_seq + 1) * rows), rows, scale=float(np.log(2))).double().cpu().numpy()
+    o, spread = E.attend(*parts[0], q, True)
+    worst = np.max(np.abs(out.reshape(n_seq, *o.shape) - o) / E.tolerance(o, spread, 2.0 ** -11))
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("G,rows,gain", [(4, 1, 1.0), (4, 8, 4.0), (5, 8, 1.0), (16, 8, 4.0)])
+def test_stated_roundings(R, d, kind, G, rows, gain):
+    """Ordinary values within the bound that follows from the roundings that the kernels state, K's in the tcgen05 kernel among them."""
+    cache, q, table, lens, offsets = attn_case(d + G, d, 1, G, [1500, 90], [rows, 1], 32, kind, gain=gain)
+    out = R.kv4_attention(torch.as_tensor(cache, device="cuda"), q, ints(table), ints(lens), ints(offsets), rows)
+    n = offsets[-1]
+    o, tol = E.rounded_attention(cache, q[:n].double().cpu().numpy(), table, lens, offsets, True, d ** -0.5,
+                                 torch.finfo(TYPES[kind]).eps / 2, G * rows > 32)
+    worst = np.max(np.abs(out[:n].double().cpu().numpy() - o) / tol)
+    assert worst <= 1, worst
+
+
+# ------------------------------------------- edges of the tcgen05 attention
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 2 ** 31 - 1])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_window_of_many_rows(R, d, window, causal, kind):
+    check_attn(R, attn_case(d + window, d, 2, 5, [200, 31, 4, 64], [3, 1, 4, 8], 16, kind), causal, window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 3])
+def test_many_rows_without_cells(R, d, window):
+    """No cells at all, fewer cells than rows, no rows; more than 32 rows per kv head."""
+    case = attn_case(3, d, 2, 16, [0, 2, 5, 40, -3], [2, 4, 0, 3, 1], 16, "bf16")
+    got = check_attn(R, case, True, window)
+    assert not got[:4].any() and got[4:6].any() and not got[-1].any()
+    check_attn(R, case, False, window)
+
+
+@pytest.mark.parametrize("kind,gain,scale", [("bf16", 1e-20, 1e19), ("bf16", 1e20, 1e-21), ("fp16", 1e-5, 2e4), ("fp16", 2e3, 1e-4),
+                                             ("bf16", 0.0, 1.0), ("fp16", 8.0, 0.5)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_ranges_of_many_rows(R, kind, gain, scale, d):
+    """(check_attn's bound does not know that this kernel rounds K to FP16.  That moves a score by up to scale * 2^-11 * sum |q k|: with queries
+    of size 8 and a scale of 1/2 over 128 channels by 0.5 * 2^-11 * 128 * 8 * 0.8 * 0.8 = 0.16, where that bound has 2^-16 of scores of
+    100 or 200, 0.003.  The reference here takes K rounded.)"""
+    cache, q, table, lens, offsets = attn_case(1, d, 1, 20, [300], [2], 32, kind, gain=gain)
+    st = status()
+    out = R.kv4_attention(torch.as_tensor(cache, device="cuda"), q, ints(table), ints(lens), ints(offsets), 2, scale=scale, status=st)
+    o, tol = E.rounded_attention(cache, q[:2].double().cpu().numpy(), table, lens, offsets, True, scale, torch.finfo(TYPES[kind]).eps / 2, True)
+    worst = np.max(np.abs(out[:2].double().cpu().numpy() - o) / tol)
+    assert int(st) == 0 and worst <= 1, worst
+
+
+@pytest.mark.parametrize("vgain", [1e-4, 3e3])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_value_range_of_many_rows(R, vgain, d):
+    check_attn(R, attn_case(2, d, 1, 5, [100], [8], 16, "bf16", vgain=vgain), True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_strided_many_rows(R, d):
+    """q inside a wider row, out inside another, and a row's neighbours left as they were."""
+    cache, q, table, lens, offsets = attn_case(4, d, 2, 5, [50, 20], [8, 3], 16, "bf16")
+    c, args, st = torch.as_tensor(cache, device="cuda"), (ints(table), ints(lens), ints(offsets), 8), status()
+    plain = R.kv4_attention(c, q, *args)
+    wide = torch.zeros((q.shape[0], 12, d), dtype=q.dtype, device="cuda")
+    wide[:, 1:11] = q
+    outw = torch.full((q.shape[0], 13, d), 3.0, dtype=q.dtype, device="cuda")
+    R.kv4_attention(c, wide[:, 1:11], *args, out=outw[:, 2:12], status=st)
+    assert torch.equal(outw[:11, 2:12], plain[:11]) and bool((outw[:, :2] == 3).all()) and bool((outw[:, 12:] == 3).all())
+    assert bool((outw[11:] == 3).all()) and int(st) == 0
+
+
+def test_reports_of_many_rows(R):
+    cache, q, table, lens, offsets = attn_case(6, 64, 1, 40, [40, 20], [2, 1], 16, "fp16")
+    c = torch.as_tensor(cache, device="cuda")
+
+    def call(table=table, lens=lens, offsets=offsets, q=q, rows=2):
+        st, out = status(), torch.full_like(q, 7.0)
+        R.kv4_attention(c, q, ints(table), ints(lens), ints(offsets), rows, out=out, status=st)
+        return int(st), out
+
+    good = call()
+    assert good[0] == 0
+    st, out = call(rows=1)
+    assert st == D.DFLASH_DEV_BAD_BLOCK and bool((out[:2] == 7).all()) and torch.equal(out[2], good[1][2])
+    assert call(offsets=np.array([0, 2, 1]))[0] == D.DFLASH_DEV_BAD_BLOCK
+    assert call(offsets=np.array([-1, 0, 1]))[0] == D.DFLASH_DEV_BAD_BLOCK
+    assert call(offsets=np.array([0, 2, 99]), rows=3)[0] == D.DFLASH_DEV_BAD_BLOCK
+    assert call(lens=np.array([1000, 20]))[0] & D.DFLASH_DEV_CAPACITY
+    bad = table.copy()
+    bad[0, 1] = -1
+    st, out = call(table=bad)
+    assert st & D.DFLASH_DEV_CAPACITY and torch.equal(out[2], good[1][2])
+    nan = q.clone()
+    nan[0, 0, 3] = float("nan")
+    st, out = call(q=nan)
+    assert st == D.DFLASH_DEV_NONFINITE and torch.equal(out[1:3], good[1][1:3])
+    assert torch.equal(out[0, 1:], good[1][0, 1:])
+
+
+# ------------------------------------------------------------- written bytes
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_written_bytes(R, d, kind):
+    """Every byte of a written cell, codes and scales; only the sign of a zero scale is free."""
+    rng = np.random.default_rng(d)
+    n, heads, page = 96, 2, 32
+    x = torch.as_tensor(rng.standard_normal((2, n, heads, d)) * np.exp(2 * rng.standard_normal((2, n, heads, 1))), device="cuda").to(TYPES[kind])
+    x[:, 0] = 0
+    x[:, 1] = 2.0 ** -24  # a scale below FP16's smallest
+    cache = R.kv4_cache(n // page, page, heads, d)
+    slots = rng.permutation(n).astype(np.int32)
+    R.kv4_write(cache, x[0], x[1], ints(slots))
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    V.store(want, slots, x[0].double().cpu().numpy(), x[1].double().cpu().numpy())
+    got = cache.cpu().numpy()
+    scales = np.zeros(18 * d, bool)
+    for at in V.word_places(d)[2:]:
+        scales[at] = scales[at + 1] = True
+    assert np.array_equal(got[..., ~scales], want[..., ~scales])
+    a, b = (np.ascontiguousarray(y[..., scales]).view(np.uint16) for y in (got, want))
+    assert np.array_equal(np.where(a == 0x8000, 0, a), np.where(b == 0x8000, 0, b))

@@ -2,9 +2,12 @@
 scale.  No GPU is used."""
 import ctypes
 
+import numpy as np
 import pytest
 
 import dflash_block_drafter_gb300 as D
+import verify_exact as E
+import verify_ref as V
 from test_verify_host import _cache, lib  # noqa: F401
 
 WIDE = 2 ** 32  # a size that 32 bits would cut to 0
@@ -51,3 +54,39 @@ def test_largest_scale(lib):  # noqa: F811
     assert call(2.0 ** 127) == D.DFLASH_OK  # no tokens: nothing to do
     for scale in (2.0 ** 127 * (1 + 2.0 ** -20), 3e38):
         assert call(scale) == D.DFLASH_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------- the exact cases
+@pytest.mark.parametrize("d,n", [(64, 30000), (128, 30000), (256, 20000)])
+@pytest.mark.parametrize("cells", [64, 16])
+def test_exact_cases_show_a_lost_tile(d, n, cells):
+    """A tile (or group) of cells left out, taken twice or replaced by an earlier one passes the bound by far, wherever it lies."""
+    rng = np.random.default_rng(d)
+    k, v = E.cells(rng, n, 1, d)
+    q = E.queries(rng, 2, 2, d)
+    o, spread = E.attend(k, v, q, False)
+    tol = E.tolerance(o, spread, 2.0 ** -11)
+    for at in (0, n // 3 // cells * cells, (n - 1) // cells * cells):
+        mine = slice(at, at + cells)
+        for weight in (-np.inf, 1.0):
+            bias = np.zeros(n)
+            bias[mine] = weight
+            assert np.all(np.max(np.abs(E.attend(k, v, q, False, bias=bias)[0] - o) / tol, -1) > 5)
+        early = slice(at - 3 * cells, at - 2 * cells) if at else slice(n - 5 * cells, n - 4 * cells)
+        for x in (k, v):
+            size = x[mine].shape[0]
+            kept = x[mine].copy()
+            x[mine] = x[early][:size]
+            assert np.all(np.max(np.abs(E.attend(k, v, q, False)[0] - o) / tol, -1) > 2.5)
+            x[mine] = kept
+
+
+def test_exact_cases_are_exact():
+    rng = np.random.default_rng(0)
+    for d in (64, 128, 256):
+        k, v = E.cells(rng, 40, 2, d)
+        for x in (k, v):
+            codes, scales = V.quantise(x.astype(np.float64))
+            assert np.all(scales == 1) and np.array_equal(V.dequantise(codes, scales), x)
+        s = np.einsum("thd,nd->thn", E.queries(rng, 3, 4, d), k[:, 0].astype(np.float64))
+        assert s.min() >= -3 and s.max() <= 0
