@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         // A row with an infinity or a NaN is reported here already: below, where the sum of its
         // weights shows them, a score of -infinity passes for a cell that the row does not see.
-        if (!again && max(top & 0xffffu, top >> 16) >= (a.bf16 ? 0x7f80u : 0x7c00u)) set_status(a.status, DFLASH_DEV_NONFINITE);
+        if (!again && sees.x < sees.y && max(top & 0xffffu, top >> 16) >= (a.bf16 ? 0x7f80u : 0x7c00u)) set_status(a.status, DFLASH_DEV_NONFINITE);
         if (again || !a.bf16) break;
         red_sum[cs * R + m] = __uint_as_float(top);
         named_bar_sync(1, kSoftThreads);

@@ -506,7 +506,7 @@ int dflash_kv4_read(const dflash_kv4_cache* cache, const int32_t* slots, int32_t
  *           [row_offsets[s], row_offsets[s + 1]), at most max_rows (1 .. 8) of
  *           them; (n_q / n_kv) * max_rows <= 128.
  *   kv_len: [n_seq] int32, the cells of each sequence, those of its rows
- *           among them: row i of r is at position kv_len - r + i.
+ *           among them: row i of r is at position kv_len - r + i.  Negative: none.
  *   table:  [n_seq, table_stride] int32, page ids.
  *   causal: non-zero: a row sees the positions up to its own; zero: all
  *           kv_len.  window W > 0: of those only the W last.

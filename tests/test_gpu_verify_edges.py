@@ -118,6 +118,20 @@ def test_queries_that_are_not_finite(R, d, kind, G, rows, bad, channel):
     assert torch.equal(got[others], want[others])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("G,rows", [(4, 8), (5, 8)])
+def test_queries_that_meet_no_cell(R, d, kind, G, rows):
+    """Rows before the first cell have no scores, whatever their queries hold: zeros and no report."""
+    cache, q, table, lens, offsets = attn_case(d, d, 1, G, [5, 70, 0], [rows, rows, 1], 16, kind)
+    q[: rows - 5] = float("inf")  # causal: positions -3 .. -1
+    q[2 * rows] = float("nan")
+    st, out = status(), torch.full_like(q, 7.0)
+    R.kv4_attention(torch.as_tensor(cache, device="cuda"), q, ints(table), ints(lens), ints(offsets), rows, out=out, status=st)
+    assert int(st) == 0 and not out[: rows - 5].any() and not out[2 * rows].any()
+    assert bool(out[rows - 5: 2 * rows].isfinite().all()) and bool((out[2 * rows + 1:] == 7).all())
+
+
 # --------------------------------------------------------------- page tables
 @pytest.mark.parametrize("held,nearest", [([-1, 1, 1], [0, 1, 1]), ([1, 5, 1], [1, 4, 1]), ([1, 1, 2 ** 31 - 1], [1, 1, 4]),
                                           ([1, 1, -(2 ** 31)], [1, 1, 0])])
@@ -306,3 +320,65 @@ def test_written_bytes(R, d, kind):
     assert np.array_equal(got[..., ~scales], want[..., ~scales])
     a, b = (np.ascontiguousarray(y[..., scales]).view(np.uint16) for y in (got, want))
     assert np.array_equal(np.where(a == 0x8000, 0, a), np.where(b == 0x8000, 0, b))
+
+
+# ------------------------------------------------------------- largest calls
+@pytest.mark.parametrize("d,heads,G,rows", [(256, 1, 5, 8), (64, 1, 5, 8), (256, 1, 4, 8), (128, 2, 1, 1)])
+def test_most_sequences(R, d, heads, G, rows):
+    """1024 sequences, some without rows or cells, rows that begin behind others of no sequence."""
+    rng = np.random.default_rng(d)
+    lens = rng.integers(0, 24, 1024)
+    many = rng.integers(0, rows + 1, 1024)
+    cache, q, table, lens, offsets = attn_case(5, d, heads, G, lens.tolist(), many.tolist(), 16, "bf16")
+    check_attn(R, (cache, q, table, lens, offsets), True, max_rows=rows)
+    first = 3
+    moved = torch.cat([torch.full_like(q[:first], float("nan")), q])
+    st, out = status(), torch.full_like(moved, 7.0)
+    args = torch.as_tensor(cache, device="cuda"), ints(table), ints(lens)
+    want = R.kv4_attention(args[0], q, args[1], args[2], ints(offsets), rows)
+    R.kv4_attention(args[0], moved, args[1], args[2], ints(offsets + first), rows, out=out, status=st)
+    n = int(offsets[-1])
+    assert int(st) == 0 and torch.equal(out[first: first + n], want[:n])
+    assert bool((out[:first] == 7).all()) and bool((out[first + n:] == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_most_heads(R, d):
+    check_attn(R, attn_case(7, d, 256, 1, [20, 3], [1, 2], 16, "fp16"), True)
+
+
+def test_cells_and_scores_in_a_graph(R):
+    """Writing, reading back and scoring captured once and replayed with other inputs."""
+    rng = np.random.default_rng(2)
+    cache, st = R.kv4_cache(8, 16, 2, 64), status()
+    both = torch.zeros((100, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    x, tokens, slots = torch.zeros((3, 70001), device="cuda"), ints(np.zeros(3)), ints(np.zeros(100))
+    k, v = both[:, 0], both[:, 1].contiguous()
+
+    def step():
+        R.kv4_write(cache, k, v, slots, status=st)
+        return R.kv4_read(cache, slots, status=st) + R.token_logprobs(x, tokens, top_k=4, status=st)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    slots.copy_(ints(np.arange(100)))
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        both.copy_(torch.as_tensor(rng.standard_normal(both.shape), device="cuda"))
+        v.copy_(both[:, 1])
+        slots.copy_(ints(rng.permutation(128)[:100]))
+        x.copy_(torch.as_tensor(rng.standard_normal(x.shape), device="cuda"))
+        tokens.copy_(ints(rng.integers(0, 70001, 3)))
+        graph.replay()
+        for a, b in zip(got, (y.clone() for y in step())):
+            assert torch.equal(a, b)
+        for a, b in zip(got, (k, v)):
+            assert np.array_equal(a.double().cpu().numpy(), V.dequantise(*V.quantise(b.double().cpu().numpy())))
+        z = x.double()
+        assert np.allclose(got[2].cpu().numpy(), (z.gather(1, tokens.long()[:, None])[:, 0] - z.logsumexp(1)).cpu().numpy(), rtol=2.0 ** -18, atol=0)
+    assert int(st) == 0
