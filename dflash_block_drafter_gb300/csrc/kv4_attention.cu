@@ -96,25 +96,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
   return r;
 }
 
-// N consecutive words (1, 2 or 4).
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 1) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-  } else {
-    static_assert(N == 4, "words");
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  }
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kernel(const Kv4AttnArgs a) {
   using F = Kv4<D>;

@@ -50,9 +50,10 @@ __device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The constants that turn the codes of a word into FP16 code - 8.  Held in
-// registers that the compiler takes for unknown: as immediates, the AND and
-// the OR of a code would be two instructions (and the FMA's second constant a
+// The constants that turn the codes of a word into FP16 code - 8 (an integer put into the
+// mantissa of 1024, as Kim et al., "Who Says Elephants Can't Run", 2022, publish it for
+// weights).  Held in registers that the compiler takes for unknown: as immediates, the
+// AND and the OR of a code would be two instructions (and the FMA's second constant a
 // move), a third of the unpacking's arithmetic.
 struct Kv4Consts {
   uint32_t base, minus_72;
@@ -73,6 +74,25 @@ struct Kv4Consts {
     return hfma2_u32(r, 0x2c002c00u, minus_72);  // / 16 - 72
   }
 };
+
+// N consecutive words (1, 2 or 4) of shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    static_assert(N == 4, "words");
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+}
 
 // P is 2^(score - reference).  A row's reference is put kKv4Lift below its largest score so
 // far and stays until a score passes it by 2^kKv4Slack, so that few tiles pay for a
