@@ -65,7 +65,11 @@ struct Geo {
   static constexpr int TILE = 16 * GROUPS;         // cells of a tile
   static constexpr int STAGE = GROUPS * Kv4<D>::GROUP_BYTES;
   static constexpr int STAGES = D == 256 ? 2 : 3;
-  static constexpr int PER_SM = D == 256 ? 2 : 3;  // CTAs per SM
+  // CTAs per SM: three, or two where three leave a thread too few registers.  Measured with
+  // two and three on 64 blocks of 8 rows over 512 .. 8192 cells, 8 kv heads: 32 rows of
+  // 128 channels 183 and 220 us (508 bytes of spill loads), 24 rows 160 and 153; 32 rows of
+  // 64 channels 139 and 128, 24 rows 122 and 110.  (256 channels: shared memory for two.)
+  static constexpr int PER_SM = D == 256 || (D == 128 && NT == 4) ? 2 : 3;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int QF = NT * (D / 32) * 512;   // Q fragments
   static constexpr int QS = NT * 256;              // fragments of the blocks' sums
@@ -595,19 +599,22 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t s
 // Shared memory of an SM, and what a CTA takes of it besides its dynamic part
 // (its static arrays and the system's 1 KB).
 constexpr int kSmemOfSm = 228 * 1024, kStaticSmem = 2560;
-int smem_of(int d, int nt) {
+struct CtaCost {
+  int smem, per_sm;
+};
+CtaCost cost_of(int d, int nt) {
   switch (d * 8 + nt) {
-#define DFLASH_KV4_SMEM(D) \
-  case D * 8 + 1: return Geo<D, 1>::SMEM; \
-  case D * 8 + 2: return Geo<D, 2>::SMEM; \
-  case D * 8 + 3: return Geo<D, 3>::SMEM; \
-  case D * 8 + 4: return Geo<D, 4>::SMEM;
-    DFLASH_KV4_SMEM(64)
-    DFLASH_KV4_SMEM(128)
-    DFLASH_KV4_SMEM(256)
-#undef DFLASH_KV4_SMEM
+#define DFLASH_KV4_COST(D, NT) \
+  case D * 8 + NT: return {Geo<D, NT>::SMEM, Geo<D, NT>::PER_SM};
+#define DFLASH_KV4_COSTS(D) \
+  DFLASH_KV4_COST(D, 1) DFLASH_KV4_COST(D, 2) DFLASH_KV4_COST(D, 3) DFLASH_KV4_COST(D, 4)
+    DFLASH_KV4_COSTS(64)
+    DFLASH_KV4_COSTS(128)
+    DFLASH_KV4_COSTS(256)
+#undef DFLASH_KV4_COSTS
+#undef DFLASH_KV4_COST
   }
-  return 0;
+  return {kSmemOfSm, 1};
 }
 
 // What the host knows of a call: its kernel, CTAs and split segments at most.
@@ -645,9 +652,9 @@ cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int ma
   const long long tiles = (static_cast<long long>(table_stride) * c->page_size + tile - 1) / tile + 1;
   const long long ctas = segments * (tiles + kOverhead);
   // one wave of CTAs: every one of them has the same share
-  const int smem = smem_of(c->head_dim, out->nt) + kPlanBytes(n_seq) + kStaticSmem;
-  const int most_per_sm = c->head_dim == 256 ? 2 : 3;
-  const int per_sm = kSmemOfSm / smem < most_per_sm ? kSmemOfSm / smem : most_per_sm;
+  const CtaCost cost = cost_of(c->head_dim, out->nt);
+  const int fit = kSmemOfSm / (cost.smem + kPlanBytes(n_seq) + kStaticSmem);
+  const int per_sm = fit < cost.per_sm ? fit : cost.per_sm;
   out->most = static_cast<int>(ctas < per_sm * sms ? ctas : per_sm * sms);
   out->jobs = static_cast<int>(segments < out->most ? segments : out->most);
   return cudaSuccess;
