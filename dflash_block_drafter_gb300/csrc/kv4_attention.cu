@@ -34,12 +34,15 @@
 // registers per 8 rows at most, two or three CTAs fit an SM, and a segment ends
 // without joining warps.  One barrier per tile orders P, the ring's stages and the
 // vote on the maximum: the reference of a row's weights moves seldom (kKv4Slack), so
-// that the first tile and few others pay for a rescaling.
-// Bulk copies of whole groups (K, V and scales together) run one or two tiles ahead,
-// into the CTA's next segment too.
+// that the first tile and few others pay for a rescaling.  Bulk copies of whole groups
+// (K, V and scales together) run one or two tiles ahead, into the CTA's next segment too.
 //
-// Measured: 16 single tokens of 24 / 2 heads of 256 over 2048 .. 32768 cells 56 us for
-// 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 80 us for 224 MB.
+// (FP16 for P and V: the tensor cores' next wider type, TF32, has the same 11 bits at
+// half the rate; more bits would mean two terms each, twice the products.)
+//
+// Measured: 16 single tokens of 24 / 2 heads of 256 over 2048 .. 32768 cells 55 us for
+// 162 MB (2.9 TB/s), 200 of 32 / 8 heads of 128 over 1 .. 2047 cells 78 us for 224 MB, 64
+// blocks of 8 rows of 32 / 8 heads of 128 over 512 .. 8192 cells 182 us for 358 MB.
 // The chains of unpacking and products of the two or three warps per scheduler bound
 // it (about half of the issue slots are used), not the copies: one per tile instead of
 // four, or deeper rings, change nothing; eight warps on a tile, four per scheduler,
@@ -624,10 +627,12 @@ struct Shape {
   int most, jobs;
   int rows() const { return tc ? 128 : 8 * nt; }
 };
-// More rows per kv head than this go to the tcgen05 kernel.  Measured on 16
-// sequences of 2048 .. 32768 cells, 2 kv heads of 256 (64 of 512 .. 8192, 8 of 128):
-// 12 rows 56 us here, 100 there; 24 rows 81 and 103 (165 and 256); 32 rows 88 and
-// 105 (226 and 255); beyond, a kernel of this kind would unpack every cell once per 32 rows.
+// More rows per kv head than this go to the tcgen05 kernel.  Measured, here and there:
+//   16 sequences of 2048 .. 32768 cells, 2 kv heads of 256: 12 rows 58 and 98 us, 24 rows
+//   81 and 100, 32 rows 91 and 101 (floor 25);
+//   64 of 512 .. 8192 cells, 8 kv heads of 128: 24 rows 154 and 255, 32 rows 182 and 255
+//   (floor 53); of 64: 24 rows 110 and 164, 32 rows 128 and 164 (floor 26).
+// Beyond, a kernel of this kind would unpack every cell once per 32 rows.
 constexpr int kTcRows = 32;
 cudaError_t shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Shape* out) {
   int dev = 0, sms = 0;

@@ -27,13 +27,16 @@
 // and O's are read back in it.
 // Roundings: K, V and P to FP16 (2^-11 relative each, P 2^-32 of the row's largest weight
 // absolute), Q by 2^-27 of a row's largest value at most (BF16 rows are scaled by a
-// power of two, FP16 exact); scores, sums and O in FP32.  The two softmax warps of a
+// power of two, FP16 exact); scores, sums and O in FP32.  (FP16: the tensor cores' next
+// wider type, TF32, has the same 11 bits at half the rate.)  The two softmax warps of a
 // quarter of the rows hand a row's reference to each other tile by tile.
 //
 // Measured: a block of 8 tokens of 24 / 2 heads of 256 over 262144 cells 91 us (568
-// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 90 us.  No unit is full
-// (issue 47 %, ALU 37 %, tensor pipe 36 %): a tile takes about 1900 cycles for its way
-// through eight barriers, and the first ones wait 12 us for the plan and Q.
+// TFLOP/s, 1.6 TB/s), 16 blocks of 2 .. 8 over 2048 .. 32768 cells 87 us; 64 blocks of 8 of
+// 40 / 8 heads over 512 .. 8192 cells 259 us at 128 channels, 170 at 64.  No unit is full
+// (issue 48 %, ALU 38 %, tensor pipe 37 %): a tile takes about 1900 cycles for its way
+// through eight barriers, and the first product waits 9 to 10 us for the plan and Q.
+// At 72 registers at launch 438, 398 and 402 bytes of spill stores (256, 128, 64 channels).
 #include "kv4_attention.cuh"
 
 namespace dflash {
