@@ -32,6 +32,7 @@ DFLASH_DEV_BAD_TOKEN = 2
 DFLASH_DEV_CAPACITY = 4
 DFLASH_DEV_BAD_BLOCK = 8
 DFLASH_DEV_TIMEOUT = 16
+DFLASH_DEV_BAD_VALUE = 32
 
 DFLASH_WT_BF16 = 0
 DFLASH_WT_Q8_0 = 1
@@ -135,6 +136,9 @@ _SIGS = {
                                             ctypes.c_float, _P, _Z, _P, _P]),
     "dflash_kv4_attention_workspace": (_Z, [_KV4, _I, _I, _I, _I]),
     "dflash_token_logprobs": (ctypes.c_int, [_P, _I, _L, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "dflash_rope_turns": (ctypes.c_int, [_P, _I, _P]),
+    "dflash_qk_norm_rope": (ctypes.c_int, [_P, _P, _L, _L, _I, _P, _P, _L, _L, _I, _I, _I, _I, _P, _P, ctypes.c_float,
+                                           _P, _L, _I, _P, _P, _I, _P, _P]),
 }
 
 
@@ -415,3 +419,26 @@ def dflash_token_logprobs(logits: int, value_type: int, row_stride: int, n_rows:
                                                 logprob or None, entropy or None, top_k, top_ids or None,
                                                 top_logprobs or None, dev_status or None, stream or None),
            "dflash_token_logprobs")
+
+
+# ------------------------------------------------------------ sampling step
+def dflash_rope_turns(inv_freq) -> list:
+    """The rotation table (unsigned 64-bit integers) of frequencies in radians per position."""
+    freqs = [float(f) for f in inv_freq]
+    n = len(freqs)
+    turns = (ctypes.c_uint64 * max(1, n))()
+    _check(load_library().dflash_rope_turns((ctypes.c_double * max(1, n))(*freqs), n, turns), "dflash_rope_turns")
+    return list(turns)[:n]
+
+
+def dflash_qk_norm_rope(q: int, q_out: int, q_stride: int, q_out_stride: int, n_q_heads: int, k: int, k_out: int,
+                        k_stride: int, k_out_stride: int, n_k_heads: int, head_dim: int, value_type: int, n_rows: int,
+                        q_weight: int, k_weight: int, eps: float, positions: int, position_stride: int, n_axes: int,
+                        axes: int, turns: int, rotary_dim: int, dev_status: int = 0, stream: int = 0) -> None:
+    if (n_q_heads | n_k_heads | head_dim | n_rows | n_axes | rotary_dim) >> 31:  # negative or wide
+        _refuse_wide("dflash_qk_norm_rope", n_q_heads, n_k_heads, head_dim, n_rows, n_axes, rotary_dim)
+    _check(load_library().dflash_qk_norm_rope(q or None, q_out or None, q_stride, q_out_stride, n_q_heads, k or None,
+                                              k_out or None, k_stride, k_out_stride, n_k_heads, head_dim, value_type,
+                                              n_rows, q_weight or None, k_weight or None, eps, positions or None,
+                                              position_stride, n_axes, axes or None, turns or None, rotary_dim,
+                                              dev_status or None, stream or None), "dflash_qk_norm_rope")

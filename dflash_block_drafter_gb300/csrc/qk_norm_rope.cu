@@ -1,0 +1,302 @@
+// Per-head RMSNorm and position rotation of query and key rows in one pass
+// (dflash_qk_norm_rope in include/dflash.h).
+//
+//   y_c = x_c w_c / sqrt(mean_c x_c^2 + eps)
+//   z_j = y_j cos a_j - y_{j+h} sin a_j,  z_{j+h} = y_{j+h} cos a_j + y_j sin a_j
+//   a_j = position (of j's axis) * frequency j,  j < h = rotary_dim / 2.
+//
+// A lane has 8 consecutive channels of a head (one 16-byte load and store), a
+// warp 256 channels: one, two or four heads.  The partner channels lie h away,
+// in another lane of the same head: h is a multiple of 8, so that four shuffles of the
+// raw words bring them.  Weights, cosines and sines of a row are folded into two
+// factors per channel, z = (x A + x' B) / rms, once per row and for all of its heads.
+// Everything is FP32, rounded once to the rows' type.  The bytes bound it: every value is read and
+// written once.
+#include "common.cuh"
+#include "internal.h"
+#include "kernels.h"
+
+#include <cmath>
+
+namespace dflash {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnroll = 4;   // loads of a lane in flight
+constexpr int kMaxAxes = 4;
+
+struct RopeSide {
+  const uint16_t* x;
+  uint16_t* out;
+  long long stride, out_stride;  // elements between rows
+  const float* weight;           // null: no norm
+  int heads, steps;              // steps: of a warp over the heads
+};
+
+struct RopeArgs {
+  RopeSide side[2];  // queries, keys
+  int n_rows, splits;  // warps of a row
+  float eps;
+  const int32_t* positions;
+  long long position_stride;
+  int n_axes, half;
+  const uint8_t* axes;
+  const uint64_t* turns;
+  int32_t* status;
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  if (BF16) return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack2(f.x, f.y);
+}
+
+// 1 / rms of a head whose sum of squares leaves FP32's range: the values are scaled by a power of two first.
+template <bool BF16, int LANES>
+__device__ __forceinline__ float far_rms(uint4 raw, float eps, bool small) {
+  const float f = small ? 0x1p70f : 0x1p-70f;
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(widen2<BF16>(w[i]), a, b);
+    a *= f, b *= f;
+    s = fmaf(a, a, fmaf(b, b, s));
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float m = s * (1.f / (8 * LANES)) + eps * f * f;
+  return m > 0.f ? rsqrtf(m) * f : 0.f;  // a head of zeros without eps stays one
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes of a head, heads of a warp
+  __shared__ __align__(16) float s_w[2][D];
+  __shared__ uint64_t s_turns[D / 2];
+  __shared__ uint8_t s_axis[D / 2];
+  __shared__ __align__(16) float2 s_angle[kWarps][D / 2];  // (cos, sin) of each warp's row
+  const int tid = threadIdx.x, lane = tid & 31;
+  float2* angle = s_angle[tid >> 5];
+  for (int i = tid; i < D; i += kThreads) {
+    s_w[0][i] = a.side[0].weight ? a.side[0].weight[i] : 1.f;
+    s_w[1][i] = a.side[1].weight ? a.side[1].weight[i] : 1.f;
+    if (i < a.half) {
+      s_turns[i] = a.turns[i];
+      int axis = a.axes ? a.axes[i] : 0;
+      if (axis >= a.n_axes) {
+        if (blockIdx.x == 0) set_status(a.status, DFLASH_DEV_BAD_VALUE);
+        axis = 0;
+      }
+      s_axis[i] = static_cast<uint8_t>(axis);
+    }
+  }
+  __syncthreads();
+  const int sub = lane / LANES, c0 = lane % LANES * 8;
+  const bool first = c0 < a.half, second = !first && c0 < 2 * a.half;
+  const int j0 = first ? c0 : second ? c0 - a.half : 0;               // frequencies of the lane's channels
+  const int p0 = first ? c0 + a.half : second ? c0 - a.half : c0;     // partner channels
+  const int from = sub * LANES + p0 / 8;
+  const int steps = a.side[0].steps + a.side[1].steps;
+  const long long units = static_cast<long long>(a.n_rows) * a.splits;
+  for (long long unit = blockIdx.x * kWarps + (tid >> 5); unit < units; unit += gridDim.x * kWarps) {
+    const long long row = a.splits == 1 ? unit : unit / a.splits;
+    const int split = static_cast<int>(unit - row * a.splits);
+    const int i0 = static_cast<int>(static_cast<long long>(steps) * split / a.splits);
+    const int i1 = static_cast<int>(static_cast<long long>(steps) * (split + 1) / a.splits);
+    if (a.half) {
+      int pos[kMaxAxes];
+      bool skip = false;
+#pragma unroll
+      for (int i = 0; i < kMaxAxes; ++i) {
+        pos[i] = i < a.n_axes ? a.positions[i * a.position_stride + row] : 0;
+        skip |= pos[i] < 0;
+      }
+      if (skip) continue;  // a row of the padded batch
+      __syncwarp();        // the last row's angles have been read
+      for (int j = lane; j < a.half; j += 32) {
+        int p = pos[0];
+        if (a.n_axes > 1) {
+          const int axis = s_axis[j];
+#pragma unroll
+          for (int i = 1; i < kMaxAxes; ++i) p = axis == i ? pos[i] : p;
+        }
+        float2 t;
+        rope_sincos(s_turns[j], p, t.y, t.x);
+        angle[j] = t;
+      }
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      // (chosen field by field: an index into the arguments would copy them to local memory)
+      const RopeSide s = {which ? a.side[1].x : a.side[0].x, which ? a.side[1].out : a.side[0].out,
+                          which ? a.side[1].stride : a.side[0].stride, which ? a.side[1].out_stride : a.side[0].out_stride,
+                          which ? a.side[1].weight : a.side[0].weight, which ? a.side[1].heads : a.side[0].heads,
+                          which ? a.side[1].steps : a.side[0].steps};
+      const int b0 = which ? max(i0 - a.side[0].steps, 0) : min(i0, s.steps);
+      const int b1 = which ? max(i1 - a.side[0].steps, 0) : min(i1, s.steps);
+      if (b0 >= b1) continue;
+      uint64_t fa[4], fb[4];  // A and B of the lane's channels
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 w = *reinterpret_cast<const float2*>(&s_w[which][c0 + e]);
+        const float2 v = *reinterpret_cast<const float2*>(&s_w[which][p0 + e]);
+        float4 t = make_float4(1.f, 0.f, 1.f, 0.f);  // cos, sin of two channels
+        if (first || second) t = *reinterpret_cast<const float4*>(&angle[j0 + e]);
+        const float sign = first ? -1.f : 1.f;
+        fa[e / 2] = pack2(w.x * t.x, w.y * t.z);
+        fb[e / 2] = pack2(sign * v.x * t.y, sign * v.y * t.w);
+      }
+      const uint16_t* src = s.x + row * s.stride + sub * D + c0;
+      uint16_t* dst = s.out + row * s.out_stride + sub * D + c0;
+      const bool norm = s.weight != nullptr;
+#pragma unroll 1
+      for (int i = b0; i < b1; i += kUnroll) {
+        uint4 raw[kUnroll];
+        float ssq[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (i + u < b1 && (i + u) * HEADS + sub < s.heads)
+            raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(i + u) * (HEADS * D)));
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          uint64_t q2 = pack2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t x = widen2<BF16>(w[k]);
+            q2 = fma2(x, x, q2);
+          }
+          float q0, q1;
+          unpack2(q2, q0, q1);
+          ssq[u] = q0 + q1;
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) ssq[u] += __shfl_xor_sync(0xffffffffu, ssq[u], o);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (i + u >= b1) break;  // (the same for the warp)
+          // (widened again: kept, the values of all loads would take 32 registers)
+          asm("" : "+r"(raw[u].x), "+r"(raw[u].y), "+r"(raw[u].z), "+r"(raw[u].w));
+          const float m = ssq[u] * (1.f / D) + a.eps;
+          float inv = norm ? rsqrtf(m) : 1.f;
+          const bool big = !(ssq[u] < 1e38f), tiny = norm && m < 1e-30f;
+          if (__any_sync(0xffffffffu, big || tiny)) {
+            const float far = far_rms<BF16, LANES>(raw[u], a.eps, tiny);
+            if (norm && (big || tiny)) inv = far;
+            if (big && !(far > 0.f) && c0 == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+          }
+          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          const uint64_t inv2 = pack2(inv, inv);
+          uint32_t out[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t p = __shfl_sync(0xffffffffu, w[k], from);
+            float z0, z1;
+            unpack2(mul2(fma2(widen2<BF16>(p), fb[k], mul2(widen2<BF16>(w[k]), fa[k])), inv2), z0, z1);
+            out[k] = BF16 ? pack_bf16x2(z0, z1) : pack_f16x2(z0, z1);
+          }
+          if ((i + u) * HEADS + sub < s.heads)
+            *reinterpret_cast<uint4*>(dst + static_cast<long long>(i + u) * (HEADS * D)) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(RopeArgs a, bool bf16, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  constexpr int HEADS = 256 / D;
+  for (RopeSide& s : a.side) s.steps = (s.heads + HEADS - 1) / HEADS;
+  const int steps = a.side[0].steps + a.side[1].steps;
+  // few rows: a row's heads are shared out until every SM has its warps
+  const long long want = static_cast<long long>(sms) * 16;
+  const int most = (steps + kUnroll - 1) / kUnroll;
+  const long long by = (want + a.n_rows - 1) / a.n_rows;
+  a.splits = static_cast<int>(by < most ? by : most);
+  const long long blocks = (static_cast<long long>(a.n_rows) * a.splits + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(blocks < 8ll * sms ? blocks : 8ll * sms);
+  if (bf16) qk_norm_rope_kernel<D, true><<<grid, kThreads, 0, st>>>(a);
+  else qk_norm_rope_kernel<D, false><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+bool bad_rows(const void* x, const void* out, int64_t stride, int64_t out_stride, int32_t heads, int32_t d) {
+  if (heads == 0) return false;
+  const int64_t width = static_cast<int64_t>(heads) * d;
+  return !x || !out || reinterpret_cast<uintptr_t>(x) % 16 || reinterpret_cast<uintptr_t>(out) % 16 || stride < width ||
+         out_stride < width || stride % 8 || out_stride % 8;
+}
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+int dflash_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
+  if (n < 0 || (n > 0 && (!inv_freq || !turns))) return DFLASH_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (!std::isfinite(inv_freq[i])) return DFLASH_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i) {
+    const double t = inv_freq[i] / 6.283185307179586476925286766559;
+    const double part = std::ldexp(t - std::floor(t), 64);  // whole turns are none
+    turns[i] = part >= 18446744073709551615.0 ? 0 : static_cast<uint64_t>(part);
+  }
+  return DFLASH_OK;
+}
+
+int dflash_qk_norm_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                        const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_k_heads,
+                        int32_t head_dim, int32_t type, int32_t n_rows, const float* q_weight, const float* k_weight,
+                        float eps, const int32_t* positions, int64_t position_stride, int32_t n_axes,
+                        const uint8_t* axes, const uint64_t* turns, int32_t rotary_dim, int32_t* dev_status,
+                        dflash_stream_t stream) {
+  if (type != DFLASH_T_BF16 && type != DFLASH_T_FP16) return DFLASH_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return DFLASH_ERR_UNSUPPORTED;
+  if (n_rows < 0 || n_q_heads < 0 || n_k_heads < 0 || rotary_dim < 0 || rotary_dim > head_dim || !(eps >= 0.f) ||
+      !(eps < INFINITY))
+    return DFLASH_ERR_INVALID_ARG;
+  if (rotary_dim % 16) return DFLASH_ERR_UNSUPPORTED;
+  if (n_q_heads > 65536 || n_k_heads > 65536) return DFLASH_ERR_CAPACITY;
+  if (rotary_dim > 0) {
+    if (n_axes < 1 || n_axes > kMaxAxes) return DFLASH_ERR_UNSUPPORTED;
+    if (n_axes > 1 && (!axes || position_stride < n_rows)) return DFLASH_ERR_INVALID_ARG;
+  }
+  if (n_rows == 0 || n_q_heads + n_k_heads == 0) return DFLASH_OK;
+  if (bad_rows(q, q_out, q_stride, q_out_stride, n_q_heads, head_dim) ||
+      bad_rows(k, k_out, k_stride, k_out_stride, n_k_heads, head_dim) ||
+      (rotary_dim > 0 && (!positions || !turns || reinterpret_cast<uintptr_t>(turns) % 8)))
+    return DFLASH_ERR_INVALID_ARG;
+  RopeArgs a{};
+  a.side[0] = {static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), q_stride, q_out_stride, q_weight, n_q_heads, 0};
+  a.side[1] = {static_cast<const uint16_t*>(k), static_cast<uint16_t*>(k_out), k_stride, k_out_stride, k_weight, n_k_heads, 0};
+  a.n_rows = n_rows;
+  a.eps = eps;
+  a.positions = positions;
+  a.position_stride = position_stride;
+  a.n_axes = n_axes;
+  a.half = rotary_dim / 2;
+  a.axes = n_axes > 1 ? axes : nullptr;
+  a.turns = turns;
+  a.status = dev_status;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = type == DFLASH_T_BF16;
+  const cudaError_t e = head_dim == 64 ? launch<64>(a, bf16, st) : head_dim == 128 ? launch<128>(a, bf16, st) : launch<256>(a, bf16, st);
+  return cuda_status(e, "qk norm rope");
+}
+
+}  // extern "C"

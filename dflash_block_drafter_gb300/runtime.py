@@ -17,7 +17,7 @@ from . import (DFLASH_ERR_INVALID_ARG, DFLASH_MAX_BLOCK, DFLASH_T_BF16, DFLASH_T
                dflash_state_read_draft_probs, dflash_state_set_spec_min_p, dflash_state_write_kv, load_library,
                dflash_state_set_defer_kv, dflash_state_flush,
                dflash_kv4_attention, dflash_kv4_attention_workspace, dflash_kv4_bytes, dflash_kv4_read,
-               dflash_kv4_write, dflash_page_tables, dflash_token_logprobs,
+               dflash_kv4_write, dflash_page_tables, dflash_qk_norm_rope, dflash_rope_turns, dflash_token_logprobs,
                make_config, make_weights)
 
 
@@ -377,3 +377,75 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
                           entropy.data_ptr(), top_k, ids.data_ptr(), top.data_ptr(),
                           0 if status is None else status.data_ptr(), _current(dev))
     return logp, entropy, ids, top
+
+
+# ------------------------------------------------------------ sampling step
+# (as the verify step's: each on the device of its tensors, on its current stream or on `stream`)
+def rope_turns(inv_freq, device="cuda:0") -> torch.Tensor:
+    """The rotation table of qk_norm_rope: int64 [rotary_dim / 2] (the bits of
+    unsigned integers) of frequencies in radians per position."""
+    turns = np.array(dflash_rope_turns(inv_freq), dtype=np.uint64).view(np.int64)
+    return torch.from_numpy(turns).to(device)
+
+
+def _of_rows(x: torch.Tensor, out, device, what: str):
+    """(type, stride, out, its stride) of rows and what they are written to (made here if None)."""
+    stride = _row_stride(x, device, what)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        return stride, out, x.shape[1] * x.shape[2]
+    if out.shape != x.shape or out.dtype != x.dtype:
+        _refuse(what + " out: the rows' shape and type")
+    return stride, out, _row_stride(out, device, what + " out")
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 turns: Optional[torch.Tensor], q_weight=None, k_weight=None, eps: float = 1e-6, axes=None, q_out=None,
+                 k_out=None, status=None, stream=None):
+    """Per-head norm (with q_weight / k_weight, float [head_dim]) and rotation
+    of rows q [n, n_q_heads, head_dim] and k [n, n_k_heads, head_dim] (or None) at
+    `positions` [n], or [n_axes, n] with `axes` (uint8, one per frequency).
+    Returns (q_out, k_out), which may be q and k themselves; rows of a negative
+    position keep what they held (unset if the outputs are made here)."""
+    dev = q.device
+    if not q.is_cuda:
+        _refuse("qk_norm_rope: CUDA tensors")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return qk_norm_rope(q, k, positions, turns, q_weight, k_weight, eps, axes, q_out, k_out, status)
+    qs, q_out, qos = _of_rows(q, q_out, dev, "qk_norm_rope q")
+    n, heads, d = q.shape
+    kp = kop = ks = kos = k_heads = 0
+    if k is not None:
+        ks, k_out, kos = _of_rows(k, k_out, dev, "qk_norm_rope k")
+        if k.shape[0] != n or k.shape[2] != d or k.dtype != q.dtype:
+            _refuse("qk_norm_rope: rows of one length and type")
+        kp, kop, k_heads = k.data_ptr(), k_out.data_ptr(), k.shape[1]
+    elif k_out is not None or k_weight is not None:
+        _refuse("qk_norm_rope: k_out and k_weight without k")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.device != dev or w.numel() != d or not w.is_contiguous()):
+            _refuse("qk_norm_rope: weights are contiguous float [head_dim] on the device of the call")
+    half, n_axes, pos = 0, 1, 0
+    if turns is not None:
+        half = turns.numel()
+        if (positions is None or turns.dtype != torch.int64 or turns.device != dev or not turns.is_contiguous()
+                or positions.dim() > 2 or positions.shape[-1] != n):
+            _refuse("qk_norm_rope: positions [n] or [n_axes, n] and int64 turns on the device of the call")
+        n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        if n_axes > 1 and axes is None:
+            _refuse("qk_norm_rope: several axes need `axes`")
+        pos = positions.data_ptr()
+        if axes is not None and (axes.dtype != torch.uint8 or axes.device != dev or axes.numel() != half
+                                 or not axes.is_contiguous()):
+            _refuse("qk_norm_rope: axes are contiguous uint8, one per frequency")
+        _int32(dev, "qk_norm_rope", positions, status)
+    else:
+        _int32(dev, "qk_norm_rope", status)
+    dflash_qk_norm_rope(q.data_ptr(), q_out.data_ptr(), qs, qos, heads, kp, kop, ks, kos, k_heads, d,
+                        _VALUE_TYPES[q.dtype], n, 0 if q_weight is None else q_weight.data_ptr(),
+                        0 if k_weight is None else k_weight.data_ptr(), eps, pos, n, n_axes,
+                        0 if axes is None else axes.data_ptr(), 0 if turns is None else turns.data_ptr(), 2 * half,
+                        0 if status is None else status.data_ptr(), _current(dev))
+    return q_out, k_out

@@ -79,7 +79,8 @@ enum dflash_device_error {
   DFLASH_DEV_CAPACITY = 4,    /* p + block_len > capacity, or a fuse position >= capacity (negative
                                  fuse positions are skipped rows; ring states accept any p >= 0) */
   DFLASH_DEV_BAD_BLOCK = 8,   /* a block_len outside [2, 8] (clamped) */
-  DFLASH_DEV_TIMEOUT = 16     /* a pipeline wait exceeded its time limit (should never happen) */
+  DFLASH_DEV_TIMEOUT = 16,    /* a pipeline wait exceeded its time limit (should never happen) */
+  DFLASH_DEV_BAD_VALUE = 32   /* a parameter in device memory is outside its range */
 };
 
 /* Backbone weight storage types ("#3322 ...", "Approach"). */
@@ -553,6 +554,48 @@ size_t dflash_kv4_attention_workspace(const dflash_kv4_cache* cache, int32_t n_q
 int dflash_token_logprobs(const void* logits, int32_t type, int64_t row_stride, int32_t n_rows, int32_t vocab,
                           const int32_t* tokens, float* logprob, float* entropy, int32_t top_k, int32_t* top_ids,
                           float* top_logprobs, int32_t* dev_status, dflash_stream_t stream);
+
+/* ------------------------------------------------------ the sampling step
+ * What a served model needs beside the verify step: queries and keys made
+ * ready for the cache, attention of requests that share a prefix, and tokens
+ * drawn from the logits.  As the verify step's operators they need no
+ * dflash_model and run on the current CUDA device. */
+
+/* The rotation table of dflash_qk_norm_rope, computed on the host:
+ *   inv_freq: [n] finite frequencies in radians per position (any schedule:
+ *             theta^(-2 j / rotary_dim), scaled or not).
+ *   turns:    [n] out (host memory): the part of a turn per position in units of 2^-64,
+ *             so that position * turns modulo 2^64 is the angle whatever the position. */
+int dflash_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/* RMSNorm per head and NeoX position rotation of rows of queries and keys.
+ *   q, k:   rows of n_q_heads (n_k_heads) * head_dim values, BF16 or FP16
+ *           (`type`), strides in elements (multiples of 8), 16-byte aligned: parts of a
+ *           fused projection's output can be passed as they are.  Either may have 0
+ *           heads.
+ *   q_out, k_out: rows of the same kind; each may be its input (the same pointer and
+ *           stride), but must not overlap the inputs otherwise.
+ *   head_dim: 64, 128 or 256.
+ *   q_weight, k_weight: [head_dim] float: x / sqrt(mean x^2 + eps) * weight; NULL:
+ *           no norm.  eps finite, >= 0; a head of zeros stays one.
+ *   rotary_dim: the first rotary_dim channels (a multiple of 16, at most head_dim) are
+ *           turned, channel j < rotary_dim / 2 with j + rotary_dim / 2, by position *
+ *           frequency j; 0: no rotation, positions and turns are not read.
+ *   positions: [n_axes, position_stride] int32, of which n_rows are read per axis.  A row with a
+ *           negative position is a row of the padded batch: it is neither read nor
+ *           written.
+ *   n_axes: 1 .. 4 (time, height, width ...); axes: [rotary_dim / 2] uint8, the axis of each
+ *           frequency's position, not read with one axis (an axis that does not exist counts
+ *           as 0: DFLASH_DEV_BAD_VALUE).
+ *   turns:  [rotary_dim / 2] uint64 in device memory, of dflash_rope_turns.
+ * Everything is FP32, rounded once to `type`.  DFLASH_DEV_NONFINITE: an infinity
+ * or a NaN among a row's values.  One launch. */
+int dflash_qk_norm_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride, int32_t n_q_heads,
+                        const void* k, void* k_out, int64_t k_stride, int64_t k_out_stride, int32_t n_k_heads,
+                        int32_t head_dim, int32_t type, int32_t n_rows, const float* q_weight, const float* k_weight,
+                        float eps, const int32_t* positions, int64_t position_stride, int32_t n_axes,
+                        const uint8_t* axes, const uint64_t* turns, int32_t rotary_dim, int32_t* dev_status,
+                        dflash_stream_t stream);
 
 #ifdef __cplusplus
 }
