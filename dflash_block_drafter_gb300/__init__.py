@@ -139,6 +139,9 @@ _SIGS = {
     "dflash_rope_turns": (ctypes.c_int, [_P, _I, _P]),
     "dflash_qk_norm_rope": (ctypes.c_int, [_P, _P, _L, _L, _I, _P, _P, _L, _L, _I, _I, _I, _I, _P, _P, ctypes.c_float,
                                            _P, _L, _I, _P, _P, _I, _P, _P]),
+    "dflash_kv4_prefix_attention": (ctypes.c_int, [_KV4, _P, _P, _I, _L, _L, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
+                                                   _P, _I, _I, ctypes.c_float, _P, _Z, _P, _P]),
+    "dflash_kv4_prefix_attention_workspace": (_Z, [_KV4, _I, _I, _I, _I, _I, _I, _I]),
 }
 
 
@@ -442,3 +445,28 @@ def dflash_qk_norm_rope(q: int, q_out: int, q_stride: int, q_out_stride: int, n_
                                               n_rows, q_weight or None, k_weight or None, eps, positions or None,
                                               position_stride, n_axes, axes or None, turns or None, rotary_dim,
                                               dev_status or None, stream or None), "dflash_qk_norm_rope")
+
+
+def dflash_kv4_prefix_attention(cache: DflashKv4Cache, q: int, out: int, value_type: int, q_stride: int,
+                                out_stride: int, n_tokens: int, n_q_heads: int, n_groups: int, group_offsets: int,
+                                prefix_len: int, prefix_table: int, prefix_stride: int, n_seq: int, max_rows: int,
+                                row_offsets: int, kv_len: int, table: int, table_stride: int, causal: bool,
+                                scale: float, workspace: int, workspace_bytes: int, dev_status: int = 0,
+                                stream: int = 0) -> None:
+    if (n_tokens | n_q_heads | n_groups | prefix_stride | n_seq | max_rows | table_stride) >> 31:  # negative or wide
+        _refuse_wide("dflash_kv4_prefix_attention", n_tokens, n_q_heads, n_groups, prefix_stride, n_seq, max_rows,
+                     table_stride)
+    _check(load_library().dflash_kv4_prefix_attention(ctypes.byref(cache), q, out, value_type, q_stride, out_stride,
+                                                      n_tokens, n_q_heads, n_groups, group_offsets, prefix_len,
+                                                      prefix_table, prefix_stride, n_seq, max_rows, row_offsets, kv_len,
+                                                      table, table_stride, 1 if causal else 0, scale, workspace,
+                                                      workspace_bytes, dev_status or None, stream or None),
+           "dflash_kv4_prefix_attention")
+
+
+def dflash_kv4_prefix_attention_workspace(cache: DflashKv4Cache, n_tokens: int, n_q_heads: int, n_groups: int,
+                                          prefix_stride: int, n_seq: int, max_rows: int, table_stride: int) -> int:
+    if (n_tokens | n_q_heads | n_groups | prefix_stride | n_seq | max_rows | table_stride) >> 31:
+        return 0
+    return load_library().dflash_kv4_prefix_attention_workspace(ctypes.byref(cache), n_tokens, n_q_heads, n_groups,
+                                                                prefix_stride, n_seq, max_rows, table_stride)

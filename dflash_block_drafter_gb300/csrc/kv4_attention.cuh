@@ -17,6 +17,13 @@
 //
 // The lengths are on the device, so every CTA forms the plan itself (prefix
 // sums over at most kKv4MaxSeq sequences).
+//
+// Attention over a shared prefix takes two passes of the same kernels.  In the first
+// (kKv4Prefix) the sequences are groups of requests: all rows of a group read the cells
+// of the group's prefix, in segments of as many whole tokens as a CTA takes,
+// the segments of one kv head side by side.  It leaves each row's maximum, sum and
+// unnormalised O in `pre`.  The second (kKv4Own) is the attention of each request
+// over its own cells, which joins them with `pre` where a row is written.
 #pragma once
 
 #include "common.cuh"
@@ -102,6 +109,9 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 // score, 32767 cells 2^-25.5 below another were lost).
 constexpr float kKv4Slack = 15.f, kKv4Lift = 7.f;
 
+// A call, or the passes of one over a shared prefix (above).
+enum Kv4Mode { kKv4Plain, kKv4Prefix, kKv4Own };
+
 struct Kv4Job;
 
 struct Kv4AttnArgs {
@@ -122,6 +132,12 @@ struct Kv4AttnArgs {
   float2* part_ml;   // [2 C][R]: maximum (log2 units) and sum
   Kv4Job* jobs;  // [C]
   int32_t* status;
+  // over a shared prefix; in its first pass n_seq, kv_len and table are those of the groups
+  const int32_t* group_offsets;  // [n_seq + 1] sequences
+  int n_all;       // sequences
+  int per_segment;  // tokens of a segment
+  float* pre;       // [n_tokens, n_q heads, D]
+  float2* pre_ml;   // [n_tokens, n_q heads]: maximum (log2 units) and sum
 };
 
 // What sequence s asks for.
@@ -132,15 +148,27 @@ struct Kv4Seq {
   int steps;
 };
 
-template <int STEP>
+template <int STEP, int MODE>
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool report) {
   Kv4Seq q;
-  q.r0 = a.row_offsets[s];
-  const int r1 = a.row_offsets[s + 1];
-  q.rows = r1 - q.r0;
-  if (q.r0 < 0 || r1 > a.n_tokens || r1 < q.r0 || q.rows > a.max_rows) {
-    if (report) set_status(a.status, DFLASH_DEV_BAD_BLOCK);
-    q.rows = 0;
+  if constexpr (MODE == kKv4Prefix) {
+    const int g0 = a.group_offsets[s], g1 = a.group_offsets[s + 1];
+    const bool apart = (s == 0 && g0 != 0) || (s == a.n_seq - 1 && g1 != a.n_all);  // sequences of no group
+    const bool bad = g0 < 0 || g1 < g0 || g1 > a.n_all;
+    q.r0 = bad ? 0 : a.row_offsets[g0];
+    const int r1 = bad ? 0 : a.row_offsets[g1];
+    q.rows = r1 - q.r0;
+    if (q.r0 < 0 || r1 > a.n_tokens || r1 < q.r0) q.rows = -1;
+    if (report && (bad || apart || q.rows < 0)) set_status(a.status, DFLASH_DEV_BAD_BLOCK);
+    q.rows = max(q.rows, 0);
+  } else {
+    q.r0 = a.row_offsets[s];
+    const int r1 = a.row_offsets[s + 1];
+    q.rows = r1 - q.r0;
+    if (q.r0 < 0 || r1 > a.n_tokens || r1 < q.r0 || q.rows > a.max_rows) {
+      if (report) set_status(a.status, DFLASH_DEV_BAD_BLOCK);
+      q.rows = 0;
+    }
   }
   const long long cap = static_cast<long long>(a.table_stride) << a.page_shift;
   int kv = a.kv_len[s];
@@ -166,15 +194,36 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool repo
 __device__ __forceinline__ uint32_t kv4_per_token(int G) { return ((1u << 17) + G - 1) / G; }
 __device__ __forceinline__ int kv4_token(int x, uint32_t per_g) { return static_cast<int>(static_cast<uint32_t>(x) * per_g >> 17); }
 
+// Segments of a sequence.
+template <int MODE>
+__device__ __forceinline__ int kv4_segments(const Kv4AttnArgs& a, int rows) {
+  if constexpr (MODE == kKv4Prefix) return a.n_kv * ((rows + a.per_segment - 1) / a.per_segment);
+  return a.n_kv;
+}
+
+// Row of `pre` of a token's head x of kv head `head`.
+__device__ __forceinline__ size_t kv4_pre_row(const Kv4AttnArgs& a, int token, int head, int x) {
+  return static_cast<size_t>(token) * (a.n_kv * a.G) + head * a.G + x;
+}
+// What brings a row's own results (maximum m, sum l) and its prefix's together: factors of both O,
+// normalised; the sum of weights in l.
+__device__ __forceinline__ float2 kv4_join(float m, float& l, float2 pre) {
+  const float top = fmaxf(m, pre.x), from = top == -INFINITY ? 0.f : top;
+  const float f = ex2_approx(m - from), g = ex2_approx(pre.x - from);
+  l = l * f + pre.y * g;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  return make_float2(f * inv, g * inv);
+}
+
 // Visible cells [lo, hi) of token i of the sequence.
 __device__ __forceinline__ int2 kv4_sees(const Kv4AttnArgs& a, const Kv4Seq& q, int i) {
   const int upto = a.causal ? q.kv - q.rows + i + 1 : q.kv;  // behind the row's own position
   return make_int2(a.window > 0 && upto > a.window ? upto - a.window : 0, max(upto, 0));
 }
 
-// Prefix sums of the sequences' units (over kv heads) in
+// Prefix sums of the sequences' units (over their segments) in
 // `pre` [n_seq + 1] by the whole CTA; returns the total.
-template <int STEP, int OV>
+template <int STEP, int OV, int MODE>
 __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* pre, long long* scratch, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
   long long carry = 0;
@@ -182,8 +231,8 @@ __device__ __forceinline__ long long kv4_plan(const Kv4AttnArgs& a, long long* p
     const int s = s0 + tid;
     long long v = 0;
     if (s < a.n_seq) {
-      const Kv4Seq q = kv4_seq<STEP>(a, s, report);
-      if (q.rows > 0) v = static_cast<long long>(q.steps + OV) * a.n_kv;
+      const Kv4Seq q = kv4_seq<STEP, MODE>(a, s, report);
+      if (q.rows > 0) v = static_cast<long long>(q.steps + OV) * kv4_segments<MODE>(a, q.rows);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -222,18 +271,22 @@ struct Kv4Part {
   Kv4Seq q;
   int s, head, rows, k0, n;  // rows: query rows
   long long end, next;  // units: the segment's end; where this part ends
+  // over a prefix, where q is the segment's: its number in the group, and the group's tokens
+  int segment, r0, tokens;
 };
 // The first part with a tile in [at, x_end).  `hint`: the part before it, which ended at
 // `at` (or a zeroed one for a CTA's first part, which may begin anywhere in a segment).
-template <int STEP, int OV>
+template <int STEP, int OV, int MODE>
 __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long long* pre, long long at, long long x_end,
                                             const Kv4Part& hint) {
   Kv4Part p = hint;
   p.n = 0;
   p.next = x_end;
   if (at >= x_end) return p;
+  constexpr bool PREFIX = MODE == kKv4Prefix;
+  int& segment = PREFIX ? p.segment : p.head;
   const bool first = hint.n == 0;
-  if (first || ++p.head == a.n_kv) {  // another sequence
+  if (first || ++segment == kv4_segments<MODE>(a, PREFIX ? p.tokens : 1)) {  // another sequence
     int lo = 0, hi = a.n_seq - 1;
     if (!first && pre[p.s + 1] <= at && at < pre[p.s + 2]) lo = hi = p.s + 1;
     while (lo < hi) {
@@ -242,20 +295,28 @@ __device__ __forceinline__ Kv4Part kv4_part(const Kv4AttnArgs& a, const long lon
       else lo = mid + 1;
     }
     p.s = lo;
-    p.q = kv4_seq<STEP>(a, lo, false);
-    p.head = 0;
+    p.q = kv4_seq<STEP, MODE>(a, lo, false);
+    segment = 0;
+    if (PREFIX) p.r0 = p.q.r0, p.tokens = p.q.rows;
   }
   const int units = p.q.steps + OV;
   long long begin = at;
   if (first) {
     const long long rel = at - pre[p.s];
-    p.head = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
-    begin = pre[p.s] + static_cast<long long>(p.head) * units;
+    segment = rel >> 32 ? static_cast<int>(rel / units) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(units));
+    begin = pre[p.s] + static_cast<long long>(segment) * units;
   }
   p.end = begin + units;
   p.next = p.end < x_end ? p.end : x_end;
   p.k0 = max(static_cast<int>(at - begin) - OV, 0);
   p.n = max(static_cast<int>(p.next - begin) - OV, 0) - p.k0;  // 0: the range ends before the segment's first tile
+  if constexpr (PREFIX) {
+    const int of_head = (p.tokens + a.per_segment - 1) / a.per_segment;
+    p.head = segment / of_head;
+    const int skip = (segment - p.head * of_head) * a.per_segment;
+    p.q.r0 = p.r0 + skip;
+    p.q.rows = min(p.tokens - skip, a.per_segment);
+  }
   p.rows = p.q.rows * a.G;
   return p;
 }
@@ -276,7 +337,7 @@ struct Kv4Job {
 constexpr int kMergeThreads = 256;
 constexpr int kFewPieces = 8;
 
-template <int D, int R>
+template <int D, int R, int MODE>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnArgs a, int most) {
   constexpr int E = D / 32, WARPS = kMergeThreads / 32, U = D == 256 ? 4 : 8;
   __shared__ int s_count[WARPS];
@@ -364,6 +425,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) t = fmaxf(t, accl[w].x);
       const float from = t == -INFINITY ? 0.f : t;
+      top = t;
       l = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -375,8 +437,38 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
         for (int e = 0; e < E; ++e) o[e] = fmaf(f, acc[w][e * 32 + lane], o[e]);
       }
     }
+    float inv = l > 0.f ? 1.f / l : 0.f;
+    if constexpr (MODE != kKv4Plain) {
+      const size_t at = kv4_pre_row(a, j0.x + m / a.G, j0.y, m % a.G);
+      float* pre = a.pre + at * D;
+      float2 f = make_float2(1.f, 0.f);
+      if constexpr (MODE == kKv4Own) f = kv4_join(top, l, __ldcg(a.pre_ml + at));
+      else if (lane == 0) __stcg(a.pre_ml + at, make_float2(top, l));
+#pragma unroll
+      for (int e = 0; e < E; e += (E < 4 ? 2 : 4)) {
+        if constexpr (E < 4) {
+          float2* x = reinterpret_cast<float2*>(pre) + lane;
+          if constexpr (MODE == kKv4Prefix) {
+            __stcg(x, make_float2(o[0], o[1]));
+          } else {
+            const float2 y = __ldcg(x);
+            o[0] = o[0] * f.x + y.x * f.y, o[1] = o[1] * f.x + y.y * f.y;
+          }
+        } else {
+          float4* x = reinterpret_cast<float4*>(pre) + (e >> 2) * 32 + lane;
+          if constexpr (MODE == kKv4Prefix) {
+            __stcg(x, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+          } else {
+            const float4 y = __ldcg(x);
+            o[e] = o[e] * f.x + y.x * f.y, o[e + 1] = o[e + 1] * f.x + y.y * f.y;
+            o[e + 2] = o[e + 2] * f.x + y.z * f.y, o[e + 3] = o[e + 3] * f.x + y.w * f.y;
+          }
+        }
+      }
+      inv = 1.f;
+    }
     if (!(l < INFINITY) && lane == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if constexpr (MODE == kKv4Prefix) continue;
     uint16_t* dst = a.out + (j0.x + m / a.G) * a.out_stride + (j0.y * a.G + m % a.G) * D;
     auto pack = [&](float x, float y) { return a.bf16 ? pack_bf16x2(x * inv, y * inv) : pack_f16x2(x * inv, y * inv); };
     if constexpr (E < 4) {
@@ -391,7 +483,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
 
 // Launches the merge behind an attention kernel of `most` CTAs, of which at
 // most `jobs` segments can be split.
-template <int D, int R>
+template <int D, int R, int MODE>
 cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   // few segments: one block per row, which many pieces want; many: at least one warp per row
@@ -404,10 +496,37 @@ cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, R>, a, most);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, R, MODE>, a, most);
 }
 
-// kv4_attention_tc.cu: up to 128 rows, tiles of 64 cells at 256 channels, else of 128, one CTA per SM.
+// What the host knows of a call: its kernel, CTAs and split segments at most.
+struct Kv4Shape {
+  bool tc;    // the tcgen05 kernel: up to 128 query rows a segment
+  int nt;     // else: 8-row tiles of them
+  int most, jobs;
+  int rows() const { return tc ? 128 : 8 * nt; }
+};
+// Checks of what both kinds of call have, and the shape of one over the requests' own cells
+// (kv4_attention.cu).
+int kv4_check_call(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride);
+cudaError_t kv4_shape_of(const dflash_kv4_cache* c, int n_q_heads, int n_seq, int max_rows, int table_stride, Kv4Shape* out);
+// CTAs of the tcgen05 kernel for so many segments.
+cudaError_t kv4_tc_shape(const dflash_kv4_cache* c, long long segments, int table_stride, Kv4Shape* out);
+// Workspace of a pass: its jobs and pieces.
+inline size_t kv4_pass_bytes(const dflash_kv4_cache* c, const Kv4Shape& s) {
+  return s.most * (sizeof(Kv4Job) + 2 * size_t(s.rows()) * (c->head_dim * 4 + 8));
+}
+inline void kv4_set_workspace(Kv4AttnArgs& a, const dflash_kv4_cache* c, const Kv4Shape& s, void* workspace) {
+  a.jobs = static_cast<Kv4Job*>(workspace);
+  a.part = reinterpret_cast<float*>(a.jobs + s.most);
+  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(2 * s.most) * s.rows() * c->head_dim);
+}
+
+// The tcgen05 kernel (kv4_attention_tc.cuh): up to 128 rows, tiles of 64 cells at 256 channels, else of
+// 128, one CTA per SM; of a plain call (kv4_attention_tc.cu) and of the passes of one over a shared prefix
+// (kv4_prefix_attention_tc.cu).
 cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st);
+cudaError_t launch_kv4_attn_tc_prefix(int d, const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st);
+cudaError_t launch_kv4_attn_tc_own(int d, const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st);
 
 }  // namespace dflash

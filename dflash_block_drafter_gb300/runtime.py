@@ -17,7 +17,8 @@ from . import (DFLASH_ERR_INVALID_ARG, DFLASH_MAX_BLOCK, DFLASH_T_BF16, DFLASH_T
                dflash_state_read_draft_probs, dflash_state_set_spec_min_p, dflash_state_write_kv, load_library,
                dflash_state_set_defer_kv, dflash_state_flush,
                dflash_kv4_attention, dflash_kv4_attention_workspace, dflash_kv4_bytes, dflash_kv4_read,
-               dflash_kv4_write, dflash_page_tables, dflash_qk_norm_rope, dflash_rope_turns, dflash_token_logprobs,
+               dflash_kv4_prefix_attention, dflash_kv4_prefix_attention_workspace, dflash_kv4_write,
+               dflash_page_tables, dflash_qk_norm_rope, dflash_rope_turns, dflash_token_logprobs,
                make_config, make_weights)
 
 
@@ -449,3 +450,45 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
                         0 if axes is None else axes.data_ptr(), 0 if turns is None else turns.data_ptr(), 2 * half,
                         0 if status is None else status.data_ptr(), _current(dev))
     return q_out, k_out
+
+
+def kv4_prefix_attention(cache: torch.Tensor, q: torch.Tensor, prefix_table: torch.Tensor, prefix_len: torch.Tensor,
+                         group_offsets: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
+                         row_offsets: torch.Tensor, max_rows: int, causal: bool = True, scale: Optional[float] = None,
+                         out=None, workspace=None, status=None, stream=None) -> torch.Tensor:
+    """Attention of rows q [tokens, n_q_heads, head_dim] over the prefix that
+    their group of sequences shares and the cells of their own sequence, which
+    `table` and `kv_len` describe; else as kv4_attention."""
+    c, dev = _kv4(cache), cache.device
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv4_prefix_attention(cache, q, prefix_table, prefix_len, group_offsets, table, kv_len, row_offsets,
+                                        max_rows, causal, scale, out, workspace, status)
+    qs = _row_stride(q, dev, "kv4_prefix_attention q")
+    _int32(dev, "kv4_prefix_attention", prefix_table, prefix_len, group_offsets, table, kv_len, row_offsets, status)
+    tokens, heads, d = q.shape
+    n, groups = kv_len.numel(), prefix_len.numel()
+    if (d != c.head_dim or table.dim() != 2 or table.shape[0] != n or row_offsets.numel() != n + 1
+            or prefix_table.dim() != 2 or prefix_table.shape[0] != groups or group_offsets.numel() != groups + 1):
+        _refuse("kv4_prefix_attention: shapes")
+    if out is None:
+        out, os_ = torch.empty((tokens, heads, d), dtype=q.dtype, device=dev), heads * d
+    else:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            _refuse("kv4_prefix_attention: out")
+        os_ = _row_stride(out, dev, "kv4_prefix_attention out")
+    if workspace is None:
+        size = dflash_kv4_prefix_attention_workspace(c, tokens, heads, groups, prefix_table.shape[1], n, max_rows,
+                                                     table.shape[1])
+        workspace = torch.empty(size + 16, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != dev or not workspace.is_contiguous():
+            _refuse("kv4_prefix_attention: workspace")
+    dflash_kv4_prefix_attention(c, q.data_ptr(), out.data_ptr(), _VALUE_TYPES[q.dtype], qs, os_, tokens, heads, groups,
+                                group_offsets.data_ptr(), prefix_len.data_ptr(), prefix_table.data_ptr(),
+                                prefix_table.shape[1], n, max_rows, row_offsets.data_ptr(), kv_len.data_ptr(),
+                                table.data_ptr(), table.shape[1], causal, d ** -0.5 if scale is None else scale,
+                                workspace.data_ptr(), size, 0 if status is None else status.data_ptr(), _current(dev))
+    return out

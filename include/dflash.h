@@ -597,6 +597,35 @@ int dflash_qk_norm_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_
                         const uint8_t* axes, const uint64_t* turns, int32_t rotary_dim, int32_t* dev_status,
                         dflash_stream_t stream);
 
+/* Attention of n_seq sequences in n_groups groups, the sequences of a group
+ * beginning with the same cells (instructions, a document, the prompt of several
+ * samples): those are computed once for all rows of the group.
+ *   group_offsets: [n_groups + 1] int32: group g's sequences are
+ *           [group_offsets[g], group_offsets[g + 1]); the groups hold all n_seq sequences in
+ *           order.  A sequence that shares nothing is in a group without a prefix.
+ *   prefix_len: [n_groups] int32, cells of each group's prefix (any number; negative: none).
+ *   prefix_table: [n_groups, prefix_stride] int32, their page ids.
+ *   kv_len, table: as for dflash_kv4_attention, but of each sequence's own cells, which
+ *           follow the prefix: cell j lies at position prefix_len + j.  causal is about
+ *           these alone; every row sees the whole prefix.
+ * All else as for dflash_kv4_attention without a window, the roundings too (over the
+ * prefix those of more than 32 rows per kv head).  n_groups <= 1024, prefix_stride * page_size <=
+ * 2^31 - 256 and n_tokens * n_q_heads < 2^31 (else DFLASH_ERR_CAPACITY).
+ * DFLASH_DEV_BAD_BLOCK also for group_offsets that descend or leave sequences out; the rows of
+ * such a group, of one whose row_offsets are refused, and of sequences left out are unspecified.
+ *   workspace: dflash_kv4_prefix_attention_workspace bytes, as there. */
+int dflash_kv4_prefix_attention(const dflash_kv4_cache* cache, const void* q, void* out, int32_t type, int64_t q_stride,
+                                int64_t out_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_groups,
+                                const int32_t* group_offsets, const int32_t* prefix_len, const int32_t* prefix_table,
+                                int32_t prefix_stride, int32_t n_seq, int32_t max_rows, const int32_t* row_offsets,
+                                const int32_t* kv_len, const int32_t* table, int32_t table_stride, int32_t causal,
+                                float scale, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                dflash_stream_t stream);
+/* Workspace of such a call on the current device (0: arguments it refuses). */
+size_t dflash_kv4_prefix_attention_workspace(const dflash_kv4_cache* cache, int32_t n_tokens, int32_t n_q_heads,
+                                             int32_t n_groups, int32_t prefix_stride, int32_t n_seq, int32_t max_rows,
+                                             int32_t table_stride);
+
 #ifdef __cplusplus
 }
 #endif

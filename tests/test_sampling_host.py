@@ -7,7 +7,7 @@ from fractions import Fraction
 import pytest
 
 import dflash_block_drafter_gb300 as D
-from test_verify_host import FAKE, P, lib  # noqa: F401
+from test_verify_host import FAKE, P, _cache, lib  # noqa: F401
 
 INV, UNS, CAP = D.DFLASH_ERR_INVALID_ARG, D.DFLASH_ERR_UNSUPPORTED, D.DFLASH_ERR_CAPACITY
 WIDE = [2 ** 32, 2 ** 32 + 8, 2 ** 31, -2 ** 32 + 8]
@@ -65,10 +65,51 @@ def test_norm_rope_sizes_beyond_32_bits(lib, size):  # noqa: F811
         assert refused(lambda: D.dflash_qk_norm_rope(*args)) == INV, name
 
 
+# --------------------------------------------------------------- shared prefixes
+GOOD_PREFIX = dict(c=ctypes.byref(_cache()), q=FAKE, out=FAKE, type=D.DFLASH_T_BF16, qs=1024, os=1024, tokens=4, nq=8, groups=1, goff=FAKE, plen=FAKE, ptable=FAKE,
+                   pwidth=4, n_seq=2, rows=2, off=FAKE, kv=FAKE, table=FAKE, width=4, causal=1, scale=0.1, ws=FAKE, wsb=1 << 40, st=None, stream=None)
+
+
+def test_prefix_attention_refusals(lib):  # noqa: F811
+    def call(**kw):
+        return lib.dflash_kv4_prefix_attention(*{**GOOD_PREFIX, **kw}.values())
+
+    for kw in (dict(q=None), dict(out=None), dict(goff=None), dict(plen=None), dict(ptable=None), dict(off=None), dict(kv=None), dict(table=None),
+               dict(q=P(4104)), dict(out=P(4104)), dict(qs=1016), dict(os=1016), dict(qs=1028), dict(os=1028), dict(tokens=-1), dict(nq=7), dict(nq=0),
+               dict(groups=0), dict(groups=-1), dict(pwidth=0), dict(n_seq=0), dict(rows=0), dict(rows=9), dict(width=0), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=math.nan), dict(scale=math.inf), dict(scale=3e38)):
+        assert call(**kw) == INV, kw
+    assert call(type=D.DFLASH_T_FP32) == UNS
+    assert call(nq=34, rows=8, qs=34 * 128, os=34 * 128) == UNS  # 17 heads of a group x 8 rows > 128
+    for kw in (dict(groups=1025), dict(n_seq=1025), dict(pwidth=1 << 25), dict(width=1 << 25), dict(tokens=1 << 28)):
+        assert call(**kw) == CAP, kw
+    assert call(tokens=0) == D.DFLASH_OK
+    work = dict(n_tokens=4, n_q_heads=8, n_groups=1, prefix_stride=4, n_seq=2, max_rows=2, table_stride=4)
+    for kw in (dict(n_q_heads=7), dict(n_groups=0), dict(n_groups=1025), dict(prefix_stride=1 << 25), dict(n_tokens=-1)):
+        assert D.dflash_kv4_prefix_attention_workspace(_cache(), **{**work, **kw}) == 0
+    assert D.dflash_kv4_prefix_attention_workspace(_cache(head_dim=96), **work) == 0
+    for bad, want in ((dict(data=4104), INV), (dict(head_dim=96), UNS)):
+        assert call(c=ctypes.byref(_cache(**bad))) == want
+
+
+@pytest.mark.parametrize("size", WIDE)
+def test_prefix_attention_sizes_beyond_32_bits(lib, size):  # noqa: F811
+    for name in ("tokens", "nq", "groups", "pwidth", "n_seq", "rows", "width"):
+        args = {**GOOD_PREFIX, "c": _cache(), name: size}
+        args = [a.value if isinstance(a, ctypes.c_void_p) else 0 if a is None else a for a in args.values()]
+        assert refused(lambda: D.dflash_kv4_prefix_attention(*args)) == INV, name
+    work = dict(n_tokens=4, n_q_heads=8, n_groups=1, prefix_stride=4, n_seq=2, max_rows=2, table_stride=4)
+    for name in work:
+        assert D.dflash_kv4_prefix_attention_workspace(_cache(), **{**work, name: size}) == 0
+
+
 def test_torch_wrappers_refuse():
     torch = pytest.importorskip("torch")
     from dflash_block_drafter_gb300 import runtime as R
     rows = torch.zeros((1, 1, 64), dtype=torch.bfloat16)  # on the CPU
     one = torch.zeros(1, dtype=torch.int32)
-    for call in (lambda: R.qk_norm_rope(rows, rows, one, torch.zeros(32, dtype=torch.int64)),):
+    cache = torch.zeros((2, 1, 1, 18 * 64), dtype=torch.uint8)
+    two = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: R.qk_norm_rope(rows, rows, one, torch.zeros(32, dtype=torch.int64)),
+                 lambda: R.kv4_prefix_attention(cache, rows, one[None], one, two, one[None], one, two, 1)):
         assert refused(call) == INV
