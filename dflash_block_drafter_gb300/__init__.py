@@ -142,6 +142,7 @@ _SIGS = {
     "dflash_kv4_prefix_attention": (ctypes.c_int, [_KV4, _P, _P, _I, _L, _L, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
                                                    _P, _I, _I, ctypes.c_float, _P, _Z, _P, _P]),
     "dflash_kv4_prefix_attention_workspace": (_Z, [_KV4, _I, _I, _I, _I, _I, _I, _I]),
+    "dflash_sample_tokens": (ctypes.c_int, [_P, _I, _L, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -470,3 +471,14 @@ def dflash_kv4_prefix_attention_workspace(cache: DflashKv4Cache, n_tokens: int, 
         return 0
     return load_library().dflash_kv4_prefix_attention_workspace(ctypes.byref(cache), n_tokens, n_q_heads, n_groups,
                                                                 prefix_stride, n_seq, max_rows, table_stride)
+
+
+def dflash_sample_tokens(logits: int, value_type: int, row_stride: int, n_rows: int, vocab: int, uniform: int,
+                         temperature: int, top_k: int, top_p: int, min_p: int, tokens: int, logprob: int, kept: int,
+                         dev_status: int = 0, stream: int = 0) -> None:
+    if (n_rows | vocab) >> 31:  # negative or wide
+        _refuse_wide("dflash_sample_tokens", n_rows, vocab)
+    _check(load_library().dflash_sample_tokens(logits, value_type, row_stride, n_rows, vocab, uniform or None,
+                                               temperature or None, top_k or None, top_p or None, min_p or None,
+                                               tokens or None, logprob or None, kept or None, dev_status or None,
+                                               stream or None), "dflash_sample_tokens")

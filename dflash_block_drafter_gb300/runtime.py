@@ -18,7 +18,7 @@ from . import (DFLASH_ERR_INVALID_ARG, DFLASH_MAX_BLOCK, DFLASH_T_BF16, DFLASH_T
                dflash_state_set_defer_kv, dflash_state_flush,
                dflash_kv4_attention, dflash_kv4_attention_workspace, dflash_kv4_bytes, dflash_kv4_read,
                dflash_kv4_prefix_attention, dflash_kv4_prefix_attention_workspace, dflash_kv4_write,
-               dflash_page_tables, dflash_qk_norm_rope, dflash_rope_turns, dflash_token_logprobs,
+               dflash_page_tables, dflash_qk_norm_rope, dflash_rope_turns, dflash_sample_tokens, dflash_token_logprobs,
                make_config, make_weights)
 
 
@@ -492,3 +492,40 @@ def kv4_prefix_attention(cache: torch.Tensor, q: torch.Tensor, prefix_table: tor
                                 table.data_ptr(), table.shape[1], causal, d ** -0.5 if scale is None else scale,
                                 workspace.data_ptr(), size, 0 if status is None else status.data_ptr(), _current(dev))
     return out
+
+
+def sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
+                  status=None, stream=None):
+    """Draw a token from each row of logits [rows, vocab] by the numbers
+    `uniform` [rows] in [0, 1): (tokens [rows], logprob [rows] among the kept
+    tokens, kept [rows]).  temperature, top_p, min_p (float) and top_k (int32)
+    are [rows] tensors on the device, or None (off)."""
+    dev = logits.device
+    kind = _VALUE_TYPES.get(logits.dtype)
+    if not logits.is_cuda or logits.dim() != 2 or kind is None:
+        _refuse("sample_tokens: [rows, vocab] logits on a CUDA device")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return sample_tokens(logits, uniform, temperature, top_k, top_p, min_p, status)
+    n, vocab = logits.shape
+    stride, by_value = logits.stride()
+    if by_value != 1 and vocab != 1:
+        _refuse("sample_tokens: dense rows")
+    at = []
+    for x in (uniform, temperature, top_p, min_p):
+        if x is None:
+            at.append(0)
+            continue
+        if x.dtype != torch.float32 or x.device != dev or x.numel() != n or not x.is_contiguous():
+            _refuse("sample_tokens: one contiguous float of the device of the call per row")
+        at.append(x.data_ptr())
+    _int32(dev, "sample_tokens", top_k, status)
+    if top_k is not None and top_k.numel() != n:
+        _refuse("sample_tokens: one top_k per row")
+    out = torch.empty((3, n), dtype=_INT32, device=dev)
+    to = out.data_ptr()
+    dflash_sample_tokens(logits.data_ptr(), kind, stride if n > 1 else vocab, n, vocab, at[0], at[1],
+                         0 if top_k is None else top_k.data_ptr(), at[2], at[3], to, to + 4 * n, to + 8 * n,
+                         0 if status is None else status.data_ptr(), _current(dev))
+    return out[0], out[1].view(torch.float32), out[2]

@@ -626,6 +626,37 @@ size_t dflash_kv4_prefix_attention_workspace(const dflash_kv4_cache* cache, int3
                                              int32_t n_groups, int32_t prefix_stride, int32_t n_seq, int32_t max_rows,
                                              int32_t table_stride);
 
+/* Tokens drawn from n_rows rows of logits (types, strides and alignment as for
+ * dflash_token_logprobs), one number of `uniform` each.  Row i's weights are
+ * w = exp((x - max) / temperature).  Of the tokens
+ *   top_k keeps those whose logit is not below the k-th largest (0 or less, or vocab and more: all);
+ *   top_p keeps of these the ones above which less than top_p of their weight lies
+ *         (1 or more: all; 0 or less: the largest);
+ *   min_p keeps those with w >= min_p (0 or less: all).
+ * Tokens of equal logits are kept or left out together, and a masked one (-infinity) is
+ * never kept.  The token is the first, in order of ids, with which the kept
+ * weights exceed uniform times all of them: the one of the definition in 64 bits, sums and
+ * thresholds (weights are right to about 2^-43, and equal on every call).
+ *   uniform: [n_rows] float in [0, 1).
+ *   temperature, top_k (int32), top_p, min_p: [n_rows] in device memory, each or NULL (1, 0,
+ *            1, 0).  A temperature of 0 is the greedy choice: the first id of the largest logit.
+ *   tokens:  [n_rows] int32 out.  -1 where every token is masked.
+ *   logprob: optional [n_rows] float out, of the token among the kept ones (greedy: 0; no
+ *            token: -infinity).
+ *   kept:    optional [n_rows] int32 out, tokens kept (greedy: 1).
+ * A row of a verify window drawn this way makes dflash_accept exact for
+ * sampling: the draft is a fixed proposal, and accepting it where it equals a draw
+ * from the target's distribution, else continuing with the draw, is that
+ * distribution.
+ * DFLASH_DEV_BAD_VALUE: uniform outside [0, 1) (the nearest is taken), temperature
+ * negative or NaN (greedy) or above 2^64 (2^64), top_p NaN (off), min_p NaN (off) or above 1 (1).
+ * DFLASH_DEV_NONFINITE: a NaN or +infinity in the row, whose token is -1.  vocab <=
+ * 2^19, n_rows <= 2^24 (else DFLASH_ERR_CAPACITY).  One launch. */
+int dflash_sample_tokens(const void* logits, int32_t type, int64_t row_stride, int32_t n_rows, int32_t vocab,
+                         const float* uniform, const float* temperature, const int32_t* top_k, const float* top_p,
+                         const float* min_p, int32_t* tokens, float* logprob, int32_t* kept, int32_t* dev_status,
+                         dflash_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

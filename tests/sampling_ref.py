@@ -44,3 +44,53 @@ def norm_rope(x, weight, eps, angle):
         z[..., :h], z[..., h:2 * h] = a * c - b * s, b * c + a * s
         size[..., :h] = size[..., h:2 * h] = np.abs(a) + np.abs(b)
     return z, size
+
+
+# --------------------------------------------------------------------- sampling
+def sample(x, uniform, temperature=None, top_k=None, top_p=None, min_p=None):
+    """(tokens, log probabilities, kept, how near a decision is to its border, relative to the weights it is about) of rows x [n, vocab]
+    in 64 bits."""
+    n, vocab = x.shape
+    tokens, logp, kept, near = np.full(n, -1), np.full(n, -np.inf), np.zeros(n, int), np.ones(n)
+    for i in range(n):
+        t = 1.0 if temperature is None else float(temperature[i])
+        k = 0 if top_k is None else int(top_k[i])
+        p = 1.0 if top_p is None else float(top_p[i])
+        low = 0.0 if min_p is None else float(min_p[i])
+        row = np.asarray(x[i], np.float64)
+        live = row > -np.inf
+        if not live.any():
+            continue
+        m = row.max()
+        if t == 0:
+            tokens[i], logp[i], kept[i] = int(np.argmax(row)), 0.0, 1
+            continue
+        with np.errstate(over="ignore", invalid="ignore"):
+            z = np.where(live, (row - m) / t, -np.inf)
+        w = np.exp(z)
+        if 0 < k < vocab:
+            live &= row >= np.partition(row, vocab - k)[vocab - k]
+        if p < 1:
+            levels, which = np.unique(row[live], return_inverse=True)
+            mass = np.bincount(which, w[live])
+            above = mass[::-1].cumsum()[::-1] - mass
+            above[-1] = 0
+            total = mass.sum()
+            fits = above < p * total
+            fits[-1] = True
+            near[i] = min(near[i], np.abs(above[above > 0] / total - p).min(initial=1.0))
+            live &= row >= levels[fits].min()
+        if low > 0:
+            with np.errstate(divide="ignore"):
+                near[i] = min(near[i], np.abs(z[live & (z < 0)] - np.log(low)).min(initial=1.0))
+            live &= w >= low
+        w = np.where(live, w, 0)
+        upto = w.cumsum()
+        total = upto[-1]
+        at = float(uniform[i]) * total
+        tokens[i] = int(np.argmax(upto > at))
+        inside = np.abs(upto[live] - at) / total
+        near[i] = min(near[i], inside.min())
+        logp[i] = z[tokens[i]] - np.log(total)
+        kept[i] = live.sum()
+    return tokens, logp, kept, near

@@ -1,0 +1,322 @@
+"""Tokens drawn from logits on the GPU: ids and counts equal to the 64-bit form's (sampling_ref.py) on every row, whatever the filters."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dflash_block_drafter_gb300 as D  # noqa: E402
+import gpu_helpers as H  # noqa: E402
+import sampling_ref as S  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def R():
+    H.need_gpu()
+    H.build_lib()
+    from dflash_block_drafter_gb300 import runtime
+    return runtime
+
+
+def ints(x):
+    return None if x is None else torch.as_tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def floats(x):
+    return None if x is None else torch.as_tensor(np.asarray(x, np.float32), device="cuda")
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def f32(x):
+    return None if x is None else np.asarray(x, np.float32)
+
+
+def check(R, x, uniform, temperature=None, top_k=None, top_p=None, min_p=None, want_status=0, rows=slice(None)):
+    """x: a tensor of logits on the device.  Weights are right to 2^-43 and the form above to 2^-50 or so: what a decision is about lies
+    further apart in these inputs, which `near` shows, or is equal in both."""
+    uniform, temperature, top_p, min_p = (f32(v) for v in (uniform, temperature, top_p, min_p))
+    st = status()
+    token, logp, kept = R.sample_tokens(x, floats(uniform), floats(temperature), ints(top_k), floats(top_p), floats(min_p), status=st)
+    token, logp, kept = (v.cpu().numpy()[rows] for v in (token, logp, kept))
+    assert int(st) == want_status
+    pick = lambda v: None if v is None else np.asarray(v)[rows]  # noqa: E731
+    t, lp, n, near = S.sample(x.double().cpu().numpy()[rows], *(pick(v) for v in (uniform, temperature, top_k, top_p, min_p)))
+    clear = near > 2.0 ** -42
+    assert clear.all() or near[~clear].max() == 0, near.min()
+    assert np.array_equal(token, t), np.flatnonzero(token != t)
+    assert np.array_equal(kept, n), (kept[kept != n], n[kept != n])
+    # an FP32 difference of the logits, its product and a logarithm, 2^-22 each, of a part that may be larger than the result
+    with np.errstate(invalid="ignore"):
+        size = np.abs(lp) + np.abs(np.log(np.maximum(n, 1)))
+        assert np.all((np.abs(logp - lp) <= 2.0 ** -21 * (1 + size)) | (logp == lp))
+    return token, logp, kept
+
+
+def logits(rng, rows, vocab, kind, spread=1.0):
+    z = rng.standard_normal((rows, vocab))
+    x = (2 * z + 0.25 * z ** 3) * spread
+    return torch.as_tensor(x, device="cuda").to(TYPES[kind])
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (5, 7), (4, 33), (9, 1023), (3, 1024), (2, 4099), (70, 5000), (8, 40000), (3, 151936), (200, 30011)])
+@pytest.mark.parametrize("mode", ["plain", "k", "p", "min", "all"])
+def test_draws(R, kind, rows, vocab, mode):
+    rng = np.random.default_rng(rows + vocab)
+    x = logits(rng, rows, vocab, kind, rng.uniform(0.2, 1.0, (rows, 1)))
+    t = rng.uniform(0.3, 1.5, rows)
+    k = np.exp(rng.uniform(0, np.log(vocab + 2), rows)).astype(int) if mode in ("k", "all") else None
+    p = rng.uniform(0.3, 1.0, rows) if mode in ("p", "all") else None
+    low = np.exp(rng.uniform(-12, 0, rows)) if mode in ("min", "all") else None
+    check(R, x, rng.random(rows), t, k, p, low)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [600, 151936])
+def test_settings_by_row(R, kind, vocab):
+    """Each filter on for some rows and off for others, greedy rows among them; filters that keep one token, or all but one."""
+    rng = np.random.default_rng(vocab)
+    n = 48
+    x = logits(rng, n, vocab, kind)
+    t = np.where(rng.random(n) < 0.2, 0, rng.uniform(0.2, 2, n))
+    k = rng.choice([0, -3, 1, 2, 50, vocab - 1, vocab, vocab + 1, 2 ** 31 - 1], n)
+    p = rng.choice([1.0, 2.0, 0.0, -1.0, 1e-9, 0.5, 0.95, 1 - 2.0 ** -24], n)
+    low = rng.choice([0.0, -1.0, 1.0, 1e-30, 0.05], n)
+    check(R, x, rng.random(n), t, k, p, low)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [1, 64, 1024, 32768, 2 ** 19])
+def test_equal_logits(R, kind, vocab):
+    """Weights of 1: the token is the whole part of u times the vocabulary, at its borders too, and no filter parts equals."""
+    x = torch.full((9, vocab), -2.5, dtype=TYPES[kind], device="cuda")
+    step = 1.0 / max(vocab, 4)
+    u = np.array([0, step, 0.25, 0.5, 0.5 - step, 0.75, 1 - step, 1 - 2.0 ** -24, 2.0 ** -30])
+    for kw in ({}, dict(top_k=[1] * 9), dict(top_p=[0.01] * 9), dict(min_p=[1.0] * 9), dict(top_k=[3] * 9, top_p=[0.5] * 9)):
+        token, logp, kept = R.sample_tokens(x, floats(u), floats([0.7] * 9), ints(kw.get("top_k")), floats(kw.get("top_p")), floats(kw.get("min_p")))
+        assert token.tolist() == np.floor(f32(u).astype(float) * vocab).astype(int).tolist()
+        assert kept.tolist() == [vocab] * 9 and np.allclose(logp.cpu().numpy(), -np.log(vocab), rtol=2.0 ** -22, atol=0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_few_levels(R, kind):
+    """Logits of a few values, hundreds of tokens each, zeros of both signs among them."""
+    rng = np.random.default_rng(3)
+    v = rng.choice([-4.0, -1.0, -0.0, 0.0, 0.5, 2.0], (24, 3001))
+    x = torch.as_tensor(v, device="cuda").to(TYPES[kind])
+    check(R, x, rng.random(24), rng.uniform(0.5, 2, 24), rng.integers(1, 3001, 24), rng.uniform(0.05, 1, 24), np.exp(-rng.uniform(0, 8, 24)))
+    zeros = torch.as_tensor(np.where(rng.random((4, 100)) < 0.5, 0.0, -0.0), device="cuda").to(TYPES[kind])
+    assert R.sample_tokens(zeros, floats([0.0] * 4), floats([0.0, 1, 1, 1]), top_k=ints([0, 1, 0, 5]))[0].tolist() == [0] * 4
+
+
+def test_draws_follow_the_distribution(R):
+    """Evenly spaced numbers draw each token as often as its weight says, to one draw."""
+    rng = np.random.default_rng(5)
+    n, vocab = 8192, 500
+    x = logits(rng, 1, vocab, "fp32").repeat(n, 1)
+    u = (np.arange(n) + 0.5) / n
+    token, _, _ = R.sample_tokens(x, floats(u), floats(np.full(n, 0.8)), top_p=floats(np.full(n, 0.9)))
+    got = np.bincount(token.cpu().numpy(), minlength=vocab)
+    _, _, kept, _ = S.sample(x[:1].double().cpu().numpy(), u[:1], [np.float32(0.8)], None, [np.float32(0.9)])
+    row = x[0].double().cpu().numpy()
+    live = row >= np.sort(row)[::-1][kept[0] - 1]
+    w = np.where(live, np.exp((row - row.max()) / np.float64(np.float32(0.8))), 0)
+    assert np.all(np.abs(got - n * w / w.sum()) <= 1)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [300, 40000])
+def test_masks(R, kind, vocab):
+    """Masked tokens are never drawn, by -infinity or the type's lowest value; k counts more than are left; a row with one token, with none."""
+    rng = np.random.default_rng(vocab)
+    n = 12
+    x = logits(rng, n, vocab, kind)
+    for low in (-INF, float(torch.finfo(TYPES[kind]).min)):
+        y = x.clone()
+        y[:, torch.as_tensor(rng.random(vocab) < 0.7, device="cuda")] = low
+        y[3] = low
+        y[3, vocab // 3] = -7.0
+        if low == -INF:
+            y[5] = low
+        t, k, p = rng.uniform(0.4, 1.2, n), rng.choice([0, vocab // 2, vocab - 1, 5], n), rng.uniform(0.5, 1.1, n)
+        token, logp, kept = check(R, y, rng.random(n), t, k, p)
+        assert token[3] == vocab // 3
+        if low == -INF:
+            assert token[5] == -1 and logp[5] == -INF and kept[5] == 0
+        check(R, y, rng.random(n), np.where(np.arange(n) % 2, 0, 0.5))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("stride,first", [(1000, 0), (1001, 1), (1003, 3), (1013, 5)])
+def test_strides(R, kind, stride, first):
+    """Rows that begin anywhere, beside values that are not theirs."""
+    rng = np.random.default_rng(stride)
+    wide = torch.full((11, stride), 1e30, dtype=TYPES[kind], device="cuda")
+    x = wide.view(-1)[: 11 * stride].view(11, stride)[:, first: first + 990]
+    x.copy_(logits(rng, 11, 990, kind))
+    check(R, x, rng.random(11), rng.uniform(0.5, 1, 11), rng.choice([0, 40], 11), rng.choice([0.9, 1.0], 11))
+    check(R, x, rng.random(11), np.zeros(11))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_far_temperatures_and_values(R, kind):
+    rng = np.random.default_rng(9)
+    t = [1e-40, 1e-30, 1e-6, 0.01, 100.0, 1e10, 2.0 ** 64, 1.0]
+    x = logits(rng, 8, 2000, kind)
+    check(R, x, rng.random(8), t)
+    check(R, x, rng.random(8), t, top_p=rng.uniform(0.1, 0.9, 8), top_k=rng.integers(1, 2000, 8))
+    big = torch.as_tensor(rng.choice([-3e38, 3e38, 1e38, -1e38, 0.0], (8, 700)), device="cuda").to(TYPES[kind])
+    check(R, big, rng.random(8), t, top_k=rng.integers(1, 700, 8))
+    check(R, big, rng.random(8), t, top_p=rng.uniform(0.1, 0.9, 8), min_p=[0.1] * 8)
+
+
+def test_reports(R):
+    rng = np.random.default_rng(2)
+    x = logits(rng, 6, 3000, "fp32")
+    u = rng.random(6)
+    for bad in (INF, float("nan")):
+        y = x.clone()
+        y[2, 1234] = bad
+        token, _, _ = check(R, y, u, want_status=D.DFLASH_DEV_NONFINITE, rows=np.array([0, 1, 3, 4, 5]))
+        st = status()
+        assert int(R.sample_tokens(y, floats(u), status=st)[0][2]) == -1 and int(st) == D.DFLASH_DEV_NONFINITE
+    want = R.sample_tokens(x, floats(u), floats([0.8] * 6))[0]
+    others = [0, 1, 3, 4, 5]
+
+    def call(at, **kw):
+        args = {**dict(uniform=u.copy(), temperature=np.full(6, 0.8), top_k=None, top_p=np.ones(6), min_p=np.zeros(6)), **kw}
+        st = status()
+        token = R.sample_tokens(x, floats(args["uniform"]), floats(args["temperature"]), None, floats(args["top_p"]), floats(args["min_p"]), status=st)[0]
+        assert int(st) == D.DFLASH_DEV_BAD_VALUE and torch.equal(token[others], want[others])
+        return int(token[at])
+
+    def put(values, value):
+        values = np.array(values, np.float32)
+        values[2] = value
+        return values
+
+    best = int(x[2].argmax())
+    for t in (-1.0, float("nan")):
+        assert call(2, temperature=put(np.full(6, 0.8), t)) == best  # greedy
+    call(2, temperature=put(np.full(6, 0.8), INF))
+    for w, near in ((-0.5, 0.0), (float("nan"), 0.0), (1.0, 1 - 2.0 ** -24), (INF, 1 - 2.0 ** -24)):
+        st = status()
+        v = put(u, near)
+        assert call(2, uniform=put(u, w)) == int(R.sample_tokens(x, floats(v), floats([0.8] * 6), status=st)[0][2]) and int(st) == 0
+    assert call(2, top_p=put(np.ones(6), float("nan"))) == int(want[2])
+    assert call(2, min_p=put(np.zeros(6), float("nan"))) == int(want[2])
+    assert call(2, min_p=put(np.zeros(6), 1.5)) == best
+
+
+def test_same_result_again(R):
+    rng = np.random.default_rng(4)
+    x = logits(rng, 40, 100003, "bf16")
+    args = (floats(rng.random(40)), floats(rng.uniform(0.5, 1, 40)), ints(rng.choice([0, 30, 5000], 40)), floats(rng.uniform(0.7, 1.1, 40)))
+    first = R.sample_tokens(x, *args)
+    for _ in range(30):
+        for a, b in zip(R.sample_tokens(x, *args), first):
+            assert torch.equal(a, b)
+
+
+def test_graph_and_stream(R):
+    rng = np.random.default_rng(6)
+    x, u, t, k = logits(rng, 16, 9000, "bf16"), floats(rng.random(16)), floats(rng.uniform(0.5, 1, 16)), ints(rng.integers(1, 100, 16))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = R.sample_tokens(x, u, t, k)
+    got = R.sample_tokens(x, u, t, k, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = R.sample_tokens(x, u, t, k)
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        x.copy_(logits(rng, 16, 9000, "bf16"))
+        u.copy_(floats(rng.random(16)))
+        t.copy_(floats(np.where(rng.random(16) < 0.3, 0, rng.uniform(0.5, 1, 16))))
+        k.copy_(ints(rng.choice([0, 10], 16)))
+        graph.replay()
+        token, _, kept, _ = S.sample(x.double().cpu().numpy(), u.cpu().numpy(), t.cpu().numpy(), k.cpu().numpy())
+        assert out[0].tolist() == token.tolist() and out[2].tolist() == kept.tolist()
+
+
+def test_no_rows(R):
+    token, logp, kept = R.sample_tokens(torch.zeros((0, 50), device="cuda"), floats(np.zeros(0)))
+    assert token.shape == logp.shape == kept.shape == (0,)
+
+
+def test_offsets_beyond_32_bits(R):
+    """A row that begins beyond 4 GB."""
+    rng = np.random.default_rng(8)
+    x = torch.full((9000, 2 ** 18), -1.0, dtype=torch.bfloat16, device="cuda")
+    x[-2:] = logits(rng, 2, 2 ** 18, "bf16")
+    u = rng.random(9000)
+    token, _, kept = R.sample_tokens(x, floats(u), top_k=ints(np.full(9000, 64)))
+    t, _, n, _ = S.sample(x[-2:].double().cpu().numpy(), f32(u)[-2:], None, [64, 64])
+    assert token[-2:].tolist() == t.tolist() and kept[-2:].tolist() == n.tolist()
+    assert token[:-2].tolist() == np.floor(f32(u)[:-2].astype(float) * 2 ** 18).astype(int).tolist()
+
+
+def test_sampled_steps_together(R):
+    """Steps of a served model that samples: rotation, cells, attention over a shared prefix, draws, acceptance, the next lengths on the device."""
+    rng = np.random.default_rng(12)
+    n, heads, G, d, page, B, vocab, steps, shared = 6, 2, 4, 64, 16, 4, 900, 5, 50
+    n_pages, width = 160, 20
+    cap = n * B
+    cache = R.kv4_cache(n_pages, page, heads, d)
+    turns = R.rope_turns([1e4 ** (-2.0 * j / d) for j in range(d // 2)])
+    weight = floats(1 + 0.2 * rng.standard_normal(d))
+    status_word = status()
+    # the prefix: pages 0 .. 3, filled as a prompt is
+    prefix = torch.as_tensor(rng.standard_normal((shared, 2 * heads, d)), device="cuda").bfloat16()
+    none = torch.empty((shared, 0, d), dtype=torch.bfloat16, device="cuda")
+    _, pk = R.qk_norm_rope(none, prefix[:, :heads], ints(np.arange(shared)), turns, k_weight=weight, status=status_word)
+    R.kv4_write(cache, pk, prefix[:, heads:], ints(np.arange(shared)), status=status_word)
+    prefix_table, prefix_len, groups = ints(np.arange(4)[None]), ints([shared]), ints([0, n])
+    held, table, ring, state = ints(np.zeros(n)), ints(np.full((n, width), -1)), ints(np.arange(4, n_pages).tolist() + [-1] * 4), ints([0, n_pages - 4])
+    length, accepted, bonus, rows = ints(np.zeros(n)), ints(np.zeros(n)), ints(np.zeros(n)), ints(np.full(n, B))
+    head = torch.as_tensor(rng.standard_normal((vocab, heads * G * d)), device="cuda").float()
+    temperature = floats(np.full(cap, 0.7))
+    drawn = 0
+    for step in range(steps):
+        qkv = torch.as_tensor(rng.standard_normal((cap, heads * G + 2 * heads, d)), device="cuda").bfloat16()
+        before = length.cpu().numpy().copy()
+        off, slots, pos = R.page_tables(length, rows, held, table, ring, state, page, cap, status=status_word)
+        q, k = qkv[:, : heads * G], qkv[:, heads * G: heads * G + heads]
+        q, k = R.qk_norm_rope(q, k, pos + shared, turns, q_weight=weight, k_weight=weight, q_out=q, k_out=k, status=status_word)
+        R.kv4_write(cache, k, qkv[:, heads * G + heads:], slots, status=status_word)
+        o = R.kv4_prefix_attention(cache, q, prefix_table, prefix_len, groups, table, length + rows, off, B, status=status_word)
+        # the same through tables whose first positions are the prefix's cells, cell by cell
+        K, W = R.kv4_read(cache, ints(np.arange(n_pages * page)))
+        K, W = K.double().cpu().numpy(), W.double().cpu().numpy()
+        tab = table.cpu().numpy()
+        for s in range(n):
+            at = np.arange(before[s] + B)
+            cells = np.concatenate([np.arange(shared), tab[s, at // page] * page + at % page])
+            for i in range(B):
+                m = shared + before[s] + i + 1
+                for h in range(heads * G):
+                    x = K[cells[:m], h // G] @ q[s * B + i, h].double().cpu().numpy() / 8.0
+                    p = np.exp(x - x.max())
+                    v = W[cells[:m], h // G]
+                    want, spread = p @ v / p.sum(), p @ np.abs(v) / p.sum()
+                    tol = spread * (2.0 ** -10 + 2.0 ** -10 * (1 + np.abs(x).max())) + m * 2.0 ** -22 + 2.0 ** -8 * np.abs(want)
+                    assert np.all(np.abs(o[s * B + i, h].double().cpu().numpy() - want) <= tol)
+        logits_ = o.float().flatten(1) @ head.t()
+        u = rng.random(cap)
+        token, _, _ = check(R, logits_, u, temperature.cpu().numpy(), top_p=np.full(cap, 0.95))
+        ids = R.sample_tokens(logits_, floats(u), temperature, top_p=floats(np.full(cap, 0.95)), status=status_word)[0]
+        drafts = rng.integers(0, vocab, (n, B - 1)).astype(np.int32)
+        drafts[:, 0] = ids.view(n, B)[:, 0].cpu().numpy()  # the first candidate is what is drawn
+        R.accept(ints(drafts), ids.view(n, B).contiguous(), rows, accepted, bonus, anchor_pos=length)
+        drawn += int(accepted.sum())
+        assert np.array_equal(length.cpu().numpy(), before + accepted.cpu().numpy() + 1)
+        assert np.array_equal(bonus.cpu().numpy(), token.reshape(n, B)[np.arange(n), accepted.cpu().numpy()])
+    assert drawn >= n * steps and int(status_word) == 0

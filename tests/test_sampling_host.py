@@ -103,6 +103,31 @@ def test_prefix_attention_sizes_beyond_32_bits(lib, size):  # noqa: F811
         assert D.dflash_kv4_prefix_attention_workspace(_cache(), **{**work, name: size}) == 0
 
 
+# --------------------------------------------------------------------- sampling
+GOOD_SAMPLE = dict(x=FAKE, type=D.DFLASH_T_BF16, stride=100, n=2, vocab=100, u=FAKE, t=None, k=None, p=None, low=None, tokens=FAKE, lp=None, kept=None,
+                   st=None, stream=None)
+
+
+def test_sample_refusals(lib):  # noqa: F811
+    def call(**kw):
+        return lib.dflash_sample_tokens(*{**GOOD_SAMPLE, **kw}.values())
+
+    for kw in (dict(x=None), dict(x=P(4097)), dict(type=D.DFLASH_T_FP32, x=P(4098)), dict(stride=99), dict(n=-1), dict(vocab=0), dict(u=None),
+               dict(tokens=None)):
+        assert call(**kw) == INV, kw
+    assert call(type=3) == UNS
+    assert call(vocab=(1 << 19) + 1, stride=1 << 20) == CAP and call(n=(1 << 24) + 1) == CAP
+    assert call(n=0) == D.DFLASH_OK
+
+
+@pytest.mark.parametrize("size", WIDE)
+def test_sample_sizes_beyond_32_bits(lib, size):  # noqa: F811
+    for name in ("n", "vocab"):
+        args = {**GOOD_SAMPLE, "stride": 2 ** 34, name: size}
+        args = [a.value if isinstance(a, ctypes.c_void_p) else 0 if a is None else a for a in args.values()]
+        assert refused(lambda: D.dflash_sample_tokens(*args)) == INV, name
+
+
 def test_torch_wrappers_refuse():
     torch = pytest.importorskip("torch")
     from dflash_block_drafter_gb300 import runtime as R
@@ -111,5 +136,6 @@ def test_torch_wrappers_refuse():
     cache = torch.zeros((2, 1, 1, 18 * 64), dtype=torch.uint8)
     two = torch.zeros(2, dtype=torch.int32)
     for call in (lambda: R.qk_norm_rope(rows, rows, one, torch.zeros(32, dtype=torch.int64)),
+                 lambda: R.sample_tokens(torch.zeros((1, 8)), torch.zeros(1)),
                  lambda: R.kv4_prefix_attention(cache, rows, one[None], one, two, one[None], one, two, 1)):
         assert refused(call) == INV
