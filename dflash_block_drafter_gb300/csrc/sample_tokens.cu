@@ -14,10 +14,23 @@
 // sixty times as slow here.
 //
 // The CTAs of a cluster hold a row in their shared memory, so that it is read once
-// from global memory however often it is looked at.  A threshold is found
-// digit by digit: counts (and weights) of up to 1024 ranges of the keys, in which
-// the largest key comes first, then of the ranges of the one in which the
-// threshold lies, until it is one key.
+// from global memory however often it is looked at.  Few tokens decide most rows, and
+// plain FP32 finds them:
+//  - With a filter, a bound below the threshold.  Of top-k: the k-th largest of the threads' own maxima, by a
+//    histogram of them.  Of top-p: the first of 512 ranges of logits below which less than
+//    (1 - p) S can lie, counted with each range's largest weight.  Of min-p: itself.  The
+//    tokens above the bound, if they are at most kList, go to the first CTA, which
+//    sorts them and decides everything with exact weights.  S itself, which a top-p without top-k compares with, comes
+//    from FP32 sums with a bound on their error; where that leaves it open which token is
+//    the last (or which u names, without a filter), S is added up exactly.
+//  - Without one, FP32 sums by CTA, warp and lane lead to the token; the exact ones are formed if a border
+//    of it lies within the error's bound.
+// Else (long lists) a threshold is found digit by digit: counts (and exact weights) of up to
+// 1024 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key.
+//
+// The bound of an FP32 sum, relative to S, in units of 2^-24: a weight's exponent y = (x - m) c is off by 3 |y| (difference, c,
+// product), and the mean of |y| over the weights, their entropy less log2 S, is 19 at most for 2^19 tokens: 40 with ln 2;
+// 2^y 4; additions, of 16 pieces in a thread, in it, over warps and CTAs: 16 + 3 + 5 + 16 + 16.  In all under 128: kError.
 #include <cstddef>
 
 #include "common.cuh"
@@ -32,7 +45,10 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
 constexpr int kMaxSplits = 16;             // CTAs of a cluster
-constexpr int kMaxRowBytes = 184 * 1024;   // of a row in one CTA
+constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
+constexpr int kList = 2048;                // tokens that the first CTA sorts
+constexpr int kQuickBins = kThreads;       // ranges of the first bounds
+constexpr float kError = 0x1p-17f;         // of an FP32 sum of weights, relative
 constexpr int kFixed = 45;                 // binary places of a weight
 constexpr float kMaxTemperature = 0x1p64f;
 
@@ -160,6 +176,63 @@ struct Keys {
     if constexpr (TYPE == DFLASH_T_BF16) return __uint_as_float(b << 16);
     return __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
   }
+  static __device__ __forceinline__ uint32_t of_value(float x) {
+    if constexpr (WIDE) return of(__float_as_uint(x));
+    if constexpr (TYPE == DFLASH_T_BF16) return of(__float_as_uint(x) >> 16);
+    return of(__half_as_ushort(__float2half_rn(x)));
+  }
+  static __device__ __forceinline__ float value_of(uint32_t key) { return value(key & SIGN ? key & ~SIGN : ~key & ALL); }
+  // the larger of two words' values, value by value, NaN if either is one
+  static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (WIDE) {
+      float f;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+      r = __float_as_uint(f);
+    } else if constexpr (TYPE == DFLASH_T_BF16) {
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+      asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    }
+    return r;
+  }
+  static __device__ __forceinline__ bool has_nan(uint32_t w) {
+    if constexpr (WIDE) return (w & 0x7fffffffu) > INF;
+    return (w & 0x7fffu) > INF || (w >> 16 & 0x7fffu) > INF;
+  }
+  static __device__ __forceinline__ float top_of(const uint4& v) {
+    using E = Elem<TYPE>;
+    return E::max_of(E::max_words(E::max_words(v.x, v.y), E::max_words(v.z, v.w)));
+  }
+  // FP32 weights of a piece
+  static __device__ __forceinline__ float quick_sum(const uint4& v, float m, float c) {
+    constexpr int VEC = Elem<TYPE>::VEC;
+    float x[VEC];
+    Elem<TYPE>::widen(v, x);
+    const uint64_t minus = pack2(-m, -m), c2 = pack2(c, c);
+    uint64_t s[VEC / 2];
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      float y0, y1;
+      unpack2(mul2(add2(pack2(x[e], x[e + 1]), minus), c2), y0, y1);
+      s[e / 2] = pack2(ex2_approx(y0), ex2_approx(y1));
+    }
+#pragma unroll
+    for (int o = VEC / 4; o; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < o; ++e) s[e] = add2(s[e], s[e + o]);
+    float s0, s1;
+    unpack2(s[0], s0, s1);
+    return s0 + s1;
+  }
+  // values of a piece above -infinity
+  static __device__ __forceinline__ int unmasked(const uint4& v) {
+    constexpr int VEC = Elem<TYPE>::VEC;
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) c += bits(v, e) != (SIGN | INF);
+    return c;
+  }
   // the key of the smallest value that is not below x
   static __device__ __forceinline__ uint32_t at_least(double x) {
     const float f = __double2float_ru(x);
@@ -189,6 +262,11 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint64_t ld_cluster64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ uint64_t shfl_up(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
 template <typename T>
@@ -207,27 +285,45 @@ struct Found {
 };
 
 struct Shared {
-  uint32_t count[kBins], lo[kBins], hi[kBins];  // of this CTA's tokens; weights in two words
-  uint32_t all_count[kBins];                    // of the cluster's, in its first CTA
-  uint64_t all_w[kBins];
+  union {
+    struct {
+      uint32_t count[kBins], lo[kBins], hi[kBins];  // of this CTA's tokens; weights in two words
+      uint32_t all_count[kBins];                    // of the cluster's, in its first CTA
+      uint64_t all_w[kBins];
+    } digits;
+    struct {
+      uint64_t list[kList];    // (key, id) in order of ids
+      uint64_t sorted[kList];  // (key, place in `list`), largest first
+      uint64_t upto[kList];    // weights before each of them
+      uint32_t hist[kQuickBins];
+    } quick;
+  };
   TableEntry table[32];
   Found found;
   uint64_t cta_w[kMaxSplits], warp_w[kWarps];
-  uint32_t cta_u[kMaxSplits], warp_u[kWarps];
+  uint32_t cta_top[kMaxSplits], cta_low[kMaxSplits], cta_n[kMaxSplits], warp_u[kWarps], warp_low[kWarps], warp_n[kWarps];
+  float cta_f[kMaxSplits], warp_f[kWarps];
   double log_min_p;
   Scale scale;
+  float bound;
+  uint32_t verdict;
 };
+constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
+// What the first CTA (or the one that u names) says of a quick answer.
+enum Verdict : uint32_t { kDone, kExactSum, kDigits };
 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
   constexpr int VEC = E::VEC;
-  extern __shared__ uint4 data[];
-  __shared__ Shared sh;
+  extern __shared__ uint4 smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  uint4* data = smem + kSharedBytes / 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / a.splits, rank = blockIdx.x - row * a.splits;
   const int n = a.splits;
+  if (n > 1) cluster_arrive_relaxed();  // (every CTA has started before another writes to it)
 
   // ---- what the row asks for
   const float t_asked = a.temperature ? a.temperature[row] : 1.f;
@@ -262,45 +358,68 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int all_pieces = (a.vocab + skip + VEC - 1) / VEC;
   const int first = rank * a.pieces;  // the CTA's pieces
   const int mine = max(min(a.pieces, all_pieces - first), 0);
-  float top = -INFINITY;
-  bool nan = false;
-  for (int i = tid; i < mine; i += kThreads) {
-    const long long p0 = static_cast<long long>(first + i) * VEC - skip;  // value of the piece's first place
-    uint4 v;
-    if (p0 >= 0 && p0 + VEC <= a.vocab) {
-      v = __ldcs(frame + first + i);
-    } else {
-      constexpr int W = VEC / 4;
-      v.x = E::raw(src, p0, a.vocab);
-      v.y = E::raw(src, p0 + W, a.vocab);
-      v.z = E::raw(src, p0 + 2 * W, a.vocab);
-      v.w = E::raw(src, p0 + 3 * W, a.vocab);
-    }
-    data[i] = v;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float x = K::value(K::bits(v, e));
-      nan |= x != x;
-      top = fmaxf(top, x);
-    }
-  }
+  float top = -INFINITY;  // of the thread's values
   {
+    constexpr int U = 4;
+    uint32_t tops = E::NOTHING;
+    for (int i0 = tid; i0 < mine; i0 += U * kThreads) {
+      uint4 v[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * kThreads;
+        const int p0 = (first + i) * VEC - skip;  // value of the piece's first place
+        v[j] = make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
+        if (i < mine && p0 >= 0 && p0 + VEC <= a.vocab) v[j] = __ldcs(frame + first + i);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * kThreads;
+        if (i >= mine) break;
+        const int p0 = (first + i) * VEC - skip;
+        if (p0 < 0 || p0 + VEC > a.vocab) {  // the row's ends: value by value
+          constexpr int W = VEC / 4;
+          v[j].x = E::raw(src, p0, a.vocab);
+          v[j].y = E::raw(src, p0 + W, a.vocab);
+          v[j].z = E::raw(src, p0 + 2 * W, a.vocab);
+          v[j].w = E::raw(src, p0 + 3 * W, a.vocab);
+        }
+        data[i] = v[j];
+        tops = K::max_nan(tops, K::max_nan(K::max_nan(v[j].x, v[j].y), K::max_nan(v[j].z, v[j].w)));
+      }
+    }
+    const bool nan = K::has_nan(tops);
+    top = E::max_of(tops);
     uint32_t key = nan ? 0xffffffffu : float_order_key(top);  // (no value's key is that large)
+    uint32_t low = top > -INFINITY ? key : 0xffffffffu;
+    const uint32_t some = __popc(__ballot_sync(0xffffffffu, top > -INFINITY));
     key = __reduce_max_sync(0xffffffffu, key);
-    if (lane == 0) sh.warp_u[warp] = key;
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) sh.warp_u[warp] = key, sh.warp_low[warp] = low, sh.warp_n[warp] = some;
+    if (tid == 0) sh.verdict = kExactSum;
+    sh.quick.hist[tid] = 0;
     __syncthreads();
+    if (n > 1) cluster_wait();
     if (tid < 32) {
-      key = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.warp_u[lane] : 0u);
+      const bool w = lane < kWarps;
+      key = __reduce_max_sync(0xffffffffu, w ? sh.warp_u[lane] : 0u);
+      low = __reduce_min_sync(0xffffffffu, w ? sh.warp_low[lane] : 0xffffffffu);
+      const uint32_t all = __reduce_add_sync(0xffffffffu, w ? sh.warp_n[lane] : 0u);
       if (n == 1) {
-        if (lane == 0) sh.cta_u[0] = key;
+        if (lane == 0) sh.cta_top[0] = key, sh.cta_low[0] = low, sh.cta_n[0] = all;
       } else if (lane < n) {
-        st_cluster(mapa_shared(smem_u32(&sh.cta_u[rank]), lane), key);
+        st_cluster(mapa_shared(smem_u32(&sh.cta_top[rank]), lane), key);
+        st_cluster(mapa_shared(smem_u32(&sh.cta_low[rank]), lane), low);
+        st_cluster(mapa_shared(smem_u32(&sh.cta_n[rank]), lane), all);
       }
     }
   }
   cluster_sync(n);
-  uint32_t top_key = 0;
-  for (int i = 0; i < n; ++i) top_key = max(top_key, sh.cta_u[i]);
+  uint32_t top_key = 0, low_key = 0xffffffffu, maxima = 0;
+  for (int i = 0; i < n; ++i) {
+    top_key = max(top_key, sh.cta_top[i]);
+    low_key = min(low_key, sh.cta_low[i]);
+    maxima += sh.cta_n[i];
+  }
   const float m = float_from_order_key(top_key);
   if (top_key == 0xffffffffu || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from
     if (rank == 0 && tid == 0) {
@@ -320,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint32_t id = 0xffffffffu;
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint4 v = data[i];
+      if (K::top_of(v) < m) continue;
 #pragma unroll
       for (int e = VEC - 1; e >= 0; --e)
         if (K::value(K::bits(v, e)) == m) id = min(id, static_cast<uint32_t>((first + i) * VEC + e - skip));
@@ -349,13 +469,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (tid == 0) sh.scale.m = m;
   __syncthreads();
   const Scale scale = sh.scale;
-  const uint32_t most = [&] {  // the key of m
-    if constexpr (K::WIDE) return K::of(__float_as_uint(m));
-    else if constexpr (TYPE == DFLASH_T_BF16) return K::of(__float_as_uint(m) >> 16);
-    else return K::of(__half_as_ushort(__float2half_rn(m)));
-  }();
+  const uint32_t most = K::of_value(m);
   uint32_t least = K::LOWEST;
   if (by_min) least = max(least, min(most, K::at_least(static_cast<double>(m) + sh.log_min_p)));
+
+  // ln(w / total) of a token, where w <= 1 and the largest weight, 1, is among those of the total
+  auto log_of = [&](float x, float others) { return (x - m) / temperature - log1pf(others); };
+  auto others_of = [&](uint64_t total) {
+    return static_cast<float>(total - (1ull << (kFixed - a.drop))) * exp2f(static_cast<float>(a.drop - kFixed));
+  };
 
   // The sum over the cluster of a value per thread, and the CTAs' sums in sh.cta_w.
   auto cluster_total = [&](uint64_t v) {
@@ -376,7 +498,418 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int i = 0; i < n; ++i) sum += sh.cta_w[i];
     return sum;
   };
+  // The exact weight of all tokens.
+  auto exact_sum = [&]() {
+    uint64_t sum = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint4 v = data[i];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v, e)), scale, sh.table);
+    }
+    return cluster_total(sum);
+  };
+  // The sum of a value per thread over this CTA's threads before it, and over all of them.
+  auto scan = [&](uint64_t v, uint64_t& all) {
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = shfl_up(x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();  // the last scan's values have been read
+    if (lane == 31) sh.warp_w[warp] = x;
+    __syncthreads();
+    x -= v;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const uint64_t y = sh.warp_w[i];
+      if (i < warp) x += y;
+      all += y;
+    }
+    return x;
+  };
+  auto tell_verdict = [&](uint32_t v) {  // (one thread)
+    for (int r = 0; r < n; ++r) {
+      if (n == 1) sh.verdict = v;
+      else st_cluster(mapa_shared(smem_u32(&sh.verdict), r), v);
+    }
+  };
 
+  const bool filter = by_k || by_p || by_min;
+  if (!filter) {
+    // ---- FP32 sums of the weights lead to the token
+    float sum = 0.f;
+    uint32_t count = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint4 v = data[i];
+      sum += K::quick_sum(v, m, scale.hi);
+      count += K::unmasked(v);
+    }
+    float ws = sum;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0) sh.warp_f[warp] = ws, sh.warp_n[warp] = count;
+    __syncthreads();
+    if (tid < 32) {
+      float cs = 0.f;
+      for (int i = 0; i < kWarps; ++i) cs += sh.warp_f[i];
+      const uint32_t c = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
+      if (n == 1) {
+        if (lane == 0) sh.cta_f[0] = cs, sh.cta_w[0] = c;
+      } else if (lane < n) {
+        st_cluster(mapa_shared(smem_u32(&sh.cta_f[rank]), lane), __float_as_uint(cs));
+        st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), lane), static_cast<uint64_t>(c));
+      }
+    }
+    cluster_sync(n);
+    float total = 0.f, below = 0.f, own = 0.f;
+    for (int i = 0; i < n; ++i) {
+      if (i == rank) below = total, own = sh.cta_f[i];
+      total += sh.cta_f[i];
+    }
+    const float at = u * total, off = kError * total;
+    if (at >= below && (at < below + own || rank == n - 1)) {  // (one CTA, by these sums)
+      float from = below;
+      int w = 0;
+      for (; w < kWarps - 1 && !(at < from + sh.warp_f[w]); ++w) from += sh.warp_f[w];
+      if (warp == w) {
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+          const int i = i0 + lane;
+          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
+          const float part = K::quick_sum(v, m, scale.hi);
+          float upto = part;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          upto += from;
+          const unsigned over = __ballot_sync(0xffffffffu, upto > at);
+          if (over) {
+            if (lane == __ffs(over) - 1) {
+              float c = upto - part;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                const float x = K::value(K::bits(v, e)), before = c;
+                c += ex2_approx((x - m) * scale.hi);
+                // the first past u, further from both of its borders than the sums may be off
+                if (before <= at && c > at) {
+                  if (before + off <= at && c - off > at) {
+                    a.tokens[row] = (first + i) * VEC + e - skip;
+                    if (a.logprob) a.logprob[row] = log_of(x, total - 1.f);
+                    if (a.kept) {
+                      uint64_t all = 0;
+                      for (int r = 0; r < n; ++r) all += sh.cta_w[r];
+                      a.kept[row] = static_cast<int32_t>(all);
+                    }
+                    tell_verdict(kDone);
+                  }
+                  break;
+                }
+              }
+            }
+            break;
+          }
+          from = __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync(n);
+    if (sh.verdict == kDone) return;
+  } else {
+    // ---- a bound below the thresholds
+    float bound = -INFINITY;  // logits from here on
+    bool quick = true;
+    float sum = 0.f;  // of all weights, by top-p alone
+    if (a.vocab <= kList) {  // the whole row is a list
+    } else if (by_k) {
+      const float low = float_from_order_key(low_key), per = m > low ? (kQuickBins - 1) / (m - low) : 0.f;
+      quick = maxima >= static_cast<uint32_t>(k_asked) && per < 1e30f && per > 0.f;
+      if (quick) {
+        if (top > -INFINITY) atomicAdd(&sh.quick.hist[min(static_cast<int>((m - top) * per), kQuickBins - 1)], 1u);
+        cluster_sync(n);
+        uint32_t c = 0;
+        if (n == 1) c = sh.quick.hist[tid];
+        else
+          for (int r = 0; r < n; ++r) c += ld_cluster(mapa_shared(smem_u32(&sh.quick.hist[tid]), r));
+        uint64_t all;
+        const uint64_t before = scan(c, all);
+        // (the values of range b lie above m - (b + 1) / per, to FP32)
+        if (before < k_asked && before + c >= k_asked) sh.bound = m - (tid + 1) / per * (1.f + 0x1p-20f);
+        __syncthreads();
+        bound = sh.bound;
+      }
+    } else if (by_p) {
+      // tokens whose exponent is beyond `cut` weigh (1 - p) / 4 together at most
+      const float rest = 1.f - fmaxf(p, 0.f), cut = log2f(static_cast<float>(a.vocab) * 4.f / rest);
+      const float per = kQuickBins / cut;
+      quick = cut < 40.f;
+      if (quick) {
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const uint4 v = data[i];
+          sum += K::quick_sum(v, m, scale.hi);
+          if ((m - K::top_of(v)) * scale.hi < cut) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const float z = (m - K::value(K::bits(v, e))) * scale.hi;
+              if (z < cut) atomicAdd(&sh.quick.hist[min(static_cast<int>(z * per), kQuickBins - 1)], 1u);
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) sh.warp_f[warp] = sum;
+        __syncthreads();
+        if (tid < 32) {
+          float cs = 0.f;
+          for (int i = 0; i < kWarps; ++i) cs += sh.warp_f[i];
+          if (n == 1) {
+            if (lane == 0) sh.cta_f[0] = cs;
+          } else if (lane < n) {
+            st_cluster(mapa_shared(smem_u32(&sh.cta_f[rank]), lane), __float_as_uint(cs));
+          }
+        }
+        cluster_sync(n);
+        sum = 0.f;
+        for (int i = 0; i < n; ++i) sum += sh.cta_f[i];
+        // what the ranges from the last one up to this thread's weigh at most
+        const int bin = kQuickBins - 1 - tid;
+        uint32_t c = 0;
+        if (n == 1) c = sh.quick.hist[bin];
+        else
+          for (int r = 0; r < n; ++r) c += ld_cluster(mapa_shared(smem_u32(&sh.quick.hist[bin]), r));
+        const float w = static_cast<float>(c) * ex2_approx(-static_cast<float>(bin) / per);
+        float x = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();  // warp_f has been read
+        if (lane == 31) sh.warp_f[warp] = x;
+        if (tid == 0) sh.bound = -INFINITY;
+        __syncthreads();
+        x += rest * 0.25f;
+        for (int i = 0; i < warp; ++i) x += sh.warp_f[i];
+        // (2^-10: more than the sums and ranges are off)
+        const float most_left = rest * sum * (1.f - 0x1p-10f);
+        // the first range that has to be kept: with it more than may be left out would be
+        if (x > most_left && x - w <= most_left) sh.bound = m - (bin + 1) / per / scale.hi * (1.f + 0x1p-20f);
+        __syncthreads();
+        bound = sh.bound;
+        quick = bound > -INFINITY;
+      }
+    }
+    // (top-p needs the whole of what top-k leaves, and in a short row of all)
+    if (by_min && !(by_p && (by_k || a.vocab <= kList))) bound = fmaxf(bound, K::value_of(least));
+
+    if (quick) {
+      // ---- the tokens from the bound on, in order of their ids, in each CTA
+      uint32_t count = 0;
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const uint4 v = data[i];
+        if (K::top_of(v) < bound) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float x = K::value(K::bits(v, e));
+          count += x >= bound && x > -INFINITY;
+        }
+      }
+      uint64_t all;
+      uint32_t to;
+      {
+        const uint32_t w = __reduce_add_sync(0xffffffffu, count);
+        __syncthreads();
+        if (lane == 0) sh.warp_n[warp] = w;
+        __syncthreads();
+        to = 0;
+        uint32_t c = 0;
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) to += sh.warp_n[i];
+          c += sh.warp_n[i];
+        }
+        all = c;
+      }
+      if (all <= kList && sh.warp_n[warp]) {
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+          const int i = i0 + lane;
+          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
+          const bool any = K::top_of(v) >= bound && K::top_of(v) > -INFINITY;
+          if (!__any_sync(0xffffffffu, any)) continue;
+          uint32_t c = 0;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float x = K::value(K::bits(v, e));
+            c += x >= bound && x > -INFINITY;
+          }
+          uint32_t upto = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          uint32_t at = to + upto - c;
+          if (c) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const uint32_t b = K::bits(v, e);
+              const float x = K::value(b);
+              if (x >= bound && x > -INFINITY)
+                sh.quick.list[at++] = static_cast<uint64_t>(K::of(b)) << 32 | static_cast<uint32_t>((first + i) * VEC + e - skip);
+            }
+          }
+          to += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+      if (tid == 0) {
+        // (not the array that the numbers of maxima lie in: a CTA may still read them)
+        if (n == 1) sh.cta_w[0] = all;
+        else st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), 0), all);
+      }
+      cluster_sync(n);
+      uint32_t keep = 0, size = 0;
+      uint64_t kept_w = 0;
+      uint32_t cut_key = 0;
+      // what the first CTA makes of its list, once it is sorted: false if S has to be exact
+      auto decide = [&](double s_lo, double s_hi) {
+        auto key_at = [&](uint32_t i) { return static_cast<uint32_t>(sh.quick.sorted[i] >> 32); };
+        // how many of the first `of` have the property, which holds down to some place
+        auto number = [&](uint32_t of, auto&& has) {
+          uint32_t c = 0;
+          for (uint32_t i = tid; i < of; i += kThreads) c += has(i);
+          c = __reduce_add_sync(0xffffffffu, c);
+          __syncthreads();
+          if (lane == 0) sh.warp_n[warp] = c;
+          __syncthreads();
+          c = 0;
+          for (int i = 0; i < kWarps; ++i) c += sh.warp_n[i];
+          return c;
+        };
+        uint32_t of = size;
+        cut_key = least;
+        if (by_k) {
+          const uint32_t k_key = key_at(min(static_cast<uint32_t>(k_asked), size) - 1);
+          cut_key = max(cut_key, k_key);
+          of = number(size, [&](uint32_t i) { return key_at(i) >= k_key; });
+        }
+        if (by_p) {
+          const double whole = by_k ? static_cast<double>(of < size ? sh.quick.upto[of] : kept_w) : 0.0;
+          const double lo = static_cast<double>(p) * (by_k ? whole : s_lo), hi = static_cast<double>(p) * (by_k ? whole : s_hi);
+          const uint32_t c = number(of, [&](uint32_t i) { return static_cast<double>(sh.quick.upto[i]) < lo; });
+          if (lo != hi) {
+            const uint32_t d = number(of, [&](uint32_t i) { return static_cast<double>(sh.quick.upto[i]) < hi; });
+            if (c != d) return false;
+          }
+          cut_key = max(cut_key, key_at(c ? c - 1 : 0));
+        }
+        keep = number(size, [&](uint32_t i) { return key_at(i) >= cut_key; });
+        return true;
+      };
+      // and the token, in order of ids
+      auto draw = [&]() {
+        const uint64_t total = keep < size ? sh.quick.upto[keep] : kept_w;
+        const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
+        const uint32_t per = (size + kThreads - 1) / kThreads;
+        const uint32_t j0 = min(tid * per, size), j1 = min(j0 + per, size);
+        uint64_t w = 0, all_w;
+        for (uint32_t j = j0; j < j1; ++j) {
+          const uint32_t key = static_cast<uint32_t>(sh.quick.list[j] >> 32);
+          if (key >= cut_key) w += weight(K::value_of(key), scale, sh.table);
+        }
+        uint64_t c = scan(w, all_w);
+        if (c <= at && at < c + w) {  // (one thread)
+          for (uint32_t j = j0; j < j1; ++j) {
+            const uint64_t entry = sh.quick.list[j];
+            const uint32_t key = static_cast<uint32_t>(entry >> 32);
+            if (key < cut_key) continue;
+            const float x = K::value_of(key);
+            c += weight(x, scale, sh.table);
+            if (c > at) {
+              a.tokens[row] = static_cast<int32_t>(entry);
+              if (a.logprob) a.logprob[row] = log_of(x, others_of(total));
+              if (a.kept) a.kept[row] = static_cast<int32_t>(keep);
+              break;
+            }
+          }
+        }
+      };
+      if (rank == 0) {
+        // the CTAs' lists one behind the other
+        uint64_t upto = 0;
+        for (int r = 0; r < n; ++r) upto += sh.cta_w[r];
+        uint32_t verdict = kDigits;
+        if (upto <= kList) {
+          size = static_cast<uint32_t>(upto);
+          for (uint32_t i = tid; i < size; i += kThreads) {
+            uint32_t r = 0, j = i;
+            while (j >= sh.cta_w[r]) j -= static_cast<uint32_t>(sh.cta_w[r++]);
+            uint64_t entry;
+            if (r == 0) {
+              entry = sh.quick.list[i];
+            } else {
+              entry = ld_cluster64(mapa_shared(smem_u32(&sh.quick.list[j]), r));
+              sh.quick.list[i] = entry;
+            }
+            sh.quick.sorted[i] = (entry & 0xffffffff00000000ull) | i;
+          }
+          uint32_t full = 2;
+          while (full < size) full *= 2;
+          for (uint32_t i = size + tid; i < full; i += kThreads) sh.quick.sorted[i] = 0;
+          __syncthreads();
+          for (uint32_t span = 2; span <= full; span *= 2)
+            for (uint32_t step = span / 2; step; step /= 2) {
+              for (uint32_t i = tid; i < full / 2; i += kThreads) {
+                const uint32_t x = 2 * i - (i & (step - 1)), y = x + step;
+                const uint64_t f = sh.quick.sorted[x], g = sh.quick.sorted[y];
+                if ((f < g) == ((x & span) == 0)) sh.quick.sorted[x] = g, sh.quick.sorted[y] = f;
+              }
+              __syncthreads();
+            }
+          // exact weights before each
+          const uint32_t per = (size + kThreads - 1) / kThreads;
+          const uint32_t j0 = min(tid * per, size), j1 = min(j0 + per, size);
+          uint64_t w = 0;
+          for (uint32_t j = j0; j < j1; ++j) {
+            const uint64_t x = weight(K::value_of(static_cast<uint32_t>(sh.quick.sorted[j] >> 32)), scale, sh.table);
+            sh.quick.upto[j] = x;
+            w += x;
+          }
+          uint64_t c = scan(w, kept_w);
+          for (uint32_t j = j0; j < j1; ++j) {
+            const uint64_t x = sh.quick.upto[j];
+            sh.quick.upto[j] = c;
+            c += x;
+          }
+          __syncthreads();
+          double s_lo = 0.0, s_hi = 0.0;
+          if (by_p && !by_k) {
+            const double s = a.vocab <= kList ? static_cast<double>(kept_w)
+                                              : static_cast<double>(sum) * static_cast<double>(1ull << (kFixed - a.drop));
+            const double off = a.vocab <= kList ? 0.0 : static_cast<double>(kError);
+            s_lo = s - s * off, s_hi = s + s * off;
+          }
+          verdict = decide(s_lo, s_hi) ? kDone : kExactSum;
+          if (verdict == kDone) draw();
+        }
+        if (tid == 0) tell_verdict(verdict);
+      }
+      cluster_sync(n);
+      const uint32_t verdict = sh.verdict;
+      if (verdict == kDone) return;
+      if (verdict == kExactSum) {
+        const double whole = static_cast<double>(exact_sum());
+        if (rank == 0) {
+          decide(whole, whole);
+          draw();
+        }
+        return;
+      }
+    }
+  }
+  // ---- digit by digit, and exact sums of all that is kept
   // One thread of the first CTA tells all CTAs what it found.
   auto tell = [&](const Found& g) {
     const uint64_t* words = reinterpret_cast<const uint64_t*>(&g);
@@ -396,8 +929,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const uint32_t range = f.hi - f.lo;
       const int shift = max(22 - __clz(range | 1), 0);
       for (int i = tid; i < kBins; i += kThreads) {
-        sh.count[i] = 0;
-        if (weights) sh.lo[i] = sh.hi[i] = 0;
+        sh.digits.count[i] = 0;
+        if (weights) sh.digits.lo[i] = sh.digits.hi[i] = 0;
       }
       __syncthreads();
       for (int i = w0 + lane; i < w1; i += 32) {
@@ -407,12 +940,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t b = K::bits(v, e), key = K::of(b);
           if (key < f.lo || key > f.hi) continue;
           const int bin = (f.hi - key) >> shift;
-          atomicAdd(&sh.count[bin], 1u);
+          atomicAdd(&sh.digits.count[bin], 1u);
           if (weights) {
             const uint64_t w = weight(K::value(b), scale, sh.table);
-            const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.lo[bin], w_lo);
+            const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.digits.lo[bin], w_lo);
             const uint32_t w_hi = static_cast<uint32_t>(w >> 32) + (old + w_lo < old ? 1u : 0u);
-            if (w_hi) atomicAdd(&sh.hi[bin], w_hi);
+            if (w_hi) atomicAdd(&sh.digits.hi[bin], w_hi);
           }
         }
       }
@@ -424,22 +957,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         uint32_t c = 0;
         uint64_t w = 0;
         if (n == 1) {
-          c = sh.count[bin];
-          if (weights) w = static_cast<uint64_t>(sh.hi[bin]) << 32 | sh.lo[bin];
+          c = sh.digits.count[bin];
+          if (weights) w = static_cast<uint64_t>(sh.digits.hi[bin]) << 32 | sh.digits.lo[bin];
         } else {
           for (int r = 0; r < n; ++r) {
-            c += ld_cluster(mapa_shared(smem_u32(&sh.count[bin]), r));
+            c += ld_cluster(mapa_shared(smem_u32(&sh.digits.count[bin]), r));
             if (weights)
-              w += (static_cast<uint64_t>(ld_cluster(mapa_shared(smem_u32(&sh.hi[bin]), r))) << 32) +
-                   ld_cluster(mapa_shared(smem_u32(&sh.lo[bin]), r));
+              w += (static_cast<uint64_t>(ld_cluster(mapa_shared(smem_u32(&sh.digits.hi[bin]), r))) << 32) +
+                   ld_cluster(mapa_shared(smem_u32(&sh.digits.lo[bin]), r));
           }
         }
         if (n == 1) {
-          sh.all_count[bin] = c;
-          sh.all_w[bin] = w;
+          sh.digits.all_count[bin] = c;
+          sh.digits.all_w[bin] = w;
         } else {
-          st_cluster(mapa_shared(smem_u32(&sh.all_count[bin]), 0), c);
-          st_cluster(mapa_shared(smem_u32(&sh.all_w[bin]), 0), w);
+          st_cluster(mapa_shared(smem_u32(&sh.digits.all_count[bin]), 0), c);
+          st_cluster(mapa_shared(smem_u32(&sh.digits.all_w[bin]), 0), w);
         }
       }
       cluster_sync(n);
@@ -450,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         uint64_t w[B], ws = 0;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-          c[j] = sh.all_count[tid * B + j];
-          w[j] = sh.all_w[tid * B + j];
+          c[j] = sh.digits.all_count[tid * B + j];
+          w[j] = sh.digits.all_w[tid * B + j];
           cs += c[j];
           ws += w[j];
         }
@@ -498,13 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       least = max(least, target > 0.0 ? search(f.lo, true, true, 0, target).lo : most);
     }
   } else if (by_p) {
-    uint64_t sum = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint4 v = data[i];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v, e)), scale, sh.table);
-    }
-    whole = cluster_total(sum);
+    whole = exact_sum();
     const double target = static_cast<double>(p) * static_cast<double>(whole);
     least = max(least, target > 0.0 ? search(K::LOWEST, true, true, 0, target).lo : most);
   }
@@ -560,10 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 if (c > at) {
                   done = true;
                   a.tokens[row] = (first + i) * VEC + e - skip;
-                  // ln(w / total): the largest weight, 1, is among the kept ones
-                  if (a.logprob)
-                    a.logprob[row] = (x - m) / temperature -
-                                     log1pf(static_cast<float>(total - (1ull << (kFixed - a.drop))) * exp2f(static_cast<float>(a.drop - kFixed)));
+                  if (a.logprob) a.logprob[row] = log_of(x, others_of(total));
                 }
               }
             }
@@ -589,7 +1113,7 @@ cudaError_t splits_of(int n_rows, long long row_pieces, int* splits, int* pieces
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   int s = 1;
-  while (s < kMaxSplits && (row_pieces * 16 > 72ll * 1024 * s || (static_cast<long long>(n_rows) * s < sms && row_pieces > 2 * kThreads * s))) s *= 2;
+  while (s < kMaxSplits && (row_pieces * 16 > 56ll * 1024 * s || (static_cast<long long>(n_rows) * s < sms && row_pieces > 2 * kThreads * s))) s *= 2;
   *splits = s;
   *pieces = static_cast<int>((row_pieces + s - 1) / s);
   return cudaSuccess;
@@ -597,8 +1121,8 @@ cudaError_t splits_of(int n_rows, long long row_pieces, int* splits, int* pieces
 
 template <int TYPE>
 cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(a.pieces) * 16;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
+  const size_t smem = kSharedBytes + static_cast<size_t>(a.pieces) * 16;
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes + kMaxRowBytes);
   if (e == cudaSuccess && a.splits > 8)  // beyond the portable size
     e = cudaFuncSetAttribute(sample_kernel<TYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
