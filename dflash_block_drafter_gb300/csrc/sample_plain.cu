@@ -1,0 +1,487 @@
+// Tokens drawn from the whole distribution, and greedy ones: dflash_sample_tokens without a filter.
+//
+// One pass over the logits.  A warp takes a batch of 2 KB at a time and leaves
+// its sum of 2^((x - r) c) with the reference r, the largest value the warp has met; the
+// batches' sums, brought to one reference, lead to the batch in which u lies, which is
+// read once more.  The token stands if both of its borders are further from u than FP32 sums
+// may be off (sampling.cuh); else the row is left to a second kernel, which forms exact sums with clusters of
+// eight CTAs (one CTA alone takes 70 us for 151936 tokens, the tail of a call of 1000 rows).  A greedy row is one look: the first batch whose reference is the largest value
+// holds its first id.
+//
+// The bytes bound it for many rows (four 16-byte loads in flight per thread, then 2^x); with few rows a
+// row's batches are split over the CTAs of a cluster.
+#include <cstddef>
+
+#include "sampling.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kLoads = 4;  // 16-byte loads of a thread per batch
+constexpr int kBatchBytes = 32 * kLoads * 16;
+constexpr int kRestCtas = 8;         // CTAs for a row that the FP32 sums leave open
+constexpr int32_t kUndecided = -2;  // the token of such a row, between the kernels
+constexpr int kMaxBatches = (1 << 19) * 4 / kBatchBytes + 1;  // (a row may begin inside a piece)
+
+// The largest of the warp's values (no NaN among them).
+__device__ __forceinline__ float warp_max(float v) { return float_from_order_key(__reduce_max_sync(0xffffffffu, float_order_key(v))); }
+
+// Inclusive sums over the lanes.
+template <typename T>
+__device__ __forceinline__ T warp_upto(T v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// A lane's pieces of a batch of a row.
+template <int TYPE>
+__device__ __forceinline__ void load_batch(const uint8_t* src, const uint4* frame, int skip, int places, int vocab, int b, int lane,
+                                           uint4 (&v)[kLoads]) {
+  using E = Elem<TYPE>;
+  constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
+  const int p0 = b * BATCH;
+  if (p0 >= skip && p0 + BATCH <= places) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) v[j] = __ldg(frame + p0 / VEC + j * 32 + lane);
+  } else {  // the row's ends: value by value
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const long long i = p0 + (j * 32 + lane) * VEC - skip;
+      constexpr int W = VEC / 4;  // values of a word
+      v[j].x = E::raw(src, i, vocab);
+      v[j].y = E::raw(src, i + W, vocab);
+      v[j].z = E::raw(src, i + 2 * W, vocab);
+      v[j].w = E::raw(src, i + 3 * W, vocab);
+    }
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleArgs a) {
+  using E = Elem<TYPE>;
+  using K = Keys<TYPE>;
+  constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
+  __shared__ float2 part[kMaxBatches];  // reference and sum of this CTA's batches
+  __shared__ Scale s_scale;
+  __shared__ float s_ref[kWarps], s_sum[kWarps];
+  __shared__ uint32_t s_count[kWarps], s_nan[kWarps];
+  __shared__ float cta_ref[kMaxSplits], cta_sum[kMaxSplits];
+  __shared__ uint32_t cta_count[kMaxSplits], cta_nan[kMaxSplits];
+  __shared__ int s_batch, s_done;
+  __shared__ float s_from;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / a.splits, rank = blockIdx.x - row * a.splits, n = a.splits;
+  if (n > 1) cluster_arrive_relaxed();
+  pdl_launch_dependents();
+  const Settings set(a, row);
+  if (tid == kThreads - 1) {
+    if (rank == 0 && !set.fine) set_status(a.status, DFLASH_DEV_BAD_VALUE);
+    s_scale.hi = 1.f;
+    if (!set.greedy) set.scale(s_scale, a.drop);
+    s_batch = 0x7fffffff;
+    s_done = 0;
+  }
+
+  const uint8_t* src = a.logits + row * a.row_bytes;
+  const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E::BYTES;
+  const uint4* frame = reinterpret_cast<const uint4*>(src - skip * E::BYTES);
+  const int places = a.vocab + skip;
+  const int batches = (places + BATCH - 1) / BATCH;
+  // this CTA's batches
+  const int b0 = static_cast<int>(static_cast<long long>(batches) * rank / n), b1 = static_cast<int>(static_cast<long long>(batches) * (rank + 1) / n);
+  auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
+  __syncthreads();  // (c)
+  const float c = s_scale.hi;
+
+  // ---- the pass
+  float ref = -INFINITY;
+  uint32_t count = 0, tops = E::NOTHING;
+  {
+    uint4 v[kLoads];
+    int b = b0 + warp;
+    if (b < b1) load(b, v);
+    for (; b < b1; b += kWarps) {
+      uint32_t top = E::NOTHING, low = v[0].x;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        top = K::max_nan(top, K::max_nan(K::max_nan(v[j].x, v[j].y), K::max_nan(v[j].z, v[j].w)));
+        low = K::min_words(low, K::min_words(K::min_words(v[j].x, v[j].y), K::min_words(v[j].z, v[j].w)));
+      }
+      tops = K::max_nan(tops, top);
+      ref = fmaxf(ref, warp_max(fmaxf(E::max_of(top), -INFINITY)));
+      const float from = ref == -INFINITY ? 0.f : ref;
+      float sum = 0.f;
+      if (!set.greedy) {
+        float s[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) s[j] = K::quick_sum(v[j], from, c);
+        sum = (s[0] + s[1]) + (s[2] + s[3]);
+        if (K::masked(low)) {
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) count += K::unmasked(v[j]);
+        } else {
+          count += kLoads * VEC;
+        }
+      }
+      static_assert(kLoads == 4, "sum");
+      if (b + kWarps < b1) load(b + kWarps, v);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) part[b - b0] = make_float2(ref, sum);
+    }
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  const bool nan = __any_sync(0xffffffffu, K::has_nan(tops));
+  if (lane == 0) s_ref[warp] = ref, s_count[warp] = count, s_nan[warp] = nan;
+  __syncthreads();
+  float m = -INFINITY;
+  uint32_t all = 0, bad = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ref[w]), all += s_count[w], bad |= s_nan[w];
+  const int mine = b1 - b0, per = (mine + kThreads - 1) / kThreads;
+  const int j0 = min(tid * per, mine), j1 = min(j0 + per, mine);  // the thread's batches, one behind the other
+  auto of_batch = [&](int j) {  // relative to m as it is by then
+    const float2 x = part[j];
+    return x.x == -INFINITY ? 0.f : x.y * ex2_approx((x.x - m) * c);
+  };
+  float own = 0.f;
+  for (int j = j0; j < j1; ++j) own += of_batch(j);
+  const float upto = warp_upto(own, lane);
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  float before = upto - own, cta = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    cta += s_sum[w];
+  }
+  // ---- the CTAs' results
+  float total = cta, at_cta = 0.f, m_own = m;
+  bool owner = true;
+  if (n > 1) {
+    cluster_wait();  // every CTA has started
+    if (tid < n) {
+      auto put = [&](void* to, uint32_t v) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(to), tid)), "r"(v) : "memory");
+      };
+      put(&cta_ref[rank], __float_as_uint(m));
+      put(&cta_sum[rank], __float_as_uint(cta));
+      put(&cta_count[rank], all);
+      put(&cta_nan[rank], bad);
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    all = bad = 0;
+    for (int r = 0; r < n; ++r) m = fmaxf(m, cta_ref[r]), all += cta_count[r], bad |= cta_nan[r];
+    auto of_cta = [&](int r) { return cta_ref[r] == -INFINITY ? 0.f : cta_sum[r] * ex2_approx((cta_ref[r] - m) * c); };
+    total = 0.f;
+    for (int r = 0; r < n; ++r) total += of_cta(r);
+    // the one CTA that goes on: the first whose sums pass u, or that has the largest value
+    float sum = 0.f;
+    int who = -1, last = 0;
+    for (int r = 0; r < n && who < 0; ++r) {
+      const float x = of_cta(r);
+      if (x > 0.f) last = r;
+      if (set.greedy ? cta_ref[r] == m : sum + x > set.u * total) who = r;
+      else sum += x;
+    }
+    if (who < 0) who = last, sum -= of_cta(last);
+    owner = who == rank;
+    at_cta = sum;
+  }
+  if (bad || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from
+    if (rank == 0 && tid == 0) {
+      if (bad || m != -INFINITY) set_status(a.status, DFLASH_DEV_NONFINITE);
+      a.tokens[row] = -1;
+      if (a.logprob) a.logprob[row] = -INFINITY;
+      if (a.kept) a.kept[row] = 0;
+    }
+    return;
+  }
+  if (!owner) return;
+
+  if (set.greedy) {
+    for (int j = j0; j < j1; ++j)
+      if (part[j].x == m) {
+        atomicMin(&s_batch, j);
+        break;
+      }
+    __syncthreads();
+    if (warp == 0) {
+      uint4 v[kLoads];
+      const int b = b0 + s_batch;
+      load(b, v);
+      uint32_t id = 0xffffffffu;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (K::value(K::bits(v[j], e)) == m) id = min(id, static_cast<uint32_t>(b * BATCH + (j * 32 + lane) * VEC + e - skip));
+      id = __reduce_min_sync(0xffffffffu, id);
+      if (lane == 0) {
+        a.tokens[row] = static_cast<int32_t>(id);
+        if (a.logprob) a.logprob[row] = 0.f;
+        if (a.kept) a.kept[row] = 1;
+      }
+    }
+    return;
+  }
+
+  // ---- the batch in which u lies, and the token in it
+  const float at = set.u * total, off = kError * total;
+  {
+    const float f = m_own == -INFINITY ? 0.f : ex2_approx((m_own - m) * c);  // of this CTA's sums
+    float x = at_cta + before * f;
+    const float end = x + own * f;
+    if (j0 < j1 && x <= at && at < end) {  // (one thread, or none where two sums differ: then the exact ones decide)
+      int j = j0;
+      for (; j < j1 - 1; ++j) {
+        const float y = of_batch(j);
+        if (at < x + y) break;
+        x += y;
+      }
+      s_batch = j;
+      s_from = x;
+    }
+  }
+  __syncthreads();
+  if (warp == 0 && s_batch != 0x7fffffff) {
+    uint4 v[kLoads];
+    const int b = b0 + s_batch;
+    load(b, v);
+    float from = s_from;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const float w = K::quick_sum(v[j], m, c);
+      const float x = warp_upto(w, lane) + from;
+      const unsigned over = __ballot_sync(0xffffffffu, x > at);
+      if (!found && over && lane == __ffs(over) - 1) {
+        float y = x - w;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float value = K::value(K::bits(v[j], e)), low = y;
+          y += ex2_approx((value - m) * c);
+          // the first past u, further from both of its borders than the sums may be off
+          if (low <= at && y > at && low + off <= at && y - off > at) {
+            a.tokens[row] = b * BATCH + (j * 32 + lane) * VEC + e - skip;
+            if (a.logprob) a.logprob[row] = set.log_of(value, m, total - 1.f);
+            if (a.kept) a.kept[row] = static_cast<int32_t>(all);
+            s_done = 1;
+          }
+        }
+      }
+      found |= over != 0;
+      from = __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  if (!s_done && tid == 0) a.tokens[row] = kUndecided;
+}
+
+// Rows that the sums left open: exact ones, by clusters of kRestCtas.  The clusters share the rows out by
+// their numbers.  A CTA has a part of the row's batches, which it reads twice: for the largest value (and the
+// tokens that are not masked), and for the weights.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleArgs a) {
+  using E = Elem<TYPE>;
+  using K = Keys<TYPE>;
+  constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
+  __shared__ uint64_t part[kMaxBatches / kRestCtas + 2];  // of this CTA's batches
+  __shared__ TableEntry table[32];
+  __shared__ Scale s_scale;
+  __shared__ uint64_t s_wide[kWarps], cta_wide[kRestCtas];
+  __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[kWarps];
+  __shared__ int s_batch;
+  __shared__ uint64_t s_from;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % kRestCtas, cluster = blockIdx.x / kRestCtas, clusters = gridDim.x / kRestCtas;
+  if (tid < 32) table[tid] = kTable[tid];
+  auto sync = [] {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  auto put = [](void* to, uint32_t v, int r) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(to), r)), "r"(v) : "memory");
+  };
+  pdl_wait();
+  for (long long r0 = cluster; r0 < a.n_rows; r0 += static_cast<long long>(clusters) * kThreads) {
+    const long long mine = r0 + static_cast<long long>(tid) * clusters;
+    const unsigned open = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
+    if (lane == 0) s_open[warp] = open;
+    sync();  // every CTA runs, and has seen the rows before one of them is drawn
+    for (int w = 0; w < kWarps; ++w)
+      for (unsigned left = s_open[w]; left; left &= left - 1) {
+        const int row = static_cast<int>(r0 + static_cast<long long>(w * 32 + __ffs(left) - 1) * clusters);
+        const Settings set(a, row);
+        if (tid == 0) set.scale(s_scale, a.drop);
+        const uint8_t* src = a.logits + row * a.row_bytes;
+        const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E::BYTES;
+        const uint4* frame = reinterpret_cast<const uint4*>(src - skip * E::BYTES);
+        const int places = a.vocab + skip;
+        const int batches = (places + BATCH - 1) / BATCH;
+        const int b0 = batches * rank / kRestCtas, b1 = batches * (rank + 1) / kRestCtas;
+        auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
+        uint32_t tops = E::NOTHING, count = 0;
+        for (int b = b0 + warp; b < b1; b += kWarps) {
+          uint4 v[kLoads];
+          load(b, v);
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) {
+            tops = E::max_words(tops, E::max_words(E::max_words(v[j].x, v[j].y), E::max_words(v[j].z, v[j].w)));
+            count += K::unmasked(v[j]);
+          }
+        }
+        const uint32_t key = __reduce_max_sync(0xffffffffu, float_order_key(E::max_of(tops)));
+        count = __reduce_add_sync(0xffffffffu, count);
+        if (lane == 0) s_key[warp] = key, s_count[warp] = count;
+        __syncthreads();
+        if (tid < kRestCtas) {
+          uint32_t x = 0, y = 0;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) x = max(x, s_key[i]), y += s_count[i];
+          put(&cta_key[rank], x, tid);
+          put(&cta_count[rank], y, tid);
+        }
+        __syncwarp();
+        sync();
+        uint32_t top = 0, all = 0;
+#pragma unroll
+        for (int r = 0; r < kRestCtas; ++r) top = max(top, cta_key[r]), all += cta_count[r];
+        Scale scale = s_scale;
+        scale.m = float_from_order_key(top);
+        for (int b = b0 + warp; b < b1; b += kWarps) {
+          uint4 v[kLoads];
+          load(b, v);
+          uint64_t sum = 0;
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v[j], e)), scale, table);
+          sum = warp_sum(sum);
+          if (lane == 0) part[b - b0] = sum;
+        }
+        __syncthreads();
+        // (a thread has a batch: a CTA has fewer)
+        static_assert(kMaxBatches / kRestCtas + 1 <= kThreads, "batches");
+        const uint64_t own = tid < b1 - b0 ? part[tid] : 0;
+        const uint64_t upto = warp_upto(own, lane);
+        if (lane == 31) s_wide[warp] = upto;
+        __syncthreads();
+        uint64_t before = upto - own, cta = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) before += s_wide[i];
+          cta += s_wide[i];
+        }
+        if (tid < kRestCtas)
+          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&cta_wide[rank]), tid)), "l"(cta) : "memory");
+        __syncwarp();
+        sync();
+        uint64_t whole = 0, below = 0;
+#pragma unroll
+        for (int r = 0; r < kRestCtas; ++r) {
+          if (r < rank) below += cta_wide[r];
+          whole += cta_wide[r];
+        }
+        const uint64_t place = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(whole));
+        if (place >= below && place < below + cta) {  // (one CTA)
+          before += below;
+          if (before <= place && place < before + own) s_batch = b0 + tid, s_from = before;  // (one thread)
+          __syncthreads();
+          if (warp == 0) {
+            uint4 v[kLoads];
+            const int b = s_batch;
+            load(b, v);
+            uint64_t from = s_from;
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+              uint64_t sum = 0;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v[j], e)), scale, table);
+              const uint64_t y = warp_upto(sum, lane) + from;
+              const unsigned over = __ballot_sync(0xffffffffu, y > place);
+              if (!found && over && lane == __ffs(over) - 1) {
+                uint64_t z = y - sum;
+                bool done = false;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                  const float value = K::value(K::bits(v[j], e));
+                  z += weight(value, scale, table);
+                  if (!done && z > place) {
+                    done = true;
+                    a.tokens[row] = b * BATCH + (j * 32 + lane) * VEC + e - skip;
+                    if (a.logprob) a.logprob[row] = set.log_of(value, scale.m, others_of(whole, a.drop));
+                    if (a.kept) a.kept[row] = static_cast<int32_t>(all);
+                  }
+                }
+              }
+              found |= over != 0;
+              from = __shfl_sync(0xffffffffu, y, 31);
+            }
+          }
+        }
+        __syncwarp();
+        sync();  // (the arrays are free, and no CTA ends while another writes to it)
+      }
+    __syncthreads();  // s_open has been read
+  }
+}
+
+// CTAs per row: until every SM has two, each warp with a batch at least.
+int splits_of(int n_rows, int vocab, int type, int sms) {
+  const int batch = kBatchBytes / (type == DFLASH_T_FP32 ? 4 : 2);
+  const int most = (vocab + batch * kWarps - 1) / (batch * kWarps);
+  int s = 1;  // powers of two
+  while (2 * s <= kMaxSplits && 2 * s <= most && static_cast<long long>(n_rows) * s < sms) s *= 2;
+  return s;
+}
+
+template <int TYPE>
+cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows) * a.splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
+  cudaError_t e = cudaSuccess;
+  if (a.splits > 8)  // beyond the portable size
+    e = cudaFuncSetAttribute(sample_plain_kernel<TYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, sample_plain_kernel<TYPE>, a);
+  if (e != cudaSuccess) return e;
+  const int most = 2 * sms / kRestCtas;  // two CTAs per SM
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows < most ? a.n_rows : most) * kRestCtas);
+  attr[0].val.clusterDim.x = kRestCtas;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_rest_kernel<TYPE>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sample_plain(SampleArgs a, int type, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  a.splits = splits_of(a.n_rows, a.vocab, type, sms);
+  return type == DFLASH_T_FP32 ? launch<DFLASH_T_FP32>(a, sms, st)
+         : type == DFLASH_T_BF16 ? launch<DFLASH_T_BF16>(a, sms, st)
+                                 : launch<DFLASH_T_FP16>(a, sms, st);
+}
+
+}  // namespace dflash

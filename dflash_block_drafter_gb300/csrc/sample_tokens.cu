@@ -5,38 +5,28 @@
 //   tokens above v and S that of all;  w_i >= min_p;  x_i > -infinity
 //   token: the first id whose kept weights up to it, in order of ids, exceed u times all of them.
 //
-// All of this is a matter of comparisons, so that a row's id has to be the one of the
-// definition whatever the order of additions: weights are whole numbers of
-// 2^-F (F = 45 for up to 2^17 tokens, one less for each doubling), right to about
-// 2^-43 relative, and sums of them are exact.  e^y is computed in pairs of FP32
-// numbers by a table of 2^(j/32) and a short series (Tang, "Table-driven
-// implementation of the exponential function", 1989): FP64 instructions are
-// sixty times as slow here.
+// (Exact weights and the error of FP32 sums: sampling.cuh.)
 //
-// The CTAs of a cluster hold a row in their shared memory, so that it is read once
-// from global memory however often it is looked at.  Few tokens decide most rows, and
-// plain FP32 finds them:
-//  - With a filter, a bound below the threshold.  Of top-k: the k-th largest of the threads' own maxima, by a
+// Rows with a filter; calls without any go to sample_plain.cu.  The CTAs of a cluster hold a row in their
+// shared memory, so that it is read once from global memory however often it is looked at.  Few tokens decide
+// most rows, and plain FP32 finds them:
+//  - A bound below the threshold.  Of top-k: the k-th largest of the threads' own maxima, by a
 //    histogram of them.  Of top-p: the first of 512 ranges of logits below which less than
 //    (1 - p) S can lie, counted with each range's largest weight.  Of min-p: itself.  The
 //    tokens above the bound, if they are at most kList, go to the first CTA, which
 //    sorts them and decides everything with exact weights.  S itself, which a top-p without top-k compares with, comes
 //    from FP32 sums with a bound on their error; where that leaves it open which token is
-//    the last (or which u names, without a filter), S is added up exactly.
-//  - Without one, FP32 sums by CTA, warp and lane lead to the token; the exact ones are formed if a border
-//    of it lies within the error's bound.
+//    the last, S is added up exactly.
+//  - A row of such a call whose filters are off: FP32 sums by CTA, warp and lane lead to the token; the exact ones
+//    are formed if a border of it lies within the error's bound.
 // Else (long lists) a threshold is found digit by digit: counts (and exact weights) of up to
 // 1024 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key.
-//
-// The bound of an FP32 sum, relative to S, in units of 2^-24: a weight's exponent y = (x - m) c is off by 3 |y| (difference, c,
-// product), and the mean of |y| over the weights, their entropy less log2 S, is 19 at most for 2^19 tokens: 40 with ln 2;
-// 2^y 4; additions, of 16 pieces in a thread, in it, over warps and CTAs: 16 + 3 + 5 + 16 + 16.  In all under 128: kError.
 #include <cstddef>
 
 #include "common.cuh"
 #include "internal.h"
 #include "kernels.h"
-#include "logits.cuh"
+#include "sampling.cuh"
 
 namespace dflash {
 namespace {
@@ -44,237 +34,9 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
-constexpr int kMaxSplits = 16;             // CTAs of a cluster
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kList = 2048;                // tokens that the first CTA sorts
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
-constexpr float kError = 0x1p-17f;         // of an FP32 sum of weights, relative
-constexpr int kFixed = 45;                 // binary places of a weight
-constexpr float kMaxTemperature = 0x1p64f;
-
-struct SampleArgs {
-  const uint8_t* logits;
-  long long row_bytes;
-  int n_rows, vocab, splits, pieces;  // pieces: 16-byte pieces of a row that a CTA holds
-  int drop;                           // places less than kFixed
-  const float* uniform;
-  const float* temperature;
-  const int32_t* top_k;
-  const float* top_p;
-  const float* min_p;
-  int32_t* tokens;
-  float* logprob;
-  int32_t* kept;
-  int32_t* status;
-};
-
-// ------------------------------------------------------------- exact weights
-struct TableEntry {
-  uint64_t fixed;  // 2^(j/32) in units of 2^-45
-  float hi, lo;    // the same, as the sum of two
-};
-__constant__ TableEntry kTable[32] = {
-    {35184372088832ull, 0x1.000000p+0f, 0x0.0p+0f},
-    {35954809514763ull, 0x1.059b0ep+0f, -0x1.9d4f52p-25f},
-    {36742117323538ull, 0x1.0b5586p+0f, 0x1.9f3122p-25f},
-    {37546664928439ull, 0x1.11301ep+0f, -0x1.fdb496p-25f},
-    {38368829831843ull, 0x1.172b84p+0f, -0x1.c15742p-27f},
-    {39208997802355ull, 0x1.1d4874p+0f, -0x1.d2e8cap-25f},
-    {40067563055812ull, 0x1.2387a6p+0f, 0x1.ceac48p-25f},
-    {40944928440254ull, 0x1.29e9e0p+0f, -0x1.5c0424p-25f},
-    {41841505624942ull, 0x1.306fe0p+0f, 0x1.4636e2p-25f},
-    {42757715293524ull, 0x1.371a74p+0f, -0x1.18aac6p-25f},
-    {43693987341416ull, 0x1.3dea64p+0f, 0x1.824684p-25f},
-    {44650761077522ull, 0x1.44e086p+0f, 0x1.8624b4p-30f},
-    {45628485430356ull, 0x1.4bfdaep+0f, -0x1.593abcp-25f},
-    {46627619158687ull, 0x1.5342b6p+0f, -0x1.2c5610p-25f},
-    {47648631066792ull, 0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
-    {48692000224427ull, 0x1.6247ecp+0f, -0x1.f8b550p-25f},
-    {49758216191608ull, 0x1.6a09e6p+0f, 0x1.9fcef4p-26f},
-    {50847779248319ull, 0x1.71f75ep+0f, 0x1.1d8beep-25f},
-    {51961200629251ull, 0x1.7a1148p+0f, -0x1.829fd0p-25f},
-    {53099002763676ull, 0x1.82589ap+0f, -0x1.accc7cp-26f},
-    {54261719520578ull, 0x1.8ace54p+0f, 0x1.15506ep-27f},
-    {55449896459148ull, 0x1.93737cp+0f, -0x1.e6474p-25f},
-    {56664091084769ull, 0x1.9c4918p+0f, 0x1.51f848p-27f},
-    {57904873110603ull, 0x1.a5503cp+0f, -0x1.b83b54p-25f},
-    {59172824724903ull, 0x1.ae89fap+0f, -0x1.a94b14p-26f},
-    {60468540864189ull, 0x1.b7f770p+0f, -0x1.a09438p-25f},
-    {61792629492389ull, 0x1.c199bep+0f, -0x1.3d56b2p-27f},
-    {63145711886113ull, 0x1.cb720ep+0f, -0x1.8837ccp-27f},
-    {64528422926153ull, 0x1.d5818ep+0f, -0x1.822dbcp-27f},
-    {65941411395383ull, 0x1.dfc974p+0f, -0x1.908c94p-25f},
-    {67385340283170ull, 0x1.ea4afap+0f, 0x1.52486cp-27f},
-    {68860887096459ull, 0x1.f50766p+0f, -0x1.246eb0p-26f},
-};
-
-// What a weight depends on besides its logit: m, and log2(e) / T as the sum of two.
-struct Scale {
-  float m, hi, lo;
-  int drop;
-};
-
-// e^((x - m) / T) in units of 2^-(kFixed - drop).  (Products and sums are written out: the
-// compiler must not contract them.)
-__device__ __forceinline__ uint64_t weight(float x, const Scale& c, const TableEntry* table) {
-  // x - m = s + e exactly
-  const float b = -c.m;
-  const float s = __fadd_rn(x, b), v = __fsub_rn(s, x);
-  const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(s, v)), __fsub_rn(b, v));
-  // times log2(e) / T: p + q
-  const float p = __fmul_rn(s, c.hi);
-  if (!(p > -48.f)) return 0;  // (masked values too)
-  const float q = __fmaf_rn(e, c.hi, __fmaf_rn(s, c.lo, __fmaf_rn(s, c.hi, -p)));
-  // = n + j / 32 + r, |r| <= 1/64
-  constexpr float ROUND = 393216.f;  // 1.5 2^18: adding it leaves multiples of 1/32
-  const float t = __fadd_rn(p, ROUND);
-  const int k = __float_as_int(t) - __float_as_int(ROUND);
-  const float r = __fsub_rn(p, __fsub_rn(t, ROUND));
-  const float rh = __fadd_rn(r, q), rl = __fsub_rn(q, __fsub_rn(rh, r));
-  // a = r ln 2, u = e^a - 1
-  constexpr float LN2 = 0x1.62e430p-1f, LN2_LO = -0x1.05c610p-29f;
-  const float ah = __fmul_rn(rh, LN2);
-  const float al = __fadd_rn(__fmaf_rn(rh, LN2, -ah), __fmaf_rn(rh, LN2_LO, __fmul_rn(rl, LN2)));
-  const float h = __fmul_rn(0.5f, ah), s2 = __fmul_rn(h, ah);
-  const float s2l = __fmaf_rn(ah, al, __fmaf_rn(h, ah, -s2));
-  const float cubic = __fmul_rn(__fmul_rn(s2, ah), __fmaf_rn(ah, __fmaf_rn(ah, 1.f / 60, 1.f / 12), 1.f / 3));  // a^3/6 + a^4/24 + a^5/120
-  const float uh = __fadd_rn(ah, s2);
-  const float ul = __fadd_rn(__fsub_rn(s2, __fsub_rn(uh, ah)), __fadd_rn(al, __fadd_rn(s2l, cubic)));
-  // times 2^(j / 32): its own whole number, and the rest in two steps of 2^-23 and 2^-45
-  const TableEntry f = table[k & 31];
-  const float vh = __fmul_rn(f.hi, uh);
-  const float vl = __fadd_rn(__fmaf_rn(f.hi, uh, -vh), __fmaf_rn(f.hi, ul, __fmul_rn(f.lo, uh)));
-  constexpr float STEP1 = 1.5f, STEP2 = 1.5f * 0x1p-22f;
-  const float t1 = __fadd_rn(__fadd_rn(vh, vl), STEP1);
-  const float rest = __fadd_rn(__fsub_rn(vh, __fsub_rn(t1, STEP1)), vl);
-  const float t2 = __fadd_rn(rest, STEP2);
-  const long long add = (static_cast<long long>(__float_as_int(t1) - __float_as_int(STEP1)) << 22) +
-                        (__float_as_int(t2) - __float_as_int(STEP2));
-  return (f.fixed + add) >> (c.drop - (k >> 5));
-}
-
-// ------------------------------------------------------------------ keys
-// Whole numbers in the order of the values, -0 with +0.
-template <int TYPE>
-struct Keys {
-  static constexpr bool WIDE = TYPE == DFLASH_T_FP32;
-  static constexpr uint32_t SIGN = WIDE ? 0x80000000u : 0x8000u, ALL = WIDE ? 0xffffffffu : 0xffffu;
-  static constexpr uint32_t INF = WIDE ? 0x7f800000u : TYPE == DFLASH_T_BF16 ? 0x7f80u : 0x7c00u;
-  // the lowest key of a value that is not masked
-  static constexpr uint32_t LOWEST = (~(SIGN | INF) & ALL) + 1;
-  static __device__ __forceinline__ uint32_t of(uint32_t bits) {
-    if (bits == SIGN) bits = 0;
-    return bits & SIGN ? ~bits & ALL : bits | SIGN;
-  }
-  static __device__ __forceinline__ uint32_t bits(const uint4& v, int e) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (WIDE) return w[e];
-    return e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
-  }
-  static __device__ __forceinline__ float value(uint32_t b) {
-    if constexpr (WIDE) return __uint_as_float(b);
-    if constexpr (TYPE == DFLASH_T_BF16) return __uint_as_float(b << 16);
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
-  }
-  static __device__ __forceinline__ uint32_t of_value(float x) {
-    if constexpr (WIDE) return of(__float_as_uint(x));
-    if constexpr (TYPE == DFLASH_T_BF16) return of(__float_as_uint(x) >> 16);
-    return of(__half_as_ushort(__float2half_rn(x)));
-  }
-  static __device__ __forceinline__ float value_of(uint32_t key) { return value(key & SIGN ? key & ~SIGN : ~key & ALL); }
-  // the larger of two words' values, value by value, NaN if either is one
-  static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (WIDE) {
-      float f;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
-      r = __float_as_uint(f);
-    } else if constexpr (TYPE == DFLASH_T_BF16) {
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    } else {
-      asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    }
-    return r;
-  }
-  static __device__ __forceinline__ bool has_nan(uint32_t w) {
-    if constexpr (WIDE) return (w & 0x7fffffffu) > INF;
-    return (w & 0x7fffu) > INF || (w >> 16 & 0x7fffu) > INF;
-  }
-  static __device__ __forceinline__ float top_of(const uint4& v) {
-    using E = Elem<TYPE>;
-    return E::max_of(E::max_words(E::max_words(v.x, v.y), E::max_words(v.z, v.w)));
-  }
-  // FP32 weights of a piece
-  static __device__ __forceinline__ float quick_sum(const uint4& v, float m, float c) {
-    constexpr int VEC = Elem<TYPE>::VEC;
-    float x[VEC];
-    Elem<TYPE>::widen(v, x);
-    const uint64_t minus = pack2(-m, -m), c2 = pack2(c, c);
-    uint64_t s[VEC / 2];
-#pragma unroll
-    for (int e = 0; e < VEC; e += 2) {
-      float y0, y1;
-      unpack2(mul2(add2(pack2(x[e], x[e + 1]), minus), c2), y0, y1);
-      s[e / 2] = pack2(ex2_approx(y0), ex2_approx(y1));
-    }
-#pragma unroll
-    for (int o = VEC / 4; o; o >>= 1)
-#pragma unroll
-      for (int e = 0; e < o; ++e) s[e] = add2(s[e], s[e + o]);
-    float s0, s1;
-    unpack2(s[0], s0, s1);
-    return s0 + s1;
-  }
-  // values of a piece above -infinity
-  static __device__ __forceinline__ int unmasked(const uint4& v) {
-    constexpr int VEC = Elem<TYPE>::VEC;
-    int c = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) c += bits(v, e) != (SIGN | INF);
-    return c;
-  }
-  // the key of the smallest value that is not below x
-  static __device__ __forceinline__ uint32_t at_least(double x) {
-    const float f = __double2float_ru(x);
-    if constexpr (WIDE) return of(__float_as_uint(f));
-    if constexpr (TYPE == DFLASH_T_BF16) return of(__bfloat16_as_ushort(__float2bfloat16_ru(f)));
-    return of(__half_as_ushort(__float2half_ru(f)));
-  }
-};
-
-// ------------------------------------------------------------------ clusters
-__device__ __forceinline__ void cluster_sync(int splits) {
-  if (splits > 1) {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
-    __syncthreads();
-  }
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint64_t ld_cluster64(uint32_t addr) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ uint64_t shfl_up(uint64_t v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
-template <typename T>
-__device__ __forceinline__ T warp_sum(T v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 struct Found {
   uint32_t lo, hi;      // keys of the range
@@ -325,29 +87,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int n = a.splits;
   if (n > 1) cluster_arrive_relaxed();  // (every CTA has started before another writes to it)
 
-  // ---- what the row asks for
-  const float t_asked = a.temperature ? a.temperature[row] : 1.f;
-  const bool t_fine = t_asked >= 0.f && t_asked <= kMaxTemperature;
-  const float temperature = t_asked > kMaxTemperature ? kMaxTemperature : t_asked;
-  const bool greedy = !(temperature > 0.f);
-  const int k_asked = a.top_k ? a.top_k[row] : 0;
-  const bool by_k = k_asked > 0 && k_asked < a.vocab;
-  const float p = a.top_p ? a.top_p[row] : 1.f;
-  const bool by_p = p < 1.f;
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
-  const bool by_min = min_p > 0.f;
-  const float u_asked = a.uniform[row];
-  const bool u_fine = u_asked >= 0.f && u_asked < 1.f;
-  const float u = u_fine ? u_asked : u_asked >= 1.f ? 0x1.fffffep-1f : 0.f;
+  const Settings set(a, row);
+  const bool by_k = set.by_k, by_p = set.by_p, by_min = set.by_min;
+  const int k_asked = set.k;
+  const float p = set.p, u = set.u;
   if (tid < 32) sh.table[tid] = kTable[tid];
   if (tid == kThreads - 1) {
-    if (rank == 0 && (!t_fine || !u_fine || p != p || !(min_p <= 1.f))) set_status(a.status, DFLASH_DEV_BAD_VALUE);
-    if (!greedy) {
-      const double c = fmin(1.4426950408889634 / static_cast<double>(temperature), 1e38);
-      sh.scale.hi = static_cast<float>(c);
-      sh.scale.lo = static_cast<float>(c - static_cast<double>(sh.scale.hi));
-      sh.scale.drop = a.drop;
-      if (by_min) sh.log_min_p = static_cast<double>(temperature) * log(static_cast<double>(fminf(min_p, 1.f)));
+    if (rank == 0 && !set.fine) set_status(a.status, DFLASH_DEV_BAD_VALUE);
+    if (!set.greedy) {
+      set.scale(sh.scale, a.drop);
+      if (by_min) sh.log_min_p = static_cast<double>(set.temperature) * log(static_cast<double>(fminf(set.min_p, 1.f)));
     }
   }
 
@@ -435,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int per_warp = (mine + kWarps - 1) / kWarps;
   const int w0 = min(warp * per_warp, mine), w1 = min(w0 + per_warp, mine);
 
-  if (greedy) {  // the first id of the largest value
+  if (set.greedy) {  // the first id of the largest value
     uint32_t id = 0xffffffffu;
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint4 v = data[i];
@@ -472,12 +221,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const uint32_t most = K::of_value(m);
   uint32_t least = K::LOWEST;
   if (by_min) least = max(least, min(most, K::at_least(static_cast<double>(m) + sh.log_min_p)));
-
-  // ln(w / total) of a token, where w <= 1 and the largest weight, 1, is among those of the total
-  auto log_of = [&](float x, float others) { return (x - m) / temperature - log1pf(others); };
-  auto others_of = [&](uint64_t total) {
-    return static_cast<float>(total - (1ull << (kFixed - a.drop))) * exp2f(static_cast<float>(a.drop - kFixed));
-  };
 
   // The sum over the cluster of a value per thread, and the CTAs' sums in sh.cta_w.
   auto cluster_total = [&](uint64_t v) {
@@ -598,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 if (before <= at && c > at) {
                   if (before + off <= at && c - off > at) {
                     a.tokens[row] = (first + i) * VEC + e - skip;
-                    if (a.logprob) a.logprob[row] = log_of(x, total - 1.f);
+                    if (a.logprob) a.logprob[row] = set.log_of(x, m, total - 1.f);
                     if (a.kept) {
                       uint64_t all = 0;
                       for (int r = 0; r < n; ++r) all += sh.cta_w[r];
@@ -829,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             c += weight(x, scale, sh.table);
             if (c > at) {
               a.tokens[row] = static_cast<int32_t>(entry);
-              if (a.logprob) a.logprob[row] = log_of(x, others_of(total));
+              if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
               if (a.kept) a.kept[row] = static_cast<int32_t>(keep);
               break;
             }
@@ -1087,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 if (c > at) {
                   done = true;
                   a.tokens[row] = (first + i) * VEC + e - skip;
-                  if (a.logprob) a.logprob[row] = log_of(x, others_of(total));
+                  if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
                 }
               }
             }
@@ -1158,10 +901,6 @@ int dflash_sample_tokens(const void* logits, int32_t type, int64_t row_stride, i
   const int size = type == DFLASH_T_FP32 ? 4 : 2;
   if (!logits || reinterpret_cast<uintptr_t>(logits) % size || !uniform || !tokens) return DFLASH_ERR_INVALID_ARG;
   SampleArgs a{};
-  const int vec = 16 / size;
-  const long long row_pieces = (vocab + vec - 1) / vec + 1;  // (a row may begin inside a piece)
-  cudaError_t e = splits_of(n_rows, row_pieces, &a.splits, &a.pieces);
-  if (e != cudaSuccess) return cuda_status(e, "sample tokens");
   a.logits = static_cast<const uint8_t*>(logits);
   a.row_bytes = row_stride * size;
   a.n_rows = n_rows;
@@ -1177,6 +916,11 @@ int dflash_sample_tokens(const void* logits, int32_t type, int64_t row_stride, i
   a.kept = kept;
   a.status = dev_status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!top_k && !top_p && !min_p) return cuda_status(launch_sample_plain(a, type, st), "sample tokens");
+  const int vec = 16 / size;
+  const long long row_pieces = (vocab + vec - 1) / vec + 1;  // (a row may begin inside a piece)
+  cudaError_t e = splits_of(n_rows, row_pieces, &a.splits, &a.pieces);
+  if (e != cudaSuccess) return cuda_status(e, "sample tokens");
   e = type == DFLASH_T_FP32 ? launch<DFLASH_T_FP32>(a, st)
       : type == DFLASH_T_BF16 ? launch<DFLASH_T_BF16>(a, st)
                               : launch<DFLASH_T_FP16>(a, st);

@@ -651,7 +651,7 @@ size_t dflash_kv4_prefix_attention_workspace(const dflash_kv4_cache* cache, int3
  * DFLASH_DEV_BAD_VALUE: uniform outside [0, 1) (the nearest is taken), temperature
  * negative or NaN (greedy) or above 2^64 (2^64), top_p NaN (off), min_p NaN (off) or above 1 (1).
  * DFLASH_DEV_NONFINITE: a NaN or +infinity in the row, whose token is -1.  vocab <=
- * 2^19, n_rows <= 2^24 (else DFLASH_ERR_CAPACITY).  One launch. */
+ * 2^19, n_rows <= 2^24 (else DFLASH_ERR_CAPACITY). */
 int dflash_sample_tokens(const void* logits, int32_t type, int64_t row_stride, int32_t n_rows, int32_t vocab,
                          const float* uniform, const float* temperature, const int32_t* top_k, const float* top_p,
                          const float* min_p, int32_t* tokens, float* logprob, int32_t* kept, int32_t* dev_status,
