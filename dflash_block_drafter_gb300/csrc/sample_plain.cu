@@ -1,15 +1,20 @@
 // Tokens drawn from the whole distribution, and greedy ones: dflash_sample_tokens without a filter.
 //
-// One pass over the logits.  A warp takes a batch of 2 KB at a time and leaves
+// One pass over the logits.  A warp takes a batch of 2 KB at a time from its ring of bulk copies and leaves
 // its sum of 2^((x - r) c) with the reference r, the largest value the warp has met; the
 // batches' sums, brought to one reference, lead to the batch in which u lies, which is
-// read once more.  The token stands if both of its borders are further from u than FP32 sums
-// may be off (sampling.cuh); else the row is left to a second kernel, which forms exact sums with clusters of
-// eight CTAs (one CTA alone takes 70 us for 151936 tokens, the tail of a call of 1000 rows).  A greedy row is one look: the first batch whose reference is the largest value
-// holds its first id.
+// read once more.  The token stands if both of its borders are further from u than these sums
+// may be off; else the row is left to a second kernel, which forms exact sums with clusters of
+// eight CTAs (one CTA alone takes 70 us for 151936 tokens, the tail of a call of 1000 rows).  A greedy row is one look: the
+// first batch whose reference is the largest value holds its first id.
 //
-// The bytes bound it for many rows (four 16-byte loads in flight per thread, then 2^x); with few rows a
-// row's batches are split over the CTAs of a cluster.
+// The bound: a weight is 2^(x c + k), where k = -r c as FP32 has it for the reference r; what k is off by is the same
+// for all weights.  The exponent y is off by 1.5 |y| 2^-24 (one rounding, and c's); the mean of |y| over the weights
+// is their entropy less log2 S, log2(vocab / S) at most: with ln 2, 1.1 log2(vocab / S) units of 2^-24.  2^y 4; sums in a
+// batch 10 (tree, loads, lanes); a batch's factor 6, a CTA's 6, roundings of single weights 2; sums of those are whole
+// numbers.  A border of a token and u S err apart by the errors of the weights on either side, u or 1 - u of each: not more.
+//
+// Few rows: a row's batches are split over the CTAs of a cluster.
 #include <cstddef>
 
 #include "sampling.cuh"
@@ -21,6 +26,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kLoads = 4;  // 16-byte loads of a thread per batch
 constexpr int kBatchBytes = 32 * kLoads * 16;
+constexpr int kStages = 2;  // batches of a warp on their way
+constexpr int kRingBytes = kWarps * kStages * kBatchBytes;
 constexpr int kRestCtas = 8;         // CTAs for a row that the FP32 sums leave open
 constexpr int32_t kUndecided = -2;  // the token of such a row, between the kernels
 constexpr int kMaxBatches = (1 << 19) * 4 / kBatchBytes + 1;  // (a row may begin inside a piece)
@@ -62,31 +69,29 @@ __device__ __forceinline__ void load_batch(const uint8_t* src, const uint4* fram
   }
 }
 
+// An FP32 sum of weights in units of 2^-40, in which sums of sums are exact.
+__device__ __forceinline__ uint64_t units(float x) { return static_cast<uint64_t>(__float2ull_rn(x * 0x1p40f)); }
+
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
   constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
+  extern __shared__ __align__(128) uint8_t ring[];  // [kWarps][kStages] batches
   __shared__ float2 part[kMaxBatches];  // reference and sum of this CTA's batches
+  __shared__ uint64_t full[kWarps][kStages];
   __shared__ Scale s_scale;
-  __shared__ float s_ref[kWarps], s_sum[kWarps];
+  __shared__ float s_ref[kWarps];
+  __shared__ uint64_t s_sum[kWarps];
   __shared__ uint32_t s_count[kWarps], s_nan[kWarps];
   __shared__ float cta_ref[kMaxSplits], cta_sum[kMaxSplits];
   __shared__ uint32_t cta_count[kMaxSplits], cta_nan[kMaxSplits];
   __shared__ int s_batch, s_done;
-  __shared__ float s_from;
+  __shared__ uint64_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / a.splits, rank = blockIdx.x - row * a.splits, n = a.splits;
   if (n > 1) cluster_arrive_relaxed();
   pdl_launch_dependents();
-  const Settings set(a, row);
-  if (tid == kThreads - 1) {
-    if (rank == 0 && !set.fine) set_status(a.status, DFLASH_DEV_BAD_VALUE);
-    s_scale.hi = 1.f;
-    if (!set.greedy) set.scale(s_scale, a.drop);
-    s_batch = 0x7fffffff;
-    s_done = 0;
-  }
 
   const uint8_t* src = a.logits + row * a.row_bytes;
   const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E::BYTES;
@@ -96,17 +101,58 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   // this CTA's batches
   const int b0 = static_cast<int>(static_cast<long long>(batches) * rank / n), b1 = static_cast<int>(static_cast<long long>(batches) * (rank + 1) / n);
   auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
+  // whole batches come through the warp's ring by bulk copies, those at the row's ends by loads
+  auto inside = [&](int b) { return b * BATCH >= skip && b * BATCH + BATCH <= places; };
+  uint8_t* mine_ring = ring + warp * kStages * kBatchBytes;
+  auto copy = [&](int b, int st) {  // (one lane)
+    mbar_arrive_expect_tx(&full[warp][st], kBatchBytes);
+    bulk_g2s(mine_ring + st * kBatchBytes, frame + static_cast<size_t>(b) * (kBatchBytes / 16), kBatchBytes, &full[warp][st]);
+  };
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(&full[warp][st], 1);
+    fence_barrier_init();
+    for (int st = 0; st < kStages; ++st) {
+      const int b = b0 + warp + st * kWarps;
+      if (b < b1 && inside(b)) copy(b, st);
+    }
+  }
+  __syncwarp();
+  const Settings set(a, row);
+  if (tid == kThreads - 1) {
+    if (rank == 0 && !set.fine) set_status(a.status, DFLASH_DEV_BAD_VALUE);
+    s_scale.hi = 1.f;
+    if (!set.greedy) set.scale(s_scale, a.drop);
+    s_batch = 0x7fffffff;
+    s_done = 0;
+  }
   __syncthreads();  // (c)
   const float c = s_scale.hi;
+  // what a reference adds to an exponent; one so low (masked values) that nothing has weight beside any other: 0
+  auto none = [&](float r) { return !(r * c > -0x1p100f); };
+  auto start = [&](float r) { return none(r) ? 0.f : -(r * c); };
 
   // ---- the pass
   float ref = -INFINITY;
   uint32_t count = 0, tops = E::NOTHING;
+  bool ok = true;
   {
-    uint4 v[kLoads];
-    int b = b0 + warp;
-    if (b < b1) load(b, v);
-    for (; b < b1; b += kWarps) {
+    int st = 0;
+    uint32_t phases = 0;  // bit st: parity of the stage's next copy
+    for (int b = b0 + warp; b < b1; b += kWarps, st = st + 1 == kStages ? 0 : st + 1) {
+      uint4 v[kLoads];
+      if (inside(b)) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][st], phases >> st & 1));
+        phases ^= 1u << st;
+        const uint4* from = reinterpret_cast<const uint4*>(mine_ring + st * kBatchBytes);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) v[j] = from[j * 32 + lane];
+        __syncwarp();
+      } else {
+        load(b, v);
+      }
+      const int next = b + kStages * kWarps;
+      // (the lanes' reads of the stage are done: their values are in registers)
+      if (ok && lane == 0 && next < b1 && inside(next)) copy(next, st);
       uint32_t top = E::NOTHING, low = v[0].x;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
@@ -115,14 +161,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
       }
       tops = K::max_nan(tops, top);
       ref = fmaxf(ref, warp_max(fmaxf(E::max_of(top), -INFINITY)));
-      const float from = ref == -INFINITY ? 0.f : ref;
       float sum = 0.f;
       if (!set.greedy) {
+        const float k = start(ref);
         float s[kLoads];
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) s[j] = K::quick_sum(v[j], from, c);
+        for (int j = 0; j < kLoads; ++j) s[j] = K::quick_sum_from(v[j], c, k);
         sum = (s[0] + s[1]) + (s[2] + s[3]);
-        if (K::masked(low)) {
+        if (__any_sync(0xffffffffu, K::masked(low))) {
 #pragma unroll
           for (int j = 0; j < kLoads; ++j) count += K::unmasked(v[j]);
         } else {
@@ -130,10 +176,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
         }
       }
       static_assert(kLoads == 4, "sum");
-      if (b + kWarps < b1) load(b + kWarps, v);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) part[b - b0] = make_float2(ref, sum);
+    }
+    if (!ok) {
+      // a copy did not come in time: none is issued any more, and what is in flight lands before the CTA ends
+      for (int i = 0; i < kStages; ++i) mbar_wait(&full[warp][i], phases >> i & 1);
+      if (lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
     }
   }
   count = __reduce_add_sync(0xffffffffu, count);
@@ -148,21 +198,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   const int j0 = min(tid * per, mine), j1 = min(j0 + per, mine);  // the thread's batches, one behind the other
   auto of_batch = [&](int j) {  // relative to m as it is by then
     const float2 x = part[j];
-    return x.x == -INFINITY ? 0.f : x.y * ex2_approx((x.x - m) * c);
+    return none(x.x) ? 0 : units(x.y * ex2_approx(start(m) - start(x.x)));
   };
-  float own = 0.f;
-  for (int j = j0; j < j1; ++j) own += of_batch(j);
-  const float upto = warp_upto(own, lane);
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  float before = upto - own, cta = 0.f;
+  uint64_t own, before, cta;  // of the thread's batches, of those before them, of the CTA's
+  auto add_up = [&]() {
+    own = 0;
+    for (int j = j0; j < j1; ++j) own += of_batch(j);
+    const uint64_t upto = warp_upto(own, lane);
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    before = upto - own, cta = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    cta += s_sum[w];
-  }
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      cta += s_sum[w];
+    }
+  };
+  add_up();
   // ---- the CTAs' results
-  float total = cta, at_cta = 0.f, m_own = m;
+  uint64_t total = cta, below = 0;
   bool owner = true;
   if (n > 1) {
     cluster_wait();  // every CTA has started
@@ -171,30 +225,33 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(to), tid)), "r"(v) : "memory");
       };
       put(&cta_ref[rank], __float_as_uint(m));
-      put(&cta_sum[rank], __float_as_uint(cta));
+      put(&cta_sum[rank], __float_as_uint(static_cast<float>(cta) * 0x1p-40f));
       put(&cta_count[rank], all);
       put(&cta_nan[rank], bad);
     }
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const float m_own = m;
     all = bad = 0;
     for (int r = 0; r < n; ++r) m = fmaxf(m, cta_ref[r]), all += cta_count[r], bad |= cta_nan[r];
-    auto of_cta = [&](int r) { return cta_ref[r] == -INFINITY ? 0.f : cta_sum[r] * ex2_approx((cta_ref[r] - m) * c); };
-    total = 0.f;
+    auto of_cta = [&](int r) { return none(cta_ref[r]) ? 0 : units(cta_sum[r] * ex2_approx(start(m) - start(cta_ref[r]))); };
+    total = 0;
     for (int r = 0; r < n; ++r) total += of_cta(r);
     // the one CTA that goes on: the first whose sums pass u, or that has the largest value
-    float sum = 0.f;
-    int who = -1, last = 0;
-    for (int r = 0; r < n && who < 0; ++r) {
-      const float x = of_cta(r);
-      if (x > 0.f) last = r;
-      if (set.greedy ? cta_ref[r] == m : sum + x > set.u * total) who = r;
-      else sum += x;
+    const uint64_t at = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(total));
+    int who = 0;
+    for (; who < n - 1; ++who) {
+      if (set.greedy) {
+        if (cta_ref[who] == m) break;
+        continue;
+      }
+      const uint64_t x = of_cta(who);
+      if (at < below + x) break;
+      below += x;
     }
-    if (who < 0) who = last, sum -= of_cta(last);
     owner = who == rank;
-    at_cta = sum;
+    if (owner && m != m_own && !set.greedy) add_up();
   }
   if (bad || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from
     if (rank == 0 && tid == 0) {
@@ -235,44 +292,51 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   }
 
   // ---- the batch in which u lies, and the token in it
-  const float at = set.u * total, off = kError * total;
-  {
-    const float f = m_own == -INFINITY ? 0.f : ex2_approx((m_own - m) * c);  // of this CTA's sums
-    float x = at_cta + before * f;
-    const float end = x + own * f;
-    if (j0 < j1 && x <= at && at < end) {  // (one thread, or none where two sums differ: then the exact ones decide)
-      int j = j0;
-      for (; j < j1 - 1; ++j) {
-        const float y = of_batch(j);
-        if (at < x + y) break;
-        x += y;
-      }
-      s_batch = j;
-      s_from = x;
+  const uint64_t at = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(total));
+  const float k = start(m);
+  const float whole = static_cast<float>(total) * 0x1p-40f;
+  const uint64_t off = units(whole * 0x1p-24f * (32.f + 1.1f * log2f(static_cast<float>(a.vocab) / whole)));
+  // (exponents beyond FP32's range: no border is far enough)
+  const bool close = !(fabsf(m) * c < 0x1p100f);
+  before += below;
+  if (!close && before <= at && at < before + own) {  // (one thread, or none where the CTAs' sums differ: then the exact ones decide)
+    uint64_t x = before;
+    int j = j0;
+    for (; j < j1 - 1; ++j) {
+      const uint64_t y = of_batch(j);
+      if (at < x + y) break;
+      x += y;
     }
+    s_batch = j;
+    s_from = x;
   }
   __syncthreads();
   if (warp == 0 && s_batch != 0x7fffffff) {
     uint4 v[kLoads];
     const int b = b0 + s_batch;
     load(b, v);
-    float from = s_from;
+    uint64_t from = s_from;
     bool found = false;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const float w = K::quick_sum(v[j], m, c);
-      const float x = warp_upto(w, lane) + from;
+      const uint64_t w = units(K::quick_sum_from(v[j], c, k));
+      const uint64_t x = warp_upto(w, lane) + from;
       const unsigned over = __ballot_sync(0xffffffffu, x > at);
       if (!found && over && lane == __ffs(over) - 1) {
-        float y = x - w;
+        uint64_t y = x - w;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float value = K::value(K::bits(v[j], e)), low = y;
-          y += ex2_approx((value - m) * c);
+          const float value = K::value(K::bits(v[j], e));
+          const uint64_t low = y;
+          y += units(ex2_approx(fmaf(value, c, k)));
           // the first past u, further from both of its borders than the sums may be off
-          if (low <= at && y > at && low + off <= at && y - off > at) {
+          if (low <= at && y > at && low + off <= at && y > at + off) {
             a.tokens[row] = b * BATCH + (j * 32 + lane) * VEC + e - skip;
-            if (a.logprob) a.logprob[row] = set.log_of(value, m, total - 1.f);
+            if (a.logprob) {  // (in these sums the largest weight is 2^(m c + k), about 1)
+              const float most = ex2_approx(fmaf(m, c, k));
+              const uint64_t w = units(most);
+              a.logprob[row] = set.log_of(value, m, static_cast<float>(total > w ? total - w : 0) * 0x1p-40f / most);
+            }
             if (a.kept) a.kept[row] = static_cast<int32_t>(all);
             s_done = 1;
           }
@@ -283,7 +347,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
     }
   }
   __syncthreads();
-  if (!s_done && tid == 0) a.tokens[row] = kUndecided;
+  if (!s_done && tid == 0) {
+    a.tokens[row] = kUndecided;
+    // (what the second kernel need not find again, where there is a place for it)
+    if (a.logprob && a.kept) a.logprob[row] = m, a.kept[row] = static_cast<int32_t>(all);
+  }
 }
 
 // Rows that the sums left open: exact ones, by clusters of kRestCtas.  The clusters share the rows out by
@@ -329,34 +397,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         const int batches = (places + BATCH - 1) / BATCH;
         const int b0 = batches * rank / kRestCtas, b1 = batches * (rank + 1) / kRestCtas;
         auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
-        uint32_t tops = E::NOTHING, count = 0;
-        for (int b = b0 + warp; b < b1; b += kWarps) {
-          uint4 v[kLoads];
-          load(b, v);
+        float m;
+        uint32_t all;
+        if (a.logprob && a.kept) {  // left there by the first kernel
+          m = __ldcg(a.logprob + row), all = static_cast<uint32_t>(__ldcg(a.kept + row));
+          __syncthreads();  // (s_scale)
+        } else {
+          uint32_t tops = E::NOTHING, count = 0;
+          for (int b = b0 + warp; b < b1; b += kWarps) {
+            uint4 v[kLoads];
+            load(b, v);
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            tops = E::max_words(tops, E::max_words(E::max_words(v[j].x, v[j].y), E::max_words(v[j].z, v[j].w)));
-            count += K::unmasked(v[j]);
+            for (int j = 0; j < kLoads; ++j) {
+              tops = E::max_words(tops, E::max_words(E::max_words(v[j].x, v[j].y), E::max_words(v[j].z, v[j].w)));
+              count += K::unmasked(v[j]);
+            }
           }
-        }
-        const uint32_t key = __reduce_max_sync(0xffffffffu, float_order_key(E::max_of(tops)));
-        count = __reduce_add_sync(0xffffffffu, count);
-        if (lane == 0) s_key[warp] = key, s_count[warp] = count;
-        __syncthreads();
-        if (tid < kRestCtas) {
-          uint32_t x = 0, y = 0;
+          const uint32_t key = __reduce_max_sync(0xffffffffu, float_order_key(E::max_of(tops)));
+          count = __reduce_add_sync(0xffffffffu, count);
+          if (lane == 0) s_key[warp] = key, s_count[warp] = count;
+          __syncthreads();
+          if (tid < kRestCtas) {
+            uint32_t x = 0, y = 0;
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) x = max(x, s_key[i]), y += s_count[i];
-          put(&cta_key[rank], x, tid);
-          put(&cta_count[rank], y, tid);
-        }
-        __syncwarp();
-        sync();
-        uint32_t top = 0, all = 0;
+            for (int i = 0; i < kWarps; ++i) x = max(x, s_key[i]), y += s_count[i];
+            put(&cta_key[rank], x, tid);
+            put(&cta_count[rank], y, tid);
+          }
+          __syncwarp();
+          sync();
+          uint32_t top = 0;
+          all = 0;
 #pragma unroll
-        for (int r = 0; r < kRestCtas; ++r) top = max(top, cta_key[r]), all += cta_count[r];
+          for (int r = 0; r < kRestCtas; ++r) top = max(top, cta_key[r]), all += cta_count[r];
+          m = float_from_order_key(top);
+        }
         Scale scale = s_scale;
-        scale.m = float_from_order_key(top);
+        scale.m = m;
         for (int b = b0 + warp; b < b1; b += kWarps) {
           uint4 v[kLoads];
           load(b, v);
@@ -450,6 +527,7 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows) * a.splits);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -457,12 +535,13 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  cudaError_t e = cudaSuccess;
-  if (a.splits > 8)  // beyond the portable size
+  cudaError_t e = cudaFuncSetAttribute(sample_plain_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e == cudaSuccess && a.splits > 8)  // beyond the portable size
     e = cudaFuncSetAttribute(sample_plain_kernel<TYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, sample_plain_kernel<TYPE>, a);
   if (e != cudaSuccess) return e;
   const int most = 2 * sms / kRestCtas;  // two CTAs per SM
+  cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows < most ? a.n_rows : most) * kRestCtas);
   attr[0].val.clusterDim.x = kRestCtas;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

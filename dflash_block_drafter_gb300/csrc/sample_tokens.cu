@@ -5,7 +5,7 @@
 //   tokens above v and S that of all;  w_i >= min_p;  x_i > -infinity
 //   token: the first id whose kept weights up to it, in order of ids, exceed u times all of them.
 //
-// (Exact weights and the error of FP32 sums: sampling.cuh.)
+// (Exact weights: sampling.cuh.)
 //
 // Rows with a filter; calls without any go to sample_plain.cu.  The CTAs of a cluster hold a row in their
 // shared memory, so that it is read once from global memory however often it is looked at.  Few tokens decide
@@ -37,6 +37,11 @@ constexpr int kBins = 1024;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kList = 2048;                // tokens that the first CTA sorts
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
+// An FP32 sum of weights may be off by, relative to the sum S of the row, in units of 2^-24: a weight's exponent
+// y = (x - m) c 3 |y| (difference, c, product), and the mean of |y| over the weights, their entropy less
+// log2 S, is 19 at most for 2^19 tokens: 40 with ln 2; 2^y 4; additions, of 16 pieces in a thread, in a
+// piece, over lanes, warps and CTAs: 16 + 3 + 5 + 16 + 16.  In all under 128.
+constexpr float kError = 0x1p-17f;
 
 struct Found {
   uint32_t lo, hi;      // keys of the range
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (i == rank) below = total, own = sh.cta_f[i];
       total += sh.cta_f[i];
     }
-    const float at = u * total, off = kError * total;
+    const float at = u * total, off = 2.f * kError * total;  // (two such sums are compared)
     if (at >= below && (at < below + own || rank == n - 1)) {  // (one CTA, by these sums)
       float from = below;
       int w = 0;

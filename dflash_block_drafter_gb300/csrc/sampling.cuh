@@ -8,10 +8,7 @@
 // implementation of the exponential function", 1989): FP64 instructions are
 // sixty times as slow here.
 //
-// Plain FP32 sums decide wherever their error leaves no doubt.  Its bound, relative to the sum S of a row, in units of
-// 2^-24: a weight's exponent y = (x - m) c is off by 3 |y| (difference, c, product), and the mean of |y| over
-// the weights, their entropy less log2 S, is 19 at most for 2^19 tokens: 40 with ln 2; 2^y 4; additions, of 16 pieces in a
-// thread, in a piece, over warps and CTAs: 16 + 3 + 5 + 16 + 16.  In all under 128: kError.
+// Plain FP32 sums decide wherever their error leaves no doubt.
 #pragma once
 
 #include "common.cuh"
@@ -24,7 +21,6 @@ namespace dflash {
 constexpr int kMaxSplits = 16;       // CTAs of a cluster
 constexpr int kFixed = 45;           // binary places of a weight
 constexpr float kMaxTemperature = 0x1p64f;
-constexpr float kError = 0x1p-17f;   // of an FP32 sum of weights, relative
 
 struct SampleArgs {
   const uint8_t* logits;
@@ -205,6 +201,27 @@ struct Keys {
     for (int e = 0; e < VEC; e += 2) {
       float y0, y1;
       unpack2(mul2(add2(pack2(x[e], x[e + 1]), minus), c2), y0, y1);
+      s[e / 2] = pack2(ex2_approx(y0), ex2_approx(y1));
+    }
+#pragma unroll
+    for (int o = VEC / 4; o; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < o; ++e) s[e] = add2(s[e], s[e + o]);
+    float s0, s1;
+    unpack2(s[0], s0, s1);
+    return s0 + s1;
+  }
+  // FP32 sum of 2^(x c + k) of a piece: an exponent is rounded once
+  static __device__ __forceinline__ float quick_sum_from(const uint4& v, float c, float k) {
+    constexpr int VEC = Elem<TYPE>::VEC;
+    float x[VEC];
+    Elem<TYPE>::widen(v, x);
+    const uint64_t c2 = pack2(c, c), k2 = pack2(k, k);
+    uint64_t s[VEC / 2];
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      float y0, y1;
+      unpack2(fma2(pack2(x[e], x[e + 1]), c2, k2), y0, y1);
       s[e / 2] = pack2(ex2_approx(y0), ex2_approx(y1));
     }
 #pragma unroll
