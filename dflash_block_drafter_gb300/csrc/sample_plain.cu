@@ -29,7 +29,7 @@ constexpr int kBatchBytes = 32 * kLoads * 16;
 constexpr int kStages = 2;  // batches of a warp on their way
 constexpr int kRingBytes = kWarps * kStages * kBatchBytes;
 constexpr int kRestCtas = 8;         // CTAs for a row that the FP32 sums leave open
-constexpr int32_t kUndecided = -2;  // the token of such a row, between the kernels
+constexpr int32_t kUndecided = -2, kClaimed = -3;  // the token of such a row, between the kernels
 constexpr int kMaxBatches = (1 << 19) * 4 / kBatchBytes + 1;  // (a row may begin inside a piece)
 
 // The largest of the warp's values (no NaN among them).
@@ -354,8 +354,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   }
 }
 
-// Rows that the sums left open: exact ones, by clusters of kRestCtas.  The clusters share the rows out by
-// their numbers.  A CTA has a part of the row's batches, which it reads twice: for the largest value (and the
+// Rows that the sums left open: exact ones, by clusters of kRestCtas.  A CTA has a part of the row's batches, which it reads twice: for the largest value (and the
 // tokens that are not masked), and for the weights.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleArgs a) {
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   __shared__ Scale s_scale;
   __shared__ uint64_t s_wide[kWarps], cta_wide[kRestCtas];
   __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[kWarps];
-  __shared__ int s_batch;
+  __shared__ int s_batch, s_row, s_told;
   __shared__ uint64_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % kRestCtas, cluster = blockIdx.x / kRestCtas, clusters = gridDim.x / kRestCtas;
@@ -379,15 +378,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   auto put = [](void* to, uint32_t v, int r) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(to), r)), "r"(v) : "memory");
   };
+  sync();  // every CTA runs before another writes to it
   pdl_wait();
-  for (long long r0 = cluster; r0 < a.n_rows; r0 += static_cast<long long>(clusters) * kThreads) {
-    const long long mine = r0 + static_cast<long long>(tid) * clusters;
-    const unsigned open = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
-    if (lane == 0) s_open[warp] = open;
-    sync();  // every CTA runs, and has seen the rows before one of them is drawn
-    for (int w = 0; w < kWarps; ++w)
-      for (unsigned left = s_open[w]; left; left &= left - 1) {
-        const int row = static_cast<int>(r0 + static_cast<long long>(w * 32 + __ffs(left) - 1) * clusters);
+  // The clusters begin at different rows, and a row belongs to the one that changes its mark.
+  const int chunks = (a.n_rows + kThreads - 1) / kThreads;
+  int chunk = static_cast<int>(static_cast<long long>(chunks) * cluster / clusters), seen = 0;
+  for (;;) {
+    if (rank == 0) {
+      int row = -1;
+      while (seen < chunks && row < 0) {
+        const int mine = chunk * kThreads + (tid + cluster * 32) % kThreads;
+        unsigned open = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
+        __syncthreads();  // s_row and s_open of the last round have been read
+        if (lane == 0) s_open[warp] = open;
+        if (tid == 0) s_row = -1;
+        __syncthreads();
+        if (tid == 0) {
+          for (int w = 0; w < kWarps && s_row < 0; ++w)
+            for (open = s_open[w]; open && s_row < 0; open &= open - 1) {
+              const int r = chunk * kThreads + (w * 32 + __ffs(open) - 1 + cluster * 32) % kThreads;
+              if (atomicCAS(a.tokens + r, kUndecided, kClaimed) == kUndecided) s_row = r;
+            }
+        }
+        __syncthreads();
+        row = s_row;
+        if (row < 0) {
+          ++seen;
+          chunk = chunk + 1 == chunks ? 0 : chunk + 1;
+        }
+      }
+      if (tid < kRestCtas) put(&s_told, static_cast<uint32_t>(row), tid);
+      __syncwarp();
+    }
+    sync();
+    const int row = s_told;
+    if (row < 0) return;
+    {
         const Settings set(a, row);
         if (tid == 0) set.scale(s_scale, a.drop);
         const uint8_t* src = a.logits + row * a.row_bytes;
@@ -507,9 +533,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           }
         }
         __syncwarp();
-        sync();  // (the arrays are free, and no CTA ends while another writes to it)
-      }
-    __syncthreads();  // s_open has been read
+        sync();  // (the arrays are free)
+    }
   }
 }
 
