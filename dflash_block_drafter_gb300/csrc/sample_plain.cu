@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   __shared__ TableEntry table[32];
   __shared__ Scale s_scale;
   __shared__ uint64_t s_wide[kWarps], cta_wide[kRestCtas];
-  __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[kWarps];
+  __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[4 * kWarps];
   __shared__ int s_batch, s_row, s_told;
   __shared__ uint64_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -381,24 +381,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   sync();  // every CTA runs before another writes to it
   pdl_wait();
   // The clusters begin at different rows, and a row belongs to the one that changes its mark.
-  const int chunks = (a.n_rows + kThreads - 1) / kThreads;
+  constexpr int LOOK = 4;  // rows of a thread at a time
+  const int chunks = (a.n_rows + LOOK * kThreads - 1) / (LOOK * kThreads);
   int chunk = static_cast<int>(static_cast<long long>(chunks) * cluster / clusters), seen = 0;
   for (;;) {
     if (rank == 0) {
       int row = -1;
       while (seen < chunks && row < 0) {
-        const int mine = chunk * kThreads + (tid + cluster * 32) % kThreads;
-        unsigned open = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
+        unsigned open[LOOK];
+#pragma unroll
+        for (int i = 0; i < LOOK; ++i) {
+          const int mine = (chunk * LOOK + i) * kThreads + tid;
+          open[i] = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
+        }
         __syncthreads();  // s_row and s_open of the last round have been read
-        if (lane == 0) s_open[warp] = open;
+        if (lane < LOOK) s_open[lane * kWarps + warp] = lane == 0 ? open[0] : lane == 1 ? open[1] : lane == 2 ? open[2] : open[3];
         if (tid == 0) s_row = -1;
         __syncthreads();
         if (tid == 0) {
-          for (int w = 0; w < kWarps && s_row < 0; ++w)
-            for (open = s_open[w]; open && s_row < 0; open &= open - 1) {
-              const int r = chunk * kThreads + (w * 32 + __ffs(open) - 1 + cluster * 32) % kThreads;
+          for (int i = 0; i < LOOK * kWarps && s_row < 0; ++i) {
+            const int w = (i + cluster) % (LOOK * kWarps);
+            for (unsigned left = s_open[w]; left && s_row < 0; left &= left - 1) {
+              const int r = chunk * LOOK * kThreads + w * 32 + __ffs(left) - 1;
               if (atomicCAS(a.tokens + r, kUndecided, kClaimed) == kUndecided) s_row = r;
             }
+          }
         }
         __syncthreads();
         row = s_row;
@@ -465,9 +472,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           load(b, v);
           uint64_t sum = 0;
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v[j], e)), scale, table);
+          for (int j = 0; j < kLoads; ++j) sum += K::exact_sum(v[j], K::LOWEST, scale, table);
           sum = warp_sum(sum);
           if (lane == 0) part[b - b0] = sum;
         }
@@ -504,31 +509,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
             const int b = s_batch;
             load(b, v);
             uint64_t from = s_from;
+            uint64_t w[kLoads], upto[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) w[j] = K::exact_sum(v[j], K::LOWEST, scale, table);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) upto[j] = warp_upto(w[j], lane);
             bool found = false;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-              uint64_t sum = 0;
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v[j], e)), scale, table);
-              const uint64_t y = warp_upto(sum, lane) + from;
-              const unsigned over = __ballot_sync(0xffffffffu, y > place);
-              if (!found && over && lane == __ffs(over) - 1) {
-                uint64_t z = y - sum;
-                bool done = false;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                  const float value = K::value(K::bits(v[j], e));
-                  z += weight(value, scale, table);
-                  if (!done && z > place) {
-                    done = true;
-                    a.tokens[row] = b * BATCH + (j * 32 + lane) * VEC + e - skip;
-                    if (a.logprob) a.logprob[row] = set.log_of(value, scale.m, others_of(whole, a.drop));
-                    if (a.kept) a.kept[row] = static_cast<int32_t>(all);
-                  }
+              const unsigned over = __ballot_sync(0xffffffffu, from + upto[j] > place);
+              if (!found && over) {  // (the same for the warp)
+                found = true;
+                const int who = __ffs(over) - 1;
+                uint4 piece;
+                piece.x = __shfl_sync(0xffffffffu, v[j].x, who);
+                piece.y = __shfl_sync(0xffffffffu, v[j].y, who);
+                piece.z = __shfl_sync(0xffffffffu, v[j].z, who);
+                piece.w = __shfl_sync(0xffffffffu, v[j].w, who);
+                const uint64_t start = from + __shfl_sync(0xffffffffu, upto[j] - w[j], who);
+                float value;
+                if (K::exact_find(piece, K::LOWEST, start, place, scale, table, lane, value)) {
+                  a.tokens[row] = b * BATCH + (j * 32 + who) * VEC + lane - skip;
+                  if (a.logprob) a.logprob[row] = set.log_of(value, scale.m, others_of(whole, a.drop));
+                  if (a.kept) a.kept[row] = static_cast<int32_t>(all);
                 }
               }
-              found |= over != 0;
-              from = __shfl_sync(0xffffffffu, y, 31);
+              from += __shfl_sync(0xffffffffu, upto[j], 31);
             }
           }
         }

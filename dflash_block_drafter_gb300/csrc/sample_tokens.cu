@@ -35,7 +35,10 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
-constexpr int kList = 2048;                // tokens that the first CTA sorts
+constexpr int kList = 1024;                // tokens that the first CTA sorts
+constexpr int kOwn = kList / kWarps;       // of a warp
+constexpr int kFew = 128;                  // tokens that it compares each with each
+constexpr int kShort = kList / 2;          // a row that is a list as a whole
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
 // An FP32 sum of weights may be off by, relative to the sum S of the row, in units of 2^-24: a weight's exponent
 // y = (x - m) c 3 |y| (difference, c, product), and the mean of |y| over the weights, their entropy less
@@ -59,10 +62,12 @@ struct Shared {
       uint64_t all_w[kBins];
     } digits;
     struct {
-      uint64_t list[kList];    // (key, id) in order of ids
-      uint64_t sorted[kList];  // (key, place in `list`), largest first
-      uint64_t upto[kList];    // weights before each of them
+      uint64_t own[kWarps][kOwn];  // (key, id) of each warp's tokens, in order of ids
+      uint64_t list[kList];        // the same of the cluster, in its first CTA
+      uint64_t sorted[kList];      // (key, place in `list`), largest first
+      uint64_t upto[kList];        // weights before each of them; of few tokens: of each
       uint32_t hist[kQuickBins];
+      uint32_t many[kMaxSplits * kWarps];  // tokens of each warp of the cluster
     } quick;
   };
   TableEntry table[32];
@@ -251,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint64_t sum = 0;
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint4 v = data[i];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum += weight(K::value(K::bits(v, e)), scale, sh.table);
+      sum += K::exact_sum(v, K::LOWEST, scale, sh.table);
     }
     return cluster_total(sum);
   };
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     float bound = -INFINITY;  // logits from here on
     bool quick = true;
     float sum = 0.f;  // of all weights, by top-p alone
-    if (a.vocab <= kList) {  // the whole row is a list
+    if (a.vocab <= kShort) {  // the whole row is a list
     } else if (by_k) {
       const float low = float_from_order_key(low_key), per = m > low ? (kQuickBins - 1) / (m - low) : 0.f;
       quick = maxima >= static_cast<uint32_t>(k_asked) && per < 1e30f && per > 0.f;
@@ -452,75 +456,106 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
     // (top-p needs the whole of what top-k leaves, and in a short row of all)
-    if (by_min && !(by_p && (by_k || a.vocab <= kList))) bound = fmaxf(bound, K::value_of(least));
+    if (by_min && !(by_p && (by_k || a.vocab <= kShort))) bound = fmaxf(bound, K::value_of(least));
 
     if (quick) {
-      // ---- the tokens from the bound on, in order of their ids, in each CTA
-      uint32_t count = 0;
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const uint4 v = data[i];
-        if (K::top_of(v) < bound) continue;
+      // ---- the tokens from the bound on, in order of their ids: each warp's own
+      uint32_t own = 0;
+      for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
+        const float most_of = K::top_of(v);
+        if (!__any_sync(0xffffffffu, most_of >= bound && most_of > -INFINITY)) continue;
+        uint32_t c = 0;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float x = K::value(K::bits(v, e));
-          count += x >= bound && x > -INFINITY;
+          c += x >= bound && x > -INFINITY;
         }
-      }
-      uint64_t all;
-      uint32_t to;
-      {
-        const uint32_t w = __reduce_add_sync(0xffffffffu, count);
-        __syncthreads();
-        if (lane == 0) sh.warp_n[warp] = w;
-        __syncthreads();
-        to = 0;
-        uint32_t c = 0;
-        for (int i = 0; i < kWarps; ++i) {
-          if (i < warp) to += sh.warp_n[i];
-          c += sh.warp_n[i];
+        uint32_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
         }
-        all = c;
-      }
-      if (all <= kList && sh.warp_n[warp]) {
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-          const int i = i0 + lane;
-          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
-          const bool any = K::top_of(v) >= bound && K::top_of(v) > -INFINITY;
-          if (!__any_sync(0xffffffffu, any)) continue;
-          uint32_t c = 0;
+        uint32_t at = own + upto - c;
+        if (c) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float x = K::value(K::bits(v, e));
-            c += x >= bound && x > -INFINITY;
-          }
-          uint32_t upto = c;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-          }
-          uint32_t at = to + upto - c;
-          if (c) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const uint32_t b = K::bits(v, e);
-              const float x = K::value(b);
-              if (x >= bound && x > -INFINITY)
-                sh.quick.list[at++] = static_cast<uint64_t>(K::of(b)) << 32 | static_cast<uint32_t>((first + i) * VEC + e - skip);
+            const uint32_t b = K::bits(v, e);
+            const float x = K::value(b);
+            if (x >= bound && x > -INFINITY) {
+              if (at < kOwn) sh.quick.own[warp][at] = static_cast<uint64_t>(K::of(b)) << 32 | static_cast<uint32_t>((first + i) * VEC + e - skip);
+              ++at;
             }
           }
-          to += __shfl_sync(0xffffffffu, upto, 31);
         }
+        own += __shfl_sync(0xffffffffu, upto, 31);
       }
-      if (tid == 0) {
-        // (not the array that the numbers of maxima lie in: a CTA may still read them)
-        if (n == 1) sh.cta_w[0] = all;
-        else st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), 0), all);
+      if (lane == 0) {
+        if (n == 1) sh.quick.many[warp] = own;
+        else st_cluster(mapa_shared(smem_u32(&sh.quick.many[rank * kWarps + warp]), 0), own);
       }
       cluster_sync(n);
       uint32_t keep = 0, size = 0;
       uint64_t kept_w = 0;
       uint32_t cut_key = 0;
+      // Few tokens: four threads for each compare it with all others.
+      bool few = false;
+      const uint32_t me = tid >> 2;
+      uint32_t my_key = 0, larger = 0;  // tokens above this one
+      uint64_t my_w = 0, above = 0;     // and their weight
+      auto decide_few = [&](double s_lo, double s_hi) {  // false if S has to be exact
+        const bool real = me < size && (tid & 3) == 0;
+        bool stays = real && my_key >= least, open = false;
+        if (by_k) stays = stays && larger < static_cast<uint32_t>(k_asked);
+        if (by_p) {
+          if (by_k) {
+            uint64_t all;
+            // (what top-k leaves, whatever min-p says of it)
+            scan(real && larger < static_cast<uint32_t>(k_asked) ? my_w : 0, all);
+            s_lo = s_hi = static_cast<double>(all);
+          }
+          const double lo = static_cast<double>(p) * s_lo, hi = static_cast<double>(p) * s_hi, over = static_cast<double>(above);
+          open = stays && larger > 0 && over >= lo && over < hi;
+          stays = stays && (larger == 0 || over < lo);
+        }
+        keep = __syncthreads_count(stays);
+        if (real) sh.quick.upto[me] = stays ? my_w : 0;
+        return !__syncthreads_or(open);
+      };
+      auto draw_few = [&]() {
+        if (warp != 0) return;
+        constexpr int EACH = kFew / 32;
+        uint64_t w[EACH], mine_w = 0;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          w[j] = lane * EACH + j < size ? sh.quick.upto[lane * EACH + j] : 0;
+          mine_w += w[j];
+        }
+        uint64_t upto = mine_w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = shfl_up(upto, o);
+          if (lane >= o) upto += y;
+        }
+        const uint64_t total = __shfl_sync(0xffffffffu, upto, 31);
+        const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
+        uint64_t c = upto - mine_w;
+        if (c <= at && at < upto) {  // (one lane)
+          int j = 0;
+          while (at >= c + w[0]) {
+            c += w[0];
+            ++j;
+#pragma unroll
+            for (int i = 0; i + 1 < EACH; ++i) w[i] = w[i + 1];
+          }
+          const uint64_t entry = sh.quick.list[lane * EACH + j];
+          a.tokens[row] = static_cast<int32_t>(entry);
+          if (a.logprob) a.logprob[row] = set.log_of(K::value_of(static_cast<uint32_t>(entry >> 32)), m, others_of(total, a.drop));
+          if (a.kept) a.kept[row] = static_cast<int32_t>(keep);
+        }
+      };
       // what the first CTA makes of its list, once it is sorted: false if S has to be exact
       auto decide = [&](double s_lo, double s_hi) {
         auto key_at = [&](uint32_t i) { return static_cast<uint32_t>(sh.quick.sorted[i] >> 32); };
@@ -585,25 +620,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
       };
       if (rank == 0) {
-        // the CTAs' lists one behind the other
-        uint64_t upto = 0;
-        for (int r = 0; r < n; ++r) upto += sh.cta_w[r];
+        // the warps' lists one behind the other
+        const uint32_t c = tid < n * kWarps ? sh.quick.many[tid] : 0;
+        const bool wide = __syncthreads_or(c > kOwn);
+        uint64_t all;
+        const uint32_t to = static_cast<uint32_t>(scan(c, all));
         uint32_t verdict = kDigits;
-        if (upto <= kList) {
-          size = static_cast<uint32_t>(upto);
-          for (uint32_t i = tid; i < size; i += kThreads) {
-            uint32_t r = 0, j = i;
-            while (j >= sh.cta_w[r]) j -= static_cast<uint32_t>(sh.cta_w[r++]);
-            uint64_t entry;
-            if (r == 0) {
-              entry = sh.quick.list[i];
-            } else {
-              entry = ld_cluster64(mapa_shared(smem_u32(&sh.quick.list[j]), r));
-              sh.quick.list[i] = entry;
-            }
-            sh.quick.sorted[i] = (entry & 0xffffffff00000000ull) | i;
+        if (!wide && all <= kList) {
+          size = static_cast<uint32_t>(all);
+          few = size <= kFew;
+          for (uint32_t j = 0; j < c; ++j) {
+            const uint64_t* from = &sh.quick.own[tid % kWarps][j];
+            sh.quick.list[to + j] = tid < kWarps ? *from : ld_cluster64(mapa_shared(smem_u32(from), tid / kWarps));
           }
-          uint32_t full = 2;
+          __syncthreads();
+        }
+        double s_lo = 0.0, s_hi = 0.0;
+        if (by_p && !by_k && a.vocab > kShort) {
+          const double whole = static_cast<double>(sum) * static_cast<double>(1ull << (kFixed - a.drop));
+          s_lo = whole - whole * static_cast<double>(kError), s_hi = whole + whole * static_cast<double>(kError);
+        }
+        if (size > 0 && few) {
+          if (tid < size) sh.quick.upto[tid] = weight(K::value_of(static_cast<uint32_t>(sh.quick.list[tid] >> 32)), scale, sh.table);
+          __syncthreads();
+          uint64_t every = 0;
+          if (me < size) my_key = static_cast<uint32_t>(sh.quick.list[me] >> 32), my_w = sh.quick.upto[me];
+          for (uint32_t j = tid & 3; j < size; j += 4) {
+            const uint32_t key = static_cast<uint32_t>(sh.quick.list[j] >> 32);
+            const uint64_t w = sh.quick.upto[j];
+            every += w;
+            if (key > my_key) above += w, ++larger;
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+            every += __shfl_xor_sync(0xffffffffu, every, o);
+            larger += __shfl_xor_sync(0xffffffffu, larger, o);
+          }
+          __syncthreads();  // the weights have been read
+          if (by_p && !by_k && a.vocab <= kShort) s_lo = s_hi = static_cast<double>(every);
+          verdict = decide_few(s_lo, s_hi) ? kDone : kExactSum;
+          if (verdict == kDone) draw_few();
+        } else if (size > 0) {
+          for (uint32_t i = tid; i < size; i += kThreads) sh.quick.sorted[i] = (sh.quick.list[i] & 0xffffffff00000000ull) | i;
+          uint32_t full = kFew;
           while (full < size) full *= 2;
           for (uint32_t i = size + tid; i < full; i += kThreads) sh.quick.sorted[i] = 0;
           __syncthreads();
@@ -632,13 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             c += x;
           }
           __syncthreads();
-          double s_lo = 0.0, s_hi = 0.0;
-          if (by_p && !by_k) {
-            const double s = a.vocab <= kList ? static_cast<double>(kept_w)
-                                              : static_cast<double>(sum) * static_cast<double>(1ull << (kFixed - a.drop));
-            const double off = a.vocab <= kList ? 0.0 : static_cast<double>(kError);
-            s_lo = s - s * off, s_hi = s + s * off;
-          }
+          if (by_p && !by_k && a.vocab <= kShort) s_lo = s_hi = static_cast<double>(kept_w);
           verdict = decide(s_lo, s_hi) ? kDone : kExactSum;
           if (verdict == kDone) draw();
         }
@@ -650,8 +704,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (verdict == kExactSum) {
         const double whole = static_cast<double>(exact_sum());
         if (rank == 0) {
-          decide(whole, whole);
-          draw();
+          if (few) {
+            decide_few(whole, whole);
+            draw_few();
+          } else {
+            decide(whole, whole);
+            draw();
+          }
         }
         return;
       }
@@ -699,9 +758,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       cluster_sync(n);
       // each CTA adds up a share of the bins over all CTAs, for the first one
-      const int share = kBins / n;
-      for (int i = tid; i < share; i += kThreads) {
-        const int bin = rank * share + i;
+      const int share = (kBins + n - 1) / n, last = min((rank + 1) * share, kBins);
+      for (int bin = rank * share + tid; bin < last; bin += kThreads) {
         uint32_t c = 0;
         uint64_t w = 0;
         if (n == 1) {
@@ -785,18 +843,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 
   // ---- the kept weights, and the place that u names
+  const float from_x = K::value_of(least);
   uint64_t sum = 0;
   uint32_t count = 0;
   for (int i = w0 + lane; i < w1; i += 32) {
     const uint4 v = data[i];
+    if (K::top_of(v) < from_x) continue;
+    sum += K::exact_sum(v, least, scale, sh.table);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const uint32_t b = K::bits(v, e);
-      if (K::of(b) >= least) {
-        sum += weight(K::value(b), scale, sh.table);
-        ++count;
-      }
-    }
+    for (int e = 0; e < VEC; ++e) count += K::of(K::bits(v, e)) >= least;
   }
   const uint64_t total = cluster_total(sum);
   const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
@@ -805,44 +860,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (at >= below && at < below + sh.cta_w[rank]) {  // (one CTA)
     for (int i = 0; i < warp; ++i) below += sh.warp_w[i];
     if (at >= below && at < below + sh.warp_w[warp]) {  // (one warp)
-      for (int i0 = w0;; i0 += 32) {
+      for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
         uint64_t part = 0;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const uint32_t b = K::bits(v, e);
-          if (K::of(b) >= least) part += weight(K::value(b), scale, sh.table);
-        }
+        if (__any_sync(0xffffffffu, !(K::top_of(v) < from_x))) part = K::exact_sum(v, least, scale, sh.table);
         uint64_t upto = part;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint64_t y = shfl_up(upto, o);
           if (lane >= o) upto += y;
         }
-        upto += below;
-        const unsigned over = __ballot_sync(0xffffffffu, upto > at);
-        if (over || i0 + 32 >= w1) {
-          if (over && lane == __ffs(over) - 1) {
-            uint64_t c = upto - part;
-            bool done = false;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const uint32_t b = K::bits(v, e);
-              const float x = K::value(b);
-              if (!done && K::of(b) >= least) {
-                c += weight(x, scale, sh.table);
-                if (c > at) {
-                  done = true;
-                  a.tokens[row] = (first + i) * VEC + e - skip;
-                  if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
-                }
-              }
-            }
+        const unsigned over = __ballot_sync(0xffffffffu, below + upto > at);
+        if (over) {
+          const int who = __ffs(over) - 1;
+          uint4 piece;
+          piece.x = __shfl_sync(0xffffffffu, v.x, who);
+          piece.y = __shfl_sync(0xffffffffu, v.y, who);
+          piece.z = __shfl_sync(0xffffffffu, v.z, who);
+          piece.w = __shfl_sync(0xffffffffu, v.w, who);
+          const uint64_t start = below + __shfl_sync(0xffffffffu, upto - part, who);
+          float x;
+          if (K::exact_find(piece, least, start, at, scale, sh.table, lane, x)) {
+            a.tokens[row] = (first + i0 + who) * VEC + lane - skip;
+            if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
           }
           break;
         }
-        below = __shfl_sync(0xffffffffu, upto, 31);
+        below += __shfl_sync(0xffffffffu, upto, 31);
       }
     }
   }
@@ -853,16 +898,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 }
 
-// CTAs per row: as many as its bytes need, more until every SM has one or a CTA has
+// CTAs per row: as many as its bytes need for two CTAs on an SM, more until every SM has one or a CTA has
 // little left.
+constexpr int kSmemOfSm = 228 * 1024;
 cudaError_t splits_of(int n_rows, long long row_pieces, int* splits, int* pieces) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int s = 1;
-  while (s < kMaxSplits && (row_pieces * 16 > 56ll * 1024 * s || (static_cast<long long>(n_rows) * s < sms && row_pieces > 2 * kThreads * s))) s *= 2;
-  *splits = s;
+  constexpr long long fits = (kSmemOfSm / 2 - 1024 - kSharedBytes) / 16;
+  long long s = (row_pieces + fits - 1) / fits;
+  if (s > kMaxSplits) s = kMaxSplits;
+  while (2 * s <= kMaxSplits && n_rows * s < sms && row_pieces > 2 * kThreads * s) s *= 2;
+  *splits = static_cast<int>(s);
   *pieces = static_cast<int>((row_pieces + s - 1) / s);
   return cudaSuccess;
 }

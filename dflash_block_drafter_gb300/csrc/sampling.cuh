@@ -84,44 +84,63 @@ struct Scale {
   int drop;
 };
 
-// e^((x - m) / T) in units of 2^-(kFixed - drop).  (Products and sums are written out: the
-// compiler must not contract them.)
-__device__ __forceinline__ uint64_t weight(float x, const Scale& c, const TableEntry* table) {
-  // x - m = s + e exactly
-  const float b = -c.m;
-  const float s = __fadd_rn(x, b), v = __fsub_rn(s, x);
-  const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(s, v)), __fsub_rn(b, v));
-  // times log2(e) / T: p + q
-  const float whole = __fmul_rn(s, c.hi);
-  // (Below 2^-48 a weight is 0, a masked value's too: without a branch, so that several weights are formed side by side.)
-  const float p = fmaxf(whole, -56.f);
-  const float q = __fmaf_rn(e, c.hi, __fmaf_rn(s, c.lo, __fmaf_rn(s, c.hi, -whole)));
-  // = n + j / 32 + r, |r| <= 1/64
+// e^((x - m) / T) in units of 2^-(kFixed - drop), N of them side by side: one is a chain of 40 instructions, and the compiler
+// does not mix the chains of several by itself (a batch of 32 in a lane: 4.2 us one by one).  Products and sums are written
+// out: the compiler must not contract them.
+template <int N>
+__device__ __forceinline__ void weights(const float (&x)[N], const Scale& c, const TableEntry* table, uint64_t (&w)[N]) {
   constexpr float ROUND = 393216.f;  // 1.5 2^18: adding it leaves multiples of 1/32
-  const float t = __fadd_rn(p, ROUND);
-  const int k = __float_as_int(t) - __float_as_int(ROUND);
-  const float r = __fsub_rn(p, __fsub_rn(t, ROUND));
-  const float rh = __fadd_rn(r, q), rl = __fsub_rn(q, __fsub_rn(rh, r));
-  // a = r ln 2, u = e^a - 1
   constexpr float LN2 = 0x1.62e430p-1f, LN2_LO = -0x1.05c610p-29f;
-  const float ah = __fmul_rn(rh, LN2);
-  const float al = __fadd_rn(__fmaf_rn(rh, LN2, -ah), __fmaf_rn(rh, LN2_LO, __fmul_rn(rl, LN2)));
-  const float h = __fmul_rn(0.5f, ah), s2 = __fmul_rn(h, ah);
-  const float s2l = __fmaf_rn(ah, al, __fmaf_rn(h, ah, -s2));
-  const float cubic = __fmul_rn(__fmul_rn(s2, ah), __fmaf_rn(ah, __fmaf_rn(ah, 1.f / 60, 1.f / 12), 1.f / 3));  // a^3/6 + a^4/24 + a^5/120
-  const float uh = __fadd_rn(ah, s2);
-  const float ul = __fadd_rn(__fsub_rn(s2, __fsub_rn(uh, ah)), __fadd_rn(al, __fadd_rn(s2l, cubic)));
-  // times 2^(j / 32): its own whole number, and the rest in two steps of 2^-23 and 2^-45
-  const TableEntry f = table[k & 31];
-  const float vh = __fmul_rn(f.hi, uh);
-  const float vl = __fadd_rn(__fmaf_rn(f.hi, uh, -vh), __fmaf_rn(f.hi, ul, __fmul_rn(f.lo, uh)));
   constexpr float STEP1 = 1.5f, STEP2 = 1.5f * 0x1p-22f;
-  const float t1 = __fadd_rn(__fadd_rn(vh, vl), STEP1);
-  const float rest = __fadd_rn(__fsub_rn(vh, __fsub_rn(t1, STEP1)), vl);
-  const float t2 = __fadd_rn(rest, STEP2);
-  const long long add = (static_cast<long long>(__float_as_int(t1) - __float_as_int(STEP1)) << 22) +
-                        (__float_as_int(t2) - __float_as_int(STEP2));
-  return whole > -48.f ? (f.fixed + add) >> (c.drop - (k >> 5)) : 0;
+  const float b = -c.m;
+  float s[N], e[N], whole[N], p[N], q[N], t[N], rh[N], rl[N], ah[N], al[N], s2[N], s2l[N], cubic[N], uh[N], ul[N], vh[N], vl[N], t1[N], t2[N];
+  int k[N];
+  TableEntry f[N];
+#define DFLASH_EACH _Pragma("unroll") for (int i = 0; i < N; ++i)
+  DFLASH_EACH s[i] = __fadd_rn(x[i], b);  // x - m = s + e exactly
+  DFLASH_EACH whole[i] = __fmul_rn(s[i], c.hi);
+  // (Below 2^-48 a weight is 0, a masked value's too: without a branch.)
+  DFLASH_EACH p[i] = fmaxf(whole[i], -56.f);
+  DFLASH_EACH t[i] = __fadd_rn(p[i], ROUND);
+  DFLASH_EACH k[i] = __float_as_int(t[i]) - __float_as_int(ROUND);
+  DFLASH_EACH f[i] = table[k[i] & 31];
+  DFLASH_EACH {
+    const float v = __fsub_rn(s[i], x[i]);
+    e[i] = __fadd_rn(__fsub_rn(x[i], __fsub_rn(s[i], v)), __fsub_rn(b, v));
+  }
+  // times log2(e) / T: p + q = n + j / 32 + r, |r| <= 1/64
+  DFLASH_EACH q[i] = __fmaf_rn(e[i], c.hi, __fmaf_rn(s[i], c.lo, __fmaf_rn(s[i], c.hi, -whole[i])));
+  DFLASH_EACH {
+    const float r = __fsub_rn(p[i], __fsub_rn(t[i], ROUND));
+    rh[i] = __fadd_rn(r, q[i]);
+    rl[i] = __fsub_rn(q[i], __fsub_rn(rh[i], r));
+  }
+  // a = r ln 2, u = e^a - 1
+  DFLASH_EACH ah[i] = __fmul_rn(rh[i], LN2);
+  DFLASH_EACH al[i] = __fadd_rn(__fmaf_rn(rh[i], LN2, -ah[i]), __fmaf_rn(rh[i], LN2_LO, __fmul_rn(rl[i], LN2)));
+  DFLASH_EACH s2[i] = __fmul_rn(__fmul_rn(0.5f, ah[i]), ah[i]);
+  DFLASH_EACH s2l[i] = __fmaf_rn(ah[i], al[i], __fmaf_rn(__fmul_rn(0.5f, ah[i]), ah[i], -s2[i]));
+  // a^3/6 + a^4/24 + a^5/120
+  DFLASH_EACH cubic[i] = __fmul_rn(__fmul_rn(s2[i], ah[i]), __fmaf_rn(ah[i], __fmaf_rn(ah[i], 1.f / 60, 1.f / 12), 1.f / 3));
+  DFLASH_EACH uh[i] = __fadd_rn(ah[i], s2[i]);
+  DFLASH_EACH ul[i] = __fadd_rn(__fsub_rn(s2[i], __fsub_rn(uh[i], ah[i])), __fadd_rn(al[i], __fadd_rn(s2l[i], cubic[i])));
+  // times 2^(j / 32): its own whole number, and the rest in two steps of 2^-23 and 2^-45
+  DFLASH_EACH vh[i] = __fmul_rn(f[i].hi, uh[i]);
+  DFLASH_EACH vl[i] = __fadd_rn(__fmaf_rn(f[i].hi, uh[i], -vh[i]), __fmaf_rn(f[i].hi, ul[i], __fmul_rn(f[i].lo, uh[i])));
+  DFLASH_EACH t1[i] = __fadd_rn(__fadd_rn(vh[i], vl[i]), STEP1);
+  DFLASH_EACH t2[i] = __fadd_rn(__fadd_rn(__fsub_rn(vh[i], __fsub_rn(t1[i], STEP1)), vl[i]), STEP2);
+  DFLASH_EACH {
+    const long long add = (static_cast<long long>(__float_as_int(t1[i]) - __float_as_int(STEP1)) << 22) +
+                          (__float_as_int(t2[i]) - __float_as_int(STEP2));
+    w[i] = whole[i] > -48.f ? (f[i].fixed + add) >> (c.drop - (k[i] >> 5)) : 0;
+  }
+#undef DFLASH_EACH
+}
+__device__ __forceinline__ uint64_t weight(float x, const Scale& c, const TableEntry* table) {
+  const float in[1] = {x};
+  uint64_t out[1];
+  weights(in, c, table, out);
+  return out[0];
 }
 
 // ------------------------------------------------------------------ keys
@@ -225,6 +244,42 @@ struct Keys {
 #pragma unroll
       for (int e = 0; e < o; ++e) x[e] += x[e + o];
     return x[0];
+  }
+  // exact weight of a piece's values whose key is `least` or more
+  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, uint32_t least, const Scale& c, const TableEntry* table) {
+    constexpr int VEC = Elem<TYPE>::VEC;
+    uint64_t sum = 0;
+#pragma unroll
+    for (int e0 = 0; e0 < VEC; e0 += 4) {
+      float x[4];
+      uint64_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = value(bits(v, e0 + e));
+      weights(x, c, table, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += of(bits(v, e0 + e)) >= least ? w[e] : 0;
+    }
+    return sum;
+  }
+  // The first value of a piece (the same in all lanes) with which the exact weights from `from` on exceed `place`: the lane
+  // that has it.  Each lane has one value.
+  static __device__ __forceinline__ bool exact_find(const uint4& v, uint32_t least, uint64_t from, uint64_t place, const Scale& c,
+                                                    const TableEntry* table, int lane, float& x) {
+    constexpr int VEC = Elem<TYPE>::VEC;
+    uint32_t b = SIGN | INF;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) b = lane == e ? bits(v, e) : b;
+    x = value(b);
+    uint64_t w = weight(x, c, table);
+    if (lane >= VEC || of(b) < least) w = 0;
+    uint64_t upto = w;
+#pragma unroll
+    for (int o = 1; o < VEC; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, from + upto > place);
+    return lane == __ffs(over) - 1;
   }
   // values of a piece above -infinity
   static __device__ __forceinline__ int unmasked(const uint4& v) {
