@@ -471,8 +471,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           uint4 v[kLoads];
           load(b, v);
           uint64_t sum = 0;
-#pragma unroll
-          for (int j = 0; j < kLoads; ++j) sum += K::exact_sum(v[j], K::LOWEST, scale, table);
+          // (not unrolled, here and below: 32 weights in line are 30 KB of instructions that are fetched for each batch)
+#pragma unroll 1
+          for (int j = 0; j < kLoads; ++j) {
+            sum += K::exact_sum(v[0], K::LOWEST, scale, table);
+            v[0] = v[1], v[1] = v[2], v[2] = v[3];
+          }
+          static_assert(kLoads == 4, "pieces");
           sum = warp_sum(sum);
           if (lane == 0) part[b - b0] = sum;
         }
@@ -509,32 +514,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
             const int b = s_batch;
             load(b, v);
             uint64_t from = s_from;
-            uint64_t w[kLoads], upto[kLoads];
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) w[j] = K::exact_sum(v[j], K::LOWEST, scale, table);
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) upto[j] = warp_upto(w[j], lane);
-            bool found = false;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < kLoads; ++j) {
-              const unsigned over = __ballot_sync(0xffffffffu, from + upto[j] > place);
-              if (!found && over) {  // (the same for the warp)
-                found = true;
+              const uint64_t w = K::exact_sum(v[0], K::LOWEST, scale, table), upto = warp_upto(w, lane);
+              const unsigned over = __ballot_sync(0xffffffffu, from + upto > place);
+              if (over) {  // (the same for the warp)
                 const int who = __ffs(over) - 1;
                 uint4 piece;
-                piece.x = __shfl_sync(0xffffffffu, v[j].x, who);
-                piece.y = __shfl_sync(0xffffffffu, v[j].y, who);
-                piece.z = __shfl_sync(0xffffffffu, v[j].z, who);
-                piece.w = __shfl_sync(0xffffffffu, v[j].w, who);
-                const uint64_t start = from + __shfl_sync(0xffffffffu, upto[j] - w[j], who);
+                piece.x = __shfl_sync(0xffffffffu, v[0].x, who);
+                piece.y = __shfl_sync(0xffffffffu, v[0].y, who);
+                piece.z = __shfl_sync(0xffffffffu, v[0].z, who);
+                piece.w = __shfl_sync(0xffffffffu, v[0].w, who);
+                const uint64_t start = from + __shfl_sync(0xffffffffu, upto - w, who);
                 float value;
                 if (K::exact_find(piece, K::LOWEST, start, place, scale, table, lane, value)) {
                   a.tokens[row] = b * BATCH + (j * 32 + who) * VEC + lane - skip;
                   if (a.logprob) a.logprob[row] = set.log_of(value, scale.m, others_of(whole, a.drop));
                   if (a.kept) a.kept[row] = static_cast<int32_t>(all);
                 }
+                break;
               }
-              from += __shfl_sync(0xffffffffu, upto[j], 31);
+              from += __shfl_sync(0xffffffffu, upto, 31);
+              v[0] = v[1], v[1] = v[2], v[2] = v[3];
             }
           }
         }
