@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   __syncthreads();  // (c)
   const float c = s_scale.hi;
   // what a reference adds to an exponent; one so low (masked values) that nothing has weight beside any other: 0
-  auto none = [&](float r) { return !(r * c > -0x1p100f); };
+  auto none = [&](float r) { return !(r * c > -0x1p21f); };
   auto start = [&](float r) { return none(r) ? 0.f : -(r * c); };
 
   // ---- the pass
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   const float k = start(m);
   const float whole = static_cast<float>(total) * 0x1p-40f;
   const uint64_t off = units(whole * 0x1p-24f * (32.f + 1.1f * log2f(static_cast<float>(a.vocab) / whole)));
-  // (exponents beyond FP32's range: no border is far enough)
-  const bool close = !(fabsf(m) * c < 0x1p100f);
+  // (k is off by 2^-4 at most, and what `none` leaves out is far below the largest value; else no border is far enough)
+  const bool close = !(fabsf(m) * c < 0x1p20f);
   before += below;
   if (!close && before <= at && at < before + own) {  // (one thread, or none where the CTAs' sums differ: then the exact ones decide)
     uint64_t x = before;
@@ -434,7 +434,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         uint32_t all;
         if (a.logprob && a.kept) {  // left there by the first kernel
           m = __ldcg(a.logprob + row), all = static_cast<uint32_t>(__ldcg(a.kept + row));
-          __syncthreads();  // (s_scale)
         } else {
           uint32_t tops = E::NOTHING, count = 0;
           for (int b = b0 + warp; b < b1; b += kWarps) {
@@ -465,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           for (int r = 0; r < kRestCtas; ++r) top = max(top, cta_key[r]), all += cta_count[r];
           m = float_from_order_key(top);
         }
-        Scale scale = s_scale;
-        scale.m = m;
+        if (tid == 0) s_scale.m = m;
+        __syncthreads();
+        const Scale* scale = &s_scale;
         for (int b = b0 + warp; b < b1; b += kWarps) {
           uint4 v[kLoads];
           load(b, v);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           // (not unrolled, here and below: 32 weights in line are 30 KB of instructions that are fetched for each batch)
 #pragma unroll 1
           for (int j = 0; j < kLoads; ++j) {
-            sum += K::exact_sum(v[0], K::LOWEST, scale, table);
+            sum += K::template exact_sum<false>(v[0], K::LOWEST, scale, table);
             v[0] = v[1], v[1] = v[2], v[2] = v[3];
           }
           static_assert(kLoads == 4, "pieces");
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
             uint64_t from = s_from;
 #pragma unroll 1
             for (int j = 0; j < kLoads; ++j) {
-              const uint64_t w = K::exact_sum(v[0], K::LOWEST, scale, table), upto = warp_upto(w, lane);
+              const uint64_t w = K::template exact_sum<false>(v[0], K::LOWEST, scale, table), upto = warp_upto(w, lane);
               const unsigned over = __ballot_sync(0xffffffffu, from + upto > place);
               if (over) {  // (the same for the warp)
                 const int who = __ffs(over) - 1;
@@ -527,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
                 piece.w = __shfl_sync(0xffffffffu, v[0].w, who);
                 const uint64_t start = from + __shfl_sync(0xffffffffu, upto - w, who);
                 float value;
-                if (K::exact_find(piece, K::LOWEST, start, place, scale, table, lane, value)) {
+                if (K::template exact_find<false>(piece, K::LOWEST, start, place, scale, table, lane, value)) {
                   a.tokens[row] = b * BATCH + (j * 32 + who) * VEC + lane - skip;
-                  if (a.logprob) a.logprob[row] = set.log_of(value, scale.m, others_of(whole, a.drop));
+                  if (a.logprob) a.logprob[row] = set.log_of(value, m, others_of(whole, a.drop));
                   if (a.kept) a.kept[row] = static_cast<int32_t>(all);
                 }
                 break;

@@ -14,13 +14,17 @@
 //    histogram of them.  Of top-p: the first of 512 ranges of logits below which less than
 //    (1 - p) S can lie, counted with each range's largest weight.  Of min-p: itself.  The
 //    tokens above the bound, if they are at most kList, go to the first CTA, which
-//    sorts them and decides everything with exact weights.  S itself, which a top-p without top-k compares with, comes
-//    from FP32 sums with a bound on their error; where that leaves it open which token is
-//    the last, S is added up exactly.
-//  - A row of such a call whose filters are off: FP32 sums by CTA, warp and lane lead to the token; the exact ones
-//    are formed if a border of it lies within the error's bound.
-// Else (long lists) a threshold is found digit by digit: counts (and exact weights) of up to
-// 1024 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key.
+//    compares them (or sorts them) and decides everything with exact weights.  S itself, which a top-p without top-k
+//    compares with, comes from FP32 sums; where their error leaves it open which token is the last, S is added up exactly.
+// Else (long lists) a threshold is found digit by digit: counts (and weights) of up to
+// 1024 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key; and the token by
+// the sums of the CTAs, warps and lanes.  FP32 weights do first, in whole numbers, whose sums are exact, and exact ones if those leave a
+// decision open: whether a border of the token, or of the last key, lies within their error of what it is compared with.
+//
+// That error: a weight is 2^(x c + k), k = -m c as FP32 has it (what it is off by is the same for all weights).
+// The exponent y is off by 1.5 |y| 2^-24 (one rounding, and c's); the mean of |y| over the weights is their entropy less log2
+// S, log2(vocab / S) at most: with ln 2, 1.1 log2(vocab / S) units of 2^-24.  2^y 4, its unit 1; a piece's sum 3, where there is one.  A border
+// and u S (or p S) err apart by the errors of the weights on either side, u or 1 - u of each: not more than one sum's.
 #include <cstddef>
 
 #include "common.cuh"
@@ -37,14 +41,9 @@ constexpr int kBins = 1024;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kList = 1024;                // tokens that the first CTA sorts
 constexpr int kOwn = kList / kWarps;       // of a warp
-constexpr int kFew = 128;                  // tokens that it compares each with each
+constexpr int kFew = 256;                  // tokens that it compares each with each
 constexpr int kShort = kList / 2;          // a row that is a list as a whole
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
-// An FP32 sum of weights may be off by, relative to the sum S of the row, in units of 2^-24: a weight's exponent
-// y = (x - m) c 3 |y| (difference, c, product), and the mean of |y| over the weights, their entropy less
-// log2 S, is 19 at most for 2^19 tokens: 40 with ln 2; 2^y 4; additions, of 16 pieces in a thread, in a
-// piece, over lanes, warps and CTAs: 16 + 3 + 5 + 16 + 16.  In all under 128.
-constexpr float kError = 0x1p-17f;
 
 struct Found {
   uint32_t lo, hi;      // keys of the range
@@ -74,7 +73,7 @@ struct Shared {
   Found found;
   uint64_t cta_w[kMaxSplits], warp_w[kWarps];
   uint32_t cta_top[kMaxSplits], cta_low[kMaxSplits], cta_n[kMaxSplits], warp_u[kWarps], warp_low[kWarps], warp_n[kWarps];
-  float cta_f[kMaxSplits], warp_f[kWarps];
+  float warp_f[kWarps];
   double log_min_p;
   Scale scale;
   float bound;
@@ -173,12 +172,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   cluster_sync(n);
-  uint32_t top_key = 0, low_key = 0xffffffffu, maxima = 0;
-  for (int i = 0; i < n; ++i) {
-    top_key = max(top_key, sh.cta_top[i]);
-    low_key = min(low_key, sh.cta_low[i]);
-    maxima += sh.cta_n[i];
-  }
+  const bool of_cta = lane < n;
+  const uint32_t top_key = __reduce_max_sync(0xffffffffu, of_cta ? sh.cta_top[lane] : 0u);
+  const uint32_t low_key = __reduce_min_sync(0xffffffffu, of_cta ? sh.cta_low[lane] : 0xffffffffu);
+  const uint32_t maxima = __reduce_add_sync(0xffffffffu, of_cta ? sh.cta_n[lane] : 0u);
   const float m = float_from_order_key(top_key);
   if (top_key == 0xffffffffu || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from
     if (rank == 0 && tid == 0) {
@@ -227,38 +224,53 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   if (tid == 0) sh.scale.m = m;
   __syncthreads();
-  const Scale scale = sh.scale;
+  const Scale* const scale = &sh.scale;
+  const float c_hi = sh.scale.hi;
   const uint32_t most = K::of_value(m);
   uint32_t least = K::LOWEST;
   if (by_min) least = max(least, min(most, K::at_least(static_cast<double>(m) + sh.log_min_p)));
 
-  // The sum over the cluster of a value per thread, and the CTAs' sums in sh.cta_w.
-  auto cluster_total = [&](uint64_t v) {
+  // The sum over the cluster of a value per thread, and the CTAs' sums in sh.cta_w; of a count too.
+  auto cluster_total = [&](uint64_t v, uint32_t& count) {
     v = warp_sum(v);
+    count = __reduce_add_sync(0xffffffffu, count);
     cluster_sync(n);  // the last values in these arrays have been read
-    if (lane == 0) sh.warp_w[warp] = v;
+    if (lane == 0) sh.warp_w[warp] = v, sh.warp_n[warp] = count;
     __syncthreads();
     if (tid < 32) {
       v = warp_sum(lane < kWarps ? sh.warp_w[lane] : uint64_t(0));
+      count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
       if (n == 1) {
-        if (lane == 0) sh.cta_w[0] = v;
+        if (lane == 0) sh.cta_w[0] = v, sh.cta_n[0] = count;
       } else if (lane < n) {
         st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), lane), v);
+        st_cluster(mapa_shared(smem_u32(&sh.cta_n[rank]), lane), count);
       }
     }
     cluster_sync(n);
-    uint64_t sum = 0;
-    for (int i = 0; i < n; ++i) sum += sh.cta_w[i];
-    return sum;
+    count = __reduce_add_sync(0xffffffffu, lane < n ? sh.cta_n[lane] : 0u);
+    return warp_sum(lane < n ? sh.cta_w[lane] : uint64_t(0));
   };
+  // FP32 weights, 2^(x c + k), in the units of the exact ones: sums are whole numbers too.
+  const float k_hi = -(m * c_hi);
+  const bool in_range = fabsf(m) * c_hi < 0x1p20f;  // (k is off by 2^-4 at most)
+  const float unit = __int_as_float((127 + kFixed - a.drop) << 23);
+  auto fixed = [&](float w) { return static_cast<uint64_t>(__float2ull_rn(w * unit)); };
+  auto quick_weight = [&](float x) { return fixed(ex2_approx(fmaf(x, c_hi, k_hi))); };
+  // What such sums may be off by together, relative: `more` units of 2^-24 and those of the exponents
+  auto error_of = [&](uint64_t sum, float more) {
+    return 0x1p-24f * (more + 1.1f * log2f(static_cast<float>(a.vocab) * unit / static_cast<float>(sum)));
+  };
+  auto one_weight = [&](float x) { return weight_by_call(x, scale, sh.table); };
   // The exact weight of all tokens.
   auto exact_sum = [&]() {
     uint64_t sum = 0;
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint4 v = data[i];
-      sum += K::exact_sum(v, K::LOWEST, scale, sh.table);
+      sum += K::template exact_sum<true>(v, K::LOWEST, scale, sh.table);
     }
-    return cluster_total(sum);
+    uint32_t none = 0;
+    return cluster_total(sum, none);
   };
   // The sum of a value per thread over this CTA's threads before it, and over all of them.
   auto scan = [&](uint64_t v, uint64_t& all) {
@@ -289,93 +301,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   };
 
   const bool filter = by_k || by_p || by_min;
-  if (!filter) {
-    // ---- FP32 sums of the weights lead to the token
-    float sum = 0.f;
-    uint32_t count = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint4 v = data[i];
-      sum += K::quick_sum(v, m, scale.hi);
-      count += K::unmasked(v);
-    }
-    float ws = sum;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-    count = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0) sh.warp_f[warp] = ws, sh.warp_n[warp] = count;
-    __syncthreads();
-    if (tid < 32) {
-      float cs = 0.f;
-      for (int i = 0; i < kWarps; ++i) cs += sh.warp_f[i];
-      const uint32_t c = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
-      if (n == 1) {
-        if (lane == 0) sh.cta_f[0] = cs, sh.cta_w[0] = c;
-      } else if (lane < n) {
-        st_cluster(mapa_shared(smem_u32(&sh.cta_f[rank]), lane), __float_as_uint(cs));
-        st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), lane), static_cast<uint64_t>(c));
-      }
-    }
-    cluster_sync(n);
-    float total = 0.f, below = 0.f, own = 0.f;
-    for (int i = 0; i < n; ++i) {
-      if (i == rank) below = total, own = sh.cta_f[i];
-      total += sh.cta_f[i];
-    }
-    const float at = u * total, off = 2.f * kError * total;  // (two such sums are compared)
-    if (at >= below && (at < below + own || rank == n - 1)) {  // (one CTA, by these sums)
-      float from = below;
-      int w = 0;
-      for (; w < kWarps - 1 && !(at < from + sh.warp_f[w]); ++w) from += sh.warp_f[w];
-      if (warp == w) {
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-          const int i = i0 + lane;
-          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
-          const float part = K::quick_sum(v, m, scale.hi);
-          float upto = part;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-          }
-          upto += from;
-          const unsigned over = __ballot_sync(0xffffffffu, upto > at);
-          if (over) {
-            if (lane == __ffs(over) - 1) {
-              float c = upto - part;
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                const float x = K::value(K::bits(v, e)), before = c;
-                c += ex2_approx((x - m) * scale.hi);
-                // the first past u, further from both of its borders than the sums may be off
-                if (before <= at && c > at) {
-                  if (before + off <= at && c - off > at) {
-                    a.tokens[row] = (first + i) * VEC + e - skip;
-                    if (a.logprob) a.logprob[row] = set.log_of(x, m, total - 1.f);
-                    if (a.kept) {
-                      uint64_t all = 0;
-                      for (int r = 0; r < n; ++r) all += sh.cta_w[r];
-                      a.kept[row] = static_cast<int32_t>(all);
-                    }
-                    tell_verdict(kDone);
-                  }
-                  break;
-                }
-              }
-            }
-            break;
-          }
-          from = __shfl_sync(0xffffffffu, upto, 31);
-        }
-      }
-    }
-    __syncwarp();
-    cluster_sync(n);
-    if (sh.verdict == kDone) return;
-  } else {
+  uint32_t from_key = K::LOWEST;  // no threshold of top-k and top-p lies below
+  uint64_t quick_total = 0;       // FP32 weights of all tokens, by top-p alone
+  if (filter) {
     // ---- a bound below the thresholds
     float bound = -INFINITY;  // logits from here on
     bool quick = true;
-    float sum = 0.f;  // of all weights, by top-p alone
     if (a.vocab <= kShort) {  // the whole row is a list
     } else if (by_k) {
       const float low = float_from_order_key(low_key), per = m > low ? (kQuickBins - 1) / (m - low) : 0.f;
@@ -383,10 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (quick) {
         if (top > -INFINITY) atomicAdd(&sh.quick.hist[min(static_cast<int>((m - top) * per), kQuickBins - 1)], 1u);
         cluster_sync(n);
-        uint32_t c = 0;
-        if (n == 1) c = sh.quick.hist[tid];
-        else
-          for (int r = 0; r < n; ++r) c += ld_cluster(mapa_shared(smem_u32(&sh.quick.hist[tid]), r));
+        const uint32_t c = n == 1 ? sh.quick.hist[tid] : static_cast<uint32_t>(cluster_sum(&sh.quick.hist[tid], n));
         uint64_t all;
         const uint64_t before = scan(c, all);
         // (the values of range b lie above m - (b + 1) / per, to FP32)
@@ -398,41 +326,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       // tokens whose exponent is beyond `cut` weigh (1 - p) / 4 together at most
       const float rest = 1.f - fmaxf(p, 0.f), cut = log2f(static_cast<float>(a.vocab) * 4.f / rest);
       const float per = kQuickBins / cut;
-      quick = cut < 40.f;
+      quick = cut < 40.f && in_range;
       if (quick) {
         for (int i = w0 + lane; i < w1; i += 32) {
           const uint4 v = data[i];
-          sum += K::quick_sum(v, m, scale.hi);
-          if ((m - K::top_of(v)) * scale.hi < cut) {
+          quick_total += fixed(K::quick_sum_from(v, c_hi, k_hi));
+          if ((m - K::top_of(v)) * c_hi < cut) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-              const float z = (m - K::value(K::bits(v, e))) * scale.hi;
+              const float z = (m - K::value(K::bits(v, e))) * c_hi;
               if (z < cut) atomicAdd(&sh.quick.hist[min(static_cast<int>(z * per), kQuickBins - 1)], 1u);
             }
           }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) sh.warp_f[warp] = sum;
+        quick_total = warp_sum(quick_total);
+        if (lane == 0) sh.warp_w[warp] = quick_total;
         __syncthreads();
         if (tid < 32) {
-          float cs = 0.f;
-          for (int i = 0; i < kWarps; ++i) cs += sh.warp_f[i];
+          const uint64_t v = warp_sum(lane < kWarps ? sh.warp_w[lane] : uint64_t(0));
           if (n == 1) {
-            if (lane == 0) sh.cta_f[0] = cs;
+            if (lane == 0) sh.cta_w[0] = v;
           } else if (lane < n) {
-            st_cluster(mapa_shared(smem_u32(&sh.cta_f[rank]), lane), __float_as_uint(cs));
+            st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), lane), v);
           }
         }
         cluster_sync(n);
-        sum = 0.f;
-        for (int i = 0; i < n; ++i) sum += sh.cta_f[i];
+        quick_total = warp_sum(lane < n ? sh.cta_w[lane] : uint64_t(0));
         // what the ranges from the last one up to this thread's weigh at most
         const int bin = kQuickBins - 1 - tid;
-        uint32_t c = 0;
-        if (n == 1) c = sh.quick.hist[bin];
-        else
-          for (int r = 0; r < n; ++r) c += ld_cluster(mapa_shared(smem_u32(&sh.quick.hist[bin]), r));
+        const uint32_t c = n == 1 ? sh.quick.hist[bin] : static_cast<uint32_t>(cluster_sum(&sh.quick.hist[bin], n));
         const float w = static_cast<float>(c) * ex2_approx(-static_cast<float>(bin) / per);
         float x = w;
 #pragma unroll
@@ -447,14 +369,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         x += rest * 0.25f;
         for (int i = 0; i < warp; ++i) x += sh.warp_f[i];
         // (2^-10: more than the sums and ranges are off)
-        const float most_left = rest * sum * (1.f - 0x1p-10f);
+        const float most_left = rest * (static_cast<float>(quick_total) / unit) * (1.f - 0x1p-10f);
         // the first range that has to be kept: with it more than may be left out would be
-        if (x > most_left && x - w <= most_left) sh.bound = m - (bin + 1) / per / scale.hi * (1.f + 0x1p-20f);
+        if (x > most_left && x - w <= most_left) sh.bound = m - (bin + 1) / per / c_hi * (1.f + 0x1p-20f);
         __syncthreads();
         bound = sh.bound;
-        quick = bound > -INFINITY;
+        if (bound > -INFINITY) from_key = max(from_key, min(most, K::at_least(bound)));
+        // (too long a list is not made; min-p may shorten it)
+        const uint32_t listed = __reduce_add_sync(0xffffffffu, (m - bound) * c_hi * per > bin ? c : 0u);
+        if (lane == 0) sh.warp_n[warp] = listed;
+        __syncthreads();
+        uint32_t all = 0;
+        for (int i = 0; i < kWarps; ++i) all += sh.warp_n[i];
+        quick = bound > -INFINITY && (by_min || all <= kList);
       }
     }
+    if (by_k && bound > -INFINITY) from_key = max(from_key, min(most, K::at_least(bound)));
     // (top-p needs the whole of what top-k leaves, and in a short row of all)
     if (by_min && !(by_p && (by_k || a.vocab <= kShort))) bound = fmaxf(bound, K::value_of(least));
 
@@ -500,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       uint32_t keep = 0, size = 0;
       uint64_t kept_w = 0;
       uint32_t cut_key = 0;
-      // Few tokens: four threads for each compare it with all others.
+      // Few tokens: four or two threads for each compare it with all others.
       bool few = false;
-      const uint32_t me = tid >> 2;
+      uint32_t each = 4, me = 0;
       uint32_t my_key = 0, larger = 0;  // tokens above this one
       uint64_t my_w = 0, above = 0;     // and their weight
       auto decide_few = [&](double s_lo, double s_hi) {  // false if S has to be exact
-        const bool real = me < size && (tid & 3) == 0;
+        const bool real = me < size && tid % each == 0;
         bool stays = real && my_key >= least, open = false;
         if (by_k) stays = stays && larger < static_cast<uint32_t>(k_asked);
         if (by_p) {
@@ -544,12 +474,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         uint64_t c = upto - mine_w;
         if (c <= at && at < upto) {  // (one lane)
           int j = 0;
-          while (at >= c + w[0]) {
-            c += w[0];
-            ++j;
 #pragma unroll
-            for (int i = 0; i + 1 < EACH; ++i) w[i] = w[i + 1];
-          }
+          for (int i = 0; i + 1 < EACH; ++i)
+            if (at >= c + w[i] && j == i) c += w[i], ++j;
           const uint64_t entry = sh.quick.list[lane * EACH + j];
           a.tokens[row] = static_cast<int32_t>(entry);
           if (a.logprob) a.logprob[row] = set.log_of(K::value_of(static_cast<uint32_t>(entry >> 32)), m, others_of(total, a.drop));
@@ -600,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         uint64_t w = 0, all_w;
         for (uint32_t j = j0; j < j1; ++j) {
           const uint32_t key = static_cast<uint32_t>(sh.quick.list[j] >> 32);
-          if (key >= cut_key) w += weight(K::value_of(key), scale, sh.table);
+          if (key >= cut_key) w += one_weight(K::value_of(key));
         }
         uint64_t c = scan(w, all_w);
         if (c <= at && at < c + w) {  // (one thread)
@@ -609,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             const uint32_t key = static_cast<uint32_t>(entry >> 32);
             if (key < cut_key) continue;
             const float x = K::value_of(key);
-            c += weight(x, scale, sh.table);
+            c += one_weight(x);
             if (c > at) {
               a.tokens[row] = static_cast<int32_t>(entry);
               if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
@@ -637,22 +564,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         double s_lo = 0.0, s_hi = 0.0;
         if (by_p && !by_k && a.vocab > kShort) {
-          const double whole = static_cast<double>(sum) * static_cast<double>(1ull << (kFixed - a.drop));
-          s_lo = whole - whole * static_cast<double>(kError), s_hi = whole + whole * static_cast<double>(kError);
+          // (the FP32 weights are relative to 2^(m c + k))
+          const double whole = static_cast<double>(quick_total) / static_cast<double>(ex2_approx(fmaf(m, c_hi, k_hi)));
+          const double off = whole * static_cast<double>(error_of(quick_total, 16.f));
+          s_lo = whole - off, s_hi = whole + off;
         }
         if (size > 0 && few) {
-          if (tid < size) sh.quick.upto[tid] = weight(K::value_of(static_cast<uint32_t>(sh.quick.list[tid] >> 32)), scale, sh.table);
+          if (tid < size) sh.quick.upto[tid] = weight(K::value_of(static_cast<uint32_t>(sh.quick.list[tid] >> 32)), *scale, sh.table);
           __syncthreads();
           uint64_t every = 0;
+          if (size > kThreads / 4) each = 2;
+          me = tid / each;
           if (me < size) my_key = static_cast<uint32_t>(sh.quick.list[me] >> 32), my_w = sh.quick.upto[me];
-          for (uint32_t j = tid & 3; j < size; j += 4) {
+          for (uint32_t j = tid % each; j < size; j += each) {
             const uint32_t key = static_cast<uint32_t>(sh.quick.list[j] >> 32);
             const uint64_t w = sh.quick.upto[j];
             every += w;
             if (key > my_key) above += w, ++larger;
           }
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
+          for (uint32_t o = 1; o < 4; o <<= 1) {
+            if (o >= each) break;
             above += __shfl_xor_sync(0xffffffffu, above, o);
             every += __shfl_xor_sync(0xffffffffu, every, o);
             larger += __shfl_xor_sync(0xffffffffu, larger, o);
@@ -667,8 +599,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           while (full < size) full *= 2;
           for (uint32_t i = size + tid; i < full; i += kThreads) sh.quick.sorted[i] = 0;
           __syncthreads();
-          for (uint32_t span = 2; span <= full; span *= 2)
-            for (uint32_t step = span / 2; step; step /= 2) {
+          // A bitonic sort, largest first.  A warp has 64 neighbours in registers, so that only steps of 64 and more go through
+          // shared memory.
+          const uint32_t x0 = warp * 64 + lane;
+          for (uint32_t span = 64; span <= full; span *= 2) {
+            for (uint32_t step = span / 2; step >= 64; step /= 2) {
               for (uint32_t i = tid; i < full / 2; i += kThreads) {
                 const uint32_t x = 2 * i - (i & (step - 1)), y = x + step;
                 const uint64_t f = sh.quick.sorted[x], g = sh.quick.sorted[y];
@@ -676,12 +611,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               }
               __syncthreads();
             }
+            if (warp * 64 < full) {
+              uint64_t x[2] = {sh.quick.sorted[x0], sh.quick.sorted[x0 + 32]};
+              for (uint32_t inner = span == 64 ? 2 : span;; inner = inner < 64 ? inner * 2 : 128) {  // (the first time all spans up to 64)
+                if (inner >= 64) {
+                  if ((x[0] < x[1]) == ((x0 & inner) == 0)) {
+                    const uint64_t t = x[0];
+                    x[0] = x[1], x[1] = t;
+                  }
+                }
+#pragma unroll 1
+                for (uint32_t step = min(inner / 2, 16u); step; step /= 2)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, x[h], step);
+                    const bool larger_here = ((lane & step) == 0) == (((x0 + 32 * h) & inner) == 0);
+                    x[h] = larger_here == (x[h] > y) ? x[h] : y;
+                  }
+                if (inner >= 64) break;
+              }
+              sh.quick.sorted[x0] = x[0], sh.quick.sorted[x0 + 32] = x[1];
+            }
+            __syncthreads();
+          }
           // exact weights before each
           const uint32_t per = (size + kThreads - 1) / kThreads;
           const uint32_t j0 = min(tid * per, size), j1 = min(j0 + per, size);
           uint64_t w = 0;
           for (uint32_t j = j0; j < j1; ++j) {
-            const uint64_t x = weight(K::value_of(static_cast<uint32_t>(sh.quick.sorted[j] >> 32)), scale, sh.table);
+            const uint64_t x = one_weight(K::value_of(static_cast<uint32_t>(sh.quick.sorted[j] >> 32)));
             sh.quick.upto[j] = x;
             w += x;
           }
@@ -716,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
   }
-  // ---- digit by digit, and exact sums of all that is kept
+  // ---- digit by digit, and sums of all that is kept
   // One thread of the first CTA tells all CTAs what it found.
   auto tell = [&](const Found& g) {
     const uint64_t* words = reinterpret_cast<const uint64_t*>(&g);
@@ -730,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   };
   // The lowest key kept by a count (weights false: tokens above it < k) or by weight (above it < target):
   // found key by key range, `with_w` is the weight down to and with it.
-  auto search = [&](uint32_t lo, bool by_weight, bool weights, uint32_t k, double target) {
+  auto search = [&](uint32_t lo, bool by_weight, bool weights, uint32_t k, double target, bool exact) {
     Found f{lo, most, 0, 0, 0, 0};
     for (int round = 0; round < 4; ++round) {  // (ten bits a round)
       const uint32_t range = f.hi - f.lo;
@@ -740,8 +698,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (weights) sh.digits.lo[i] = sh.digits.hi[i] = 0;
       }
       __syncthreads();
+      const float lowest = K::value_of(f.lo);
       for (int i = w0 + lane; i < w1; i += 32) {
         const uint4 v = data[i];
+        if (K::top_of(v) < lowest) continue;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const uint32_t b = K::bits(v, e), key = K::of(b);
@@ -749,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const int bin = (f.hi - key) >> shift;
           atomicAdd(&sh.digits.count[bin], 1u);
           if (weights) {
-            const uint64_t w = weight(K::value(b), scale, sh.table);
+            const uint64_t w = exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
             const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.digits.lo[bin], w_lo);
             const uint32_t w_hi = static_cast<uint32_t>(w >> 32) + (old + w_lo < old ? 1u : 0u);
             if (w_hi) atomicAdd(&sh.digits.hi[bin], w_hi);
@@ -766,12 +726,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           c = sh.digits.count[bin];
           if (weights) w = static_cast<uint64_t>(sh.digits.hi[bin]) << 32 | sh.digits.lo[bin];
         } else {
-          for (int r = 0; r < n; ++r) {
-            c += ld_cluster(mapa_shared(smem_u32(&sh.digits.count[bin]), r));
-            if (weights)
-              w += (static_cast<uint64_t>(ld_cluster(mapa_shared(smem_u32(&sh.digits.hi[bin]), r))) << 32) +
-                   ld_cluster(mapa_shared(smem_u32(&sh.digits.lo[bin]), r));
-          }
+          c = static_cast<uint32_t>(cluster_sum(&sh.digits.count[bin], n));
+          if (weights) w = (cluster_sum(&sh.digits.hi[bin], n) << 32) + cluster_sum(&sh.digits.lo[bin], n);
         }
         if (n == 1) {
           sh.digits.all_count[bin] = c;
@@ -827,74 +783,121 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return f;
   };
 
-  uint64_t whole = 0;  // weight of all that top-k leaves
-  if (by_k) {
-    const Found f = search(K::LOWEST, false, by_p, k_asked, 0.0);
-    least = max(least, f.lo);
-    whole = f.with_w;
-    if (by_p) {
-      const double target = static_cast<double>(p) * static_cast<double>(whole);
-      least = max(least, target > 0.0 ? search(f.lo, true, true, 0, target).lo : most);
+  // The token among those whose key is `cut` or more; false if the FP32 weights leave it open.
+  auto draw_from = [&](uint32_t cut, bool exact) {
+    const float from_x = K::value_of(cut);
+    auto sum_of = [&](const uint4& v) {
+      if (exact) return K::template exact_sum<true>(v, cut, scale, sh.table);
+      uint64_t sum = 0;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const uint32_t b = K::bits(v, e);
+        if (K::of(b) >= cut) sum += quick_weight(K::value(b));
+      }
+      return sum;
+    };
+    uint64_t sum = 0;
+    uint32_t count = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint4 v = data[i];
+      if (K::top_of(v) < from_x) continue;
+      sum += sum_of(v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) count += K::of(K::bits(v, e)) >= cut;
     }
-  } else if (by_p) {
-    whole = exact_sum();
-    const double target = static_cast<double>(p) * static_cast<double>(whole);
-    least = max(least, target > 0.0 ? search(K::LOWEST, true, true, 0, target).lo : most);
-  }
-
-  // ---- the kept weights, and the place that u names
-  const float from_x = K::value_of(least);
-  uint64_t sum = 0;
-  uint32_t count = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint4 v = data[i];
-    if (K::top_of(v) < from_x) continue;
-    sum += K::exact_sum(v, least, scale, sh.table);
+    const uint64_t total = cluster_total(sum, count);
+    const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
+    const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
+    uint64_t below = 0;
+    for (int i = 0; i < rank; ++i) below += sh.cta_w[i];
+    if (at >= below && at < below + sh.cta_w[rank]) {  // (one CTA)
+      for (int i = 0; i < warp; ++i) below += sh.warp_w[i];
+      if (at >= below && at < below + sh.warp_w[warp]) {  // (one warp)
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+          const int i = i0 + lane;
+          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
+          uint64_t part = 0;
+          if (__any_sync(0xffffffffu, !(K::top_of(v) < from_x))) part = sum_of(v);
+          uint64_t upto = part;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) count += K::of(K::bits(v, e)) >= least;
-  }
-  const uint64_t total = cluster_total(sum);
-  const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
-  uint64_t below = 0;
-  for (int i = 0; i < rank; ++i) below += sh.cta_w[i];
-  if (at >= below && at < below + sh.cta_w[rank]) {  // (one CTA)
-    for (int i = 0; i < warp; ++i) below += sh.warp_w[i];
-    if (at >= below && at < below + sh.warp_w[warp]) {  // (one warp)
-      for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
-        uint64_t part = 0;
-        if (__any_sync(0xffffffffu, !(K::top_of(v) < from_x))) part = K::exact_sum(v, least, scale, sh.table);
-        uint64_t upto = part;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = shfl_up(upto, o);
-          if (lane >= o) upto += y;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, below + upto > at);
-        if (over) {
-          const int who = __ffs(over) - 1;
-          uint4 piece;
-          piece.x = __shfl_sync(0xffffffffu, v.x, who);
-          piece.y = __shfl_sync(0xffffffffu, v.y, who);
-          piece.z = __shfl_sync(0xffffffffu, v.z, who);
-          piece.w = __shfl_sync(0xffffffffu, v.w, who);
-          const uint64_t start = below + __shfl_sync(0xffffffffu, upto - part, who);
-          float x;
-          if (K::exact_find(piece, least, start, at, scale, sh.table, lane, x)) {
-            a.tokens[row] = (first + i0 + who) * VEC + lane - skip;
-            if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = shfl_up(upto, o);
+            if (lane >= o) upto += y;
           }
-          break;
+          const unsigned over = __ballot_sync(0xffffffffu, below + upto > at);
+          if (over) {
+            // a lane has a value of the piece
+            const int who = __ffs(over) - 1;
+            uint4 piece;
+            piece.x = __shfl_sync(0xffffffffu, v.x, who);
+            piece.y = __shfl_sync(0xffffffffu, v.y, who);
+            piece.z = __shfl_sync(0xffffffffu, v.z, who);
+            piece.w = __shfl_sync(0xffffffffu, v.w, who);
+            below += __shfl_sync(0xffffffffu, upto - part, who);
+            uint32_t b = K::SIGN | K::INF;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) b = lane == e ? K::bits(piece, e) : b;
+            const float x = K::value(b);
+            const uint64_t w = lane < VEC && K::of(b) >= cut ? (exact ? one_weight(x) : quick_weight(x)) : 0;
+            uint64_t here = w;
+#pragma unroll
+            for (int o = 1; o < VEC; o <<= 1) {
+              const uint64_t y = shfl_up(here, o);
+              if (lane >= o) here += y;
+            }
+            here += below;
+            const unsigned past = __ballot_sync(0xffffffffu, here > at);
+            // (further from both of its borders than the FP32 sums may be off)
+            if (lane == __ffs(past) - 1 && here - w + off <= at && here > at + off) {
+              a.tokens[row] = (first + i0 + who) * VEC + lane - skip;
+              if (a.kept) a.kept[row] = static_cast<int32_t>(count);
+              if (a.logprob) {
+                const uint64_t one = exact ? 1ull << (kFixed - a.drop) : quick_weight(m);
+                a.logprob[row] = set.log_of(x, m, static_cast<float>(total > one ? total - one : 0) / static_cast<float>(one));
+              }
+              if (!exact) tell_verdict(kDone);
+            }
+            break;
+          }
+          below += __shfl_sync(0xffffffffu, upto, 31);
         }
-        below += __shfl_sync(0xffffffffu, upto, 31);
       }
     }
-  }
-  __syncwarp();
-  if (a.kept) {
-    const uint64_t c = cluster_total(count);
-    if (rank == 0 && tid == 0) a.kept[row] = static_cast<int32_t>(c);
+    __syncwarp();
+    if (exact) return true;
+    cluster_sync(n);
+    return sh.verdict == kDone;
+  };
+
+  // By FP32 weights first, and by exact ones if they leave a decision open.
+  bool exact = !in_range || (by_p && !by_k && quick_total == 0);
+  for (;;) {
+    uint32_t cut = least;
+    bool open = false;
+    if (by_k || by_p) {
+      uint32_t from = from_key;
+      uint64_t whole = 0;  // weight of all that top-k leaves
+      if (by_k) {
+        const Found f = search(from, false, by_p, k_asked, 0.0, exact);
+        from = f.lo, whole = f.with_w, cut = max(cut, f.lo);
+      } else {
+        whole = exact ? exact_sum() : quick_total;
+      }
+      if (by_p) {
+        const double target = static_cast<double>(p) * static_cast<double>(whole);
+        if (target > 0.0) {
+          const Found f = search(from, true, true, 0, target, exact);
+          cut = max(cut, f.lo);
+          const double off = exact ? 0.0 : static_cast<double>(whole) * static_cast<double>(error_of(whole, 12.f));
+          open = !exact && !(static_cast<double>(f.above_w) + off < target && static_cast<double>(f.with_w) >= target + off);
+        } else {
+          cut = most;
+        }
+      }
+    }
+    if (!open) open = !draw_from(cut, exact);
+    if (!open) return;
+    exact = true;
   }
 }
 

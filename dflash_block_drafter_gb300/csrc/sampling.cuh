@@ -142,6 +142,8 @@ __device__ __forceinline__ uint64_t weight(float x, const Scale& c, const TableE
   weights(in, c, table, out);
   return out[0];
 }
+// By a call, for steps that few rows take: their instructions come from L2, so that there is one copy.
+__device__ __noinline__ static uint64_t weight_by_call(float x, const Scale* c, const TableEntry* table) { return weight(x, *c, table); }
 
 // ------------------------------------------------------------------ keys
 // Whole numbers in the order of the values, -0 with +0.
@@ -245,32 +247,38 @@ struct Keys {
       for (int e = 0; e < o; ++e) x[e] += x[e + o];
     return x[0];
   }
-  // exact weight of a piece's values whose key is `least` or more
-  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, uint32_t least, const Scale& c, const TableEntry* table) {
-    constexpr int VEC = Elem<TYPE>::VEC;
+  // exact weight of a piece's values whose key is `least` or more (CALL: by calls, else four side by side)
+  template <bool CALL>
+  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, uint32_t least, const Scale* c, const TableEntry* table) {
+    constexpr int VEC = Elem<TYPE>::VEC, N = CALL ? 1 : 4;
     uint64_t sum = 0;
 #pragma unroll
-    for (int e0 = 0; e0 < VEC; e0 += 4) {
-      float x[4];
-      uint64_t w[4];
+    for (int e0 = 0; e0 < VEC; e0 += N) {
+      float x[N];
+      uint64_t w[N];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = value(bits(v, e0 + e));
-      weights(x, c, table, w);
+      for (int e = 0; e < N; ++e) x[e] = value(bits(v, e0 + e));
+      if constexpr (CALL) {
+        w[0] = weight_by_call(x[0], c, table);
+      } else {
+        weights(x, *c, table, w);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += of(bits(v, e0 + e)) >= least ? w[e] : 0;
+      for (int e = 0; e < N; ++e) sum += of(bits(v, e0 + e)) >= least ? w[e] : 0;
     }
     return sum;
   }
   // The first value of a piece (the same in all lanes) with which the exact weights from `from` on exceed `place`: the lane
   // that has it.  Each lane has one value.
-  static __device__ __forceinline__ bool exact_find(const uint4& v, uint32_t least, uint64_t from, uint64_t place, const Scale& c,
+  template <bool CALL>
+  static __device__ __forceinline__ bool exact_find(const uint4& v, uint32_t least, uint64_t from, uint64_t place, const Scale* c,
                                                     const TableEntry* table, int lane, float& x) {
     constexpr int VEC = Elem<TYPE>::VEC;
     uint32_t b = SIGN | INF;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) b = lane == e ? bits(v, e) : b;
     x = value(b);
-    uint64_t w = weight(x, c, table);
+    uint64_t w = CALL ? weight_by_call(x, c, table) : weight(x, *c, table);
     if (lane >= VEC || of(b) < least) w = 0;
     uint64_t upto = w;
 #pragma unroll
@@ -290,8 +298,8 @@ struct Keys {
     return c;
   }
   // the key of the smallest value that is not below x
-  static __device__ __forceinline__ uint32_t at_least(double x) {
-    const float f = __double2float_ru(x);
+  static __device__ __forceinline__ uint32_t at_least(double x) { return at_least(__double2float_ru(x)); }
+  static __device__ __forceinline__ uint32_t at_least(float f) {
     if constexpr (WIDE) return of(__float_as_uint(f));
     if constexpr (TYPE == DFLASH_T_BF16) return of(__bfloat16_as_ushort(__float2bfloat16_ru(f)));
     return of(__half_as_ushort(__float2half_ru(f)));
@@ -315,8 +323,19 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
 }
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+// The sum of a word over the CTAs of a cluster: all reads first, which take long (one after the other 4 us with 16 CTAs).
+__device__ __forceinline__ uint64_t cluster_sum(const uint32_t* word, int n) {
+  const uint32_t at = smem_u32(word);
+  uint32_t v[kMaxSplits];
+#pragma unroll
+  for (int r = 0; r < kMaxSplits; ++r) v[r] = r < n ? ld_cluster(mapa_shared(at, r)) : 0;
+  uint64_t sum = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxSplits; ++r) sum += v[r];
+  return sum;
 }
 __device__ __forceinline__ uint64_t ld_cluster64(uint32_t addr) {
   uint64_t v;
