@@ -72,12 +72,14 @@ struct Shared {
   TableEntry table[32];
   Found found;
   uint64_t cta_w[kMaxSplits], warp_w[kWarps];
-  uint32_t cta_top[kMaxSplits], cta_low[kMaxSplits], cta_n[kMaxSplits], warp_u[kWarps], warp_low[kWarps], warp_n[kWarps];
+  uint32_t cta_top[kMaxSplits], cta_low[kMaxSplits], cta_n[kMaxSplits], cta_c[kMaxSplits], warp_u[kWarps], warp_low[kWarps], warp_n[kWarps];
   float warp_f[kWarps];
   double log_min_p;
   Scale scale;
   float bound;
   uint32_t verdict;
+  int where;      // the values in which u lies, and the weight before them
+  uint64_t from;
 };
 constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
 // What the first CTA (or the one that u names) says of a quick answer.
@@ -230,27 +232,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   uint32_t least = K::LOWEST;
   if (by_min) least = max(least, min(most, K::at_least(static_cast<double>(m) + sh.log_min_p)));
 
-  // The sum over the cluster of a value per thread, and the CTAs' sums in sh.cta_w; of a count too.
-  auto cluster_total = [&](uint64_t v, uint32_t& count) {
-    v = warp_sum(v);
-    count = __reduce_add_sync(0xffffffffu, count);
-    cluster_sync(n);  // the last values in these arrays have been read
-    if (lane == 0) sh.warp_w[warp] = v, sh.warp_n[warp] = count;
-    __syncthreads();
-    if (tid < 32) {
-      v = warp_sum(lane < kWarps ? sh.warp_w[lane] : uint64_t(0));
-      count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
-      if (n == 1) {
-        if (lane == 0) sh.cta_w[0] = v, sh.cta_n[0] = count;
-      } else if (lane < n) {
-        st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), lane), v);
-        st_cluster(mapa_shared(smem_u32(&sh.cta_n[rank]), lane), count);
-      }
-    }
-    cluster_sync(n);
-    count = __reduce_add_sync(0xffffffffu, lane < n ? sh.cta_n[lane] : 0u);
-    return warp_sum(lane < n ? sh.cta_w[lane] : uint64_t(0));
-  };
   // FP32 weights, 2^(x c + k), in the units of the exact ones: sums are whole numbers too.
   const float k_hi = -(m * c_hi);
   const bool in_range = fabsf(m) * c_hi < 0x1p20f;  // (k is off by 2^-4 at most)
@@ -262,16 +243,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return 0x1p-24f * (more + 1.1f * log2f(static_cast<float>(a.vocab) * unit / static_cast<float>(sum)));
   };
   auto one_weight = [&](float x) { return weight_by_call(x, scale, sh.table); };
-  // The exact weight of all tokens.
-  auto exact_sum = [&]() {
-    uint64_t sum = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint4 v = data[i];
-      sum += K::template exact_sum<true>(v, K::LOWEST, scale, sh.table);
-    }
-    uint32_t none = 0;
-    return cluster_total(sum, none);
-  };
   // The sum of a value per thread over this CTA's threads before it, and over all of them.
   auto scan = [&](uint64_t v, uint64_t& all) {
     uint64_t x = v;
@@ -292,6 +263,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       all += y;
     }
     return x;
+  };
+  // The sum over the cluster of the CTAs' v and counts, and that of the CTAs before this one.
+  auto exchange = [&](uint64_t v, uint32_t& count, uint64_t& below) {
+    if (n == 1) {
+      below = 0;
+      return v;
+    }
+    if (tid < n) {
+      st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), tid), v);
+      st_cluster(mapa_shared(smem_u32(&sh.cta_c[rank]), tid), count);
+    }
+    __syncwarp();
+    cluster_sync(n);
+    const uint64_t w = lane < n ? sh.cta_w[lane] : 0;
+    count = __reduce_add_sync(0xffffffffu, lane < n ? sh.cta_c[lane] : 0u);
+    below = warp_sum(lane < rank ? w : uint64_t(0));
+    return warp_sum(w);
+  };
+  // The rare steps take a thread's values one by one, neighbours in the row: few instructions (unrolled over pieces they took 5 us
+  // each the first time, most of it to fetch them), and a thread's sum leads to its values.
+  const int per_thread = (mine * VEC + kThreads - 1) / kThreads | 1;  // odd: no two lanes in a bank
+  const int t0 = min(tid * per_thread, mine * VEC), t1 = min(t0 + per_thread, mine * VEC);
+  auto bits_at = [&](int i) -> uint32_t {
+    if constexpr (K::WIDE) return reinterpret_cast<const uint32_t*>(data)[i];
+    else return reinterpret_cast<const uint16_t*>(data)[i];
+  };
+  // The exact weight of all tokens.
+  auto exact_sum = [&]() {
+    uint64_t sum = 0, all, below;
+    uint32_t none = 0;
+#pragma unroll 1
+    for (int i = t0; i < t1; ++i) sum += one_weight(K::value(bits_at(i)));
+    scan(sum, all);
+    return exchange(all, none, below);
   };
   auto tell_verdict = [&](uint32_t v) {  // (one thread)
     for (int r = 0; r < n; ++r) {
@@ -698,22 +703,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (weights) sh.digits.lo[i] = sh.digits.hi[i] = 0;
       }
       __syncthreads();
-      const float lowest = K::value_of(f.lo);
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const uint4 v = data[i];
-        if (K::top_of(v) < lowest) continue;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const uint32_t b = K::bits(v, e), key = K::of(b);
-          if (key < f.lo || key > f.hi) continue;
-          const int bin = (f.hi - key) >> shift;
-          atomicAdd(&sh.digits.count[bin], 1u);
-          if (weights) {
-            const uint64_t w = exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
-            const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.digits.lo[bin], w_lo);
-            const uint32_t w_hi = static_cast<uint32_t>(w >> 32) + (old + w_lo < old ? 1u : 0u);
-            if (w_hi) atomicAdd(&sh.digits.hi[bin], w_hi);
-          }
+#pragma unroll 1
+      for (int i = t0; i < t1; ++i) {
+        const uint32_t b = bits_at(i), key = K::of(b);
+        if (key < f.lo || key > f.hi) continue;
+        const int bin = (f.hi - key) >> shift;
+        atomicAdd(&sh.digits.count[bin], 1u);
+        if (weights) {
+          const uint64_t w = exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
+          const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.digits.lo[bin], w_lo);
+          const uint32_t w_hi = static_cast<uint32_t>(w >> 32) + (old + w_lo < old ? 1u : 0u);
+          if (w_hi) atomicAdd(&sh.digits.hi[bin], w_hi);
         }
       }
       cluster_sync(n);
@@ -785,85 +785,61 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   // The token among those whose key is `cut` or more; false if the FP32 weights leave it open.
   auto draw_from = [&](uint32_t cut, bool exact) {
-    const float from_x = K::value_of(cut);
-    auto sum_of = [&](const uint4& v) {
-      if (exact) return K::template exact_sum<true>(v, cut, scale, sh.table);
-      uint64_t sum = 0;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const uint32_t b = K::bits(v, e);
-        if (K::of(b) >= cut) sum += quick_weight(K::value(b));
-      }
-      return sum;
+    auto weight_at = [&](int i) -> uint64_t {
+      const uint32_t b = bits_at(i);
+      if (K::of(b) < cut) return 0;
+      return exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
     };
-    uint64_t sum = 0;
+    uint64_t sum = 0, all, below;
     uint32_t count = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint4 v = data[i];
-      if (K::top_of(v) < from_x) continue;
-      sum += sum_of(v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) count += K::of(K::bits(v, e)) >= cut;
+#pragma unroll 1
+    for (int i = t0; i < t1; ++i) {
+      sum += weight_at(i);
+      count += K::of(bits_at(i)) >= cut;
     }
-    const uint64_t total = cluster_total(sum, count);
+    count = __reduce_add_sync(0xffffffffu, count);
+    uint64_t before = scan(sum, all);
+    if (lane == 0) sh.warp_n[warp] = count;
+    if (tid == 0) sh.where = -1;
+    __syncthreads();
+    count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
+    const uint64_t total = exchange(all, count, below);
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
     const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
-    uint64_t below = 0;
-    for (int i = 0; i < rank; ++i) below += sh.cta_w[i];
-    if (at >= below && at < below + sh.cta_w[rank]) {  // (one CTA)
-      for (int i = 0; i < warp; ++i) below += sh.warp_w[i];
-      if (at >= below && at < below + sh.warp_w[warp]) {  // (one warp)
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-          const int i = i0 + lane;
-          const uint4 v = i < w1 ? data[i] : make_uint4(E::NOTHING, E::NOTHING, E::NOTHING, E::NOTHING);
-          uint64_t part = 0;
-          if (__any_sync(0xffffffffu, !(K::top_of(v) < from_x))) part = sum_of(v);
-          uint64_t upto = part;
+    before += below;
+    if (before <= at && at < before + sum) sh.where = t0, sh.from = before;  // (one thread of the cluster)
+    __syncthreads();
+    if (warp == 0 && sh.where >= 0) {
+      uint64_t from = sh.from;
+      const int end = min(sh.where + per_thread, mine * VEC);
+      for (int i0 = sh.where; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const uint64_t w = i < end ? weight_at(i) : 0;
+        uint64_t upto = w;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = shfl_up(upto, o);
-            if (lane >= o) upto += y;
-          }
-          const unsigned over = __ballot_sync(0xffffffffu, below + upto > at);
-          if (over) {
-            // a lane has a value of the piece
-            const int who = __ffs(over) - 1;
-            uint4 piece;
-            piece.x = __shfl_sync(0xffffffffu, v.x, who);
-            piece.y = __shfl_sync(0xffffffffu, v.y, who);
-            piece.z = __shfl_sync(0xffffffffu, v.z, who);
-            piece.w = __shfl_sync(0xffffffffu, v.w, who);
-            below += __shfl_sync(0xffffffffu, upto - part, who);
-            uint32_t b = K::SIGN | K::INF;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) b = lane == e ? K::bits(piece, e) : b;
-            const float x = K::value(b);
-            const uint64_t w = lane < VEC && K::of(b) >= cut ? (exact ? one_weight(x) : quick_weight(x)) : 0;
-            uint64_t here = w;
-#pragma unroll
-            for (int o = 1; o < VEC; o <<= 1) {
-              const uint64_t y = shfl_up(here, o);
-              if (lane >= o) here += y;
-            }
-            here += below;
-            const unsigned past = __ballot_sync(0xffffffffu, here > at);
-            // (further from both of its borders than the FP32 sums may be off)
-            if (lane == __ffs(past) - 1 && here - w + off <= at && here > at + off) {
-              a.tokens[row] = (first + i0 + who) * VEC + lane - skip;
-              if (a.kept) a.kept[row] = static_cast<int32_t>(count);
-              if (a.logprob) {
-                const uint64_t one = exact ? 1ull << (kFixed - a.drop) : quick_weight(m);
-                a.logprob[row] = set.log_of(x, m, static_cast<float>(total > one ? total - one : 0) / static_cast<float>(one));
-              }
-              if (!exact) tell_verdict(kDone);
-            }
-            break;
-          }
-          below += __shfl_sync(0xffffffffu, upto, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = shfl_up(upto, o);
+          if (lane >= o) upto += y;
         }
+        upto += from;
+        const unsigned past = __ballot_sync(0xffffffffu, upto > at);
+        if (past) {
+          // (further from both of its borders than the FP32 sums may be off)
+          if (lane == __ffs(past) - 1 && upto - w + off <= at && upto > at + off) {
+            a.tokens[row] = first * VEC + i - skip;
+            if (a.kept) a.kept[row] = static_cast<int32_t>(count);
+            if (a.logprob) {
+              const uint64_t one = exact ? 1ull << (kFixed - a.drop) : quick_weight(m);
+              a.logprob[row] = set.log_of(K::value(bits_at(i)), m, static_cast<float>(total > one ? total - one : 0) / static_cast<float>(one));
+            }
+            if (!exact) tell_verdict(kDone);
+          }
+          break;
+        }
+        from = __shfl_sync(0xffffffffu, upto, 31);
       }
+      __syncwarp();
     }
-    __syncwarp();
     if (exact) return true;
     cluster_sync(n);
     return sh.verdict == kDone;
