@@ -5,11 +5,11 @@
 //   z_j = y_j cos a_j - y_{j+h} sin a_j,  z_{j+h} = y_{j+h} cos a_j + y_j sin a_j
 //   a_j = position (of j's axis) * frequency j,  j < h = rotary_dim / 2.
 //
-// A lane has 8 consecutive channels of a head (one 16-byte load and store), a
-// warp 256 channels: one, two or four heads.  The partner channels lie h away,
-// in another lane of the same head: h is a multiple of 8, so that four shuffles of the
-// raw words bring them.  Weights, cosines and sines of a row are folded into two
-// factors per channel, z = (x A + x' B) / rms, once per row and for all of its heads.
+// A lane has 8 pairs of channels of a head, two 16-byte loads and stores h apart (of the
+// channels that are not turned 16 neighbours), a warp 512 channels: two, four or eight heads.  So both channels of a
+// pair are in one lane.  (With 8 neighbours in a lane and the partners by shuffles, a value took 0.6 instructions of a warp
+// instead of 0.3, and 30001 rows of 32 / 8 heads of 128 144 us.)  Weights, cosines and sines of a row are folded into
+// two factors per channel, z = (x A + x' B) / rms, once per row and for all of its heads.
 // Everything is FP32, rounded once to the rows' type.  The bytes bound it: every value is read and
 // written once.
 #include "common.cuh"
@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnroll = 4;   // loads of a lane in flight
+constexpr int kUnroll = 2;   // steps of a warp whose loads are in flight
 constexpr int kMaxAxes = 4;
 
 struct RopeSide {
@@ -46,35 +46,44 @@ struct RopeArgs {
   int32_t* status;
 };
 
+// Two pieces of 8 channels as FP32.
 template <bool BF16>
-__device__ __forceinline__ uint64_t widen2(uint32_t w) {
-  if (BF16) return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack2(f.x, f.y);
+__device__ __forceinline__ void widen(const uint4 (&raw)[2], float (&x)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w[4] = {raw[h].x, raw[h].y, raw[h].z, raw[h].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (BF16) {
+        x[8 * h + 2 * k] = __uint_as_float(w[k] << 16);
+        x[8 * h + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        x[8 * h + 2 * k] = f.x;
+        x[8 * h + 2 * k + 1] = f.y;
+      }
+    }
+  }
 }
 
 // 1 / rms of a head whose sum of squares leaves FP32's range: the values are scaled by a power of two first.
 template <bool BF16, int LANES>
-__device__ __forceinline__ float far_rms(uint4 raw, float eps, bool small) {
+__device__ __noinline__ float far_rms(uint4 a, uint4 b, float eps, bool small) {
   const float f = small ? 0x1p70f : 0x1p-70f;
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float s = 0.f;
+  const uint4 raw[2] = {a, b};
+  float x[16], s = 0.f;
+  widen<BF16>(raw, x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    unpack2(widen2<BF16>(w[i]), a, b);
-    a *= f, b *= f;
-    s = fmaf(a, a, fmaf(b, b, s));
-  }
+  for (int i = 0; i < 16; ++i) s = fmaf(x[i] * f, x[i] * f, s);
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float m = s * (1.f / (8 * LANES)) + eps * f * f;
+  const float m = s * (1.f / (16 * LANES)) + eps * f * f;
   return m > 0.f ? rsqrtf(m) * f : 0.f;  // a head of zeros without eps stays one
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeArgs a) {
-  constexpr int LANES = D / 8, HEADS = 32 / LANES;  // lanes of a head, heads of a warp
+  constexpr int LANES = D / 16, HEADS = 32 / LANES;  // lanes of a head, heads of a step of a warp
   __shared__ __align__(16) float s_w[2][D];
   __shared__ uint64_t s_turns[D / 2];
   __shared__ uint8_t s_axis[D / 2];
@@ -95,11 +104,11 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeArg
     }
   }
   __syncthreads();
-  const int sub = lane / LANES, c0 = lane % LANES * 8;
-  const bool first = c0 < a.half, second = !first && c0 < 2 * a.half;
-  const int j0 = first ? c0 : second ? c0 - a.half : 0;               // frequencies of the lane's channels
-  const int p0 = first ? c0 + a.half : second ? c0 - a.half : c0;     // partner channels
-  const int from = sub * LANES + p0 / 8;
+  const int sub = lane / LANES, at = lane % LANES;
+  const bool turned = at < a.half / 8;
+  const int j0 = at * 8;                                        // frequencies of the lane's pairs
+  const int ca = turned ? j0 : at * 16;                         // its channels (those behind the turned ones begin at 2 half)
+  const int cb = turned ? j0 + a.half : ca + 8;
   const int steps = a.side[0].steps + a.side[1].steps;
   const long long units = static_cast<long long>(a.n_rows) * a.splits;
   for (long long unit = blockIdx.x * kWarps + (tid >> 5); unit < units; unit += gridDim.x * kWarps) {
@@ -140,72 +149,65 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeArg
       const int b0 = which ? max(i0 - a.side[0].steps, 0) : min(i0, s.steps);
       const int b1 = which ? max(i1 - a.side[0].steps, 0) : min(i1, s.steps);
       if (b0 >= b1) continue;
-      uint64_t fa[4], fb[4];  // A and B of the lane's channels
+      // z_a = (a aa + b ab) / rms, z_b = (b ba + a bb) / rms
+      float aa[8], ab[8], ba[8], bb[8];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const float2 w = *reinterpret_cast<const float2*>(&s_w[which][c0 + e]);
-        const float2 v = *reinterpret_cast<const float2*>(&s_w[which][p0 + e]);
-        float4 t = make_float4(1.f, 0.f, 1.f, 0.f);  // cos, sin of two channels
-        if (first || second) t = *reinterpret_cast<const float4*>(&angle[j0 + e]);
-        const float sign = first ? -1.f : 1.f;
-        fa[e / 2] = pack2(w.x * t.x, w.y * t.z);
-        fb[e / 2] = pack2(sign * v.x * t.y, sign * v.y * t.w);
+        const float2 w = *reinterpret_cast<const float2*>(&s_w[which][ca + e]);
+        const float2 v = *reinterpret_cast<const float2*>(&s_w[which][cb + e]);
+        float4 t = make_float4(1.f, 0.f, 1.f, 0.f);  // cos, sin of two pairs
+        if (turned) t = *reinterpret_cast<const float4*>(&angle[j0 + e]);
+        aa[e] = w.x * t.x, aa[e + 1] = w.y * t.z;
+        ab[e] = -v.x * t.y, ab[e + 1] = -v.y * t.w;
+        ba[e] = v.x * t.x, ba[e + 1] = v.y * t.z;
+        bb[e] = w.x * t.y, bb[e + 1] = w.y * t.w;
       }
-      const uint16_t* src = s.x + row * s.stride + sub * D + c0;
-      uint16_t* dst = s.out + row * s.out_stride + sub * D + c0;
+      const uint16_t* src = s.x + row * s.stride + sub * D;
+      uint16_t* dst = s.out + row * s.out_stride + sub * D;
       const bool norm = s.weight != nullptr;
 #pragma unroll 1
       for (int i = b0; i < b1; i += kUnroll) {
-        uint4 raw[kUnroll];
-        float ssq[kUnroll];
+        uint4 raw[kUnroll][2];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (i + u < b1 && (i + u) * HEADS + sub < s.heads)
-            raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(i + u) * (HEADS * D)));
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-          uint64_t q2 = pack2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t x = widen2<BF16>(w[k]);
-            q2 = fma2(x, x, q2);
+          raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+          if (i + u < b1 && (i + u) * HEADS + sub < s.heads) {
+            const uint16_t* from = src + (i + u) * (HEADS * D);
+            raw[u][0] = __ldcs(reinterpret_cast<const uint4*>(from + ca));
+            raw[u][1] = __ldcs(reinterpret_cast<const uint4*>(from + cb));
           }
-          float q0, q1;
-          unpack2(q2, q0, q1);
-          ssq[u] = q0 + q1;
         }
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1)
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) ssq[u] += __shfl_xor_sync(0xffffffffu, ssq[u], o);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           if (i + u >= b1) break;  // (the same for the warp)
-          // (widened again: kept, the values of all loads would take 32 registers)
-          asm("" : "+r"(raw[u].x), "+r"(raw[u].y), "+r"(raw[u].z), "+r"(raw[u].w));
-          const float m = ssq[u] * (1.f / D) + a.eps;
-          float inv = norm ? rsqrtf(m) : 1.f;
-          const bool big = !(ssq[u] < 1e38f), tiny = norm && m < 1e-30f;
-          if (__any_sync(0xffffffffu, big || tiny)) {
-            const float far = far_rms<BF16, LANES>(raw[u], a.eps, tiny);
-            if (norm && (big || tiny)) inv = far;
-            if (big && !(far > 0.f) && c0 == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-          }
-          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-          const uint64_t inv2 = pack2(inv, inv);
-          uint32_t out[4];
+          float x[16], ssq = 0.f, ssq2 = 0.f;
+          widen<BF16>(raw[u], x);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t p = __shfl_sync(0xffffffffu, w[k], from);
-            float z0, z1;
-            unpack2(mul2(fma2(widen2<BF16>(p), fb[k], mul2(widen2<BF16>(w[k]), fa[k])), inv2), z0, z1);
-            out[k] = BF16 ? pack_bf16x2(z0, z1) : pack_f16x2(z0, z1);
+          for (int e = 0; e < 16; e += 2) ssq = fmaf(x[e], x[e], ssq), ssq2 = fmaf(x[e + 1], x[e + 1], ssq2);
+          ssq += ssq2;
+#pragma unroll
+          for (int o = 1; o < LANES; o <<= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
+          const float m = ssq * (1.f / D) + a.eps;
+          float inv = norm ? rsqrtf(m) : 1.f;
+          const bool big = !(ssq < 1e38f), tiny = norm && m < 1e-30f;
+          if (__any_sync(0xffffffffu, big || tiny)) {
+            const float far = far_rms<BF16, LANES>(raw[u][0], raw[u][1], a.eps, tiny);
+            if (norm && (big || tiny)) inv = far;
+            if (big && !(far > 0.f) && at == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
           }
-          if ((i + u) * HEADS + sub < s.heads)
-            *reinterpret_cast<uint4*>(dst + static_cast<long long>(i + u) * (HEADS * D)) = make_uint4(out[0], out[1], out[2], out[3]);
+          uint32_t za[4], zb[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float z0 = fmaf(x[8 + e], ab[e], x[e] * aa[e]) * inv, z1 = fmaf(x[9 + e], ab[e + 1], x[e + 1] * aa[e + 1]) * inv;
+            const float y0 = fmaf(x[e], bb[e], x[8 + e] * ba[e]) * inv, y1 = fmaf(x[e + 1], bb[e + 1], x[9 + e] * ba[e + 1]) * inv;
+            za[e / 2] = BF16 ? pack_bf16x2(z0, z1) : pack_f16x2(z0, z1);
+            zb[e / 2] = BF16 ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
+          }
+          if ((i + u) * HEADS + sub < s.heads) {
+            uint16_t* to = dst + (i + u) * (HEADS * D);
+            *reinterpret_cast<uint4*>(to + ca) = make_uint4(za[0], za[1], za[2], za[3]);
+            *reinterpret_cast<uint4*>(to + cb) = make_uint4(zb[0], zb[1], zb[2], zb[3]);
+          }
         }
       }
     }
@@ -218,7 +220,7 @@ cudaError_t launch(RopeArgs a, bool bf16, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  constexpr int HEADS = 256 / D;
+  constexpr int HEADS = 512 / D;
   for (RopeSide& s : a.side) s.steps = (s.heads + HEADS - 1) / HEADS;
   const int steps = a.side[0].steps + a.side[1].steps;
   // few rows: a row's heads are shared out until every SM has its warps
