@@ -441,11 +441,13 @@ def dflash_qk_norm_rope(q: int, q_out: int, q_stride: int, q_out_stride: int, n_
                         axes: int, turns: int, rotary_dim: int, dev_status: int = 0, stream: int = 0) -> None:
     if (n_q_heads | n_k_heads | head_dim | n_rows | n_axes | rotary_dim) >> 31:  # negative or wide
         _refuse_wide("dflash_qk_norm_rope", n_q_heads, n_k_heads, head_dim, n_rows, n_axes, rotary_dim)
-    _check(load_library().dflash_qk_norm_rope(q or None, q_out or None, q_stride, q_out_stride, n_q_heads, k or None,
-                                              k_out or None, k_stride, k_out_stride, n_k_heads, head_dim, value_type,
-                                              n_rows, q_weight or None, k_weight or None, eps, positions or None,
-                                              position_stride, n_axes, axes or None, turns or None, rotary_dim,
-                                              dev_status or None, stream or None), "dflash_qk_norm_rope")
+    # (None and 0 are both the null pointer)
+    status = load_library().dflash_qk_norm_rope(q, q_out, q_stride, q_out_stride, n_q_heads, k, k_out, k_stride,
+                                                k_out_stride, n_k_heads, head_dim, value_type, n_rows, q_weight,
+                                                k_weight, eps, positions, position_stride, n_axes, axes, turns,
+                                                rotary_dim, dev_status, stream)
+    if status:
+        raise DflashError(status, "dflash_qk_norm_rope")
 
 
 def dflash_kv4_prefix_attention(cache: DflashKv4Cache, q: int, out: int, value_type: int, q_stride: int,
@@ -478,7 +480,8 @@ def dflash_sample_tokens(logits: int, value_type: int, row_stride: int, n_rows: 
                          dev_status: int = 0, stream: int = 0) -> None:
     if (n_rows | vocab) >> 31:  # negative or wide
         _refuse_wide("dflash_sample_tokens", n_rows, vocab)
-    _check(load_library().dflash_sample_tokens(logits, value_type, row_stride, n_rows, vocab, uniform or None,
-                                               temperature or None, top_k or None, top_p or None, min_p or None,
-                                               tokens or None, logprob or None, kept or None, dev_status or None,
-                                               stream or None), "dflash_sample_tokens")
+    # (None and 0 are both the null pointer)
+    status = load_library().dflash_sample_tokens(logits, value_type, row_stride, n_rows, vocab, uniform, temperature,
+                                                 top_k, top_p, min_p, tokens, logprob, kept, dev_status, stream)
+    if status:
+        raise DflashError(status, "dflash_sample_tokens")

@@ -206,7 +206,7 @@ def _elsewhere(dev: torch.device, stream):
         if stream.device_index != dev.index:
             _refuse("the stream is of another device")
         return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+    return torch.cuda.device(dev) if dev.index != torch._C._cuda_getDevice() else None
 
 
 def _current(dev: torch.device) -> int:
@@ -389,17 +389,6 @@ def rope_turns(inv_freq, device="cuda:0") -> torch.Tensor:
     return torch.from_numpy(turns).to(device)
 
 
-def _of_rows(x: torch.Tensor, out, device, what: str):
-    """(type, stride, out, its stride) of rows and what they are written to (made here if None)."""
-    stride = _row_stride(x, device, what)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        return stride, out, x.shape[1] * x.shape[2]
-    if out.shape != x.shape or out.dtype != x.dtype:
-        _refuse(what + " out: the rows' shape and type")
-    return stride, out, _row_stride(out, device, what + " out")
-
-
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
                  turns: Optional[torch.Tensor], q_weight=None, k_weight=None, eps: float = 1e-6, axes=None, q_out=None,
                  k_out=None, status=None, stream=None):
@@ -408,48 +397,71 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     `positions` [n], or [n_axes, n] with `axes` (uint8, one per frequency).
     Returns (q_out, k_out), which may be q and k themselves; rows of a negative
     position keep what they held (unset if the outputs are made here)."""
-    dev = q.device
+    dev, dtype = q.device, q.dtype
     if not q.is_cuda:
         _refuse("qk_norm_rope: CUDA tensors")
     where = _elsewhere(dev, stream)
     if where is not None:
         with where:
             return qk_norm_rope(q, k, positions, turns, q_weight, k_weight, eps, axes, q_out, k_out, status)
-    qs, q_out, qos = _of_rows(q, q_out, dev, "qk_norm_rope q")
+    qs = _row_stride(q, dev, "qk_norm_rope q")
     n, heads, d = q.shape
-    kp = kop = ks = kos = k_heads = 0
+    if q_out is None:
+        q_out, qos = torch.empty((n, heads, d), dtype=dtype, device=dev), heads * d
+    else:
+        qos = _row_stride(q_out, dev, "qk_norm_rope q_out")
+        if q_out.shape != q.shape or q_out.dtype != dtype:
+            _refuse("qk_norm_rope q_out: the rows' shape and type")
+    kp = kop = None
+    ks = kos = k_heads = 0
     if k is not None:
-        ks, k_out, kos = _of_rows(k, k_out, dev, "qk_norm_rope k")
-        if k.shape[0] != n or k.shape[2] != d or k.dtype != q.dtype:
+        ks = _row_stride(k, dev, "qk_norm_rope k")
+        kn, k_heads, kd = k.shape
+        if kn != n or kd != d or k.dtype != dtype:
             _refuse("qk_norm_rope: rows of one length and type")
-        kp, kop, k_heads = k.data_ptr(), k_out.data_ptr(), k.shape[1]
+        if k_out is None:
+            k_out, kos = torch.empty((n, k_heads, d), dtype=dtype, device=dev), k_heads * d
+        else:
+            kos = _row_stride(k_out, dev, "qk_norm_rope k_out")
+            if k_out.shape != k.shape or k_out.dtype != dtype:
+                _refuse("qk_norm_rope k_out: the rows' shape and type")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None or k_weight is not None:
         _refuse("qk_norm_rope: k_out and k_weight without k")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.float32 or w.device != dev or w.numel() != d or not w.is_contiguous()):
-            _refuse("qk_norm_rope: weights are contiguous float [head_dim] on the device of the call")
-    half, n_axes, pos = 0, 1, 0
+    qw = kw = None
+    if q_weight is not None:
+        qw = _weight(q_weight, dev, d)
+    if k_weight is not None:
+        kw = _weight(k_weight, dev, d)
+    half, n_axes, pos, tp, ap = 0, 1, None, None, None
     if turns is not None:
         half = turns.numel()
-        if (positions is None or turns.dtype != torch.int64 or turns.device != dev or not turns.is_contiguous()
-                or positions.dim() > 2 or positions.shape[-1] != n):
-            _refuse("qk_norm_rope: positions [n] or [n_axes, n] and int64 turns on the device of the call")
-        n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions is None or turns.dtype != torch.int64 or turns.device != dev or not turns.is_contiguous():
+            _refuse("qk_norm_rope: positions, and contiguous int64 turns on the device of the call")
+        if positions.dim() == 2:
+            n_axes = positions.shape[0]
+        if positions.numel() != n_axes * n or positions.dim() > 2:
+            _refuse("qk_norm_rope: positions [n] or [n_axes, n]")
         if n_axes > 1 and axes is None:
             _refuse("qk_norm_rope: several axes need `axes`")
-        pos = positions.data_ptr()
-        if axes is not None and (axes.dtype != torch.uint8 or axes.device != dev or axes.numel() != half
-                                 or not axes.is_contiguous()):
-            _refuse("qk_norm_rope: axes are contiguous uint8, one per frequency")
+        if axes is not None:
+            if axes.dtype != torch.uint8 or axes.device != dev or axes.numel() != half or not axes.is_contiguous():
+                _refuse("qk_norm_rope: axes are contiguous uint8, one per frequency")
+            ap = axes.data_ptr()
         _int32(dev, "qk_norm_rope", positions, status)
-    else:
+        pos, tp = positions.data_ptr(), turns.data_ptr()
+    elif status is not None:
         _int32(dev, "qk_norm_rope", status)
     dflash_qk_norm_rope(q.data_ptr(), q_out.data_ptr(), qs, qos, heads, kp, kop, ks, kos, k_heads, d,
-                        _VALUE_TYPES[q.dtype], n, 0 if q_weight is None else q_weight.data_ptr(),
-                        0 if k_weight is None else k_weight.data_ptr(), eps, pos, n, n_axes,
-                        0 if axes is None else axes.data_ptr(), 0 if turns is None else turns.data_ptr(), 2 * half,
-                        0 if status is None else status.data_ptr(), _current(dev))
+                        _VALUE_TYPES[dtype], n, qw, kw, eps, pos, n, n_axes, ap, tp, 2 * half,
+                        None if status is None else status.data_ptr(), _current(dev))
     return q_out, k_out
+
+
+def _weight(w: torch.Tensor, device, d: int) -> int:
+    if w.dtype != torch.float32 or w.device != device or w.numel() != d or not w.is_contiguous():
+        _refuse("qk_norm_rope: weights are contiguous float [head_dim] on the device of the call")
+    return w.data_ptr()
 
 
 def kv4_prefix_attention(cache: torch.Tensor, q: torch.Tensor, prefix_table: torch.Tensor, prefix_len: torch.Tensor,
@@ -512,20 +524,23 @@ def sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, temperature=None,
     stride, by_value = logits.stride()
     if by_value != 1 and vocab != 1:
         _refuse("sample_tokens: dense rows")
-    at = []
-    for x in (uniform, temperature, top_p, min_p):
-        if x is None:
-            at.append(0)
-            continue
-        if x.dtype != torch.float32 or x.device != dev or x.numel() != n or not x.is_contiguous():
-            _refuse("sample_tokens: one contiguous float of the device of the call per row")
-        at.append(x.data_ptr())
-    _int32(dev, "sample_tokens", top_k, status)
-    if top_k is not None and top_k.numel() != n:
-        _refuse("sample_tokens: one top_k per row")
+    if top_k is not None or status is not None:
+        _int32(dev, "sample_tokens", top_k, status)
+        if top_k is not None and top_k.numel() != n:
+            _refuse("sample_tokens: one top_k per row")
     out = torch.empty((3, n), dtype=_INT32, device=dev)
     to = out.data_ptr()
-    dflash_sample_tokens(logits.data_ptr(), kind, stride if n > 1 else vocab, n, vocab, at[0], at[1],
-                         0 if top_k is None else top_k.data_ptr(), at[2], at[3], to, to + 4 * n, to + 8 * n,
-                         0 if status is None else status.data_ptr(), _current(dev))
-    return out[0], out[1].view(torch.float32), out[2]
+    dflash_sample_tokens(logits.data_ptr(), kind, stride if n > 1 else vocab, n, vocab, _of_row(uniform, dev, n),
+                         _of_row(temperature, dev, n), None if top_k is None else top_k.data_ptr(),
+                         _of_row(top_p, dev, n), _of_row(min_p, dev, n), to, to + 4 * n, to + 8 * n,
+                         None if status is None else status.data_ptr(), _current(dev))
+    tokens, logprob, kept = out.unbind()
+    return tokens, logprob.view(torch.float32), kept
+
+
+def _of_row(x: Optional[torch.Tensor], device, n: int) -> Optional[int]:
+    if x is None:
+        return None
+    if x.dtype != torch.float32 or x.device != device or x.numel() != n or not x.is_contiguous():
+        _refuse("sample_tokens: one contiguous float of the device of the call per row")
+    return x.data_ptr()
