@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
   __shared__ float2 accl[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_cta = -1;
+  if constexpr (MODE == kKv4Prefix) pdl_launch_dependents();  // (the pass over the own cells)
   pdl_wait();
   int before = 0;  // split segments of earlier CTAs
   for (int c0 = 0; c0 < most; c0 += kMergeThreads) {
@@ -481,22 +482,29 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
   }
 }
 
-// Launches the merge behind an attention kernel of `most` CTAs, of which at
-// most `jobs` segments can be split.
-template <int D, int R, int MODE>
-cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
+// Launches a kernel; `early`: it may begin while the one before still ends.
+template <typename... P, typename... A>
+cudaError_t kv4_launch(void (*kernel)(P...), bool early, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  // few segments: one block per row, which many pieces want; many: at least one warp per row
-  const int y = 1536 / jobs, few = (R + 7) / 8;
-  cfg.gridDim = dim3(jobs, y < few ? few : y < R ? y : R);
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, R, MODE>, a, most);
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Launches the merge behind an attention kernel of `most` CTAs, of which at
+// most `jobs` segments can be split.
+template <int D, int R, int MODE>
+cudaError_t launch_kv4_merge(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
+  // few segments: one block per row, which many pieces want; many: at least one warp per row
+  const int y = 1536 / jobs, few = (R + 7) / 8;
+  return kv4_launch(kv4_merge_kernel<D, R, MODE>, true, dim3(jobs, y < few ? few : y < R ? y : R), kMergeThreads, 0, st, a, most);
 }
 
 // What the host knows of a call: its kernel, CTAs and split segments at most.

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   pdl_launch_dependents();
   if (c >= C || T == 0) {
     if (tid == 0) a.jobs[c].n_rows = 0;
+    if constexpr (MODE == kKv4Own) pdl_wait();
     return;
   }
   if (warp == kQkWarp) {
@@ -571,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           if (whole) row = kv4_pre_row(a, p.q.r0 + kv4_token(m, per_g), p.head, m - kv4_token(m, per_g) * a.G);
         if constexpr (MODE == kKv4Own) {
           if (whole && mine) {
-            const float2 both = kv4_join(m_ref, l, a.pre_ml[row]);
+            pdl_wait();
+            const float2 both = kv4_join(m_ref, l, __ldcg(a.pre_ml + row));
             inv = both.x, from_pre = both.y;
           }
         } else if constexpr (MODE == kKv4Plain) {
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               if (MODE != kKv4Prefix && whole) {
                 if constexpr (MODE == kKv4Own) {
                   const float4* pre = reinterpret_cast<const float4*>(a.pre + row * D + col + 8 * k);
-                  const float4 x = pre[0], y = pre[1];
+                  const float4 x = __ldcg(pre), y = __ldcg(pre + 1);
                   v[0] = fmaf(x.x, from_pre, v[0]), v[1] = fmaf(x.y, from_pre, v[1]), v[2] = fmaf(x.z, from_pre, v[2]), v[3] = fmaf(x.w, from_pre, v[3]);
                   v[4] = fmaf(y.x, from_pre, v[4]), v[5] = fmaf(y.y, from_pre, v[5]), v[6] = fmaf(y.z, from_pre, v[6]), v[7] = fmaf(y.w, from_pre, v[7]);
                 }
@@ -732,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     }
     if (!ok && lane == 0) set_status(a.status, DFLASH_DEV_TIMEOUT);
   }
+  if constexpr (MODE == kKv4Own) pdl_wait();  // (the merge reads what the pass over the prefix has left)
   // every warp whole again before the CTA-wide barrier, then the tensor memory goes
   __syncwarp();
   tc_fence_before();
@@ -749,8 +752,7 @@ cudaError_t launch(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kv4_attn_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        G::SMEM + 8 * (kKv4MaxSeq + 1));
   if (e != cudaSuccess) return e;
-  kv4_attn_tc_kernel<D, MODE><<<most, kThreads, G::SMEM + 8 * (a.n_seq + 1), st>>>(a);
-  e = cudaGetLastError();
+  e = kv4_launch(kv4_attn_tc_kernel<D, MODE>, MODE == kKv4Own, dim3(most), kThreads, G::SMEM + 8 * (a.n_seq + 1), st, a);
   if (e != cudaSuccess || most == 1) return e;
   return launch_kv4_merge<D, kRows, MODE>(a, most, jobs, st);
 }

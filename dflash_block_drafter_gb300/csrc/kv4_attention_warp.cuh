@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
   pdl_launch_dependents();
   if (c >= C || T == 0) {
     if (tid == 0) a.jobs[c].n_rows = 0;
+    if constexpr (MODE == kKv4Own) pdl_wait();
     return;
   }
   const long long x_end = kv4_start(T, C, c + 1);
@@ -559,11 +560,12 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
         if (whole) {
           if constexpr (MODE == kKv4Own) {
             const size_t at = kv4_pre_row(a, q.r0 + kv4_token(m, per_g), head, m - kv4_token(m, per_g) * a.G);
-            const float2 both = kv4_join(m_ref[n2][e], l, a.pre_ml[at]);
+            pdl_wait();
+            const float2 both = kv4_join(m_ref[n2][e], l, __ldcg(a.pre_ml + at));
             const float* pre = a.pre + at * D + col;
 #pragma unroll
             for (int j = 0; j < JT; ++j) {
-              const float2 x = *(reinterpret_cast<const float2*>(pre) + j);
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(pre) + j);
               o[j][n2][e] = o[j][n2][e] * both.x + x.x * both.y;
               o[j][n2][2 + e] = o[j][n2][2 + e] * both.x + x.y * both.y;
             }
@@ -597,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::PER_SM)) kv4_attn_kerne
     issued = next_issued;
   }
   if (!job && tid == 0) a.jobs[c].n_rows = 0;
+  if constexpr (MODE == kKv4Own) pdl_wait();  // (the merge reads what the pass over the prefix has left)
 }
 
 template <int D, int NT, int MODE>
@@ -605,8 +608,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, int most, int jobs, cudaStream_t s
   cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        G::SMEM + kPlanBytes(kKv4MaxSeq));
   if (e != cudaSuccess) return e;
-  kv4_attn_kernel<D, NT, MODE><<<most, kThreads, G::SMEM + kPlanBytes(a.n_seq), st>>>(a);
-  e = cudaGetLastError();
+  e = kv4_launch(kv4_attn_kernel<D, NT, MODE>, MODE == kKv4Own, dim3(most), kThreads, G::SMEM + kPlanBytes(a.n_seq), st, a);
   if (e != cudaSuccess || most == 1) return e;
   return launch_kv4_merge<D, G::R, MODE>(a, most, jobs, st);
 }
