@@ -29,7 +29,7 @@ constexpr int kBatchBytes = 32 * kLoads * 16;
 constexpr int kStages = 2;  // batches of a warp on their way
 constexpr int kRingBytes = kWarps * kStages * kBatchBytes;
 constexpr int kRestCtas = 8;         // CTAs for a row that the FP32 sums leave open
-constexpr int32_t kUndecided = -2, kClaimed = -3;  // the token of such a row, between the kernels
+constexpr int32_t kClaimed = -2, kUndecided = -3;  // the token of such a row, between the kernels: kUndecided less the places (plus 16) that its weights have less
 constexpr int kMaxBatches = (1 << 19) * 4 / kBatchBytes + 1;  // (a row may begin inside a piece)
 
 // The largest of the warp's values (no NaN among them).
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   }
   __syncthreads();
   if (!s_done && tid == 0) {
-    a.tokens[row] = kUndecided;
+    a.tokens[row] = kUndecided - 16 - (close ? a.drop : drop_of(whole / ex2_approx(fmaf(m, c, k)), a.drop));
     // (what the second kernel need not find again, where there is a place for it)
     if (a.logprob && a.kept) a.logprob[row] = m, a.kept[row] = static_cast<int32_t>(all);
   }
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   __shared__ Scale s_scale;
   __shared__ uint64_t s_wide[kWarps], cta_wide[kRestCtas];
   __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[4 * kWarps];
-  __shared__ int s_batch, s_row, s_told;
+  __shared__ int s_batch, s_row, s_drop, s_told, s_told_drop;
   __shared__ uint64_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % kRestCtas, cluster = blockIdx.x / kRestCtas, clusters = gridDim.x / kRestCtas;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
 #pragma unroll
         for (int i = 0; i < LOOK; ++i) {
           const int mine = (chunk * LOOK + i) * kThreads + tid;
-          open[i] = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) == kUndecided);
+          open[i] = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) <= kUndecided);
         }
         __syncthreads();  // s_row and s_open of the last round have been read
         if (lane < LOOK) s_open[lane * kWarps + warp] = lane == 0 ? open[0] : lane == 1 ? open[1] : lane == 2 ? open[2] : open[3];
@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
             const int w = (i + cluster) % (LOOK * kWarps);
             for (unsigned left = s_open[w]; left && s_row < 0; left &= left - 1) {
               const int r = chunk * LOOK * kThreads + w * 32 + __ffs(left) - 1;
-              if (atomicCAS(a.tokens + r, kUndecided, kClaimed) == kUndecided) s_row = r;
+              const int32_t mark = __ldcg(a.tokens + r);
+              if (mark <= kUndecided && atomicCAS(a.tokens + r, mark, kClaimed) == mark) s_row = r, s_drop = kUndecided - 16 - mark;
             }
           }
         }
@@ -414,15 +415,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           chunk = chunk + 1 == chunks ? 0 : chunk + 1;
         }
       }
-      if (tid < kRestCtas) put(&s_told, static_cast<uint32_t>(row), tid);
+      if (tid < kRestCtas) put(&s_told, static_cast<uint32_t>(row), tid), put(&s_told_drop, static_cast<uint32_t>(s_drop), tid);
       __syncwarp();
     }
     sync();
-    const int row = s_told;
+    const int row = s_told, drop = s_told_drop;
     if (row < 0) return;
     {
         const Settings set(a, row);
-        if (tid == 0) set.scale(s_scale, a.drop);
+        if (tid == 0) set.scale(s_scale, drop);
         const uint8_t* src = a.logits + row * a.row_bytes;
         const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E::BYTES;
         const uint4* frame = reinterpret_cast<const uint4*>(src - skip * E::BYTES);
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         }
         if (tid == 0) s_scale.m = m;
         __syncthreads();
-        const Scale* scale = &s_scale;
+        const Scale& scale = s_scale;
         for (int b = b0 + warp; b < b1; b += kWarps) {
           uint4 v[kLoads];
           load(b, v);
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           // (not unrolled, here and below: 32 weights in line are 30 KB of instructions that are fetched for each batch)
 #pragma unroll 1
           for (int j = 0; j < kLoads; ++j) {
-            sum += K::template exact_sum<false>(v[0], K::LOWEST, scale, table);
+            sum += K::exact_sum(v[0], scale, table);
             v[0] = v[1], v[1] = v[2], v[2] = v[3];
           }
           static_assert(kLoads == 4, "pieces");
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
             uint64_t from = s_from;
 #pragma unroll 1
             for (int j = 0; j < kLoads; ++j) {
-              const uint64_t w = K::template exact_sum<false>(v[0], K::LOWEST, scale, table), upto = warp_upto(w, lane);
+              const uint64_t w = K::exact_sum(v[0], scale, table), upto = warp_upto(w, lane);
               const unsigned over = __ballot_sync(0xffffffffu, from + upto > place);
               if (over) {  // (the same for the warp)
                 const int who = __ffs(over) - 1;
@@ -527,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
                 piece.w = __shfl_sync(0xffffffffu, v[0].w, who);
                 const uint64_t start = from + __shfl_sync(0xffffffffu, upto - w, who);
                 float value;
-                if (K::template exact_find<false>(piece, K::LOWEST, start, place, scale, table, lane, value)) {
+                if (K::exact_find(piece, start, place, scale, table, lane, value)) {
                   a.tokens[row] = b * BATCH + (j * 32 + who) * VEC + lane - skip;
-                  if (a.logprob) a.logprob[row] = set.log_of(value, m, others_of(whole, a.drop));
+                  if (a.logprob) a.logprob[row] = set.log_of(value, m, others_of(whole, drop));
                   if (a.kept) a.kept[row] = static_cast<int32_t>(all);
                 }
                 break;

@@ -42,23 +42,23 @@ constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kList = 1024;                // tokens that the first CTA sorts
 constexpr int kOwn = kList / kWarps;       // of a warp
 constexpr int kFew = 256;                  // tokens that it compares each with each
+constexpr int kListDrop = -7;              // places less than kFixed of a list's weights
 constexpr int kShort = kList / 2;          // a row that is a list as a whole
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
 
+// The keys among which the lowest one kept lies, the weight (or number) of the tokens above them and of all, and whether it is
+// known to lie there.
 struct Found {
-  uint32_t lo, hi;      // keys of the range
-  uint32_t above;       // tokens above it
-  uint32_t all;         // fewer tokens than are asked for: all are kept
-  uint64_t above_w;     // their weight, if weights are asked for
-  uint64_t with_w;      // the same with the range's own
+  uint32_t lo, hi;
+  uint64_t above, whole, certain;
 };
 
 struct Shared {
   union {
     struct {
-      uint32_t count[kBins], lo[kBins], hi[kBins];  // of this CTA's tokens; weights in two words
-      uint32_t all_count[kBins];                    // of the cluster's, in its first CTA
-      uint64_t all_w[kBins];
+      uint32_t lo[kBins], hi[kBins];  // weights of this CTA's tokens, in two words
+      uint64_t all[kBins];            // of the cluster's, in its first CTA
+      uint64_t above[kMaxSplits], rest[kMaxSplits];  // the CTAs' outside of all ranges
     } digits;
     struct {
       uint64_t own[kWarps][kOwn];  // (key, id) of each warp's tokens, in order of ids
@@ -76,7 +76,8 @@ struct Shared {
   float warp_f[kWarps];
   double log_min_p;
   Scale scale;
-  float bound;
+  float bound, upper;
+  uint64_t target;
   uint32_t verdict;
   int where;      // the values in which u lies, and the weight before them
   uint64_t from;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (tid == kThreads - 1) {
     if (rank == 0 && !set.fine) set_status(a.status, DFLASH_DEV_BAD_VALUE);
     if (!set.greedy) {
-      set.scale(sh.scale, a.drop);
+      set.scale(sh.scale, kListDrop);
       if (by_min) sh.log_min_p = static_cast<double>(set.temperature) * log(static_cast<double>(fminf(set.min_p, 1.f)));
     }
   }
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // FP32 weights, 2^(x c + k), in the units of the exact ones: sums are whole numbers too.
   const float k_hi = -(m * c_hi);
   const bool in_range = fabsf(m) * c_hi < 0x1p20f;  // (k is off by 2^-4 at most)
+  const float one = ex2_approx(fmaf(m, c_hi, k_hi));  // the largest of them
   const float unit = __int_as_float((127 + kFixed - a.drop) << 23);
   auto fixed = [&](float w) { return static_cast<uint64_t>(__float2ull_rn(w * unit)); };
   auto quick_weight = [&](float x) { return fixed(ex2_approx(fmaf(x, c_hi, k_hi))); };
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       below = 0;
       return v;
     }
+    cluster_sync(n);  // the last values have been read
     if (tid < n) {
       st_cluster(mapa_shared(smem_u32(&sh.cta_w[rank]), tid), v);
       st_cluster(mapa_shared(smem_u32(&sh.cta_c[rank]), tid), count);
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   const bool filter = by_k || by_p || by_min;
   uint32_t from_key = K::LOWEST;  // no threshold of top-k and top-p lies below
+  uint32_t to_key = most;         // nor one of top-p alone above
   uint64_t quick_total = 0;       // FP32 weights of all tokens, by top-p alone
   if (filter) {
     // ---- a bound below the thresholds
@@ -369,16 +373,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         __syncthreads();  // warp_f has been read
         if (lane == 31) sh.warp_f[warp] = x;
-        if (tid == 0) sh.bound = -INFINITY;
+        if (tid == 0) sh.bound = -INFINITY, sh.upper = INFINITY;
         __syncthreads();
+        float every = 0.f;
+        for (int i = 0; i < kWarps; ++i) {
+          const float y = sh.warp_f[i];
+          if (i < warp) x += y;
+          every += y;
+        }
+        const float over = every * (1.f + 0x1p-13f) - x;  // the ranges above this one, at most (544 roundings)
         x += rest * 0.25f;
-        for (int i = 0; i < warp; ++i) x += sh.warp_f[i];
-        // (2^-10: more than the sums and ranges are off)
-        const float most_left = rest * (static_cast<float>(quick_total) / unit) * (1.f - 0x1p-10f);
+        // (2^-10: more than the sums and ranges are off; the FP32 weights are relative to 2^(m c + k))
+        const float sum = static_cast<float>(quick_total) / unit / one, whole = sum * (1.f - 0x1p-10f);
+        const float most_left = rest * whole, least_kept = p * whole;
+        if (tid == 0) sh.scale.drop = drop_of(sum, a.drop);
         // the first range that has to be kept: with it more than may be left out would be
         if (x > most_left && x - w <= most_left) sh.bound = m - (bin + 1) / per / c_hi * (1.f + 0x1p-20f);
+        // and the last one that has to be left for others to be kept
+        if (over <= least_kept && over + w > least_kept) sh.upper = m - bin / per / c_hi * (1.f - 0x1p-20f);
         __syncthreads();
         bound = sh.bound;
+        if (sh.upper < INFINITY) to_key = min(most, K::at_least(sh.upper));
         if (bound > -INFINITY) from_key = max(from_key, min(most, K::at_least(bound)));
         // (too long a list is not made; min-p may shorten it)
         const uint32_t listed = __reduce_add_sync(0xffffffffu, (m - bound) * c_hi * per > bin ? c : 0u);
@@ -484,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             if (at >= c + w[i] && j == i) c += w[i], ++j;
           const uint64_t entry = sh.quick.list[lane * EACH + j];
           a.tokens[row] = static_cast<int32_t>(entry);
-          if (a.logprob) a.logprob[row] = set.log_of(K::value_of(static_cast<uint32_t>(entry >> 32)), m, others_of(total, a.drop));
+          if (a.logprob) a.logprob[row] = set.log_of(K::value_of(static_cast<uint32_t>(entry >> 32)), m, others_of(total, scale->drop));
           if (a.kept) a.kept[row] = static_cast<int32_t>(keep);
         }
       };
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             c += one_weight(x);
             if (c > at) {
               a.tokens[row] = static_cast<int32_t>(entry);
-              if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, a.drop));
+              if (a.logprob) a.logprob[row] = set.log_of(x, m, others_of(total, scale->drop));
               if (a.kept) a.kept[row] = static_cast<int32_t>(keep);
               break;
             }
@@ -570,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         double s_lo = 0.0, s_hi = 0.0;
         if (by_p && !by_k && a.vocab > kShort) {
           // (the FP32 weights are relative to 2^(m c + k))
-          const double whole = static_cast<double>(quick_total) / static_cast<double>(ex2_approx(fmaf(m, c_hi, k_hi)));
+          const double whole = static_cast<double>(quick_total) / static_cast<double>(one) * static_cast<double>(exp2f(a.drop - scale->drop));
           const double off = whole * static_cast<double>(error_of(quick_total, 16.f));
           s_lo = whole - off, s_hi = whole + off;
         }
@@ -680,109 +695,95 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   // ---- digit by digit, and sums of all that is kept
-  // One thread of the first CTA tells all CTAs what it found.
-  auto tell = [&](const Found& g) {
-    const uint64_t* words = reinterpret_cast<const uint64_t*>(&g);
-    for (int r = 0; r < n; ++r)
-#pragma unroll
-      for (int q = 0; q < static_cast<int>(sizeof(Found) / 8); ++q) {
-        uint64_t* to = reinterpret_cast<uint64_t*>(&sh.found) + q;
-        if (n == 1) *to = words[q];
-        else st_cluster(mapa_shared(smem_u32(to), r), words[q]);
-      }
-  };
-  // The lowest key kept by a count (weights false: tokens above it < k) or by weight (above it < target):
-  // found key by key range, `with_w` is the weight down to and with it.
-  auto search = [&](uint32_t lo, bool by_weight, bool weights, uint32_t k, double target, bool exact) {
-    Found f{lo, most, 0, 0, 0, 0};
-    for (int round = 0; round < 4; ++round) {  // (ten bits a round)
-      const uint32_t range = f.hi - f.lo;
-      const int shift = max(22 - __clz(range | 1), 0);
-      for (int i = tid; i < kBins; i += kThreads) {
-        sh.digits.count[i] = 0;
-        if (weights) sh.digits.lo[i] = sh.digits.hi[i] = 0;
-      }
+  // The lowest key kept among [lo, hi]: the one down to which the tokens from `base` on weigh p of them all or more (in
+  // numbers: down to which there are `number` of them), found range by range.  `sure`: the last range in which it lies whatever
+  // the errors of the weights; true if it is the last.
+  auto search = [&](uint32_t base, uint32_t lo, uint32_t hi, bool numbers, uint64_t number, bool exact, Found& sure) {
+    Found f{lo, hi, 0, 0, 1};
+    for (int round = 0;; ++round) {  // (ten bits a round)
+      const int shift = max(22 - __clz((f.hi - f.lo) | 1), 0);
+      for (int i = tid; i < kBins; i += kThreads) sh.digits.lo[i] = sh.digits.hi[i] = 0;
       __syncthreads();
+      uint64_t above = 0, rest = 0;  // (the first time)
+      const uint32_t first_key = round ? f.lo : base, last_key = round ? f.hi : most;
 #pragma unroll 1
       for (int i = t0; i < t1; ++i) {
         const uint32_t b = bits_at(i), key = K::of(b);
-        if (key < f.lo || key > f.hi) continue;
-        const int bin = (f.hi - key) >> shift;
-        atomicAdd(&sh.digits.count[bin], 1u);
-        if (weights) {
-          const uint64_t w = exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
+        if (key < first_key || key > last_key) continue;
+        const uint64_t w = numbers ? 1 : exact ? one_weight(K::value(b)) : quick_weight(K::value(b));
+        if (key > f.hi) {
+          above += w;
+        } else if (key < f.lo) {
+          rest += w;
+        } else {
+          const int bin = (f.hi - key) >> shift;
           const uint32_t w_lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.digits.lo[bin], w_lo);
           const uint32_t w_hi = static_cast<uint32_t>(w >> 32) + (old + w_lo < old ? 1u : 0u);
           if (w_hi) atomicAdd(&sh.digits.hi[bin], w_hi);
         }
       }
+      uint64_t all;
+      if (round == 0) {
+        scan(above, all);
+        if (tid == 0) n == 1 ? void(sh.digits.above[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.digits.above[rank]), 0), all);
+        scan(rest, all);
+        if (tid == 0) n == 1 ? void(sh.digits.rest[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.digits.rest[rank]), 0), all);
+      }
       cluster_sync(n);
       // each CTA adds up a share of the bins over all CTAs, for the first one
       const int share = (kBins + n - 1) / n, last = min((rank + 1) * share, kBins);
       for (int bin = rank * share + tid; bin < last; bin += kThreads) {
-        uint32_t c = 0;
-        uint64_t w = 0;
         if (n == 1) {
-          c = sh.digits.count[bin];
-          if (weights) w = static_cast<uint64_t>(sh.digits.hi[bin]) << 32 | sh.digits.lo[bin];
+          sh.digits.all[bin] = static_cast<uint64_t>(sh.digits.hi[bin]) << 32 | sh.digits.lo[bin];
         } else {
-          c = static_cast<uint32_t>(cluster_sum(&sh.digits.count[bin], n));
-          if (weights) w = (cluster_sum(&sh.digits.hi[bin], n) << 32) + cluster_sum(&sh.digits.lo[bin], n);
-        }
-        if (n == 1) {
-          sh.digits.all_count[bin] = c;
-          sh.digits.all_w[bin] = w;
-        } else {
-          st_cluster(mapa_shared(smem_u32(&sh.digits.all_count[bin]), 0), c);
-          st_cluster(mapa_shared(smem_u32(&sh.digits.all_w[bin]), 0), w);
+          const uint64_t w = (cluster_sum(&sh.digits.hi[bin], n) << 32) + cluster_sum(&sh.digits.lo[bin], n);
+          st_cluster(mapa_shared(smem_u32(&sh.digits.all[bin]), 0), w);
         }
       }
       cluster_sync(n);
       if (rank == 0) {
         // sums down to each bin, two a thread
         constexpr int B = kBins / kThreads;
-        uint32_t c[B], cs = 0;
-        uint64_t w[B], ws = 0;
+        uint64_t w[B], sum = 0;
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-          c[j] = sh.digits.all_count[tid * B + j];
-          w[j] = sh.digits.all_w[tid * B + j];
-          cs += c[j];
-          ws += w[j];
+        for (int j = 0; j < B; ++j) sum += w[j] = sh.digits.all[tid * B + j];
+        uint64_t upto = scan(sum, all);
+        if (round == 0) {
+          f.whole = all;
+          for (int r = 0; r < n; ++r) f.above += sh.digits.above[r], f.whole += sh.digits.above[r] + sh.digits.rest[r];
+          // (FP64 is slow: in one thread)
+          if (tid == 0) sh.target = numbers ? number : static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(f.whole)));
+          __syncthreads();
         }
-        uint32_t ci = cs;
-        uint64_t wi = ws;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, ci, o);
-          const uint64_t y = shfl_up(wi, o);
-          if (lane >= o) ci += x, wi += y;
-        }
-        if (lane == 31) sh.warp_u[warp] = ci, sh.warp_w[warp] = wi;
-        __syncthreads();
-        ci += f.above - cs, wi += f.above_w - ws;
-        for (int i = 0; i < warp; ++i) ci += sh.warp_u[i], wi += sh.warp_w[i];
+        upto += f.above;
+        const uint64_t target = sh.target;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           // the range in which the threshold lies: the last one kept
-          const bool here = by_weight ? static_cast<double>(wi) < target && !(static_cast<double>(wi + w[j]) < target)
-                                      : ci < k && ci + c[j] >= k;
-          if (here && c[j]) {
-            const uint32_t hi = f.hi - (static_cast<uint32_t>(tid * B + j) << shift);
-            const uint32_t width = (1u << shift) - 1;
-            tell(Found{hi - f.lo > width ? hi - width : f.lo, hi, ci, 0, wi, wi + w[j]});
+          if (upto < target && upto + w[j] >= target) {
+            const uint32_t to = f.hi - (static_cast<uint32_t>(tid * B + j) << shift), width = (1u << shift) - 1;
+            const uint64_t off = numbers || exact ? 0 : fixed(static_cast<float>(f.whole) / unit * error_of(f.whole, 8.f));
+            sh.found = Found{to - f.lo > width ? to - width : f.lo, to, upto, f.whole, upto + off < target && upto + w[j] >= target + off};
           }
-          ci += c[j], wi += w[j];
+          upto += w[j];
         }
-        if (tid == kThreads - 1 && !by_weight && ci < k) tell(Found{f.lo, f.hi, ci, 1, wi, wi});
+        // (fewer tokens than are asked for: all are kept)
+        if (tid == kThreads - 1 && upto < target) sh.found = Found{base, base, 0, f.whole, 1};
+        __syncthreads();
+        constexpr int WORDS = sizeof(Found) / 8;
+        if (tid >= WORDS && tid < n * WORDS) {
+          uint64_t* word = reinterpret_cast<uint64_t*>(&sh.found) + tid % WORDS;
+          st_cluster(mapa_shared(smem_u32(word), tid / WORDS), *word);
+        }
       }
       cluster_sync(n);
       f = sh.found;
-      if (shift == 0 || f.all) break;
+      if (f.certain) sure = f;
+      if (shift == 0 || f.lo == f.hi || round == 3) return f.certain != 0;
     }
-    return f;
   };
 
+  float sum = 0.f;  // of the tokens that matter, by FP32 weights (0: not known)
   // The token among those whose key is `cut` or more; false if the FP32 weights leave it open.
   auto draw_from = [&](uint32_t cut, bool exact) {
     auto weight_at = [&](int i) -> uint64_t {
@@ -804,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncthreads();
     count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
     const uint64_t total = exchange(all, count, below);
+    if (!exact) sum = static_cast<float>(total) / unit / one;
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
     const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
     before += below;
@@ -829,8 +831,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             a.tokens[row] = first * VEC + i - skip;
             if (a.kept) a.kept[row] = static_cast<int32_t>(count);
             if (a.logprob) {
-              const uint64_t one = exact ? 1ull << (kFixed - a.drop) : quick_weight(m);
-              a.logprob[row] = set.log_of(K::value(bits_at(i)), m, static_cast<float>(total > one ? total - one : 0) / static_cast<float>(one));
+              const uint64_t top_w = exact ? 1ull << (kFixed - scale->drop) : quick_weight(m);
+              a.logprob[row] = set.log_of(K::value(bits_at(i)), m, static_cast<float>(total > top_w ? total - top_w : 0) / static_cast<float>(top_w));
             }
             if (!exact) tell_verdict(kDone);
           }
@@ -845,35 +847,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return sh.verdict == kDone;
   };
 
-  // By FP32 weights first, and by exact ones if they leave a decision open.
-  bool exact = !in_range || (by_p && !by_k && quick_total == 0);
-  for (;;) {
-    uint32_t cut = least;
-    bool open = false;
-    if (by_k || by_p) {
-      uint32_t from = from_key;
-      uint64_t whole = 0;  // weight of all that top-k leaves
-      if (by_k) {
-        const Found f = search(from, false, by_p, k_asked, 0.0, exact);
-        from = f.lo, whole = f.with_w, cut = max(cut, f.lo);
-      } else {
-        whole = exact ? exact_sum() : quick_total;
-      }
-      if (by_p) {
-        const double target = static_cast<double>(p) * static_cast<double>(whole);
-        if (target > 0.0) {
-          const Found f = search(from, true, true, 0, target, exact);
-          cut = max(cut, f.lo);
-          const double off = exact ? 0.0 : static_cast<double>(whole) * static_cast<double>(error_of(whole, 12.f));
-          open = !exact && !(static_cast<double>(f.above_w) + off < target && static_cast<double>(f.with_w) >= target + off);
-        } else {
-          cut = most;
-        }
-      }
+  if (by_k) {
+    Found f;
+    search(K::LOWEST, from_key, most, true, k_asked, true, f);
+    from_key = f.lo;
+  }
+  uint32_t cut = max(least, by_k ? from_key : K::LOWEST);
+  // By FP32 weights first, and by exact ones what they leave open.
+  Found sure{from_key, max(to_key, from_key), 0, 0, 1};
+  bool known = !by_p;
+  if (by_p && !(p > 0.f)) cut = most, known = true;
+  for (bool exact = !in_range;; exact = true) {
+    if (exact) {
+      __syncthreads();
+      if (tid == 0) sh.scale.drop = sum > 0.f ? drop_of(sum, a.drop) : a.drop;
+      __syncthreads();
     }
-    if (!open) open = !draw_from(cut, exact);
-    if (!open) return;
-    exact = true;
+    if (!known) {
+      known = search(by_k ? from_key : K::LOWEST, sure.lo, sure.hi, false, 0, exact, sure);
+      if (known) cut = max(cut, sure.lo);
+      if (!exact) sum = static_cast<float>(sure.whole) / unit / one;
+    }
+    if (known && draw_from(cut, exact)) return;
   }
 }
 

@@ -2,8 +2,9 @@
 //
 // A drawn id is a matter of comparisons, so that it has to be the one of the
 // definition whatever the order of additions: weights are whole numbers of
-// 2^-F (F = 45 for up to 2^17 tokens, one less for each doubling), right to about
-// 2^-43 relative, and sums of them are exact.  e^y is computed in pairs of FP32
+// 2^-F, right to about 2^-43 relative or half a unit, and sums of them are exact.  F is as large as
+// sums below 2^62 allow (45 if 2^17 tokens may weigh 1 each, 61 if all weigh less than 2), so that the roundings of a whole
+// vocabulary are 2^-43 of its weight at most.  e^y is computed in pairs of FP32
 // numbers by a table of 2^(j/32) and a short series (Tang, "Table-driven
 // implementation of the exponential function", 1989): FP64 instructions are
 // sixty times as slow here.
@@ -19,14 +20,14 @@
 namespace dflash {
 
 constexpr int kMaxSplits = 16;       // CTAs of a cluster
-constexpr int kFixed = 45;           // binary places of a weight
+constexpr int kFixed = 45;           // binary places of a weight as it is computed
 constexpr float kMaxTemperature = 0x1p64f;
 
 struct SampleArgs {
   const uint8_t* logits;
   long long row_bytes;
   int n_rows, vocab, splits, pieces;  // pieces: 16-byte pieces of a row that a CTA holds
-  int drop;                           // places less than kFixed
+  int drop;                           // places less than kFixed that sums of any row allow
   const float* uniform;
   const float* temperature;
   const int32_t* top_k;
@@ -84,7 +85,7 @@ struct Scale {
   int drop;
 };
 
-// e^((x - m) / T) in units of 2^-(kFixed - drop), N of them side by side: one is a chain of 40 instructions, and the compiler
+// e^((x - m) / T) in units of 2^-(kFixed - drop), drop >= -16, N of them side by side: one is a chain of 45 instructions, and the compiler
 // does not mix the chains of several by itself (a batch of 32 in a lane: 4.2 us one by one).  Products and sums are written
 // out: the compiler must not contract them.
 template <int N>
@@ -99,8 +100,8 @@ __device__ __forceinline__ void weights(const float (&x)[N], const Scale& c, con
 #define DFLASH_EACH _Pragma("unroll") for (int i = 0; i < N; ++i)
   DFLASH_EACH s[i] = __fadd_rn(x[i], b);  // x - m = s + e exactly
   DFLASH_EACH whole[i] = __fmul_rn(s[i], c.hi);
-  // (Below 2^-48 a weight is 0, a masked value's too: without a branch.)
-  DFLASH_EACH p[i] = fmaxf(whole[i], -56.f);
+  // (2^-72 is 0, as a masked value's weight is: without a branch)
+  DFLASH_EACH p[i] = fmaxf(whole[i], -72.f);
   DFLASH_EACH t[i] = __fadd_rn(p[i], ROUND);
   DFLASH_EACH k[i] = __float_as_int(t[i]) - __float_as_int(ROUND);
   DFLASH_EACH f[i] = table[k[i] & 31];
@@ -132,7 +133,8 @@ __device__ __forceinline__ void weights(const float (&x)[N], const Scale& c, con
   DFLASH_EACH {
     const long long add = (static_cast<long long>(__float_as_int(t1[i]) - __float_as_int(STEP1)) << 22) +
                           (__float_as_int(t2[i]) - __float_as_int(STEP2));
-    w[i] = whole[i] > -48.f ? (f[i].fixed + add) >> (c.drop - (k[i] >> 5)) : 0;
+    const int places = c.drop + 17 - (k[i] >> 5), right = min(places, 63);  // (1 or more)
+    w[i] = places < 64 ? (((f[i].fixed + add) << 17) + (1ull << (right - 1))) >> right : 0;
   }
 #undef DFLASH_EACH
 }
@@ -212,27 +214,6 @@ struct Keys {
     using E = Elem<TYPE>;
     return E::max_of(E::max_words(E::max_words(v.x, v.y), E::max_words(v.z, v.w)));
   }
-  // FP32 weights of a piece
-  static __device__ __forceinline__ float quick_sum(const uint4& v, float m, float c) {
-    constexpr int VEC = Elem<TYPE>::VEC;
-    float x[VEC];
-    Elem<TYPE>::widen(v, x);
-    const uint64_t minus = pack2(-m, -m), c2 = pack2(c, c);
-    uint64_t s[VEC / 2];
-#pragma unroll
-    for (int e = 0; e < VEC; e += 2) {
-      float y0, y1;
-      unpack2(mul2(add2(pack2(x[e], x[e + 1]), minus), c2), y0, y1);
-      s[e / 2] = pack2(ex2_approx(y0), ex2_approx(y1));
-    }
-#pragma unroll
-    for (int o = VEC / 4; o; o >>= 1)
-#pragma unroll
-      for (int e = 0; e < o; ++e) s[e] = add2(s[e], s[e + o]);
-    float s0, s1;
-    unpack2(s[0], s0, s1);
-    return s0 + s1;
-  }
   // FP32 sum of 2^(x c + k) of a piece: an exponent is rounded once.  (Pairs of values in one instruction
   // take fewer instructions and more time: 65 us instead of 59 for 1000 rows of 151936.)
   static __device__ __forceinline__ float quick_sum_from(const uint4& v, float c, float k) {
@@ -247,10 +228,9 @@ struct Keys {
       for (int e = 0; e < o; ++e) x[e] += x[e + o];
     return x[0];
   }
-  // exact weight of a piece's values whose key is `least` or more (CALL: by calls, else four side by side)
-  template <bool CALL>
-  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, uint32_t least, const Scale* c, const TableEntry* table) {
-    constexpr int VEC = Elem<TYPE>::VEC, N = CALL ? 1 : 4;
+  // exact weight of a piece's values, four side by side
+  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, const Scale& c, const TableEntry* table) {
+    constexpr int VEC = Elem<TYPE>::VEC, N = 4;
     uint64_t sum = 0;
 #pragma unroll
     for (int e0 = 0; e0 < VEC; e0 += N) {
@@ -258,29 +238,22 @@ struct Keys {
       uint64_t w[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] = value(bits(v, e0 + e));
-      if constexpr (CALL) {
-        w[0] = weight_by_call(x[0], c, table);
-      } else {
-        weights(x, *c, table, w);
-      }
+      weights(x, c, table, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum += of(bits(v, e0 + e)) >= least ? w[e] : 0;
+      for (int e = 0; e < N; ++e) sum += w[e];
     }
     return sum;
   }
   // The first value of a piece (the same in all lanes) with which the exact weights from `from` on exceed `place`: the lane
   // that has it.  Each lane has one value.
-  template <bool CALL>
-  static __device__ __forceinline__ bool exact_find(const uint4& v, uint32_t least, uint64_t from, uint64_t place, const Scale* c,
+  static __device__ __forceinline__ bool exact_find(const uint4& v, uint64_t from, uint64_t place, const Scale& c,
                                                     const TableEntry* table, int lane, float& x) {
     constexpr int VEC = Elem<TYPE>::VEC;
     uint32_t b = SIGN | INF;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) b = lane == e ? bits(v, e) : b;
     x = value(b);
-    uint64_t w = CALL ? weight_by_call(x, c, table) : weight(x, *c, table);
-    if (lane >= VEC || of(b) < least) w = 0;
-    uint64_t upto = w;
+    uint64_t upto = lane < VEC ? weight(x, c, table) : 0;
 #pragma unroll
     for (int o = 1; o < VEC; o <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -381,6 +354,10 @@ struct Settings {
   // ln(w / total) of a token, where the largest weight, 1, is among those of the total: `others` are the total less 1
   __device__ __forceinline__ float log_of(float x, float m, float others) const { return (x - m) / temperature - log1pf(others); }
 };
+// The places less than kFixed of the weights of tokens that weigh `sum` together, as FP32 sums have it.
+__device__ __forceinline__ int drop_of(float sum, int most) {
+  return min(max((__float_as_int(sum * (1.f + 0x1p-9f)) >> 23) - 127, 0) - 16, most);
+}
 __device__ __forceinline__ float others_of(uint64_t total, int drop) {
   return static_cast<float>(total - (1ull << (kFixed - drop))) * exp2f(static_cast<float>(drop - kFixed));
 }

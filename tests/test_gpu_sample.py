@@ -115,6 +115,52 @@ def test_few_levels(R, kind):
     assert R.sample_tokens(zeros, floats([0.0] * 4), floats([0.0, 1, 1, 1]), top_k=ints([0, 1, 0, 5]))[0].tolist() == [0] * 4
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [2000, 40000, 151936, 2 ** 19 - 3])
+def test_flat_rows(R, kind, vocab):
+    """Nuclei, numbers and least weights that keep hundreds of tokens to all but a few: lists of each length, and rows without one."""
+    rng = np.random.default_rng(vocab)
+    n = 24
+    x = logits(rng, n, vocab, kind, np.exp(rng.uniform(np.log(0.02), np.log(0.5), (n, 1))))
+    p = 1 - np.exp(rng.uniform(np.log(1e-8), np.log(0.9), n))
+    k = np.exp(rng.uniform(np.log(100), np.log(vocab), n)).astype(int)
+    low = np.exp(-np.exp(rng.uniform(np.log(0.02), np.log(12), n)))
+    u, t = rng.random(n), rng.uniform(0.5, 2, n)
+    for kw in (dict(top_p=p), dict(top_k=k), dict(min_p=low), dict(top_p=p, top_k=k), dict(top_p=p, min_p=low), dict(top_k=k, min_p=low),
+               dict(top_p=p, top_k=k, min_p=low)):
+        check(R, x, u, t, **kw)
+
+
+@pytest.mark.parametrize("sizes", [(1, 128), (129, 256), (257, 511), (512, 1024), (1025, 1400)])
+def test_lists(R, sizes):
+    """As many tokens as named stand out: those that a filter's list takes in."""
+    rng = np.random.default_rng(sizes[0])
+    n, vocab = 32, 60000
+    v = rng.uniform(-30, -20, (n, vocab))
+    for i, c in enumerate(np.linspace(*sizes, n).astype(int)):
+        v[i, rng.permutation(vocab)[:c]] = rng.uniform(0, 1, c)
+    x = torch.as_tensor(v, device="cuda").float()
+    u = rng.random(n)
+    size = np.linspace(*sizes, n).astype(int)
+    for kw in (dict(top_p=np.full(n, 0.999)), dict(top_k=size), dict(min_p=np.full(n, 0.05)), dict(top_k=size, top_p=rng.uniform(0.5, 1, n)),
+               dict(top_p=rng.uniform(0.5, 1, n), min_p=rng.uniform(0.3, 0.6, n)), dict(top_k=np.maximum(size - 1, 1), min_p=rng.uniform(0.3, 0.6, n))):
+        _, _, kept = check(R, x, u, None, **kw)
+        assert kept.max() <= sizes[1]
+
+
+@pytest.mark.parametrize("offset", [-2.0 ** 13, 2.0 ** 13, 2.0 ** 16])
+def test_logits_far_from_zero(R, offset):
+    """A common addend that FP32 weights of 2^(x c + k) hardly bear: k is off by percents, or out of its range."""
+    rng = np.random.default_rng(abs(int(offset)))
+    n, vocab = 24, 30000
+    x = (torch.as_tensor(rng.standard_normal((n, vocab)) * rng.uniform(0.02, 0.5, (n, 1)), device="cuda") + offset).float()
+    t = np.exp(rng.uniform(np.log(0.012), np.log(0.3), n))
+    p = 1 - np.exp(rng.uniform(np.log(1e-5), np.log(0.9), n))
+    for kw in ({}, dict(top_p=p), dict(top_k=rng.integers(1, 3000, n), top_p=p), dict(min_p=np.exp(-rng.uniform(0, 12, n))),
+               dict(top_p=p, min_p=np.exp(-rng.uniform(0, 12, n)))):
+        check(R, x, rng.random(n), t, **kw)
+
+
 def test_draws_follow_the_distribution(R):
     """Evenly spaced numbers draw each token as often as its weight says, to one draw."""
     rng = np.random.default_rng(5)
