@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   };
 
-  float sum = 0.f;  // of the tokens that matter, by FP32 weights (0: not known)
+  float weight_of_all = 0.f;  // of the tokens that matter, by FP32 weights (0: not known)
   // The token among those whose key is `cut` or more; false if the FP32 weights leave it open.
   auto draw_from = [&](uint32_t cut, bool exact) {
     auto weight_at = [&](int i) -> uint64_t {
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncthreads();
     count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
     const uint64_t total = exchange(all, count, below);
-    if (!exact) sum = static_cast<float>(total) / unit / one;
+    if (!exact) weight_of_all = static_cast<float>(total) / unit / one;
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
     const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
     before += below;
@@ -860,13 +860,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   for (bool exact = !in_range;; exact = true) {
     if (exact) {
       __syncthreads();
-      if (tid == 0) sh.scale.drop = sum > 0.f ? drop_of(sum, a.drop) : a.drop;
+      if (tid == 0) sh.scale.drop = weight_of_all > 0.f ? drop_of(weight_of_all, a.drop) : a.drop;
       __syncthreads();
     }
     if (!known) {
       known = search(by_k ? from_key : K::LOWEST, sure.lo, sure.hi, false, 0, exact, sure);
       if (known) cut = max(cut, sure.lo);
-      if (!exact) sum = static_cast<float>(sure.whole) / unit / one;
+      if (!exact) weight_of_all = static_cast<float>(sure.whole) / unit / one;
     }
     if (known && draw_from(cut, exact)) return;
   }
