@@ -857,19 +857,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   Found sure{from_key, max(to_key, from_key), 0, 0, 1};
   bool known = !by_p;
   if (by_p && !(p > 0.f)) cut = most, known = true;
-  for (bool exact = !in_range;; exact = true) {
-    if (exact) {
-      __syncthreads();
-      if (tid == 0) sh.scale.drop = weight_of_all > 0.f ? drop_of(weight_of_all, a.drop) : a.drop;
-      __syncthreads();
-    }
-    if (!known) {
-      known = search(by_k ? from_key : K::LOWEST, sure.lo, sure.hi, false, 0, exact, sure);
-      if (known) cut = max(cut, sure.lo);
-      if (!exact) weight_of_all = static_cast<float>(sure.whole) / unit / one;
-    }
-    if (known && draw_from(cut, exact)) return;
+  auto exact_from_here = [&]() {
+    __syncthreads();
+    if (tid == 0) sh.scale.drop = weight_of_all > 0.f ? drop_of(weight_of_all, a.drop) : a.drop;
+    __syncthreads();
+  };
+  for (bool exact = !in_range; !known; exact = true) {
+    if (exact) exact_from_here();
+    known = search(by_k ? from_key : K::LOWEST, sure.lo, sure.hi, false, 0, exact, sure) || exact;
+    if (!exact) weight_of_all = static_cast<float>(sure.whole) / unit / one;
   }
+  if (by_p && p > 0.f) cut = max(cut, sure.lo);
+  if (in_range && draw_from(cut, false)) return;
+  exact_from_here();
+  draw_from(cut, true);
 }
 
 // CTAs per row: as many as its bytes need for two CTAs on an SM, more until every SM has one or a CTA has

@@ -309,6 +309,29 @@ def test_graphs_and_streams(R):
     c.check(R, got=outs[0][: c.tokens])
 
 
+def test_calls_behind_one_another(R):
+    """Different calls that share a workspace, one behind the other without a wait, calls without a prefix between them."""
+    rng = np.random.default_rng(31)
+    cases = [Case(R, 11, 128, 2, 4, [(3000, uneven(rng, 9, 500, 1))], 16, False, "bf16"),
+             Case(R, 12, 128, 2, 4, [(40, [(3, 1)]), (0, uneven(rng, 3, 90, 5))], 16, False, "bf16"),
+             Case(R, 13, 128, 2, 9, [(1200, uneven(rng, 12, 300, 8)), (700, uneven(rng, 30, 40, 8))], 16, False, "bf16"),
+             Case(R, 14, 128, 2, 9, [(9000, [(0, 1)])], 16, False, "bf16")]
+    want = [c.run(R) for c in cases]
+    held = [c.args() for c in cases]
+    space = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        k = int(rng.integers(4))
+        got.append((k, R.kv4_prefix_attention(*held[k], workspace=space)))
+        if i % 5 == 4:
+            cache, q, _, _, _, table, own, off, most = held[k][:9]
+            R.kv4_attention(cache, q, table, own, off, most, workspace=space)
+    torch.cuda.synchronize()
+    for k, o in got:
+        assert torch.equal(o[: cases[k].tokens], want[k])
+
+
 def test_most_groups_and_sequences(R):
     rng = np.random.default_rng(1)
     Case(R, 5, 64, 1, 2, [(int(rng.integers(0, 40)), [(int(rng.integers(1, 20)), 1)]) for _ in range(1024)], 16, False).check(R)

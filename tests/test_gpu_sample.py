@@ -293,6 +293,109 @@ def test_graph_and_stream(R):
         assert out[0].tolist() == token.tolist() and out[2].tolist() == kept.tolist()
 
 
+def raw(R, x, u, tokens, logprob=None, kept=None, **kw):
+    at = lambda v: 0 if v is None else v.data_ptr()  # noqa: E731
+    D.dflash_sample_tokens(x.data_ptr(), {torch.float32: D.DFLASH_T_FP32, torch.bfloat16: D.DFLASH_T_BF16, torch.float16: D.DFLASH_T_FP16}[x.dtype],
+                           x.stride(0), x.shape[0], x.shape[1], u.data_ptr(), at(kw.get("temperature")), at(kw.get("top_k")), at(kw.get("top_p")),
+                           at(kw.get("min_p")), at(tokens), at(logprob), at(kept), 0, torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(3000, 1024), (700, 32768), (40, 2 ** 18)])
+def test_numbers_on_a_border(R, kind, n, vocab):
+    """u on the border of two tokens in every row: 2^-k of equal weights is exact, and the token behind the border is the one.  With and
+    without the outputs that may be left out."""
+    x = torch.full((n, vocab), 1.5, dtype=TYPES[kind], device="cuda")
+    want = torch.as_tensor(np.random.default_rng(n).integers(0, vocab, n), device="cuda").int()
+    u = want.float() / vocab
+    hot = x.clone()
+    hot[:, ::2] = -INF  # half of them are left
+    for y, factor in ((x, 1), (hot, 2)):
+        token, logp, kept = R.sample_tokens(y, u)
+        right = want if factor == 1 else want // 2 * 2 + 1
+        assert torch.equal(token, right) and kept.tolist() == [vocab // factor] * n
+        assert np.allclose(logp.cpu().numpy(), -np.log(vocab // factor), rtol=2.0 ** -22, atol=0)
+        for outs in ({}, dict(logprob=logp), dict(kept=kept)):
+            for o in outs.values():
+                o.fill_(7)
+            token.fill_(7)
+            raw(R, y, u, token, **outs)
+            assert torch.equal(token, right)
+            assert all(not bool((o == 7).any()) for o in outs.values())
+
+
+@pytest.mark.parametrize("kind", ["fp32", "fp16"])
+def test_outputs_left_out(R, kind):
+    rng = np.random.default_rng(21)
+    x = logits(rng, 30, 20011, kind, np.exp(rng.uniform(-3, 0, (30, 1))))
+    u = floats(rng.random(30))
+    for kw in ({}, dict(top_k=ints(rng.integers(1, 3000, 30))), dict(top_p=floats(rng.uniform(0.5, 1, 30))), dict(min_p=floats(rng.uniform(0.01, 1, 30))),
+               dict(temperature=floats(np.zeros(30)), top_k=ints(np.ones(30)))):
+        token, logp, kept = R.sample_tokens(x, u, **kw)
+        for outs in ({}, dict(logprob=torch.empty_like(logp)), dict(kept=torch.empty_like(kept))):
+            t = torch.empty_like(token)
+            raw(R, x, u, t, **outs, **kw)
+            assert torch.equal(t, token)
+            assert all(torch.equal(o, dict(logprob=logp, kept=kept)[k]) for k, o in outs.items())
+
+
+def test_calls_at_once(R):
+    """Calls with and without filters on three streams, and one behind the other on each."""
+    rng = np.random.default_rng(17)
+    cases = []
+    for i, (n, vocab, kind) in enumerate([(300, 2 ** 15, "fp32"), (64, 50000, "bf16"), (9, 151936, "fp16")]):
+        x = logits(rng, n, vocab, kind, np.exp(rng.uniform(-3, 0, (n, 1))))
+        if i == 0:
+            x[::2] = 0.5  # equal weights: u on a border
+        u = floats(np.round(rng.random(n) * 2 ** 15 - 0.5) / 2 ** 15)
+        for kw in ({}, dict(top_p=floats(rng.uniform(0.5, 1, n))), dict(top_k=ints(rng.integers(1, 4000, n)))):
+            cases.append((x, u, kw, R.sample_tokens(x, u, **kw)))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for i in range(len(cases)):
+            x, u, kw, want = cases[(i * 4) % len(cases)]
+            with torch.cuda.stream(streams[i % 3]):
+                got.append((R.sample_tokens(x, u, **kw), want))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(v, w) for v, w in zip(a, b))
+
+
+def test_graph_without_filters(R):
+    """Two captured calls replayed on two streams, rows that their second kernel decides among them."""
+    rng = np.random.default_rng(23)
+    held = []
+    for n, vocab, kind in ((500, 4096, "fp32"), (20, 100003, "bf16")):
+        x, u = logits(rng, n, vocab, kind), floats(rng.random(n))
+        R.sample_tokens(x, u)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = R.sample_tokens(x, u)
+        held.append((g, x, u, out))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        for g, x, u, out in held:
+            x.copy_(logits(rng, *x.shape, "fp32"))
+            x[::3] = -0.25
+            u.copy_(floats(np.floor(rng.random(len(u)) * 4096) / 4096))
+        torch.cuda.synchronize()
+        for s, (g, *_) in zip(streams, held):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for g, x, u, out in held:
+            token, _, kept, near = S.sample(x.double().cpu().numpy(), u.cpu().numpy())
+            clear = near > 2.0 ** -42
+            assert clear.sum() > len(u) // 2 and out[2].tolist() == kept.tolist()
+            assert np.array_equal(out[0].cpu().numpy()[clear], token[clear])
+        equal = held[0][1].shape[1]  # (a power of two: the token is known there too)
+        assert held[0][3][0][::3].tolist() == (held[0][2][::3] * equal).int().tolist()
+
+
 def test_no_rows(R):
     token, logp, kept = R.sample_tokens(torch.zeros((0, 50), device="cuda"), floats(np.zeros(0)))
     assert token.shape == logp.shape == kept.shape == (0,)
