@@ -39,6 +39,7 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 1024;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
+constexpr int kPerSm = 2;                  // CTAs
 constexpr int kList = 1024;                // tokens that the first CTA sorts
 constexpr int kOwn = kList / kWarps;       // of a warp
 constexpr int kFew = 256;                  // tokens that it compares each with each
@@ -58,7 +59,6 @@ struct Shared {
     struct {
       uint32_t lo[kBins], hi[kBins];  // weights of this CTA's tokens, in two words
       uint64_t all[kBins];            // of the cluster's, in its first CTA
-      uint64_t above[kMaxSplits], rest[kMaxSplits];  // the CTAs' outside of all ranges
     } digits;
     struct {
       uint64_t own[kWarps][kOwn];  // (key, id) of each warp's tokens, in order of ids
@@ -72,6 +72,7 @@ struct Shared {
   TableEntry table[32];
   Found found;
   uint64_t cta_w[kMaxSplits], warp_w[kWarps];
+  uint64_t cta_above[kMaxSplits], cta_rest[kMaxSplits];  // weights outside of the ranges, in the first CTA
   uint32_t cta_top[kMaxSplits], cta_low[kMaxSplits], cta_n[kMaxSplits], cta_c[kMaxSplits], warp_u[kWarps], warp_low[kWarps], warp_n[kWarps];
   float warp_f[kWarps];
   double log_min_p;
@@ -82,12 +83,15 @@ struct Shared {
   int where;      // the values in which u lies, and the weight before them
   uint64_t from;
 };
+// (a CTA that goes on to the digits leaves a slower one its histogram)
+static_assert(offsetof(Shared, quick.hist) >= sizeof(Shared::digits), "the digits lie before the histogram");
+static_assert(kList <= 64 * kWarps && kFew <= kThreads / 2, "a warp sorts 64 tokens, two threads compare one");
 constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
 // What the first CTA (or the one that u names) says of a quick answer.
 enum Verdict : uint32_t { kDone, kExactSum, kDigits };
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
   constexpr int VEC = E::VEC;
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (i < warp) x += y;
           every += y;
         }
-        const float over = every * (1.f + 0x1p-13f) - x;  // the ranges above this one, at most (544 roundings)
+        const float over = every * (1.f + 0x1p-13f) - x;  // the ranges above this one, at most (2^-13: more than all roundings)
         x += rest * 0.25f;
         // (2^-10: more than the sums and ranges are off; the FP32 weights are relative to 2^(m c + k))
         const float sum = static_cast<float>(quick_total) / unit / one, whole = sum * (1.f - 0x1p-10f);
@@ -725,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       uint64_t all;
       if (round == 0) {
         scan(above, all);
-        if (tid == 0) n == 1 ? void(sh.digits.above[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.digits.above[rank]), 0), all);
+        if (tid == 0) n == 1 ? void(sh.cta_above[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.cta_above[rank]), 0), all);
         scan(rest, all);
-        if (tid == 0) n == 1 ? void(sh.digits.rest[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.digits.rest[rank]), 0), all);
+        if (tid == 0) n == 1 ? void(sh.cta_rest[0] = all) : st_cluster(mapa_shared(smem_u32(&sh.cta_rest[rank]), 0), all);
       }
       cluster_sync(n);
       // each CTA adds up a share of the bins over all CTAs, for the first one
@@ -750,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         uint64_t upto = scan(sum, all);
         if (round == 0) {
           f.whole = all;
-          for (int r = 0; r < n; ++r) f.above += sh.digits.above[r], f.whole += sh.digits.above[r] + sh.digits.rest[r];
+          for (int r = 0; r < n; ++r) f.above += sh.cta_above[r], f.whole += sh.cta_above[r] + sh.cta_rest[r];
           // (FP64 is slow: in one thread)
           if (tid == 0) sh.target = numbers ? number : static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(f.whole)));
           __syncthreads();
@@ -874,14 +878,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 }
 
 // CTAs per row: as many as its bytes need for two CTAs on an SM, more until every SM has one or a CTA has
-// little left.
+// little left.  (A row takes its CTAs 12 to 15 us, of which its bytes are on their way for 3 to 5.  256 rows of 151936 FP16 values,
+// the 50 largest of each, calls in a row: 63 us with two CTAs of 512 threads, 66 with four of 256, which are better with cold
+// caches, 62 to 69, and for 128 FP32 rows of 100003, 88 to 91, but worse for a block of 8 rows, 34 to 28.)
 constexpr int kSmemOfSm = 228 * 1024;
 cudaError_t splits_of(int n_rows, long long row_pieces, int* splits, int* pieces) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  constexpr long long fits = (kSmemOfSm / 2 - 1024 - kSharedBytes) / 16;
+  constexpr long long fits = (kSmemOfSm / kPerSm - 1024 - kSharedBytes) / 16;
   long long s = (row_pieces + fits - 1) / fits;
   if (s > kMaxSplits) s = kMaxSplits;
   while (2 * s <= kMaxSplits && n_rows * s < sms && row_pieces > 2 * kThreads * s) s *= 2;
