@@ -17,7 +17,7 @@
 //    compares them (or sorts them) and decides everything with exact weights.  S itself, which a top-p without top-k
 //    compares with, comes from FP32 sums; where their error leaves it open which token is the last, S is added up exactly.
 // Else (long lists) a threshold is found digit by digit: counts (and weights) of up to
-// 1024 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key; and the token by
+// 2048 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key; and the token by
 // the sums of the CTAs, warps and lanes.  FP32 weights do first, in whole numbers, whose sums are exact, and exact ones if those leave a
 // decision open: whether a border of the token, or of the last key, lies within their error of what it is compared with.
 //
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBins = 1024;
+constexpr int kBins = 2048;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kPerSm = 2;                  // CTAs
 constexpr int kList = 1024;                // tokens that the first CTA sorts
@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
   // the errors of the weights; true if it is the last.
   auto search = [&](uint32_t base, uint32_t lo, uint32_t hi, bool numbers, uint64_t number, bool exact, Found& sure) {
     Found f{lo, hi, 0, 0, 1};
-    for (int round = 0;; ++round) {  // (ten bits a round)
-      const int shift = max(22 - __clz((f.hi - f.lo) | 1), 0);
+    for (int round = 0;; ++round) {  // (eleven bits a round)
+      const int shift = max(21 - __clz((f.hi - f.lo) | 1), 0);
       for (int i = tid; i < kBins; i += kThreads) sh.digits.lo[i] = sh.digits.hi[i] = 0;
       __syncthreads();
       uint64_t above = 0, rest = 0;  // (the first time)
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
       }
       cluster_sync(n);
       if (rank == 0) {
-        // sums down to each bin, two a thread
+        // sums down to each bin, four a thread
         constexpr int B = kBins / kThreads;
         uint64_t w[B], sum = 0;
 #pragma unroll
