@@ -30,6 +30,7 @@ constexpr int kStages = 2;  // batches of a warp on their way
 constexpr int kRingBytes = kWarps * kStages * kBatchBytes;
 constexpr int kRestCtas = 8;         // CTAs for a row that the FP32 sums leave open
 constexpr int32_t kClaimed = -2, kUndecided = -3;  // the token of such a row, between the kernels: kUndecided less the places (plus 16) that its weights have less
+constexpr int kRestWarps = 8, kRestThreads = 32 * kRestWarps, kRestLoads = 2;  // of its CTAs
 constexpr int kMaxBatches = (1 << 19) * 4 / kBatchBytes + 1;  // (a row may begin inside a piece)
 
 // The largest of the warp's values (no NaN among them).
@@ -47,18 +48,18 @@ __device__ __forceinline__ T warp_upto(T v, int lane) {
 }
 
 // A lane's pieces of a batch of a row.
-template <int TYPE>
+template <int TYPE, int LOADS>
 __device__ __forceinline__ void load_batch(const uint8_t* src, const uint4* frame, int skip, int places, int vocab, int b, int lane,
-                                           uint4 (&v)[kLoads]) {
+                                           uint4 (&v)[LOADS]) {
   using E = Elem<TYPE>;
-  constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
+  constexpr int VEC = E::VEC, BATCH = 32 * LOADS * VEC;
   const int p0 = b * BATCH;
   if (p0 >= skip && p0 + BATCH <= places) {
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) v[j] = __ldg(frame + p0 / VEC + j * 32 + lane);
+    for (int j = 0; j < LOADS; ++j) v[j] = __ldg(frame + p0 / VEC + j * 32 + lane);
   } else {  // the row's ends: value by value
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
+    for (int j = 0; j < LOADS; ++j) {
       const long long i = p0 + (j * 32 + lane) * VEC - skip;
       constexpr int W = VEC / 4;  // values of a word
       v[j].x = E::raw(src, i, vocab);
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   const int batches = (places + BATCH - 1) / BATCH;
   // this CTA's batches
   const int b0 = static_cast<int>(static_cast<long long>(batches) * rank / n), b1 = static_cast<int>(static_cast<long long>(batches) * (rank + 1) / n);
-  auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
+  auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE, kLoads>(src, frame, skip, places, a.vocab, b, lane, v); };
   // whole batches come through the warp's ring by bulk copies, those at the row's ends by loads
   auto inside = [&](int b) { return b * BATCH >= skip && b * BATCH + BATCH <= places; };
   uint8_t* mine_ring = ring + warp * kStages * kBatchBytes;
@@ -357,15 +358,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
 // Rows that the sums left open: exact ones, by clusters of kRestCtas.  A CTA has a part of the row's batches, which it reads twice: for the largest value (and the
 // tokens that are not masked), and for the weights.
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
-  constexpr int VEC = E::VEC, BATCH = 32 * kLoads * VEC;
-  __shared__ uint64_t part[kMaxBatches / kRestCtas + 2];  // of this CTA's batches
+  constexpr int VEC = E::VEC, BATCH = 32 * kRestLoads * VEC;  // (not the first kernel's batches)
+  __shared__ uint64_t part[(1 << 19) * 4 / (512 * kRestLoads) / kRestCtas + 2];  // of this CTA's batches
   __shared__ TableEntry table[32];
   __shared__ Scale s_scale;
-  __shared__ uint64_t s_wide[kWarps], cta_wide[kRestCtas];
-  __shared__ uint32_t s_key[kWarps], s_count[kWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[4 * kWarps];
+  __shared__ uint64_t s_wide[kRestWarps], cta_wide[kRestCtas];
+  __shared__ uint32_t s_key[kRestWarps], s_count[kRestWarps], cta_key[kRestCtas], cta_count[kRestCtas], s_open[4 * kRestWarps];
   __shared__ int s_batch, s_row, s_drop, s_told, s_told_drop;
   __shared__ uint64_t s_from;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
   pdl_wait();
   // The clusters begin at different rows, and a row belongs to the one that changes its mark.
   constexpr int LOOK = 4;  // rows of a thread at a time
-  const int chunks = (a.n_rows + LOOK * kThreads - 1) / (LOOK * kThreads);
+  const int chunks = (a.n_rows + LOOK * kRestThreads - 1) / (LOOK * kRestThreads);
   int chunk = static_cast<int>(static_cast<long long>(chunks) * cluster / clusters), seen = 0;
   for (;;) {
     if (rank == 0) {
@@ -391,18 +392,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         unsigned open[LOOK];
 #pragma unroll
         for (int i = 0; i < LOOK; ++i) {
-          const int mine = (chunk * LOOK + i) * kThreads + tid;
+          const int mine = (chunk * LOOK + i) * kRestThreads + tid;
           open[i] = __ballot_sync(0xffffffffu, mine < a.n_rows && __ldcg(a.tokens + mine) <= kUndecided);
         }
         __syncthreads();  // s_row and s_open of the last round have been read
-        if (lane < LOOK) s_open[lane * kWarps + warp] = lane == 0 ? open[0] : lane == 1 ? open[1] : lane == 2 ? open[2] : open[3];
+        if (lane < LOOK) s_open[lane * kRestWarps + warp] = lane == 0 ? open[0] : lane == 1 ? open[1] : lane == 2 ? open[2] : open[3];
         if (tid == 0) s_row = -1;
         __syncthreads();
         if (tid == 0) {
-          for (int i = 0; i < LOOK * kWarps && s_row < 0; ++i) {
-            const int w = (i + cluster) % (LOOK * kWarps);
+          for (int i = 0; i < LOOK * kRestWarps && s_row < 0; ++i) {
+            const int w = (i + cluster) % (LOOK * kRestWarps);
             for (unsigned left = s_open[w]; left && s_row < 0; left &= left - 1) {
-              const int r = chunk * LOOK * kThreads + w * 32 + __ffs(left) - 1;
+              const int r = chunk * LOOK * kRestThreads + w * 32 + __ffs(left) - 1;
               const int32_t mark = __ldcg(a.tokens + r);
               if (mark <= kUndecided && atomicCAS(a.tokens + r, mark, kClaimed) == mark) s_row = r, s_drop = kUndecided - 16 - mark;
             }
@@ -430,18 +431,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         const int places = a.vocab + skip;
         const int batches = (places + BATCH - 1) / BATCH;
         const int b0 = batches * rank / kRestCtas, b1 = batches * (rank + 1) / kRestCtas;
-        auto load = [&](int b, uint4 (&v)[kLoads]) { load_batch<TYPE>(src, frame, skip, places, a.vocab, b, lane, v); };
+        auto load = [&](int b, uint4 (&v)[kRestLoads]) { load_batch<TYPE, kRestLoads>(src, frame, skip, places, a.vocab, b, lane, v); };
         float m;
         uint32_t all;
         if (a.logprob && a.kept) {  // left there by the first kernel
           m = __ldcg(a.logprob + row), all = static_cast<uint32_t>(__ldcg(a.kept + row));
         } else {
           uint32_t tops = E::NOTHING, count = 0;
-          for (int b = b0 + warp; b < b1; b += kWarps) {
-            uint4 v[kLoads];
+          for (int b = b0 + warp; b < b1; b += kRestWarps) {
+            uint4 v[kRestLoads];
             load(b, v);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
+            for (int j = 0; j < kRestLoads; ++j) {
               tops = E::max_words(tops, E::max_words(E::max_words(v[j].x, v[j].y), E::max_words(v[j].z, v[j].w)));
               count += K::unmasked(v[j]);
             }
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
           if (tid < kRestCtas) {
             uint32_t x = 0, y = 0;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) x = max(x, s_key[i]), y += s_count[i];
+            for (int i = 0; i < kRestWarps; ++i) x = max(x, s_key[i]), y += s_count[i];
             put(&cta_key[rank], x, tid);
             put(&cta_count[rank], y, tid);
           }
@@ -468,30 +469,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         if (tid == 0) s_scale.m = m;
         __syncthreads();
         const Scale& scale = s_scale;
-        for (int b = b0 + warp; b < b1; b += kWarps) {
-          uint4 v[kLoads];
-          load(b, v);
+        uint4 next[kRestLoads];
+        if (b0 + warp < b1) load(b0 + warp, next);
+        for (int b = b0 + warp; b < b1; b += kRestWarps) {
+          uint4 v[kRestLoads];
+#pragma unroll
+          for (int j = 0; j < kRestLoads; ++j) v[j] = next[j];
+          if (b + kRestWarps < b1) load(b + kRestWarps, next);
           uint64_t sum = 0;
-          // (not unrolled, here and below: 32 weights in line are 30 KB of instructions that are fetched for each batch)
+          // (not unrolled, here and below: the weights of a batch in line are many KB of instructions that are fetched for each)
 #pragma unroll 1
-          for (int j = 0; j < kLoads; ++j) {
+          for (int j = 0; j < kRestLoads; ++j) {
             sum += K::exact_sum(v[0], scale, table);
-            v[0] = v[1], v[1] = v[2], v[2] = v[3];
+            v[0] = v[1];
           }
-          static_assert(kLoads == 4, "pieces");
+          static_assert(kRestLoads == 2, "pieces");
           sum = warp_sum(sum);
           if (lane == 0) part[b - b0] = sum;
         }
         __syncthreads();
-        // (a thread has a batch: a CTA has fewer)
-        static_assert(kMaxBatches / kRestCtas + 1 <= kThreads, "batches");
-        const uint64_t own = tid < b1 - b0 ? part[tid] : 0;
+        // a thread has two neighbours
+        static_assert(sizeof(part) / 8 <= 2 * kRestThreads, "batches");
+        const int mine = 2 * tid;
+        const uint64_t first = mine < b1 - b0 ? part[mine] : 0, own = first + (mine + 1 < b1 - b0 ? part[mine + 1] : 0);
         const uint64_t upto = warp_upto(own, lane);
         if (lane == 31) s_wide[warp] = upto;
         __syncthreads();
         uint64_t before = upto - own, cta = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
+        for (int i = 0; i < kRestWarps; ++i) {
           if (i < warp) before += s_wide[i];
           cta += s_wide[i];
         }
@@ -508,15 +514,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
         const uint64_t place = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(whole));
         if (place >= below && place < below + cta) {  // (one CTA)
           before += below;
-          if (before <= place && place < before + own) s_batch = b0 + tid, s_from = before;  // (one thread)
+          if (before <= place && place < before + own) {  // (one thread)
+            const bool second = place >= before + first;
+            s_batch = b0 + mine + second, s_from = before + (second ? first : 0);
+          }
           __syncthreads();
           if (warp == 0) {
-            uint4 v[kLoads];
+            uint4 v[kRestLoads];
             const int b = s_batch;
             load(b, v);
             uint64_t from = s_from;
 #pragma unroll 1
-            for (int j = 0; j < kLoads; ++j) {
+            for (int j = 0; j < kRestLoads; ++j) {
               const uint64_t w = K::exact_sum(v[0], scale, table), upto = warp_upto(w, lane);
               const unsigned over = __ballot_sync(0xffffffffu, from + upto > place);
               if (over) {  // (the same for the warp)
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rest_kernel(const SampleAr
                 break;
               }
               from += __shfl_sync(0xffffffffu, upto, 31);
-              v[0] = v[1], v[1] = v[2], v[2] = v[3];
+              v[0] = v[1];
             }
           }
         }
@@ -574,6 +583,7 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, sample_plain_kernel<TYPE>, a);
   if (e != cudaSuccess) return e;
   const int most = 2 * sms / kRestCtas;  // two CTAs per SM
+  cfg.blockDim = dim3(kRestThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_rows < most ? a.n_rows : most) * kRestCtas);
   attr[0].val.clusterDim.x = kRestCtas;
