@@ -10,7 +10,7 @@
 // Word w of a row (32 bits, channels 8w .. 8w + 7, channel 8w + i in bits
 // 4i .. 4i + 3) is not stored at place w but where the attention kernel's
 // warp reads it with wide, conflict-free shared-memory loads and without any
-// shuffling between lanes (kv4_attention.cu states the fragments):
+// shuffling between lanes (kv4_attention_warp.cuh states the fragments):
 //   K: the lane quad t of block b takes word 4b + t; all words of one t lie
 //      side by side (place t * D / 32 + b);
 //   V: the lanes of channel group g take words u * 8 + g; all words of one g

@@ -25,6 +25,11 @@
 // The exponent y is off by 1.5 |y| 2^-24 (one rounding, and c's); the mean of |y| over the weights is their entropy less log2
 // S, log2(vocab / S) at most: with ln 2, 1.1 log2(vocab / S) units of 2^-24.  2^y 4, its unit 1; a piece's sum 3, where there is one.  A border
 // and u S (or p S) err apart by the errors of the weights on either side, u or 1 - u of each: not more than one sum's.
+//
+// Measured: 8 rows of 151936 BF16 values, top-p, 26 to 28 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
+// 63 us (floor 11); 128 rows of 100003 FP32 values with settings of their own 80 to 90 us (floor 7.5).  A row takes its cluster 12 to 15 us,
+// a chain of seven short phases between barriers (maximum, bound, list, weights, decision; issue slots 35 %), and there are two or three rows
+// behind one another; the last kind ends with a flat row whose nucleus goes digit by digit, 40 us if FP32 decides it and 80 if not.
 #include <cstddef>
 
 #include "common.cuh"
