@@ -41,8 +41,8 @@ int check_prefix_call(const dflash_kv4_cache* c, int n_tokens, int n_q_heads, in
 cudaError_t shape_call(const dflash_kv4_cache* c, int n_tokens, int n_q_heads, int n_groups, int prefix_stride, int n_seq,
                        int max_rows, int table_stride, Call* out) {
   out->per_segment = 128 / (n_q_heads / c->n_kv_heads);
-  const int tokens = n_seq * max_rows < n_tokens ? n_seq * max_rows : n_tokens;  // that lie in a sequence, at most
-  const long long segments = (static_cast<long long>(tokens / out->per_segment) + n_groups) * c->n_kv_heads;
+  // (also where a sequence has more than max_rows rows, which is refused: other groups' pieces have their merge)
+  const long long segments = (static_cast<long long>(n_tokens / out->per_segment) + n_groups) * c->n_kv_heads;
   cudaError_t e = kv4_tc_shape(c, segments, prefix_stride, &out->prefix);
   if (e == cudaSuccess) e = kv4_shape_of(c, n_q_heads, n_seq, max_rows, table_stride, &out->own);
   if (e != cudaSuccess) return e;

@@ -21,7 +21,7 @@ namespace dflash {
 
 constexpr int kMaxSplits = 16;       // CTAs of a cluster
 constexpr int kFixed = 45;           // binary places of a weight as it is computed
-constexpr float kMaxTemperature = 0x1p64f;
+constexpr float kMinTemperature = 0x1p-125f, kMaxTemperature = 0x1p64f;
 
 struct SampleArgs {
   const uint8_t* logits;
@@ -331,7 +331,7 @@ struct Settings {
   bool greedy, by_k, by_p, by_min, fine;
   __device__ __forceinline__ Settings(const SampleArgs& a, int row) {
     const float t = a.temperature ? a.temperature[row] : 1.f;
-    temperature = t > kMaxTemperature ? kMaxTemperature : t;
+    temperature = t > kMaxTemperature ? kMaxTemperature : t > 0.f && t < kMinTemperature ? kMinTemperature : t;
     greedy = !(temperature > 0.f);
     k = a.top_k ? a.top_k[row] : 0;
     by_k = k > 0 && k < a.vocab;
@@ -346,7 +346,7 @@ struct Settings {
   }
   // log2(e) / T as the sum of two
   __device__ __forceinline__ void scale(Scale& s, int drop) const {
-    const double c = fmin(1.4426950408889634 / static_cast<double>(temperature), 1e38);
+    const double c = 1.4426950408889634 / static_cast<double>(temperature);
     s.hi = static_cast<float>(c);
     s.lo = static_cast<float>(c - static_cast<double>(s.hi));
     s.drop = drop;

@@ -611,8 +611,9 @@ int dflash_qk_norm_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_
  * All else as for dflash_kv4_attention without a window, the roundings too (over the
  * prefix those of more than 32 rows per kv head).  n_groups <= 1024, prefix_stride * page_size <=
  * 2^31 - 256 and n_tokens * n_q_heads < 2^31 (else DFLASH_ERR_CAPACITY).
- * DFLASH_DEV_BAD_BLOCK also for group_offsets that descend or leave sequences out; the rows of
- * such a group, of one whose row_offsets are refused, and of sequences left out are unspecified.
+ * DFLASH_DEV_BAD_BLOCK also for group_offsets that descend, where every row is unspecified, or leave
+ * sequences out; the rows of such sequences, of sequences refused and of a group whose row_offsets are refused are
+ * unspecified.
  *   workspace: dflash_kv4_prefix_attention_workspace bytes, as there. */
 int dflash_kv4_prefix_attention(const dflash_kv4_cache* cache, const void* q, void* out, int32_t type, int64_t q_stride,
                                 int64_t out_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_groups,
@@ -639,7 +640,8 @@ size_t dflash_kv4_prefix_attention_workspace(const dflash_kv4_cache* cache, int3
  * thresholds (weights are right to about 2^-43, and equal on every call).
  *   uniform: [n_rows] float in [0, 1).
  *   temperature, top_k (int32), top_p, min_p: [n_rows] in device memory, each or NULL (1, 0,
- *            1, 0).  A temperature of 0 is the greedy choice: the first id of the largest logit.
+ *            1, 0).  A temperature of 0 is the greedy choice: the first id of the largest logit; others below
+ *            2^-125 act as that.
  *   tokens:  [n_rows] int32 out.  -1 where every token is masked.
  *   logprob: optional [n_rows] float out, of the token among the kept ones (greedy: 0; no
  *            token: -infinity).

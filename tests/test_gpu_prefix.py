@@ -253,6 +253,16 @@ def test_reports(R, G):
     assert report(slice(7, 7), offsets=(2, 30)) & D.DFLASH_DEV_BAD_BLOCK
     assert report(slice(0, 2), offsets=(3, 30)) & D.DFLASH_DEV_BAD_BLOCK
     assert report(slice(0, 3), prefix=(1, 10000)) & D.DFLASH_DEV_CAPACITY  # (its cells behind the table's pages are NaN or elsewhere)
+    # a sequence of more rows than the call allows: what is not of it stays
+    many = Case(R, 1, 64, 2, G, [(100, [(20, 8), (30, 8)]), (2000, uneven(np.random.default_rng(3), 9, 90, 2))], 16, False)
+    first, st = many.run(R), status()
+    args = list(many.args())
+    args[8] = 2
+    got = R.kv4_prefix_attention(*args, status=st)
+    assert int(st) & D.DFLASH_DEV_BAD_BLOCK
+    late = got[16: many.tokens].double(), first[16:].double()
+    # another kernel's roundings: of P and V 2^-11 each, of K 2^-11 of scores below 5, all of sums of p |v| / sum p < 1, for both; the results spread by 0.03
+    assert bool((late[0] - late[1]).abs().max() <= 2.0 ** -7)
     assert report(slice(3, 7), prefix_table=((0, 2), 1 << 20)) & D.DFLASH_DEV_CAPACITY
     assert report(slice(0, 3), prefix_table=((1, 0), -7)) & D.DFLASH_DEV_CAPACITY
 

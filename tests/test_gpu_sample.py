@@ -222,6 +222,20 @@ def test_far_temperatures_and_values(R, kind):
     check(R, big, rng.random(8), t, top_p=rng.uniform(0.1, 0.9, 8), min_p=[0.1] * 8)
 
 
+def test_smallest_temperatures(R):
+    """Logits as far apart as the smallest temperature; those below act as it."""
+    rng = np.random.default_rng(10)
+    least = np.float32(2.0 ** -125)
+    x = torch.as_tensor(rng.standard_normal((12, 3000)) * 2.0 ** -125 * rng.uniform(0.5, 4, (12, 1)), device="cuda").float()
+    u, p, k = rng.random(12), rng.uniform(0.2, 1, 12), rng.integers(1, 3000, 12)
+    t = np.concatenate([np.full(8, least), np.geomspace(2.0 ** -125, 2.0 ** -120, 4)])
+    for kw in ({}, dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p), dict(min_p=p)):
+        check(R, x, u, t, **kw)
+    small = np.float32([1e-45, 1e-40, 1e-39, 2.0 ** -126, 2.0 ** -125, 2e-38, 2e-38, 2e-38, 2e-38, 2e-38, 2e-38, 2e-38])
+    for a, b in zip(R.sample_tokens(x, floats(u), floats(small)), R.sample_tokens(x, floats(u), floats(np.maximum(small, least)))):
+        assert torch.equal(a, b)
+
+
 def test_reports(R):
     rng = np.random.default_rng(2)
     x = logits(rng, 6, 3000, "fp32")
