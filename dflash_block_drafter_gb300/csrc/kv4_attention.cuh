@@ -335,7 +335,9 @@ struct Kv4Job {
 // segment of 150 pieces costs a warp 19 of them, four or eight in flight, not 150
 // in turn.
 constexpr int kMergeThreads = 256;
-constexpr int kFewPieces = 8;
+// (Over a prefix, whose segments of 128 rows have 10 to 20 pieces each, 16: 16 blocks of 8 over 32768 shared cells 123 -> 119 us.)
+template <int MODE>
+constexpr int kFewPieces = MODE == kKv4Prefix ? 16 : 8;
 
 template <int D, int R, int MODE>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnArgs a, int most) {
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4AttnA
   if (c < 0) return;
   const int4 j0 = __ldcg(reinterpret_cast<const int4*>(a.jobs + c));  // r0, head, rows, last
   const int n = j0.w - c + 1;
-  const bool few = n <= kFewPieces;
+  const bool few = n <= kFewPieces<MODE>;
   const int i0 = few ? 0 : warp, step = few ? 1 : WARPS;
   const int m0 = few ? blockIdx.y * WARPS + warp : blockIdx.y, m_step = gridDim.y * (few ? WARPS : 1);
   for (int m = m0; m < j0.z; m += m_step) {

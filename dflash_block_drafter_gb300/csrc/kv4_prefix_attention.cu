@@ -11,9 +11,9 @@
 // and waits for it where it needs what that has left (64 tokens 130 -> 125 us, 8 tokens over 8192 cells 45 -> 35; with the
 // passes in the other order, the prefix's waiting for the own cells', 138).
 //
-// Measured: 64 tokens of 24 / 2 heads of 256 over 32768 shared and 1 .. 4096 own cells 125 us (floor 29): the prefix's products 79
-// (480 TFLOP/s, tensor pipe 38 %: a tile's way through eight barriers, as without a prefix), its pieces' merge 14, the own cells
-// 34, their merge 9.  16 blocks of 8 124 us (floor 29); 200 tokens of 32 / 8 heads of 128 in five groups 105 us (floor 21).
+// Measured: 64 tokens of 24 / 2 heads of 256 over 32768 shared and 1 .. 4096 own cells 122 us (floor 29): the prefix's products 79
+// (480 TFLOP/s, tensor pipe 38 %: a tile's way through eight barriers, as without a prefix), its pieces' merge 12, the own cells
+// 34, their merge 9.  16 blocks of 8 119 us (floor 29); 200 tokens of 32 / 8 heads of 128 in five groups 105 us (floor 21).
 #include <cstddef>
 
 #include "kv4_attention_warp.cuh"
