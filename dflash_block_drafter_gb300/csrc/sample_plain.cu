@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   }
   __syncthreads();
   if (!s_done && tid == 0) {
-    a.tokens[row] = kUndecided - 16 - (close ? a.drop : drop_of(whole / ex2_approx(fmaf(m, c, k)), a.drop));
+    a.tokens[row] = kUndecided - 16 - (close ? a.drop + 1 : drop_of(whole / ex2_approx(fmaf(m, c, k)), a.drop));
     // (what the second kernel need not find again, where there is a place for it)
     if (a.logprob && a.kept) a.logprob[row] = m, a.kept[row] = static_cast<int32_t>(all);
   }
@@ -426,11 +426,12 @@ __global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const Samp
       __syncwarp();
     }
     sync();
-    const int row = s_told, drop = s_told_drop;
+    const int row = s_told;
+    int drop = s_told_drop;  // more than a.drop: not known
     if (row < 0) return;
     {
         const Settings set(a, row);
-        if (tid == 0) set.scale(s_scale, drop);
+        if (tid == 0) set.scale(s_scale, min(drop, a.drop));
         const uint8_t* src = a.logits + row * a.row_bytes;
         const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E::BYTES;
         const uint4* frame = reinterpret_cast<const uint4*>(src - skip * E::BYTES);
@@ -475,47 +476,57 @@ __global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const Samp
         if (tid == 0) s_scale.m = m;
         __syncthreads();
         const Scale& scale = s_scale;
-        uint4 next[kRestLoads];
-        if (b0 + warp < b1) load(b0 + warp, next);
-        for (int b = b0 + warp; b < b1; b += kRestWarps) {
-          uint4 v[kRestLoads];
-#pragma unroll
-          for (int j = 0; j < kRestLoads; ++j) v[j] = next[j];
-          if (b + kRestWarps < b1) load(b + kRestWarps, next);
-          uint64_t sum = 0;
-          // (not unrolled, here and below: the weights of a batch in line are many KB of instructions that are fetched for each)
-#pragma unroll 1
-          for (int j = 0; j < kRestLoads; ++j) {
-            sum += K::exact_sum(v[0], scale, table);
-            v[0] = v[1];
-          }
-          static_assert(kRestLoads == 2, "pieces");
-          sum = warp_sum(sum);
-          if (lane == 0) part[b - b0] = sum;
-        }
-        __syncthreads();
-        // a thread has two neighbours
-        static_assert(sizeof(part) / 8 <= 2 * kRestThreads, "batches");
         const int mine = 2 * tid;
-        const uint64_t first = mine < b1 - b0 ? part[mine] : 0, own = first + (mine + 1 < b1 - b0 ? part[mine + 1] : 0);
-        const uint64_t upto = warp_upto(own, lane);
-        if (lane == 31) s_wide[warp] = upto;
-        __syncthreads();
-        uint64_t before = upto - own, cta = 0;
+        uint64_t first, own, before, cta, whole, below;
+        for (;;) {
+          uint4 next[kRestLoads];
+          if (b0 + warp < b1) load(b0 + warp, next);
+          for (int b = b0 + warp; b < b1; b += kRestWarps) {
+            uint4 v[kRestLoads];
 #pragma unroll
-        for (int i = 0; i < kRestWarps; ++i) {
-          if (i < warp) before += s_wide[i];
-          cta += s_wide[i];
-        }
-        if (tid < kRestCtas)
-          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&cta_wide[rank]), tid)), "l"(cta) : "memory");
-        __syncwarp();
-        sync();
-        uint64_t whole = 0, below = 0;
+            for (int j = 0; j < kRestLoads; ++j) v[j] = next[j];
+            if (b + kRestWarps < b1) load(b + kRestWarps, next);
+            uint64_t sum = 0;
+            // (not unrolled, here and below: the weights of a batch in line are many KB of instructions that are fetched for each)
+#pragma unroll 1
+            for (int j = 0; j < kRestLoads; ++j) {
+              sum += K::exact_sum(v[0], scale, table);
+              v[0] = v[1];
+            }
+            static_assert(kRestLoads == 2, "pieces");
+            sum = warp_sum(sum);
+            if (lane == 0) part[b - b0] = sum;
+          }
+          __syncthreads();
+          // a thread has two neighbours
+          static_assert(sizeof(part) / 8 <= 2 * kRestThreads, "batches");
+          first = mine < b1 - b0 ? part[mine] : 0;
+          own = first + (mine + 1 < b1 - b0 ? part[mine + 1] : 0);
+          const uint64_t upto = warp_upto(own, lane);
+          if (lane == 31) s_wide[warp] = upto;
+          __syncthreads();
+          before = upto - own, cta = 0;
 #pragma unroll
-        for (int r = 0; r < kRestCtas; ++r) {
-          if (r < rank) below += cta_wide[r];
-          whole += cta_wide[r];
+          for (int i = 0; i < kRestWarps; ++i) {
+            if (i < warp) before += s_wide[i];
+            cta += s_wide[i];
+          }
+          if (tid < kRestCtas)
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&cta_wide[rank]), tid)), "l"(cta) : "memory");
+          __syncwarp();
+          sync();
+          whole = 0, below = 0;
+#pragma unroll
+          for (int r = 0; r < kRestCtas; ++r) {
+            if (r < rank) below += cta_wide[r];
+            whole += cta_wide[r];
+          }
+          if (drop <= a.drop) break;
+          // what the weights come to is known now: with all the places that it allows
+          drop = drop_of(static_cast<float>(whole) * exp2f(static_cast<float>(a.drop - kFixed)), a.drop);
+          sync();
+          if (tid == 0) s_scale.drop = drop;
+          __syncthreads();
         }
         const uint64_t place = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(whole));
         if (place >= below && place < below + cta) {  // (one CTA)

@@ -95,6 +95,20 @@ constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
 // What the first CTA (or the one that u names) says of a quick answer.
 enum Verdict : uint32_t { kDone, kExactSum, kDigits };
 
+// The exact weights of a thread's values, by a call: few rows have to know them.
+template <int TYPE>
+__device__ __noinline__ uint64_t exact_values(const uint4* data, int t0, int t1, const Scale* c, const TableEntry* table) {
+  uint64_t sum = 0;
+#pragma unroll 1
+  for (int i = t0; i < t1; ++i) {
+    uint32_t b;
+    if constexpr (Keys<TYPE>::WIDE) b = reinterpret_cast<const uint32_t*>(data)[i];
+    else b = reinterpret_cast<const uint16_t*>(data)[i];
+    sum += weight(Keys<TYPE>::value(b), *c, table);
+  }
+  return sum;
+}
+
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleArgs a) {
   using E = Elem<TYPE>;
@@ -303,11 +317,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
   };
   // The exact weight of all tokens.
   auto exact_sum = [&]() {
-    uint64_t sum = 0, all, below;
+    uint64_t all, below;
     uint32_t none = 0;
-#pragma unroll 1
-    for (int i = t0; i < t1; ++i) sum += one_weight(K::value(bits_at(i)));
-    scan(sum, all);
+    scan(exact_values<TYPE>(data, t0, t1, scale, sh.table), all);
     return exchange(all, none, below);
   };
   auto tell_verdict = [&](uint32_t v) {  // (one thread)
@@ -867,8 +879,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
   bool known = !by_p;
   if (by_p && !(p > 0.f)) cut = most, known = true;
   auto exact_from_here = [&]() {
+    if (!(weight_of_all > 0.f)) {  // not known: by the fewest places first
+      __syncthreads();
+      if (tid == 0) sh.scale.drop = a.drop;
+      __syncthreads();
+      weight_of_all = static_cast<float>(exact_sum()) * exp2f(static_cast<float>(a.drop - kFixed));
+    }
     __syncthreads();
-    if (tid == 0) sh.scale.drop = weight_of_all > 0.f ? drop_of(weight_of_all, a.drop) : a.drop;
+    if (tid == 0) sh.scale.drop = drop_of(weight_of_all, a.drop);
     __syncthreads();
   };
   for (bool exact = !in_range; !known; exact = true) {

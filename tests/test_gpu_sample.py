@@ -161,6 +161,23 @@ def test_logits_far_from_zero(R, offset):
         check(R, x, rng.random(n), t, **kw)
 
 
+@pytest.mark.parametrize("offset", [0.0, 2.0 ** 16])
+def test_long_tails(R, offset):
+    """One token has most of the weight, and what is decided lies among 2^19 small ones: weights far below the largest count."""
+    rng = np.random.default_rng(41)
+    n, vocab = 12, 2 ** 19 - 3
+    # (steps of 2^-7 at 2^16; T 2^-6, so that the tail is 2^-29 .. 2^-35 of the largest)
+    v = (rng.integers(-3, 1, (n, vocab)) - 41) * 2.0 ** -7
+    v[np.arange(n), rng.integers(0, vocab, n)] = 0
+    x = torch.as_tensor(v + offset, device="cuda").float()
+    t = np.full(n, 2.0 ** -6 / 1.0)
+    tail = np.exp(v / 2.0 ** -6).sum(1) - 1
+    for part in (0.2, 0.5, 0.9):
+        check(R, x, rng.random(n), t, top_p=1 - tail / (1 + tail) * part)
+        check(R, x, 1 - tail / (1 + tail) * part, t, top_p=np.full(n, 1 - 1e-7), min_p=np.full(n, 1e-20))
+        check(R, x, 1 - tail / (1 + tail) * part, t)
+
+
 def test_draws_follow_the_distribution(R):
     """Evenly spaced numbers draw each token as often as its weight says, to one draw."""
     rng = np.random.default_rng(5)
