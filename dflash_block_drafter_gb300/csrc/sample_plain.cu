@@ -16,7 +16,7 @@
 //
 // Few rows: a row's batches are split over the CTAs of a cluster.
 //
-// Measured: 1000 rows of 151936 BF16 values 91 us (floor 45).  The first kernel takes 60 (5.1 TB/s, issue slots at 70 %: an
+// Measured: 1000 rows of 151936 BF16 values 89 us (floor 45).  The first kernel takes 60 (5.1 TB/s, issue slots at 70 %: an
 // exponential and seven instructions a value), the second 25 to 30 for the 15 or so rows left to it: a claim, 16 us of exact weights,
 // the search for the token.
 #include <cstddef>
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
 
 // Rows that the sums left open: exact ones, by clusters of kRestCtas.  A CTA has a part of the row's batches, which it reads for
 // the weights, and before that for the largest value and the tokens that are not masked, where the first kernel had no place to
-// leave these.  (Half the threads' batches with loads ahead 91 us for 1000 rows, 93 without; CTAs of 512 threads, for which an SM
+// leave these.  (Batches of half the first kernel's size with loads ahead 91 us for 1000 rows, 93 without; CTAs of 512 threads, for which an SM
 // has to be empty, 104.)
 template <int TYPE>
 __global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const SampleArgs a) {

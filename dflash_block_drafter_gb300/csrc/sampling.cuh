@@ -229,15 +229,17 @@ struct Keys {
     return x[0];
   }
   // exact weight of a piece's values, four side by side
-  static __device__ __forceinline__ uint64_t exact_sum(const uint4& v, const Scale& c, const TableEntry* table) {
+  static __device__ __forceinline__ uint64_t exact_sum(uint4 v, const Scale& c, const TableEntry* table) {
     constexpr int VEC = Elem<TYPE>::VEC, N = 4;
     uint64_t sum = 0;
-#pragma unroll
+    // (not unrolled: the instructions of a piece in line are fetched slower than they run)
+#pragma unroll 1
     for (int e0 = 0; e0 < VEC; e0 += N) {
       float x[N];
       uint64_t w[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = value(bits(v, e0 + e));
+      for (int e = 0; e < N; ++e) x[e] = value(bits(v, e));
+      v.x = v.z, v.y = v.w;  // (16-bit values: the other four)
       weights(x, c, table, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) sum += w[e];
