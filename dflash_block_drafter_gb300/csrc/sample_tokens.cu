@@ -16,9 +16,9 @@
 //    tokens above the bound, if they are at most kList, go to the first CTA, which
 //    compares them (or sorts them) and decides everything with exact weights.  S itself, which a top-p without top-k
 //    compares with, comes from FP32 sums; where their error leaves it open which token is the last, S is added up exactly.
-// Else (long lists) a threshold is found digit by digit: counts (and weights) of up to
+// Else (long lists) a threshold is found digit by digit: counts, or weights, of up to
 // 2048 ranges of the keys, then of the ranges of the one in which the threshold lies, until it is one key; and the token by
-// the sums of the CTAs, warps and lanes.  FP32 weights do first, in whole numbers, whose sums are exact, and exact ones if those leave a
+// the sums of the CTAs and threads.  FP32 weights do first, in whole numbers, whose sums are exact, and exact ones if those leave a
 // decision open: whether a border of the token, or of the last key, lies within their error of what it is compared with.
 //
 // That error: a weight is 2^(x c + k), k = -m c as FP32 has it (what it is off by is the same for all weights).
@@ -27,7 +27,7 @@
 // and u S (or p S) err apart by the errors of the weights on either side, u or 1 - u of each: not more than one sum's.
 //
 // Measured: 8 rows of 151936 BF16 values, top-p, 26 to 28 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
-// 63 us (floor 11); 128 rows of 100003 FP32 values with settings of their own 80 to 90 us (floor 7.5).  A row takes its cluster 12 to 15 us,
+// 62 us (floor 11); 128 rows of 100003 FP32 values with settings of their own 79 to 97 us (floor 7.5).  A row takes its cluster 12 to 15 us,
 // a chain of seven short phases between barriers (maximum, bound, list, weights, decision; issue slots 35 %), and there are two or three rows
 // behind one another; the last kind ends with a flat row whose nucleus goes digit by digit, 40 us if FP32 decides it and 80 if not.
 #include <cstddef>
