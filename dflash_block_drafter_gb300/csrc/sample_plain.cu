@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const Samp
   const int rank = blockIdx.x % kRestCtas, cluster = blockIdx.x / kRestCtas, clusters = gridDim.x / kRestCtas;
   if (tid < 32) table[tid] = kTable[tid];
   auto sync = [] {
+    __syncwarp();  // (the barrier wants its warp's lanes together)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   };

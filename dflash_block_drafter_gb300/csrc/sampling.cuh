@@ -282,8 +282,10 @@ struct Keys {
 };
 
 // ------------------------------------------------------------------ clusters
+// (The aligned barrier wants its warp's lanes together, which a branch by lane before it does not promise.)
 __device__ __forceinline__ void cluster_sync(int splits) {
   if (splits > 1) {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   } else {

@@ -131,6 +131,17 @@ def test_flat_rows(R, kind, vocab):
         check(R, x, u, t, **kw)
 
 
+@pytest.mark.parametrize("ctas,n", [(1, 153), (2, 77), (3, 51), (4, 39), (5, 31), (6, 26), (7, 22), (9, 17), (12, 13)])
+def test_long_lists_by_ctas(R, ctas, n):
+    """Rows of so many CTAs (as many as hold a row, where the rows are enough for all SMs), that find their thresholds digit by digit: shares of the
+    ranges that end inside a warp among them."""
+    rng = np.random.default_rng(ctas)
+    x = logits(rng, n, 18500 * ctas, "fp32", rng.uniform(0.02, 0.1, (n, 1)))
+    u, p, k = rng.random(n), rng.uniform(0.3, 0.99, n), rng.integers(2000, 15000, n)
+    for kw in (dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p, min_p=np.full(n, 0.1))):
+        check(R, x, u, rng.uniform(0.7, 1.5, n), **kw)
+
+
 @pytest.mark.parametrize("sizes", [(1, 128), (129, 256), (257, 511), (512, 1024), (1025, 1400)])
 def test_lists(R, sizes):
     """As many tokens as named stand out: those that a filter's list takes in."""
