@@ -70,10 +70,9 @@ __device__ __forceinline__ void widen(const uint4 (&raw)[2], float (&x)[16]) {
   }
 }
 
-// 1 / rms of a head whose sum of squares leaves FP32's range: the values are scaled by a power of two first.
+// Sum of squares of a head's values times f, a power of two that keeps them in FP32's range.
 template <bool BF16, int LANES>
-__device__ __noinline__ float far_rms(uint4 a, uint4 b, float eps, bool small) {
-  const float f = small ? 0x1p70f : 0x1p-70f;
+__device__ __noinline__ float far_squares(uint4 a, uint4 b, float f) {
   const uint4 raw[2] = {a, b};
   float x[16], s = 0.f;
   widen<BF16>(raw, x);
@@ -81,8 +80,7 @@ __device__ __noinline__ float far_rms(uint4 a, uint4 b, float eps, bool small) {
   for (int i = 0; i < 16; ++i) s = fmaf(x[i] * f, x[i] * f, s);
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float m = s * (1.f / (16 * LANES)) + eps * f * f;
-  return m > 0.f ? rsqrtf(m) * f : 0.f;  // a head of zeros without eps stays one
+  return s;
 }
 
 template <int D, bool BF16>
@@ -94,9 +92,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const Ro
   __shared__ __align__(16) float2 s_angle[kWarps][D / 2];  // (cos, sin) of each warp's row
   const int tid = threadIdx.x, lane = tid & 31;
   float2* angle = s_angle[tid >> 5];
+  // weights (or an eps) whose products with values of heads that are neither `big` nor `tiny` below may leave FP32's range
+  bool wide = a.eps > 1e38f;
   for (int i = tid; i < D; i += kThreads) {
-    s_w[0][i] = a.side[0].weight ? a.side[0].weight[i] : 1.f;
-    s_w[1][i] = a.side[1].weight ? a.side[1].weight[i] : 1.f;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const float w = a.side[which].weight ? a.side[which].weight[i] : 1.f;
+      wide |= !(fabsf(w) <= 0x1p62f) || (w != 0.f && fabsf(w) < 0x1p-62f);
+      s_w[which][i] = w;
+    }
     if (i < a.half) {
       s_turns[i] = a.turns[i];
       int axis = a.axes ? a.axes[i] : 0;
@@ -107,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const Ro
       s_axis[i] = static_cast<uint8_t>(axis);
     }
   }
-  __syncthreads();
+  wide = __syncthreads_or(wide);
+  const float most = wide ? -1.f : 1e38f;  // of a sum of squares, for heads that need no care
   const int sub = lane / LANES, at = lane % LANES;
   const bool turned = at < a.half / 8;
   const int j0 = at * 8;                                        // frequencies of the lane's pairs
@@ -193,11 +198,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const Ro
           for (int o = 1; o < LANES; o <<= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
           const float m = ssq * (1.f / D) + a.eps;
           float inv = norm ? rsqrtf(m) : 1.f;
-          const bool big = !(ssq < 1e38f), tiny = norm && m < 1e-30f;
-          if (__any_sync(0xffffffffu, big || tiny)) {
-            const float far = far_rms<BF16, LANES>(raw[u][0], raw[u][1], a.eps, tiny);
-            if (norm && (big || tiny)) inv = far;
-            if (big && !(far > 0.f) && at == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+          const bool tiny = norm && m < 1e-30f;
+          if (__any_sync(0xffffffffu, !(ssq < most) || tiny)) {
+            const bool big = !(ssq < 1e38f);
+            // The values are scaled by powers of two until the largest is about 1 (`f`, for the sum of squares, and `to_one`), and 1 / rms
+            // is that of the scaled ones, so that products with the weights leave the range only where results do.
+            const float f = big ? 0x1p-70f : tiny ? 0x1p90f : 0.5f;
+            const float far = far_squares<BF16, LANES>(raw[u][0], raw[u][1], f);
+            if (big && !(far < INFINITY) && at == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
+            if (norm && (!(ssq < most) || tiny)) {
+              auto power = [](float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); };
+              const float mean = far * (1.f / D) + a.eps * f * f, r = rsqrtf(mean);
+              // (2^100: beside an eps far above the squares, inv has its bits still)
+              const float to_one = far > 0.f && far < INFINITY ? fminf(power(rsqrtf(far)), power(r) * 0x1p100f) : 1.f;
+              inv = mean > 0.f ? r / to_one : 0.f;  // a head of zeros without eps stays one
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = x[e] * f * to_one;
+            }
           }
           uint32_t za[4], zb[4];
 #pragma unroll

@@ -144,6 +144,27 @@ def test_values_beyond_the_squares_range(R, d, gain, eps):
     assert int(st) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 3e38])
+def test_heads_at_the_types_ends(R, d, rot, eps):
+    """Heads of the largest values (whose products with a weight, and sums of pairs, pass FP32's range before the root divides them), of subnormal ones
+    and of ordinary ones beside each other, and weights of any size: the results are ordinary."""
+    c = case("bf16", 24, 9, 5, d, rot, seed=d + rot)
+    rng = np.random.default_rng(d)
+    for x, t in ((c["xq"], c["q"]), (c["xk"], c["k"])):
+        size = np.asarray([3.3e38, 2.0 ** -133, 1.0, 1e19, 2.0 ** -126, 1e-17])[rng.integers(0, 6, x.shape[:2])][..., None]
+        x[:] = S.to_type(np.sign(x) * rng.uniform(0.5, 1.0, x.shape) * size * np.where(size < 1e-39, 8, 1), "bf16")
+        t.copy_(torch.as_tensor(x, device="cuda").float().bfloat16())
+        assert np.array_equal(t.double().cpu().numpy(), x) and np.all(x.any(-1))
+    for gain in (1.0, 2.5, 1e25, 1e-25):
+        c["weights"] = (gain * (1 + 0.3 * rng.standard_normal((2, d)))).astype(np.float32).astype(np.float64)
+        st = status()
+        got = call(R, c, eps=eps, st=st)
+        assert int(st) == 0 and all(bool(torch.isfinite(g).all()) for g in got)
+        check(c, got, eps=eps)
+
+
 def test_heads_of_zeros(R):
     c = case("bf16", 3, 4, 2, 64, 64)
     c["t"][1] = 0
