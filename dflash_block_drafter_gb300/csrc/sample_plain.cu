@@ -4,7 +4,7 @@
 // its sum of 2^((x - r) c) with the reference r, the largest value the warp has met; the
 // batches' sums, brought to one reference, lead to the batch in which u lies, which is
 // read once more.  The token stands if both of its borders are further from u than these sums
-// may be off; else the row is left to a second kernel, which forms exact sums with clusters of
+// may be off (for u below 2^-24 none is); else the row is left to a second kernel, which forms exact sums with clusters of
 // eight CTAs (one CTA alone takes 70 us for 151936 tokens, the tail of a call of 1000 rows).  A greedy row is one look: the
 // first batch whose reference is the largest value holds its first id.
 //
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
 // leave these.  (Batches of half the first kernel's size with loads ahead 91 us for 1000 rows, 93 without; CTAs of 512 threads, for which an SM
 // has to be empty, 104.)
 template <int TYPE>
-__global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const __grid_constant__ SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
   constexpr int VEC = E::VEC, BATCH = 32 * kRestLoads * VEC;  // (not the first kernel's batches)
@@ -530,7 +530,9 @@ __global__ void __launch_bounds__(kRestThreads, 2) sample_rest_kernel(const Samp
           __syncthreads();
         }
         const uint64_t place = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(whole));
-        if (place >= below && place < below + cta) {  // (one CTA)
+        if (set.u < kSmallNumber) {
+          if (rank == 0) draw_small<TYPE>(a, row, K::LOWEST, m, whole, drop, all, reinterpret_cast<double*>(s_wide));
+        } else if (place >= below && place < below + cta) {  // (one CTA)
           before += below;
           if (before <= place && place < before + own) {  // (one thread)
             const bool second = place >= before + first;

@@ -110,7 +110,7 @@ __device__ __noinline__ uint64_t exact_values(const uint4* data, int t0, int t1,
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
   using E = Elem<TYPE>;
   using K = Keys<TYPE>;
   constexpr int VEC = E::VEC;
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
     }
   };
 
-  const bool filter = by_k || by_p || by_min;
+  const bool small = u < kSmallNumber;  // drawn by FP64 weights: these rows find their thresholds digit by digit
+  const bool filter = (by_k || by_p || by_min) && !small;
   uint32_t from_key = K::LOWEST;  // no threshold of top-k and top-p lies below
   uint32_t to_key = most;         // nor one of top-p alone above
   uint64_t quick_total = 0;       // FP32 weights of all tokens, by top-p alone
@@ -827,6 +828,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
     count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
     const uint64_t total = exchange(all, count, below);
     if (!exact) weight_of_all = static_cast<float>(total) / unit / one;
+    if (exact && small) {
+      if (rank == 0) draw_small<TYPE>(a, row, cut, m, total, scale->drop, count, reinterpret_cast<double*>(sh.warp_w));
+      return true;
+    }
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
     const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
     before += below;
@@ -895,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
     if (!exact) weight_of_all = static_cast<float>(sure.whole) / unit / one;
   }
   if (by_p && p > 0.f) cut = max(cut, sure.lo);
-  if (in_range && draw_from(cut, false)) return;
+  if (in_range && !small && draw_from(cut, false)) return;
   exact_from_here();
   draw_from(cut, true);
 }

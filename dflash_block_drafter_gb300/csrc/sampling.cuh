@@ -366,6 +366,73 @@ __device__ __forceinline__ float others_of(uint64_t total, int drop) {
   return static_cast<float>(total - (1ull << (kFixed - drop))) * exp2f(static_cast<float>(drop - kFixed));
 }
 
+// Numbers below this leave the token to sums in FP64, in which small weights keep all their places (units of 2^-45 to 2^-61 are 0 beside
+// u times the sum here, and a weight that rounds to 0 could never be drawn, not even by 0 itself).
+constexpr float kSmallNumber = 0x1p-24f;
+
+// Draws by such a number, by one CTA: the first token with which the weights of keys from `cut` on, which come to `total` with `drop` places less
+// and are `kept` tokens, exceed u times that.  Reads the row in order of ids, as far as it has to.  (Eight rows of 151936 values, all with such a
+// number: 60 to 115 us where the first ids have weight, 170 to 260 where only the last 100 have.)
+template <int TYPE>
+__device__ __noinline__ void draw_small(const SampleArgs& a, int row, uint32_t cut, float m, uint64_t total, int drop, uint32_t kept, double* sums) {
+  constexpr int PER = 8;  // neighbours of a thread
+  const Settings set(a, row);
+  const uint8_t* src = a.logits + row * a.row_bytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  // (below the largest weight, 1, so that one passes it)
+  const double target = static_cast<double>(set.u) * static_cast<double>(total) * static_cast<double>(exp2f(static_cast<float>(drop - kFixed)));
+  auto value = [&](int i) { return i < a.vocab ? Elem<TYPE>::one(src, i) : -INFINITY; };
+  auto weight_of = [&](float x) {  // (those that FP64 has as 0 without its exponential)
+    const bool none = !(x > -INFINITY) || Keys<TYPE>::of_value(x) < cut || (x - m) / set.temperature < -750.f;
+    return none ? 0.0 : exp((static_cast<double>(x) - static_cast<double>(m)) / static_cast<double>(set.temperature));
+  };
+  double from = 0.0;  // weights before the threads' values
+#pragma unroll 1
+  for (int i0 = 0; i0 < a.vocab; i0 += PER * blockDim.x) {
+    const int first = i0 + tid * PER;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = 0; e < PER; ++e) sum += weight_of(value(first + e));
+    if (!__syncthreads_or(sum > 0.0)) continue;  // (and the last sums have been read)
+    double upto = sum;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    double before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) before = 0.0;
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < warps; ++i) {
+      if (i == warp) upto += from, before += from;
+      from += sums[i];
+    }
+    // (a lane without weight may have a sum that differs in its last place from the one before)
+    const unsigned past = __ballot_sync(0xffffffffu, sum > 0.0 && upto > target);
+    if (!__syncthreads_or(past != 0)) continue;
+    int* lanes = reinterpret_cast<int*>(sums);  // the first of each warp
+    if (lane == 0) lanes[warp] = __ffs(past) - 1;
+    __syncthreads();
+    int who = 0;
+    while (lanes[who] < 0) ++who;
+    if (warp == who && lane == lanes[who]) {
+      int id = 0;
+#pragma unroll 1
+      for (int e = 0; e < PER && before <= target; ++e) {
+        const double w = weight_of(value(first + e));
+        if (w > 0.0) id = first + e;  // (the last one, should the sums end a place below)
+        before += w;
+      }
+      a.tokens[row] = id;
+      if (a.logprob) a.logprob[row] = set.log_of(value(id), m, others_of(total, drop));
+      if (a.kept) a.kept[row] = static_cast<int32_t>(kept);
+    }
+    return;
+  }
+}
+
 // Rows without a filter (sample_plain.cu).
 cudaError_t launch_sample_plain(SampleArgs a, int type, cudaStream_t st);
 

@@ -637,7 +637,8 @@ size_t dflash_kv4_prefix_attention_workspace(const dflash_kv4_cache* cache, int3
  * Tokens of equal logits are kept or left out together, and a masked one (-infinity) is
  * never kept.  The token is the first, in order of ids, with which the kept
  * weights exceed uniform times all of them: the one of the definition in 64 bits, sums and
- * thresholds (weights are right to about 2^-43, and equal on every call).
+ * thresholds.  Weights are right to about 2^-43 of their sum, and each to FP64 for a uniform below 2^-24 (0 draws
+ * the first id kept that has a weight in 64 bits); equal on every call.
  *   uniform: [n_rows] float in [0, 1).
  *   temperature, top_k (int32), top_p, min_p: [n_rows] in device memory, each or NULL (1, 0,
  *            1, 0).  A temperature of 0 is the greedy choice: the first id of the largest logit; others below

@@ -116,6 +116,46 @@ def test_few_levels(R, kind):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [90, 500, 5000, 100003])
+@pytest.mark.parametrize("small", [20, 150, 600])
+def test_smallest_numbers(R, kind, vocab, small):
+    """Numbers about and below the weights of single tokens, 0 among them: in order of ids come tokens that weigh nothing in 64 bits, then tokens of
+    2^-100 to 2^-45 of the largest, then those that carry the sum.  Each filter keeps the small ones, or none."""
+    rng = np.random.default_rng(vocab + small)
+    n, small = 24, min(small, vocab // 2)
+    v = np.full((n, vocab), float(torch.finfo(TYPES[kind]).min))
+    v[:, : vocab // 3: 3] = -2000.0
+    for i in range(n):
+        v[i, np.sort(rng.permutation(vocab - 40)[:small])] = np.sort(rng.uniform(-69, -31, small))
+        v[i, rng.permutation(np.arange(vocab - 40, vocab))[:12]] = rng.uniform(-3, 0, 12)
+    v[:, 1::4] = np.where(rng.random((n, 1)) < 0.3, -INF, v[:, 1::4])
+    x = torch.as_tensor(v, device="cuda").to(TYPES[kind])
+    row = x.double().cpu().numpy()
+    u = f32(np.exp2(rng.uniform(-105, -20, n)))
+    u[:8] = [0, 0, 1e-45, 2.0 ** -126, 1e-30, 1e-20, 2.0 ** -24, 2.0 ** -25]
+    cover = small + 12
+    for kw in ({}, dict(top_k=np.full(n, cover)), dict(top_k=np.full(n, vocab - 1)), dict(top_k=np.full(n, 12)), dict(min_p=np.full(n, 1e-36)),
+               dict(top_p=np.full(n, 1 - 2.0 ** -24)), dict(top_k=np.full(n, cover), min_p=np.full(n, 1e-25), temperature=np.full(n, 1.25)),
+               dict(temperature=np.full(n, 0.75))):
+        kw = {k: (w if k == "top_k" else f32(w)) for k, w in kw.items()}
+        token, logp, kept, _ = S.sample(row, u, **kw)
+        # how near a border lies to the number, relative to the number: further than the sums are off, which is 2^-43 of the whole sum for numbers from
+        # 2^-24 on, and 2^-42 of themselves (the whole sum's, and FP64 roundings) for those below
+        t = kw.get("temperature", np.ones(n, np.float32)).astype(float)[:, None]
+        for i in range(n):
+            z = (row[i] - row[i].max()) / t[i]
+            live = row[i] >= np.sort(row[i])[::-1][kept[i] - 1]
+            upto = np.where(live, np.exp(z), 0).cumsum()
+            at = float(u[i]) * upto[-1]
+            assert at == 0 or np.abs(upto / at - 1).min() > (2.0 ** -18 if u[i] >= 2.0 ** -24 else 2.0 ** -41)
+        got = [w.cpu().numpy() for w in R.sample_tokens(x, floats(u), floats(kw.get("temperature")), ints(kw.get("top_k")), floats(kw.get("top_p")),
+                                                        floats(kw.get("min_p")))]
+        assert got[0].tolist() == token.tolist(), kw
+        assert got[2].tolist() == kept.tolist()
+        assert np.allclose(got[1], logp, rtol=2.0 ** -20, atol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("vocab", [2000, 40000, 151936, 2 ** 19 - 3])
 def test_flat_rows(R, kind, vocab):
     """Nuclei, numbers and least weights that keep hundreds of tokens to all but a few: lists of each length, and rows without one."""
