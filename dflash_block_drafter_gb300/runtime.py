@@ -206,7 +206,7 @@ def _elsewhere(dev: torch.device, stream):
         if stream.device_index != dev.index:
             _refuse("the stream is of another device")
         return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if dev.index != torch._C._cuda_getDevice() else None
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
 
 
 def _current(dev: torch.device) -> int:

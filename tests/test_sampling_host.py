@@ -139,3 +139,13 @@ def test_torch_wrappers_refuse():
                  lambda: R.sample_tokens(torch.zeros((1, 8)), torch.zeros(1)),
                  lambda: R.kv4_prefix_attention(cache, rows, one[None], one, two, one[None], one, two, 1)):
         assert refused(call) == INV
+
+
+def test_wrappers_ask_torch_for_the_current_device(monkeypatch):
+    """By its public call: a private binding may be gone in another release."""
+    torch = pytest.importorskip("torch")
+    from dflash_block_drafter_gb300 import runtime as R
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert R._elsewhere(torch.device("cuda", 1), None) is None
+    assert isinstance(R._elsewhere(torch.device("cuda", 0), None), torch.cuda.device)
