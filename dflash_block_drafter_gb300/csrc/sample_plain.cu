@@ -8,11 +8,13 @@
 // eight CTAs (one CTA alone takes 70 us for 151936 tokens, the tail of a call of 1000 rows).  A greedy row is one look: the
 // first batch whose reference is the largest value holds its first id.
 //
-// The bound: a weight is 2^(x c + k), where k = -r c as FP32 has it for the reference r; what k is off by is the same
-// for all weights.  The exponent y is off by 1.5 |y| 2^-24 (one rounding, and c's); the mean of |y| over the weights
-// is their entropy less log2 S, log2(vocab / S) at most: with ln 2, 1.1 log2(vocab / S) units of 2^-24.  2^y 4; sums in a
-// batch 10 (tree, loads, lanes); a batch's factor 6, a CTA's 6, roundings of single weights 2; sums of those are whole
-// numbers.  A border of a token and u S err apart by the errors of the weights on either side, u or 1 - u of each: not more.
+// The bound, in units of 2^-24 of the row's sum S: a weight is 2^(x c + k) 2^d, where k = -r c as FP32 has it for the batch's reference r and
+// d = k_m - k brings it to the row's; what the row's own k is off by is the same for all weights.  Of the exponent Y = (x - m) c the constant c is off by
+// |Y| at most (one rounding), and x c + k and d, which are Y together, by one rounding each, |Y| in all: with ln 2, 1.39 |Y|.  The mean of |Y| over the
+// weights is their entropy less log2 S, log2(vocab / S) at most.  Then 2^y 4, a piece's sum 3, the batch's 7, its factor 5, a CTA's number 6: 25.
+// The border of a token, which lies about u S, and u S are sums of the same numbers, so that a weight's error counts 1 - u times before the border and u
+// times behind it: 1.39 log2(vocab / S) + 25 / 2.  Only in the batch in which u lies are pieces and single weights not what S was made of: 12 more for the
+// batch's sum, its product and a piece's sum.  Together below 28 + 1.4 log2(vocab / S).
 //
 // Few rows: a row's batches are split over the CTAs of a cluster.
 //
@@ -256,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
       below += x;
     }
     owner = who == rank;
-    if (owner && m != m_own && !set.greedy) add_up();
+    if (owner && !set.greedy) {
+      if (m != m_own) add_up();
+      total += cta - of_cta(rank);  // (of the numbers that the borders are made of)
+    }
   }
   if (bad || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from
     if (rank == 0 && tid == 0) {
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
   const uint64_t at = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(total));
   const float k = start(m);
   const float whole = static_cast<float>(total) * 0x1p-40f;
-  const uint64_t off = units(whole * 0x1p-24f * (32.f + 1.1f * log2f(static_cast<float>(a.vocab) / whole)));
+  const uint64_t off = units(whole * 0x1p-24f * (28.f + 1.4f * log2f(static_cast<float>(a.vocab) / whole)));
   // (k is off by 2^-4 at most, and what `none` leaves out is far below the largest value; else no border is far enough)
   const bool close = !(fabsf(m) * c < 0x1p20f);
   before += below;
@@ -320,11 +325,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
     uint4 v[kLoads];
     const int b = b0 + s_batch;
     load(b, v);
+    const float k_r = start(part[s_batch].x), factor = ex2_approx(k - k_r);  // as in the batch's sum
     uint64_t from = s_from;
     bool found = false;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const uint64_t w = units(K::quick_sum_from(v[j], c, k));
+      const uint64_t w = units(K::quick_sum_from(v[j], c, k_r) * factor);
       const uint64_t x = warp_upto(w, lane) + from;
       const unsigned over = __ballot_sync(0xffffffffu, x > at);
       if (!found && over && lane == __ffs(over) - 1) {
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
         for (int e = 0; e < VEC; ++e) {
           const float value = K::value(K::bits(v[j], e));
           const uint64_t low = y;
-          y += units(ex2_approx(fmaf(value, c, k)));
+          y += units(ex2_approx(fmaf(value, c, k_r)) * factor);
           // the first past u, further from both of its borders than the sums may be off
           if (low <= at && y > at && low + off <= at && y > at + off) {
             a.tokens[row] = b * BATCH + (j * 32 + lane) * VEC + e - skip;

@@ -21,10 +21,11 @@
 // the sums of the CTAs and threads.  FP32 weights do first, in whole numbers, whose sums are exact, and exact ones if those leave a
 // decision open: whether a border of the token, or of the last key, lies within their error of what it is compared with.
 //
-// That error: a weight is 2^(x c + k), k = -m c as FP32 has it (what it is off by is the same for all weights).
-// The exponent y is off by 1.5 |y| 2^-24 (one rounding, and c's); the mean of |y| over the weights is their entropy less log2
-// S, log2(vocab / S) at most: with ln 2, 1.1 log2(vocab / S) units of 2^-24.  2^y 4, its unit 1; a piece's sum 3, where there is one.  A border
-// and u S (or p S) err apart by the errors of the weights on either side, u or 1 - u of each: not more than one sum's.
+// That error, in units of 2^-24 of the sum S: a weight is 2^(x c + k), k = -m c as FP32 has it (what it is off by is the same for all weights).
+// The exponent y is off by 2 |y| (its own rounding and c's, |y| each at most), and the mean of |y| over the weights is their entropy less log2 S,
+// log2(vocab / S) at most: with ln 2, 1.39 log2(vocab / S).  2^y 4, its rounding to a whole number less than 1.  A border and u S (or p S) are sums of
+// the same numbers, so that a weight's error counts 1 - u times before the border and u times behind it: 1.39 log2(vocab / S) + 5 / 2, below
+// 1.4 log2(vocab / S) + 4.  S itself against exact weights has a piece's sum, 3, and the largest weight that it is divided by, 4, besides: 12, and 13 is taken.
 //
 // Measured: 8 rows of 151936 BF16 values, top-p, 26 to 28 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
 // 62 us (floor 11); 128 rows of 100003 FP32 values with settings of their own 79 to 97 us (floor 7.5).  A row takes its cluster 12 to 15 us,
@@ -263,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
   const float unit = __int_as_float((127 + kFixed - a.drop) << 23);
   auto fixed = [&](float w) { return static_cast<uint64_t>(__float2ull_rn(w * unit)); };
   auto quick_weight = [&](float x) { return fixed(ex2_approx(fmaf(x, c_hi, k_hi))); };
-  // What such sums may be off by together, relative: `more` units of 2^-24 and those of the exponents
+  // What such sums may be off by, relative: `more` units of 2^-24 and those of the exponents
   auto error_of = [&](uint64_t sum, float more) {
-    return 0x1p-24f * (more + 1.1f * log2f(static_cast<float>(a.vocab) * unit / static_cast<float>(sum)));
+    return 0x1p-24f * (more + 1.4f * log2f(static_cast<float>(a.vocab) * unit / static_cast<float>(sum)));
   };
   auto one_weight = [&](float x) { return weight_by_call(x, scale, sh.table); };
   // The sum of a value per thread over this CTA's threads before it, and over all of them.
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
         if (by_p && !by_k && a.vocab > kShort) {
           // (the FP32 weights are relative to 2^(m c + k))
           const double whole = static_cast<double>(quick_total) / static_cast<double>(one) * static_cast<double>(exp2f(a.drop - scale->drop));
-          const double off = whole * static_cast<double>(error_of(quick_total, 16.f));
+          const double off = whole * static_cast<double>(error_of(quick_total, 13.f));
           s_lo = whole - off, s_hi = whole + off;
         }
         if (size > 0 && few) {
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
           // the range in which the threshold lies: the last one kept
           if (upto < target && upto + w[j] >= target) {
             const uint32_t to = f.hi - (static_cast<uint32_t>(tid * B + j) << shift), width = (1u << shift) - 1;
-            const uint64_t off = numbers || exact ? 0 : fixed(static_cast<float>(f.whole) / unit * error_of(f.whole, 8.f));
+            const uint64_t off = numbers || exact ? 0 : fixed(static_cast<float>(f.whole) / unit * error_of(f.whole, 4.f));
             sh.found = Found{to - f.lo > width ? to - width : f.lo, to, upto, f.whole, upto + off < target && upto + w[j] >= target + off};
           }
           upto += w[j];
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
       return true;
     }
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
-    const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 8.f));
+    const uint64_t off = exact ? 0 : fixed(static_cast<float>(total) / unit * error_of(total, 4.f));
     before += below;
     if (before <= at && at < before + sum) sh.where = t0, sh.from = before;  // (one thread of the cluster)
     __syncthreads();

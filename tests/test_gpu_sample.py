@@ -182,6 +182,35 @@ def test_long_lists_by_ctas(R, ctas, n):
         check(R, x, u, rng.uniform(0.7, 1.5, n), **kw)
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab,heavy", [(1500, 0), (1500, 1000), (40000, 0), (40000, 500), (40000, 1000)])
+@pytest.mark.parametrize("mode", ["plain", "p", "k"])
+def test_numbers_near_borders(R, kind, vocab, heavy, mode):
+    """u as near to the border of two tokens as FP32 has it, and up to 100 steps of 2^-24 beside: about as far as FP32 sums may be off.  Where
+    `heavy` neighbours have most of the weight (alike, so that all their roundings are), the largest logit is another's."""
+    rng = np.random.default_rng(vocab + heavy)
+    n = 120
+    x = logits(rng, n, vocab, kind, np.exp(rng.uniform(-2.5, -0.5, (n, 1))))
+    if heavy:
+        x[:, :] = torch.as_tensor(rng.uniform(-30, -14, (n, vocab)), device="cuda").to(TYPES[kind])
+        at = rng.integers(0, vocab - heavy, n)
+        for i in range(n):
+            x[i, at[i]: at[i] + heavy] = float(rng.uniform(-9, -1))
+            x[i, (at[i] + vocab // 2) % vocab] = float(rng.uniform(-0.1, 0.1))
+    t = f32(rng.uniform(0.6, 1.4, n))
+    p = f32(rng.uniform(0.9, 0.9999, n)) if mode == "p" else None
+    k = np.full(n, vocab - 3) if mode == "k" else None
+    row = x.double().cpu().numpy()
+    token, _, kept, _ = S.sample(row, rng.random(n), t, k, p)
+    u = np.zeros(n, np.float32)
+    for i in range(n):
+        live = row[i] >= np.sort(row[i])[::-1][kept[i] - 1]
+        upto = np.where(live, np.exp((row[i] - row[i].max()) / float(t[i])), 0).cumsum()
+        u[i] = np.float32(upto[token[i]] / upto[-1]) + np.float32(rng.integers(-100, 101) * 2.0 ** -24 * (i % 3 > 0))
+    u = np.clip(u, 0, f32(1 - 2.0 ** -24))
+    check(R, x, u, t, k, p)
+
+
 @pytest.mark.parametrize("sizes", [(1, 128), (129, 256), (257, 511), (512, 1024), (1025, 1400)])
 def test_lists(R, sizes):
     """As many tokens as named stand out: those that a filter's list takes in."""
