@@ -383,8 +383,10 @@ __device__ __noinline__ void draw_small(const SampleArgs& a, int row, uint32_t c
   const double target = static_cast<double>(set.u) * static_cast<double>(total) * static_cast<double>(exp2f(static_cast<float>(drop - kFixed)));
   auto value = [&](int i) { return i < a.vocab ? Elem<TYPE>::one(src, i) : -INFINITY; };
   auto weight_of = [&](float x) {  // (those that FP64 has as 0 without its exponential)
-    const bool none = !(x > -INFINITY) || Keys<TYPE>::of_value(x) < cut || (x - m) / set.temperature < -750.f;
-    return none ? 0.0 : exp((static_cast<double>(x) - static_cast<double>(m)) / static_cast<double>(set.temperature));
+    if (!(x > -INFINITY) || Keys<TYPE>::of_value(x) < cut || (x - m) / set.temperature < -750.f) return 0.0;
+    const double z = (static_cast<double>(x) - static_cast<double>(m)) / static_cast<double>(set.temperature);
+    // (2^-1074, its smallest number, from ln 2^-1075 on: the exponential may have the last of them as 0)
+    return fmax(exp(z), z > -745.13321910194110842 ? 0x1p-1074 : 0.0);
   };
   double from = 0.0;  // weights before the threads' values
 #pragma unroll 1

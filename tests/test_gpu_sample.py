@@ -155,6 +155,20 @@ def test_smallest_numbers(R, kind, vocab, small):
         assert np.allclose(got[1], logp, rtol=2.0 ** -20, atol=2.0 ** -20)
 
 
+@pytest.mark.parametrize("vocab", [40, 3000])
+def test_the_smallest_weights(R, vocab):
+    """Weights at the end of FP64's range, which 0 draws if they are first: from half of 2^-1074 on they are some."""
+    z = np.float32([-746.0, -745.5, -745.25, -745.1875, -745.125, -745.0625, -745.0, -744.0, -720.0, -709.0])
+    x = torch.full((len(z), vocab), -800.0, device="cuda")
+    x[:, 7] = torch.as_tensor(z, device="cuda")
+    x[:, 30] = -1.0
+    x[:, 31] = 0.0
+    want = np.where(z > -745.1332, 7, 30)  # (e^-745.125 is 1.008 halves of 2^-1074)
+    u = floats(np.zeros(len(z)))
+    assert R.sample_tokens(x, u)[0].tolist() == want.tolist()
+    assert R.sample_tokens(x, u, top_k=ints(np.full(len(z), vocab - 1)))[0].tolist() == want.tolist()
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("vocab", [2000, 40000, 151936, 2 ** 19 - 3])
 def test_flat_rows(R, kind, vocab):
