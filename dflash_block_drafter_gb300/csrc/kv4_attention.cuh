@@ -335,7 +335,8 @@ struct Kv4Job {
 // segment of 150 pieces costs a warp 19 of them, four or eight in flight, not 150
 // in turn.
 constexpr int kMergeThreads = 256;
-// (Over a prefix, whose segments of 128 rows have 10 to 20 pieces each, 16: 16 blocks of 8 over 32768 shared cells 123 -> 119 us.)
+// (Over a prefix, whose segments of 128 rows have 10 to 20 pieces each, 16.  With 8, 16 and 32: 16 blocks of 8 over 32768 shared cells 122, 119 and
+// 119 us, over 8192 83, 79 and 79; 64 tokens over 32768 126, 124 and 124; 8 blocks over 131072, 38 pieces each, 181, 182 and 180.)
 template <int MODE>
 constexpr int kFewPieces = MODE == kKv4Prefix ? 16 : 8;
 

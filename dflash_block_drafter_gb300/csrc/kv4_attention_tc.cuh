@@ -36,7 +36,8 @@
 // 40 / 8 heads over 512 .. 8192 cells 259 us at 128 channels, 170 at 64.  No unit is full
 // (issue 48 %, ALU 38 %, tensor pipe 37 %): a tile takes about 1900 cycles for its way
 // through eight barriers, and the first product waits 9 to 10 us for the plan and Q.
-// At 72 registers at launch 430, 398 and 402 bytes of spill stores (256, 128, 64 channels).
+// At 72 registers at launch 430, 398 and 402 bytes of spill stores (256, 128, 64 channels); of the pass over a prefix 466, 446 and 450, of that over
+// the own cells behind one 486, 398 and 402.
 #pragma once
 
 #include "kv4_attention.cuh"

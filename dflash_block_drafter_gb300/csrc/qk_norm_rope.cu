@@ -10,11 +10,11 @@
 // pair are in one lane.  (With 8 neighbours in a lane and the partners by shuffles, a value took 0.6 instructions of a warp
 // instead of 0.3, and 30001 rows of 32 / 8 heads of 128 144 us.)  Weights, cosines and sines of a row are folded into
 // two factors per channel, z = (x A + x' B) / rms, once per row and for all of its heads.
-// Everything is FP32, rounded once to the rows' type.  The bytes bound it: every value is read and
-// written once.
+// Everything is FP32, rounded once to the rows' type.  Heads whose squares leave its range, and all heads where a weight is very large or
+// small, are scaled by powers of two first.  The bytes bound it: every value is read and written once.
 //
-// Measured: 30001 rows of 32 / 8 heads of 128 104 us, 5.9 TB/s (floor 90 us at the 6.8 TB/s of a copy; 307 MB read, issue
-// slots at 50 %); 4097 rows of 16 / 16 heads of 64 with three axes 13 us (rows still in L2).  Few rows are a launch: 8 rows 4 us.
+// Measured, calls in a row: 30001 rows of 32 / 8 heads of 128 104 us, 5.9 TB/s (floor 90 us at the 6.8 TB/s of a copy; 307 MB read,
+// issue slots at 50 %); 4097 rows of 16 / 16 heads of 64 with three axes 12 us (floor 5; rows still in L2).  Few rows are a launch: 8 rows 6 us.
 #include "common.cuh"
 #include "internal.h"
 #include "kernels.h"
@@ -250,7 +250,7 @@ cudaError_t launch(RopeArgs a, bool bf16, cudaStream_t st) {
   const long long by = (want + a.n_rows - 1) / a.n_rows;
   a.splits = static_cast<int>(by < most ? by : most);
   const long long blocks = (static_cast<long long>(a.n_rows) * a.splits + kWarps - 1) / kWarps;
-  // One wave.  Measured on 30001 rows of 32 / 8 heads of 128 (floor 90 us): 103 us; CTAs of less loads, three or four
+  // One wave.  Measured on 30001 rows of 32 / 8 heads of 128 (floor 90 us): 104 us; CTAs of less loads, three or four
   // on an SM, 105 to 129; several waves 107 to 117.
   const unsigned grid = static_cast<unsigned>(blocks < 1ll * kPerSm * sms ? blocks : 1ll * kPerSm * sms);
   if (bf16) qk_norm_rope_kernel<D, true><<<grid, kThreads, 0, st>>>(a);

@@ -27,8 +27,9 @@
 // the same numbers, so that a weight's error counts 1 - u times before the border and u times behind it: 1.39 log2(vocab / S) + 5 / 2, below
 // 1.4 log2(vocab / S) + 4.  S itself against exact weights has a piece's sum, 3, and the largest weight that it is divided by, 4, besides: 12, and 13 is taken.
 //
-// Measured: 8 rows of 151936 BF16 values, top-p, 26 to 28 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
-// 62 us (floor 11); 128 rows of 100003 FP32 values with settings of their own 79 to 97 us (floor 7.5).  A row takes its cluster 12 to 15 us,
+// Measured, calls in a row: 8 rows of 151936 BF16 values, top-p, 24 to 30 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
+// 62 to 65 us (floor 11), top-k 50 with top-p 70, min-p 52, top-p 0.9 to 0.99 142 to 245, top-p 0.9 of flat rows 288; 128 rows of 100003 FP32 values
+// with settings of their own 57 to 111 us, 86 in the mean of 24 seeds (floor 7.5).  A row takes its cluster 12 to 15 us,
 // a chain of seven short phases between barriers (maximum, bound, list, weights, decision; issue slots 35 %), and there are two or three rows
 // behind one another; the last kind ends with a flat row whose nucleus goes digit by digit, 40 us if FP32 decides it and 80 if not.
 #include <cstddef>
@@ -46,11 +47,16 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 2048;
 constexpr int kMaxRowBytes = 160 * 1024;   // of a row in one CTA
 constexpr int kPerSm = 2;                  // CTAs
+// Lists.  256 rows of 151936 FP16 values: with the 600 best of each, 118 us, and 222 without lists of more than 512, whose rows go digit by
+// digit; with the 90, 130 and 200 best (lists are somewhat longer) 71, 82 and 96 us, and 70, 86 and 89 if no more than 128 are compared each
+// with each, 81, 85 and 88 if no more than 64.
 constexpr int kList = 1024;                // tokens that the first CTA sorts
 constexpr int kOwn = kList / kWarps;       // of a warp
 constexpr int kFew = 256;                  // tokens that it compares each with each
 constexpr int kListDrop = -7;              // places less than kFixed of a list's weights
-constexpr int kShort = kList / 2;          // a row that is a list as a whole
+// A row that is a list as a whole.  (400 rows of 300 and 500 values: 29 to 31 us; with a bound first 19 to 25 by top-k and 29 to 34 by top-p.  Rows of few
+// pieces have no bound: their threads' maxima are too few.)
+constexpr int kShort = kList / 2;
 constexpr int kQuickBins = kThreads;       // ranges of the first bounds
 
 // The keys among which the lowest one kept lies, the weight (or number) of the tokens above them and of all, and whether it is
