@@ -86,19 +86,20 @@ __device__ __noinline__ float far_squares(uint4 a, uint4 b, float f) {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int LANES = D / 16, HEADS = 32 / LANES;  // lanes of a head, heads of a step of a warp
+  constexpr uint32_t ONES = BF16 ? 0x3f803f80u : 0x3c003c00u;
   __shared__ __align__(16) float s_w[2][D];
   __shared__ uint64_t s_turns[D / 2];
   __shared__ uint8_t s_axis[D / 2];
   __shared__ __align__(16) float2 s_angle[kWarps][D / 2];  // (cos, sin) of each warp's row
   const int tid = threadIdx.x, lane = tid & 31;
   float2* angle = s_angle[tid >> 5];
-  // weights (or an eps) whose products with values of heads that are neither `big` nor `tiny` below may leave FP32's range
+  // weights (or an eps) whose products with values of heads that are neither `big` nor `low` below may leave FP32's range
   bool wide = a.eps > 1e38f;
   for (int i = tid; i < D; i += kThreads) {
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const float w = a.side[which].weight ? a.side[which].weight[i] : 1.f;
-      wide |= !(fabsf(w) <= 0x1p62f) || (w != 0.f && fabsf(w) < 0x1p-62f);
+      wide |= !(fabsf(w) <= 0x1p62f) || (w != 0.f && fabsf(w) < 0x1p-30f);
       s_w[which][i] = w;
     }
     if (i < a.half) {
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const Ro
         uint4 raw[kUnroll][2];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+          raw[u][0] = raw[u][1] = make_uint4(ONES, ONES, ONES, ONES);  // (a head that there is not is an ordinary one)
           if (i + u < b1 && (i + u) * HEADS + sub < s.heads) {
             const uint16_t* from = src + (i + u) * (HEADS * D);
             raw[u][0] = __ldcs(reinterpret_cast<const uint4*>(from + ca));
@@ -198,22 +199,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_rope_kernel(const Ro
           for (int o = 1; o < LANES; o <<= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
           const float m = ssq * (1.f / D) + a.eps;
           float inv = norm ? rsqrtf(m) : 1.f;
-          const bool tiny = norm && m < 1e-30f;
-          if (__any_sync(0xffffffffu, !(ssq < most) || tiny)) {
+          const bool low = norm && ssq < 1e-20f;
+          if (__any_sync(0xffffffffu, !(ssq < most) || low)) {
+            // The values are scaled by powers of two until the largest is about 1 (f, for their squares, and h), and 1 / rms is that of
+            // the scaled ones, so that products with the weights leave the range only where results do.
             const bool big = !(ssq < 1e38f);
-            // The values are scaled by powers of two until the largest is about 1 (`f`, for the sum of squares, and `to_one`), and 1 / rms
-            // is that of the scaled ones, so that products with the weights leave the range only where results do.
-            const float f = big ? 0x1p-70f : tiny ? 0x1p90f : 0.5f;
+            const float f = big ? 0x1p-70f : low ? 0x1p90f : 0.5f;
             const float far = far_squares<BF16, LANES>(raw[u][0], raw[u][1], f);
             if (big && !(far < INFINITY) && at == 0) set_status(a.status, DFLASH_DEV_NONFINITE);
-            if (norm && (!(ssq < most) || tiny)) {
+            if (norm && (!(ssq < most) || low)) {
               auto power = [](float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); };
-              const float mean = far * (1.f / D) + a.eps * f * f, r = rsqrtf(mean);
+              // 1 / rms of the values times g, the same power where the squares count
+              const bool least = m < 1e-30f, same = big || least || !low;
+              const float g = same ? f : 0.5f;
+              const float r = rsqrtf((big || least ? far : 0.25f * ssq) * (1.f / D) + a.eps * g * g);
+              const float back = same ? 1.f : 0x1p-91f;  // g / f
               // (2^100: beside an eps far above the squares, inv has its bits still)
-              const float to_one = far > 0.f && far < INFINITY ? fminf(power(rsqrtf(far)), power(r) * 0x1p100f) : 1.f;
-              inv = mean > 0.f ? r / to_one : 0.f;  // a head of zeros without eps stays one
+              const float h = far > 0.f && far < INFINITY ? fminf(power(rsqrtf(far)), power(r) * 0x1p100f * back) : 1.f;
+              inv = r < INFINITY ? r / h * back : 0.f;  // a head of zeros without eps stays one
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = x[e] * f * to_one;
+              for (int e = 0; e < 16; ++e) x[e] = x[e] * f * h;
             }
           }
           uint32_t za[4], zb[4];

@@ -165,6 +165,23 @@ def test_heads_at_the_types_ends(R, d, rot, eps):
         check(c, got, eps=eps)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("eps", [1e-30, 1e-20, 1e-6, 1e10])
+def test_small_heads_beside_eps(R, d, eps):
+    """Heads whose squares are far below eps, so that 1 / rms is eps's: the products with the weights lose nothing below FP32's range."""
+    c = case("bf16", 24, 9, 5, d, 32, seed=d)
+    rng = np.random.default_rng(d)
+    for x, t in ((c["xq"], c["q"]), (c["xk"], c["k"])):
+        size = np.exp2(rng.uniform(-130, -40, x.shape[:2]))[..., None]
+        x[:] = S.to_type(np.sign(x) * rng.uniform(0.5, 1.0, x.shape) * size, "bf16")
+        t.copy_(torch.as_tensor(x, device="cuda").float().bfloat16())
+    for gain in (1.0, 1e-3, 1e-8, 1e-18, 1e9, 1e20):
+        c["weights"] = (gain * (1 + 0.3 * rng.standard_normal((2, d)))).astype(np.float32).astype(np.float64)
+        st = status()
+        check(c, call(R, c, eps=eps, st=st), eps=eps)
+        assert int(st) == 0
+
+
 def test_heads_of_zeros(R):
     c = case("bf16", 3, 4, 2, 64, 64)
     c["t"][1] = 0
