@@ -11,8 +11,8 @@
 // and waits for it where it needs what that has left (this step took 64 tokens from 130 to 125 us and 8 tokens over 8192 cells from 45 to 35; with
 // the passes in the other order, the prefix's waiting for the own cells', 138 instead of 130).
 //
-// Measured, calls in a row: 64 tokens of 24 / 2 heads of 256 over 32768 shared and 1 .. 4096 own cells 122 to 125 us (floor 29), 16 blocks of 8 119 to
-// 122 (floor 29), 200 tokens of 32 / 8 heads of 128 in five groups 106 (floor 21), 8 tokens over 8192 shared cells 35.  The 64 tokens' launches one by
+// Measured, calls in a row: 64 tokens of 24 / 2 heads of 256 over 32768 shared and 1 .. 4096 own cells 122 to 126 us (floor 29), 16 blocks of 8 119 to
+// 123 (floor 29), 200 tokens of 32 / 8 heads of 128 in five groups 106 (floor 21), 8 tokens over 8192 shared cells 35.  The 64 tokens' launches one by
 // one under the profiler: the prefix's products 79 to 82 (480 TFLOP/s, tensor pipe 38 %: a tile's way through eight barriers, as without a
 // prefix), its pieces' merge 11, the own cells 33, their merge 8.  Where no group has a prefix, 64 tokens of up to 1023 cells take 51 us, and 27 by
 // dflash_kv4_attention.

@@ -366,8 +366,8 @@ __device__ __forceinline__ float others_of(uint64_t total, int drop) {
   return static_cast<float>(total - (1ull << (kFixed - drop))) * exp2f(static_cast<float>(drop - kFixed));
 }
 
-// Numbers below this leave the token to sums in FP64, in which small weights keep all their places (units of 2^-45 to 2^-61 are 0 beside
-// u times the sum here, and a weight that rounds to 0 could never be drawn, not even by 0 itself).
+// Numbers below this leave the token to sums in FP64, in which small weights keep all their places.  (In whole numbers u times the sum would be few units
+// or none, and a weight that rounds to 0 could never be drawn, not even by 0.)
 constexpr float kSmallNumber = 0x1p-24f;
 
 // Draws by such a number, by one CTA: the first token with which the weights of keys from `cut` on, which come to `total` with `drop` places less
