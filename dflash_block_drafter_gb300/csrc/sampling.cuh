@@ -422,10 +422,12 @@ __device__ __noinline__ void draw_small(const SampleArgs& a, int row, uint32_t c
     if (warp == who && lane == lanes[who]) {
       int id = 0;
 #pragma unroll 1
-      for (int e = 0; e < PER && before <= target; ++e) {
+      for (int e = 0; e < PER; ++e) {
         const double w = weight_of(value(first + e));
-        if (w > 0.0) id = first + e;  // (the last one, should the sums end a place below)
+        if (!(w > 0.0)) continue;
+        id = first + e;  // (one with a weight, also where the sums before it and with it end a place beside those above)
         before += w;
+        if (before > target) break;
       }
       a.tokens[row] = id;
       if (a.logprob) a.logprob[row] = set.log_of(value(id), m, others_of(total, drop));
