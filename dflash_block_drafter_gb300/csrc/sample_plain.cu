@@ -244,7 +244,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
     for (int r = 0; r < n; ++r) m = fmaxf(m, cta_ref[r]), all += cta_count[r], bad |= cta_nan[r];
     auto of_cta = [&](int r) { return none(cta_ref[r]) ? 0 : units(cta_sum[r] * ex2_approx(start(m) - start(cta_ref[r]))); };
     total = 0;
-    for (int r = 0; r < n; ++r) total += of_cta(r);
+    uint64_t share = 0;
+    for (int r = 0; r < n; ++r) {
+      const uint64_t x = of_cta(r);
+      total += x;
+      if (r == rank) share = x;
+    }
     // the one CTA that goes on: the first whose sums pass u, or that has the largest value
     const uint64_t at = static_cast<uint64_t>(static_cast<double>(set.u) * static_cast<double>(total));
     int who = 0;
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_plain_kernel(const SampleA
     owner = who == rank;
     if (owner && !set.greedy) {
       if (m != m_own) add_up();
-      total += cta - of_cta(rank);  // (of the numbers that the borders are made of)
+      total += cta - share;  // (of the numbers that the borders are made of)
     }
   }
   if (bad || !(m < INFINITY) || m == -INFINITY) {  // not finite, or nothing to draw from

@@ -336,12 +336,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
     }
   };
 
-  const bool small = u < kSmallNumber;  // drawn by FP64 weights: these rows find their thresholds digit by digit
-  const bool filter = (by_k || by_p || by_min) && !small;
+  const bool filter = by_k || by_p || by_min;
   uint32_t from_key = K::LOWEST;  // no threshold of top-k and top-p lies below
   uint32_t to_key = most;         // nor one of top-p alone above
   uint64_t quick_total = 0;       // FP32 weights of all tokens, by top-p alone
-  if (filter) {
+  if (filter && u >= kSmallNumber) {  // (smaller numbers draw by FP64 weights: their rows find their thresholds digit by digit)
     // ---- a bound below the thresholds
     float bound = -INFINITY;  // logits from here on
     bool quick = true;
@@ -835,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
     count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
     const uint64_t total = exchange(all, count, below);
     if (!exact) weight_of_all = static_cast<float>(total) / unit / one;
-    if (exact && small) {
+    if (exact && u < kSmallNumber) {
       if (rank == 0) draw_small<TYPE>(a, row, cut, m, total, scale->drop, count, reinterpret_cast<double*>(sh.warp_w));
       return true;
     }
@@ -907,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const __grid_c
     if (!exact) weight_of_all = static_cast<float>(sure.whole) / unit / one;
   }
   if (by_p && p > 0.f) cut = max(cut, sure.lo);
-  if (in_range && !small && draw_from(cut, false)) return;
+  if (in_range && u >= kSmallNumber && draw_from(cut, false)) return;
   exact_from_here();
   draw_from(cut, true);
 }
