@@ -18,7 +18,7 @@
 //
 // Few rows: a row's batches are split over the CTAs of a cluster.
 //
-// Measured, calls in a row: 1000 rows of 151936 BF16 values 88 to 90 us (floor 45), greedy ones 74.  The first kernel takes 58 to 60 (5.1 TB/s, issue
+// Measured, calls in a row: 1000 rows of 151936 BF16 values 88 to 91 us (floor 45), greedy ones 74.  The first kernel takes 58 to 60 (5.1 TB/s, issue
 // slots at 70 %: an exponential and seven instructions a value), the second 25 to 30 for the 15 or so rows left to it: a claim, 16 us of exact
 // weights, the search for the token.
 #include <cstddef>

@@ -27,7 +27,7 @@
 // the same numbers, so that a weight's error counts 1 - u times before the border and u times behind it: 1.39 log2(vocab / S) + 5 / 2, below
 // 1.4 log2(vocab / S) + 4.  S itself against exact weights has a piece's sum, 3, and the largest weight that it is divided by, 4, besides: 12, and 13 is taken.
 //
-// Measured, calls in a row: 8 rows of 151936 BF16 values, top-p, 24 to 30 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
+// Measured, calls in a row: 8 rows of 151936 BF16 values, top-p, 24 to 31 us, of which 24 are the host's (floor 0.4); 256 rows of FP16 values, top-k 50,
 // 62 to 65 us (floor 11), top-k 50 with top-p 70, min-p 52, top-p 0.9 to 0.99 142 to 245, top-p 0.9 of flat rows 288; 128 rows of 100003 FP32 values
 // with settings of their own 53 to 125 us, 88 in the mean of 80 seeds (floor 7.5).  A row takes its cluster 12 to 15 us,
 // a chain of seven short phases between barriers (maximum, bound, list, weights, decision; issue slots 35 %), and there are two or three rows
